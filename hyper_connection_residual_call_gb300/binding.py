@@ -7,8 +7,10 @@ runs in the library's CUDA kernels:
   pointers (ints), a ``TsWeight`` struct and a CUDA stream handle; they return
   the ``ts_status`` code.
 * ``hc_call`` / ``hc_inject_call`` / ``hc_mixer`` / ``hc_inject_add`` /
-  ``hc_replicate_entry`` / ``hc_stack``: the same calls for torch CUDA
-  tensors. They allocate outputs/workspace with torch when not given, pass
+  ``hc_replicate_entry`` / ``hc_stack``, and for a speculative decoding step
+  ``hc_rope`` / ``hc_kv_write`` / ``hc_kv_read`` / ``hc_kv_compact`` /
+  ``hc_tree_build`` / ``hc_tree_attention`` / ``hc_verify``: the same calls
+  for torch CUDA tensors. They allocate outputs/workspace with torch when not given, pass
   the current torch stream, and raise ``HCError`` on any error status.
 
 There is no fallback: if the library is not built or cannot be loaded, every
@@ -25,6 +27,8 @@ from .build import LIB_PATH
 
 TS_OK, TS_ERR_INVALID_ARG, TS_ERR_UNSUPPORTED, TS_ERR_CUDA, TS_ERR_WORKSPACE, TS_ERR_TIMEOUT = range(6)
 TS_W_BF16, TS_W_INT4_AFFINE = 0, 1
+TS_KV_BF16, TS_KV_FP8, TS_KV_INT4 = range(3)
+TS_ROPE_PLAIN, TS_ROPE_LINEAR, TS_ROPE_NTK, TS_ROPE_BY_PARTS = range(4)
 RMS_EPS = 1e-6  # families/qwen4/mod.rs, RMS_EPS
 
 EXPORTS = ("ts_hc_workspace_bytes", "ts_hc_workspace_layout", "ts_hc_call", "ts_hc_inject_add",
@@ -32,7 +36,9 @@ EXPORTS = ("ts_hc_workspace_bytes", "ts_hc_workspace_layout", "ts_hc_call", "ts_
            "ts_hc_replicate_entry", "ts_hc_ple_workspace_bytes", "ts_hc_ple_workspace_layout", "ts_hc_ple",
            "ts_hc_last_error",
            "ts_hc_device_status", "ts_hc_call_noalloc", "ts_hc_stack_workspace_bytes", "ts_hc_stack",
-           "ts_hc_stack_ple_workspace_bytes", "ts_hc_stack_ple", "ts_hc_selftest_timeout")
+           "ts_hc_stack_ple_workspace_bytes", "ts_hc_stack_ple", "ts_hc_selftest_timeout",
+           "ts_hc_rope_table", "ts_hc_rope", "ts_hc_kv_write", "ts_hc_kv_read", "ts_hc_kv_compact", "ts_hc_tree_build",
+           "ts_hc_tree_attention_workspace_bytes", "ts_hc_tree_attention", "ts_hc_verify")
 TS_HC_STATIC_SCRATCH_BYTES = 64 * 1024 * 1024  # include/ts_hc.h
 
 
@@ -73,6 +79,38 @@ class TsHcPleModule(ctypes.Structure):
         ("norm_query_w", ctypes.c_void_p),
         ("norm_conv_w", ctypes.c_void_p),
         ("conv_w", ctypes.c_void_p),
+    ]
+
+
+class TsHcRopeScaling(ctypes.Structure):
+    """``ts_hc_rope_scaling``: how a rotary table's frequencies are changed for long contexts."""
+    _fields_ = [
+        ("type", ctypes.c_int32),
+        ("factor", ctypes.c_float),
+        ("original_positions", ctypes.c_float),
+        ("beta_fast", ctypes.c_float),
+        ("beta_slow", ctypes.c_float),
+        ("magnitude", ctypes.c_float),
+    ]
+
+
+class TsHcKvCache(ctypes.Structure):
+    """``ts_hc_kv_cache``: a paged cache's format and tensors."""
+    _fields_ = [
+        ("type", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("n_pages", ctypes.c_long),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("k_biases", ctypes.c_void_p),
+        ("v_biases", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
     ]
 
 
@@ -134,6 +172,25 @@ def library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.ts_hc_stack_ple.argtypes = [vp, i, mp, mp, i, mp, ctypes.POINTER(TsHcPleModule), vp, vp, SUBLAYER_FN,
                                         vp, vp, i, i, i, i, f, vp, sz, vp]
         lib.ts_hc_stack_ple.restype = i
+        cp = ctypes.POINTER(TsHcKvCache)
+        lib.ts_hc_rope_table.argtypes = [vp, i, i, ctypes.c_double, ctypes.POINTER(TsHcRopeScaling), vp]
+        lib.ts_hc_rope_table.restype = i
+        lib.ts_hc_rope.argtypes = [vp, l, vp, l, vp, vp, i, vp, l, vp, l, i, i, i, i, i, i, i, vp]
+        lib.ts_hc_rope.restype = i
+        lib.ts_hc_kv_write.argtypes = [vp, l, vp, l, cp, vp, i, i, vp]
+        lib.ts_hc_kv_write.restype = i
+        lib.ts_hc_kv_read.argtypes = [cp, vp, vp, vp, i, i, vp]
+        lib.ts_hc_kv_read.restype = i
+        lib.ts_hc_kv_compact.argtypes = [cp, vp, vp, vp, vp, i, i, vp]
+        lib.ts_hc_kv_compact.restype = i
+        lib.ts_hc_tree_build.argtypes = [vp, l, vp, vp, vp, i, i, vp]
+        lib.ts_hc_tree_build.restype = i
+        lib.ts_hc_tree_attention_workspace_bytes.argtypes = [i, i, i, cp]
+        lib.ts_hc_tree_attention_workspace_bytes.restype = sz
+        lib.ts_hc_tree_attention.argtypes = [vp, l, cp, vp, vp, l, vp, vp, i, i, i, f, vp, sz, vp]
+        lib.ts_hc_tree_attention.restype = i
+        lib.ts_hc_verify.argtypes = [vp, vp, vp, vp, l, vp, vp, vp, vp, vp, vp, i, i, i, vp]
+        lib.ts_hc_verify.restype = i
         lib.ts_hc_selftest_timeout.argtypes = [vp]
         lib.ts_hc_selftest_timeout.restype = i
         lib.ts_hc_last_error.argtypes = []
@@ -259,6 +316,50 @@ def ts_hc_stack_ple(emb, T, attn, mlp, n_layers, final_mixer, ple, ple_rows, ple
                                      None if ple is None else ctypes.byref(ple), ple_rows, ple_conv_state,
                                      sublayer if sublayer is not None else SUBLAYER_FN(), user, mixed_out,
                                      max_chunk, H, C, lowrank, eps, workspace, workspace_bytes, stream)
+
+
+def ts_hc_rope_table(table, max_pos, rot, theta, scaling, stream) -> int:
+    """``scaling``: a ``TsHcRopeScaling`` or None."""
+    return library().ts_hc_rope_table(table, max_pos, rot, theta, _wref(scaling), stream)
+
+
+def ts_hc_rope(q, q_stride, k, k_stride, positions, table, max_pos, q_out, q_out_stride, k_out, k_out_stride, N, q_heads,
+               k_heads, D, rot, interleaved, inverse, stream) -> int:
+    return library().ts_hc_rope(q, q_stride, k, k_stride, positions, table, max_pos, q_out, q_out_stride, k_out,
+                                k_out_stride, N, q_heads, k_heads, D, rot, interleaved, inverse, stream)
+
+
+def ts_hc_kv_write(k, k_stride, v, v_stride, cache, ctx_len, B, T, stream) -> int:
+    """``cache``: a ``TsHcKvCache`` (here and below)."""
+    return library().ts_hc_kv_write(k, k_stride, v, v_stride, _wref(cache), ctx_len, B, T, stream)
+
+
+def ts_hc_kv_read(cache, start, k_out, v_out, B, n, stream) -> int:
+    return library().ts_hc_kv_read(_wref(cache), start, k_out, v_out, B, n, stream)
+
+
+def ts_hc_kv_compact(cache, ctx_len, path, n_accepted, new_len, B, T, stream) -> int:
+    return library().ts_hc_kv_compact(_wref(cache), ctx_len, path, n_accepted, new_len, B, T, stream)
+
+
+def ts_hc_tree_build(parents, parents_stride, ctx_len, mask, positions, B, T, stream) -> int:
+    return library().ts_hc_tree_build(parents, parents_stride, ctx_len, mask, positions, B, T, stream)
+
+
+def ts_hc_tree_attention_workspace_bytes(B: int, T: int, q_heads: int, cache) -> int:
+    return library().ts_hc_tree_attention_workspace_bytes(B, T, q_heads, _wref(cache))
+
+
+def ts_hc_tree_attention(q, q_stride, cache, ctx_len, mask, mask_stride, out, lse, B, T, q_heads, scale, workspace,
+                         workspace_bytes, stream) -> int:
+    return library().ts_hc_tree_attention(q, q_stride, _wref(cache), ctx_len, mask, mask_stride, out, lse, B, T, q_heads,
+                                          scale, workspace, workspace_bytes, stream)
+
+
+def ts_hc_verify(logits, draft_probs, tokens, parents, parents_stride, temperature, u, noise, n_accepted, path,
+                 next_token, B, T, V, stream) -> int:
+    return library().ts_hc_verify(logits, draft_probs, tokens, parents, parents_stride, temperature, u, noise, n_accepted,
+                                  path, next_token, B, T, V, stream)
 
 
 def ts_hc_selftest_timeout(stream) -> int:
@@ -669,3 +770,298 @@ def hc_stack(emb, layers, final, sublayer, *, C: int, max_chunk: Optional[int] =
     M_last = T - (max(T, 1) - 1) // max_chunk * max_chunk if T else 0
     raw_last = ws[:2 * M_last * C * H].view(torch.bfloat16).view(M_last, C * H)
     return mixed_out, raw_last
+
+
+# ------------------------------------------------------------- a speculative decoding step
+
+def _rows(t, name):
+    """(tokens, heads, D, token stride) of bf16 rows [N, heads, D] or [B, T, heads, D]: each token's
+    heads side by side, the tokens at one stride (a slice of a projection's output will do)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise HCError(TS_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise HCError(TS_ERR_INVALID_ARG, f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        (n, h, d), step = shape, stride[0]
+    elif len(shape) == 4:
+        b, n, h, d = shape
+        step = stride[1] if n != 1 else stride[0]
+        if b > 1 and n > 1 and stride[0] != n * step:
+            raise HCError(TS_ERR_INVALID_ARG, f"{name}: its sequences' tokens are not at one stride: {tuple(stride)}")
+        n *= b
+    else:
+        raise HCError(TS_ERR_INVALID_ARG, f"{name} has shape {tuple(shape)}, expected [tokens, heads, D] or [B, T, heads, D]")
+    if (d > 1 and stride[-1] != 1) or (h > 1 and stride[-2] != d):
+        raise HCError(TS_ERR_INVALID_ARG, f"{name}: a token's heads must lie side by side, strides are {tuple(stride)}")
+    return n, h, d, step if n > 1 else h * d
+
+
+def _made(t, stream):
+    """A tensor that this module allocated, about to be used on ``stream`` (None: the current one)."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def rope_table(max_pos: int, rot: int, theta: float, *, scaling: Optional[TsHcRopeScaling] = None, device=None, stream=None):
+    """The rotary table fp32 [max_pos, rot/2, 2] of (cos, sin) for ``hc_rope``."""
+    torch = _torch()
+    table = _made(torch.empty((max_pos, max(rot // 2, 0), 2), dtype=torch.float32, device=device or "cuda"), stream)
+    _check(ts_hc_rope_table(table.data_ptr(), max_pos, rot, theta, scaling, _stream_handle(stream)))
+    return table
+
+
+def hc_rope(q, k, positions, table, *, interleaved: bool = False, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of ``q`` [N, q_heads, D] and ``k`` [N, k_heads, D] (or [B, T, heads, D]; k may be
+    None) bf16 at ``positions`` int32 (N of them), by ``table`` [max_pos, rot/2, 2]. ``inverse`` turns back
+    (the gradient). Returns (q_out, k_out); passing q and k as them turns in place."""
+    torch = _torch()
+    n, hq, d, sq = _rows(q, "q")
+    if q_out is None:
+        q_out = _made(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream)
+        so = hq * d
+    else:
+        no, ho, do, so = _rows(q_out, "q_out")
+        if (no, ho, do) != (n, hq, d):
+            raise HCError(TS_ERR_INVALID_ARG, f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+    hk, sk, sko, kp, kop = 0, 0, 0, None, None
+    if k is not None:
+        nk, hk, dk, sk = _rows(k, "k")
+        if (nk, dk) != (n, d):
+            raise HCError(TS_ERR_INVALID_ARG, f"k has shape {tuple(k.shape)}, q has {tuple(q.shape)}")
+        if k_out is None:
+            k_out = _made(torch.empty(k.shape, dtype=torch.bfloat16, device=k.device), stream)
+            sko = hk * d
+        else:
+            no, ho, do, sko = _rows(k_out, "k_out")
+            if (no, ho, do) != (n, hk, d):
+                raise HCError(TS_ERR_INVALID_ARG, f"k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    _need(positions, "positions", torch.int32)
+    if positions.numel() != n:
+        raise HCError(TS_ERR_INVALID_ARG, f"positions has {positions.numel()} entries for {n} tokens")
+    _need(table, "table", torch.float32)
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise HCError(TS_ERR_INVALID_ARG, f"table has shape {tuple(table.shape)}, expected [max_pos, rot/2, 2]")
+    _check(library().ts_hc_rope(q.data_ptr(), sq, kp, sk, positions.data_ptr(), table.data_ptr(), table.shape[0],
+                                q_out.data_ptr(), so, kop, sko, n, hq, hk, d, 2 * table.shape[1], interleaved, inverse,
+                                _stream_handle(stream)))
+    return q_out, k_out
+
+
+class KVCache:
+    """A paged cache of one layer's keys and values: the caller's tensors and their format.
+
+    ``kind`` "bf16": k, v bf16 [pages, heads, page_size, D]; "fp8": uint8 (e4m3 codes) of that shape and
+    k_scale, v_scale uint8 [pages, heads, page_size]; "int4": uint8 [pages, heads, page_size, D/2] and
+    k_scale, v_scale, k_bias, v_bias fp16 [pages, heads, page_size, D/group]. ``page_table`` int32
+    [B, max_pages]. The tensors are read and written where they are; replacing one makes a new KVCache.
+    """
+
+    def __init__(self, kind: str, k, v, page_table, *, k_scale=None, v_scale=None, k_bias=None, v_bias=None, group: int = 0):
+        torch = _torch()
+        kinds = {"bf16": TS_KV_BF16, "fp8": TS_KV_FP8, "int4": TS_KV_INT4}
+        if kind not in kinds:
+            raise HCError(TS_ERR_INVALID_ARG, f"unknown cache kind {kind!r}")
+        dtype = torch.bfloat16 if kind == "bf16" else torch.uint8
+        _need(k, "cache.k", dtype)
+        if k.dim() != 4:
+            raise HCError(TS_ERR_INVALID_ARG, f"cache.k has shape {tuple(k.shape)}, expected [pages, heads, page_size, row]")
+        _need(v, "cache.v", dtype, k.shape)
+        pages, heads, size, row = k.shape
+        d = row * 2 if kind == "int4" else row
+        _need(page_table, "cache.page_table", torch.int32)
+        if page_table.dim() != 2:
+            raise HCError(TS_ERR_INVALID_ARG, f"cache.page_table has shape {tuple(page_table.shape)}, expected [B, max_pages]")
+        if kind == "fp8":
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                _need(t, "cache." + name, torch.uint8, (pages, heads, size))
+        if kind == "int4":
+            if group not in (32, 64, 128) or d % group:
+                raise HCError(TS_ERR_UNSUPPORTED, f"cache.group = {group}: INT4 groups of 32, 64 or 128 and at most head_dim = {d} are supported")
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale), ("k_bias", k_bias), ("v_bias", v_bias)):
+                _need(t, "cache." + name, torch.float16, (pages, heads, size, d // group))
+        self.kind, self.group, self.page_size, self.heads, self.head_dim = kind, group, size, heads, d
+        self.batch, self.max_pages = page_table.shape
+        self.tensors = (k, v, page_table, k_scale, v_scale, k_bias, v_bias)  # kept alive with the struct
+        self.struct = TsHcKvCache(kinds[kind], group, size, heads, d, self.max_pages, pages, k.data_ptr(), v.data_ptr(),
+                                  *(t.data_ptr() if t is not None else None for t in (k_scale, v_scale, k_bias, v_bias)),
+                                  page_table.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+
+def kv_cache(kind: str, pages: int, heads: int, page_size: int, head_dim: int, page_table, *, group: int = 64) -> KVCache:
+    """A ``KVCache`` over newly allocated, zeroed tensors."""
+    torch = _torch()
+    dev, lead = page_table.device, (pages, heads, page_size)
+    zeros = lambda *shape, dtype: torch.zeros(shape, dtype=dtype, device=dev)  # noqa: E731
+    if kind == "bf16":
+        return KVCache(kind, *(zeros(*lead, head_dim, dtype=torch.bfloat16) for _ in range(2)), page_table)
+    if kind == "fp8":
+        k, v = (zeros(*lead, head_dim, dtype=torch.uint8) for _ in range(2))
+        ks, vs = (zeros(*lead, dtype=torch.uint8) for _ in range(2))
+        return KVCache(kind, k, v, page_table, k_scale=ks, v_scale=vs)
+    k, v = (zeros(*lead, head_dim // 2, dtype=torch.uint8) for _ in range(2))
+    ks, vs, kb, vb = (zeros(*lead, head_dim // max(group, 1), dtype=torch.float16) for _ in range(4))
+    return KVCache(kind, k, v, page_table, k_scale=ks, v_scale=vs, k_bias=kb, v_bias=vb, group=group)
+
+
+def _lengths(t, name, batch):
+    _need(t, name, _torch().int32, (batch,))
+
+
+def hc_kv_write(k, v, cache: KVCache, ctx_len, *, stream=None):
+    """Stores ``k``, ``v`` [B, T, heads, D] bf16 at positions ctx_len[b] .. ctx_len[b] + T - 1, quantised to
+    the cache's kind; ``ctx_len`` int32 [B]. Returns the cache."""
+    n, h, d, sk = _rows(k, "k")
+    nv, hv, dv, sv = _rows(v, "v")
+    if k.dim() != 4 or k.shape[0] != cache.batch or (h, d) != (cache.heads, cache.head_dim):
+        raise HCError(TS_ERR_INVALID_ARG, f"k has shape {tuple(k.shape)}, expected [{cache.batch}, T, {cache.heads}, {cache.head_dim}]")
+    if v.shape != k.shape:
+        raise HCError(TS_ERR_INVALID_ARG, f"v has shape {tuple(v.shape)}, k has {tuple(k.shape)}")
+    _lengths(ctx_len, "ctx_len", cache.batch)
+    _check(library().ts_hc_kv_write(k.data_ptr(), sk, v.data_ptr(), sv, cache.ref, ctx_len.data_ptr(), cache.batch, k.shape[1],
+                                    _stream_handle(stream)))
+    return cache
+
+
+def hc_kv_read(cache: KVCache, start, n: int, *, k_out=None, v_out=None, stream=None):
+    """Positions start[b] .. start[b] + n - 1 of each sequence as bf16 [B, n, heads, D]; ``start`` int32 [B].
+    Returns (k, v)."""
+    torch = _torch()
+    shape = (cache.batch, n, cache.heads, cache.head_dim)
+    _lengths(start, "start", cache.batch)
+    if k_out is None:
+        k_out = _made(torch.empty(shape, dtype=torch.bfloat16, device=start.device), stream)
+    else:
+        _need(k_out, "k_out", torch.bfloat16, shape)
+    if v_out is None:
+        v_out = _made(torch.empty(shape, dtype=torch.bfloat16, device=start.device), stream)
+    else:
+        _need(v_out, "v_out", torch.bfloat16, shape)
+    _check(library().ts_hc_kv_read(cache.ref, start.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), cache.batch, n,
+                                   _stream_handle(stream)))
+    return k_out, v_out
+
+
+def hc_kv_compact(cache: KVCache, ctx_len, path, n_accepted, *, new_len=None, stream=None):
+    """Moves the accepted nodes' rows (``path`` int32 [B, T] and ``n_accepted`` int32 [B] of ``hc_verify``)
+    to the positions after ``ctx_len``; returns new_len int32 [B] = ctx_len + n_accepted + 1."""
+    torch = _torch()
+    _lengths(ctx_len, "ctx_len", cache.batch)
+    _lengths(n_accepted, "n_accepted", cache.batch)
+    _need(path, "path", torch.int32)
+    if path.dim() != 2 or path.shape[0] != cache.batch:
+        raise HCError(TS_ERR_INVALID_ARG, f"path has shape {tuple(path.shape)}, expected [{cache.batch}, T]")
+    if new_len is None:
+        new_len = _made(torch.empty_like(ctx_len), stream)
+    _lengths(new_len, "new_len", cache.batch)
+    _check(library().ts_hc_kv_compact(cache.ref, ctx_len.data_ptr(), path.data_ptr(), n_accepted.data_ptr(), new_len.data_ptr(),
+                                      cache.batch, path.shape[1], _stream_handle(stream)))
+    return new_len
+
+
+def hc_tree_build(parents, ctx_len=None, *, batch: Optional[int] = None, mask=None, positions=None, stream=None):
+    """(mask int32 [B, T, ceil(T/32)], positions int32 [B, T]) of trees given by ``parents`` int32 [B, T], or
+    [T] for one tree that ``batch`` sequences (or ctx_len's) share."""
+    torch = _torch()
+    _need(parents, "parents", torch.int32)
+    t = parents.shape[-1]
+    if parents.dim() == 1:
+        b, step = (ctx_len.shape[0] if ctx_len is not None else batch or 1), 0
+    else:
+        b, step = parents.shape[0], t
+    if parents.dim() > 2 or (batch is not None and batch != b):
+        raise HCError(TS_ERR_INVALID_ARG, f"parents has shape {tuple(parents.shape)}, expected [B, T] or [T]")
+    if ctx_len is not None:
+        _lengths(ctx_len, "ctx_len", b)
+    if mask is None:
+        mask = _made(torch.empty((b, t, (t + 31) // 32), dtype=torch.int32, device=parents.device), stream)
+    _need(mask, "mask", torch.int32, (b, t, (t + 31) // 32))
+    if positions is None:
+        positions = _made(torch.empty((b, t), dtype=torch.int32, device=parents.device), stream)
+    _need(positions, "positions", torch.int32, (b, t))
+    _check(ts_hc_tree_build(parents.data_ptr(), step, None if ctx_len is None else ctx_len.data_ptr(), mask.data_ptr(),
+                            positions.data_ptr(), b, t, _stream_handle(stream)))
+    return mask, positions
+
+
+def tree_attention_workspace(B: int, T: int, q_heads: int, cache: KVCache, device=None):
+    torch = _torch()
+    n = ts_hc_tree_attention_workspace_bytes(B, T, q_heads, cache.struct)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or cache.tensors[0].device)
+
+
+def hc_tree_attention(q, cache: KVCache, ctx_len, *, mask=None, scale: Optional[float] = None, out=None, lse=None, ws=None,
+                      stream=None):
+    """Attention of ``q`` [B, T, q_heads, D] bf16, the nodes at ctx_len[b] .. ctx_len[b] + T - 1, over the cache.
+    ``mask`` int32 [B, T, ceil(T/32)] (or [T, ceil(T/32)] for one tree) of ``hc_tree_build``; None: a chain.
+    ``scale`` defaults to D ** -0.5. Returns (out bf16 [B, T, q_heads, D], lse fp32 [B, T, q_heads])."""
+    torch = _torch()
+    _, h, d, sq = _rows(q, "q")
+    if q.dim() != 4 or q.shape[0] != cache.batch or d != cache.head_dim:
+        raise HCError(TS_ERR_INVALID_ARG, f"q has shape {tuple(q.shape)}, expected [{cache.batch}, T, heads, {cache.head_dim}]")
+    b, t = q.shape[0], q.shape[1]
+    _lengths(ctx_len, "ctx_len", b)
+    words = (t + 31) // 32
+    step = 0
+    if mask is not None:
+        _need(mask, "mask", torch.int32, (t, words) if mask.dim() == 2 else (b, t, words))
+        step = t * words if mask.dim() == 3 else 0
+    if out is None:
+        out = _made(torch.empty((b, t, h, d), dtype=torch.bfloat16, device=q.device), stream)
+    else:
+        _need(out, "out", torch.bfloat16, (b, t, h, d))
+    if lse is None:
+        lse = _made(torch.empty((b, t, h), dtype=torch.float32, device=q.device), stream)
+    else:
+        _need(lse, "lse", torch.float32, (b, t, h))
+    if ws is None:
+        ws = _made(tree_attention_workspace(b, t, h, cache, q.device), stream)
+    _check(library().ts_hc_tree_attention(q.data_ptr(), sq, cache.ref, ctx_len.data_ptr(),
+                                          None if mask is None else mask.data_ptr(), step, out.data_ptr(), lse.data_ptr(), b, t,
+                                          h, d ** -0.5 if scale is None else scale, ws.data_ptr(),
+                                          ws.numel() * ws.element_size(), _stream_handle(stream)))
+    return out, lse
+
+
+def hc_verify(logits, tokens, parents=None, temperature=None, *, draft_probs=None, u=None, noise=None, n_accepted=None, path=None,
+              next_token=None, stream=None):
+    """Which of the drafted ``tokens`` int32 [B, T] hold, given the target's ``logits`` fp32 [B, T, V] and the
+    draft's ``draft_probs`` fp32 [B, T, V]; ``parents`` int32 [B, T], [T] or None (a chain); ``temperature``
+    fp32 [B]; ``u`` fp32 [B, T] in [0, 1) and ``noise`` fp32 [B, V] exponential variates. Without draft_probs, u
+    and noise every sequence is greedy. Returns (n_accepted [B], path [B, T], next_token [B]), int32."""
+    torch = _torch()
+    _need(logits, "logits", torch.float32)
+    if logits.dim() != 3:
+        raise HCError(TS_ERR_INVALID_ARG, f"logits has shape {tuple(logits.shape)}, expected [B, T, V]")
+    b, t, v = logits.shape
+    _need(tokens, "tokens", torch.int32, (b, t))
+    step = 0
+    if parents is not None:
+        _need(parents, "parents", torch.int32, (t,) if parents.dim() == 1 else (b, t))
+        step = t if parents.dim() == 2 else 0
+    if draft_probs is not None:
+        _need(draft_probs, "draft_probs", torch.float32, (b, t, v))
+        _need(u, "u", torch.float32, (b, t))
+        _need(noise, "noise", torch.float32, (b, v))
+        _need(temperature, "temperature", torch.float32, (b,))
+    elif u is not None or noise is not None:
+        raise HCError(TS_ERR_INVALID_ARG, "draft_probs, u and noise are given together, or none of them (greedy)")
+    if n_accepted is None:
+        n_accepted = _made(torch.empty(b, dtype=torch.int32, device=logits.device), stream)
+    if path is None:
+        path = _made(torch.empty((b, t), dtype=torch.int32, device=logits.device), stream)
+    if next_token is None:
+        next_token = _made(torch.empty(b, dtype=torch.int32, device=logits.device), stream)
+    _need(n_accepted, "n_accepted", torch.int32, (b,))
+    _need(path, "path", torch.int32, (b, t))
+    _need(next_token, "next_token", torch.int32, (b,))
+    ptr = lambda x: None if x is None else x.data_ptr()  # noqa: E731
+    _check(library().ts_hc_verify(logits.data_ptr(), ptr(draft_probs), tokens.data_ptr(), ptr(parents), step,
+                                  ptr(temperature) if draft_probs is not None else None, ptr(u), ptr(noise),
+                                  n_accepted.data_ptr(), path.data_ptr(), next_token.data_ptr(), b, t, v,
+                                  _stream_handle(stream)))
+    return n_accepted, path, next_token

@@ -1,0 +1,926 @@
+// hc_attn.cu -- attention of a few drafted tokens (a chain or a tree) over the
+// paged cache: blocks of 16 or 32 rows (ts_hc_tree_attention in include/ts_hc.h).
+//
+//   row (t, h) sees the committed keys and the nodes of its mask row;
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(x_j - m),  x_j = scale log2(e) q . k_j
+//
+// With T nodes and G query heads a key head an item has T*G rows that share one
+// pass over the keys: 4 T G D flops for each key's row bytes, so that up to some
+// 32 rows the operator is bound by the cache's bytes. The layout follows from
+// that: each warp streams 16-key chunks of its own (every fourth of the line)
+// through a ring of its own in shared memory (cp.async; nothing but __syncwarp
+// between a chunk's arrival and its use), with its own running maximum and sum, and
+// the four warps' results are joined once per item. The products are m16n8k16
+// tensor-core products with the rows as M: rows are few, and their S and P stay
+// in the registers in which one product leaves them and the next wants them.
+//
+// FP8 and INT4 codes go to shared memory as they are, so that the ring holds more
+// keys, and become operands in registers: e4m3 to bf16 by moving the bits and one
+// exact multiplication, the row's scale applied to the scores and to P. An INT4
+// key's codes go into the product as they are (q - 8, exact in bf16), one product
+// sum a group, and its scale and bias enter in fp32:
+//   q . k = sum_groups scale (sum Q (q - 8)) + (bias + 8 scale) sum Q
+// An INT4 value becomes q * scale + bias in fp16.
+#include <algorithm>
+
+#include "hc_attn.cuh"
+
+namespace tshc {
+
+namespace {
+
+constexpr int kWarps = kAttnThreads / 32;
+constexpr int kChunk = 16;               // keys a warp takes at a time
+constexpr int kTile = kChunk * kWarps;   // keys of a tile
+constexpr float kRescale = 8.f;          // the reference maximum moves when it is exceeded by this much (log2)
+
+template <int kType, int D>
+struct Format {
+    static constexpr int kRow = kType == kKvBf16 ? 2 * D : kType == kKvFp8 ? D : D / 2;  // bytes of a row's codes
+    static constexpr int kCodes = kChunk * kRow;
+    static constexpr int kMaxGroups = D / 32;
+    // one scale array's bytes of a chunk (INT4: room for groups of 32)
+    static constexpr int kScale = kType == kKvBf16 ? 0 : kType == kKvFp8 ? 16 : kChunk * kMaxGroups * 2;
+    static constexpr int kStage = 2 * kCodes + (kType == kKvInt4 ? 4 : 2) * kScale;
+    // about 24 KB a warp in flight
+    static constexpr int kStages = kType == kKvBf16 ? (D == 64 ? 6 : D == 128 ? 3 : 2) : kType == kKvFp8 ? (D == 64 ? 8 : D == 128 ? 5 : 3)
+                                                                                     : (D == 64 ? 8 : D == 128 ? 8 : 5);
+};
+
+template <int kType, int D, int MT>
+struct Smem {
+    using F = Format<kType, D>;
+    static constexpr int kRing = kWarps * F::kStages * F::kStage;
+    static constexpr int kMerge = kWarps * 16 * MT * (D + 2) * 4;  // overlays the ring
+    static constexpr int kQ = 16 * MT * D * 2 + (kType == kKvInt4 ? 16 * MT * (D / 32) * 4 : 0);
+    static constexpr int kTotal = (kRing > kMerge ? kRing : kMerge) + kQ;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
+{
+    const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (kHalf)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// e4m3 codes in the high bytes of the two halves of w -> bf16x2. A code's 4
+// exponent and 3 mantissa bits, moved under bf16's sign, read as the value times
+// 2^-120 (denormals included); the multiplication by 2^120 is exact.
+__device__ __forceinline__ uint32_t e4m3_hi_bf16x2(uint32_t w)
+{
+    const uint32_t r = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
+    uint32_t y;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(r), "r"(0x7B807B80u));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t e4m3_lo_bf16x2(uint32_t w) { return e4m3_hi_bf16x2(w << 8); }
+
+// INT4 codes in bits 0-3 of the two halves of w -> q - 8, bf16x2 (exact).
+__device__ __forceinline__ uint32_t int4_bf16x2(uint32_t w)
+{
+    const uint32_t bits = (w & 0x000F000Fu) | 0x43004300u;  // 128 + q
+    uint32_t y;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(bits), "r"(0xC308C308u));  // - 136
+    return y;
+}
+
+// INT4 codes in bits 0-3 of the two halves of w -> q * scale + bias, fp16x2.
+__device__ __forceinline__ uint32_t int4_f16x2(uint32_t w, __half2 scale, __half2 bias)
+{
+    const uint32_t bits = (w & 0x000F000Fu) | 0x64006400u;  // 1024 + q
+    const __half2 q = __hsub2(reinterpret_cast<const __half2 &>(bits), __half2half2(__ushort_as_half(0x6400)));
+    const __half2 v = __hfma2(q, scale, bias);
+    return reinterpret_cast<const uint32_t &>(v);
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// N consecutive 32-bit words (N = 1, 2 or 4).
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t *w, uint32_t a)
+{
+    if (N == 1)
+        w[0] = lds32(a);
+    else if (N == 2)
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
+    else
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Where 16-byte piece `unit` of row `row` lies in a chunk's codes: permuted so
+// that the reads below meet no bank twice (for rows of 128 bytes and more).
+template <int kType, int D, bool kValue>
+__device__ __forceinline__ int piece_at(int row, int unit)
+{
+    constexpr int kRow = Format<kType, D>::kRow, kUnits = kRow / 16;
+    int s;
+    if (kType == kKvBf16)
+        s = row & 7;  // ldmatrix: 8 rows at one unit
+    else if (kType == kKvInt4 && !kValue)
+        s = (row * kRow / 128) & (kUnits - 1) & 7;  // 8 rows at one unit, a word a lane
+    else if (kUnits >= 8)
+        s = kValue ? (row & 6) : ((row & 1) << 2);  // keys: rows 2i, 2i+1 at 4 units; values: rows 0, 2, 4, 6 at 2 units
+    else
+        s = kValue ? (row >> 1) & (kUnits - 1) : (row * kRow / 128) & (kUnits - 1);
+    return row * kRow + ((unit ^ s) << 4);
+}
+
+// Element d that lane quarter c's pair index (k16 step, which of its 4 elements)
+// of a quantised key stands for: a lane reads whole pieces, and the query is laid
+// out to match.
+template <int kType, int D>
+__device__ __forceinline__ int key_element(int c, int step, int e)
+{
+    if (kType == kKvBf16)
+        return step * 16 + 2 * c + (e & 1) + (e >> 1) * 8;
+    if (kType == kKvFp8) {  // word `step` of the lane's words: pairs (0, 2) and (1, 3) of its 4 codes
+        const int d = (e & 1) * 2 + (e >> 1);
+        return ((step >> 2) * 4 + c) * 16 + (step & 3) * 4 + d;
+    }
+    // INT4: two steps a word, pairs (0, 4), (1, 5) then (2, 6), (3, 7) of its 8 codes; the four
+    // words of a step's lanes are 32 elements side by side, which lie in one group
+    return ((step >> 1) * 4 + c) * 8 + (step & 1) * 2 + (e >> 1) + (e & 1) * 4;
+}
+
+// Element d of value column n-tile j for lane group g.
+template <int kType, int D>
+__device__ __forceinline__ int value_element(int j, int g)
+{
+    if (kType == kKvBf16)
+        return j * 8 + g;
+    constexpr int kPiece = kType == kKvFp8 ? (D >= 128 ? 16 : 8) : (D == 256 ? 32 : D / 8);  // elements a lane reads at once
+    return (j / kPiece) * (8 * kPiece) + g * kPiece + j % kPiece;
+}
+
+template <int kType, int D, int MT>
+struct Walk {
+    using F = Format<kType, D>;
+    static constexpr bool kHalf = kType == kKvInt4;  // P and the values in fp16
+    static constexpr int kSteps = D / 16;
+    static constexpr int kCols = D / 8;
+
+    const AttnParams &p;
+    uint32_t ring;            // this warp's ring (shared address)
+    uint32_t qs;              // the block's query fragments (shared address)
+    uint32_t qsum;            // INT4: the sums of the query's groups [group][row] (shared address)
+    int lane, g, c, warp;
+    int groups;               // INT4 groups of a row
+    float o[MT][kCols][4];
+    float m[MT][2], l[MT][2];
+
+    __device__ __forceinline__ Walk(const AttnParams &params) : p(params) {}
+
+    // Starts the copies of chunk `pos` (its first key) of page `page` into stage s.
+    __device__ __forceinline__ void fetch(int s, int page, int head, int pos)
+    {
+        const bool ok = page >= 0;
+        const size_t row = kv_row(p.c, ok ? page : 0, head, pos);
+        const uint32_t dst = ring + s * F::kStage;
+        const uint8_t *k = p.c.k + row * F::kRow, *v = p.c.v + row * F::kRow;
+        constexpr int kUnits = F::kRow / 16;
+#pragma unroll
+        for (int i = 0; i < (kChunk * kUnits + 31) / 32; ++i) {
+            const int u = lane + 32 * i;
+            if (kChunk * kUnits >= 32 || u < kChunk * kUnits) {
+                const int r = u / kUnits, x = u % kUnits;
+                cp_async16(dst + piece_at<kType, D, false>(r, x), k + (size_t)u * 16, ok);
+                cp_async16(dst + F::kCodes + piece_at<kType, D, true>(r, x), v + (size_t)u * 16, ok);
+            }
+        }
+        if (kType == kKvFp8 && lane < 2)
+            cp_async16(dst + 2 * F::kCodes + lane * F::kScale, (lane ? p.c.vs : p.c.ks) + row, ok);
+        if (kType == kKvInt4) {  // 16 * groups * 2 bytes of each of the four arrays
+            const int n = groups * 2;
+            for (int u = lane; u < 4 * n; u += 32) {
+                const int a = u / n, x = u - a * n;
+                const uint8_t *src = a == 0 ? p.c.ks : a == 1 ? p.c.kb : a == 2 ? p.c.vs : p.c.vb;
+                cp_async16(dst + 2 * F::kCodes + a * F::kScale + x * 16, src + row * groups * 2 + x * 16, ok);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[i][j][e] = 0.f;
+            m[i][0] = m[i][1] = -INFINITY;
+            l[i][0] = l[i][1] = 0.f;
+        }
+    }
+
+    // Zeros in the place of what must not meet a zero weight: values past the
+    // last key (whatever lies there) and infinities and NaNs of the nodes' values.
+    // Returns whether a node held any. Warp-wide, only on chunks that reach past the context.
+    __device__ __forceinline__ bool tame(int s, int pos, int ctx, int keys)
+    {
+        const uint32_t v = ring + s * F::kStage + F::kCodes;
+        bool wild = false;
+        if (kType == kKvBf16) {
+            for (int u = lane; u < kChunk * F::kRow / 16; u += 32) {
+                const int r = u / (F::kRow / 16);
+                if (pos + r < ctx)
+                    continue;
+                const uint32_t a = v + u * 16;  // the permutation stays inside a row
+                uint32_t w[4];
+                lds_words<4>(w, a);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
+                    if (pos + r >= keys)
+                        w[i] = 0;
+                    else if (lo || hi) {
+                        wild = true;
+                        w[i] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
+                    }
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+            }
+        } else if (kType == kKvFp8) {
+            const uint32_t a = ring + s * F::kStage + 2 * F::kCodes + F::kScale + lane;
+            if (lane < kChunk && pos + lane >= ctx) {
+                const bool past = pos + lane >= keys;
+                if (past || lds_u8(a) == kFp8BadRow) {
+                    wild = !past;
+                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(1) : "memory");
+                }
+            }
+        } else {
+            const uint32_t a = ring + s * F::kStage + 2 * F::kCodes + 2 * F::kScale;
+            for (int u = lane; u < kChunk * groups; u += 32) {
+                const int r = u / groups;
+                if (pos + r < ctx)
+                    continue;
+                const bool past = pos + r >= keys;
+                const uint32_t sc = lds_u16(a + 2 * u), bi = lds_u16(a + F::kScale + 2 * u);
+                const bool bad = (sc & 0x7C00u) == 0x7C00u || (bi & 0x7C00u) == 0x7C00u;
+                if (past || bad) {
+                    wild |= !past;
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a + 2 * u), "h"((uint16_t)0) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a + F::kScale + 2 * u), "h"((uint16_t)0) : "memory");
+                }
+            }
+        }
+        return __any_sync(0xFFFFFFFFu, wild);
+    }
+
+    // One chunk: scores, softmax update, weighted values. `tail`: it reaches past
+    // the context, so the mask is looked at.
+    __device__ __forceinline__ void chunk(int s, int pos, bool tail, int b, int row0, const SeqLen &seq)
+    {
+        const uint32_t stage = ring + s * F::kStage;
+        float x[MT][2][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[i][n][e] = 0.f;
+
+        // scores
+        if (kType == kKvBf16) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                uint32_t kb[4];
+                const int r = (lane & 7) + ((lane >> 4) << 3);
+                ldmatrix4(kb, stage + piece_at<kType, D, false>(r, 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t qa[4];
+                    lds_words<4>(qa, qs + ((i * kSteps + k) * 32 + lane) * 16);
+                    mma16816<false>(x[i][0], qa, kb[0], kb[1]);
+                    mma16816<false>(x[i][1], qa, kb[2], kb[3]);
+                }
+            }
+        } else if (kType == kKvFp8) {
+            constexpr int kPieces = F::kRow / 64;  // of 16 bytes, for each lane of a row's four
+#pragma unroll
+            for (int y = 0; y < kPieces; ++y) {
+                uint32_t w[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    lds_words<4>(w[n], stage + piece_at<kType, D, false>(n * 8 + g, y * 4 + c));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t k00 = e4m3_lo_bf16x2(w[0][k]), k01 = e4m3_hi_bf16x2(w[0][k]);
+                    const uint32_t k10 = e4m3_lo_bf16x2(w[1][k]), k11 = e4m3_hi_bf16x2(w[1][k]);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        uint32_t qa[4];
+                        lds_words<4>(qa, qs + ((i * kSteps + y * 4 + k) * 32 + lane) * 16);
+                        mma16816<false>(x[i][0], qa, k00, k01);
+                        mma16816<false>(x[i][1], qa, k10, k11);
+                    }
+                }
+            }
+        } else {
+            const int spans = p.c.group / 32;  // 32-element spans of a group
+            int y = 0;
+            for (int grp = 0; grp < groups; ++grp) {
+                float z[MT][2][4];
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            z[i][n][e] = 0.f;
+                for (int span = 0; span < spans; ++span, ++y) {
+                    const uint32_t w0 = lds32(stage + piece_at<kType, D, false>(g, y) + c * 4);
+                    const uint32_t w1 = lds32(stage + piece_at<kType, D, false>(8 + g, y) + c * 4);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t k00 = int4_bf16x2(w0 >> (8 * k)), k01 = int4_bf16x2(w0 >> (8 * k + 4));
+                        const uint32_t k10 = int4_bf16x2(w1 >> (8 * k)), k11 = int4_bf16x2(w1 >> (8 * k + 4));
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            uint32_t qa[4];
+                            lds_words<4>(qa, qs + ((i * kSteps + 2 * y + k) * 32 + lane) * 16);
+                            mma16816<false>(z[i][0], qa, k00, k01);
+                            mma16816<false>(z[i][1], qa, k10, k11);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t a = stage + 2 * F::kCodes + 2 * ((n * 8 + 2 * c + e) * groups + grp);
+                        const float sc = __half2float(__ushort_as_half((unsigned short)lds_u16(a)));
+                        const float bi = fmaf(8.f, sc, __half2float(__ushort_as_half((unsigned short)lds_u16(a + F::kScale))));
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float sum = __uint_as_float(lds32(qsum + 4 * (grp * 16 * MT + i * 16 + h * 8 + g)));
+                                x[i][n][2 * h + e] += fmaf(sc, z[i][n][2 * h + e], bi * sum);
+                            }
+                    }
+            }
+        }
+
+        // softmax: this lane has keys 8n + 2c and 8n + 2c + 1 of rows g and g + 8
+        float vs[2][2];
+        float f[2][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                f[n][e] = p.scale_log2;
+                vs[n][e] = 1.f;
+                if (kType == kKvFp8) {
+                    const uint32_t a = stage + 2 * F::kCodes + n * 8 + 2 * c + e;
+                    f[n][e] *= fp8_scale(lds_u8(a));
+                    vs[n][e] = fp8_scale(lds_u8(a + F::kScale));
+                }
+            }
+        bool move = false;
+        float mx[MT][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = row0 + i * 16 + h * 8 + g;
+                const uint32_t *mask = nullptr;
+                int t = 0;
+                if (tail) {
+                    t = row / p.G;
+                    if (t < p.T)
+                        mask = attn_mask_row(p, b, t);
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float v = x[i][n][2 * h + e] * f[n][e];
+                        if (tail) {
+                            const int at = pos + n * 8 + 2 * c + e;
+                            const bool sees = t < p.T && at < seq.keys && (at < seq.ctx || attn_sees(p, mask, t, at - seq.ctx));
+                            v = sees ? v : -INFINITY;
+                        }
+                        x[i][n][2 * h + e] = v;
+                        top = fmaxf(top, v);
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                mx[i][h] = top;
+                move |= top > m[i][h] + kRescale || (m[i][h] == -INFINITY && top > -INFINITY);
+            }
+        if (__any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float to = fmaxf(m[i][h], mx[i][h]);
+                    const float by = to == -INFINITY ? 1.f : ex2(m[i][h] - to);
+                    m[i][h] = to;
+                    l[i][h] *= by;
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) {
+                        o[i][j][2 * h] *= by;
+                        o[i][j][2 * h + 1] *= by;
+                    }
+                }
+        }
+        uint32_t pa[MT][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float ref = m[i][h] == -INFINITY ? 0.f : m[i][h];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float a = ex2(x[i][n][2 * h] - ref), z = ex2(x[i][n][2 * h + 1] - ref);
+                    l[i][h] += a + z;
+                    // P to 16 bits: its rounding (2^-9 in bf16) is independent from key to key and
+                    // averages out; the sum l is of the unrounded P
+                    pa[i][2 * n + h] = kHalf ? pack2_f16(a, z) : pack2_bf16(a * vs[n][0], z * vs[n][1]);
+                }
+            }
+
+        // weighted values
+        const uint32_t vstage = stage + F::kCodes;
+        if (kType == kKvBf16) {
+#pragma unroll
+            for (int j = 0; j < kCols; j += 2) {
+                uint32_t vb[4];
+                const int r = lane & 15;
+                ldmatrix4_trans(vb, vstage + piece_at<kType, D, true>(r, j + (lane >> 4)));
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    mma16816<false>(o[i][j], pa[i], vb[0], vb[1]);
+                    mma16816<false>(o[i][j + 1], pa[i], vb[2], vb[3]);
+                }
+            }
+        } else {
+            constexpr int kPiece = kType == kKvFp8 ? (D >= 128 ? 16 : 8) : (D == 256 ? 32 : D / 8);  // elements
+            constexpr int kBytes = kType == kKvFp8 ? kPiece : kPiece / 2;
+            constexpr int kWords = kBytes / 4;
+            constexpr int kPer = kType == kKvFp8 ? 4 : 8;                                           // elements of a word
+            constexpr int kPieces = D / (8 * kPiece);
+#pragma unroll
+            for (int y = 0; y < kPieces; ++y) {
+                uint32_t w[4][4];  // keys 2c, 2c+1, 2c+8, 2c+9
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int r = 2 * c + (t & 1) + (t >> 1) * 8, byte = (y * 8 + g) * kBytes;
+                    lds_words<kWords>(w[t], vstage + piece_at<kType, D, true>(r, byte / 16) + byte % 16);
+                }
+                __half2 sc[2], bi[2];
+                if (kType == kKvInt4) {
+                    const int grp = ((y * 8 + g) * kPiece) / p.c.group;  // a piece lies in one group
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t a = stage + 2 * F::kCodes + 2 * F::kScale + 2 * ((2 * c + 8 * t) * groups + grp);
+                        sc[t] = __halves2half2(__ushort_as_half((unsigned short)lds_u16(a)),
+                                               __ushort_as_half((unsigned short)lds_u16(a + 2 * groups)));
+                        bi[t] = __halves2half2(__ushort_as_half((unsigned short)lds_u16(a + F::kScale)),
+                                               __ushort_as_half((unsigned short)lds_u16(a + F::kScale + 2 * groups)));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) {
+                    uint32_t lo[2], hi[2];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {  // the two keys' low and high 16 bits side by side
+                        lo[t] = __byte_perm(w[2 * t][k], w[2 * t + 1][k], 0x5410);
+                        hi[t] = __byte_perm(w[2 * t][k], w[2 * t + 1][k], 0x7632);
+                    }
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) {
+                        uint32_t vb[2];
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (kType == kKvFp8) {
+                                const uint32_t z = e < 2 ? lo[t] : hi[t];
+                                vb[t] = (e & 1) ? e4m3_hi_bf16x2(z) : e4m3_lo_bf16x2(z);
+                            } else {
+                                vb[t] = int4_f16x2((e < 4 ? lo[t] : hi[t]) >> (4 * (e & 3)), sc[t], bi[t]);
+                            }
+                        }
+                        const int j = y * kPiece + k * kPer + e;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+                            mma16816<kHalf>(o[i][j], pa[i], vb[0], vb[1]);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// Element (row, d) of a block's rows, which the query was permuted from.
+__device__ __forceinline__ const uint16_t *query_row(const AttnParams &p, int b, int head, int row)
+{
+    const int t = row / p.G, h = head * p.G + row % p.G;
+    return p.q + ((size_t)b * p.T + t) * p.q_stride + (size_t)h * p.c.D;
+}
+
+// MT * 16 rows a block; grid: any number of CTAs up to kAttnMaxGrid.
+template <int kType, int D, int MT>
+__global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const AttnParams p, const int least)
+{
+    using W = Walk<kType, D, MT>;
+    using F = Format<kType, D>;
+    using S = Smem<kType, D, MT>;
+    constexpr int kRows = 16 * MT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ LineScratch scratch;
+    __shared__ int wild_any;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x;
+    const Line line(p, kTile, scratch);
+    const int ctas = attn_ctas(line.total, gridDim.x, least);
+    if ((int)blockIdx.x >= ctas || line.total == 0)
+        return;
+    long at = attn_first(line.total, ctas, blockIdx.x);
+    const long end = attn_first(line.total, ctas, blockIdx.x + 1);
+    const long first = at;
+    line.find(p, kTile, at, scratch);
+    int b = scratch.b;
+    long base = scratch.base;
+
+    uint8_t *qsm = smem + (S::kTotal - S::kQ);
+    W w(p);
+    w.lane = tid & 31;
+    w.warp = tid >> 5;
+    w.g = w.lane >> 2;
+    w.c = w.lane & 3;
+    w.ring = smem_addr(smem) + w.warp * F::kStages * F::kStage;
+    w.qs = smem_addr(qsm);
+    float *qsum = reinterpret_cast<float *>(qsm + 16 * MT * D * 2);
+    w.qsum = smem_addr(qsum);
+    w.groups = kType == kKvInt4 ? D / p.c.group : 0;
+    float *merge = reinterpret_cast<float *>(smem);  // [warp][row][D], then maxima and sums [warp][row]
+    float *merge_m = merge + kWarps * kRows * D, *merge_l = merge_m + kWarps * kRows;
+
+    while (at < end) {
+        SeqLen seq = attn_seq(p, b, kTile);
+        const long span = seq.tiles * line.per;
+        if (at >= base + span) {
+            base += span;
+            ++b;
+            continue;
+        }
+        if (seq.bad && tid == 0 && p.status)
+            atomicExch(p.status, kStatusBadArg);
+        const long in = at - base;
+        const int item = (int)(in / seq.tiles), t0 = (int)(in - (long)item * seq.tiles);
+        const int head = item / p.row_blocks, row0 = (item % p.row_blocks) * kRows;
+        const int t1 = (int)min((long)seq.tiles, t0 + (end - at));
+
+        // the query, as the fragments that the products take
+        for (int i = tid; i < MT * W::kSteps * 32 * 4; i += kAttnThreads) {
+            const int e = i & 3, ln = (i >> 2) & 31, k = (i >> 7) % W::kSteps, mt = (i >> 7) / W::kSteps;
+            const int row = row0 + mt * 16 + (ln >> 2) + (e & 1) * 8;  // a0, a2: row g; a1, a3: row g + 8
+            uint32_t v = 0;
+            if (row < p.rows) {
+                const uint16_t *q = query_row(p, b, head, row);
+                const int d0 = key_element<kType, D>(ln & 3, k, (e >> 1) * 2), d1 = key_element<kType, D>(ln & 3, k, (e >> 1) * 2 + 1);
+                v = (uint32_t)q[d0] | ((uint32_t)q[d1] << 16);
+            }
+            reinterpret_cast<uint32_t *>(qsm)[i] = v;
+        }
+        if (kType == kKvInt4)
+            for (int i = tid; i < kRows * w.groups; i += kAttnThreads) {
+                const int row = row0 + i % kRows, grp = i / kRows;
+                float sum = 0.f;
+                if (row < p.rows) {
+                    const uint32_t *q = reinterpret_cast<const uint32_t *>(query_row(p, b, head, row) + grp * p.c.group);
+                    for (int d = 0; d < p.c.group / 2; ++d)
+                        sum += bf16_lo(q[d]) + bf16_hi(q[d]);
+                }
+                qsum[i] = sum;
+            }
+        if (tid == 0)
+            wild_any = 0;
+        __syncthreads();
+
+        w.clear();
+        // pages of the next 32 tiles' chunks, one a lane
+        int pages = -1, pages_next = -1;
+        const auto page_of = [&](int t) {
+            const long pos = (long)t * kTile + w.warp * kChunk;
+            return t < t1 && pos < seq.keys ? (int)kv_page(p.c, b, pos) : -1;
+        };
+        pages = page_of(t0 + w.lane);
+        pages_next = page_of(t0 + 32 + w.lane);
+        int fetched = t0;
+        const auto fetch_next = [&]() {
+            if (fetched < t1) {
+                const int i = (fetched - t0) & 31;
+                if (i == 0 && fetched > t0) {
+                    pages = pages_next;
+                    pages_next = page_of(fetched + 32 + w.lane);
+                }
+                const int page = __shfl_sync(0xFFFFFFFFu, pages, i);
+                const int pos = fetched * kTile + w.warp * kChunk;
+                if (pos < seq.keys) {
+                    if (page < 0 && w.lane == 0 && p.status)
+                        atomicExch(p.status, kStatusBadArg);
+                    w.fetch((fetched - t0) % F::kStages, page, head, pos);
+                }
+            }
+            ++fetched;
+            cp_commit();
+        };
+#pragma unroll
+        for (int s = 0; s < F::kStages - 1; ++s)
+            fetch_next();
+        bool wild = false;
+        int stage = 0;
+        for (int t = t0; t < t1; ++t) {
+            cp_wait<F::kStages - 2>();
+            __syncwarp();
+            fetch_next();
+            const int pos = t * kTile + w.warp * kChunk;
+            if (pos < seq.keys) {
+                const bool tail = pos + kChunk > seq.ctx;
+                if (tail) {
+                    wild |= w.tame(stage, pos, seq.ctx, seq.keys);
+                    __syncwarp();
+                    w.chunk(stage, pos, true, b, row0, seq);
+                } else {
+                    w.chunk(stage, pos, false, b, row0, seq);
+                }
+            }
+            stage = stage + 1 == F::kStages ? 0 : stage + 1;
+        }
+        cp_wait<0>();
+        if (wild && w.lane == 0)
+            wild_any = 1;
+        __syncthreads();
+
+        // join the warps
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float sum = w.l[i][h];
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                const int r = i * 16 + h * 8 + w.g;
+                if (w.c == 0) {
+                    merge_m[w.warp * kRows + r] = w.m[i][h];
+                    merge_l[w.warp * kRows + r] = sum;
+                }
+                float *row = merge + (size_t)(w.warp * kRows + r) * D;
+#pragma unroll
+                for (int j = 0; j < W::kCols; ++j) {  // lane quarter c holds columns 2c, 2c + 1 of n-tile j
+                    row[value_element<kType, D>(j, 2 * w.c)] = w.o[i][j][2 * h];
+                    row[value_element<kType, D>(j, 2 * w.c + 1)] = w.o[i][j][2 * h + 1];
+                }
+            }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == seq.tiles;
+        float *slot = p.part + (size_t)(2 * blockIdx.x + (at > first ? 1 : 0)) * attn_slot_floats(kRows, D);
+        for (int i = tid; i < kRows * (D / 4); i += kAttnThreads) {
+            const int r = i / (D / 4), d = (i % (D / 4)) * 4, row = row0 + r;
+            if (row >= p.rows)
+                continue;
+            float top = merge_m[r];
+#pragma unroll
+            for (int v = 1; v < kWarps; ++v)
+                top = fmaxf(top, merge_m[v * kRows + r]);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) {
+                const float f = ex2(merge_m[v * kRows + r] - ref);
+                sum += f * merge_l[v * kRows + r];
+                const float4 x = *reinterpret_cast<const float4 *>(merge + (size_t)(v * kRows + r) * D + d);
+                acc.x += f * x.x;
+                acc.y += f * x.y;
+                acc.z += f * x.z;
+                acc.w += f * x.w;
+            }
+            const int t = row / p.G, h = head * p.G + row % p.G;
+            if (wild_any) {
+                const int from = t0 * kTile, to = min(seq.keys, t1 * kTile);
+                acc.x += attn_wild_values(p, b, head, t, d, seq.ctx, from, to);
+                acc.y += attn_wild_values(p, b, head, t, d + 1, seq.ctx, from, to);
+                acc.z += attn_wild_values(p, b, head, t, d + 2, seq.ctx, from, to);
+                acc.w += attn_wild_values(p, b, head, t, d + 3, seq.ctx, from, to);
+            }
+            if (whole) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const size_t n = ((size_t)b * p.T + t) * p.q_heads + h;
+                *reinterpret_cast<uint2 *>(p.out + n * D + d) =
+                    make_uint2(pack2_bf16(acc.x * inv, acc.y * inv), pack2_bf16(acc.z * inv, acc.w * inv));
+                if (d == 0 && p.lse)
+                    p.lse[n] = top == -INFINITY ? (sum == 0.f ? -INFINITY : sum) : (top + log2f(sum)) * 0.6931471805599453f;
+            } else {
+                *reinterpret_cast<float4 *>(slot + (size_t)r * D + d) = acc;
+                if (d == 0) {
+                    slot[(size_t)kRows * D + r] = top;
+                    slot[(size_t)kRows * (D + 1) + r] = sum;
+                }
+            }
+        }
+        __syncthreads();
+        at += t1 - t0;
+    }
+}
+
+// Joins the segments of the items that more than one CTA worked on. A block
+// serves up to four rows of one item, a warp a row; lane i looks at segment i's
+// maximum and sum, and the warp adds the segments' sums in their order.
+template <int D>
+__global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnParams p, const int rows, const int tile, const int grid, const int least)
+{
+    __shared__ LineScratch scratch;
+    pdl_launch_dependents();
+    pdl_wait();
+    const Line line(p, tile, scratch);
+    if (line.total == 0)
+        return;
+    const int ctas = attn_ctas(line.total, grid, least);
+    // blockIdx.x: sequence, head, row block; blockIdx.y: four rows of it
+    const int blocks = p.c.heads * p.row_blocks;
+    const int b = blockIdx.x / blocks, item = blockIdx.x % blocks;
+    const SeqLen seq = attn_seq(p, b, tile);
+    if (seq.tiles == 0)
+        return;  // only when the page table holds nothing; the few-row kernel wrote nothing either
+    // the line's index of sequence b: the thread that has it in its run
+    if (b >= line.b0 && b < line.b1) {
+        long at = line.base;
+        for (int i = line.b0; i < b; ++i)
+            at += attn_seq(p, i, tile).tiles * line.per;
+        scratch.base = at;
+    }
+    __syncthreads();
+    const long from = scratch.base + (long)item * seq.tiles;
+    const int c0 = attn_cta_of(line.total, ctas, from), c1 = attn_cta_of(line.total, ctas, from + seq.tiles - 1);
+    if (c0 == c1)
+        return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.y * kWarps + warp, row = (item % p.row_blocks) * rows + r;
+    if (r >= rows || row >= p.rows)
+        return;
+    const size_t floats = attn_slot_floats(rows, D);
+    // a CTA's segment of this item is its first unless the CTA began before the item
+    const auto slot = [&](int c) {
+        return p.part + (size_t)(2 * c + (attn_first(line.total, ctas, c) < from ? 1 : 0)) * floats;
+    };
+    float top = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32)
+        top = fmaxf(top, slot(c)[(size_t)rows * D + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    constexpr int kVec = D / 32;  // floats a lane: 2, 4 or 8
+    float acc[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+        acc[i] = 0.f;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+        const float *s = slot(c);
+        const float f = ex2(s[(size_t)rows * D + r] - ref);
+        sum += f * s[(size_t)rows * (D + 1) + r];
+        const float2 *x = reinterpret_cast<const float2 *>(s + (size_t)r * D);
+#pragma unroll
+        for (int i = 0; i < kVec / 2; ++i) {
+            const float2 v = x[lane + 32 * i];
+            acc[2 * i] += f * v.x;
+            acc[2 * i + 1] += f * v.y;
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int t = row / p.G, h = (item / p.row_blocks) * p.G + row % p.G;
+    const size_t n = ((size_t)b * p.T + t) * p.q_heads + h;
+    uint32_t *out = reinterpret_cast<uint32_t *>(p.out + n * D);
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i)
+        out[lane + 32 * i] = pack2_bf16(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    if (lane == 0 && p.lse)
+        p.lse[n] = top == -INFINITY ? (sum == 0.f ? -INFINITY : sum) : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+constexpr int kLeastTiles = 2;  // tiles a CTA has at least, where there is a choice
+
+template <int kType, int D, int MT>
+cudaError_t launch_few(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
+{
+    constexpr int kRows = 16 * MT;
+    constexpr int kSmem = Smem<kType, D, MT>::kTotal;
+    p.row_blocks = (p.rows + kRows - 1) / kRows;
+    auto *kernel = hc_attn_few_kernel<kType, D, MT>;
+    static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (set != cudaSuccess)
+        return set;
+    static const int per_sm = [kernel] {  // of this build's kernel on this GPU type
+        int n = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kAttnThreads, kSmem) == cudaSuccess ? std::max(n, 1) : 1;
+    }();
+    const int grid = std::min(per_sm * cfg.sm_count, kAttnMaxGrid);
+    cudaLaunchConfig_t lc{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    lc.stream = stream;
+    lc.blockDim = dim3(kAttnThreads);
+    lc.gridDim = dim3(grid);
+    lc.dynamicSmemBytes = kSmem;
+    cudaError_t e = cudaLaunchKernelEx(&lc, kernel, p, kLeastTiles);
+    if (e != cudaSuccess)
+        return e;
+    lc.dynamicSmemBytes = 0;
+    const int used = std::min(kRows, p.rows);
+    lc.gridDim = dim3((unsigned)((long)p.B * p.c.heads * p.row_blocks), (unsigned)((used + kWarps - 1) / kWarps));
+    return cudaLaunchKernelEx(&lc, hc_attn_join_kernel<D>, p, kRows, kTile, grid, kLeastTiles);
+}
+
+template <int kType>
+cudaError_t launch_type(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t stream)
+{
+    switch (p.c.D) {
+    case 64: return p.rows <= 16 ? launch_few<kType, 64, 1>(p, cfg, stream) : launch_few<kType, 64, 2>(p, cfg, stream);
+    case 128: return p.rows <= 16 ? launch_few<kType, 128, 1>(p, cfg, stream) : launch_few<kType, 128, 2>(p, cfg, stream);
+    default: return launch_few<kType, 256, 1>(p, cfg, stream);
+    }
+}
+
+}  // namespace
+
+size_t attn_part_bytes(int B, int T, int q_heads, const KvView &c)
+{
+    const long rows = (long)T * (q_heads / c.heads);
+    const int block = rows <= 16 || c.D == 256 ? 16 : 32;
+    return sizeof(float) * 2 * kAttnMaxGrid * attn_slot_floats(block, c.D);
+}
+
+cudaError_t launch_tree_attention(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
+{
+    switch (p.c.type) {
+    case kKvBf16: return launch_type<kKvBf16>(p, cfg, stream);
+    case kKvFp8: return launch_type<kKvFp8>(p, cfg, stream);
+    default: return launch_type<kKvInt4>(p, cfg, stream);
+    }
+}
+
+}  // namespace tshc

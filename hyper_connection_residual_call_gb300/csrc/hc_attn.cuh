@@ -1,0 +1,188 @@
+// hc_attn.cuh -- what the tree attention's kernels share: how the work is cut
+// over the CTAs, where partial results lie, and which nodes a row sees.
+//
+// An item is one (sequence, key head, block of rows): its keys in tiles, all
+// with the same softmax rows. The items' tiles form one line, in the order
+// sequence, head, row block, tile, and CTA c of G takes the tiles
+// [c N / G, (c + 1) N / G) of it: every CTA has the same number of tiles (to
+// one) whatever the sequences' lengths are, and a long context is split over
+// as many CTAs as it takes. An item that lies within one CTA is written to the
+// output by it; the segments of the others go to the workspace, at most two
+// for a CTA (its first and its last item), and a second kernel joins them in
+// CTA order, so the result does not depend on timing.
+#pragma once
+
+#include "hc_kv.cuh"
+
+namespace tshc {
+
+constexpr int kAttnMaxGrid = 4 * 152;  // CTAs that can write partials (a launch takes at most this many)
+constexpr int kAttnThreads = 128;      // of every kernel that walks the line
+
+// Tiles of sequence b's items and its keys. A length that does not fit the page
+// table is cut to it (and recorded by the caller).
+struct SeqLen {
+    int ctx, keys, tiles;
+    bool bad;
+};
+
+__device__ __forceinline__ SeqLen attn_seq(const AttnParams &p, int b, int tile)
+{
+    SeqLen s;
+    const long cap = (long)p.c.max_pages << p.c.page_shift;
+    const int raw = __ldg(p.ctx_len + b);
+    s.ctx = (int)max(0l, min((long)raw, cap));
+    const long keys = min((long)s.ctx + p.T, cap);
+    s.bad = raw < 0 || (long)raw + p.T > cap;
+    s.keys = (int)keys;
+    s.tiles = (int)((keys + tile - 1) / tile);
+    return s;
+}
+
+struct LineScratch {
+    long warp_sum[kAttnThreads / 32];
+    long base;
+    int b;
+};
+
+// The line, scanned by all kAttnThreads threads of a block: `total` tiles; each
+// thread knows where its own run of sequences [b0, b1) lies.
+struct Line {
+    long total, base, sum, per;
+    int b0, b1;
+
+    __device__ __forceinline__ Line(const AttnParams &p, int tile, LineScratch &sc)
+    {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        const int chunk = (p.B + kAttnThreads - 1) / kAttnThreads;
+        per = (long)p.c.heads * p.row_blocks;
+        b0 = min(p.B, tid * chunk);
+        b1 = min(p.B, b0 + chunk);
+        sum = 0;
+        for (int b = b0; b < b1; ++b)
+            sum += attn_seq(p, b, tile).tiles * per;
+        long incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        if (lane == 31)
+            sc.warp_sum[warp] = incl;
+        __syncthreads();
+        long before = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kAttnThreads / 32; ++w) {
+            if (w < warp)
+                before += sc.warp_sum[w];
+            total += sc.warp_sum[w];
+        }
+        base = before + incl - sum;
+    }
+
+    // The sequence whose tiles hold x (x < total), in sc.b, and the line's index
+    // of its first tile, in sc.base.
+    __device__ __forceinline__ void find(const AttnParams &p, int tile, long x, LineScratch &sc) const
+    {
+        if (x >= base && x < base + sum) {  // one thread
+            long at = base;
+            int b = b0;
+            for (;; ++b) {
+                const long n = attn_seq(p, b, tile).tiles * per;
+                if (x < at + n)
+                    break;
+                at += n;
+            }
+            sc.base = at;
+            sc.b = b;
+        }
+        __syncthreads();
+    }
+};
+
+// CTAs that take part: none has fewer than `least` tiles but the only one.
+__device__ __forceinline__ int attn_ctas(long n, int grid, int least)
+{
+    return (int)max(1l, min((long)grid, n / least));
+}
+
+__device__ __forceinline__ long attn_first(long n, int ctas, int c) { return (long)c * n / ctas; }
+
+// The CTA whose range holds tile x.
+__device__ __forceinline__ int attn_cta_of(long n, int ctas, long x) { return (int)(((x + 1) * ctas - 1) / n); }
+
+// A partial slot: unnormalised sums [rows][D], then the rows' maxima (in units of
+// log2) and sums.
+__host__ __device__ __forceinline__ size_t attn_slot_floats(int rows, int D) { return (size_t)rows * (D + 2); }
+
+// Whether node row t sees position ctx + i (i >= 0).
+__device__ __forceinline__ bool attn_sees(const AttnParams &p, const uint32_t *mask_row, int t, int i)
+{
+    if (i >= p.T)
+        return false;
+    return p.mask ? ((__ldg(mask_row + (i >> 5)) >> (i & 31)) & 1u) != 0 : i <= t;
+}
+
+__device__ __forceinline__ const uint32_t *attn_mask_row(const AttnParams &p, int b, int t)
+{
+    return p.mask ? p.mask + (size_t)b * p.mask_stride + (size_t)t * p.mask_words : nullptr;
+}
+
+// One element of a stored value, as it would be read back (rare paths only).
+__device__ __forceinline__ float kv_value_at(const KvView &c, size_t row, int d)
+{
+    if (c.type == kKvBf16)
+        return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(c.v)[row * c.D + d] << 16);
+    if (c.type == kKvFp8) {
+        const __half_raw h = __nv_cvt_fp8_to_halfraw(c.v[row * c.D + d], __NV_E4M3);
+        return __half2float(__half(h)) * fp8_scale(c.vs[row]);
+    }
+    const size_t g = row * (size_t)(c.D / c.group) + d / c.group;
+    const int code = (c.v[row * (c.D / 2) + d / 2] >> (4 * (d & 1))) & 15;
+    return fmaf((float)code, __half2float(reinterpret_cast<const __half *>(c.vs)[g]), __half2float(reinterpret_cast<const __half *>(c.vb)[g]));
+}
+
+// The sum of the infinities and NaNs among element d of the nodes' values that
+// row t sees, for the nodes at positions [from, to) (0 where there are none).
+// The kernels put zeros in the place of such values of nodes -- in a product, a
+// zero weight would not keep them from the rows that do not see them -- and add
+// this where one was found.
+__device__ __noinline__ float attn_wild_values(const AttnParams &p, int b, int head, int t, int d, int ctx, int from, int to)
+{
+    const uint32_t *mask = attn_mask_row(p, b, t);
+    float sum = 0.f;
+    for (int pos = max(from, ctx); pos < to; ++pos) {
+        if (!attn_sees(p, mask, t, pos - ctx))
+            continue;
+        const long page = kv_page(p.c, b, pos);
+        if (page < 0)
+            continue;
+        const float v = kv_value_at(p.c, kv_row(p.c, page, head, pos), d);
+        if (!finite_f32(v))
+            sum += v;
+    }
+    return sum;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return reinterpret_cast<const uint32_t &>(v);
+}
+
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return reinterpret_cast<const uint32_t &>(v);
+}
+
+}  // namespace tshc

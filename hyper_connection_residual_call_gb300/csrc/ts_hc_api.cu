@@ -160,6 +160,19 @@ ts_status api_error(ts_status st, const char *fmt, ...)
     return st;
 }
 
+ts_status device_api(int *sm_count, unsigned **status)
+{
+    DeviceInfo dev;
+    const ts_status st = device_info(&dev);
+    if (st == TS_OK) {
+        *sm_count = dev.sm_count;
+        *status = dev.status;
+    }
+    return st;
+}
+
+ts_status cuda_error(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+
 ts_status check_shape_api(int M, int H, int C, int lowrank) { return check_shape(M, H, C, lowrank); }
 
 ts_status check_ple_shape(int H, int C)

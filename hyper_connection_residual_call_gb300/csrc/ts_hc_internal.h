@@ -22,4 +22,9 @@ ts_status check_module(const ts_hc_module *m, bool with_inject, int H, int C, in
 ts_status check_ple_shape(int H, int C);
 ts_status check_ple_module(const ts_hc_ple_module *m);
 
+// The current device's SM count and its status word.
+ts_status device_api(int *sm_count, unsigned **status);
+// The status and message of a failed CUDA call.
+ts_status cuda_error(cudaError_t e, const char *what);
+
 }  // namespace tshc

@@ -421,6 +421,196 @@ ts_status ts_hc_stack_ple(const void *emb, int T, const ts_hc_module *attn, cons
                           void *user, void *mixed_out, int max_chunk, int H, int C, int lowrank,
                           float eps, void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ---- a speculative decoding step: rotary positions, a quantised cache, tree attention, verification ----
+ *
+ * What a sublayer and the step around the stack need when a model decodes several drafted tokens at a
+ * time. A step has B sequences of T tokens each ("nodes"): node 0 is the last committed token, the
+ * others are drafts, a chain or a tree in which a node comes after its parent. The nodes' keys and
+ * values lie in the cache at positions ctx_len[b] .. ctx_len[b] + T - 1, after the sequence's
+ * ctx_len[b] committed ones. A step runs
+ *   ts_hc_tree_build   the nodes' masks and positions from their parents       (once)
+ *   ts_hc_rope         turns the query and key heads                           (per layer)
+ *   ts_hc_kv_write     stores the keys and values                              (per layer)
+ *   ts_hc_tree_attention                                                       (per layer)
+ *   ts_hc_verify       on ts_hc_exit_logits' logits: which drafts hold         (once)
+ *   ts_hc_kv_compact   moves the accepted nodes' rows to the committed ones    (per layer)
+ *
+ * Lengths, page ids, parents and tokens are device data, so that a step can be captured in a graph
+ * and replayed with other contents. What the host cannot check of them the kernels do: an id, a
+ * position or a length out of range is not followed (its row reads zeros and is not written) and
+ * TS_ERR_INVALID_ARG is recorded in the device status word (ts_hc_device_status).
+ * B == 0 or T == 0 (N == 0, n == 0) is a no-op, as M == 0 is above.
+ */
+
+typedef enum {
+    TS_ROPE_PLAIN = 0,        /* f_i = theta^(-2i/rot) */
+    TS_ROPE_LINEAR = 1,       /* f_i / factor: positions interpolated */
+    TS_ROPE_NTK = 2,          /* theta replaced by theta * factor^(rot/(rot-2)) */
+    TS_ROPE_BY_PARTS = 3      /* f_i / factor where f_i turns fewer than beta_slow times in
+                                 original_positions, f_i where more than beta_fast times, a
+                                 linear blend of the two between */
+} ts_rope_scaling_type;
+
+typedef struct {
+    int32_t type;             /* ts_rope_scaling_type */
+    float factor;             /* > 0 */
+    float original_positions; /* BY_PARTS: > 0 */
+    float beta_fast;          /* BY_PARTS: > beta_slow */
+    float beta_slow;          /* BY_PARTS: >= 0 */
+    float magnitude;          /* > 0: multiplies cos and sin (1 for none) */
+} ts_hc_rope_scaling;
+
+/*
+ * The cosines and sines of a rotary embedding: table fp32 [max_pos][rot/2][2] = (cos, sin) of
+ * pos * f_i, times magnitude, with the angle formed and reduced in 64 bits.
+ *
+ *   table    16-byte aligned, written; rot even, in [2, 1024]; theta > 1
+ *   scaling  NULL for TS_ROPE_PLAIN
+ */
+ts_status ts_hc_rope_table(float *table, int max_pos, int rot, double theta,
+                           const ts_hc_rope_scaling *scaling, cudaStream_t stream);
+
+/*
+ * Rotary positions for the query and key heads of N tokens, one launch:
+ *   (y0, y1) = (x0 c - x1 s, x0 s + x1 c),  (c, s) = table[positions[n]][i],  i < rot/2
+ * where pair i is (x[i], x[i + rot/2]) of the head, or (x[2i], x[2i+1]) when interleaved != 0.
+ * Elements rot .. D-1 of a head are copied. inverse != 0 turns the other way (s -> -s): the
+ * gradient of the operator, and what undoes it (up to rounding) for a magnitude of 1.
+ * fp32 arithmetic, rounded to bf16 once.
+ *
+ *   q, k            bf16: head h of token n at q + n*q_stride + h*D; strides in elements, multiples
+ *                   of 8, >= heads*D (a slice of a fused projection's output can be passed);
+ *                   k may be NULL with k_heads == 0
+ *   q_out, k_out    bf16, laid out likewise with their own strides; q_out == q with the same stride
+ *                   turns in place (buffers must not overlap otherwise)
+ *   positions       int32 [N], in [0, max_pos)
+ *   D               a multiple of 8 in [8, 1024]; rot even, 2 <= rot <= D
+ */
+ts_status ts_hc_rope(const void *q, long q_stride, const void *k, long k_stride, const int32_t *positions,
+                     const float *table, int max_pos, void *q_out, long q_out_stride, void *k_out,
+                     long k_out_stride, int N, int q_heads, int k_heads, int D, int rot, int interleaved,
+                     int inverse, cudaStream_t stream);
+
+typedef enum {
+    TS_KV_BF16 = 0,           /* bf16 [D] */
+    TS_KV_FP8 = 1,            /* e4m3 [D] and one scale 2^(byte - 127) a row: the smallest power of two
+                                 with max|x| <= 448 * scale, at least 2^-117. Byte 255 marks a row that
+                                 held an infinity or a NaN; it reads back as NaN. No code is a NaN */
+    TS_KV_INT4 = 2            /* uint8 [D/2], element 2i in the low nibble of byte i, and fp16 scale and
+                                 bias per group, as TS_W_INT4_AFFINE: x = q * scale + bias with
+                                 scale = (max - min) / 15, bias = min (rounded to fp16; values beyond
+                                 +-57344 saturate there), q = round((x - bias) / scale), ties to
+                                 even, in [0, 15]. A group that held an infinity or a NaN reads back as NaN */
+} ts_kvtype;
+
+/*
+ * A paged cache of one layer's keys and values. Position p of sequence b lies in page
+ * page_table[b][p / page_size] at place p % page_size. "Row" is one token's vector of one head.
+ * Codes are [n_pages][n_kv_heads][page_size][row], scales likewise: FP8 uint8
+ * [n_pages][n_kv_heads][page_size], INT4 fp16 [n_pages][n_kv_heads][page_size][head_dim/group].
+ */
+typedef struct {
+    int32_t type;             /* ts_kvtype */
+    int32_t group;            /* INT4: 32, 64 or 128, at most head_dim */
+    int32_t page_size;        /* a power of two in [16, 1024] */
+    int32_t n_kv_heads;       /* [1, 1024] */
+    int32_t head_dim;         /* 64, 128 or 256 */
+    int32_t max_pages;        /* entries per sequence of page_table */
+    long n_pages;
+    void *k, *v;              /* 16-byte aligned, as are the scales and biases */
+    void *k_scales, *v_scales; /* FP8, INT4; else NULL */
+    void *k_biases, *v_biases; /* INT4; else NULL */
+    const int32_t *page_table; /* int32 [B][max_pages] */
+} ts_hc_kv_cache;
+
+/*
+ * Stores T tokens' keys and values of B sequences at positions ctx_len[b] .. ctx_len[b] + T - 1,
+ * quantised to the cache's type.
+ *   k, v      bf16: head h of token t of sequence b at k + (b*T + t)*k_stride + h*D; strides in
+ *             elements, multiples of 8, >= n_kv_heads*D; 16-byte aligned
+ *   ctx_len   int32 [B]
+ * Two nodes never share a place unless two page-table entries are the same page.
+ */
+ts_status ts_hc_kv_write(const void *k, long k_stride, const void *v, long v_stride, const ts_hc_kv_cache *cache,
+                         const int32_t *ctx_len, int B, int T, cudaStream_t stream);
+
+/*
+ * Reads positions start[b] .. start[b] + n - 1 of each sequence back as bf16 [B][n][n_kv_heads][D]
+ * (FP8 rows are exact in bf16; INT4's q * scale + bias is formed in fp32 and rounded once).
+ */
+ts_status ts_hc_kv_read(const ts_hc_kv_cache *cache, const int32_t *start, void *k_out, void *v_out, int B, int n,
+                        cudaStream_t stream);
+
+/*
+ * After a verification: the rows of the accepted nodes, at ctx_len[b] + path[b][i], move to
+ * ctx_len[b] + i for i = 1 .. n_accepted[b] (codes and scales as they are), and new_len[b] =
+ * ctx_len[b] + n_accepted[b] + 1. A path ascends, so that no row is overwritten before it is read.
+ *   path         int32 [B][T] and n_accepted int32 [B], as ts_hc_verify writes them
+ *   new_len      int32 [B] or NULL; must not be ctx_len
+ */
+ts_status ts_hc_kv_compact(const ts_hc_kv_cache *cache, const int32_t *ctx_len, const int32_t *path,
+                           const int32_t *n_accepted, int32_t *new_len, int B, int T, cudaStream_t stream);
+
+/*
+ * The masks and positions of B trees of T nodes. parents[b*parents_stride + i] is node i's parent,
+ * less than i; node 0 is the root (its entry is not read). parents_stride 0 shares one tree. A node
+ * i > 0 whose parent is negative is absent: no node sees it and it sees none of them.
+ *   mask       uint32 [B][T][(T+31)/32] or NULL: bit j%32 of word j/32 of row i is set where node i
+ *              sees node j (itself and its ancestors)
+ *   positions  int32 [B][T] or NULL: ctx_len[b] + the node's depth (ctx_len NULL: the depth)
+ */
+ts_status ts_hc_tree_build(const int32_t *parents, long parents_stride, const int32_t *ctx_len, uint32_t *mask,
+                           int32_t *positions, int B, int T, cudaStream_t stream);
+
+/*
+ * Attention of B*T nodes over the cache. Head h's keys and values are head h / (q_heads/n_kv_heads)
+ * of the cache. Row (b, t, h) sees the positions j < ctx_len[b], and ctx_len[b] + i for the nodes i
+ * that its mask row has (mask NULL: i <= t, a chain):
+ *   out = softmax_j(scale * q . k_j) v,   lse = log sum_j exp(scale * q . k_j)
+ * A row that sees nothing gets zeros and an lse of -infinity. What a row does not see does not
+ * reach it, whatever it holds: an infinity or a NaN in an unseen node's key or value (or in a page
+ * past the end) changes nothing.
+ *   q          bf16: head h of node t of sequence b at q + (b*T + t)*q_stride + h*D (a multiple of 8,
+ *              >= q_heads*D), 16-byte aligned
+ *   mask       uint32, sequence b's [T][(T+31)/32] at mask + b*mask_stride (words; 0 shares one)
+ *   out        bf16 [B][T][q_heads][D], 16-byte aligned; lse fp32 [B][T][q_heads] or NULL
+ *   workspace  >= ts_hc_tree_attention_workspace_bytes(...) bytes, 256-byte aligned; it need not be
+ *              initialised and must not be shared by calls that can run at the same time
+ * The products run on the tensor cores in bf16 (an INT4 row's values in fp16) with fp32 sums; the softmax's
+ * maximum and sum are fp32. T <= 4096, T * q_heads/n_kv_heads <= 32768.
+ */
+size_t ts_hc_tree_attention_workspace_bytes(int B, int T, int q_heads, const ts_hc_kv_cache *cache);
+ts_status ts_hc_tree_attention(const void *q, long q_stride, const ts_hc_kv_cache *cache, const int32_t *ctx_len,
+                               const uint32_t *mask, long mask_stride, void *out, float *lse, int B, int T,
+                               int q_heads, float scale, void *workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/*
+ * Which drafted tokens hold, and the token after them. Per sequence, from the root: p is the target's
+ * distribution at the node reached, softmax(logits / temperature), q the draft's, from which the
+ * node's children were drawn independently. With R = p and S = 1, for each child in node order, with
+ * x its token:
+ *     u * S * q[x] < R[x]:  the child is accepted; the walk goes on at it
+ *     otherwise:            R = max(R - S q, 0), S = sum R       (kept as max(p - c q, 0), c += S)
+ * and at the node where no child is left the next token is argmax_v R[v] / noise[v] over exponential
+ * variates (p in R's place where nothing is left of it), which draws from R. So the tokens are distributed as the
+ * target's own samples. A sequence with temperature <= 0 is greedy: a child holds where it is the argmax of
+ * the logits, and the next token is the argmax. Ties go to the lowest index.
+ *   logits       fp32 [B][T][V]: row i is the target's at node i (its successor's distribution)
+ *   draft_probs  fp32 [B][T][V]: row i is the draft's at node i; rows of nodes without children are
+ *                not read. NULL (with u and noise NULL): every sequence is greedy, temperature is not read
+ *   tokens       int32 [B][T]; parents as in ts_hc_tree_build (NULL: a chain)
+ *   temperature  fp32 [B]
+ *   u            fp32 [B][T], in [0, 1): node i's at u[b][i] (the root's is not read)
+ *   noise        fp32 [B][V], > 0
+ *   n_accepted   int32 [B]; path int32 [B][T]: 0 and the accepted nodes, then -1; next_token int32 [B]
+ * Only the rows that a walk reaches are read. T <= 4096, V < 2^30.
+ */
+ts_status ts_hc_verify(const float *logits, const float *draft_probs, const int32_t *tokens,
+                       const int32_t *parents, long parents_stride, const float *temperature, const float *u,
+                       const float *noise, int32_t *n_accepted, int32_t *path, int32_t *next_token, int B, int T,
+                       int V, cudaStream_t stream);
+
 /*
  * Self-test of the failure path. Launches one thread that waits, with the same
  * bounded wait the kernels use for their asynchronous copies, on a
