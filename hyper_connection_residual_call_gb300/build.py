@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libts_hc.so")
 
 SOURCES = ["ts_hc_api.cu", "ts_hc_stack.cu", "hc_gemv.cu", "hc_tc.cu", "hc_ple.cu",
-           "ts_hc_spec_api.cu", "hc_rope.cu", "hc_kv.cu", "hc_attn.cu", "hc_verify.cu"]
+           "ts_hc_spec_api.cu", "hc_rope.cu", "hc_kv.cu", "hc_attn.cu", "hc_attn_tc.cu", "hc_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -22,6 +22,7 @@
 //   q . k = sum_groups scale (sum Q (q - 8)) + (bias + 8 scale) sum Q
 // An INT4 value becomes q * scale + bias in fp16.
 #include <algorithm>
+#include <type_traits>
 
 #include "hc_attn.cuh"
 
@@ -576,7 +577,7 @@ __device__ __forceinline__ const uint16_t *query_row(const AttnParams &p, int b,
 
 // MT * 16 rows a block; grid: any number of CTAs up to kAttnMaxGrid.
 template <int kType, int D, int MT>
-__global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const AttnParams p, const int least)
+__global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const __grid_constant__ AttnParams p, const int least)
 {
     using W = Walk<kType, D, MT>;
     using F = Format<kType, D>;
@@ -592,12 +593,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const Attn
     const int ctas = attn_ctas(line.total, gridDim.x, least);
     if ((int)blockIdx.x >= ctas || line.total == 0)
         return;
-    long at = attn_first(line.total, ctas, blockIdx.x);
-    const long end = attn_first(line.total, ctas, blockIdx.x + 1);
-    const long first = at;
-    line.find(p, kTile, at, scratch);
-    int b = scratch.b;
-    long base = scratch.base;
+    const Cut cut(line.total, ctas);
+    Items it;
+    it.at = it.first = cut.first(blockIdx.x);
+    it.end = cut.first(blockIdx.x + 1);
+    line.find(p, kTile, it.at, scratch);
+    it.b = scratch.b;
+    it.base = scratch.base;
 
     uint8_t *qsm = smem + (S::kTotal - S::kQ);
     W w(p);
@@ -613,20 +615,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const Attn
     float *merge = reinterpret_cast<float *>(smem);  // [warp][row][D], then maxima and sums [warp][row]
     float *merge_m = merge + kWarps * kRows * D, *merge_l = merge_m + kWarps * kRows;
 
-    while (at < end) {
-        SeqLen seq = attn_seq(p, b, kTile);
-        const long span = seq.tiles * line.per;
-        if (at >= base + span) {
-            base += span;
-            ++b;
-            continue;
-        }
+    while (it.next(p, kTile)) {
+        const SeqLen seq = it.seq;
+        const int b = it.b, head = it.head, row0 = it.block * kRows, t0 = it.t0, t1 = it.t1;
         if (seq.bad && tid == 0 && p.status)
             atomicExch(p.status, kStatusBadArg);
-        const long in = at - base;
-        const int item = (int)(in / seq.tiles), t0 = (int)(in - (long)item * seq.tiles);
-        const int head = item / p.row_blocks, row0 = (item % p.row_blocks) * kRows;
-        const int t1 = (int)min((long)seq.tiles, t0 + (end - at));
 
         // the query, as the fragments that the products take
         for (int i = tid; i < MT * W::kSteps * 32 * 4; i += kAttnThreads) {
@@ -731,8 +724,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const Attn
                 }
             }
         __syncthreads();
-        const bool whole = t0 == 0 && t1 == seq.tiles;
-        float *slot = p.part + (size_t)(2 * blockIdx.x + (at > first ? 1 : 0)) * attn_slot_floats(kRows, D);
+        const bool whole = it.whole();
+        float *slot = p.part + (size_t)(2 * blockIdx.x + it.slot()) * attn_slot_floats(kRows, D);
         for (int i = tid; i < kRows * (D / 4); i += kAttnThreads) {
             const int r = i / (D / 4), d = (i % (D / 4)) * 4, row = row0 + r;
             if (row >= p.rows)
@@ -778,13 +771,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const Attn
             }
         }
         __syncthreads();
-        at += t1 - t0;
     }
 }
 
-// Joins the segments of the items that more than one CTA worked on. A block
-// serves up to four rows of one item, a warp a row; lane i looks at segment i's
-// maximum and sum, and the warp adds the segments' sums in their order.
+// Joins the segments of the items that more than one CTA worked on: a warp a row,
+// lane i with the maximum and the sum of segment i (of up to 32 at a time), and the
+// segments' rows added in their order, eight loads in flight. What the kernel costs
+// is its chain of dependent loads -- lengths, maxima, rows -- so that it does little else.
 template <int D>
 __global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnParams p, const int rows, const int tile, const int grid, const int least)
 {
@@ -799,8 +792,6 @@ __global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnPa
     const int blocks = p.c.heads * p.row_blocks;
     const int b = blockIdx.x / blocks, item = blockIdx.x % blocks;
     const SeqLen seq = attn_seq(p, b, tile);
-    if (seq.tiles == 0)
-        return;  // only when the page table holds nothing; the few-row kernel wrote nothing either
     // the line's index of sequence b: the thread that has it in its run
     if (b >= line.b0 && b < line.b1) {
         long at = line.base;
@@ -810,42 +801,70 @@ __global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnPa
     }
     __syncthreads();
     const long from = scratch.base + (long)item * seq.tiles;
-    const int c0 = attn_cta_of(line.total, ctas, from), c1 = attn_cta_of(line.total, ctas, from + seq.tiles - 1);
+    const Cut cut(line.total, ctas);
+    const int c0 = cut.cta_of(from), c1 = cut.cta_of(from + seq.tiles - 1);
     if (c0 == c1)
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = blockIdx.y * kWarps + warp, row = (item % p.row_blocks) * rows + r;
     if (r >= rows || row >= p.rows)
         return;
+    // A CTA's segment of this item is its first, unless it is CTA c0 and began before the item.
     const size_t floats = attn_slot_floats(rows, D);
-    // a CTA's segment of this item is its first unless the CTA began before the item
-    const auto slot = [&](int c) {
-        return p.part + (size_t)(2 * c + (attn_first(line.total, ctas, c) < from ? 1 : 0)) * floats;
-    };
-    float top = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32)
-        top = fmaxf(top, slot(c)[(size_t)rows * D + r]);
+    const int skew = cut.first(c0) < from ? 1 : 0;
+    const auto slot = [&](int c) { return p.part + (size_t)(2 * c + (c == c0 ? skew : 0)) * floats; };
+    constexpr int kVec = D / 32 >= 4 ? 4 : 2;  // floats of a load
+    constexpr int kLoads = D / (32 * kVec);    // loads of a lane: 1, or 2 for D = 256
+    using Vec = typename std::conditional<kVec == 4, float4, float2>::type;
+    float acc[kLoads * kVec];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    constexpr int kVec = D / 32;  // floats a lane: 2, 4 or 8
-    float acc[kVec];
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
+    for (int i = 0; i < kLoads * kVec; ++i)
         acc[i] = 0.f;
-    float sum = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const float *s = slot(c);
-        const float f = ex2(s[(size_t)rows * D + r] - ref);
-        sum += f * s[(size_t)rows * (D + 1) + r];
-        const float2 *x = reinterpret_cast<const float2 *>(s + (size_t)r * D);
+    float sum = 0.f, top = -INFINITY;
+    for (int base = c0; base <= c1; base += 32) {
+        const int n = min(32, c1 - base + 1);
+        float m = -INFINITY, l = 0.f;
+        if (lane < n) {
+            const float *s = slot(base + lane);
+            m = s[(size_t)rows * D + r];
+            l = s[(size_t)rows * (D + 1) + r];
+        }
+        float now = m;
 #pragma unroll
-        for (int i = 0; i < kVec / 2; ++i) {
-            const float2 v = x[lane + 32 * i];
-            acc[2 * i] += f * v.x;
-            acc[2 * i + 1] += f * v.y;
+        for (int o = 16; o > 0; o >>= 1)
+            now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, o));
+        const float to = fmaxf(top, now), ref = to == -INFINITY ? 0.f : to;
+        const float by = ex2(top - ref);  // 0 at the first
+        const float f = ex2(m - ref);
+        top = to;
+        float part = f * l;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+        sum = sum * by + part;
+#pragma unroll
+        for (int i = 0; i < kLoads * kVec; ++i)
+            acc[i] *= by;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            Vec v[8][kLoads];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < n) {
+                    const Vec *x = reinterpret_cast<const Vec *>(slot(base + i0 + i) + (size_t)r * D);
+#pragma unroll
+                    for (int k = 0; k < kLoads; ++k)
+                        v[i][k] = __ldcg(x + lane + 32 * k);
+                }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < n) {
+                    const float g = __shfl_sync(0xFFFFFFFFu, f, i0 + i);
+#pragma unroll
+                    for (int k = 0; k < kLoads; ++k)
+#pragma unroll
+                        for (int e = 0; e < kVec; ++e)
+                            acc[k * kVec + e] += g * reinterpret_cast<const float *>(&v[i][k])[e];
+                }
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -853,8 +872,10 @@ __global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnPa
     const size_t n = ((size_t)b * p.T + t) * p.q_heads + h;
     uint32_t *out = reinterpret_cast<uint32_t *>(p.out + n * D);
 #pragma unroll
-    for (int i = 0; i < kVec / 2; ++i)
-        out[lane + 32 * i] = pack2_bf16(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    for (int k = 0; k < kLoads; ++k)
+#pragma unroll
+        for (int e = 0; e < kVec / 2; ++e)
+            out[(lane + 32 * k) * (kVec / 2) + e] = pack2_bf16(acc[k * kVec + 2 * e] * inv, acc[k * kVec + 2 * e + 1] * inv);
     if (lane == 0 && p.lse)
         p.lse[n] = top == -INFINITY ? (sum == 0.f ? -INFINITY : sum) : (top + log2f(sum)) * 0.6931471805599453f;
 }
@@ -889,10 +910,7 @@ cudaError_t launch_few(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
     cudaError_t e = cudaLaunchKernelEx(&lc, kernel, p, kLeastTiles);
     if (e != cudaSuccess)
         return e;
-    lc.dynamicSmemBytes = 0;
-    const int used = std::min(kRows, p.rows);
-    lc.gridDim = dim3((unsigned)((long)p.B * p.c.heads * p.row_blocks), (unsigned)((used + kWarps - 1) / kWarps));
-    return cudaLaunchKernelEx(&lc, hc_attn_join_kernel<D>, p, kRows, kTile, grid, kLeastTiles);
+    return launch_attn_join(p, kRows, kTile, grid, kLeastTiles, stream);
 }
 
 template <int kType>
@@ -907,15 +925,38 @@ cudaError_t launch_type(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t 
 
 }  // namespace
 
-size_t attn_part_bytes(int B, int T, int q_heads, const KvView &c)
+cudaError_t launch_attn_join(const AttnParams &p, int rows, int tile, int grid, int least, cudaStream_t stream)
+{
+    cudaLaunchConfig_t lc{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    lc.stream = stream;
+    lc.blockDim = dim3(kAttnThreads);
+    const int used = std::min(rows, p.rows);
+    lc.gridDim = dim3((unsigned)((long)p.B * p.c.heads * p.row_blocks), (unsigned)((used + kWarps - 1) / kWarps));
+    switch (p.c.D) {
+    case 64: return cudaLaunchKernelEx(&lc, hc_attn_join_kernel<64>, p, rows, tile, grid, least);
+    case 128: return cudaLaunchKernelEx(&lc, hc_attn_join_kernel<128>, p, rows, tile, grid, least);
+    default: return cudaLaunchKernelEx(&lc, hc_attn_join_kernel<256>, p, rows, tile, grid, least);
+    }
+}
+
+size_t attn_part_bytes(int, int T, int q_heads, const KvView &c)
 {
     const long rows = (long)T * (q_heads / c.heads);
-    const int block = rows <= 16 || c.D == 256 ? 16 : 32;
-    return sizeof(float) * 2 * kAttnMaxGrid * attn_slot_floats(block, c.D);
+    const int wide = attn_wide_rows(c, rows);
+    if (wide)
+        return sizeof(float) * 2 * kAttnWideGrid * attn_slot_floats(wide, c.D);
+    return sizeof(float) * 2 * kAttnMaxGrid * attn_slot_floats(rows <= 16 || c.D == 256 ? 16 : 32, c.D);
 }
 
 cudaError_t launch_tree_attention(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
 {
+    if (attn_wide_rows(p.c, p.rows))
+        return launch_attn_wide(p, cfg, stream);
     switch (p.c.type) {
     case kKvBf16: return launch_type<kKvBf16>(p, cfg, stream);
     case kKvFp8: return launch_type<kKvFp8>(p, cfg, stream);

@@ -4,7 +4,7 @@
 // An item is one (sequence, key head, block of rows): its keys in tiles, all
 // with the same softmax rows. The items' tiles form one line, in the order
 // sequence, head, row block, tile, and CTA c of G takes the tiles
-// [c N / G, (c + 1) N / G) of it: every CTA has the same number of tiles (to
+// its N/G tiles of it: every CTA has the same number of tiles (to
 // one) whatever the sequences' lengths are, and a long context is split over
 // as many CTAs as it takes. An item that lies within one CTA is written to the
 // output by it; the segments of the others go to the workspace, at most two
@@ -17,7 +17,8 @@
 namespace tshc {
 
 constexpr int kAttnMaxGrid = 4 * 152;  // CTAs that can write partials (a launch takes at most this many)
-constexpr int kAttnThreads = 128;      // of every kernel that walks the line
+constexpr int kAttnWideGrid = 160;     // the same for the wide kernel, one CTA an SM
+constexpr int kAttnThreads = 128;
 
 // Tiles of sequence b's items and its keys. A length that does not fit the page
 // table is cut to it (and recorded by the caller).
@@ -39,14 +40,16 @@ __device__ __forceinline__ SeqLen attn_seq(const AttnParams &p, int b, int tile)
     return s;
 }
 
+constexpr int kAttnMaxWarps = 16;
+
 struct LineScratch {
-    long warp_sum[kAttnThreads / 32];
+    long warp_sum[kAttnMaxWarps];
     long base;
     int b;
 };
 
-// The line, scanned by all kAttnThreads threads of a block: `total` tiles; each
-// thread knows where its own run of sequences [b0, b1) lies.
+// The line, scanned by all threads of a block (kAttnThreads at least, whose first
+// kAttnThreads each take a run of sequences [b0, b1)): `total` tiles.
 struct Line {
     long total, base, sum, per;
     int b0, b1;
@@ -73,8 +76,7 @@ struct Line {
         __syncthreads();
         long before = 0;
         total = 0;
-#pragma unroll
-        for (int w = 0; w < kAttnThreads / 32; ++w) {
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) {
             if (w < warp)
                 before += sc.warp_sum[w];
             total += sc.warp_sum[w];
@@ -108,10 +110,54 @@ __device__ __forceinline__ int attn_ctas(long n, int grid, int least)
     return (int)max(1l, min((long)grid, n / least));
 }
 
-__device__ __forceinline__ long attn_first(long n, int ctas, int c) { return (long)c * n / ctas; }
+// How the line is cut: the first `more` CTAs have share + 1 tiles, the others share.
+struct Cut {
+    long share, more;
+    __device__ __forceinline__ Cut(long n, int ctas) : share(n / ctas), more(n - share * ctas) {}
+    __device__ __forceinline__ long first(int c) const { return c * share + min((long)c, more); }
+    // The CTA whose range holds tile x.
+    __device__ __forceinline__ int cta_of(long x) const
+    {
+        const long big = more * (share + 1);
+        return x < big ? (int)(x / (share + 1)) : (int)(more + (x - big) / share);
+    }
+};
 
-// The CTA whose range holds tile x.
-__device__ __forceinline__ int attn_cta_of(long n, int ctas, long x) { return (int)(((x + 1) * ctas - 1) / n); }
+// A CTA's items in turn: the tiles [t0, t1) of one item each.
+struct Items {
+    long at, end, first, base;
+    long from;                // the line's index of this segment's first tile
+    int b, head, block, t0, t1;
+    SeqLen seq;
+
+    // (A call of its own in kernels whose roles each walk the items: their code has to
+    // fit the instruction caches.)
+    __device__ __noinline__ bool next(const AttnParams &p, int tile)
+    {
+        while (at < end) {
+            seq = attn_seq(p, b, tile);
+            const long span = (long)seq.tiles * p.c.heads * p.row_blocks;
+            if (at >= base + span) {
+                base += span;
+                ++b;
+                continue;
+            }
+            const long in = at - base;
+            const int item = span <= 0x7FFFFFFF ? (int)in / seq.tiles : (int)(in / seq.tiles);
+            t0 = (int)(in - (long)item * seq.tiles);
+            head = item / p.row_blocks;
+            block = item - head * p.row_blocks;
+            t1 = (int)min((long)seq.tiles, t0 + (end - at));
+            from = at;
+            at += t1 - t0;
+            return true;
+        }
+        return false;
+    }
+    // Whether the segment is all of its item, and if not, which of the CTA's two slots it takes.
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == seq.tiles; }
+    __device__ __forceinline__ int slot() const { return from > first ? 1 : 0; }
+};
 
 // A partial slot: unnormalised sums [rows][D], then the rows' maxima (in units of
 // log2) and sums.
@@ -149,7 +195,7 @@ __device__ __forceinline__ float kv_value_at(const KvView &c, size_t row, int d)
 // The kernels put zeros in the place of such values of nodes -- in a product, a
 // zero weight would not keep them from the rows that do not see them -- and add
 // this where one was found.
-__device__ __noinline__ float attn_wild_values(const AttnParams &p, int b, int head, int t, int d, int ctx, int from, int to)
+static __device__ __noinline__ float attn_wild_values(const AttnParams &p, int b, int head, int t, int d, int ctx, int from, int to)
 {
     const uint32_t *mask = attn_mask_row(p, b, t);
     float sum = 0.f;
@@ -164,6 +210,19 @@ __device__ __noinline__ float attn_wild_values(const AttnParams &p, int b, int h
             sum += v;
     }
     return sum;
+}
+
+// Which of the 32 positions ctx + n0 .. ctx + n0 + 31 node row t sees (n0 may be
+// negative: the context), bit i for ctx + n0 + i.
+static __device__ __noinline__ uint32_t attn_sees32(const AttnParams &p, const uint32_t *mask_row, int t, int n0, const SeqLen &seq)
+{
+    const auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
+    const uint32_t present = low(seq.keys - seq.ctx - n0);
+    if (!p.mask)
+        return low(t + 1 - n0) & present;
+    const int w = n0 >> 5;
+    const auto word = [&](int i) { return i < 0 ? 0xFFFFFFFFu : i < p.mask_words ? __ldg(mask_row + i) & low(p.T - 32 * i) : 0u; };
+    return __funnelshift_r(word(w), word(w + 1), n0 & 31) & present;
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -184,5 +243,11 @@ __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi)
     const __half2 v = __floats2half2_rn(lo, hi);
     return reinterpret_cast<const uint32_t &>(v);
 }
+
+// The wide kernel's rows of a block (0: the few-row kernel serves) and its launcher.
+int attn_wide_rows(const KvView &c, long rows);
+cudaError_t launch_attn_wide(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t stream);
+// Joins the segments that either kernel left: blocks of `rows` rows, tiles of `tile` keys.
+cudaError_t launch_attn_join(const AttnParams &p, int rows, int tile, int grid, int least, cudaStream_t stream);
 
 }  // namespace tshc

@@ -1053,6 +1053,15 @@ bool make_map_kblocks(CUtensorMap *map, const void *base, uint64_t rows, uint64_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+bool tc_make_map_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows)
+{
+    return make_map(map, base, rows, cols, box_cols, box_rows, true);
+}
+
+namespace {
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_tc(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                       int cluster_x, Args &&...args)

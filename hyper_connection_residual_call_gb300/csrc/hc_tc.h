@@ -1,6 +1,7 @@
 // hc_tc.h -- launch parameters of the tensor-core (tcgen05) batched path.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -121,5 +122,8 @@ struct TcCall {
 size_t tc_down_smem(int NT, int ns, int wt);
 size_t tc_up_smem(int NT, int ns, int C, int HBt, int wt);
 cudaError_t launch_tc_call(const TcCall &t, cudaStream_t stream);
+
+// A tensor map of a row-major bf16 matrix, 128-byte swizzled boxes (box_cols <= 64).
+bool tc_make_map_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows);
 
 }  // namespace tshc
