@@ -774,17 +774,25 @@ def hc_stack(emb, layers, final, sublayer, *, C: int, max_chunk: Optional[int] =
 
 # ------------------------------------------------------------- a speculative decoding step
 
+# These calls run once per layer and step on a few rows, where their host time is what counts: what is
+# checked for every tensor is checked here with a few attribute reads, and the errors are worded elsewhere.
+
 def _rows(t, name):
     """(tokens, heads, D, token stride) of bf16 rows [N, heads, D] or [B, T, heads, D]: each token's
     heads side by side, the tokens at one stride (a slice of a projection's output will do)."""
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise HCError(TS_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    try:
+        ok = t.dtype is torch.bfloat16 and t.is_cuda
+        shape, stride = t.shape, t.stride()
+    except AttributeError:
+        ok = False
+    if not ok:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise HCError(TS_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
         raise HCError(TS_ERR_INVALID_ARG, f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    shape, stride = t.shape, t.stride()
     if len(shape) == 3:
-        (n, h, d), step = shape, stride[0]
+        n, h, d = shape
+        step = stride[0]
     elif len(shape) == 4:
         b, n, h, d = shape
         step = stride[1] if n != 1 else stride[0]
@@ -793,9 +801,27 @@ def _rows(t, name):
         n *= b
     else:
         raise HCError(TS_ERR_INVALID_ARG, f"{name} has shape {tuple(shape)}, expected [tokens, heads, D] or [B, T, heads, D]")
-    if (d > 1 and stride[-1] != 1) or (h > 1 and stride[-2] != d):
+    if (stride[-1] != 1 and d > 1) or (stride[-2] != d and h > 1):
         raise HCError(TS_ERR_INVALID_ARG, f"{name}: a token's heads must lie side by side, strides are {tuple(stride)}")
     return n, h, d, step if n > 1 else h * d
+
+
+def _is(t, name, dtype, shape=None):
+    """``_need`` with its common answer found first; returns the address."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (shape is None or t.shape == shape):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _stream_of(stream, t) -> int:
+    """The handle of ``stream``, or of the stream that is current on ``t``'s device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())  # current_stream() without its object: 0.1 us for 3
 
 
 def _made(t, stream):
@@ -820,7 +846,9 @@ def hc_rope(q, k, positions, table, *, interleaved: bool = False, inverse: bool 
     torch = _torch()
     n, hq, d, sq = _rows(q, "q")
     if q_out is None:
-        q_out = _made(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream)
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if stream is not None:
+            q_out.record_stream(stream)
         so = hq * d
     else:
         no, ho, do, so = _rows(q_out, "q_out")
@@ -829,25 +857,29 @@ def hc_rope(q, k, positions, table, *, interleaved: bool = False, inverse: bool 
     hk, sk, sko, kp, kop = 0, 0, 0, None, None
     if k is not None:
         nk, hk, dk, sk = _rows(k, "k")
-        if (nk, dk) != (n, d):
+        if nk != n or dk != d:
             raise HCError(TS_ERR_INVALID_ARG, f"k has shape {tuple(k.shape)}, q has {tuple(q.shape)}")
         if k_out is None:
-            k_out = _made(torch.empty(k.shape, dtype=torch.bfloat16, device=k.device), stream)
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+            if stream is not None:
+                k_out.record_stream(stream)
             sko = hk * d
         else:
             no, ho, do, sko = _rows(k_out, "k_out")
             if (no, ho, do) != (n, hk, d):
                 raise HCError(TS_ERR_INVALID_ARG, f"k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
         kp, kop = k.data_ptr(), k_out.data_ptr()
-    _need(positions, "positions", torch.int32)
+    pp = _is(positions, "positions", torch.int32)
     if positions.numel() != n:
         raise HCError(TS_ERR_INVALID_ARG, f"positions has {positions.numel()} entries for {n} tokens")
-    _need(table, "table", torch.float32)
-    if table.dim() != 3 or table.shape[2] != 2:
-        raise HCError(TS_ERR_INVALID_ARG, f"table has shape {tuple(table.shape)}, expected [max_pos, rot/2, 2]")
-    _check(library().ts_hc_rope(q.data_ptr(), sq, kp, sk, positions.data_ptr(), table.data_ptr(), table.shape[0],
-                                q_out.data_ptr(), so, kop, sko, n, hq, hk, d, 2 * table.shape[1], interleaved, inverse,
-                                _stream_handle(stream)))
+    tp = _is(table, "table", torch.float32)
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2:
+        raise HCError(TS_ERR_INVALID_ARG, f"table has shape {tuple(shape)}, expected [max_pos, rot/2, 2]")
+    st = (_lib or library()).ts_hc_rope(q.data_ptr(), sq, kp, sk, pp, tp, shape[0], q_out.data_ptr(), so, kop, sko, n, hq, hk, d,
+                                        2 * shape[1], interleaved, inverse, _stream_of(stream, q))
+    if st:
+        _check(st)
     return q_out, k_out
 
 
@@ -885,6 +917,7 @@ class KVCache:
                 _need(t, "cache." + name, torch.float16, (pages, heads, size, d // group))
         self.kind, self.group, self.page_size, self.heads, self.head_dim = kind, group, size, heads, d
         self.batch, self.max_pages = page_table.shape
+        self.lengths = (self.batch,)
         self.tensors = (k, v, page_table, k_scale, v_scale, k_bias, v_bias)  # kept alive with the struct
         self.struct = TsHcKvCache(kinds[kind], group, size, heads, d, self.max_pages, pages, k.data_ptr(), v.data_ptr(),
                                   *(t.data_ptr() if t is not None else None for t in (k_scale, v_scale, k_bias, v_bias)),
@@ -908,22 +941,21 @@ def kv_cache(kind: str, pages: int, heads: int, page_size: int, head_dim: int, p
     return KVCache(kind, k, v, page_table, k_scale=ks, v_scale=vs, k_bias=kb, v_bias=vb, group=group)
 
 
-def _lengths(t, name, batch):
-    _need(t, name, _torch().int32, (batch,))
-
-
 def hc_kv_write(k, v, cache: KVCache, ctx_len, *, stream=None):
     """Stores ``k``, ``v`` [B, T, heads, D] bf16 at positions ctx_len[b] .. ctx_len[b] + T - 1, quantised to
     the cache's kind; ``ctx_len`` int32 [B]. Returns the cache."""
-    n, h, d, sk = _rows(k, "k")
-    nv, hv, dv, sv = _rows(v, "v")
-    if k.dim() != 4 or k.shape[0] != cache.batch or (h, d) != (cache.heads, cache.head_dim):
-        raise HCError(TS_ERR_INVALID_ARG, f"k has shape {tuple(k.shape)}, expected [{cache.batch}, T, {cache.heads}, {cache.head_dim}]")
-    if v.shape != k.shape:
-        raise HCError(TS_ERR_INVALID_ARG, f"v has shape {tuple(v.shape)}, k has {tuple(k.shape)}")
-    _lengths(ctx_len, "ctx_len", cache.batch)
-    _check(library().ts_hc_kv_write(k.data_ptr(), sk, v.data_ptr(), sv, cache.ref, ctx_len.data_ptr(), cache.batch, k.shape[1],
-                                    _stream_handle(stream)))
+    _, h, d, sk = _rows(k, "k")
+    _, _, _, sv = _rows(v, "v")
+    shape = k.shape
+    if len(shape) != 4 or shape[0] != cache.batch or h != cache.heads or d != cache.head_dim:
+        raise HCError(TS_ERR_INVALID_ARG, f"k has shape {tuple(shape)}, expected [{cache.batch}, T, {cache.heads}, {cache.head_dim}]")
+    if v.shape != shape:
+        raise HCError(TS_ERR_INVALID_ARG, f"v has shape {tuple(v.shape)}, k has {tuple(shape)}")
+    st = (_lib or library()).ts_hc_kv_write(k.data_ptr(), sk, v.data_ptr(), sv, cache.ref,
+                                            _is(ctx_len, "ctx_len", _torch().int32, cache.lengths), cache.batch, shape[1],
+                                            _stream_of(stream, k))
+    if st:
+        _check(st)
     return cache
 
 
@@ -932,17 +964,19 @@ def hc_kv_read(cache: KVCache, start, n: int, *, k_out=None, v_out=None, stream=
     Returns (k, v)."""
     torch = _torch()
     shape = (cache.batch, n, cache.heads, cache.head_dim)
-    _lengths(start, "start", cache.batch)
+    sp = _is(start, "start", torch.int32, cache.lengths)
     if k_out is None:
-        k_out = _made(torch.empty(shape, dtype=torch.bfloat16, device=start.device), stream)
-    else:
-        _need(k_out, "k_out", torch.bfloat16, shape)
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=start.device)
+        if stream is not None:
+            k_out.record_stream(stream)
     if v_out is None:
-        v_out = _made(torch.empty(shape, dtype=torch.bfloat16, device=start.device), stream)
-    else:
-        _need(v_out, "v_out", torch.bfloat16, shape)
-    _check(library().ts_hc_kv_read(cache.ref, start.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), cache.batch, n,
-                                   _stream_handle(stream)))
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=start.device)
+        if stream is not None:
+            v_out.record_stream(stream)
+    st = (_lib or library()).ts_hc_kv_read(cache.ref, sp, _is(k_out, "k_out", torch.bfloat16, shape),
+                                           _is(v_out, "v_out", torch.bfloat16, shape), cache.batch, n, _stream_of(stream, start))
+    if st:
+        _check(st)
     return k_out, v_out
 
 
@@ -950,16 +984,17 @@ def hc_kv_compact(cache: KVCache, ctx_len, path, n_accepted, *, new_len=None, st
     """Moves the accepted nodes' rows (``path`` int32 [B, T] and ``n_accepted`` int32 [B] of ``hc_verify``)
     to the positions after ``ctx_len``; returns new_len int32 [B] = ctx_len + n_accepted + 1."""
     torch = _torch()
-    _lengths(ctx_len, "ctx_len", cache.batch)
-    _lengths(n_accepted, "n_accepted", cache.batch)
-    _need(path, "path", torch.int32)
+    cp = _is(ctx_len, "ctx_len", torch.int32, cache.lengths)
+    np_ = _is(n_accepted, "n_accepted", torch.int32, cache.lengths)
+    pp = _is(path, "path", torch.int32)
     if path.dim() != 2 or path.shape[0] != cache.batch:
         raise HCError(TS_ERR_INVALID_ARG, f"path has shape {tuple(path.shape)}, expected [{cache.batch}, T]")
     if new_len is None:
         new_len = _made(torch.empty_like(ctx_len), stream)
-    _lengths(new_len, "new_len", cache.batch)
-    _check(library().ts_hc_kv_compact(cache.ref, ctx_len.data_ptr(), path.data_ptr(), n_accepted.data_ptr(), new_len.data_ptr(),
-                                      cache.batch, path.shape[1], _stream_handle(stream)))
+    st = (_lib or library()).ts_hc_kv_compact(cache.ref, cp, pp, np_, _is(new_len, "new_len", torch.int32, cache.lengths), cache.batch,
+                                              path.shape[1], _stream_of(stream, ctx_len))
+    if st:
+        _check(st)
     return new_len
 
 
@@ -976,7 +1011,7 @@ def hc_tree_build(parents, ctx_len=None, *, batch: Optional[int] = None, mask=No
     if parents.dim() > 2 or (batch is not None and batch != b):
         raise HCError(TS_ERR_INVALID_ARG, f"parents has shape {tuple(parents.shape)}, expected [B, T] or [T]")
     if ctx_len is not None:
-        _lengths(ctx_len, "ctx_len", b)
+        _need(ctx_len, "ctx_len", torch.int32, (b,))
     if mask is None:
         mask = _made(torch.empty((b, t, (t + 31) // 32), dtype=torch.int32, device=parents.device), stream)
     _need(mask, "mask", torch.int32, (b, t, (t + 31) // 32))
@@ -984,7 +1019,7 @@ def hc_tree_build(parents, ctx_len=None, *, batch: Optional[int] = None, mask=No
         positions = _made(torch.empty((b, t), dtype=torch.int32, device=parents.device), stream)
     _need(positions, "positions", torch.int32, (b, t))
     _check(ts_hc_tree_build(parents.data_ptr(), step, None if ctx_len is None else ctx_len.data_ptr(), mask.data_ptr(),
-                            positions.data_ptr(), b, t, _stream_handle(stream)))
+                            positions.data_ptr(), b, t, _stream_of(stream, parents)))
     return mask, positions
 
 
@@ -1001,29 +1036,38 @@ def hc_tree_attention(q, cache: KVCache, ctx_len, *, mask=None, scale: Optional[
     ``scale`` defaults to D ** -0.5. Returns (out bf16 [B, T, q_heads, D], lse fp32 [B, T, q_heads])."""
     torch = _torch()
     _, h, d, sq = _rows(q, "q")
-    if q.dim() != 4 or q.shape[0] != cache.batch or d != cache.head_dim:
-        raise HCError(TS_ERR_INVALID_ARG, f"q has shape {tuple(q.shape)}, expected [{cache.batch}, T, heads, {cache.head_dim}]")
-    b, t = q.shape[0], q.shape[1]
-    _lengths(ctx_len, "ctx_len", b)
-    words = (t + 31) // 32
-    step = 0
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != cache.batch or d != cache.head_dim:
+        raise HCError(TS_ERR_INVALID_ARG, f"q has shape {tuple(shape)}, expected [{cache.batch}, T, heads, {cache.head_dim}]")
+    b, t = shape[0], shape[1]
+    mp, step = None, 0
     if mask is not None:
-        _need(mask, "mask", torch.int32, (t, words) if mask.dim() == 2 else (b, t, words))
-        step = t * words if mask.dim() == 3 else 0
+        words = (t + 31) // 32
+        if mask.dim() == 2:
+            mp = _is(mask, "mask", torch.int32, (t, words))
+        else:
+            mp, step = _is(mask, "mask", torch.int32, (b, t, words)), t * words
     if out is None:
-        out = _made(torch.empty((b, t, h, d), dtype=torch.bfloat16, device=q.device), stream)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        if stream is not None:
+            out.record_stream(stream)
+        op = out.data_ptr()
     else:
-        _need(out, "out", torch.bfloat16, (b, t, h, d))
+        op = _is(out, "out", torch.bfloat16, shape)
     if lse is None:
-        lse = _made(torch.empty((b, t, h), dtype=torch.float32, device=q.device), stream)
+        lse = torch.empty((b, t, h), dtype=torch.float32, device=q.device)
+        if stream is not None:
+            lse.record_stream(stream)
+        lp = lse.data_ptr()
     else:
-        _need(lse, "lse", torch.float32, (b, t, h))
+        lp = _is(lse, "lse", torch.float32, (b, t, h))
     if ws is None:
         ws = _made(tree_attention_workspace(b, t, h, cache, q.device), stream)
-    _check(library().ts_hc_tree_attention(q.data_ptr(), sq, cache.ref, ctx_len.data_ptr(),
-                                          None if mask is None else mask.data_ptr(), step, out.data_ptr(), lse.data_ptr(), b, t,
-                                          h, d ** -0.5 if scale is None else scale, ws.data_ptr(),
-                                          ws.numel() * ws.element_size(), _stream_handle(stream)))
+    st = (_lib or library()).ts_hc_tree_attention(q.data_ptr(), sq, cache.ref, _is(ctx_len, "ctx_len", torch.int32, cache.lengths), mp,
+                                                  step, op, lp, b, t, h, d ** -0.5 if scale is None else scale, ws.data_ptr(), ws.nbytes,
+                                                  _stream_of(stream, q))
+    if st:
+        _check(st)
     return out, lse
 
 
@@ -1034,34 +1078,33 @@ def hc_verify(logits, tokens, parents=None, temperature=None, *, draft_probs=Non
     fp32 [B]; ``u`` fp32 [B, T] in [0, 1) and ``noise`` fp32 [B, V] exponential variates. Without draft_probs, u
     and noise every sequence is greedy. Returns (n_accepted [B], path [B, T], next_token [B]), int32."""
     torch = _torch()
-    _need(logits, "logits", torch.float32)
-    if logits.dim() != 3:
-        raise HCError(TS_ERR_INVALID_ARG, f"logits has shape {tuple(logits.shape)}, expected [B, T, V]")
-    b, t, v = logits.shape
-    _need(tokens, "tokens", torch.int32, (b, t))
-    step = 0
+    i32, f32 = torch.int32, torch.float32
+    lp = _is(logits, "logits", f32)
+    shape = logits.shape
+    if len(shape) != 3:
+        raise HCError(TS_ERR_INVALID_ARG, f"logits has shape {tuple(shape)}, expected [B, T, V]")
+    b, t, v = shape
+    tp = _is(tokens, "tokens", i32, (b, t))
+    step, pp, dp, up, np_, cp = 0, None, None, None, None, None
     if parents is not None:
-        _need(parents, "parents", torch.int32, (t,) if parents.dim() == 1 else (b, t))
-        step = t if parents.dim() == 2 else 0
+        if parents.dim() == 1:
+            pp = _is(parents, "parents", i32, (t,))
+        else:
+            pp, step = _is(parents, "parents", i32, (b, t)), t
     if draft_probs is not None:
-        _need(draft_probs, "draft_probs", torch.float32, (b, t, v))
-        _need(u, "u", torch.float32, (b, t))
-        _need(noise, "noise", torch.float32, (b, v))
-        _need(temperature, "temperature", torch.float32, (b,))
+        dp, up = _is(draft_probs, "draft_probs", f32, shape), _is(u, "u", f32, (b, t))
+        np_, cp = _is(noise, "noise", f32, (b, v)), _is(temperature, "temperature", f32, (b,))
     elif u is not None or noise is not None:
         raise HCError(TS_ERR_INVALID_ARG, "draft_probs, u and noise are given together, or none of them (greedy)")
     if n_accepted is None:
-        n_accepted = _made(torch.empty(b, dtype=torch.int32, device=logits.device), stream)
+        n_accepted = _made(torch.empty(b, dtype=i32, device=logits.device), stream)
     if path is None:
-        path = _made(torch.empty((b, t), dtype=torch.int32, device=logits.device), stream)
+        path = _made(torch.empty((b, t), dtype=i32, device=logits.device), stream)
     if next_token is None:
-        next_token = _made(torch.empty(b, dtype=torch.int32, device=logits.device), stream)
-    _need(n_accepted, "n_accepted", torch.int32, (b,))
-    _need(path, "path", torch.int32, (b, t))
-    _need(next_token, "next_token", torch.int32, (b,))
-    ptr = lambda x: None if x is None else x.data_ptr()  # noqa: E731
-    _check(library().ts_hc_verify(logits.data_ptr(), ptr(draft_probs), tokens.data_ptr(), ptr(parents), step,
-                                  ptr(temperature) if draft_probs is not None else None, ptr(u), ptr(noise),
-                                  n_accepted.data_ptr(), path.data_ptr(), next_token.data_ptr(), b, t, v,
-                                  _stream_handle(stream)))
+        next_token = _made(torch.empty(b, dtype=i32, device=logits.device), stream)
+    st = (_lib or library()).ts_hc_verify(lp, dp, tp, pp, step, cp, up, np_, _is(n_accepted, "n_accepted", i32, (b,)),
+                                          _is(path, "path", i32, (b, t)), _is(next_token, "next_token", i32, (b,)), b, t, v,
+                                          _stream_of(stream, logits))
+    if st:
+        _check(st)
     return n_accepted, path, next_token
