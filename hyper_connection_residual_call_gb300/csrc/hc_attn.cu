@@ -43,18 +43,24 @@ struct Format {
     // one scale array's bytes of a chunk (INT4: room for groups of 32)
     static constexpr int kScale = kType == kKvBf16 ? 0 : kType == kKvFp8 ? 16 : kChunk * kMaxGroups * 2;
     static constexpr int kStage = 2 * kCodes + (kType == kKvInt4 ? 4 : 2) * kScale;
-    // about 24 KB a warp in flight
-    static constexpr int kStages = kType == kKvBf16 ? (D == 64 ? 6 : D == 128 ? 3 : 2) : kType == kKvFp8 ? (D == 64 ? 8 : D == 128 ? 5 : 3)
-                                                                                     : (D == 64 ? 8 : D == 128 ? 8 : 5);
+    // some 8 to 24 KB a warp in flight
+    static constexpr int kStages = kType == kKvBf16 ? (D == 64 ? 6 : D == 128 ? 3 : 2) : kType == kKvFp8 ? (D == 64 ? 6 : 3)
+                                                                                     : (D == 64 ? 8 : 4);
+    // CTAs an SM: converting codes is a chain of short dependent steps, which more warps hide
+    template <int MT>
+    static constexpr int blocks() { return kType == kKvBf16 || D * MT > 128 || (D == 64 && MT == 2) ? 2 : 4; }
 };
 
 template <int kType, int D, int MT>
 struct Smem {
     using F = Format<kType, D>;
     static constexpr int kRing = kWarps * F::kStages * F::kStage;
-    static constexpr int kMerge = kWarps * 16 * MT * (D + 2) * 4;  // overlays the ring
-    static constexpr int kQ = 16 * MT * D * 2 + (kType == kKvInt4 ? 16 * MT * (D / 32) * 4 : 0);
-    static constexpr int kTotal = (kRing > kMerge ? kRing : kMerge) + kQ;
+    static constexpr int kPitch = D + 8;                             // floats: rows 8 banks apart
+    static constexpr int kMerge = kWarps * 16 * MT * (kPitch + 2) * 4;  // overlays the ring
+    static constexpr int kOver = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kSums = kType == kKvInt4 ? 16 * MT * F::kMaxGroups * 4 : 0;
+    static constexpr int kTables = kType == kKvInt4 ? F::kMaxGroups * 16 * 12 : 0;  // of a warp
+    static constexpr int kTotal = kOver + 16 * MT * D * 2 + kSums + kWarps * kTables + 512;  // and alignment
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
@@ -160,39 +166,28 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t a)
     return v;
 }
 
-// Where 16-byte piece `unit` of row `row` lies in a chunk's codes: permuted so
-// that the reads below meet no bank twice (for rows of 128 bytes and more).
+// 16-byte pieces of a row's codes are permuted so that the reads below meet no
+// bank twice (for rows of 128 bytes and more): piece `unit` of row `row` lies at
+// unit ^ swizzle(row). The permutation is linear over XOR in the bits that matter, so
+// that a lane's address for another row or piece is its first one with constants
+// added and XORed.
+template <int kType, int D, bool kValue>
+__host__ __device__ constexpr int swizzle(int row)
+{
+    constexpr int kRow = Format<kType, D>::kRow, kUnits = kRow / 16;
+    if (kType == kKvBf16)
+        return row & 7;  // ldmatrix: 8 rows at one unit
+    if (kType == kKvInt4 && !kValue)
+        return (row * kRow / 128) & (kUnits - 1) & 7;  // 8 rows at one unit, a word a lane
+    if (kUnits >= 8)
+        return kValue ? (row & 6) : ((row & 1) << 2);  // keys: rows 2i, 2i+1 at 4 units; values: rows 0, 2, 4, 6 at 2 units
+    return kValue ? (row >> 1) & (kUnits - 1) : (row * kRow / 128) & (kUnits - 1);
+}
+
 template <int kType, int D, bool kValue>
 __device__ __forceinline__ int piece_at(int row, int unit)
 {
-    constexpr int kRow = Format<kType, D>::kRow, kUnits = kRow / 16;
-    int s;
-    if (kType == kKvBf16)
-        s = row & 7;  // ldmatrix: 8 rows at one unit
-    else if (kType == kKvInt4 && !kValue)
-        s = (row * kRow / 128) & (kUnits - 1) & 7;  // 8 rows at one unit, a word a lane
-    else if (kUnits >= 8)
-        s = kValue ? (row & 6) : ((row & 1) << 2);  // keys: rows 2i, 2i+1 at 4 units; values: rows 0, 2, 4, 6 at 2 units
-    else
-        s = kValue ? (row >> 1) & (kUnits - 1) : (row * kRow / 128) & (kUnits - 1);
-    return row * kRow + ((unit ^ s) << 4);
-}
-
-// Element d that lane quarter c's pair index (k16 step, which of its 4 elements)
-// of a quantised key stands for: a lane reads whole pieces, and the query is laid
-// out to match.
-template <int kType, int D>
-__device__ __forceinline__ int key_element(int c, int step, int e)
-{
-    if (kType == kKvBf16)
-        return step * 16 + 2 * c + (e & 1) + (e >> 1) * 8;
-    if (kType == kKvFp8) {  // word `step` of the lane's words: pairs (0, 2) and (1, 3) of its 4 codes
-        const int d = (e & 1) * 2 + (e >> 1);
-        return ((step >> 2) * 4 + c) * 16 + (step & 3) * 4 + d;
-    }
-    // INT4: two steps a word, pairs (0, 4), (1, 5) then (2, 6), (3, 7) of its 8 codes; the four
-    // words of a step's lanes are 32 elements side by side, which lie in one group
-    return ((step >> 1) * 4 + c) * 8 + (step & 1) * 2 + (e >> 1) + (e & 1) * 4;
+    return row * Format<kType, D>::kRow + ((unit ^ swizzle<kType, D, kValue>(row)) << 4);
 }
 
 // Element d of value column n-tile j for lane group g.
@@ -208,20 +203,52 @@ __device__ __forceinline__ int value_element(int j, int g)
 template <int kType, int D, int MT>
 struct Walk {
     using F = Format<kType, D>;
+    static_assert(kType != kKvBf16 || F::kStage % 512 == 0, "constants are XORed into a bf16 stage's addresses");
     static constexpr bool kHalf = kType == kKvInt4;  // P and the values in fp16
     static constexpr int kSteps = D / 16;
     static constexpr int kCols = D / 8;
 
+    static constexpr int kUnits = F::kRow / 16;
+
     const AttnParams &p;
     uint32_t ring;            // this warp's ring (shared address)
     uint32_t qs;              // the block's query fragments (shared address)
-    uint32_t qsum;            // INT4: the sums of the query's groups [group][row] (shared address)
+    uint32_t qsum;            // INT4: the sums of the query's groups [group][row tile][8] of (row g, row g + 8)
+    uint32_t tables;          // INT4: this warp's (scale, bias) of a chunk, by group and key
     int lane, g, c, warp;
     int groups;               // INT4 groups of a row
+    int spans;                // and 32-element spans of a group
+    int fetch_k, fetch_v;     // where this lane's first piece of a chunk goes
+    int read_k, read_v;       // where its first reads of the keys and values lie
+    const uint8_t *scales;    // INT4: the array that this lane fetches from
+    float sc;                 // |scale| * log2(e), not 0 (its sign went into the query)
     float o[MT][kCols][4];
-    float m[MT][2], l[MT][2];
+    float m[MT][2], l[MT][2]; // the reference of each row's weights (times sc), their sum
 
     __device__ __forceinline__ Walk(const AttnParams &params) : p(params) {}
+
+    __device__ __forceinline__ void start(int tid)
+    {
+        lane = tid & 31;
+        warp = tid >> 5;
+        g = lane >> 2;
+        c = lane & 3;
+        sc = fmaxf(fabsf(p.scale_log2), 1e-38f);
+        groups = kType == kKvInt4 ? D / p.c.group : 0;
+        spans = kType == kKvInt4 ? p.c.group / 32 : 0;
+        fetch_k = piece_at<kType, D, false>(lane / kUnits, lane % kUnits);
+        fetch_v = piece_at<kType, D, true>(lane / kUnits, lane % kUnits);
+        if (kType == kKvBf16) {
+            read_k = piece_at<kType, D, false>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+            read_v = piece_at<kType, D, true>(lane & 15, lane >> 4);
+        } else {
+            constexpr int kBytes = kType == kKvFp8 ? (D >= 128 ? 16 : 8) : D / 16;  // of a value's row that a lane reads at once
+            read_k = kType == kKvFp8 ? piece_at<kType, D, false>(g, c) : piece_at<kType, D, false>(g, 0) + c * 4;
+            read_v = piece_at<kType, D, true>(2 * c, g * kBytes / 16) + g * kBytes % 16;
+        }
+        if (kType == kKvInt4)
+            scales = lane < 8 ? p.c.ks : lane < 16 ? p.c.kb : lane < 24 ? p.c.vs : p.c.vb;
+    }
 
     // Starts the copies of chunk `pos` (its first key) of page `page` into stage s.
     __device__ __forceinline__ void fetch(int s, int page, int head, int pos)
@@ -229,26 +256,21 @@ struct Walk {
         const bool ok = page >= 0;
         const size_t row = kv_row(p.c, ok ? page : 0, head, pos);
         const uint32_t dst = ring + s * F::kStage;
-        const uint8_t *k = p.c.k + row * F::kRow, *v = p.c.v + row * F::kRow;
-        constexpr int kUnits = F::kRow / 16;
+        const uint8_t *k = p.c.k + row * F::kRow + lane * 16, *v = p.c.v + row * F::kRow + lane * 16;
+        constexpr int kStep = 32 / kUnits;  // rows that the warp's 32 pieces are
+        static_assert(kChunk * kUnits >= 32, "a chunk is at least a piece for each lane");
 #pragma unroll
-        for (int i = 0; i < (kChunk * kUnits + 31) / 32; ++i) {
-            const int u = lane + 32 * i;
-            if (kChunk * kUnits >= 32 || u < kChunk * kUnits) {
-                const int r = u / kUnits, x = u % kUnits;
-                cp_async16(dst + piece_at<kType, D, false>(r, x), k + (size_t)u * 16, ok);
-                cp_async16(dst + F::kCodes + piece_at<kType, D, true>(r, x), v + (size_t)u * 16, ok);
-            }
+        for (int i = 0; i < kChunk * kUnits / 32; ++i) {
+            cp_async16(dst + (fetch_k ^ (swizzle<kType, D, false>(kStep * i) << 4)) + i * 512, k + i * 512, ok);
+            cp_async16(dst + F::kCodes + (fetch_v ^ (swizzle<kType, D, true>(kStep * i) << 4)) + i * 512, v + i * 512, ok);
         }
         if (kType == kKvFp8 && lane < 2)
             cp_async16(dst + 2 * F::kCodes + lane * F::kScale, (lane ? p.c.vs : p.c.ks) + row, ok);
-        if (kType == kKvInt4) {  // 16 * groups * 2 bytes of each of the four arrays
-            const int n = groups * 2;
-            for (int u = lane; u < 4 * n; u += 32) {
-                const int a = u / n, x = u - a * n;
-                const uint8_t *src = a == 0 ? p.c.ks : a == 1 ? p.c.kb : a == 2 ? p.c.vs : p.c.vb;
-                cp_async16(dst + 2 * F::kCodes + a * F::kScale + x * 16, src + row * groups * 2 + x * 16, ok);
-            }
+        if (kType == kKvInt4) {  // 16 * groups * 2 bytes of each of the four arrays, eight lanes an array
+            const uint8_t *src = scales + row * groups * 2;
+            const uint32_t at = dst + 2 * F::kCodes + (lane >> 3) * F::kScale;
+            for (int x = lane & 7; x < groups * 2; x += 8)
+                cp_async16(at + x * 16, src + x * 16, ok);
         }
     }
 
@@ -321,11 +343,32 @@ struct Walk {
         return __any_sync(0xFFFFFFFFu, wild);
     }
 
+    // INT4: a chunk's scales and biases, which lie by key and group, as the products take them:
+    // for the keys (scale, bias + 8 scale) in fp32 by group and key, for the values the fp16 scales,
+    // then the biases, by group and key. Read with one load each below.
+    __device__ __forceinline__ void lay_out_scales(uint32_t stage)
+    {
+        const int t = lane & 15;
+        for (int grp = lane >> 4; grp < groups; grp += 2) {
+            const uint32_t a = stage + 2 * F::kCodes + 2 * (t * groups + grp);
+            const float s = __half2float(__ushort_as_half((unsigned short)lds_u16(a)));
+            const float bias = fmaf(8.f, s, __half2float(__ushort_as_half((unsigned short)lds_u16(a + F::kScale))));
+            asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(tables + (grp * 16 + t) * 8), "f"(s), "f"(bias) : "memory");
+            const uint32_t vt = tables + F::kMaxGroups * 128 + (grp * 16 + t) * 2;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(vt), "h"((uint16_t)lds_u16(a + 2 * F::kScale)) : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(vt + F::kMaxGroups * 32), "h"((uint16_t)lds_u16(a + 3 * F::kScale)) : "memory");
+        }
+        __syncwarp();
+    }
+
     // One chunk: scores, softmax update, weighted values. `tail`: it reaches past
     // the context, so the mask is looked at.
     __device__ __forceinline__ void chunk(int s, int pos, bool tail, int b, int row0, const SeqLen &seq)
     {
         const uint32_t stage = ring + s * F::kStage;
+        // bf16 stages are multiples of 512 bytes, so that a constant can be XORed into the whole address
+        const uint32_t vbase = stage + F::kCodes + read_v;
+        const auto key_at = [&](int x) { return kType == kKvBf16 ? (stage + read_k) ^ x : stage + (read_k ^ x); };
         float x[MT][2][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -334,14 +377,15 @@ struct Walk {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     x[i][n][e] = 0.f;
+        if (kType == kKvInt4)
+            lay_out_scales(stage);
 
         // scores
         if (kType == kKvBf16) {
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
                 uint32_t kb[4];
-                const int r = (lane & 7) + ((lane >> 4) << 3);
-                ldmatrix4(kb, stage + piece_at<kType, D, false>(r, 2 * k + ((lane >> 3) & 1)));
+                ldmatrix4(kb, key_at(k << 5));
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     uint32_t qa[4];
@@ -357,7 +401,7 @@ struct Walk {
                 uint32_t w[2][4];
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
-                    lds_words<4>(w[n], stage + piece_at<kType, D, false>(n * 8 + g, y * 4 + c));
+                    lds_words<4>(w[n], key_at(y << 6) + n * 8 * F::kRow);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t k00 = e4m3_lo_bf16x2(w[0][k]), k01 = e4m3_hi_bf16x2(w[0][k]);
@@ -371,99 +415,98 @@ struct Walk {
                     }
                 }
             }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ks = fp8_scale(lds_u8(stage + 2 * F::kCodes + n * 8 + 2 * c + e));
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            x[i][n][2 * h + e] *= ks;
+                }
         } else {
-            const int spans = p.c.group / 32;  // 32-element spans of a group
-            int y = 0;
-            for (int grp = 0; grp < groups; ++grp) {
-                float z[MT][2][4];
+            float z[MT][2][4];
+            uint32_t table = tables + 2 * c * 8, sums = qsum + g * 8;  // of the group at hand
+            int span = 0;
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
+            for (int y = 0; y < D / 32; ++y) {  // 32 elements of every key, all in one group
+                if (span == 0) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int i = 0; i < MT; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            z[i][n][e] = 0.f;
-                for (int span = 0; span < spans; ++span, ++y) {
-                    const uint32_t w0 = lds32(stage + piece_at<kType, D, false>(g, y) + c * 4);
-                    const uint32_t w1 = lds32(stage + piece_at<kType, D, false>(8 + g, y) + c * 4);
+                        for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t k00 = int4_bf16x2(w0 >> (8 * k)), k01 = int4_bf16x2(w0 >> (8 * k + 4));
-                        const uint32_t k10 = int4_bf16x2(w1 >> (8 * k)), k11 = int4_bf16x2(w1 >> (8 * k + 4));
+                            for (int e = 0; e < 4; ++e)
+                                z[i][n][e] = 0.f;
+                }
+                const uint32_t w0 = lds32(key_at(y << 4)), w1 = lds32(key_at(y << 4) + 8 * F::kRow);
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            uint32_t qa[4];
-                            lds_words<4>(qa, qs + ((i * kSteps + 2 * y + k) * 32 + lane) * 16);
-                            mma16816<false>(z[i][0], qa, k00, k01);
-                            mma16816<false>(z[i][1], qa, k10, k11);
-                        }
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t k00 = int4_bf16x2(w0 >> (8 * k)), k01 = int4_bf16x2(w0 >> (8 * k + 4));
+                    const uint32_t k10 = int4_bf16x2(w1 >> (8 * k)), k11 = int4_bf16x2(w1 >> (8 * k + 4));
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        uint32_t qa[4];
+                        lds_words<4>(qa, qs + ((i * kSteps + 2 * y + k) * 32 + lane) * 16);
+                        mma16816<false>(z[i][0], qa, k00, k01);
+                        mma16816<false>(z[i][1], qa, k10, k11);
                     }
                 }
+                if (++span == spans) {
+                    span = 0;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < 2; ++n) {
+                        uint32_t t[4];  // (scale, bias) of keys 8n + 2c and 8n + 2c + 1
+                        lds_words<4>(t, table + n * 64);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t a = stage + 2 * F::kCodes + 2 * ((n * 8 + 2 * c + e) * groups + grp);
-                        const float sc = __half2float(__ushort_as_half((unsigned short)lds_u16(a)));
-                        const float bi = fmaf(8.f, sc, __half2float(__ushort_as_half((unsigned short)lds_u16(a + F::kScale))));
+                        for (int i = 0; i < MT; ++i) {
+                            uint32_t q[2];
+                            lds_words<2>(q, sums + i * 64);
 #pragma unroll
-                        for (int i = 0; i < MT; ++i)
+                            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float sum = __uint_as_float(lds32(qsum + 4 * (grp * 16 * MT + i * 16 + h * 8 + g)));
-                                x[i][n][2 * h + e] += fmaf(sc, z[i][n][2 * h + e], bi * sum);
-                            }
+                                for (int h = 0; h < 2; ++h) {
+                                    float &v = x[i][n][2 * h + e];
+                                    v = fmaf(__uint_as_float(t[2 * e]), z[i][n][2 * h + e], v);
+                                    v = fmaf(__uint_as_float(t[2 * e + 1]), __uint_as_float(q[h]), v);
+                                }
+                        }
                     }
+                    table += 128;
+                    sums += MT * 64;
+                }
             }
         }
 
         // softmax: this lane has keys 8n + 2c and 8n + 2c + 1 of rows g and g + 8
-        float vs[2][2];
-        float f[2][2];
+        if (tail) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                f[n][e] = p.scale_log2;
-                vs[n][e] = 1.f;
-                if (kType == kKvFp8) {
-                    const uint32_t a = stage + 2 * F::kCodes + n * 8 + 2 * c + e;
-                    f[n][e] *= fp8_scale(lds_u8(a));
-                    vs[n][e] = fp8_scale(lds_u8(a + F::kScale));
+                for (int h = 0; h < 2; ++h) {
+                    const int t = (row0 + i * 16 + h * 8 + g) / p.G;
+                    const uint32_t see = t < p.T ? attn_sees32(p, attn_mask_row(p, b, t), t, pos - seq.ctx, seq) : 0u;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (!((see >> (n * 8 + 2 * c + e)) & 1u))
+                                x[i][n][2 * h + e] = -INFINITY;
                 }
-            }
+        }
         bool move = false;
         float mx[MT][2];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int row = row0 + i * 16 + h * 8 + g;
-                const uint32_t *mask = nullptr;
-                int t = 0;
-                if (tail) {
-                    t = row / p.G;
-                    if (t < p.T)
-                        mask = attn_mask_row(p, b, t);
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float v = x[i][n][2 * h + e] * f[n][e];
-                        if (tail) {
-                            const int at = pos + n * 8 + 2 * c + e;
-                            const bool sees = t < p.T && at < seq.keys && (at < seq.ctx || attn_sees(p, mask, t, at - seq.ctx));
-                            v = sees ? v : -INFINITY;
-                        }
-                        x[i][n][2 * h + e] = v;
-                        top = fmaxf(top, v);
-                    }
+                float top = fmaxf(fmaxf(x[i][0][2 * h], x[i][0][2 * h + 1]), fmaxf(x[i][1][2 * h], x[i][1][2 * h + 1]));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                mx[i][h] = top;
-                move |= top > m[i][h] + kRescale || (m[i][h] == -INFINITY && top > -INFINITY);
+                mx[i][h] = top * sc;
+                move |= mx[i][h] > m[i][h] + kRescale;  // also the first that is not -infinity
             }
         if (__any_sync(0xFFFFFFFFu, move)) {
 #pragma unroll
@@ -481,6 +524,14 @@ struct Walk {
                     }
                 }
         }
+        float vs[2][2];
+        if (kType == kKvFp8) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    vs[n][e] = fp8_scale(lds_u8(stage + 2 * F::kCodes + F::kScale + n * 8 + 2 * c + e));
+        }
         uint32_t pa[MT][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -489,22 +540,20 @@ struct Walk {
                 const float ref = m[i][h] == -INFINITY ? 0.f : m[i][h];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const float a = ex2(x[i][n][2 * h] - ref), z = ex2(x[i][n][2 * h + 1] - ref);
+                    const float a = ex2(fmaf(x[i][n][2 * h], sc, -ref)), z = ex2(fmaf(x[i][n][2 * h + 1], sc, -ref));
                     l[i][h] += a + z;
-                    // P to 16 bits: its rounding (2^-9 in bf16) is independent from key to key and
+                    // P to 16 bits: its rounding (2^-8 in bf16) is independent from key to key and
                     // averages out; the sum l is of the unrounded P
-                    pa[i][2 * n + h] = kHalf ? pack2_f16(a, z) : pack2_bf16(a * vs[n][0], z * vs[n][1]);
+                    pa[i][2 * n + h] = kHalf ? pack2_f16(a, z) : kType == kKvFp8 ? pack2_bf16(a * vs[n][0], z * vs[n][1]) : pack2_bf16(a, z);
                 }
             }
 
         // weighted values
-        const uint32_t vstage = stage + F::kCodes;
         if (kType == kKvBf16) {
 #pragma unroll
             for (int j = 0; j < kCols; j += 2) {
                 uint32_t vb[4];
-                const int r = lane & 15;
-                ldmatrix4_trans(vb, vstage + piece_at<kType, D, true>(r, j + (lane >> 4)));
+                ldmatrix4_trans(vb, vbase ^ (j << 4));
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     mma16816<false>(o[i][j], pa[i], vb[0], vb[1]);
@@ -512,31 +561,26 @@ struct Walk {
                 }
             }
         } else {
-            constexpr int kPiece = kType == kKvFp8 ? (D >= 128 ? 16 : 8) : (D == 256 ? 32 : D / 8);  // elements
+            constexpr int kPiece = kType == kKvFp8 ? (D >= 128 ? 16 : 8) : D / 8;  // elements
             constexpr int kBytes = kType == kKvFp8 ? kPiece : kPiece / 2;
             constexpr int kWords = kBytes / 4;
-            constexpr int kPer = kType == kKvFp8 ? 4 : 8;                                           // elements of a word
+            constexpr int kPer = kType == kKvFp8 ? 4 : 8;                          // elements of a word
             constexpr int kPieces = D / (8 * kPiece);
+            uint32_t vsc[2] = {0, 0}, vbi[2] = {0, 0};  // INT4: of keys (2c, 2c + 1) and (2c + 8, 2c + 9)
+            if (kType == kKvInt4) {
+                const int grp = g * kPiece / p.c.group;  // a piece lies in one group
+                const uint32_t a = tables + F::kMaxGroups * 128 + grp * 32 + c * 4;
+                vsc[0] = lds32(a);
+                vsc[1] = lds32(a + 16);
+                vbi[0] = lds32(a + F::kMaxGroups * 32);
+                vbi[1] = lds32(a + F::kMaxGroups * 32 + 16);
+            }
 #pragma unroll
             for (int y = 0; y < kPieces; ++y) {
                 uint32_t w[4][4];  // keys 2c, 2c+1, 2c+8, 2c+9
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int r = 2 * c + (t & 1) + (t >> 1) * 8, byte = (y * 8 + g) * kBytes;
-                    lds_words<kWords>(w[t], vstage + piece_at<kType, D, true>(r, byte / 16) + byte % 16);
-                }
-                __half2 sc[2], bi[2];
-                if (kType == kKvInt4) {
-                    const int grp = ((y * 8 + g) * kPiece) / p.c.group;  // a piece lies in one group
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const uint32_t a = stage + 2 * F::kCodes + 2 * F::kScale + 2 * ((2 * c + 8 * t) * groups + grp);
-                        sc[t] = __halves2half2(__ushort_as_half((unsigned short)lds_u16(a)),
-                                               __ushort_as_half((unsigned short)lds_u16(a + 2 * groups)));
-                        bi[t] = __halves2half2(__ushort_as_half((unsigned short)lds_u16(a + F::kScale)),
-                                               __ushort_as_half((unsigned short)lds_u16(a + F::kScale + 2 * groups)));
-                    }
-                }
+                for (int t = 0; t < 4; ++t)
+                    lds_words<kWords>(w[t], vbase + ((t & 1) + (t >> 1) * 8) * F::kRow + y * 128);
 #pragma unroll
                 for (int k = 0; k < kWords; ++k) {
                     uint32_t lo[2], hi[2];
@@ -554,7 +598,8 @@ struct Walk {
                                 const uint32_t z = e < 2 ? lo[t] : hi[t];
                                 vb[t] = (e & 1) ? e4m3_hi_bf16x2(z) : e4m3_lo_bf16x2(z);
                             } else {
-                                vb[t] = int4_f16x2((e < 4 ? lo[t] : hi[t]) >> (4 * (e & 3)), sc[t], bi[t]);
+                                vb[t] = int4_f16x2((e < 4 ? lo[t] : hi[t]) >> (4 * (e & 3)), reinterpret_cast<const __half2 &>(vsc[t]),
+                                                   reinterpret_cast<const __half2 &>(vbi[t]));
                             }
                         }
                         const int j = y * kPiece + k * kPer + e;
@@ -577,7 +622,7 @@ __device__ __forceinline__ const uint16_t *query_row(const AttnParams &p, int b,
 
 // MT * 16 rows a block; grid: any number of CTAs up to kAttnMaxGrid.
 template <int kType, int D, int MT>
-__global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const __grid_constant__ AttnParams p, const int least)
+__global__ void __launch_bounds__(kAttnThreads, (Format<kType, D>::template blocks<MT>())) hc_attn_few_kernel(const __grid_constant__ AttnParams p, const int least)
 {
     using W = Walk<kType, D, MT>;
     using F = Format<kType, D>;
@@ -601,52 +646,23 @@ __global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const __gr
     it.b = scratch.b;
     it.base = scratch.base;
 
-    uint8_t *qsm = smem + (S::kTotal - S::kQ);
+    uint8_t *ring = smem + ((512u - (smem_addr(smem) & 511u)) & 511u);
+    uint8_t *qsm = ring + S::kOver;
     W w(p);
-    w.lane = tid & 31;
-    w.warp = tid >> 5;
-    w.g = w.lane >> 2;
-    w.c = w.lane & 3;
-    w.ring = smem_addr(smem) + w.warp * F::kStages * F::kStage;
+    w.start(tid);
+    w.ring = smem_addr(ring) + w.warp * F::kStages * F::kStage;
     w.qs = smem_addr(qsm);
     float *qsum = reinterpret_cast<float *>(qsm + 16 * MT * D * 2);
     w.qsum = smem_addr(qsum);
-    w.groups = kType == kKvInt4 ? D / p.c.group : 0;
-    float *merge = reinterpret_cast<float *>(smem);  // [warp][row][D], then maxima and sums [warp][row]
-    float *merge_m = merge + kWarps * kRows * D, *merge_l = merge_m + kWarps * kRows;
+    w.tables = w.qsum + S::kSums + w.warp * S::kTables;
+    float *merge = reinterpret_cast<float *>(ring);  // [warp][row][D], then maxima and sums [warp][row]
+    float *merge_m = merge + kWarps * kRows * S::kPitch, *merge_l = merge_m + kWarps * kRows;
 
     while (it.next(p, kTile)) {
         const SeqLen seq = it.seq;
         const int b = it.b, head = it.head, row0 = it.block * kRows, t0 = it.t0, t1 = it.t1;
         if (seq.bad && tid == 0 && p.status)
             atomicExch(p.status, kStatusBadArg);
-
-        // the query, as the fragments that the products take
-        for (int i = tid; i < MT * W::kSteps * 32 * 4; i += kAttnThreads) {
-            const int e = i & 3, ln = (i >> 2) & 31, k = (i >> 7) % W::kSteps, mt = (i >> 7) / W::kSteps;
-            const int row = row0 + mt * 16 + (ln >> 2) + (e & 1) * 8;  // a0, a2: row g; a1, a3: row g + 8
-            uint32_t v = 0;
-            if (row < p.rows) {
-                const uint16_t *q = query_row(p, b, head, row);
-                const int d0 = key_element<kType, D>(ln & 3, k, (e >> 1) * 2), d1 = key_element<kType, D>(ln & 3, k, (e >> 1) * 2 + 1);
-                v = (uint32_t)q[d0] | ((uint32_t)q[d1] << 16);
-            }
-            reinterpret_cast<uint32_t *>(qsm)[i] = v;
-        }
-        if (kType == kKvInt4)
-            for (int i = tid; i < kRows * w.groups; i += kAttnThreads) {
-                const int row = row0 + i % kRows, grp = i / kRows;
-                float sum = 0.f;
-                if (row < p.rows) {
-                    const uint32_t *q = reinterpret_cast<const uint32_t *>(query_row(p, b, head, row) + grp * p.c.group);
-                    for (int d = 0; d < p.c.group / 2; ++d)
-                        sum += bf16_lo(q[d]) + bf16_hi(q[d]);
-                }
-                qsum[i] = sum;
-            }
-        if (tid == 0)
-            wild_any = 0;
-        __syncthreads();
 
         w.clear();
         // pages of the next 32 tiles' chunks, one a lane
@@ -676,9 +692,59 @@ __global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const __gr
             ++fetched;
             cp_commit();
         };
-#pragma unroll
-        for (int s = 0; s < F::kStages - 1; ++s)
+#pragma unroll 1
+        for (int s = 0; s < F::kStages - 1; ++s)  // on their way while the query is laid out
             fetch_next();
+
+        // The query, as the fragments that the products take. A thread reads 16 bytes of a row, four
+        // pairs, each of which is one register of one lane's fragment.
+        {
+            constexpr int kPieces = D / 8, kStep = kAttnThreads / kPieces, kPasses = kRows / kStep;
+            const int x8 = tid % kPieces;
+            uint4 v[kPasses];
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int row = row0 + tid / kPieces + i * kStep;
+                v[i] = row < p.rows ? *reinterpret_cast<const uint4 *>(query_row(p, b, head, row) + x8 * 8) : make_uint4(0, 0, 0, 0);
+            }
+            const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int r = tid / kPieces + i * kStep, rr = r & 15;
+                const uint4 q = make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+                uint32_t *frag = reinterpret_cast<uint32_t *>(qsm) + (r >> 4) * W::kSteps * 128 + (rr & 7) * 16 + (rr >> 3);
+                if (kType == kKvBf16) {  // pair w: lane quarter w, register 0 or 2
+                    uint32_t *at = frag + (x8 >> 1) * 128 + (x8 & 1) * 2;
+                    at[0] = q.x;
+                    at[4] = q.y;
+                    at[8] = q.z;
+                    at[12] = q.w;
+                } else if (kType == kKvFp8) {  // a lane quarter's 16 elements are four steps: pairs (0, 2) and (1, 3) of each four
+                    uint32_t *at = frag + ((x8 >> 3) * 4 + (x8 & 1) * 2) * 128 + ((x8 >> 1) & 3) * 4;
+                    at[0] = __byte_perm(q.x, q.y, 0x5410);
+                    at[2] = __byte_perm(q.x, q.y, 0x7632);
+                    at[128] = __byte_perm(q.z, q.w, 0x5410);
+                    at[130] = __byte_perm(q.z, q.w, 0x7632);
+                } else {  // a lane quarter's 8 elements are two steps: pairs (0, 4), (1, 5) and (2, 6), (3, 7)
+                    uint32_t *at = frag + (x8 >> 2) * 256 + (x8 & 3) * 4;
+                    at[0] = __byte_perm(q.x, q.z, 0x5410);
+                    at[2] = __byte_perm(q.x, q.z, 0x7632);
+                    at[128] = __byte_perm(q.y, q.w, 0x5410);
+                    at[130] = __byte_perm(q.y, q.w, 0x7632);
+                    float sum = ((bf16_lo(q.x) + bf16_hi(q.x)) + (bf16_lo(q.y) + bf16_hi(q.y))) +
+                                ((bf16_lo(q.z) + bf16_hi(q.z)) + (bf16_lo(q.w) + bf16_hi(q.w)));
+                    const int lanes = p.c.group / 8;  // 4, 8 or 16 lanes hold a group
+                    for (int o = lanes / 2; o > 0; o >>= 1)
+                        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                    if (x8 % lanes == 0)
+                        qsum[((x8 / lanes * MT + (r >> 4)) * 8 + (rr & 7)) * 2 + (rr >> 3)] = sum;
+                }
+            }
+        }
+        if (tid == 0)
+            wild_any = 0;
+        __syncthreads();
+
         bool wild = false;
         int stage = 0;
         for (int t = t0; t < t1; ++t) {
@@ -691,10 +757,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const __gr
                 if (tail) {
                     wild |= w.tame(stage, pos, seq.ctx, seq.keys);
                     __syncwarp();
-                    w.chunk(stage, pos, true, b, row0, seq);
-                } else {
-                    w.chunk(stage, pos, false, b, row0, seq);
                 }
+                w.chunk(stage, pos, tail, b, row0, seq);
             }
             stage = stage + 1 == F::kStages ? 0 : stage + 1;
         }
@@ -716,11 +780,18 @@ __global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const __gr
                     merge_m[w.warp * kRows + r] = w.m[i][h];
                     merge_l[w.warp * kRows + r] = sum;
                 }
-                float *row = merge + (size_t)(w.warp * kRows + r) * D;
+                float *row = merge + (w.warp * kRows + r) * S::kPitch;
+                if (kType == kKvBf16) {  // lane quarter c holds columns 2c, 2c + 1 of n-tile j
 #pragma unroll
-                for (int j = 0; j < W::kCols; ++j) {  // lane quarter c holds columns 2c, 2c + 1 of n-tile j
-                    row[value_element<kType, D>(j, 2 * w.c)] = w.o[i][j][2 * h];
-                    row[value_element<kType, D>(j, 2 * w.c + 1)] = w.o[i][j][2 * h + 1];
+                    for (int j = 0; j < W::kCols; ++j)
+                        *reinterpret_cast<float2 *>(row + j * 8 + 2 * w.c) = make_float2(w.o[i][j][2 * h], w.o[i][j][2 * h + 1]);
+                } else {  // n-tiles j .. j + 3 are four elements side by side, of the pieces 2c and 2c + 1
+#pragma unroll
+                    for (int j = 0; j < W::kCols; j += 4)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float4 *>(row + value_element<kType, D>(j, 2 * w.c + e)) =
+                                make_float4(w.o[i][j][2 * h + e], w.o[i][j + 1][2 * h + e], w.o[i][j + 2][2 * h + e], w.o[i][j + 3][2 * h + e]);
                 }
             }
         __syncthreads();
@@ -741,7 +812,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) hc_attn_few_kernel(const __gr
             for (int v = 0; v < kWarps; ++v) {
                 const float f = ex2(merge_m[v * kRows + r] - ref);
                 sum += f * merge_l[v * kRows + r];
-                const float4 x = *reinterpret_cast<const float4 *>(merge + (size_t)(v * kRows + r) * D + d);
+                const float4 x = *reinterpret_cast<const float4 *>(merge + (v * kRows + r) * S::kPitch + d);
                 acc.x += f * x.x;
                 acc.y += f * x.y;
                 acc.z += f * x.z;

@@ -62,6 +62,7 @@ struct Line {
         b0 = min(p.B, tid * chunk);
         b1 = min(p.B, b0 + chunk);
         sum = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b)
             sum += attn_seq(p, b, tile).tiles * per;
         long incl = sum;
@@ -76,6 +77,7 @@ struct Line {
         __syncthreads();
         long before = 0;
         total = 0;
+#pragma unroll 1
         for (int w = 0; w < (int)blockDim.x / 32; ++w) {
             if (w < warp)
                 before += sc.warp_sum[w];
@@ -91,6 +93,7 @@ struct Line {
         if (x >= base && x < base + sum) {  // one thread
             long at = base;
             int b = b0;
+#pragma unroll 1
             for (;; ++b) {
                 const long n = attn_seq(p, b, tile).tiles * per;
                 if (x < at + n)
