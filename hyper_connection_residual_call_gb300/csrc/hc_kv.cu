@@ -24,64 +24,182 @@ namespace {
 constexpr int kKvThreads = 256;
 constexpr float kInt4Most = 57344.f;
 
-// Reductions over aligned groups of W lanes.
-template <int W>
-__device__ __forceinline__ float group_max(float v)
-{
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
-}
+// Where a thread works: D/16 lanes a row, of which a lane has elements [8 part, 8 part + 8)
+// of each half, so that the lanes' accesses lie side by side; the key's and the value's
+// row of one token and head. Rows go over a run of up to kRun tokens of one head first:
+// their codes and scales lie side by side in a page, and a warp's stores of 2-byte
+// scales are one piece of memory (72 us -> see hc_kv_write_kernel).
+constexpr int kRun = 32;
 
-__device__ __forceinline__ float lanes_max(float v, int w)
-{
-    for (int o = w / 2; o > 0; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
-}
-
-template <int W>
-__device__ __forceinline__ bool group_any(bool v)
-{
-    // The mask's bits of this thread's group of W lanes (W divides 32).
-    const unsigned b = __ballot_sync(0xFFFFFFFFu, v);
-    const unsigned lane = threadIdx.x & 31;
-    return ((b >> (lane / W * W)) & (W == 32 ? 0xFFFFFFFFu : (1u << W) - 1u)) != 0;
-}
-
-__device__ __forceinline__ bool lanes_any(bool v, int w)
-{
-    const unsigned b = __ballot_sync(0xFFFFFFFFu, v);
-    const unsigned lane = threadIdx.x & 31;
-    return ((b >> (lane & ~(unsigned)(w - 1))) & ((1u << w) - 1u)) != 0;
-}
-
-// Which row a thread works on: D/16 lanes a row, 16 elements a lane; rows in the
-// order of the bf16 side ([b][t][head], keys then values), so that its accesses
-// are contiguous over the block.
 template <int kLanes>
 struct RowAt {
-    bool valid, value;        // value: a value's row, else a key's
-    int part, b, h;
-    int t;                    // token within the sequence
+    bool valid, placed;       // placed: the row has a place in the cache (if not, that is recorded)
+    int part, h;
     size_t token;             // b * T + t
-    __device__ RowAt(const KvParams &p, unsigned idx)  // 32-bit divisions: the host keeps 2 B T heads lanes below 2^31
+    size_t row;
+    __device__ __forceinline__ RowAt(const KvParams &p, unsigned idx)  // 32 bits: the host keeps the rows' lanes below 2^31
     {
         part = (int)(idx % kLanes);
-        unsigned r = idx / kLanes;
-        const unsigned per = (unsigned)p.B * p.T * p.c.heads;
-        value = r >= per;
-        r -= value ? per : 0;
-        valid = r < per;
-        const unsigned tok = r / (unsigned)p.c.heads;
-        h = (int)(r - tok * p.c.heads);
-        b = (int)(tok / (unsigned)p.T);
-        t = (int)(tok - (unsigned)b * p.T);
-        token = tok;
+        const unsigned r = idx / kLanes, r1 = p.by_run.div(r), r2 = p.by_heads.div(r1), b = p.by_runs.div(r2);
+        const unsigned t = (r2 - b * p.by_runs.d) * p.by_run.d + (r - r1 * p.by_run.d);
+        h = (int)(r1 - r2 * p.by_heads.d);
+        token = (size_t)b * p.T + t;
+        valid = b < (unsigned)p.B && t < (unsigned)p.T;
+        placed = false;
+        row = 0;
+        if (!valid)
+            return;
+        const int start = __ldg(p.start + b);
+        const long pos = (long)start + t;
+        const long page = start < 0 ? -1 : kv_page(p.c, (int)b, pos);
+        placed = page >= 0;
+        if (placed)
+            row = kv_row(p.c, page, h, pos);
+        else if (part == 0 && p.status)
+            atomicExch(p.status, kStatusBadArg);
     }
 };
 
+// q = clamp(round(d / scale), 0, 15), ties to even. The quotient by the reciprocal is
+// corrected once with its exact remainder (Markstein's step): a quotient that lies on a
+// tie, which d and scale of few bits often do, comes out as the tie itself.
+__device__ __forceinline__ float quotient(float d, float by, float inv)
+{
+    const float q = d * inv;
+    return fmaf(fmaf(-q, by, d), inv, q);
+}
+
+__device__ __forceinline__ float int4_code(float d, float scale, float inv)
+{
+    constexpr float kEven = 12582912.f;  // 1.5 * 2^23: the sum is rounded to a whole number, ties to even
+    return fminf(fmaxf(quotient(d, scale, inv), 0.f), 15.f) + kEven - kEven;
+}
+
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// bf16 pairs in an order that signed 16-bit comparison keeps (its own inverse).
+__device__ __forceinline__ uint32_t ordered16x2(uint32_t w) { return w ^ (((w >> 15) & 0x00010001u) * 0x7FFFu); }
+
+// One row's elements of this lane (a: of the first half, b: of the second), quantised and stored.
+template <int kType, int kLanes>
+__device__ __forceinline__ void write_row(const KvView &c, const RowAt<kLanes> &at, uint8_t *codes, uint8_t *scales, uint8_t *biases,
+                                          const uint4 a, const uint4 b)
+{
+    if (kType == kKvBf16) {
+        if (at.placed) {
+            uint4 *out = reinterpret_cast<uint4 *>(codes + at.row * (kLanes * 32)) + at.part;
+            out[0] = a;
+            out[kLanes] = b;
+        }
+        return;
+    }
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (kType == kKvFp8) {
+        // |x| as 16-bit integers keeps its order, and infinities and NaNs are the largest
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+            top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        top = max(top & 0xFFFFu, top >> 16);
+        const bool bad = top >= 0x7F80u;
+        const int byte = bad ? kFp8BadRow : fp8_scale_byte(__uint_as_float(top << 16));
+        const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);  // 2^-e, exact
+        uint32_t out[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(w[2 * j]) * inv, bf16_hi(w[2 * j]) * inv), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi =
+                __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(w[2 * j + 1]) * inv, bf16_hi(w[2 * j + 1]) * inv), __NV_SATFINITE, __NV_E4M3);
+            out[j] = bad ? 0u : lo | hi << 16;
+        }
+        if (at.placed) {
+            uint2 *to = reinterpret_cast<uint2 *>(codes + at.row * (kLanes * 16)) + at.part;
+            to[0] = make_uint2(out[0], out[1]);
+            to[kLanes] = make_uint2(out[2], out[3]);
+            if (at.part == 0)
+                scales[at.row] = (uint8_t)byte;
+        }
+        return;
+    }
+    // INT4: a group of 32 or more elements is 4 or more lanes of a half, or both halves.
+    // range[k]: the largest element in the low 16 bits and the complement of the smallest in the high
+    // ones, both as ordered integers, so that one signed maximum serves both.
+    uint32_t range[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t most = ordered16x2(w[4 * k]), least = most;
+#pragma unroll
+        for (int j = 4 * k + 1; j < 4 * k + 4; ++j) {
+            const uint32_t o = ordered16x2(w[j]);
+            most = __vmaxs2(most, o);
+            least = __vmins2(least, o);
+        }
+        least = ~least;
+        range[k] = __vmaxs2(__byte_perm(most, least, 0x5410), __byte_perm(most, least, 0x7632));
+#pragma unroll
+        for (int o = 2; o > 0; o >>= 1)  // groups of 32: 4 lanes
+            range[k] = __vmaxs2(range[k], __shfl_xor_sync(0xFFFFFFFFu, range[k], o));
+        if (kLanes >= 8 && c.group >= 64)
+            range[k] = __vmaxs2(range[k], __shfl_xor_sync(0xFFFFFFFFu, range[k], 4));
+        if (kLanes >= 16 && c.group >= 128)
+            range[k] = __vmaxs2(range[k], __shfl_xor_sync(0xFFFFFFFFu, range[k], 8));
+    }
+    if (c.group > kLanes * 8)
+        range[0] = range[1] = __vmaxs2(range[0], range[1]);
+    uint32_t word[2];
+    __half scale[2], bias[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        // Infinities and NaNs are the largest or the smallest.
+        const bool bad = (int16_t)(range[k] & 0xFFFFu) >= 0x7F80 || (int16_t)(range[k] >> 16) >= 0x7F7F;
+        // Values saturate at +-57344, so that q * scale + bias stays inside fp16 for every q.
+        const uint32_t most = ordered16x2(range[k] & 0xFFFFu) << 16, least = ordered16x2(~range[k] >> 16) << 16;
+        const float top = fminf(fmaxf(__uint_as_float(most), -kInt4Most), kInt4Most);
+        const float low = fminf(fmaxf(__uint_as_float(least), -kInt4Most), kInt4Most);
+        const __half s = __float2half_rn(quotient(top - low, 15.f, 1.f / 15.f));
+        bias[k] = __float2half_rn(low);
+        scale[k] = bad ? __ushort_as_half(0x7E00) : s;
+        const float sf = __half2float(s), bf = __half2float(bias[k]);
+        const bool none = bad || !(sf > 0.f);
+        const float inv = none ? 0.f : rcp(sf);
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t v = w[4 * k + i / 2];
+            q[i] = int4_code(((i & 1) ? bf16_hi(v) : bf16_lo(v)) - bf, sf, inv);
+        }
+        // four codes are a whole number below 2^16: its bits over 2^23
+        const float lo4 = fmaf(fmaf(fmaf(q[3], 16.f, q[2]), 16.f, q[1]), 16.f, q[0]) + 8388608.f;
+        const float hi4 = fmaf(fmaf(fmaf(q[7], 16.f, q[6]), 16.f, q[5]), 16.f, q[4]) + 8388608.f;
+        word[k] = none ? 0u : __byte_perm(__float_as_uint(lo4), __float_as_uint(hi4), 0x5410);
+    }
+    if (at.placed) {
+        uint32_t *to = reinterpret_cast<uint32_t *>(codes + at.row * (kLanes * 8)) + at.part;
+        to[0] = word[0];
+        to[kLanes] = word[1];
+        // a group's lanes: the first stores the first half's scale and bias, the second the other's
+        const int lanes = c.group / 8, turn = at.part % lanes, groups = kLanes * 16 / c.group;
+        if (turn < 2 && at.part < kLanes && !(turn == 1 && c.group > kLanes * 8)) {
+            const size_t g = at.row * groups + (at.part + turn * kLanes) / lanes;
+            reinterpret_cast<__half *>(scales)[g] = turn ? scale[1] : scale[0];
+            reinterpret_cast<__half *>(biases)[g] = turn ? bias[1] : bias[0];
+        }
+    }
+}
+
+// A thread has the key's and the value's elements of its token and head: their loads
+// are in flight together, and they share what finding the place costs. (Four rows of
+// each a thread were no faster: the kernels are bound by their instructions as much as
+// by HBM, 32768 tokens x 8 heads of FP8.) 32768 tokens x 8 heads x 128: FP8 written in
+// 29 us and read in 31 us, each 0.2 GB, 1.0 of the measured copy rate
 template <int kType, int kLanes>
 __global__ void __launch_bounds__(kKvThreads) hc_kv_write_kernel(const KvParams p)
 {
@@ -91,99 +209,64 @@ __global__ void __launch_bounds__(kKvThreads) hc_kv_write_kernel(const KvParams 
     // Lanes past the last row stay for the shuffles; a whole warp of them leaves.
     if (!__any_sync(0xFFFFFFFFu, at.valid))
         return;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    long page = -1, pos = 0;
+    uint4 k0 = make_uint4(0, 0, 0, 0), k1 = k0, v0 = k0, v1 = k0;
     if (at.valid) {
-        const uint4 *in = reinterpret_cast<const uint4 *>((at.value ? p.v + at.token * p.v_stride : p.k + at.token * p.k_stride)
-                                                          + (size_t)at.h * (kLanes * 16) + at.part * 16);
-        a = in[0];
-        b = in[1];
-        pos = (long)p.start[at.b] + at.t;
-        page = p.start[at.b] < 0 ? -1 : kv_page(p.c, at.b, pos);
-        if (page < 0 && at.part == 0 && p.status)
-            atomicExch(p.status, kStatusBadArg);
+        const size_t off = (size_t)at.h * (kLanes * 16) + at.part * 8;
+        const uint4 *k = reinterpret_cast<const uint4 *>(p.k + at.token * p.k_stride + off);
+        const uint4 *v = reinterpret_cast<const uint4 *>(p.v + at.token * p.v_stride + off);
+        k0 = k[0];
+        k1 = k[kLanes];
+        v0 = v[0];
+        v1 = v[kLanes];
     }
-    const size_t row = page < 0 ? 0 : kv_row(p.c, page, at.h, pos);
-    uint8_t *codes = at.value ? p.c.v : p.c.k;
+    write_row<kType, kLanes>(p.c, at, p.c.k, p.c.ks, p.c.kb, k0, k1);
+    write_row<kType, kLanes>(p.c, at, p.c.v, p.c.vs, p.c.vb, v0, v1);
+}
+
+// This lane's elements of a stored row (a: of the first half, b: of the second), as bf16.
+template <int kType, int kLanes>
+__device__ __forceinline__ void read_row(const KvView &c, const RowAt<kLanes> &at, const uint8_t *codes, const uint8_t *scales,
+                                         const uint8_t *biases, uint4 &a, uint4 &b)
+{
+    a = b = make_uint4(0, 0, 0, 0);
+    if (!at.placed)
+        return;
     if (kType == kKvBf16) {
-        if (page >= 0) {
-            uint4 *out = reinterpret_cast<uint4 *>(codes + row * (kLanes * 32)) + at.part * 2;
-            out[0] = a;
-            out[1] = b;
-        }
+        const uint4 *in = reinterpret_cast<const uint4 *>(codes + at.row * (kLanes * 32)) + at.part;
+        a = in[0];
+        b = in[kLanes];
         return;
     }
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    float x[16];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        x[2 * j] = bf16_lo(w[j]);
-        x[2 * j + 1] = bf16_hi(w[j]);
-    }
-    bool bad = false;
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-        bad |= !finite_f32(x[j]);
-    uint8_t *scales = at.value ? p.c.vs : p.c.ks;
+    uint32_t w[8];
     if (kType == kKvFp8) {
-        float m = 0.f;
+        const uint2 *in = reinterpret_cast<const uint2 *>(codes + at.row * (kLanes * 16)) + at.part;
+        const uint2 in0 = in[0], in1 = in[kLanes];
+        const float s = fp8_scale(scales[at.row]);
+        const uint32_t v[4] = {in0.x, in0.y, in1.x, in1.y};
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            m = fmaxf(m, fabsf(x[j]));
-        bad = group_any<kLanes>(bad);
-        m = group_max<kLanes>(m);
-        const int byte = bad ? kFp8BadRow : fp8_scale_byte(m);
-        const float inv = bad ? 0.f : __uint_as_float((uint32_t)(254 - byte) << 23);  // 2^-e, exact
-        uint32_t out[4];
+        for (int j = 0; j < 8; ++j) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v[j / 2] >> (16 * (j & 1))), __NV_E4M3);
+            const float2 f = __half22float2(__half2(h));
+            const __nv_bfloat162 y = __floats2bfloat162_rn(f.x * s, f.y * s);
+            w[j] = reinterpret_cast<const uint32_t &>(y);
+        }
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t word = 0;
+        for (int k = 0; k < 2; ++k) {
+            const int part = at.part + k * kLanes;
+            const uint32_t in = reinterpret_cast<const uint32_t *>(codes + at.row * (kLanes * 8))[part];
+            const size_t g = at.row * (size_t)(kLanes * 16 / c.group) + part / (c.group / 8);
+            const float s = __half2float(reinterpret_cast<const __half *>(scales)[g]), bias = __half2float(reinterpret_cast<const __half *>(biases)[g]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 f = make_float2(bad ? 0.f : x[4 * j + 2 * i] * inv, bad ? 0.f : x[4 * j + 2 * i + 1] * inv);
-                word |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) << (16 * i);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t v = in >> (8 * j);
+                const __nv_bfloat162 y = __floats2bfloat162_rn(fmaf((float)(v & 15u), s, bias), fmaf((float)((v >> 4) & 15u), s, bias));
+                w[4 * k + j] = reinterpret_cast<const uint32_t &>(y);
             }
-            out[j] = word;
-        }
-        if (page >= 0) {
-            reinterpret_cast<uint4 *>(codes + row * (kLanes * 16))[at.part] = make_uint4(out[0], out[1], out[2], out[3]);
-            if (at.part == 0)
-                scales[row] = (uint8_t)byte;
-        }
-        return;
-    }
-    // INT4: groups of 32, 64 or 128 elements are 2, 4 or 8 lanes
-    const int gl = p.c.group / 16;
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int j = 1; j < 16; ++j) {
-        lo = fminf(lo, x[j]);
-        hi = fmaxf(hi, x[j]);
-    }
-    bad = lanes_any(bad, gl);
-    hi = lanes_max(hi, gl);
-    lo = -lanes_max(-lo, gl);
-    // Values saturate at +-57344, so that q * scale + bias stays inside fp16 for every q.
-    lo = fminf(fmaxf(lo, -kInt4Most), kInt4Most);
-    hi = fminf(fmaxf(hi, -kInt4Most), kInt4Most);
-    const __half s = __float2half_rn(__fdiv_rn(hi - lo, 15.f));
-    const __half bias = __float2half_rn(lo);
-    const float sf = __half2float(s), bf = __half2float(bias);
-    uint32_t out[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        float q = sf > 0.f ? rintf(__fdiv_rn(x[j] - bf, sf)) : 0.f;
-        q = bad ? 0.f : fminf(fmaxf(q, 0.f), 15.f);
-        out[j / 8] |= (uint32_t)(int)q << (4 * (j % 8));
-    }
-    if (page >= 0) {
-        reinterpret_cast<uint2 *>(codes + row * (kLanes * 8))[at.part] = make_uint2(out[0], out[1]);
-        if (at.part % gl == 0) {
-            const size_t g = row * (size_t)(kLanes / gl) + at.part / gl;
-            reinterpret_cast<__half *>(scales)[g] = bad ? __ushort_as_half(0x7E00) : s;
-            reinterpret_cast<__half *>(at.value ? p.c.vb : p.c.kb)[g] = bias;
         }
     }
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+    b = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 template <int kType, int kLanes>
@@ -194,55 +277,15 @@ __global__ void __launch_bounds__(kKvThreads) hc_kv_read_kernel(const KvParams p
     const RowAt<kLanes> at(p, blockIdx.x * kKvThreads + threadIdx.x);
     if (!at.valid)
         return;
-    const long pos = (long)p.start[at.b] + at.t;
-    const long page = p.start[at.b] < 0 ? -1 : kv_page(p.c, at.b, pos);
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (page >= 0) {
-        const size_t row = kv_row(p.c, page, at.h, pos);
-        const uint8_t *codes = at.value ? p.c.v : p.c.k, *scales = at.value ? p.c.vs : p.c.ks;
-        if (kType == kKvBf16) {
-            const uint4 *in = reinterpret_cast<const uint4 *>(codes + row * (kLanes * 32)) + at.part * 2;
-            a = in[0];
-            b = in[1];
-        } else {
-            float x[16];
-            if (kType == kKvFp8) {
-                const uint4 in = reinterpret_cast<const uint4 *>(codes + row * (kLanes * 16))[at.part];
-                const float s = fp8_scale(scales[row]);
-                const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j / 2] >> (16 * (j & 1))), __NV_E4M3);
-                    const float2 f = __half22float2(__half2(h));
-                    x[2 * j] = f.x * s;
-                    x[2 * j + 1] = f.y * s;
-                }
-            } else {
-                const int gl = p.c.group / 16;
-                const uint2 in = reinterpret_cast<const uint2 *>(codes + row * (kLanes * 8))[at.part];
-                const size_t g = row * (size_t)(kLanes / gl) + at.part / gl;
-                const float s = __half2float(reinterpret_cast<const __half *>(scales)[g]);
-                const float bias = __half2float(reinterpret_cast<const __half *>(at.value ? p.c.vb : p.c.kb)[g]);
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    x[j] = fmaf((float)(((j < 8 ? in.x : in.y) >> (4 * (j & 7))) & 15u), s, bias);
-            }
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-                w[j] = reinterpret_cast<const uint32_t &>(v);
-            }
-            a = make_uint4(w[0], w[1], w[2], w[3]);
-            b = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-    } else if (at.part == 0 && p.status) {
-        atomicExch(p.status, kStatusBadArg);
-    }
-    uint4 *out = reinterpret_cast<uint4 *>((at.value ? p.v_out : p.k_out)
-                                           + ((size_t)at.token * p.c.heads + at.h) * (kLanes * 16)) + at.part * 2;
-    out[0] = a;
-    out[1] = b;
+    uint4 k0, k1, v0, v1;
+    read_row<kType, kLanes>(p.c, at, p.c.k, p.c.ks, p.c.kb, k0, k1);
+    read_row<kType, kLanes>(p.c, at, p.c.v, p.c.vs, p.c.vb, v0, v1);
+    const size_t off = (at.token * p.c.heads + at.h) * (kLanes * 16) + at.part * 8;
+    uint4 *k = reinterpret_cast<uint4 *>(p.k_out + off), *v = reinterpret_cast<uint4 *>(p.v_out + off);
+    k[0] = k0;
+    k[kLanes] = k1;
+    v[0] = v0;
+    v[kLanes] = v1;
 }
 
 // Bytes of one row's codes and of one scale array's row.
@@ -352,7 +395,7 @@ __global__ void __launch_bounds__(128) hc_tree_build_kernel(const TreeBuildParam
 template <int kLanes>
 cudaError_t launch_rows(const KvParams &p, bool write, cudaStream_t stream)
 {
-    const size_t n = (size_t)2 * p.B * p.T * p.c.heads * kLanes;
+    const size_t n = (size_t)p.B * p.by_runs.d * p.by_heads.d * p.by_run.d * kLanes;
     const dim3 grid((unsigned)((n + kKvThreads - 1) / kKvThreads));
     void (*kernel)(KvParams) = nullptr;
     switch (p.c.type) {
@@ -363,8 +406,12 @@ cudaError_t launch_rows(const KvParams &p, bool write, cudaStream_t stream)
     return launch_pdl(kernel, grid, dim3(kKvThreads), 0, true, stream, p);
 }
 
-cudaError_t launch_any(const KvParams &p, bool write, cudaStream_t stream)
+cudaError_t launch_any(KvParams p, bool write, cudaStream_t stream)
 {
+    const int run = std::min(p.T, kRun);
+    p.by_run = FastDiv((uint32_t)run);
+    p.by_heads = FastDiv((uint32_t)p.c.heads);
+    p.by_runs = FastDiv((uint32_t)((p.T + run - 1) / run));
     switch (p.c.D) {
     case 64: return launch_rows<4>(p, write, stream);
     case 128: return launch_rows<8>(p, write, stream);

@@ -56,9 +56,10 @@ __device__ __forceinline__ float2 turn(float x0, float x1, float2 cs)
     return make_float2(fmaf(x0, cs.x, -(x1 * cs.y)), fmaf(x0, cs.y, x1 * cs.x));
 }
 
-// Unit u of a head is 16 of its elements and the 8 pairs they form: vectors
-// (u, u + rot/16) of 8 elements in the half layout, (2u, 2u + 1) interleaved;
-// the units after rot/16 are the elements that are copied. A thread keeps its
+// Unit u of a head is 16 of its elements and the 8 pairs they form: vectors u and
+// u + rot/16 of 8 elements (the two halves of pairs in the half layout, four pairs
+// each interleaved), so that the lanes' vectors lie side by side; the units after
+// rot/16 are the elements that are copied, split likewise. A thread keeps its
 // unit's 8 (cos, sin) in registers and walks the heads lane, lane + lanes, ...
 // of one token, so a table row is read once per `lanes` threads' units and not
 // once per head. rot and D multiples of 16.
@@ -78,22 +79,25 @@ __global__ void __launch_bounds__(kRopeThreads) hc_rope_kernel(const RopeParams 
     const bool rotate = u < turned;
     int v0, v1;
     if (!rotate) {
-        v0 = turned * 2 + (u - turned) * 2;
-        v1 = v0 + 1;
+        v0 = turned * 2 + (u - turned);
+        v1 = v0 + (p.D / 16 - turned);
     } else {
-        v0 = kInterleaved ? 2 * u : u;
-        v1 = kInterleaved ? 2 * u + 1 : u + turned;
+        v0 = u;
+        v1 = u + turned;
     }
     float2 cs[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        cs[j] = make_float2(0.f, 0.f);
     if (rotate) {
         const int pos = p.positions[n];
         const bool ok = pos >= 0 && pos < p.max_pos;
         if (!ok && p.status && u == 0 && lane == 0)
             atomicExch(p.status, kStatusInvalidArg);
-        const float4 *t = reinterpret_cast<const float4 *>(p.table + ((size_t)(ok ? pos : 0) * (p.rot / 2) + u * 8) * 2);
+        const float4 *t = reinterpret_cast<const float4 *>(p.table + (size_t)(ok ? pos : 0) * p.rot);  // two pairs each
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float4 w = __ldg(t + j);
+            float4 w = __ldg(t + (kInterleaved ? (j < 2 ? 2 * v0 + j : 2 * v1 + j - 2) : 4 * u + j));
             if (!ok)
                 w = make_float4(0.f, 0.f, 0.f, 0.f);
             if (p.inverse) {
@@ -104,41 +108,51 @@ __global__ void __launch_bounds__(kRopeThreads) hc_rope_kernel(const RopeParams 
             cs[2 * j + 1] = make_float2(w.z, w.w);
         }
     }
-#pragma unroll 4
-    for (int h = lane; h < heads; h += lanes) {
-        const bool is_q = h < p.q_heads;
-        const int hh = is_q ? h : h - p.q_heads;
-        const uint4 *in = reinterpret_cast<const uint4 *>(
-            (is_q ? p.q + (size_t)n * p.q_stride : p.k + (size_t)n * p.k_stride) + (size_t)hh * p.D);
-        uint4 *out = reinterpret_cast<uint4 *>(
-            (is_q ? p.q_out + (size_t)n * p.q_out_stride : p.k_out + (size_t)n * p.k_out_stride) + (size_t)hh * p.D);
-        if (!rotate) {
-            if (p.copy_rest) {
-                const uint4 a = in[v0], b = in[v1];
-                out[v0] = a;
-                out[v1] = b;
-            }
-            continue;
-        }
-        const uint4 a = in[v0], b = in[v1];
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-        uint32_t ya[4], yb[4];
+    // Four heads' loads in flight. Turned and copied units take the same path, with the result chosen at
+    // the end: a warp holds both kinds where a part of the head is turned.
+    for (int h0 = lane; h0 < heads; h0 += 4 * lanes) {
+        uint4 in[4][2];
+        uint4 *out[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (kInterleaved) {
-                const float2 y = turn(bf16_lo(aw[j]), bf16_hi(aw[j]), cs[j]);
-                const float2 z = turn(bf16_lo(bw[j]), bf16_hi(bw[j]), cs[4 + j]);
-                ya[j] = pack_bf16(y.x, y.y);
-                yb[j] = pack_bf16(z.x, z.y);
-            } else {
-                const float2 y = turn(bf16_lo(aw[j]), bf16_lo(bw[j]), cs[2 * j]);
-                const float2 z = turn(bf16_hi(aw[j]), bf16_hi(bw[j]), cs[2 * j + 1]);
-                ya[j] = pack_bf16(y.x, z.x);
-                yb[j] = pack_bf16(y.y, z.y);
+        for (int i = 0; i < 4; ++i) {
+            const int h = h0 + i * lanes;
+            if (h < heads) {
+                const bool is_q = h < p.q_heads;
+                const int hh = is_q ? h : h - p.q_heads;
+                const uint4 *src = reinterpret_cast<const uint4 *>((is_q ? p.q + (size_t)n * p.q_stride : p.k + (size_t)n * p.k_stride) +
+                                                                   (size_t)hh * p.D);
+                out[i] = reinterpret_cast<uint4 *>((is_q ? p.q_out + (size_t)n * p.q_out_stride : p.k_out + (size_t)n * p.k_out_stride) +
+                                                   (size_t)hh * p.D);
+                in[i][0] = src[v0];
+                in[i][1] = src[v1];
             }
         }
-        out[v0] = make_uint4(ya[0], ya[1], ya[2], ya[3]);
-        out[v1] = make_uint4(yb[0], yb[1], yb[2], yb[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (h0 + i * lanes >= heads)
+                break;
+            const uint32_t aw[4] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w};
+            const uint32_t bw[4] = {in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
+            uint32_t ya[4], yb[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (kInterleaved) {
+                    const float2 y = turn(bf16_lo(aw[j]), bf16_hi(aw[j]), cs[j]);
+                    const float2 z = turn(bf16_lo(bw[j]), bf16_hi(bw[j]), cs[4 + j]);
+                    ya[j] = pack_bf16(y.x, y.y);
+                    yb[j] = pack_bf16(z.x, z.y);
+                } else {
+                    const float2 y = turn(bf16_lo(aw[j]), bf16_lo(bw[j]), cs[2 * j]);
+                    const float2 z = turn(bf16_hi(aw[j]), bf16_hi(bw[j]), cs[2 * j + 1]);
+                    ya[j] = pack_bf16(y.x, z.x);
+                    yb[j] = pack_bf16(y.y, z.y);
+                }
+                ya[j] = rotate ? ya[j] : aw[j];
+                yb[j] = rotate ? yb[j] : bw[j];
+            }
+            out[i][v0] = make_uint4(ya[0], ya[1], ya[2], ya[3]);
+            out[i][v1] = make_uint4(yb[0], yb[1], yb[2], yb[3]);
+        }
     }
 }
 

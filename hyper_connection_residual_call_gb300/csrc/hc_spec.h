@@ -29,6 +29,25 @@ struct RopeParams {
     unsigned *status;
 };
 
+// Division of n < 2^31 by a fixed d, a multiplication and a shift (Granlund and
+// Montgomery): n * mul >> (31 + L) with mul = floor(2^(31+L) / d) + 1, L = ceil(log2 d).
+struct FastDiv {
+    uint32_t mul, shift, d;
+    FastDiv(uint32_t by = 1) : mul(0), shift(0), d(by)
+    {
+        uint32_t L = 0;
+        while ((1ull << L) < by)
+            ++L;
+        if (L > 0) {
+            mul = (uint32_t)((1ull << (31 + L)) / by + 1);
+            shift = L - 1;
+        }
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return mul ? __umulhi(n, mul) >> shift : n; }
+#endif
+};
+
 // A cache's tensors; bytes per row and per row's scales by type.
 struct KvView {
     int type, group, page_shift, heads, D, max_pages;
@@ -44,6 +63,7 @@ struct KvParams {
     long k_stride, v_stride;
     const int32_t *start;     // ctx_len or start
     int B, T;
+    FastDiv by_run, by_heads, by_runs;  // rows run over tokens, then heads, then runs of tokens, then sequences
     unsigned *status;
 };
 

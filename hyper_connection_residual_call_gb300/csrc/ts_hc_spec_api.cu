@@ -118,7 +118,7 @@ ts_status launched(cudaError_t e, const char *what) { return e == cudaSuccess ? 
 // Rows of the cache that one call moves, one thread for 16 elements: 32-bit indices.
 ts_status check_rows(long B, long T, const ts_hc_kv_cache *c)
 {
-    if (2 * B * T * c->n_kv_heads * (c->head_dim / 16) > INT_MAX)
+    if (2 * B * (T + 31) * c->n_kv_heads * (c->head_dim / 16) > INT_MAX)  // (runs of 32 tokens)
         return api_error(TS_ERR_UNSUPPORTED, "%ld tokens of %d heads are too many for one call: split them", B * T,
                          (int)c->n_kv_heads);
     return TS_OK;
