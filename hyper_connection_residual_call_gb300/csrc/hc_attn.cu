@@ -17,9 +17,9 @@
 // FP8 and INT4 codes go to shared memory as they are, so that the ring holds more
 // keys, and become operands in registers: e4m3 to bf16 by moving the bits and one
 // exact multiplication, the row's scale applied to the scores and to P. An INT4
-// key's codes go into the product as they are (q - 8, exact in bf16), one product
-// sum a group, and its scale and bias enter in fp32:
-//   q . k = sum_groups scale (sum Q (q - 8)) + (bias + 8 scale) sum Q
+// key's codes go into the product as they are (16 + q, exact in bf16, by one shift and
+// one logical operation), one product sum a group, and its scale and bias enter in fp32:
+//   q . k = sum_groups scale (sum Q (q + 16)) + (bias - 16 scale) sum Q
 // An INT4 value becomes q * scale + bias in fp16.
 #include <algorithm>
 #include <type_traits>
@@ -102,6 +102,22 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The first product of a sum: d = a b.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void mma16816_or_first(bool first, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (first)  // known when compiled
+        mma16816_first(d, a, b0, b1);
+    else
+        mma16816<false>(d, a, b0, b1);
+}
+
 // e4m3 codes in the high bytes of the two halves of w -> bf16x2. A code's 4
 // exponent and 3 mantissa bits, moved under bf16's sign, read as the value times
 // 2^-120 (denormals included); the multiplication by 2^120 is exact.
@@ -115,13 +131,14 @@ __device__ __forceinline__ uint32_t e4m3_hi_bf16x2(uint32_t w)
 
 __device__ __forceinline__ uint32_t e4m3_lo_bf16x2(uint32_t w) { return e4m3_hi_bf16x2(w << 8); }
 
-// INT4 codes in bits 0-3 of the two halves of w -> q - 8, bf16x2 (exact).
+// INT4 codes of an 8-code word at bits 4 i and 16 + 4 i -> 16 + q, bf16x2 (exact): the
+// code goes to mantissa bits 3-6 of 16.
+template <int i>
 __device__ __forceinline__ uint32_t int4_bf16x2(uint32_t w)
 {
-    const uint32_t bits = (w & 0x000F000Fu) | 0x43004300u;  // 128 + q
-    uint32_t y;
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(bits), "r"(0xC308C308u));  // - 136
-    return y;
+    constexpr int kShift = 3 - 4 * i;
+    const uint32_t at = kShift > 0 ? w << (kShift > 0 ? kShift : 0) : w >> (kShift > 0 ? 0 : -kShift);
+    return (at & 0x00780078u) | 0x41804180u;
 }
 
 // INT4 codes in bits 0-3 of the two halves of w -> q * scale + bias, fp16x2.
@@ -218,6 +235,7 @@ struct Walk {
     int lane, g, c, warp;
     int groups;               // INT4 groups of a row
     int spans;                // and 32-element spans of a group
+    int group_shift;          // log2 of a row's scales' bytes, 2 * groups
     int fetch_k, fetch_v;     // where this lane's first piece of a chunk goes
     int read_k, read_v;       // where its first reads of the keys and values lie
     const uint8_t *scales;    // INT4: the array that this lane fetches from
@@ -236,6 +254,7 @@ struct Walk {
         sc = fmaxf(fabsf(p.scale_log2), 1e-38f);
         groups = kType == kKvInt4 ? D / p.c.group : 0;
         spans = kType == kKvInt4 ? p.c.group / 32 : 0;
+        group_shift = kType == kKvInt4 ? 32 - __clz(groups) : 0;
         fetch_k = piece_at<kType, D, false>(lane / kUnits, lane % kUnits);
         fetch_v = piece_at<kType, D, true>(lane / kUnits, lane % kUnits);
         if (kType == kKvBf16) {
@@ -256,7 +275,8 @@ struct Walk {
         const bool ok = page >= 0;
         const size_t row = kv_row(p.c, ok ? page : 0, head, pos);
         const uint32_t dst = ring + s * F::kStage;
-        const uint8_t *k = p.c.k + row * F::kRow + lane * 16, *v = p.c.v + row * F::kRow + lane * 16;
+        const size_t at = row * F::kRow + lane * 16;
+        const uint8_t *k = p.c.k + at, *v = p.c.v + at;
         constexpr int kStep = 32 / kUnits;  // rows that the warp's 32 pieces are
         static_assert(kChunk * kUnits >= 32, "a chunk is at least a piece for each lane");
 #pragma unroll
@@ -267,10 +287,13 @@ struct Walk {
         if (kType == kKvFp8 && lane < 2)
             cp_async16(dst + 2 * F::kCodes + lane * F::kScale, (lane ? p.c.vs : p.c.ks) + row, ok);
         if (kType == kKvInt4) {  // 16 * groups * 2 bytes of each of the four arrays, eight lanes an array
-            const uint8_t *src = scales + row * groups * 2;
-            const uint32_t at = dst + 2 * F::kCodes + (lane >> 3) * F::kScale;
-            for (int x = lane & 7; x < groups * 2; x += 8)
-                cp_async16(at + x * 16, src + x * 16, ok);
+            const uint8_t *src = scales + (row << group_shift) + (lane & 7) * 16;
+            const uint32_t to = dst + 2 * F::kCodes + (lane >> 3) * F::kScale + (lane & 7) * 16;
+            const int n = 1 << group_shift;  // pieces: 16 keys of 2 * groups bytes
+            if ((lane & 7) < n)
+                cp_async16(to, src, ok);
+            if (F::kMaxGroups > 4 && n > 8)
+                cp_async16(to + 128, src + 128, ok);
         }
     }
 
@@ -344,7 +367,7 @@ struct Walk {
     }
 
     // INT4: a chunk's scales and biases, which lie by key and group, as the products take them:
-    // for the keys (scale, bias + 8 scale) in fp32 by group and key, for the values the fp16 scales,
+    // for the keys (scale, bias - 16 scale) in fp32 by group and key, for the values the fp16 scales,
     // then the biases, by group and key. Read with one load each below.
     __device__ __forceinline__ void lay_out_scales(uint32_t stage)
     {
@@ -352,7 +375,7 @@ struct Walk {
         for (int grp = lane >> 4; grp < groups; grp += 2) {
             const uint32_t a = stage + 2 * F::kCodes + 2 * (t * groups + grp);
             const float s = __half2float(__ushort_as_half((unsigned short)lds_u16(a)));
-            const float bias = fmaf(8.f, s, __half2float(__ushort_as_half((unsigned short)lds_u16(a + F::kScale))));
+            const float bias = fmaf(-16.f, s, __half2float(__ushort_as_half((unsigned short)lds_u16(a + F::kScale))));
             asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(tables + (grp * 16 + t) * 8), "f"(s), "f"(bias) : "memory");
             const uint32_t vt = tables + F::kMaxGroups * 128 + (grp * 16 + t) * 2;
             asm volatile("st.shared.u16 [%0], %1;" ::"r"(vt), "h"((uint16_t)lds_u16(a + 2 * F::kScale)) : "memory");
@@ -370,13 +393,6 @@ struct Walk {
         const uint32_t vbase = stage + F::kCodes + read_v;
         const auto key_at = [&](int x) { return kType == kKvBf16 ? (stage + read_k) ^ x : stage + (read_k ^ x); };
         float x[MT][2][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[i][n][e] = 0.f;
         if (kType == kKvInt4)
             lay_out_scales(stage);
 
@@ -390,8 +406,8 @@ struct Walk {
                 for (int i = 0; i < MT; ++i) {
                     uint32_t qa[4];
                     lds_words<4>(qa, qs + ((i * kSteps + k) * 32 + lane) * 16);
-                    mma16816<false>(x[i][0], qa, kb[0], kb[1]);
-                    mma16816<false>(x[i][1], qa, kb[2], kb[3]);
+                    mma16816_or_first(k == 0, x[i][0], qa, kb[0], kb[1]);
+                    mma16816_or_first(k == 0, x[i][1], qa, kb[2], kb[3]);
                 }
             }
         } else if (kType == kKvFp8) {
@@ -410,8 +426,8 @@ struct Walk {
                     for (int i = 0; i < MT; ++i) {
                         uint32_t qa[4];
                         lds_words<4>(qa, qs + ((i * kSteps + y * 4 + k) * 32 + lane) * 16);
-                        mma16816<false>(x[i][0], qa, k00, k01);
-                        mma16816<false>(x[i][1], qa, k10, k11);
+                        mma16816_or_first(y + k == 0, x[i][0], qa, k00, k01);
+                        mma16816_or_first(y + k == 0, x[i][1], qa, k10, k11);
                     }
                 }
             }
@@ -431,27 +447,25 @@ struct Walk {
             uint32_t table = tables + 2 * c * 8, sums = qsum + g * 8;  // of the group at hand
             int span = 0;
 #pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[i][n][e] = z[i][n][e] = 0.f;
+#pragma unroll
             for (int y = 0; y < D / 32; ++y) {  // 32 elements of every key, all in one group
-                if (span == 0) {
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                z[i][n][e] = 0.f;
-                }
                 const uint32_t w0 = lds32(key_at(y << 4)), w1 = lds32(key_at(y << 4) + 8 * F::kRow);
+                const uint32_t k0[4] = {int4_bf16x2<0>(w0), int4_bf16x2<1>(w0), int4_bf16x2<2>(w0), int4_bf16x2<3>(w0)};
+                const uint32_t k1[4] = {int4_bf16x2<0>(w1), int4_bf16x2<1>(w1), int4_bf16x2<2>(w1), int4_bf16x2<3>(w1)};
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t k00 = int4_bf16x2(w0 >> (8 * k)), k01 = int4_bf16x2(w0 >> (8 * k + 4));
-                    const uint32_t k10 = int4_bf16x2(w1 >> (8 * k)), k11 = int4_bf16x2(w1 >> (8 * k + 4));
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         uint32_t qa[4];
                         lds_words<4>(qa, qs + ((i * kSteps + 2 * y + k) * 32 + lane) * 16);
-                        mma16816<false>(z[i][0], qa, k00, k01);
-                        mma16816<false>(z[i][1], qa, k10, k11);
+                        mma16816<false>(z[i][0], qa, k0[2 * k], k0[2 * k + 1]);
+                        mma16816<false>(z[i][1], qa, k1[2 * k], k1[2 * k + 1]);
                     }
                 }
                 if (++span == spans) {
@@ -471,6 +485,7 @@ struct Walk {
                                     float &v = x[i][n][2 * h + e];
                                     v = fmaf(__uint_as_float(t[2 * e]), z[i][n][2 * h + e], v);
                                     v = fmaf(__uint_as_float(t[2 * e + 1]), __uint_as_float(q[h]), v);
+                                    z[i][n][2 * h + e] = 0.f;
                                 }
                         }
                     }
@@ -673,7 +688,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Format<kType, D>::template bloc
         };
         pages = page_of(t0 + w.lane);
         pages_next = page_of(t0 + 32 + w.lane);
-        int fetched = t0;
+        int fetched = t0, into = 0;
         const auto fetch_next = [&]() {
             if (fetched < t1) {
                 const int i = (fetched - t0) & 31;
@@ -686,10 +701,11 @@ __global__ void __launch_bounds__(kAttnThreads, (Format<kType, D>::template bloc
                 if (pos < seq.keys) {
                     if (page < 0 && w.lane == 0 && p.status)
                         atomicExch(p.status, kStatusBadArg);
-                    w.fetch((fetched - t0) % F::kStages, page, head, pos);
+                    w.fetch(into, page, head, pos);
                 }
             }
             ++fetched;
+            into = into + 1 == F::kStages ? 0 : into + 1;
             cp_commit();
         };
 #pragma unroll 1
@@ -845,13 +861,21 @@ __global__ void __launch_bounds__(kAttnThreads, (Format<kType, D>::template bloc
     }
 }
 
-// Joins the segments of the items that more than one CTA worked on: a warp a row,
-// lane i with the maximum and the sum of segment i (of up to 32 at a time), and the
-// segments' rows added in their order, eight loads in flight. What the kernel costs
-// is its chain of dependent loads -- lengths, maxima, rows -- so that it does little else.
-template <int D>
-__global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnParams p, const int rows, const int tile, const int grid, const int least)
+constexpr int kJoinLoads = 4;  // segments whose rows a lane has in flight
+
+// Joins the segments of the items that more than one CTA worked on: a warp a row (or,
+// kWarpsARow = 4, a block a row, its warps with every fourth segment, for few rows in
+// many segments), lane i with the maximum and the sum of segment i (of up to 32 at a
+// time), and the segments' rows added in their order. What the kernel costs is its chain
+// of dependent loads -- lengths, then maxima and the first rows together, then further
+// rows, some 0.7 us each -- and how many warps wait at a time. 64 items of 256 rows in 3
+// to 4 segments, 28 MB: 17 us (23 with four rows a warp); 12 rows in 76 segments: 9 us a
+// warp a row with eight loads in flight, 16 with four, 8 with a block a row.
+template <int D, int kWarpsARow>
+__global__ void __launch_bounds__(kAttnThreads, D == 256 ? 8 : 10) hc_attn_join_kernel(const __grid_constant__ AttnParams p, const int rows, const int tile,
+                                                                                       const int grid, const int least)
 {
+    __shared__ float across[kWarpsARow > 1 ? kWarps : 1][D + 2];
     __shared__ LineScratch scratch;
     pdl_launch_dependents();
     pdl_wait();
@@ -859,7 +883,7 @@ __global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnPa
     if (line.total == 0)
         return;
     const int ctas = attn_ctas(line.total, grid, least);
-    // blockIdx.x: sequence, head, row block; blockIdx.y: four rows of it
+    // blockIdx.x: sequence, head, row block; blockIdx.y: the rows of it
     const int blocks = p.c.heads * p.row_blocks;
     const int b = blockIdx.x / blocks, item = blockIdx.x % blocks;
     const SeqLen seq = attn_seq(p, b, tile);
@@ -877,7 +901,7 @@ __global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnPa
     if (c0 == c1)
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.y * kWarps + warp, row = (item % p.row_blocks) * rows + r;
+    const int r = kWarpsARow > 1 ? blockIdx.y : blockIdx.y * kWarps + warp, row = (item % p.row_blocks) * rows + r;
     if (r >= rows || row >= p.rows)
         return;
     // A CTA's segment of this item is its first, unless it is CTA c0 and began before the item.
@@ -892,14 +916,30 @@ __global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnPa
     for (int i = 0; i < kLoads * kVec; ++i)
         acc[i] = 0.f;
     float sum = 0.f, top = -INFINITY;
-    for (int base = c0; base <= c1; base += 32) {
-        const int n = min(32, c1 - base + 1);
+    const int first = kWarpsARow > 1 ? warp : 0;  // this warp's segments: first, first + kWarpsARow, ...
+    const int segs = (c1 - c0 - first) / kWarpsARow + (c1 - c0 >= first ? 1 : 0);
+#pragma unroll 1
+    for (int base = 0; base < segs; base += 32) {
+        const int n = min(32, segs - base);
+        const auto seg = [&](int i) { return slot(c0 + first + (base + i) * kWarpsARow); };
+        Vec v[kJoinLoads][kLoads];
+        const auto load = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < kJoinLoads; ++i)
+                if (i0 + i < n) {
+                    const Vec *x = reinterpret_cast<const Vec *>(seg(i0 + i) + (size_t)r * D);
+#pragma unroll
+                    for (int k = 0; k < kLoads; ++k)
+                        v[i][k] = __ldcg(x + lane + 32 * k);
+                }
+        };
         float m = -INFINITY, l = 0.f;
         if (lane < n) {
-            const float *s = slot(base + lane);
-            m = s[(size_t)rows * D + r];
-            l = s[(size_t)rows * (D + 1) + r];
+            const float *s = seg(lane) + (size_t)rows * D + r;
+            m = __ldcg(s);
+            l = __ldcg(s + rows);
         }
+        load(0);
         float now = m;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -916,18 +956,12 @@ __global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnPa
 #pragma unroll
         for (int i = 0; i < kLoads * kVec; ++i)
             acc[i] *= by;
-        for (int i0 = 0; i0 < n; i0 += 8) {
-            Vec v[8][kLoads];
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += kJoinLoads) {
+            if (i0 > 0)
+                load(i0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i0 + i < n) {
-                    const Vec *x = reinterpret_cast<const Vec *>(slot(base + i0 + i) + (size_t)r * D);
-#pragma unroll
-                    for (int k = 0; k < kLoads; ++k)
-                        v[i][k] = __ldcg(x + lane + 32 * k);
-                }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < kJoinLoads; ++i)
                 if (i0 + i < n) {
                     const float g = __shfl_sync(0xFFFFFFFFu, f, i0 + i);
 #pragma unroll
@@ -936,6 +970,37 @@ __global__ void __launch_bounds__(kAttnThreads) hc_attn_join_kernel(const AttnPa
                         for (int e = 0; e < kVec; ++e)
                             acc[k * kVec + e] += g * reinterpret_cast<const float *>(&v[i][k])[e];
                 }
+        }
+    }
+    if (kWarpsARow > 1) {  // the warps' sums, in their order
+        float *mine = across[warp];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                mine[(lane + 32 * k) * kVec + e] = acc[k * kVec + e];
+        if (lane == 0) {
+            mine[D] = top;
+            mine[D + 1] = sum;
+        }
+        __syncthreads();
+        if (warp > 0)
+            return;
+        top = fmaxf(fmaxf(across[0][D], across[kWarpsARow > 1 ? 1 : 0][D]), fmaxf(across[kWarpsARow > 1 ? 2 : 0][D], across[kWarpsARow > 1 ? 3 : 0][D]));
+        const float ref = top == -INFINITY ? 0.f : top;
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kLoads * kVec; ++i)
+            acc[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < (kWarpsARow > 1 ? kWarps : 1); ++w) {
+            const float f = ex2(across[w][D] - ref);
+            sum += f * across[w][D + 1];
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    acc[k * kVec + e] += f * across[w][(lane + 32 * k) * kVec + e];
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -1007,12 +1072,17 @@ cudaError_t launch_attn_join(const AttnParams &p, int rows, int tile, int grid, 
     lc.stream = stream;
     lc.blockDim = dim3(kAttnThreads);
     const int used = std::min(rows, p.rows);
-    lc.gridDim = dim3((unsigned)((long)p.B * p.c.heads * p.row_blocks), (unsigned)((used + kWarps - 1) / kWarps));
+    const long items = (long)p.B * p.c.heads * p.row_blocks;
+    // few rows: each has many segments, or there is little to do either way
+    const bool few = items * used <= 2 * grid;
+    lc.gridDim = dim3((unsigned)items, (unsigned)(few ? used : (used + kWarps - 1) / kWarps));
+    void (*kernel)(AttnParams, int, int, int, int) = nullptr;
     switch (p.c.D) {
-    case 64: return cudaLaunchKernelEx(&lc, hc_attn_join_kernel<64>, p, rows, tile, grid, least);
-    case 128: return cudaLaunchKernelEx(&lc, hc_attn_join_kernel<128>, p, rows, tile, grid, least);
-    default: return cudaLaunchKernelEx(&lc, hc_attn_join_kernel<256>, p, rows, tile, grid, least);
+    case 64: kernel = few ? hc_attn_join_kernel<64, kWarps> : hc_attn_join_kernel<64, 1>; break;
+    case 128: kernel = few ? hc_attn_join_kernel<128, kWarps> : hc_attn_join_kernel<128, 1>; break;
+    default: kernel = few ? hc_attn_join_kernel<256, kWarps> : hc_attn_join_kernel<256, 1>; break;
     }
+    return cudaLaunchKernelEx(&lc, kernel, p, rows, tile, grid, least);
 }
 
 size_t attn_part_bytes(int, int T, int q_heads, const KvView &c)
