@@ -22,8 +22,10 @@
 // a tile that reaches past the context, where what lies behind the last key, and
 // infinities and NaNs of nodes, are taken out); warp 12 issues the products, warp 13
 // the copies: TMA boxes for bf16 tiles, bulk copies of FP8 codes to a ring of their
-// own. A warp runs on scheduler (its number mod 4): with 64 rows or fewer the softmax
-// is on schedulers 0 and 1, and most of the conversion on 2 and 3.
+// own. FP8 tiles of 64 rows or fewer (kNarrow) are bound by their conversion, so that
+// warps 2, 3, 6 and 7, which own no row there, take part in it. A warp runs on scheduler
+// (its number mod 4): the softmax is then on schedulers 0 and 1 and most of the conversion
+// on 2 and 3.
 // Every wait is bounded; the first that runs out records TS_ERR_TIMEOUT and ends
 // the others.
 #include <algorithm>
@@ -37,14 +39,15 @@ namespace tshc {
 namespace {
 
 constexpr int kKeys = 128;               // keys of a tile
-constexpr int kSoftThreads = 256, kConvThreads = 192;  // with the last two warps 16: the most that leaves 128 registers a thread
-constexpr int kThreads = kSoftThreads + kConvThreads + 64;
+constexpr int kThreads = 512;            // 16 warps: the most that leaves 128 registers a thread
 constexpr int kMmaWarp = 12, kLoadWarp = 13;
 constexpr float kGrow = 8.f;             // log2: how far a row's maximum may grow over its reference
 constexpr uint32_t kTmemCols = 512;      // S of two streams, O of two streams
 
-template <int kType, int D, int NT>
+// kNarrow: 64 rows or fewer, so that half of the softmax warps have none and convert too.
+template <int kType, int D, int NT, bool kNarrow>
 struct Plan {
+    static constexpr int kSoftThreads = kNarrow ? 128 : 256, kConvThreads = kThreads - 64 - kSoftThreads;
     static constexpr int kTileBytes = kKeys * D * 2;              // a tile's keys or values as bf16
     static constexpr int kHalf = kKeys * 128;                     // 64 columns of it
     static constexpr int kQBytes = NT * kTileBytes;
@@ -59,7 +62,10 @@ struct Plan {
 
 template <int NT>
 struct Shared {
+    // Each barrier has one role that waits on it, or waiters whose own arrivals its next phase needs: a
+    // parity tells a phase from the next only, so that nobody may fall a phase behind.
     uint64_t full[8], empty[8];          // a tile slot
+    uint64_t go[8];                      // bf16: an empty slot is the conversion warps' to fill
     uint64_t raw_full[8], raw_empty[8];  // an FP8 code slot
     uint64_t q_full, q_empty;
     uint64_t s_ready[2], p_ready[2], o_done[2];
@@ -142,22 +148,16 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return y;
 }
 
-// 16 e4m3 codes -> two 16-byte pieces of bf16 (columns permuted as above), times
-// 2^-120 of the bf16 with the bits `factor`: a code's bits moved under bf16's sign
-// read as its value times 2^-120. For a row's scale 2^e the factor is 2^(120 + e).
-__device__ __forceinline__ void fp8_to_bf16(const uint4 in, uint32_t factor, uint4 &lo, uint4 &hi)
+// 8 e4m3 codes -> 8 bf16 (columns permuted as above), times 2^-120 of the bf16 with
+// the bits `factor`: a code's bits moved under bf16's sign read as its value times
+// 2^-120. For a row's scale 2^e the factor is 2^(120 + e). (The conversion instruction to
+// fp16, two to fp32 and one to bf16, and the scale: the same time, 160 us for 159.)
+__device__ __forceinline__ uint4 fp8_to_bf16(uint32_t w0, uint32_t w1, uint32_t factor)
 {
     const uint32_t f = factor * 0x10001u;
-    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-    uint32_t y[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t a = w[i] << 8, b = w[i];
-        y[2 * i] = mul_bf16x2(((a >> 4) & 0x07F007F0u) | (a & 0x80008000u), f);
-        y[2 * i + 1] = mul_bf16x2(((b >> 4) & 0x07F007F0u) | (b & 0x80008000u), f);
-    }
-    lo = make_uint4(y[0], y[1], y[2], y[3]);
-    hi = make_uint4(y[4], y[5], y[6], y[7]);
+    const uint32_t a = w0 << 8, b = w0, c = w1 << 8, d = w1;
+    return make_uint4(mul_bf16x2(((a >> 4) & 0x07F007F0u) | (a & 0x80008000u), f), mul_bf16x2(((b >> 4) & 0x07F007F0u) | (b & 0x80008000u), f),
+                      mul_bf16x2(((c >> 4) & 0x07F007F0u) | (c & 0x80008000u), f), mul_bf16x2(((d >> 4) & 0x07F007F0u) | (d & 0x80008000u), f));
 }
 
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v)
@@ -181,11 +181,12 @@ __device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t see)
             x[c] = 0xFF800000u;
 }
 
-template <int kType, int D, int NT>
+template <int kType, int D, int NT, bool kNarrow>
 __global__ void __launch_bounds__(kThreads, 1)
 hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const int least)
 {
-    using P = Plan<kType, D, NT>;
+    using P = Plan<kType, D, NT, kNarrow>;
+    constexpr int kSoftThreads = P::kSoftThreads, kConvThreads = P::kConvThreads;
     constexpr int kRows = 128 * NT;
     constexpr int kPieces = D / 8;
     extern __shared__ uint8_t smem_raw[];
@@ -211,6 +212,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         for (int i = 0; i < 8; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.go[i], 1);
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.raw_empty[i], 1);
         }
@@ -218,7 +220,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         mbar_init(&sh.q_empty, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.s_ready[s], 1);
-            mbar_init(&sh.p_ready[s], 128);
+            mbar_init(&sh.p_ready[s], kSoftThreads / 2);
             mbar_init(&sh.o_done[s], 1);
         }
         sh.dead = 0;
@@ -235,7 +237,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     const uint32_t tmem = sh.tmem;
     unsigned *status = p.status;
 
-    if (warp < 8) {
+    if (warp < 8 && !(kNarrow && (warp & 2))) {
         // ---------------------------------------------------------- softmax
         const int s = warp >> 2, row_in = tid & 127;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -439,9 +441,11 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         }
     } else if (warp < kMmaWarp || warp > kLoadWarp) {
         // ---------------------------------------------------------- conversion
-        const int ct = warp < kMmaWarp ? tid - kSoftThreads : tid - kSoftThreads - 64;
+        // 8-11, 14, 15 in turn, then the softmax warps without rows (2, 3, 6, 7)
+        const int ct = (warp >= 8 ? warp - 8 - (warp > kLoadWarp ? 2 : 0) : 6 + (warp & 1) + (warp >> 2) * 2) * 32 + lane;
         int index = 0;                    // tile slots used so far
         int raw = 0;                      // code slots used so far
+        uint32_t go_phase = 0;            // bit s: of go[s]
         uint32_t q_phase = 1;
         bool ok = true;
         for (int item = 0; ok && it.next(p, kKeys); ++item) {
@@ -499,12 +503,16 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 const int slot = (index + e) % P::kSlots, use = (index + e) / P::kSlots;
                 const int pos = (it_t0 + j) * kKeys;
                 const bool tail = pos + kKeys > seq.ctx;
-                // every slot's phases are waited for in turn, the copy warp's too: a parity tells one phase from the next only
-                ok = wait_or_dead(&sh.empty[slot], (use & 1) ^ 1, sh, status);
+                if (kType == kKvBf16) {
+                    if (!(value && tail))
+                        continue;  // the copy warp's
+                    ok = wait_or_dead(&sh.go[slot], (go_phase >> slot) & 1, sh, status);
+                    go_phase ^= 1u << slot;
+                } else {
+                    ok = wait_or_dead(&sh.empty[slot], (use & 1) ^ 1, sh, status);
+                }
                 if (!ok)
                     break;
-                if (kType == kKvBf16 && !(value && tail))
-                    continue;  // the copy warp's
                 const uint32_t tile = base + slot * P::kTileBytes;
                 const int rs = kType == kKvFp8 ? raw % P::kRaw : 0;
                 bool wild = false;
@@ -514,67 +522,76 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         break;
                     const uint32_t codes = base + P::kRing + rs * P::kRawBytes;
                     const uint32_t valid = *reinterpret_cast<volatile uint32_t *>(&sh.raw_valid[rs]);
-                    // A thread keeps its 16 columns and goes down the rows by kStep, a multiple of 8: every
-                    // address is its first one plus a constant.
-                    constexpr int kUnits = D / 16, kStep = kConvThreads / kUnits, kPasses = (kKeys + kStep - 1) / kStep;
+                    // The rows are shared out over kShares warps' worth of threads; warps 8 and 9, whose schedulers
+                    // have the narrow softmax and no other conversion, take two shares each. A thread keeps its 16
+                    // columns and goes down the rows by kStep, a multiple of 8: every address is its first one plus
+                    // a constant.
+                    constexpr int kWarps = kConvThreads / 32, kShares = kNarrow ? kWarps + 2 : kWarps;
+                    constexpr int kUnits = D / 16, kStep = kShares * 32 / kUnits, kPasses = (kKeys + kStep - 1) / kStep;
                     static_assert(kStep % 8 == 0, "the permutation of a row's pieces");
-                    const int r0 = ct / kUnits, x = ct % kUnits;
                     const uint8_t *src = smem_raw + (codes - smem_addr(smem_raw));
-                    // half of the lanes store their two pieces the other way round, so that a store's lanes meet no bank twice
-                    const bool swap = (x >> 2) & 1;
-                    const uint32_t a = tile_piece(tile, r0, 2 * x + swap), b = tile_piece(tile, r0, 2 * x + !swap);
-                    const bool last = r0 + kStep * (kPasses - 1) < kKeys;  // the same for a warp
-                    uint4 in[kPasses];
-                    int byte[kPasses], most = 0;
-#pragma unroll
-                    for (int i = 0; i < kPasses; ++i)
-                        if (i + 1 < kPasses || last) {
-                            in[i] = reinterpret_cast<const uint4 *>(src + (r0 + kStep * i) * D)[x];
-                            byte[i] = src[P::kRawCodes + r0 + kStep * i];
-                            most = max(most, byte[i]);
-                        }
-                    // Whole tiles of the context whose rows' factors are bf16 go straight through; branches
-                    // inside this loop cost more than its arithmetic (2020 cycles a tile against 3300 unrolled
-                    // with them, 16 warps of four kinds of code sharing the instruction caches).
-                    const bool plain = !(tail && value) && valid == 0xFFu && most <= 134;
-                    if (__all_sync(0xFFFFFFFFu, plain)) {
+#pragma unroll 1
+                    for (int share = ct; share < kShares * 32; share += kConvThreads) {
+                        const int r0 = share / kUnits, x = share % kUnits;
+                        // half of the lanes convert and store their second 8 columns first, so that a store's lanes meet
+                        // no bank twice
+                        const bool swap = (x >> 2) & 1;
+                        const uint32_t a = tile_piece(tile, r0, 2 * x + swap), b = tile_piece(tile, r0, 2 * x + !swap);
+                        const bool last = r0 + kStep * (kPasses - 1) < kKeys;  // the same for a warp
+                        const uint8_t *at = src + r0 * D + x * 16;
+                        uint4 in[kPasses];
+                        int byte[kPasses], most = 0;
 #pragma unroll
                         for (int i = 0; i < kPasses; ++i)
                             if (i + 1 < kPasses || last) {
-                                uint4 lo, hi;
-                                fp8_to_bf16(in[i], (uint32_t)(120 + byte[i]) << 7, lo, hi);
+                                in[i] = *reinterpret_cast<const uint4 *>(at + kStep * i * D);
+                                byte[i] = src[P::kRawCodes + r0 + kStep * i];
+                                most = max(most, byte[i]);
+                            }
+                        // Whole tiles of the context whose rows' factors are bf16 go straight through; branches
+                        // inside this loop cost more than its arithmetic (2020 cycles a tile against 3300 unrolled
+                        // with them, 16 warps of four kinds of code sharing the instruction caches).
+                        const bool plain = !(tail && value) && valid == 0xFFu && most <= 134;
+                        if (__all_sync(0xFFFFFFFFu, plain)) {
+#pragma unroll
+                            for (int i = 0; i < kPasses; ++i)
+                                if (i + 1 < kPasses || last) {
+                                    const uint32_t f = (uint32_t)(120 + byte[i]) << 7;
+                                    sts128(a + kStep * i * 128, fp8_to_bf16(swap ? in[i].z : in[i].x, swap ? in[i].w : in[i].y, f));
+                                    sts128(b + kStep * i * 128, fp8_to_bf16(swap ? in[i].x : in[i].z, swap ? in[i].y : in[i].w, f));
+                                }
+                        } else {
+#pragma unroll 1
+                            for (int i = 0; i < kPasses; ++i) {
+                                const int r = r0 + kStep * i;
+                                if (r >= kKeys)
+                                    break;
+                                const int by = src[P::kRawCodes + r];
+                                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                                bool use_it = (valid >> (r >> 4)) & 1u;
+                                if (tail && value && pos + r >= seq.ctx) {
+                                    if (pos + r >= seq.keys) {
+                                        use_it = false;
+                                    } else if (by == kFp8BadRow) {
+                                        wild |= use_it;
+                                        use_it = false;
+                                    }
+                                }
+                                if (use_it) {
+                                    const uint4 v = *reinterpret_cast<const uint4 *>(at + kStep * i * D);
+                                    const bool big = by > 134 && by != kFp8BadRow;  // its factor is not a bf16: two steps
+                                    const uint32_t f = by == kFp8BadRow ? 0x7FC0u : big ? 0x7B80u : (uint32_t)(120 + by) << 7;
+                                    lo = fp8_to_bf16(v.x, v.y, f);
+                                    hi = fp8_to_bf16(v.z, v.w, f);
+                                    if (big) {
+                                        const uint32_t g = (uint32_t)by << 7 | (uint32_t)by << 23;
+                                        lo = make_uint4(mul_bf16x2(lo.x, g), mul_bf16x2(lo.y, g), mul_bf16x2(lo.z, g), mul_bf16x2(lo.w, g));
+                                        hi = make_uint4(mul_bf16x2(hi.x, g), mul_bf16x2(hi.y, g), mul_bf16x2(hi.z, g), mul_bf16x2(hi.w, g));
+                                    }
+                                }
                                 sts128(a + kStep * i * 128, swap ? hi : lo);
                                 sts128(b + kStep * i * 128, swap ? lo : hi);
                             }
-                    } else {
-#pragma unroll 1
-                        for (int i = 0; i < kPasses; ++i) {
-                            const int r = r0 + kStep * i;
-                            if (r >= kKeys)
-                                break;
-                            int by = src[P::kRawCodes + r];
-                            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                            bool use_it = (valid >> (r >> 4)) & 1u;
-                            if (tail && value && pos + r >= seq.ctx) {
-                                if (pos + r >= seq.keys) {
-                                    use_it = false;
-                                } else if (by == kFp8BadRow) {
-                                    wild |= use_it;
-                                    use_it = false;
-                                }
-                            }
-                            if (use_it) {
-                                const bool big = by > 134 && by != kFp8BadRow;  // its factor is not a bf16: two steps
-                                fp8_to_bf16(reinterpret_cast<const uint4 *>(src + r * D)[x],
-                                            by == kFp8BadRow ? 0x7FC0u : big ? 0x7B80u : (uint32_t)(120 + by) << 7, lo, hi);
-                                if (big) {
-                                    const uint32_t f = (uint32_t)by << 7 | (uint32_t)by << 23;
-                                    lo = make_uint4(mul_bf16x2(lo.x, f), mul_bf16x2(lo.y, f), mul_bf16x2(lo.z, f), mul_bf16x2(lo.w, f));
-                                    hi = make_uint4(mul_bf16x2(hi.x, f), mul_bf16x2(hi.y, f), mul_bf16x2(hi.z, f), mul_bf16x2(hi.w, f));
-                                }
-                            }
-                            sts128(a + kStep * i * 128, swap ? hi : lo);
-                            sts128(b + kStep * i * 128, swap ? lo : hi);
                         }
                     }
                 } else {  // bf16 values that reach past the context
@@ -723,8 +740,11 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     ok = wait_or_dead(&sh.empty[slot], (((index + e) / P::kSlots) & 1) ^ 1, sh, status);
                     if (!ok)
                         break;
-                    if (value && pos + kKeys > seq.ctx)
-                        continue;  // the conversion warps'
+                    if (value && pos + kKeys > seq.ctx) {  // the conversion warps' to fill
+                        if (lane == 0)
+                            mbar_arrive(&sh.go[slot]);
+                        continue;
+                    }
                     if (lane == 0)
                         mbar_arrive_expect_tx(&sh.full[slot], P::kTileBytes);
                     __syncwarp();
@@ -779,11 +799,11 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
 
 constexpr int kLeastWide = 2;  // tiles a CTA has at least, where there is a choice
 
-template <int kType, int D, int NT>
+template <int kType, int D, int NT, bool kNarrow = false>
 cudaError_t launch_wide(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
 {
-    using Pl = Plan<kType, D, NT>;
-    auto *kernel = hc_attn_wide_kernel<kType, D, NT>;
+    using Pl = Plan<kType, D, NT, kNarrow>;
+    auto *kernel = hc_attn_wide_kernel<kType, D, NT, kNarrow>;
     static_assert(Pl::kTotal + sizeof(Shared<NT>) <= 227 * 1024, "shared memory");
     static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Pl::kTotal);
     if (set != cudaSuccess)
@@ -836,9 +856,12 @@ cudaError_t launch_attn_wide(const AttnParams &p, const LaunchCfg &cfg, cudaStre
             return two ? launch_wide<kKvBf16, 64, 2>(p, cfg, stream) : launch_wide<kKvBf16, 64, 1>(p, cfg, stream);
         return two ? launch_wide<kKvBf16, 128, 2>(p, cfg, stream) : launch_wide<kKvBf16, 128, 1>(p, cfg, stream);
     }
+    const bool narrow = p.rows <= 64;
     if (p.c.D == 64)
-        return two ? launch_wide<kKvFp8, 64, 2>(p, cfg, stream) : launch_wide<kKvFp8, 64, 1>(p, cfg, stream);
-    return two ? launch_wide<kKvFp8, 128, 2>(p, cfg, stream) : launch_wide<kKvFp8, 128, 1>(p, cfg, stream);
+        return two ? launch_wide<kKvFp8, 64, 2>(p, cfg, stream)
+                   : narrow ? launch_wide<kKvFp8, 64, 1, true>(p, cfg, stream) : launch_wide<kKvFp8, 64, 1>(p, cfg, stream);
+    return two ? launch_wide<kKvFp8, 128, 2>(p, cfg, stream)
+               : narrow ? launch_wide<kKvFp8, 128, 1, true>(p, cfg, stream) : launch_wide<kKvFp8, 128, 1>(p, cfg, stream);
 }
 
 }  // namespace tshc
