@@ -17,15 +17,16 @@
 //     which have maxima, sums and accumulators of their own and meet at the end.
 //   - O is rescaled only when a row's maximum grows by more than 2^8 over the one
 //     it is kept relative to.
-// Roles: warps 0-3 and 4-7 softmax of the two streams; warps 8-11, 14 and 15 put
+// Roles: warps 0-7 softmax, four a stream; warps 8-11, 14 and 15 put
 // what has to be converted into shared memory (the query; FP8 tiles; the values of
 // a tile that reaches past the context, where what lies behind the last key, and
 // infinities and NaNs of nodes, are taken out); warp 12 issues the products, warp 13
 // the copies: TMA boxes for bf16 tiles, bulk copies of FP8 codes to a ring of their
-// own. FP8 tiles of 64 rows or fewer (kNarrow) are bound by their conversion, so that
-// warps 2, 3, 6 and 7, which own no row there, take part in it. A warp runs on scheduler
-// (its number mod 4): the softmax is then on schedulers 0 and 1 and most of the conversion
-// on 2 and 3.
+// own. FP8 blocks of 64 rows or fewer (kNarrow) take the keys' codes as they are: the
+// query is split into two e4m3 parts, whose products with the codes are exact, and the
+// keys' scales go to the scores; and a row's softmax is two threads' work (4 x 64 rows
+// over 65536 keys: 130 us; with one thread a row 156, with converted keys 165). For 128
+// rows there is no second copy of the row's scores to share, and more rows hide the conversion.
 // Every wait is bounded; the first that runs out records TS_ERR_TIMEOUT and ends
 // the others.
 #include <algorithm>
@@ -39,34 +40,46 @@ namespace tshc {
 namespace {
 
 constexpr int kKeys = 128;               // keys of a tile
-constexpr int kThreads = 512;            // 16 warps: the most that leaves 128 registers a thread
+constexpr int kSoftThreads = 256, kConvThreads = 192;
+constexpr int kThreads = kSoftThreads + kConvThreads + 64;  // 16 warps: the most that leaves 128 registers a thread
 constexpr int kMmaWarp = 12, kLoadWarp = 13;
 constexpr float kGrow = 8.f;             // log2: how far a row's maximum may grow over its reference
 constexpr uint32_t kTmemCols = 512;      // S of two streams, O of two streams
 
-// kNarrow: 64 rows or fewer, so that half of the softmax warps have none and convert too.
+// kNarrow: 64 rows or fewer of FP8.
 template <int kType, int D, int NT, bool kNarrow>
 struct Plan {
-    static constexpr int kSoftThreads = kNarrow ? 128 : 256, kConvThreads = kThreads - 64 - kSoftThreads;
     static constexpr int kTileBytes = kKeys * D * 2;              // a tile's keys or values as bf16
     static constexpr int kHalf = kKeys * 128;                     // 64 columns of it
     static constexpr int kQBytes = NT * kTileBytes;
     static constexpr int kRawCodes = kKeys * D;                   // FP8
     static constexpr int kRawBytes = kType == kKvFp8 ? kRawCodes + 256 : 0;  // and its rows' scales
-    static constexpr int kBudget = (NT == 1 ? 223 : 225) * 1024 - kQBytes;  // beside the barriers (and NT = 1's maxima and sums)
-    static constexpr int kSlots = kType == kKvFp8 ? 3 : std::min(8, kBudget / kTileBytes);
-    static constexpr int kRaw = kType == kKvFp8 ? std::min(8, (kBudget - kSlots * kTileBytes) / kRawBytes) : 1;
-    static constexpr int kQ = kSlots * kTileBytes, kRing = kQ + kQBytes;
-    static constexpr int kTotal = kRing + kRaw * kRawBytes + 1024;  // and alignment
+    static constexpr int kExchange = kNarrow ? 2 * 64 * 36 * 4 : 0;  // 32 columns of 64 rows, twice, rows 36 floats apart
+    static constexpr int kBudget = (NT == 1 ? 220 : 222) * 1024 - kQBytes - kExchange;  // beside the barriers and tables
+    // Narrow blocks' keys go into the products as they lie in the cache, so that only values are converted.
+    static constexpr bool kRawKeys = kNarrow;
+    static constexpr int kKeyBytes = kRawKeys ? kKeys * D : kTileBytes;
+    // Key tiles are needed two products ahead, value tiles (and, FP8, their codes) a little later. 256 FP8 rows have
+    // room for three converted tiles: one of keys, which both products are through with early, and two of values
+    // (4 x 512 rows over 16384 keys: 139 us; two of keys and one of values 156).
+    static constexpr int kKeySlots = kRawKeys ? 3 : D == 64 ? 4 : kType == kKvFp8 && NT == 2 ? 1 : 2;
+    static constexpr int kSlots = kType == kKvFp8 ? 2 : std::min(8, (kBudget - kKeySlots * kKeyBytes) / kTileBytes);
+    static constexpr int kRaw = kType == kKvFp8 ? std::min(8, (kBudget - kSlots * kTileBytes - kKeySlots * kKeyBytes) / kRawBytes) : 1;
+    static constexpr int kQ = kSlots * kTileBytes, kKeyRing = kQ + kQBytes, kRing = kKeyRing + kKeySlots * kKeyBytes;
+    static constexpr int kTrade = kRing + kRaw * kRawBytes, kTotal = kTrade + kExchange + 1024;  // and alignment
+    static_assert(kType != kKvFp8 || kRaw >= 2, "codes of a tile's keys and values");
 };
 
-template <int NT>
+constexpr int kScaleSlots = 8;  // of the keys' scales: they are read until a tile's softmax is through, two units after its product
+
+template <int NT, bool kRawKeys>
 struct Shared {
     // Each barrier has one role that waits on it, or waiters whose own arrivals its next phase needs: a
     // parity tells a phase from the next only, so that nobody may fall a phase behind.
-    uint64_t full[8], empty[8];          // a tile slot
-    uint64_t go[8];                      // bf16: an empty slot is the conversion warps' to fill
+    uint64_t full[8], empty[8];          // a value slot
+    uint64_t go[8];                      // bf16: an empty value slot is the conversion warps' to fill
     uint64_t raw_full[8], raw_empty[8];  // an FP8 code slot
+    uint64_t k_full[4], k_empty[4];      // a key slot
     uint64_t q_full, q_empty;
     uint64_t s_ready[2], p_ready[2], o_done[2];
     uint32_t tmem;
@@ -74,23 +87,29 @@ struct Shared {
     int wild[4];                         // by item: a node's value held an infinity or a NaN
     uint32_t raw_valid[8];               // which 16-key chunks of a code slot lie in a page
     float m[2][NT == 1 ? 128 : 1], l[2][NT == 1 ? 128 : 1];  // of the two streams
+    alignas(16) uint8_t key_scale[kRawKeys ? kScaleSlots : 1][128];
+    alignas(16) float factor[2][2][kRawKeys ? 128 : 4];      // of a stream's tile, by turns: its keys' scales times log2(e) scale
+    float q_scale[2][kRawKeys ? 64 : 1];                     // of the query's rows, by items in turn
+    float top[2][2][2][kRawKeys ? 64 : 1];                   // of a stream's tile, by turns: each column half's maxima
     LineScratch line;
 };
 
 // Waits for the phase; false when it (or another wait of the block) ran out. The
 // warp's lanes leave together with one answer. (One lane looking for all of them
 // was slower: 165 us against 132 for 4 x 64 nodes over 16384 bf16 keys.)
-template <int NT>
-__device__ __forceinline__ bool wait_or_dead(uint64_t *bar, uint32_t parity, Shared<NT> &sh, unsigned *status)
+template <typename S>
+__device__ __forceinline__ bool wait_or_dead(uint64_t *bar, uint32_t parity, S &sh, unsigned *status)
 {
     bool there = mbar_try_wait(bar, parity);
     if (!there) {
         const uint64_t t0 = global_timer_ns();
         for (;;) {
+            if (*reinterpret_cast<volatile int *>(&sh.dead))
+                break;
 #pragma unroll 1
             for (int i = 0; i < 16 && !there; ++i)
                 there = mbar_try_wait(bar, parity);
-            if (there || *reinterpret_cast<volatile int *>(&sh.dead))
+            if (there)
                 break;
             if (global_timer_ns() - t0 > kWaitLimitNs) {
                 *reinterpret_cast<volatile int *>(&sh.dead) = 1;
@@ -105,36 +124,8 @@ __device__ __forceinline__ bool wait_or_dead(uint64_t *bar, uint32_t parity, Sha
 
 __device__ __forceinline__ void named_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-// The order in which a segment of n tiles' keys and values are first used, and so
-// loaded: two products ahead of the values. NT = 2 (each tile serves both
-// streams): K0 V0 K1 V1 ...; NT = 1 (tiles alternate): K0 K1 V0 K2 V1 ...
-template <int NT>
-__device__ __forceinline__ int key_index(int j)
-{
-    return NT == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1;
-}
-
-template <int NT>
-__device__ __forceinline__ int value_index(int j, int n)
-{
-    return NT == 2 ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * j + 1;
-}
-
-// The e-th of them.
-template <int NT>
-__device__ __forceinline__ void load_at(int e, int n, int &tile, bool &value)
-{
-    if (NT == 2) {
-        tile = e >> 1;
-        value = e & 1;
-    } else {
-        value = e == 2 * n - 1 || (e > 0 && !(e & 1));
-        tile = e == 2 * n - 1 ? n - 1 : e == 0 ? 0 : (e & 1) ? (e + 1) >> 1 : (e >> 1) - 1;
-    }
-}
-
-// FP8 columns: the conversion leaves elements (0, 2, 1, 3) of each four, in keys,
-// values and query alike; the results are put back when they are written.
+// FP8: the conversion leaves elements (0, 2, 1, 3) of each four. The query takes the same
+// order against converted keys, and the results are put back when they are written.
 template <int kType>
 __device__ __forceinline__ constexpr int column_of(int d)
 {
@@ -166,10 +157,58 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v)
 }
 
 
+// Eight elements of a query row, 16 lanes a row, as two e4m3 parts: the row is scaled by
+// the smallest power of two that brings it to at most 448, the first part is its nearest
+// e4m3, the second the rest's. A bf16 has 8 significant bits, each part 4: the sum is
+// exact for scaled elements of 2^-2 or more and off by at most 2^-10, half of e4m3's least
+// spacing, for smaller ones; the row's largest is more than 224, so that is at most 2^-17.8
+// of it. Returns the scale to undo (NaN for a row with an infinity
+// or a NaN).
+__device__ __forceinline__ float split_e4m3(const uint4 q, uint2 &hi, uint2 &lo)
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    const unsigned lanes = 0xFFFFu << (threadIdx.x & 16);  // the row's
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        top = __vmaxu2(top, __shfl_xor_sync(lanes, top, o));
+    top = max(top & 0xFFFFu, top >> 16);
+    const bool bad = top >= 0x7F80u;
+    const int byte = fp8_scale_byte(__uint_as_float(top << 16));
+    const float inv = bad ? 0.f : __uint_as_float((uint32_t)(254 - byte) << 23);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = make_float2(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+        h[i] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+        const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h[i], __NV_E4M3)));
+        l[i] = __nv_cvt_float2_to_fp8x2(make_float2(v.x - f.x, v.y - f.y), __NV_SATFINITE, __NV_E4M3);
+    }
+    hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+    return bad ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)byte << 23);
+}
+
 // Address of 16-byte piece x (8 columns) of row r in a 128-row tile of D columns.
 __device__ __forceinline__ uint32_t tile_piece(uint32_t tile, int r, int x)
 {
     return tile + (uint32_t)(x >> 3) * (kKeys * 128) + (uint32_t)r * 128 + (uint32_t)(((x & 7) ^ (r & 7)) << 4);
+}
+
+// Scores times their columns' factors (one address for all lanes).
+__device__ __forceinline__ void scale_columns(uint32_t (&x)[32], const float *factor)
+{
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(factor + c);
+        x[c] = __float_as_uint(__uint_as_float(x[c]) * f.x);
+        x[c + 1] = __float_as_uint(__uint_as_float(x[c + 1]) * f.y);
+        x[c + 2] = __float_as_uint(__uint_as_float(x[c + 2]) * f.z);
+        x[c + 3] = __float_as_uint(__uint_as_float(x[c + 3]) * f.w);
+    }
 }
 
 // Scores that a row does not see become -infinity.
@@ -186,11 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const int least)
 {
     using P = Plan<kType, D, NT, kNarrow>;
-    constexpr int kSoftThreads = P::kSoftThreads, kConvThreads = P::kConvThreads;
     constexpr int kRows = 128 * NT;
     constexpr int kPieces = D / 8;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ Shared<NT> sh;
+    constexpr bool kRawKeys = P::kRawKeys;
+    __shared__ Shared<NT, kRawKeys> sh;
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -216,6 +255,10 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.raw_empty[i], 1);
         }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sh.k_full[i], 1);
+            mbar_init(&sh.k_empty[i], 1);
+        }
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
         for (int s = 0; s < 2; ++s) {
@@ -237,15 +280,22 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     const uint32_t tmem = sh.tmem;
     unsigned *status = p.status;
 
-    if (warp < 8 && !(kNarrow && (warp & 2))) {
+    if (warp < 8) {
         // ---------------------------------------------------------- softmax
-        const int s = warp >> 2, row_in = tid & 127;
+        // A stream's warps: four, one for each 32 rows; narrow, four too, two for each 32 of 64 rows, with half
+        // of the columns each: the query's rows lie twice in its tile, and the streams take the copies on
+        // different lanes, so that all schedulers have their part of both.
+        const int s = kNarrow ? (warp >> 1) & 1 : warp >> 2, half = kNarrow ? warp >> 2 : 0;
+        const int row_in = tid & (kNarrow ? 63 : 127);
+        constexpr int kCols = kNarrow ? 64 : 128, kChunks = kCols / 32;  // a thread's columns
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lane_base + s * kKeys, to = tmem + lane_base + 256 + s * 128;
+        const uint32_t ts = tmem + lane_base + s * kKeys + half * 64, to = tmem + lane_base + 256 + s * 128 + half * 64;
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-38f);  // its sign went into the query; not 0, for masked scores' sake
         uint32_t s_phase = 0, o_phase = 0;
-        bool ok = true;
-        for (int item = 0; ok && it.next(p, kKeys); ++item) {
+        int key_tile = 0, turn = 0;       // raw keys: tiles before this item's
+        // (A wait that ran out ends nothing here: the warps go on through the same barriers, on whatever lies
+        // there, and every further wait returns at once.)
+        for (int item = 0; it.next(p, kKeys); ++item) {
             const SeqLen seq = it.seq;
             const int it_b = it.b, it_head = it.head, it_t0 = it.t0, it_t1 = it.t1, it_block = it.block;  // (the walk itself lives in memory)
             if (seq.bad && tid == 0 && status)
@@ -256,28 +306,40 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             const int t = valid ? row / p.G : 0;
             const uint32_t *mask = attn_mask_row(p, it_b, t);
             // a warp of rows past the last has nothing to do (rows do not meet)
-            const bool idle = row0 + (NT == 2 ? s * 128 : 0) + (warp & 3) * 32 >= p.rows;
+            const bool idle = !kNarrow && row0 + (NT == 2 ? s * 128 : 0) + (warp & 3) * 32 >= p.rows;
             float m = -INFINITY, mc = 0.f, l = 0.f;  // the reference (raw units), the same times sc (0 for none), the sum
             int units = 0;
+            float q_scale = 1.f;
             for (int j = NT == 2 ? 0 : s; j < n; j += 3 - NT, ++units) {
-                ok = wait_or_dead(&sh.s_ready[s], s_phase, sh, status);
-                if (!ok)
-                    break;
+                wait_or_dead(&sh.s_ready[s], s_phase, sh, status);
                 s_phase ^= 1;
                 tc_fence_after();
+                const float *factor = sh.factor[s][turn] + half * 64;
+                if (kRawKeys) {  // the tile's factors, one a thread
+                    const int i = half * 64 + row_in;
+                    sh.factor[s][turn][i] = fp8_scale(sh.key_scale[(key_tile + j) % kScaleSlots][i]) * sc;
+                    if (units == 0)
+                        q_scale = sh.q_scale[item & 1][row_in];
+                    named_sync(3 + s, kSoftThreads / 2);
+                    turn ^= 1;
+                }
                 if (!idle) {
                     const int pos = (it_t0 + j) * kKeys;
                     const bool tail = pos + kKeys > seq.ctx;
-                    const auto see = [&](int i) { return attn_sees32(p, mask, t, pos + 32 * i - seq.ctx, seq); };
+                    const auto see = [&](int i) { return attn_sees32(p, mask, t, pos + half * 64 + 32 * i - seq.ctx, seq); };
                     uint32_t x[32], y[32];
                     // the row's maximum: two loads in flight, four chains
                     float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int i = 0; i < 4; i += 2) {
+                    for (int i = 0; i < kChunks; i += 2) {
                         tmem_ld32_async(ts + 32 * i, x);
                         tmem_ld32_async(ts + 32 * i + 32, y);
                         tmem_wait_ld32(x);
                         tmem_wait_ld32(y);
+                        if (kRawKeys) {
+                            scale_columns(x, factor + 32 * i);
+                            scale_columns(y, factor + 32 * i + 32);
+                        }
                         if (tail) {
                             hide(x, see(i));
                             hide(y, see(i + 1));
@@ -288,18 +350,25 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             for (int v = 0; v < 4; ++v)
                                 tops[v] = fmaxf(tops[v], fmaxf(__uint_as_float(x[c + v]), __uint_as_float(y[c + v])));
                     }
-                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    const bool grow = top * sc > mc + kGrow || (m == -INFINITY && top > -INFINITY);
+                    // with raw keys the scores have the factor already, and the query row's scale is still to come
+                    const float by_row = kRawKeys ? q_scale : sc;
+                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    if (kNarrow) {  // the row's other half
+                        sh.top[s][turn][half][row_in] = top;
+                        named_sync(5 + s, kSoftThreads / 2);
+                        top = fmaxf(top, sh.top[s][turn][half ^ 1][row_in]);
+                    }
+                    const bool grow = top * by_row > mc + kGrow || (m == -INFINITY && top > -INFINITY);
                     if (__any_sync(0xFFFFFFFFu, grow)) {
                         const float to_m = fmaxf(m, top);
-                        const float to_mc = to_m == -INFINITY ? 0.f : to_m * sc;
+                        const float to_mc = to_m == -INFINITY ? 0.f : to_m * by_row;
                         const float by = m == -INFINITY ? 0.f : ex2(mc - to_mc);
                         m = to_m;
                         mc = to_mc;
                         l *= by;
                         if (units > 0) {  // before the first, the accumulator holds nothing
 #pragma unroll 1
-                            for (int i = 0; i < D / 32; ++i) {
+                            for (int i = 0; i < (kNarrow ? 2 : D / 32); ++i) {
                                 tmem_ld32(to + 32 * i, x);
 #pragma unroll
                                 for (int c = 0; c < 32; ++c)
@@ -308,7 +377,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             }
                         }
                     }
-                    const uint64_t sc2 = f32x2(sc, sc), off2 = f32x2(-mc, -mc);
+                    const uint64_t sc2 = f32x2(by_row, by_row), off2 = f32x2(-mc, -mc);
                     uint64_t sums[4] = {0, 0, 0, 0};
                     const auto weigh = [&](const uint32_t(&v)[32], int i) {
                         uint32_t w[16];
@@ -327,15 +396,19 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     // columns that this row has read
                     tmem_ld32_async(ts, x);
 #pragma unroll 1
-                    for (int i = 0; i < 4; i += 2) {
+                    for (int i = 0; i < kChunks; i += 2) {
                         tmem_wait_ld32(x);
                         tmem_ld32_async(ts + 32 * (i + 1), y);
+                        if (kRawKeys)
+                            scale_columns(x, factor + 32 * i);
                         if (tail)
                             hide(x, see(i));
                         weigh(x, i);
                         tmem_wait_ld32(y);
-                        if (i == 0)
+                        if (i + 2 < kChunks)
                             tmem_ld32_async(ts + 64, x);
+                        if (kRawKeys)
+                            scale_columns(y, factor + 32 * (i + 1));
                         if (tail)
                             hide(y, see(i + 1));
                         weigh(y, i + 1);
@@ -348,18 +421,19 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 tc_fence_before();
                 mbar_arrive(&sh.p_ready[s]);
             }
-            if (ok && units > 0) {
-                ok = wait_or_dead(&sh.o_done[s], o_phase, sh, status);
+            if (units > 0) {
+                wait_or_dead(&sh.o_done[s], o_phase, sh, status);
                 o_phase ^= 1;
                 tc_fence_after();
             }
             // results: with NT = 1 both streams hold sums of every row
             if (NT == 1) {
-                sh.m[s][row_in] = m == -INFINITY ? -INFINITY : mc;
-                sh.l[s][row_in] = l;
+                if (half == 0)
+                    sh.m[s][row_in] = m == -INFINITY ? -INFINITY : mc;
+                sh.l[s][half * 64 + row_in] = l;
                 named_sync(2, kSoftThreads);
             }
-            if (ok && !idle) {
+            if (!idle) {
                 float w0 = 1.f, w1 = 0.f, sum = l, top = m == -INFINITY ? -INFINITY : mc;
                 bool two = false;
                 if (NT == 1) {
@@ -369,7 +443,12 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     w0 = ex2(a - ref);
                     w1 = ex2(z - ref);
                     two = n > 1;  // the odd tiles' accumulator holds something
-                    sum = w0 * sh.l[0][row_in] + (two ? w1 * sh.l[1][row_in] : 0.f);
+                    float l0 = sh.l[0][row_in], l1 = sh.l[1][row_in];
+                    if (kNarrow) {
+                        l0 += sh.l[0][64 + row_in];
+                        l1 += sh.l[1][64 + row_in];
+                    }
+                    sum = w0 * l0 + (two ? w1 * l1 : 0.f);
                 }
                 const bool whole = it_t0 == 0 && it_t1 == seq.tiles;
                 const float scale = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
@@ -380,19 +459,45 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 const int wild = *reinterpret_cast<volatile int *>(&sh.wild[item & 3]);
                 const int from = it_t0 * kKeys, upto = min(seq.keys, it_t1 * kKeys);
                 const uint32_t o0 = tmem + lane_base + 256 + (NT == 2 ? s * 128 : 0), o1 = o0 + 128;
-                // NT = 1: each stream's threads write half of the columns
-                const int i0 = NT == 1 ? s * (D / 64) : 0, i1 = NT == 1 ? i0 + D / 64 : D / 32;
+                // NT = 1: each stream's threads write half of the columns; narrow, the second stream hands its
+                // part of the sums, which lies on other lanes, to the first, which writes
+                const int i0 = kNarrow ? 2 * half : NT == 1 ? s * (D / 64) : 0, i1 = NT == 1 ? i0 + D / 64 : D / 32;
+                float *trade = reinterpret_cast<float *>(smem_raw + (base - smem_addr(smem_raw)) + P::kTrade) + (half * 64 + row_in) * 36;
 #pragma unroll 1
                 for (int i = i0; i < i1; ++i) {
                     uint32_t x[32];
                     __syncwarp();
-                    tmem_ld32(o0 + 32 * i, x);
-                    if (NT == 1 && two) {
-                        uint32_t y[32];
-                        tmem_ld32(o1 + 32 * i, y);
+                    if (kNarrow) {
+                        tmem_ld32(to + 32 * (i - i0), x);
+                        if (s == 1)
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            x[c] = __float_as_uint(w0 * __uint_as_float(x[c]) + w1 * __uint_as_float(y[c]));
+                            for (int c = 0; c < 32; c += 4)
+                                *reinterpret_cast<float4 *>(trade + c) =
+                                    two ? make_float4(w1 * __uint_as_float(x[c]), w1 * __uint_as_float(x[c + 1]), w1 * __uint_as_float(x[c + 2]),
+                                                      w1 * __uint_as_float(x[c + 3]))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                        named_sync(2, kSoftThreads);
+                        if (s == 0)
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 y = *reinterpret_cast<const float4 *>(trade + c);
+                                x[c] = __float_as_uint(fmaf(w0, __uint_as_float(x[c]), y.x));
+                                x[c + 1] = __float_as_uint(fmaf(w0, __uint_as_float(x[c + 1]), y.y));
+                                x[c + 2] = __float_as_uint(fmaf(w0, __uint_as_float(x[c + 2]), y.z));
+                                x[c + 3] = __float_as_uint(fmaf(w0, __uint_as_float(x[c + 3]), y.w));
+                            }
+                        named_sync(2, kSoftThreads);
+                        if (s == 1)
+                            continue;
+                    } else {
+                        tmem_ld32(o0 + 32 * i, x);
+                        if (NT == 1 && two) {
+                            uint32_t y[32];
+                            tmem_ld32(o1 + 32 * i, y);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                x[c] = __float_as_uint(w0 * __uint_as_float(x[c]) + w1 * __uint_as_float(y[c]));
+                        }
                     }
                     if (!valid)
                         continue;
@@ -415,7 +520,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                                                  __uint_as_float(x[column_of<kType>(4 * v + 2)]), __uint_as_float(x[column_of<kType>(4 * v + 3)]));
                     }
                 }
-                if (wild && valid) {  // infinities and NaNs of values that the row sees: they are the element's sum
+                if (wild && valid && !(kNarrow && s == 1)) {  // infinities and NaNs of values that the row sees: they are the element's sum
                     for (int d = 32 * i0; d < 32 * i1; ++d) {
                         const float v = attn_wild_values(p, it_b, it_head, t, d, seq.ctx, from, upto);
                         if (finite_f32(v))
@@ -426,7 +531,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             slot[(size_t)r * D + d] = v;
                     }
                 }
-                if (valid && (NT == 2 || s == 0)) {
+                if (valid && (NT == 2 || (s == 0 && half == 0))) {
                     if (!whole) {
                         slot[(size_t)kRows * D + r] = top;
                         slot[(size_t)kRows * (D + 1) + r] = sum;
@@ -438,17 +543,16 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             if (NT == 1)
                 named_sync(2, kSoftThreads);  // the accumulators may be used again
             tc_fence_before();
+            key_tile += n;
         }
     } else if (warp < kMmaWarp || warp > kLoadWarp) {
         // ---------------------------------------------------------- conversion
-        // 8-11, 14, 15 in turn, then the softmax warps without rows (2, 3, 6, 7)
-        const int ct = (warp >= 8 ? warp - 8 - (warp > kLoadWarp ? 2 : 0) : 6 + (warp & 1) + (warp >> 2) * 2) * 32 + lane;
+        const int ct = warp < kMmaWarp ? tid - kSoftThreads : tid - kSoftThreads - 64;
         int index = 0;                    // tile slots used so far
         int raw = 0;                      // code slots used so far
         uint32_t go_phase = 0;            // bit s: of go[s]
         uint32_t q_phase = 1;
-        bool ok = true;
-        for (int item = 0; ok && it.next(p, kKeys); ++item) {
+        for (int item = 0; it.next(p, kKeys); ++item) {  // (as above: no wait ends it)
             const SeqLen seq = it.seq;
             const int it_b = it.b, it_head = it.head, it_t0 = it.t0, it_t1 = it.t1, it_block = it.block;  // (the walk itself lives in memory)
             const int n = it_t1 - it_t0, row0 = it_block * kRows;
@@ -456,16 +560,17 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 *reinterpret_cast<volatile int *>(&sh.wild[item & 3]) = 0;
             named_sync(1, kConvThreads);
             // the query
-            ok = wait_or_dead(&sh.q_empty, q_phase, sh, status);
+            wait_or_dead(&sh.q_empty, q_phase, sh, status);
             q_phase ^= 1;
-            if (ok) {
+            {
                 const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
                 // a thread keeps its 16-byte piece of a row and goes down the rows, eight loads in flight
                 constexpr int kStep = kConvThreads / kPieces;
                 const int x = ct % kPieces;
                 int row = row0 + ct / kPieces, t = row / p.G, g = row - t * p.G;
                 const uint16_t *q = p.q + (size_t)it_b * p.T * p.q_stride + (size_t)it_head * p.G * D + x * 8;
-                for (int r0 = ct / kPieces; r0 < kRows; r0 += 8 * kStep) {
+                constexpr int kQRows = kNarrow ? 64 : kRows;
+                for (int r0 = ct / kPieces; r0 < kQRows; r0 += 8 * kStep) {
                     uint4 v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -480,10 +585,23 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int r = r0 + i * kStep;
-                        if (r >= kRows)
+                        if (r >= kQRows)  // the same for the lanes of a row
                             break;
                         uint4 w = make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
-                        if (kType == kKvFp8)  // elements (0, 2, 1, 3) of each four
+                        if (kRawKeys) {
+                            uint2 hi, lo;
+                            const float scale = split_e4m3(w, hi, lo);
+                            const uint32_t at = base + P::kQ + r * 128 + ((((uint32_t)x >> 1) ^ (r & 7)) << 4) + (x & 1) * 8;
+#pragma unroll
+                            for (int copy = 0; copy < 2; ++copy) {
+                                asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(at + copy * 64 * 128), "r"(hi.x), "r"(hi.y) : "memory");
+                                asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(at + (kKeys + copy * 64) * 128), "r"(lo.x), "r"(lo.y) : "memory");
+                            }
+                            if (x == 0)
+                                sh.q_scale[item & 1][r] = scale;
+                            continue;
+                        }
+                        if (kType == kKvFp8)  // the converted keys' columns are permuted
                             w = make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632), __byte_perm(w.z, w.w, 0x5410),
                                            __byte_perm(w.z, w.w, 0x7632));
                         sts128(tile_piece(base + P::kQ + (r >> 7) * P::kTileBytes, r & 127, x), w);
@@ -496,43 +614,37 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             }
             // tiles
 #pragma unroll 1
-            for (int e = 0; ok && e < 2 * n; ++e) {
-                int j;
-                bool value;
-                load_at<NT>(e, n, j, value);
-                const int slot = (index + e) % P::kSlots, use = (index + e) / P::kSlots;
+            for (int e = 0; e < 2 * n; ++e) {  // keys and values in turn; the keys only where they are converted
+                const int j = e >> 1, tile_no = index + j;
+                const bool value = e & 1;
+                if (!value && (kType == kKvBf16 || kRawKeys))
+                    continue;
+                const int slot = value ? tile_no % P::kSlots : tile_no % P::kKeySlots;
+                const int use = value ? tile_no / P::kSlots : tile_no / P::kKeySlots;
                 const int pos = (it_t0 + j) * kKeys;
-                const bool tail = pos + kKeys > seq.ctx;
+                const bool tail = value && pos + kKeys > seq.ctx;
                 if (kType == kKvBf16) {
-                    if (!(value && tail))
+                    if (!tail)
                         continue;  // the copy warp's
-                    ok = wait_or_dead(&sh.go[slot], (go_phase >> slot) & 1, sh, status);
+                    wait_or_dead(&sh.go[slot], (go_phase >> slot) & 1, sh, status);
                     go_phase ^= 1u << slot;
                 } else {
-                    ok = wait_or_dead(&sh.empty[slot], (use & 1) ^ 1, sh, status);
+                    wait_or_dead(value ? &sh.empty[slot] : &sh.k_empty[slot], (use & 1) ^ 1, sh, status);
                 }
-                if (!ok)
-                    break;
-                const uint32_t tile = base + slot * P::kTileBytes;
+                const uint32_t tile = base + (value ? slot * P::kTileBytes : P::kKeyRing + slot * P::kKeyBytes);
                 const int rs = kType == kKvFp8 ? raw % P::kRaw : 0;
                 bool wild = false;
                 if (kType == kKvFp8) {
-                    ok = wait_or_dead(&sh.raw_full[rs], (raw / P::kRaw) & 1, sh, status);
-                    if (!ok)
-                        break;
+                    wait_or_dead(&sh.raw_full[rs], (raw / P::kRaw) & 1, sh, status);
                     const uint32_t codes = base + P::kRing + rs * P::kRawBytes;
                     const uint32_t valid = *reinterpret_cast<volatile uint32_t *>(&sh.raw_valid[rs]);
-                    // The rows are shared out over kShares warps' worth of threads; warps 8 and 9, whose schedulers
-                    // have the narrow softmax and no other conversion, take two shares each. A thread keeps its 16
-                    // columns and goes down the rows by kStep, a multiple of 8: every address is its first one plus
-                    // a constant.
-                    constexpr int kWarps = kConvThreads / 32, kShares = kNarrow ? kWarps + 2 : kWarps;
-                    constexpr int kUnits = D / 16, kStep = kShares * 32 / kUnits, kPasses = (kKeys + kStep - 1) / kStep;
+                    // A thread keeps its 16 columns and goes down the rows by kStep, a multiple of 8: every address is
+                    // its first one plus a constant.
+                    constexpr int kUnits = D / 16, kStep = kConvThreads / kUnits, kPasses = (kKeys + kStep - 1) / kStep;
                     static_assert(kStep % 8 == 0, "the permutation of a row's pieces");
                     const uint8_t *src = smem_raw + (codes - smem_addr(smem_raw));
-#pragma unroll 1
-                    for (int share = ct; share < kShares * 32; share += kConvThreads) {
-                        const int r0 = share / kUnits, x = share % kUnits;
+                    {
+                        const int r0 = ct / kUnits, x = ct % kUnits;
                         // half of the lanes convert and store their second 8 columns first, so that a store's lanes meet
                         // no bank twice
                         const bool swap = (x >> 2) & 1;
@@ -551,7 +663,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         // Whole tiles of the context whose rows' factors are bf16 go straight through; branches
                         // inside this loop cost more than its arithmetic (2020 cycles a tile against 3300 unrolled
                         // with them, 16 warps of four kinds of code sharing the instruction caches).
-                        const bool plain = !(tail && value) && valid == 0xFFu && most <= 134;
+                        const bool plain = !tail && valid == 0xFFu && most <= 134;
                         if (__all_sync(0xFFFFFFFFu, plain)) {
 #pragma unroll
                             for (int i = 0; i < kPasses; ++i)
@@ -569,7 +681,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                                 const int by = src[P::kRawCodes + r];
                                 uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
                                 bool use_it = (valid >> (r >> 4)) & 1u;
-                                if (tail && value && pos + r >= seq.ctx) {
+                                if (tail && pos + r >= seq.ctx) {
                                     if (pos + r >= seq.keys) {
                                         use_it = false;
                                     } else if (by == kFp8BadRow) {
@@ -622,17 +734,17 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 fence_async_shared();
                 named_sync(1, kConvThreads);
                 if (ct == 0) {
-                    mbar_arrive(&sh.full[slot]);
+                    mbar_arrive(value ? &sh.full[slot] : &sh.k_full[slot]);
                     if (kType == kKvFp8)
                         mbar_arrive(&sh.raw_empty[rs]);
                 }
                 ++raw;
             }
-            index += 2 * n;
+            index += n;
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- products
-        constexpr uint32_t kIdescS = umma_idesc_bf16(128, kKeys), kIdescO = umma_idesc_bf16(128, D) | kIdescBMnMajor;
+        constexpr uint32_t kIdescS = kRawKeys ? umma_idesc_e4m3(128, kKeys) : umma_idesc_bf16(128, kKeys), kIdescO = umma_idesc_bf16(128, D) | kIdescBMnMajor;
         int index = 0;
         uint32_t q_phase = 0, p_phase[2] = {0, 0};
         bool ok = true;
@@ -643,22 +755,28 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             if (!ok)
                 break;
             const auto scores = [&](int u) {
-                const int s = u & 1, j = NT == 2 ? u >> 1 : u, e = index + key_index<NT>(j);
-                const int slot = e % P::kSlots;
-                if (!wait_or_dead(&sh.full[slot], (e / P::kSlots) & 1, sh, status))
+                const int s = u & 1, j = NT == 2 ? u >> 1 : u, e = index + j;
+                const int slot = e % P::kKeySlots;
+                if (!wait_or_dead(&sh.k_full[slot], (e / P::kKeySlots) & 1, sh, status))
                     return false;
                 tc_fence_after();
                 const uint32_t q = desc_lo(base + P::kQ + (NT == 2 ? s * P::kTileBytes : 0), 16);
-                const uint32_t k = desc_lo(base + slot * P::kTileBytes, 16);
+                const uint32_t k = desc_lo(base + P::kKeyRing + slot * P::kKeyBytes, 16);
                 if (elect_one()) {
+                    if (kRawKeys) {  // the query's two parts, each a tile of 128 rows of 128 bytes
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t at = ((i >> 2) * P::kHalf + (i & 3) * 32) >> 4;
-                        umma_bf16_lo(tmem + s * kKeys, q + at, k + at, kIdescS, i > 0);
+                        for (int i = 0; i < 2 * (D / 32); ++i)
+                            umma_e4m3_lo(tmem + s * kKeys, q + ((i >> 2) * kKeys * 128 + (i & 3) * 32) / 16, k + (i & 3) * 2, kIdescS, i > 0);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint32_t at = ((i >> 2) * P::kHalf + (i & 3) * 32) >> 4;
+                            umma_bf16_lo(tmem + s * kKeys, q + at, k + at, kIdescS, i > 0);
+                        }
                     }
                     umma_commit(&sh.s_ready[s]);
                     if (NT == 1 || s == 1)
-                        umma_commit(&sh.empty[slot]);
+                        umma_commit(&sh.k_empty[slot]);
                     if (u == units - 1)
                         umma_commit(&sh.q_empty);
                 }
@@ -672,7 +790,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         ok = scores(u + 2);
                     continue;
                 }
-                const int s = u & 1, j = NT == 2 ? u >> 1 : u, e = index + value_index<NT>(j, n);
+                const int s = u & 1, j = NT == 2 ? u >> 1 : u, e = index + j;
                 const int slot = e % P::kSlots;
                 ok = wait_or_dead(&sh.full[slot], (e / P::kSlots) & 1, sh, status) &&
                      wait_or_dead(&sh.p_ready[s], p_phase[s], sh, status);
@@ -684,7 +802,8 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < kKeys / 16; ++i)
-                        umma_bf16_ts_lo(tmem + 256 + s * 128, tmem + s * kKeys + i * 8, v + i * (2048 >> 4), kIdescO, i > 0 || u >= 2);
+                        umma_bf16_ts_lo(tmem + 256 + s * 128, tmem + s * kKeys + (kNarrow && i >= 4 ? 64 + (i - 4) * 8 : i * 8), v + i * (2048 >> 4), kIdescO,
+                                        i > 0 || u >= 2);
                     if (NT == 1 || s == 1)
                         umma_commit(&sh.empty[slot]);
                     if (u + 2 >= units)
@@ -694,92 +813,132 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 if (u + 2 < units)
                     ok = scores(u + 2);
             }
-            index += 2 * n;
+            index += n;
         }
     } else {
         // ---------------------------------------------------------- copies
         const int per_page = min(kKeys, 1 << p.c.page_shift);  // keys of a chunk that lies in one page
         const int chunks = kKeys / per_page;                   // at most 8
         const long total_rows = (p.c.n_pages * p.c.heads) << p.c.page_shift;
-        int index = 0, raw = 0;
+        int index = 0;
         bool ok = true;
-        if (kType == kKvBf16 && lane == 0) {
+        if ((kType == kKvBf16 || kRawKeys) && lane == 0)
             tma_prefetch_map(&map_k);
+        if (kType == kKvBf16 && lane == 1)
             tma_prefetch_map(&map_v);
-        }
+        // One pass a tile, keys and values together: the warp's own instructions were what bound a stream of
+        // tiles (1400 cycles for each of the two, of some 130 instructions in turn). Lane 8 i + c copies chunk c:
+        //   bf16: the two 64-column halves of the keys (i = 0, 1) and of the values (2, 3);
+        //   FP8:  the keys' codes (0) and scales (1), the values' codes (2) and scales (3).
+        const int part = lane >> 3, c = lane & 7;
+        const bool value = part >= 2, chunk = c < chunks;
+        uint8_t *const tiles = smem_raw + (base - smem_addr(smem_raw));
         while (ok && it.next(p, kKeys)) {
             const SeqLen seq = it.seq;
             const int it_b = it.b, it_head = it.head, it_t0 = it.t0, it_t1 = it.t1;  // (the walk itself lives in memory)
             const int n = it_t1 - it_t0;
-            // pages: lane 8 i + c holds chunk c of tile 4 g + i, for the group g being loaded and its neighbours
+            // pages: lane 8 i + c holds chunk c of tile 4 g + i, for the group g at hand and the next
             const auto pages_of = [&](int g) {
-                const int j = 4 * g + (lane >> 3), c = lane & 7;
+                const int j = 4 * g + part;
                 const long pos = (long)(it_t0 + j) * kKeys + c * per_page;
-                return j < n && c < chunks && pos < seq.keys ? (int)kv_page(p.c, it_b, pos) : -1;
+                return j < n && chunk && pos < seq.keys ? (int)kv_page(p.c, it_b, pos) : -1;
             };
-            int before = -1, now = pages_of(0), after = pages_of(1), group = 0;
+            int now = pages_of(0), after = pages_of(1);
 #pragma unroll 1
-            for (int e = 0; ok && e < 2 * n; ++e) {
-                int j;
-                bool value;
-                load_at<NT>(e, n, j, value);
-                if (!value && (j >> 2) != group) {
-                    before = now;
+            for (int j = 0; ok && j < n; ++j) {
+                if (j > 0 && (j & 3) == 0) {
                     now = after;
-                    group = j >> 2;
-                    after = pages_of(group + 1);
+                    after = pages_of((j >> 2) + 1);
                 }
-                const int page = __shfl_sync(0xFFFFFFFFu, (j >> 2) == group ? now : before, (j & 3) * 8 + (lane & 7));
-                const int pos = (it_t0 + j) * kKeys, mine = pos + lane * per_page;
-                const bool chunk = lane < chunks, there = chunk && page >= 0;
+                const int page = __shfl_sync(0xFFFFFFFFu, now, (j & 3) * 8 + c);
+                const int pos = (it_t0 + j) * kKeys, mine = pos + c * per_page;
+                const bool there = chunk && page >= 0, tail = pos + kKeys > seq.ctx;
                 if (chunk && page < 0 && mine < seq.keys && status)
                     atomicExch(status, kStatusBadArg);
                 const long row = there ? (long)kv_row(p.c, page, it_head, mine) : total_rows;
-                if (kType == kKvBf16) {
-                    const int slot = (index + e) % P::kSlots;
-                    ok = wait_or_dead(&sh.empty[slot], (((index + e) / P::kSlots) & 1) ^ 1, sh, status);
+                const int tile = index + j, ks = tile % P::kKeySlots;
+                if (kType == kKvBf16 || kRawKeys) {
+                    ok = wait_or_dead(&sh.k_empty[ks], ((tile / P::kKeySlots) & 1) ^ 1, sh, status);
                     if (!ok)
                         break;
-                    if (value && pos + kKeys > seq.ctx) {  // the conversion warps' to fill
-                        if (lane == 0)
-                            mbar_arrive(&sh.go[slot]);
-                        continue;
-                    }
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&sh.full[slot], P::kTileBytes);
-                    __syncwarp();
-                    if (chunk) {  // a chunk without a page is read past the last row: zeros
-                        uint8_t *dst = smem_raw + (base - smem_addr(smem_raw)) + slot * P::kTileBytes + lane * per_page * 128;
-#pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-                            tma_load_2d(dst + h * P::kHalf, value ? &map_v : &map_k, h * 64, (int)row, &sh.full[slot]);
-                    }
-                    __syncwarp();
-                } else {
-                    const int rs = raw % P::kRaw;
-                    ok = wait_or_dead(&sh.raw_empty[rs], ((raw / P::kRaw) & 1) ^ 1, sh, status);
-                    if (!ok)
-                        break;
-                    const unsigned have = __ballot_sync(0xFFFFFFFFu, there);
-                    if (lane == 0) {
-                        uint32_t bits = 0;
-                        for (int c = 0; c < chunks; ++c)
-                            if ((have >> c) & 1u)
-                                bits |= ((1u << (per_page / 16)) - 1u) << (c * (per_page / 16));
-                        *reinterpret_cast<volatile uint32_t *>(&sh.raw_valid[rs]) = bits;
-                        mbar_arrive_expect_tx(&sh.raw_full[rs], __popc(have) * per_page * (D + 1));
-                    }
-                    __syncwarp();
-                    if (there) {
-                        uint8_t *dst = smem_raw + (base - smem_addr(smem_raw)) + P::kRing + rs * P::kRawBytes;
-                        bulk_copy_g2s(dst + lane * per_page * D, (value ? p.c.v : p.c.k) + row * D, per_page * D, &sh.raw_full[rs]);
-                        bulk_copy_g2s(dst + P::kRawCodes + lane * per_page, (value ? p.c.vs : p.c.ks) + row, per_page, &sh.raw_full[rs]);
-                    }
-                    __syncwarp();
-                    ++raw;
                 }
+                // the keys first: their product runs ahead of the values'
+                uint8_t *const key_tile = tiles + P::kKeyRing + ks * P::kKeyBytes;
+                if (kType == kKvBf16) {
+                    const int vs = tile % P::kSlots, half = part & 1;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&sh.k_full[ks], P::kTileBytes);
+                    __syncwarp();
+                    // a chunk without a page is read past the last row: zeros
+                    if (chunk && !value && half < D / 64)
+                        tma_load_2d(key_tile + half * P::kHalf + c * per_page * 128, &map_k, half * 64, (int)row, &sh.k_full[ks]);
+                    __syncwarp();
+                    ok = wait_or_dead(&sh.empty[vs], ((tile / P::kSlots) & 1) ^ 1, sh, status);
+                    if (!ok)
+                        break;
+                    if (lane == 0) {
+                        if (tail)  // the conversion warps' to fill
+                            mbar_arrive(&sh.go[vs]);
+                        else
+                            mbar_arrive_expect_tx(&sh.full[vs], P::kTileBytes);
+                    }
+                    __syncwarp();
+                    if (chunk && value && half < D / 64 && !tail)
+                        tma_load_2d(tiles + vs * P::kTileBytes + half * P::kHalf + c * per_page * 128, &map_v, half * 64, (int)row, &sh.full[vs]);
+                } else {
+                    const unsigned have = __ballot_sync(0xFFFFFFFFu, there && part == 0);
+                    const int bytes = __popc(have) * per_page;
+                    // which chunks of 16 keys lie in a page: bits of `have`, each per_page / 16 times
+                    uint32_t bits = 0xFFu;
+                    if (have != (1u << chunks) - 1) {
+                        bits = 0;
+                        for (int i = 0; i < 8; ++i)
+                            bits |= ((have >> (i * 16 / per_page)) & 1u) << i;
+                    }
+                    // a ring slot of codes and scales for the keys' or the values' lanes
+                    const auto codes_to = [&](int raw, bool values) {
+                        const int rs = raw % P::kRaw;
+                        if (!wait_or_dead(&sh.raw_empty[rs], ((raw / P::kRaw) & 1) ^ 1, sh, status))
+                            return false;
+                        if (lane == 0) {
+                            *reinterpret_cast<volatile uint32_t *>(&sh.raw_valid[rs]) = bits;
+                            mbar_arrive_expect_tx(&sh.raw_full[rs], bytes * (D + 1));
+                        }
+                        __syncwarp();
+                        if (value == values && there) {
+                            uint8_t *codes = tiles + P::kRing + rs * P::kRawBytes;
+                            const uint8_t *from = values ? p.c.v : p.c.k, *scales = values ? p.c.vs : p.c.ks;
+                            const bool code = !(part & 1);
+                            bulk_copy_g2s(code ? codes + c * per_page * D : codes + P::kRawCodes + c * per_page, code ? from + row * D : scales + row,
+                                          code ? per_page * D : per_page, &sh.raw_full[rs]);
+                        }
+                        __syncwarp();
+                        return true;
+                    };
+                    if (kRawKeys) {
+                        uint8_t *scales = sh.key_scale[tile % kScaleSlots];
+                        if (part == 1 && chunk && !there)  // codes 0 with a scale of 1
+                            for (int i = 0; i < per_page; i += 4)
+                                *reinterpret_cast<volatile uint32_t *>(scales + c * per_page + i) = 0x7F7F7F7Fu;
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&sh.k_full[ks], P::kKeyBytes + bytes);
+                        __syncwarp();
+                        if (part == 0 && chunk)  // without a page: past the last row, zeros
+                            tma_load_2d(key_tile + c * per_page * D, &map_k, 0, (int)row, &sh.k_full[ks]);
+                        if (part == 1 && there)
+                            bulk_copy_g2s(scales + c * per_page, p.c.ks + row, per_page, &sh.k_full[ks]);
+                        __syncwarp();
+                        ok = codes_to(tile, true);
+                    } else {
+                        ok = codes_to(2 * tile, false) && codes_to(2 * tile + 1, true);
+                    }
+                    if (!ok)
+                        break;
+                }
+                __syncwarp();
             }
-            index += 2 * n;
+            index += n;
         }
     }
 
@@ -804,7 +963,7 @@ cudaError_t launch_wide(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
 {
     using Pl = Plan<kType, D, NT, kNarrow>;
     auto *kernel = hc_attn_wide_kernel<kType, D, NT, kNarrow>;
-    static_assert(Pl::kTotal + sizeof(Shared<NT>) <= 227 * 1024, "shared memory");
+    static_assert(Pl::kTotal + sizeof(Shared<NT, Pl::kRawKeys>) <= 227 * 1024, "shared memory");
     static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Pl::kTotal);
     if (set != cudaSuccess)
         return set;
@@ -814,6 +973,11 @@ cudaError_t launch_wide(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
         const uint64_t rows = (uint64_t)p.c.n_pages * p.c.heads << p.c.page_shift;
         const uint32_t box = (uint32_t)std::min(kKeys, 1 << p.c.page_shift);
         if (!tc_make_map_2d(&map_k, p.c.k, rows, D, 64, box) || !tc_make_map_2d(&map_v, p.c.v, rows, D, 64, box))
+            return cudaErrorInvalidValue;
+    }
+    if (Pl::kRawKeys) {
+        const uint64_t rows = (uint64_t)p.c.n_pages * p.c.heads << p.c.page_shift;
+        if (!tc_make_map_2d_u8(&map_k, p.c.k, rows, D, 128, (uint32_t)std::min(kKeys, 1 << p.c.page_shift)))
             return cudaErrorInvalidValue;
     }
     cudaLaunchConfig_t lc{};
@@ -836,12 +1000,12 @@ cudaError_t launch_wide(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
 }  // namespace
 
 // Rows of a block of the wide kernel, or 0 where it does not serve: more than 32
-// rows; head_dim 64 or 128 (two accumulators and two score tiles fill TMEM); bf16
-// and FP8 rows (an INT4 key's exact value does not fit a bf16); fewer rows in the
-// pool than a tensor map's coordinates reach.
+// rows; bf16 rows of 64 or 128 elements (two accumulators and two score tiles fill
+// TMEM), FP8 rows of 128 (a row is one 128-byte line of an operand; an INT4 key's exact
+// value does not fit a bf16); fewer rows in the pool than a tensor map's coordinates reach.
 int attn_wide_rows(const KvView &c, long rows)
 {
-    if (rows <= 32 || c.D == 256 || c.type == kKvInt4)
+    if (rows <= 32 || !(c.type == kKvBf16 ? c.D <= 128 : c.type == kKvFp8 && c.D == 128))
         return 0;
     if (((c.n_pages * c.heads) << c.page_shift) >= (1l << 31) - kKeys)
         return 0;
@@ -856,12 +1020,8 @@ cudaError_t launch_attn_wide(const AttnParams &p, const LaunchCfg &cfg, cudaStre
             return two ? launch_wide<kKvBf16, 64, 2>(p, cfg, stream) : launch_wide<kKvBf16, 64, 1>(p, cfg, stream);
         return two ? launch_wide<kKvBf16, 128, 2>(p, cfg, stream) : launch_wide<kKvBf16, 128, 1>(p, cfg, stream);
     }
-    const bool narrow = p.rows <= 64;
-    if (p.c.D == 64)
-        return two ? launch_wide<kKvFp8, 64, 2>(p, cfg, stream)
-                   : narrow ? launch_wide<kKvFp8, 64, 1, true>(p, cfg, stream) : launch_wide<kKvFp8, 64, 1>(p, cfg, stream);
     return two ? launch_wide<kKvFp8, 128, 2>(p, cfg, stream)
-               : narrow ? launch_wide<kKvFp8, 128, 1, true>(p, cfg, stream) : launch_wide<kKvFp8, 128, 1>(p, cfg, stream);
+               : p.rows <= 64 ? launch_wide<kKvFp8, 128, 1, true>(p, cfg, stream) : launch_wide<kKvFp8, 128, 1>(p, cfg, stream);
 }
 
 }  // namespace tshc

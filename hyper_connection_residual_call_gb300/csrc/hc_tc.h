@@ -125,5 +125,7 @@ cudaError_t launch_tc_call(const TcCall &t, cudaStream_t stream);
 
 // A tensor map of a row-major bf16 matrix, 128-byte swizzled boxes (box_cols <= 64).
 bool tc_make_map_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows);
+// The same of a matrix of bytes (box_cols <= 128).
+bool tc_make_map_2d_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows);
 
 }  // namespace tshc

@@ -577,7 +577,9 @@ ts_status ts_hc_tree_build(const int32_t *parents, long parents_stride, const in
  *   workspace  >= ts_hc_tree_attention_workspace_bytes(...) bytes, 256-byte aligned; it need not be
  *              initialised and must not be shared by calls that can run at the same time
  * The products run on the tensor cores in bf16 (an INT4 row's values in fp16) with fp32 sums; the softmax's
- * maximum and sum are fp32. T <= 4096, T * q_heads/n_kv_heads <= 32768.
+ * maximum and sum are fp32. Over FP8 rows of 128 elements, 33 to 64 rows a key head
+ * (T * q_heads/n_kv_heads) meet the keys as two e4m3 parts each, which leaves an element of q off by at
+ * most 2^-17.8 of its row's largest. T <= 4096, T * q_heads/n_kv_heads <= 32768.
  */
 size_t ts_hc_tree_attention_workspace_bytes(int B, int T, int q_heads, const ts_hc_kv_cache *cache);
 ts_status ts_hc_tree_attention(const void *q, long q_stride, const ts_hc_kv_cache *cache, const int32_t *ctx_len,

@@ -534,6 +534,98 @@ def test_attention_is_deterministic_and_replays(kind):
     assert torch.equal(o, out) and torch.equal(l, lse)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("hq,hk,t", [(3, 1, 11), (8, 2, 12), (4, 1, 16), (13, 1, 5), (8, 1, 12), (16, 1, 8), (43, 1, 3), (8, 1, 32)])
+def test_attention_wide_blocks(kind, hq, hk, t):
+    """33 to 256 rows a key head: contexts around a tile's end, items that are cut and whole ones, odd groups."""
+    run_attention(22, kind, 0, 128, hq, hk, 16, [0, 1, 127, 128, 129, 300, 1025, 2600], t, [random_tree(np.random.default_rng(t), t)] * 8)
+
+
+def test_attention_fp8_query_of_wide_range():
+    """Up to 64 rows the query meets the codes as two e4m3 parts: an element is off by at most 2^-17.8 of its
+    row's largest (half of the second part's least spacing, 2^-10, of a largest element of more than 224), so
+    that a score is off by 2^-17.8 max|q| scale sum|k| more."""
+    g = gen(23)
+    t, ctx, d = 12, 300, 128
+    cache = make_cache(g, "fp8", 1, ctx + t, 1, 16, d)
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.hc_kv_write(randn(g, 1, ctx + t, 1, d), randn(g, 1, ctx + t, 1, d), cache, zero)
+    k, v = (R.f64(x[0]) for x in B.hc_kv_read(cache, zero, ctx + t))
+    q = randn(g, 1, t, 4, d)
+    q[..., 7] *= 64.0
+    q[:, 1] *= 2.0 ** -60
+    q[:, 2] *= 2.0 ** 20
+    q[:, 3] = 0
+    q[:, 4, :, 1:] = 0
+    see = np.tril(np.ones((t, t), bool))
+    out, lse = B.hc_tree_attention(q, cache, zero + ctx, scale=d ** -0.5)
+    out, lse, q64 = R.f64(out[0]), R.f64(lse[0]), R.f64(q[0])
+    want, want_lse, weight, reach = R.attention(q64, k, v, ctx, see, d ** -0.5)
+    delta = (d + 8) * U32 * reach + 2.0 ** -17.8 * np.abs(q64).max(-1) * d ** -0.5 * np.abs(k).sum(-1).max()
+    assert (np.abs(out - want) <= (1.5 * U16 + np.expm1(np.minimum(2 * delta, 600.0))[..., None] * 2 + 64 * U32) * weight + U16 * np.abs(want) + U32).all()
+    assert (np.abs(lse - want_lse) <= 2 * delta + 64 * U32 * (1 + np.abs(want_lse))).all()
+    # a NaN or an infinity in a row of the query reaches that row alone
+    bad = q.clone()
+    bad[0, 5, 2, 100], bad[0, 6, 1, 3] = float("nan"), float("inf")
+    out2, lse2 = B.hc_tree_attention(bad, cache, zero + ctx, scale=d ** -0.5)
+    assert bool(torch.isnan(out2[0, 5, 2]).all()) and bool(torch.isnan(lse2[0, 5, 2])) and not bool(torch.isfinite(out2[0, 6, 1]).any())
+    rest = torch.ones(t, 4, dtype=torch.bool, device="cuda")
+    rest[5, 2] = rest[6, 1] = False
+    again = B.hc_tree_attention(q, cache, zero + ctx, scale=d ** -0.5)
+    assert torch.equal(out2[0][rest], again[0][0][rest]) and torch.equal(lse2[0][rest], again[1][0][rest])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("hq", [4, 8, 16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_wide_blocks_keep_unseen_infinities_out(kind, hq, bad):
+    """Bad nodes, a bad row behind the last one, and rows that see nothing at all: 48, 96 and 192 rows."""
+    g = gen(24)
+    t, d = 12, 128
+    lens = torch.tensor([150, 0], dtype=torch.int32, device="cuda")
+    zero = torch.zeros_like(lens)
+    cache = make_cache(g, kind, 2, 200, 1, 32, d)
+    k, v = randn(g, 2, 170, 1, d), randn(g, 2, 170, 1, d)
+    see = R.sees(TREE)
+    see[7:9] = False  # in the second sequence these rows see nothing
+    mask = R.words(see)[None].expand(2, -1, -1).contiguous().cuda()
+    q = randn(g, 2, t, hq, d)
+    B.hc_kv_write(k, v, cache, zero)
+    out, lse = B.hc_tree_attention(q, cache, lens, mask=mask)
+    assert bool(torch.isfinite(out).all())
+    assert torch.count_nonzero(out[1, 7:9]) == 0 and bool(torch.isneginf(lse[1, 7:9]).all())
+    for i, n in enumerate((150, 0)):
+        k[i, n + 4, 0, 5], v[i, n + 5, 0, 7] = bad, bad
+        k[i, n + t:], v[i, n + t:] = bad, bad
+    B.hc_kv_write(k, v, cache, zero)
+    out2, lse2 = B.hc_tree_attention(q, cache, lens, mask=mask)
+    clean = torch.from_numpy(~(see[:, 4] | see[:, 5])).cuda()
+    assert torch.equal(out2[:, clean], out[:, clean]) and torch.equal(lse2[:, clean], lse[:, clean])
+    saw = torch.from_numpy(see[:, 5]).cuda()
+    assert not bool(torch.isfinite(out2[:, saw][..., 7]).any())
+    assert B.device_status() == B.TS_OK
+
+
+@pytest.mark.parametrize("kind,hq", [("bf16", 4), ("bf16", 16), ("fp8", 4), ("fp8", 8), ("fp8", 16)])
+def test_attention_wide_blocks_many_times(kind, hq):
+    """64, 128 and 256 rows, several items a block, 200 times: no wait runs out and every run has the same bits."""
+    g = gen(25)
+    b, t, ctx = 24, 16, 1800
+    cache = make_cache(g, kind, b, ctx + t, 2, 64, 128)
+    zero = torch.zeros(b, dtype=torch.int32, device="cuda")
+    B.hc_kv_write(randn(g, b, ctx + t, 2, 128), randn(g, b, ctx + t, 2, 128), cache, zero)
+    q, lens = randn(g, b, t, 2 * hq, 128), zero + ctx - 37 * torch.arange(b, device="cuda", dtype=torch.int32)
+    out, lse = B.hc_tree_attention(q, cache, lens)
+    o, l = torch.empty_like(out), torch.empty_like(lse)
+    ws = B.tree_attention_workspace(b, t, 2 * hq, cache)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        B.hc_tree_attention(q, cache, lens, out=o, lse=l, ws=ws)
+        differ += (o != out).sum() + (l != lse).sum()
+    assert int(differ) == 0
+    assert B.device_status() == B.TS_OK
+
+
 def test_attention_pages_past_2_to_31_elements():
     """A pool of more than 2^31 elements, the sequence at its end."""
     d, heads, page = 128, 8, 64
