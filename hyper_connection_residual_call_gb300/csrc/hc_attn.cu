@@ -863,6 +863,43 @@ __global__ void __launch_bounds__(kAttnThreads, (Format<kType, D>::template bloc
 
 constexpr int kJoinLoads = 4;  // segments whose rows a lane has in flight
 
+// The CTAs c0 .. c1 whose segments make up blockIdx.x's item (sequence, head, row block);
+// c0 = c1 where there is nothing to join.
+struct Segments {
+    int b, item, c0 = 0, c1 = 0, skew = 0;
+
+    __device__ __forceinline__ Segments(const AttnParams &p, int rows, int tile, int grid, int least, LineScratch &scratch)
+    {
+        const Line line(p, tile, scratch);
+        const int ctas = attn_ctas(line.total, grid, least);
+        const int blocks = p.c.heads * p.row_blocks;
+        b = blockIdx.x / blocks;
+        item = blockIdx.x % blocks;
+        if (line.total == 0)
+            return;
+        const SeqLen seq = attn_seq(p, b, tile);
+        // the line's index of sequence b: the thread that has it in its run
+        if (b >= line.b0 && b < line.b1) {
+            long at = line.base;
+            for (int i = line.b0; i < b; ++i)
+                at += attn_seq(p, i, tile).tiles * line.per;
+            scratch.base = at;
+        }
+        __syncthreads();
+        const long from = scratch.base + (long)item * seq.tiles;
+        const Cut cut(line.total, ctas);
+        c0 = cut.cta_of(from);
+        c1 = cut.cta_of(from + seq.tiles - 1);
+        skew = cut.first(c0) < from ? 1 : 0;
+    }
+
+    // A CTA's segment of this item is its first, unless it is CTA c0 and began before the item.
+    __device__ __forceinline__ float *slot(const AttnParams &p, int c, int rows, int D) const
+    {
+        return p.part + (size_t)(2 * c + (c == c0 ? skew : 0)) * attn_slot_floats(rows, D);
+    }
+};
+
 // Joins the segments of the items that more than one CTA worked on: a warp a row (or,
 // kWarpsARow = 4, a block a row, its warps with every fourth segment, for few rows in
 // many segments), lane i with the maximum and the sum of segment i (of up to 32 at a
@@ -879,35 +916,15 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 8 : 10) hc_attn_join_
     __shared__ LineScratch scratch;
     pdl_launch_dependents();
     pdl_wait();
-    const Line line(p, tile, scratch);
-    if (line.total == 0)
-        return;
-    const int ctas = attn_ctas(line.total, grid, least);
-    // blockIdx.x: sequence, head, row block; blockIdx.y: the rows of it
-    const int blocks = p.c.heads * p.row_blocks;
-    const int b = blockIdx.x / blocks, item = blockIdx.x % blocks;
-    const SeqLen seq = attn_seq(p, b, tile);
-    // the line's index of sequence b: the thread that has it in its run
-    if (b >= line.b0 && b < line.b1) {
-        long at = line.base;
-        for (int i = line.b0; i < b; ++i)
-            at += attn_seq(p, i, tile).tiles * line.per;
-        scratch.base = at;
-    }
-    __syncthreads();
-    const long from = scratch.base + (long)item * seq.tiles;
-    const Cut cut(line.total, ctas);
-    const int c0 = cut.cta_of(from), c1 = cut.cta_of(from + seq.tiles - 1);
+    const Segments of(p, rows, tile, grid, least, scratch);
+    const int b = of.b, item = of.item, c0 = of.c0, c1 = of.c1;
     if (c0 == c1)
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = kWarpsARow > 1 ? blockIdx.y : blockIdx.y * kWarps + warp, row = (item % p.row_blocks) * rows + r;
     if (r >= rows || row >= p.rows)
         return;
-    // A CTA's segment of this item is its first, unless it is CTA c0 and began before the item.
-    const size_t floats = attn_slot_floats(rows, D);
-    const int skew = cut.first(c0) < from ? 1 : 0;
-    const auto slot = [&](int c) { return p.part + (size_t)(2 * c + (c == c0 ? skew : 0)) * floats; };
+    const auto slot = [&](int c) { return of.slot(p, c, rows, D); };
     constexpr int kVec = D / 32 >= 4 ? 4 : 2;  // floats of a load
     constexpr int kLoads = D / (32 * kVec);    // loads of a lane: 1, or 2 for D = 256
     using Vec = typename std::conditional<kVec == 4, float4, float2>::type;
@@ -1016,6 +1033,76 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 8 : 10) hc_attn_join_
         p.lse[n] = top == -INFINITY ? (sum == 0.f ? -INFINITY : sum) : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
+// The same for the wide kernel's slots, whose sums lie by four columns: a block has eight
+// rows, whose pieces fill a line, and a thread adds up its row's pieces, of up to four
+// segments at a time, with its own factors.
+template <int D>
+__global__ void __launch_bounds__(kAttnThreads, 8) hc_attn_join_wide_kernel(const __grid_constant__ AttnParams p, const int rows, const int tile,
+                                                                            const int grid, const int least)
+{
+    constexpr int kLoads = D / 64;  // pieces of a thread: a row has D / 4, 16 threads a row
+    __shared__ LineScratch scratch;
+    pdl_launch_dependents();
+    pdl_wait();
+    const Segments of(p, rows, tile, grid, least, scratch);
+    if (of.c0 == of.c1)
+        return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.y * 8 + (lane & 7), row = (of.item % p.row_blocks) * rows + r;
+    const int piece = warp * (D / 16) + (lane >> 3);  // and every fourth from there
+    float acc[kLoads][4] = {}, sum = 0.f, top = -INFINITY;
+#pragma unroll 1
+    for (int c = of.c0; c <= of.c1; c += kJoinLoads) {
+        float m[kJoinLoads], l[kJoinLoads];
+        float4 v[kJoinLoads][kLoads];
+#pragma unroll
+        for (int i = 0; i < kJoinLoads; ++i) {
+            m[i] = -INFINITY;
+            if (c + i <= of.c1) {
+                const float *s = of.slot(p, c + i, rows, D);
+                m[i] = __ldcg(s + (size_t)rows * D + r);
+                l[i] = __ldcg(s + (size_t)rows * (D + 1) + r);
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k)
+                    v[i][k] = __ldcg(reinterpret_cast<const float4 *>(s) + (size_t)(piece + 4 * k) * rows + r);
+            }
+        }
+        const float to = fmaxf(fmaxf(fmaxf(top, m[0]), m[1]), fmaxf(m[2], m[3])), ref = to == -INFINITY ? 0.f : to;
+        const float by = ex2(top - ref);  // 0 at the first
+        top = to;
+        sum *= by;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[k][e] *= by;
+#pragma unroll
+        for (int i = 0; i < kJoinLoads; ++i)
+            if (c + i <= of.c1) {
+                const float f = ex2(m[i] - ref);
+                sum += f * l[i];
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    acc[k][0] += f * v[i][k].x;
+                    acc[k][1] += f * v[i][k].y;
+                    acc[k][2] += f * v[i][k].z;
+                    acc[k][3] += f * v[i][k].w;
+                }
+            }
+    }
+    if (row >= p.rows)
+        return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int t = row / p.G, h = (of.item / p.row_blocks) * p.G + row % p.G;
+    const size_t n = ((size_t)of.b * p.T + t) * p.q_heads + h;
+    uint2 *out = reinterpret_cast<uint2 *>(p.out + n * D);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k)
+        out[piece + 4 * k] = make_uint2(pack2_bf16(acc[k][0] * inv, acc[k][1] * inv), pack2_bf16(acc[k][2] * inv, acc[k][3] * inv));
+    if (piece == 0 && p.lse)
+        p.lse[n] = top == -INFINITY ? (sum == 0.f ? -INFINITY : sum) : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
 constexpr int kLeastTiles = 2;  // tiles a CTA has at least, where there is a choice
 
 template <int kType, int D, int MT>
@@ -1046,7 +1133,7 @@ cudaError_t launch_few(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
     cudaError_t e = cudaLaunchKernelEx(&lc, kernel, p, kLeastTiles);
     if (e != cudaSuccess)
         return e;
-    return launch_attn_join(p, kRows, kTile, grid, kLeastTiles, stream);
+    return launch_attn_join(p, kRows, kTile, grid, kLeastTiles, false, stream);
 }
 
 template <int kType>
@@ -1061,7 +1148,7 @@ cudaError_t launch_type(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_attn_join(const AttnParams &p, int rows, int tile, int grid, int least, cudaStream_t stream)
+cudaError_t launch_attn_join(const AttnParams &p, int rows, int tile, int grid, int least, bool by_columns, cudaStream_t stream)
 {
     cudaLaunchConfig_t lc{};
     cudaLaunchAttribute at[1];
@@ -1075,9 +1162,12 @@ cudaError_t launch_attn_join(const AttnParams &p, int rows, int tile, int grid, 
     const long items = (long)p.B * p.c.heads * p.row_blocks;
     // few rows: each has many segments, or there is little to do either way
     const bool few = items * used <= 2 * grid;
-    lc.gridDim = dim3((unsigned)items, (unsigned)(few ? used : (used + kWarps - 1) / kWarps));
+    const int a_block = by_columns ? 8 : few ? 1 : kWarps;  // rows
+    lc.gridDim = dim3((unsigned)items, (unsigned)((used + a_block - 1) / a_block));
     void (*kernel)(AttnParams, int, int, int, int) = nullptr;
-    switch (p.c.D) {
+    if (by_columns)
+        kernel = p.c.D == 64 ? hc_attn_join_wide_kernel<64> : hc_attn_join_wide_kernel<128>;
+    else switch (p.c.D) {
     case 64: kernel = few ? hc_attn_join_kernel<64, kWarps> : hc_attn_join_kernel<64, 1>; break;
     case 128: kernel = few ? hc_attn_join_kernel<128, kWarps> : hc_attn_join_kernel<128, 1>; break;
     default: kernel = few ? hc_attn_join_kernel<256, kWarps> : hc_attn_join_kernel<256, 1>; break;

@@ -162,8 +162,8 @@ struct Items {
     __device__ __forceinline__ int slot() const { return from > first ? 1 : 0; }
 };
 
-// A partial slot: unnormalised sums [rows][D], then the rows' maxima (in units of
-// log2) and sums.
+// A partial slot: unnormalised sums [rows][D] (the wide kernel's [D / 4][rows][4]), then
+// the rows' maxima (in units of log2) and sums.
 __host__ __device__ __forceinline__ size_t attn_slot_floats(int rows, int D) { return (size_t)rows * (D + 2); }
 
 // Whether node row t sees position ctx + i (i >= 0).
@@ -251,6 +251,6 @@ __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi)
 int attn_wide_rows(const KvView &c, long rows);
 cudaError_t launch_attn_wide(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t stream);
 // Joins the segments that either kernel left: blocks of `rows` rows, tiles of `tile` keys.
-cudaError_t launch_attn_join(const AttnParams &p, int rows, int tile, int grid, int least, cudaStream_t stream);
+cudaError_t launch_attn_join(const AttnParams &p, int rows, int tile, int grid, int least, bool by_columns, cudaStream_t stream);
 
 }  // namespace tshc

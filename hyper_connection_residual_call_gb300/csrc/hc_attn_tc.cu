@@ -81,7 +81,7 @@ struct Shared {
     uint64_t raw_full[8], raw_empty[8];  // an FP8 code slot
     uint64_t k_full[4], k_empty[4];      // a key slot
     uint64_t q_full, q_empty;
-    uint64_t s_ready[2], p_ready[2], o_done[2];
+    uint64_t s_ready[2], p_half[2], p_ready[2], o_done[2];
     uint32_t tmem;
     int dead;                            // a wait ran out
     int wild[4];                         // by item: a node's value held an infinity or a NaN
@@ -263,6 +263,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         mbar_init(&sh.q_empty, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.s_ready[s], 1);
+            mbar_init(&sh.p_half[s], kSoftThreads / 2);
             mbar_init(&sh.p_ready[s], kSoftThreads / 2);
             mbar_init(&sh.o_done[s], 1);
         }
@@ -412,11 +413,18 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         if (tail)
                             hide(y, see(i + 1));
                         weigh(y, i + 1);
+                        if (!kNarrow && i == 0) {  // the product can begin with the first 64 keys
+                            tmem_wait_st();
+                            tc_fence_before();
+                            mbar_arrive(&sh.p_half[s]);
+                        }
                     }
                     float a, z;
                     f32x2_unpack(fadd2(fadd2(sums[0], sums[1]), fadd2(sums[2], sums[3])), a, z);
                     l += a + z;
                     tmem_wait_st();
+                } else {
+                    mbar_arrive(&sh.p_half[s]);
                 }
                 tc_fence_before();
                 mbar_arrive(&sh.p_ready[s]);
@@ -513,10 +521,11 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             out[v] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     } else {
-                        float4 *out = reinterpret_cast<float4 *>(slot + (size_t)r * D + 32 * i);
+                        // by four columns, so that the lanes' stores lie side by side
+                        float4 *out = reinterpret_cast<float4 *>(slot) + (size_t)(8 * i) * kRows + r;
 #pragma unroll
                         for (int v = 0; v < 8; ++v)
-                            out[v] = make_float4(__uint_as_float(x[column_of<kType>(4 * v)]), __uint_as_float(x[column_of<kType>(4 * v + 1)]),
+                            out[v * kRows] = make_float4(__uint_as_float(x[column_of<kType>(4 * v)]), __uint_as_float(x[column_of<kType>(4 * v + 1)]),
                                                  __uint_as_float(x[column_of<kType>(4 * v + 2)]), __uint_as_float(x[column_of<kType>(4 * v + 3)]));
                     }
                 }
@@ -528,7 +537,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         if (whole)
                             p.out[at * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
                         else
-                            slot[(size_t)r * D + d] = v;
+                            slot[((size_t)(d >> 2) * kRows + r) * 4 + (d & 3)] = v;
                     }
                 }
                 if (valid && (NT == 2 || (s == 0 && half == 0))) {
@@ -792,18 +801,35 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 }
                 const int s = u & 1, j = NT == 2 ? u >> 1 : u, e = index + j;
                 const int slot = e % P::kSlots;
-                ok = wait_or_dead(&sh.full[slot], (e / P::kSlots) & 1, sh, status) &&
-                     wait_or_dead(&sh.p_ready[s], p_phase[s], sh, status);
+                ok = wait_or_dead(&sh.full[slot], (e / P::kSlots) & 1, sh, status);
+                if (!ok)
+                    break;
+                const uint32_t v = desc_lo(base + slot * P::kTileBytes, P::kHalf);
+                const auto weighted = [&](int i) {
+                    umma_bf16_ts_lo(tmem + 256 + s * 128, tmem + s * kKeys + (kNarrow && i >= 4 ? 64 + (i - 4) * 8 : i * 8), v + i * (2048 >> 4), kIdescO,
+                                    i > 0 || u >= 2);
+                };
+                constexpr int kEarly = kNarrow ? 0 : 4;  // steps of the first 64 keys
+                if (!kNarrow) {
+                    ok = wait_or_dead(&sh.p_half[s], p_phase[s], sh, status);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (elect_one())
+#pragma unroll
+                        for (int i = 0; i < kEarly; ++i)
+                            weighted(i);
+                    __syncwarp();
+                }
+                ok = wait_or_dead(&sh.p_ready[s], p_phase[s], sh, status);
                 if (!ok)
                     break;
                 p_phase[s] ^= 1;
                 tc_fence_after();
-                const uint32_t v = desc_lo(base + slot * P::kTileBytes, P::kHalf);
                 if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i)
-                        umma_bf16_ts_lo(tmem + 256 + s * 128, tmem + s * kKeys + (kNarrow && i >= 4 ? 64 + (i - 4) * 8 : i * 8), v + i * (2048 >> 4), kIdescO,
-                                        i > 0 || u >= 2);
+                    for (int i = kEarly; i < kKeys / 16; ++i)
+                        weighted(i);
                     if (NT == 1 || s == 1)
                         umma_commit(&sh.empty[slot]);
                     if (u + 2 >= units)
@@ -994,7 +1020,7 @@ cudaError_t launch_wide(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
     cudaError_t e = cudaLaunchKernelEx(&lc, kernel, p, map_k, map_v, kLeastWide);
     if (e != cudaSuccess)
         return e;
-    return launch_attn_join(p, 128 * NT, kKeys, grid, kLeastWide, stream);
+    return launch_attn_join(p, 128 * NT, kKeys, grid, kLeastWide, true, stream);
 }
 
 }  // namespace
