@@ -22,11 +22,24 @@
 // a tile that reaches past the context, where what lies behind the last key, and
 // infinities and NaNs of nodes, are taken out); warp 12 issues the products, warp 13
 // the copies: TMA boxes for bf16 tiles, bulk copies of FP8 codes to a ring of their
-// own. FP8 blocks of 64 rows or fewer (kNarrow) take the keys' codes as they are: the
-// query is split into two e4m3 parts, whose products with the codes are exact, and the
-// keys' scales go to the scores; and a row's softmax is two threads' work (4 x 64 rows
-// over 65536 keys: 130 us; with one thread a row 156, with converted keys 165). For 128
-// rows there is no second copy of the row's scores to share, and more rows hide the conversion.
+// own.
+//
+// Blocks of 64 rows or fewer (kNarrow) have the query's rows twice in a tile, on lanes
+// 0-63 and 64-127, and each stream works on a copy of its own: a row's softmax is two
+// threads' work, each with half of the columns, which stay in registers from the maximum
+// to the weights, and the two streams' warps are spread over all four schedulers. FP8
+// keys then go into the product as the codes that they are: the query is split into two
+// e4m3 parts, whose products with the codes are exact, and the keys' scales go to the
+// scores. 4 x 64 rows over 65536 FP8 keys: converted keys 165 us, codes 156, two threads
+// a row 130, scores in registers 111. (For more rows there is no lane left for a copy, and
+// the conversion is hidden as well: 161 us for 96 rows either way.)
+//
+// What bounds it: 4 x 512 rows over 16384 bf16 keys take 120 us, 55 of them tensor-core
+// time: a stream's chain of product, softmax and product, of some 3500 cycles a tile
+// against 2048 of products. 4 x 64 rows over 32768 bf16 keys, 89 us for 60 of bytes: five
+// tiles in shared memory are what is in flight. 64 FP8 rows, 111 us for 60 of bytes: the
+// softmax's chain, the conversion of the values and the copy warp's instructions, each
+// some 2000 of the 2400 cycles a tile.
 // Every wait is bounded; the first that runs out records TS_ERR_TIMEOUT and ends
 // the others.
 #include <algorithm>
@@ -46,7 +59,7 @@ constexpr int kMmaWarp = 12, kLoadWarp = 13;
 constexpr float kGrow = 8.f;             // log2: how far a row's maximum may grow over its reference
 constexpr uint32_t kTmemCols = 512;      // S of two streams, O of two streams
 
-// kNarrow: 64 rows or fewer of FP8.
+// kNarrow: 64 rows or fewer.
 template <int kType, int D, int NT, bool kNarrow>
 struct Plan {
     static constexpr int kTileBytes = kKeys * D * 2;              // a tile's keys or values as bf16
@@ -56,8 +69,8 @@ struct Plan {
     static constexpr int kRawBytes = kType == kKvFp8 ? kRawCodes + 256 : 0;  // and its rows' scales
     static constexpr int kExchange = kNarrow ? 2 * 64 * 36 * 4 : 0;  // 32 columns of 64 rows, twice, rows 36 floats apart
     static constexpr int kBudget = (NT == 1 ? 220 : 222) * 1024 - kQBytes - kExchange;  // beside the barriers and tables
-    // Narrow blocks' keys go into the products as they lie in the cache, so that only values are converted.
-    static constexpr bool kRawKeys = kNarrow;
+    // Narrow blocks' FP8 keys go into the products as they lie in the cache, so that only values are converted.
+    static constexpr bool kRawKeys = kNarrow && kType == kKvFp8;
     static constexpr int kKeyBytes = kRawKeys ? kKeys * D : kTileBytes;
     // Key tiles are needed two products ahead, value tiles (and, FP8, their codes) a little later. 256 FP8 rows have
     // room for three converted tiles: one of keys, which both products are through with early, and two of values
@@ -72,7 +85,7 @@ struct Plan {
 
 constexpr int kScaleSlots = 8;  // of the keys' scales: they are read until a tile's softmax is through, two units after its product
 
-template <int NT, bool kRawKeys>
+template <int NT, bool kRawKeys, bool kNarrow>
 struct Shared {
     // Each barrier has one role that waits on it, or waiters whose own arrivals its next phase needs: a
     // parity tells a phase from the next only, so that nobody may fall a phase behind.
@@ -90,7 +103,7 @@ struct Shared {
     alignas(16) uint8_t key_scale[kRawKeys ? kScaleSlots : 1][128];
     alignas(16) float factor[2][2][kRawKeys ? 128 : 4];      // of a stream's tile, by turns: its keys' scales times log2(e) scale
     float q_scale[2][kRawKeys ? 64 : 1];                     // of the query's rows, by items in turn
-    float top[2][2][2][kRawKeys ? 64 : 1];                   // of a stream's tile, by turns: each column half's maxima
+    float top[2][2][2][kNarrow ? 64 : 1];                   // of a stream's tile, by turns: each column half's maxima
     LineScratch line;
 };
 
@@ -229,7 +242,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     constexpr int kPieces = D / 8;
     extern __shared__ uint8_t smem_raw[];
     constexpr bool kRawKeys = P::kRawKeys;
-    __shared__ Shared<NT, kRawKeys> sh;
+    __shared__ Shared<NT, kRawKeys, kNarrow> sh;
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -290,7 +303,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         const int row_in = tid & (kNarrow ? 63 : 127);
         constexpr int kCols = kNarrow ? 64 : 128, kChunks = kCols / 32;  // a thread's columns
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lane_base + s * kKeys + half * 64, to = tmem + lane_base + 256 + s * 128 + half * 64;
+        const uint32_t ts = tmem + lane_base + s * kKeys + half * 64, to = tmem + lane_base + 256 + s * 128 + half * (D / 2);
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-38f);  // its sign went into the query; not 0, for masked scores' sake
         uint32_t s_phase = 0, o_phase = 0;
         int key_tile = 0, turn = 0;       // raw keys: tiles before this item's
@@ -322,8 +335,8 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     if (units == 0)
                         q_scale = sh.q_scale[item & 1][row_in];
                     named_sync(3 + s, kSoftThreads / 2);
-                    turn ^= 1;
                 }
+                turn ^= 1;
                 if (!idle) {
                     const int pos = (it_t0 + j) * kKeys;
                     const bool tail = pos + kKeys > seq.ctx;
@@ -368,13 +381,15 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         mc = to_mc;
                         l *= by;
                         if (units > 0) {  // before the first, the accumulator holds nothing
+                            uint32_t z[16];
 #pragma unroll 1
-                            for (int i = 0; i < (kNarrow ? 2 : D / 32); ++i) {
-                                tmem_ld32(to + 32 * i, x);
+                            for (int i = 0; i < (kNarrow ? D / 32 : D / 16); ++i) {
+                                tmem_ld16_async(to + 16 * i, z);
+                                tmem_wait_ld(z);
 #pragma unroll
-                                for (int c = 0; c < 32; ++c)
-                                    x[c] = __float_as_uint(__uint_as_float(x[c]) * by);
-                                tmem_st32_async(to + 32 * i, x);
+                                for (int c = 0; c < 16; ++c)
+                                    z[c] = __float_as_uint(__uint_as_float(z[c]) * by);
+                                tmem_st16_async(to + 16 * i, z);
                             }
                         }
                     }
@@ -393,30 +408,31 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         }
                         tmem_st16_async(ts + 16 * i, w);
                     };
-                    // P: the next load runs while this one's columns are worked on; each store goes over
-                    // columns that this row has read
-                    tmem_ld32_async(ts, x);
+                    if (kNarrow) {  // the registers still hold all of the thread's scores
+                        weigh(x, 0);
+                        weigh(y, 1);
+                    } else {
+                        // P: the next load runs while this one's columns are worked on; each store goes over
+                        // columns that this row has read
+                        tmem_ld32_async(ts, x);
 #pragma unroll 1
-                    for (int i = 0; i < kChunks; i += 2) {
-                        tmem_wait_ld32(x);
-                        tmem_ld32_async(ts + 32 * (i + 1), y);
-                        if (kRawKeys)
-                            scale_columns(x, factor + 32 * i);
-                        if (tail)
-                            hide(x, see(i));
-                        weigh(x, i);
-                        tmem_wait_ld32(y);
-                        if (i + 2 < kChunks)
-                            tmem_ld32_async(ts + 64, x);
-                        if (kRawKeys)
-                            scale_columns(y, factor + 32 * (i + 1));
-                        if (tail)
-                            hide(y, see(i + 1));
-                        weigh(y, i + 1);
-                        if (!kNarrow && i == 0) {  // the product can begin with the first 64 keys
-                            tmem_wait_st();
-                            tc_fence_before();
-                            mbar_arrive(&sh.p_half[s]);
+                        for (int i = 0; i < 4; i += 2) {
+                            tmem_wait_ld32(x);
+                            tmem_ld32_async(ts + 32 * (i + 1), y);
+                            if (tail)
+                                hide(x, see(i));
+                            weigh(x, i);
+                            tmem_wait_ld32(y);
+                            if (i == 0)
+                                tmem_ld32_async(ts + 64, x);
+                            if (tail)
+                                hide(y, see(i + 1));
+                            weigh(y, i + 1);
+                            if (i == 0) {  // the product can begin with the first 64 keys
+                                tmem_wait_st();
+                                tc_fence_before();
+                                mbar_arrive(&sh.p_half[s]);
+                            }
                         }
                     }
                     float a, z;
@@ -469,7 +485,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 const uint32_t o0 = tmem + lane_base + 256 + (NT == 2 ? s * 128 : 0), o1 = o0 + 128;
                 // NT = 1: each stream's threads write half of the columns; narrow, the second stream hands its
                 // part of the sums, which lies on other lanes, to the first, which writes
-                const int i0 = kNarrow ? 2 * half : NT == 1 ? s * (D / 64) : 0, i1 = NT == 1 ? i0 + D / 64 : D / 32;
+                const int i0 = kNarrow ? D / 64 * half : NT == 1 ? s * (D / 64) : 0, i1 = NT == 1 ? i0 + D / 64 : D / 32;
                 float *trade = reinterpret_cast<float *>(smem_raw + (base - smem_addr(smem_raw)) + P::kTrade) + (half * 64 + row_in) * 36;
 #pragma unroll 1
                 for (int i = i0; i < i1; ++i) {
@@ -614,6 +630,8 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             w = make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632), __byte_perm(w.z, w.w, 0x5410),
                                            __byte_perm(w.z, w.w, 0x7632));
                         sts128(tile_piece(base + P::kQ + (r >> 7) * P::kTileBytes, r & 127, x), w);
+                        if (kNarrow)  // and the copy
+                            sts128(tile_piece(base + P::kQ, r + 64, x), w);
                     }
                 }
                 fence_async_shared();
@@ -984,12 +1002,12 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
 
 constexpr int kLeastWide = 2;  // tiles a CTA has at least, where there is a choice
 
-template <int kType, int D, int NT, bool kNarrow = false>
+template <int kType, int D, int NT, bool kNarrow>
 cudaError_t launch_wide(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
 {
     using Pl = Plan<kType, D, NT, kNarrow>;
     auto *kernel = hc_attn_wide_kernel<kType, D, NT, kNarrow>;
-    static_assert(Pl::kTotal + sizeof(Shared<NT, Pl::kRawKeys>) <= 227 * 1024, "shared memory");
+    static_assert(Pl::kTotal + sizeof(Shared<NT, Pl::kRawKeys, kNarrow>) <= 227 * 1024, "shared memory");
     static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Pl::kTotal);
     if (set != cudaSuccess)
         return set;
@@ -1040,14 +1058,16 @@ int attn_wide_rows(const KvView &c, long rows)
 
 cudaError_t launch_attn_wide(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t stream)
 {
-    const bool two = attn_wide_rows(p.c, p.rows) == 256;
+    const bool narrow = p.rows <= 64, two = attn_wide_rows(p.c, p.rows) == 256;
     if (p.c.type == kKvBf16) {
         if (p.c.D == 64)
-            return two ? launch_wide<kKvBf16, 64, 2>(p, cfg, stream) : launch_wide<kKvBf16, 64, 1>(p, cfg, stream);
-        return two ? launch_wide<kKvBf16, 128, 2>(p, cfg, stream) : launch_wide<kKvBf16, 128, 1>(p, cfg, stream);
+            return two ? launch_wide<kKvBf16, 64, 2, false>(p, cfg, stream)
+                       : narrow ? launch_wide<kKvBf16, 64, 1, true>(p, cfg, stream) : launch_wide<kKvBf16, 64, 1, false>(p, cfg, stream);
+        return two ? launch_wide<kKvBf16, 128, 2, false>(p, cfg, stream)
+                   : narrow ? launch_wide<kKvBf16, 128, 1, true>(p, cfg, stream) : launch_wide<kKvBf16, 128, 1, false>(p, cfg, stream);
     }
-    return two ? launch_wide<kKvFp8, 128, 2>(p, cfg, stream)
-               : p.rows <= 64 ? launch_wide<kKvFp8, 128, 1, true>(p, cfg, stream) : launch_wide<kKvFp8, 128, 1>(p, cfg, stream);
+    return two ? launch_wide<kKvFp8, 128, 2, false>(p, cfg, stream)
+               : narrow ? launch_wide<kKvFp8, 128, 1, true>(p, cfg, stream) : launch_wide<kKvFp8, 128, 1, false>(p, cfg, stream);
 }
 
 }  // namespace tshc
