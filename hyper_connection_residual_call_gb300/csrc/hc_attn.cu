@@ -639,8 +639,8 @@ __global__ void __launch_bounds__(kAttnThreads, (Format<kType, D>::template bloc
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LineScratch scratch;
     __shared__ int wild_any;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // after the wait: the join reads the lengths before its own
     const int tid = threadIdx.x;
     const Line line(p, kTile, scratch);
     const int ctas = attn_ctas(line.total, gridDim.x, least);
@@ -908,8 +908,9 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 8 : 10) hc_attn_join_
     __shared__ float across[kWarpsARow > 1 ? kWarps : 1][D + 2];
     __shared__ LineScratch scratch;
     pdl_launch_dependents();
-    pdl_wait();
+    // the lengths only, which nothing changes from the attention kernel's start on
     const Segments of(p, rows, tile, grid, least, scratch);
+    pdl_wait();
     const int b = of.b, item = of.item, c0 = of.c0, c1 = of.c1;
     if (c0 == c1)
         return;
@@ -1036,8 +1037,9 @@ __global__ void __launch_bounds__(kAttnThreads, 8) hc_attn_join_wide_kernel(cons
     constexpr int kLoads = D / 64;  // pieces of a thread: a row has D / 4, 16 threads a row
     __shared__ LineScratch scratch;
     pdl_launch_dependents();
-    pdl_wait();
+    // the lengths only, which nothing changes from the attention kernel's start on
     const Segments of(p, rows, tile, grid, least, scratch);
+    pdl_wait();
     if (of.c0 == of.c1)
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

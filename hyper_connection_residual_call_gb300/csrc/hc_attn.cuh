@@ -31,7 +31,7 @@ __device__ __forceinline__ SeqLen attn_seq(const AttnParams &p, int b, int tile)
 {
     SeqLen s;
     const long cap = (long)p.c.max_pages << p.c.page_shift;
-    const int raw = __ldg(p.ctx_len + b);
+    const int raw = __ldcg(p.ctx_len + b);  // from L2: the join reads it before its wait
     s.ctx = (int)max(0l, min((long)raw, cap));
     const long keys = min((long)s.ctx + p.T, cap);
     s.bad = raw < 0 || (long)raw + p.T > cap;

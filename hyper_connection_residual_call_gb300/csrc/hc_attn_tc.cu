@@ -243,8 +243,8 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     extern __shared__ uint8_t smem_raw[];
     constexpr bool kRawKeys = P::kRawKeys;
     __shared__ Shared<NT, kRawKeys, kNarrow> sh;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // after the wait: the join reads the lengths before its own
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
 
