@@ -131,6 +131,20 @@ __device__ __forceinline__ uint32_t e4m3_hi_bf16x2(uint32_t w)
 
 __device__ __forceinline__ uint32_t e4m3_lo_bf16x2(uint32_t w) { return e4m3_hi_bf16x2(w << 8); }
 
+// Two rows' scale bytes -> their scales 2^(byte - 127), bf16x2 (255: NaN).
+__device__ __forceinline__ uint32_t fp8_scales_bf16x2(uint32_t bytes)
+{
+    const uint32_t e = __byte_perm(bytes, 0, 0x4140);
+    return e << 7 | ((e + 0x00010001u) >> 2 & 0x00400040u);
+}
+
+__device__ __forceinline__ uint32_t mul2_bf16(uint32_t a, uint32_t b)
+{
+    uint32_t y;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+
 // INT4 codes of an 8-code word at bits 4 i and 16 + 4 i -> 16 + q, bf16x2 (exact): the
 // code goes to mantissa bits 3-6 of 16.
 template <int i>
@@ -247,6 +261,7 @@ struct Walk {
     float sc;                 // |scale| * log2(e), not 0 (its sign went into the query)
     float o[MT][kCols][4];
     float m[MT][2], l[MT][2]; // the reference of each row's weights (times sc), their sum
+    float rounded[MT][2];     // bf16 weights: the sum of what the products take of them
 
     __device__ __forceinline__ Walk(const AttnParams &params) : p(params) {}
 
@@ -309,7 +324,7 @@ struct Walk {
                 for (int e = 0; e < 4; ++e)
                     o[i][j][e] = 0.f;
             m[i][0] = m[i][1] = -INFINITY;
-            l[i][0] = l[i][1] = 0.f;
+            l[i][0] = l[i][1] = rounded[i][0] = rounded[i][1] = 0.f;
         }
     }
 
@@ -524,6 +539,7 @@ struct Walk {
                     const float by = to == -INFINITY ? 1.f : ex2(m[i][h] - to);
                     m[i][h] = to;
                     l[i][h] *= by;
+                    rounded[i][h] *= by;
 #pragma unroll
                     for (int j = 0; j < kCols; ++j) {
                         o[i][j][2 * h] *= by;
@@ -531,13 +547,11 @@ struct Walk {
                     }
                 }
         }
-        float vs[2][2];
+        uint32_t vs[2];  // the scales of the values of keys 8n + 2c and 8n + 2c + 1, bf16x2
         if (kType == kKvFp8) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    vs[n][e] = fp8_scale(lds_u8(stage + 2 * F::kCodes + F::kScale + n * 8 + 2 * c + e));
+                vs[n] = fp8_scales_bf16x2(lds_u16(stage + 2 * F::kCodes + F::kScale + n * 8 + 2 * c));
         }
         uint32_t pa[MT][4];
 #pragma unroll
@@ -549,9 +563,16 @@ struct Walk {
                 for (int n = 0; n < 2; ++n) {
                     const float a = ex2(fmaf(x[i][n][2 * h], sc, -ref)), z = ex2(fmaf(x[i][n][2 * h + 1], sc, -ref));
                     l[i][h] += a + z;
-                    // P to 16 bits: its rounding (2^-8 in bf16) is independent from key to key and
-                    // averages out; the sum l is of the unrounded P
-                    pa[i][2 * n + h] = kHalf ? pack2_f16(a, z) : kType == kKvFp8 ? pack2_bf16(a * vs[n][0], z * vs[n][1]) : pack2_bf16(a, z);
+                    // P to 16 bits. In bf16 its rounding is as large as the result's own: dividing by the sum of
+                    // the rounded P (the logarithm is of the other) makes the weights sum to one, so that a row that
+                    // one key dominates gets that key's value.
+                    if (kHalf) {
+                        pa[i][2 * n + h] = pack2_f16(a, z);
+                    } else {
+                        const uint32_t w = pack2_bf16(a, z);
+                        rounded[i][h] += bf16_lo(w) + bf16_hi(w);
+                        pa[i][2 * n + h] = kType == kKvFp8 ? mul2_bf16(w, vs[n]) : w;
+                    }
                 }
             }
 
@@ -784,6 +805,17 @@ __global__ void __launch_bounds__(kAttnThreads, (Format<kType, D>::template bloc
                 float sum = w.l[i][h];
                 sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
                 sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                if (!W::kHalf) {
+                    float rounded = w.rounded[i][h];
+                    rounded += __shfl_xor_sync(0xFFFFFFFFu, rounded, 1);
+                    rounded += __shfl_xor_sync(0xFFFFFFFFu, rounded, 2);
+                    const float by = rounded == 0.f ? 1.f : sum / rounded;
+#pragma unroll
+                    for (int j = 0; j < W::kCols; ++j) {
+                        w.o[i][j][2 * h] *= by;
+                        w.o[i][j][2 * h + 1] *= by;
+                    }
+                }
                 const int r = i * 16 + h * 8 + w.g;
                 if (w.c == 0) {
                     merge_m[w.warp * kRows + r] = w.m[i][h];
