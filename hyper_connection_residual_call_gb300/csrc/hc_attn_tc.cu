@@ -32,14 +32,19 @@
 // e4m3 parts, whose products with the codes are exact, and the keys' scales go to the
 // scores. 4 x 64 rows over 65536 FP8 keys: converted keys 165 us, codes 156, two threads
 // a row 130, scores in registers 111. (For more rows there is no lane left for a copy, and
-// the conversion is hidden as well: 161 us for 96 rows either way.)
+// the conversion is hidden as well: some 160 us for 96 rows either way.)
 //
-// What bounds it: 4 x 512 rows over 16384 bf16 keys take 120 us, 55 of them tensor-core
+// As in hc_attn.cu, a row's sums are divided by the sum of the weights as they were
+// rounded, which costs some 2% (119.6 -> 123 us, 110 -> 112) and takes the results'
+// error against 64 bits from 1.3 times a plain fp32 form's to 1.15 (its mean).
+//
+// What bounds it: 4 x 512 rows over 16384 bf16 keys take 123 us, 55 of them tensor-core
 // time: a stream's chain of product, softmax and product, of some 3500 cycles a tile
-// against 2048 of products. 4 x 64 rows over 32768 bf16 keys, 89 us for 60 of bytes: five
-// tiles in shared memory are what is in flight. 64 FP8 rows, 111 us for 60 of bytes: the
+// against 2048 of products. 4 x 64 rows over 32768 bf16 keys, 88 us for 60 of bytes: five
+// tiles in shared memory are what is in flight. 64 FP8 rows, 112 us for 60 of bytes: the
 // softmax's chain, the conversion of the values and the copy warp's instructions, each
 // some 2000 of the 2400 cycles a tile.
+//
 // Every wait is bounded; the first that runs out records TS_ERR_TIMEOUT and ends
 // the others.
 #include <algorithm>
@@ -99,7 +104,7 @@ struct Shared {
     int dead;                            // a wait ran out
     int wild[4];                         // by item: a node's value held an infinity or a NaN
     uint32_t raw_valid[8];               // which 16-key chunks of a code slot lie in a page
-    float m[2][NT == 1 ? 128 : 1], l[2][NT == 1 ? 128 : 1];  // of the two streams
+    float m[2][NT == 1 ? 128 : 1], l[2][NT == 1 ? 128 : 1], lr[2][NT == 1 ? 128 : 1];  // of the two streams
     alignas(16) uint8_t key_scale[kRawKeys ? kScaleSlots : 1][128];
     alignas(16) float factor[2][2][kRawKeys ? 128 : 4];      // of a stream's tile, by turns: its keys' scales times log2(e) scale
     float q_scale[2][kRawKeys ? 64 : 1];                     // of the query's rows, by items in turn
@@ -224,6 +229,12 @@ __device__ __forceinline__ void scale_columns(uint32_t (&x)[32], const float *fa
     }
 }
 
+// sum += both halves of w.
+__device__ __forceinline__ void add_bf16x2(float &sum, uint32_t w)
+{
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.f32.bf16 %0, lo, %0;\n\tadd.f32.bf16 %0, hi, %0;\n\t}" : "+f"(sum) : "r"(w));
+}
+
 // Scores that a row does not see become -infinity.
 __device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t see)
 {
@@ -321,7 +332,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             const uint32_t *mask = attn_mask_row(p, it_b, t);
             // a warp of rows past the last has nothing to do (rows do not meet)
             const bool idle = !kNarrow && row0 + (NT == 2 ? s * 128 : 0) + (warp & 3) * 32 >= p.rows;
-            float m = -INFINITY, mc = 0.f, l = 0.f;  // the reference (raw units), the same times sc (0 for none), the sum
+            float m = -INFINITY, l = 0.f, lr = 0.f;  // the reference (in units of log2), the weights' sum, that of the rounded weights
             int units = 0;
             float q_scale = 1.f;
             for (int j = NT == 2 ? 0 : s; j < n; j += 3 - NT, ++units) {
@@ -372,14 +383,12 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         named_sync(5 + s, kSoftThreads / 2);
                         top = fmaxf(top, sh.top[s][turn][half ^ 1][row_in]);
                     }
-                    const bool grow = top * by_row > mc + kGrow || (m == -INFINITY && top > -INFINITY);
-                    if (__any_sync(0xFFFFFFFFu, grow)) {
-                        const float to_m = fmaxf(m, top);
-                        const float to_mc = to_m == -INFINITY ? 0.f : to_m * by_row;
-                        const float by = m == -INFINITY ? 0.f : ex2(mc - to_mc);
+                    top *= by_row;
+                    if (__any_sync(0xFFFFFFFFu, top > m + kGrow)) {  // also the first that is not -infinity
+                        const float to_m = fmaxf(m, top), by = ex2(m - (to_m == -INFINITY ? 0.f : to_m));
                         m = to_m;
-                        mc = to_mc;
                         l *= by;
+                        lr *= by;
                         if (units > 0) {  // before the first, the accumulator holds nothing
                             uint32_t z[16];
 #pragma unroll 1
@@ -393,8 +402,10 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             }
                         }
                     }
-                    const uint64_t sc2 = f32x2(by_row, by_row), off2 = f32x2(-mc, -mc);
+                    const float off = m == -INFINITY ? 0.f : -m;
+                    const uint64_t sc2 = f32x2(by_row, by_row), off2 = f32x2(off, off);
                     uint64_t sums[4] = {0, 0, 0, 0};
+                    float rounded[2] = {0.f, 0.f};
                     const auto weigh = [&](const uint32_t(&v)[32], int i) {
                         uint32_t w[16];
 #pragma unroll
@@ -405,6 +416,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             z = ex2(z);
                             sums[c & 3] = fadd2(sums[c & 3], f32x2(a, z));
                             w[c] = pack2_bf16(a, z);
+                            add_bf16x2(rounded[c & 1], w[c]);
                         }
                         tmem_st16_async(ts + 16 * i, w);
                     };
@@ -438,6 +450,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     float a, z;
                     f32x2_unpack(fadd2(fadd2(sums[0], sums[1]), fadd2(sums[2], sums[3])), a, z);
                     l += a + z;
+                    lr += rounded[0] + rounded[1];
                     tmem_wait_st();
                 } else {
                     mbar_arrive(&sh.p_half[s]);
@@ -453,12 +466,15 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             // results: with NT = 1 both streams hold sums of every row
             if (NT == 1) {
                 if (half == 0)
-                    sh.m[s][row_in] = m == -INFINITY ? -INFINITY : mc;
+                    sh.m[s][row_in] = m;
                 sh.l[s][half * 64 + row_in] = l;
+                sh.lr[s][half * 64 + row_in] = lr;
                 named_sync(2, kSoftThreads);
             }
             if (!idle) {
-                float w0 = 1.f, w1 = 0.f, sum = l, top = m == -INFINITY ? -INFINITY : mc;
+                // the weights' sum over the rounded weights' makes up for the rounding (as in hc_attn.cu)
+                const auto made_up = [](float sum, float rounded) { return rounded == 0.f ? 1.f : sum / rounded; };
+                float w0 = 1.f, w1 = 0.f, sum = l, top = m;
                 bool two = false;
                 if (NT == 1) {
                     const float a = sh.m[0][row_in], z = sh.m[1][row_in];
@@ -467,12 +483,18 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     w0 = ex2(a - ref);
                     w1 = ex2(z - ref);
                     two = n > 1;  // the odd tiles' accumulator holds something
-                    float l0 = sh.l[0][row_in], l1 = sh.l[1][row_in];
+                    float l0 = sh.l[0][row_in], l1 = sh.l[1][row_in], r0 = sh.lr[0][row_in], r1 = sh.lr[1][row_in];
                     if (kNarrow) {
                         l0 += sh.l[0][64 + row_in];
                         l1 += sh.l[1][64 + row_in];
+                        r0 += sh.lr[0][64 + row_in];
+                        r1 += sh.lr[1][64 + row_in];
                     }
                     sum = w0 * l0 + (two ? w1 * l1 : 0.f);
+                    w0 *= made_up(l0, r0);
+                    w1 *= made_up(l1, r1);
+                } else {
+                    w0 = made_up(l, lr);
                 }
                 const bool whole = it_t0 == 0 && it_t1 == seq.tiles;
                 const float scale = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
@@ -521,6 +543,10 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
                                 x[c] = __float_as_uint(w0 * __uint_as_float(x[c]) + w1 * __uint_as_float(y[c]));
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                x[c] = __float_as_uint(w0 * __uint_as_float(x[c]));
                         }
                     }
                     if (!valid)
