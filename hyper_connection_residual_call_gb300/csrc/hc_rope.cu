@@ -6,7 +6,9 @@
 //
 // The operator does 3 flops an element and is bound by its bytes: each head's
 // row once in and once out, and the token's table row (rot * 4 bytes against
-// heads * D * 4).
+// heads * D * 4). 16384 tokens x 40 heads x 128, half of each turned: 55 us for 0.34 GB,
+// 0.91 of the measured copy rate. 4099 tokens x 18 heads x 64: 8.5 us for 20 MB, and one
+// token 4 us: a launch, and a chain of two dependent loads.
 #include <cuda_bf16.h>
 
 #include <algorithm>
