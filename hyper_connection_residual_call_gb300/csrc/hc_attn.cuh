@@ -247,6 +247,28 @@ __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi)
     return reinterpret_cast<const uint32_t &>(v);
 }
 
+// INT4 codes of an 8-code word at bits 4 i and 16 + 4 i -> 16 + q, bf16x2 (exact): the
+// code goes to mantissa bits 3-6 of 16.
+template <int i>
+__device__ __forceinline__ uint32_t int4_bf16x2(uint32_t w)
+{
+    constexpr int kShift = 3 - 4 * i;
+    const uint32_t at = kShift > 0 ? w << (kShift > 0 ? kShift : 0) : w >> (kShift > 0 ? 0 : -kShift);
+    return (at & 0x00780078u) | 0x41804180u;
+}
+
+// INT4 codes in bits 0-3 (kHigh: 4-7) of the two halves of w -> q * scale + bias, fp16x2.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t int4_f16x2(uint32_t w, __half2 scale, __half2 bias)
+{
+    const uint32_t bits = (w & (kHigh ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;  // 1024 + q, or 1024 + 16 q
+    const __half2 at = reinterpret_cast<const __half2 &>(bits);
+    const __half2 q = kHigh ? __hfma2(at, __half2half2(__ushort_as_half(0x2C00)), __half2half2(__ushort_as_half(0xD400)))  // / 16 - 64, exact
+                            : __hsub2(at, __half2half2(__ushort_as_half(0x6400)));
+    const __half2 v = __hfma2(q, scale, bias);
+    return reinterpret_cast<const uint32_t &>(v);
+}
+
 // The wide kernel's rows of a block (0: the few-row kernel serves) and its launcher.
 int attn_wide_rows(const KvView &c, long rows);
 cudaError_t launch_attn_wide(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t stream);

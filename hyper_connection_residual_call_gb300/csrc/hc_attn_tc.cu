@@ -70,22 +70,26 @@ struct Plan {
     static constexpr int kTileBytes = kKeys * D * 2;              // a tile's keys or values as bf16
     static constexpr int kHalf = kKeys * 128;                     // 64 columns of it
     static constexpr int kQBytes = NT * kTileBytes;
-    static constexpr int kRawCodes = kKeys * D;                   // FP8
-    static constexpr int kRawBytes = kType == kKvFp8 ? kRawCodes + 256 : 0;  // and its rows' scales
+    static constexpr bool kCoded = kType != kKvBf16;
+    static constexpr int kRawRow = kType == kKvFp8 ? D : D / 2;   // bytes of a row's codes
+    static constexpr int kRawCodes = kKeys * kRawRow;             // a tile's, with its rows' scales (INT4: scales, then biases)
+    static constexpr int kRawScales = kType == kKvFp8 ? 256 : kKeys * (D / 32) * 2;
+    static constexpr int kRawBytes = !kCoded ? 0 : kType == kKvFp8 ? kRawCodes + kRawScales : kRawCodes + 2 * kRawScales;
     static constexpr int kExchange = kNarrow ? 2 * 64 * 36 * 4 : 0;  // 32 columns of 64 rows, twice, rows 36 floats apart
     static constexpr int kBudget = (NT == 1 ? 220 : 222) * 1024 - kQBytes - kExchange;  // beside the barriers and tables
     // Narrow blocks' FP8 keys go into the products as they lie in the cache, so that only values are converted.
     static constexpr bool kRawKeys = kNarrow && kType == kKvFp8;
-    static constexpr int kKeyBytes = kRawKeys ? kKeys * D : kTileBytes;
+    // An INT4 key's value is kept as the sum of two bf16 tiles (16 bits of significand), one behind the other.
+    static constexpr int kKeyBytes = kRawKeys ? kKeys * D : kType == kKvInt4 ? 2 * kTileBytes : kTileBytes;
     // Key tiles are needed two products ahead, value tiles (and, FP8, their codes) a little later. 256 FP8 rows have
     // room for three converted tiles: one of keys, which both products are through with early, and two of values
     // (4 x 512 rows over 16384 keys: 139 us; two of keys and one of values 156).
-    static constexpr int kKeySlots = kRawKeys ? 3 : D == 64 ? 4 : kType == kKvFp8 && NT == 2 ? 1 : 2;
-    static constexpr int kSlots = kType == kKvFp8 ? 2 : std::min(8, (kBudget - kKeySlots * kKeyBytes) / kTileBytes);
-    static constexpr int kRaw = kType == kKvFp8 ? std::min(8, (kBudget - kSlots * kTileBytes - kKeySlots * kKeyBytes) / kRawBytes) : 1;
+    static constexpr int kKeySlots = kRawKeys ? 3 : D == 64 ? 4 : kType == kKvInt4 || (kType == kKvFp8 && NT == 2) ? 1 : 2;
+    static constexpr int kSlots = kCoded ? 2 : std::min(8, (kBudget - kKeySlots * kKeyBytes) / kTileBytes);
+    static constexpr int kRaw = kCoded ? std::min(8, (kBudget - kSlots * kTileBytes - kKeySlots * kKeyBytes) / kRawBytes) : 1;
     static constexpr int kQ = kSlots * kTileBytes, kKeyRing = kQ + kQBytes, kRing = kKeyRing + kKeySlots * kKeyBytes;
     static constexpr int kTrade = kRing + kRaw * kRawBytes, kTotal = kTrade + kExchange + 1024;  // and alignment
-    static_assert(kType != kKvFp8 || kRaw >= 2, "codes of a tile's keys and values");
+    static_assert(!kCoded || kRaw >= 2, "codes of a tile's keys and values");
 };
 
 constexpr int kScaleSlots = 8;  // of the keys' scales: they are read until a tile's softmax is through, two units after its product
@@ -142,12 +146,13 @@ __device__ __forceinline__ bool wait_or_dead(uint64_t *bar, uint32_t parity, S &
 
 __device__ __forceinline__ void named_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-// FP8: the conversion leaves elements (0, 2, 1, 3) of each four. The query takes the same
-// order against converted keys, and the results are put back when they are written.
+// The conversion of FP8 leaves elements (0, 2, 1, 3) of each four, that of INT4
+// (0, 4, 1, 5, 2, 6, 3, 7) of each eight. The query takes the same order against converted
+// keys, and the results are put back when they are written.
 template <int kType>
 __device__ __forceinline__ constexpr int column_of(int d)
 {
-    return kType == kKvFp8 ? (d & ~3) | ((d & 1) << 1) | ((d >> 1) & 1) : d;
+    return kType == kKvFp8 ? (d & ~3) | ((d & 1) << 1) | ((d >> 1) & 1) : kType == kKvInt4 ? (d & ~7) | ((d & 3) << 1) | ((d >> 2) & 1) : d;
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
@@ -230,9 +235,13 @@ __device__ __forceinline__ void scale_columns(uint32_t (&x)[32], const float *fa
 }
 
 // sum += both halves of w.
-__device__ __forceinline__ void add_bf16x2(float &sum, uint32_t w)
+template <bool kHalf>
+__device__ __forceinline__ void add_pair(float &sum, uint32_t w)
 {
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.f32.bf16 %0, lo, %0;\n\tadd.f32.bf16 %0, hi, %0;\n\t}" : "+f"(sum) : "r"(w));
+    if (kHalf)
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.f32.f16 %0, lo, %0;\n\tadd.f32.f16 %0, hi, %0;\n\t}" : "+f"(sum) : "r"(w));
+    else
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.f32.bf16 %0, lo, %0;\n\tadd.f32.bf16 %0, hi, %0;\n\t}" : "+f"(sum) : "r"(w));
 }
 
 // Scores that a row does not see become -infinity.
@@ -252,7 +261,8 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     constexpr int kRows = 128 * NT;
     constexpr int kPieces = D / 8;
     extern __shared__ uint8_t smem_raw[];
-    constexpr bool kRawKeys = P::kRawKeys;
+    constexpr bool kRawKeys = P::kRawKeys, kCoded = P::kCoded;
+    constexpr bool kHalf = kType == kKvInt4;  // weights and values in fp16, which holds an INT4 value's 11 bits
     __shared__ Shared<NT, kRawKeys, kNarrow> sh;
     pdl_wait();
     pdl_launch_dependents();  // after the wait: the join reads the lengths before its own
@@ -415,8 +425,8 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             a = ex2(a);
                             z = ex2(z);
                             sums[c & 3] = fadd2(sums[c & 3], f32x2(a, z));
-                            w[c] = pack2_bf16(a, z);
-                            add_bf16x2(rounded[c & 1], w[c]);
+                            w[c] = kHalf ? pack2_f16(a, z) : pack2_bf16(a, z);
+                            add_pair<kHalf>(rounded[c & 1], w[c]);
                         }
                         tmem_st16_async(ts + 16 * i, w);
                     };
@@ -652,7 +662,10 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                                 sh.q_scale[item & 1][r] = scale;
                             continue;
                         }
-                        if (kType == kKvFp8)  // the converted keys' columns are permuted
+                        if (kType == kKvInt4)  // the converted keys' columns are permuted
+                            w = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632), __byte_perm(w.y, w.w, 0x5410),
+                                           __byte_perm(w.y, w.w, 0x7632));
+                        if (kType == kKvFp8)
                             w = make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632), __byte_perm(w.z, w.w, 0x5410),
                                            __byte_perm(w.z, w.w, 0x7632));
                         sts128(tile_piece(base + P::kQ + (r >> 7) * P::kTileBytes, r & 127, x), w);
@@ -685,7 +698,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     wait_or_dead(value ? &sh.empty[slot] : &sh.k_empty[slot], (use & 1) ^ 1, sh, status);
                 }
                 const uint32_t tile = base + (value ? slot * P::kTileBytes : P::kKeyRing + slot * P::kKeyBytes);
-                const int rs = kType == kKvFp8 ? raw % P::kRaw : 0;
+                const int rs = kCoded ? raw % P::kRaw : 0;
                 bool wild = false;
                 if (kType == kKvFp8) {
                     wait_or_dead(&sh.raw_full[rs], (raw / P::kRaw) & 1, sh, status);
@@ -759,6 +772,55 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             }
                         }
                     }
+                } else if (kType == kKvInt4) {
+                    wait_or_dead(&sh.raw_full[rs], (raw / P::kRaw) & 1, sh, status);
+                    const uint32_t valid = *reinterpret_cast<volatile uint32_t *>(&sh.raw_valid[rs]);
+                    const uint8_t *src = smem_raw + (base + P::kRing + rs * P::kRawBytes - smem_addr(smem_raw));
+                    // A thread has 32 columns of a row, which lie in one group: four pieces, each from one word.
+                    constexpr int kUnits = D / 32, kStep = kConvThreads / kUnits;
+                    static_assert(kStep % 8 == 0, "the permutation of a row's pieces");
+                    const int r0 = ct / kUnits, x = ct % kUnits, groups = D / p.c.group, grp = x * 32 / p.c.group;
+                    const bool swap = x >> 1;  // half of the lanes store their pieces in another order: no bank twice
+#pragma unroll 1
+                    for (int r = r0; r < kKeys; r += kStep) {
+                        uint4 in = *reinterpret_cast<const uint4 *>(src + r * P::kRawRow + x * 16);
+                        const uint16_t *scales = reinterpret_cast<const uint16_t *>(src + P::kRawCodes) + r * groups + grp;
+                        uint32_t sb = scales[0], bb = scales[P::kRawScales / 2];
+                        bool use_it = (valid >> (r >> 4)) & 1u;
+                        if (tail && pos + r >= seq.ctx) {
+                            if (pos + r >= seq.keys) {
+                                use_it = false;
+                            } else if ((sb & 0x7C00u) == 0x7C00u || (bb & 0x7C00u) == 0x7C00u) {
+                                wild |= use_it;
+                                use_it = false;
+                            }
+                        }
+                        if (!use_it)
+                            sb = bb = 0;
+                        const __half hs = __ushort_as_half((unsigned short)sb), hb = __ushort_as_half((unsigned short)bb);
+                        const float fs = __half2float(hs), fb = fmaf(-16.f, fs, __half2float(hb));
+                        const __half2 s2 = __half2half2(hs), b2 = __half2half2(hb);
+                        const uint32_t words[4] = {swap ? in.z : in.x, swap ? in.w : in.y, swap ? in.x : in.z, swap ? in.y : in.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t at = tile_piece(tile, r, 4 * x + (j ^ (swap ? 2 : 0))), w = words[j];
+                            if (value) {
+                                sts128(at, make_uint4(int4_f16x2<false>(w, s2, b2), int4_f16x2<true>(w, s2, b2), int4_f16x2<false>(w >> 8, s2, b2),
+                                                      int4_f16x2<true>(w >> 8, s2, b2)));
+                            } else {
+                                const uint32_t q[4] = {int4_bf16x2<0>(w), int4_bf16x2<1>(w), int4_bf16x2<2>(w), int4_bf16x2<3>(w)};
+                                uint32_t hi[4], lo[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float a = fmaf(bf16_lo(q[i]), fs, fb), z = fmaf(bf16_hi(q[i]), fs, fb);
+                                    hi[i] = pack2_bf16(a, z);
+                                    lo[i] = pack2_bf16(a - bf16_lo(hi[i]), z - bf16_hi(hi[i]));
+                                }
+                                sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                                sts128(at + P::kTileBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                            }
+                        }
+                    }
                 } else {  // bf16 values that reach past the context
 #pragma unroll 4
                     for (int u = ct; u < kKeys * kPieces; u += kConvThreads) {
@@ -788,7 +850,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 named_sync(1, kConvThreads);
                 if (ct == 0) {
                     mbar_arrive(value ? &sh.full[slot] : &sh.k_full[slot]);
-                    if (kType == kKvFp8)
+                    if (kCoded)
                         mbar_arrive(&sh.raw_empty[rs]);
                 }
                 ++raw;
@@ -797,7 +859,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- products
-        constexpr uint32_t kIdescS = kRawKeys ? umma_idesc_e4m3(128, kKeys) : umma_idesc_bf16(128, kKeys), kIdescO = umma_idesc_bf16(128, D) | kIdescBMnMajor;
+        constexpr uint32_t kIdescS = kRawKeys ? umma_idesc_e4m3(128, kKeys) : umma_idesc_bf16(128, kKeys), kIdescO = (kHalf ? umma_idesc_f16(128, D) : umma_idesc_bf16(128, D)) | kIdescBMnMajor;
         int index = 0;
         uint32_t q_phase = 0, p_phase[2] = {0, 0};
         bool ok = true;
@@ -822,10 +884,12 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             umma_e4m3_lo(tmem + s * kKeys, q + ((i >> 2) * kKeys * 128 + (i & 3) * 32) / 16, k + (i & 3) * 2, kIdescS, i > 0);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            const uint32_t at = ((i >> 2) * P::kHalf + (i & 3) * 32) >> 4;
-                            umma_bf16_lo(tmem + s * kKeys, q + at, k + at, kIdescS, i > 0);
-                        }
+                        for (int part = 0; part < P::kKeyBytes / P::kTileBytes; ++part)  // INT4: two parts of a key
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                const uint32_t at = ((i >> 2) * P::kHalf + (i & 3) * 32) >> 4;
+                                umma_bf16_lo(tmem + s * kKeys, q + at, k + part * (P::kTileBytes >> 4) + at, kIdescS, part + i > 0);
+                            }
                     }
                     umma_commit(&sh.s_ready[s]);
                     if (NT == 1 || s == 1)
@@ -899,7 +963,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         // One pass a tile, keys and values together: the warp's own instructions were what bound a stream of
         // tiles (1400 cycles for each of the two, of some 130 instructions in turn). Lane 8 i + c copies chunk c:
         //   bf16: the two 64-column halves of the keys (i = 0, 1) and of the values (2, 3);
-        //   FP8:  the keys' codes (0) and scales (1), the values' codes (2) and scales (3).
+        //   FP8, INT4: the keys' codes (0) and scales (1; INT4: and biases), the values' codes (2) and scales (3).
         const int part = lane >> 3, c = lane & 7;
         const bool value = part >= 2, chunk = c < chunks;
         uint8_t *const tiles = smem_raw + (base - smem_addr(smem_raw));
@@ -970,17 +1034,23 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         const int rs = raw % P::kRaw;
                         if (!wait_or_dead(&sh.raw_empty[rs], ((raw / P::kRaw) & 1) ^ 1, sh, status))
                             return false;
+                        const int groups = kType == kKvInt4 ? D / p.c.group : 0, of_row = kType == kKvFp8 ? 1 : 2 * groups;  // a row's scales, bytes
                         if (lane == 0) {
                             *reinterpret_cast<volatile uint32_t *>(&sh.raw_valid[rs]) = bits;
-                            mbar_arrive_expect_tx(&sh.raw_full[rs], bytes * (D + 1));
+                            mbar_arrive_expect_tx(&sh.raw_full[rs], bytes * (P::kRawRow + (kType == kKvInt4 ? 2 : 1) * of_row));
                         }
                         __syncwarp();
                         if (value == values && there) {
                             uint8_t *codes = tiles + P::kRing + rs * P::kRawBytes;
-                            const uint8_t *from = values ? p.c.v : p.c.k, *scales = values ? p.c.vs : p.c.ks;
-                            const bool code = !(part & 1);
-                            bulk_copy_g2s(code ? codes + c * per_page * D : codes + P::kRawCodes + c * per_page, code ? from + row * D : scales + row,
-                                          code ? per_page * D : per_page, &sh.raw_full[rs]);
+                            const uint8_t *from = values ? p.c.v : p.c.k, *scales = values ? p.c.vs : p.c.ks, *biases = values ? p.c.vb : p.c.kb;
+                            if (!(part & 1)) {
+                                bulk_copy_g2s(codes + c * per_page * P::kRawRow, from + row * P::kRawRow, per_page * P::kRawRow, &sh.raw_full[rs]);
+                            } else {
+                                uint8_t *to = codes + P::kRawCodes + c * per_page * of_row;
+                                bulk_copy_g2s(to, scales + row * of_row, per_page * of_row, &sh.raw_full[rs]);
+                                if (kType == kKvInt4)
+                                    bulk_copy_g2s(to + P::kRawScales, biases + row * of_row, per_page * of_row, &sh.raw_full[rs]);
+                            }
                         }
                         __syncwarp();
                         return true;
@@ -1075,7 +1145,7 @@ cudaError_t launch_wide(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
 // value does not fit a bf16); fewer rows in the pool than a tensor map's coordinates reach.
 int attn_wide_rows(const KvView &c, long rows)
 {
-    if (rows <= 32 || !(c.type == kKvBf16 ? c.D <= 128 : c.type == kKvFp8 && c.D == 128))
+    if (rows <= (c.type == kKvInt4 ? 64 : 32) || !(c.type == kKvBf16 ? c.D <= 128 : c.D == 128))
         return 0;
     if (((c.n_pages * c.heads) << c.page_shift) >= (1l << 31) - kKeys)
         return 0;
@@ -1092,6 +1162,8 @@ cudaError_t launch_attn_wide(const AttnParams &p, const LaunchCfg &cfg, cudaStre
         return two ? launch_wide<kKvBf16, 128, 2, false>(p, cfg, stream)
                    : narrow ? launch_wide<kKvBf16, 128, 1, true>(p, cfg, stream) : launch_wide<kKvBf16, 128, 1, false>(p, cfg, stream);
     }
+    if (p.c.type == kKvInt4)
+        return two ? launch_wide<kKvInt4, 128, 2, false>(p, cfg, stream) : launch_wide<kKvInt4, 128, 1, false>(p, cfg, stream);
     return two ? launch_wide<kKvFp8, 128, 2, false>(p, cfg, stream)
                : narrow ? launch_wide<kKvFp8, 128, 1, true>(p, cfg, stream) : launch_wide<kKvFp8, 128, 1, false>(p, cfg, stream);
 }

@@ -49,6 +49,9 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N)
          | ((uint32_t)(M >> 4) << 24);      // M / 16
 }
 
+// The same with fp16 A and B.
+__host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) { return umma_idesc_bf16(M, N) & ~(1u << 7 | 1u << 10); }
+
 // Descriptors of an MN-major tile, 128-byte swizzle: rows of K hold 64 elements
 // (128 bytes) of M or N, 8 rows an atom (1024 bytes), atoms along K 1024 bytes
 // apart (the stride byte offset); the next 64 elements of M or N lie the leading

@@ -626,6 +626,44 @@ def test_attention_wide_blocks_many_times(kind, hq):
     assert B.device_status() == B.TS_OK
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("hq,hk,t", [(3, 1, 11), (4, 1, 16), (8, 1, 12), (16, 1, 8), (43, 1, 3), (8, 2, 64)])
+def test_attention_wide_blocks_int4(group, hq, hk, t):
+    """A key as two bf16 parts is off by at most 2^-18 of itself, 64 u32, which the bound's D u32 for a sum in
+    fp32 (of some ten steps) covers."""
+    run_attention(26, "int4", group, 128, hq, hk, 16, [0, 1, 127, 128, 129, 300, 1025, 2600], t, [random_tree(np.random.default_rng(t), t)] * 8)
+
+
+@pytest.mark.parametrize("hq", [4, 8, 16])
+def test_attention_wide_blocks_int4_unseen_and_many_times(hq):
+    """Unseen bad nodes change nothing; rows past the end neither; 100 runs have the same bits and no wait runs out."""
+    g = gen(27)
+    t, d = 12, 128
+    lens = torch.tensor([1500, 150, 0], dtype=torch.int32, device="cuda")
+    zero = torch.zeros_like(lens)
+    cache = make_cache(g, "int4", 3, 1600, 1, 32, d, 32)
+    k, v = randn(g, 3, 1530, 1, d), randn(g, 3, 1530, 1, d)
+    see = R.sees(TREE)
+    mask = R.words(see)[None].expand(3, -1, -1).contiguous().cuda()
+    q = randn(g, 3, t, hq, d)
+    B.hc_kv_write(k, v, cache, zero)
+    out, lse = B.hc_tree_attention(q, cache, lens, mask=mask)
+    assert bool(torch.isfinite(out).all())
+    for i, n in enumerate(lens.tolist()):
+        k[i, n + 4, 0, 5], v[i, n + 5, 0, 7] = float("nan"), float("nan")
+        k[i, n + t:], v[i, n + t:] = float("nan"), float("nan")
+    B.hc_kv_write(k, v, cache, zero)
+    clean = torch.from_numpy(~(see[:, 4] | see[:, 5])).cuda()
+    saw = torch.from_numpy(see[:, 5]).cuda()
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(100):
+        out2, lse2 = B.hc_tree_attention(q, cache, lens, mask=mask)
+        differ += (out2[:, clean] != out[:, clean]).sum() + (lse2[:, clean] != lse[:, clean]).sum()
+    assert int(differ) == 0
+    assert not bool(torch.isfinite(out2[:, saw][..., 7]).any())
+    assert B.device_status() == B.TS_OK
+
+
 def test_attention_pages_past_2_to_31_elements():
     """A pool of more than 2^31 elements, the sequence at its end."""
     d, heads, page = 128, 8, 64
