@@ -20,9 +20,9 @@
 // Roles: warps 0-7 softmax, four a stream; warps 8-11, 14 and 15 put
 // what has to be converted into shared memory (the query; FP8 tiles; the values of
 // a tile that reaches past the context, where what lies behind the last key, and
-// infinities and NaNs of nodes, are taken out); warp 12 issues the products, warp 13
-// the copies: TMA boxes for bf16 tiles, bulk copies of FP8 codes to a ring of their
-// own.
+// infinities and NaNs of nodes, are taken out; INT4 tiles: a key as the sum of two bf16, a
+// value in fp16); warp 12 issues the products, warp 13 the copies: TMA boxes for bf16
+// tiles, bulk copies of codes to a ring of their own.
 //
 // Blocks of 64 rows or fewer (kNarrow) have the query's rows twice in a tile, on lanes
 // 0-63 and 64-127, and each stream works on a copy of its own: a row's softmax is two
@@ -78,7 +78,7 @@ struct Plan {
     static constexpr int kExchange = kNarrow ? 2 * 64 * 36 * 4 : 0;  // 32 columns of 64 rows, twice, rows 36 floats apart
     static constexpr int kBudget = (NT == 1 ? 220 : 222) * 1024 - kQBytes - kExchange;  // beside the barriers and tables
     // Narrow blocks' FP8 keys go into the products as they lie in the cache, so that only values are converted.
-    static constexpr bool kRawKeys = kNarrow && kType == kKvFp8;
+    static constexpr bool kRawKeys = kNarrow && kType == kKvFp8 && D == 128;  // a row is one 128-byte line of an operand
     // An INT4 key's value is kept as the sum of two bf16 tiles (16 bits of significand), one behind the other.
     static constexpr int kKeyBytes = kRawKeys ? kKeys * D : kType == kKvInt4 ? 2 * kTileBytes : kTileBytes;
     // Key tiles are needed two products ahead, value tiles (and, FP8, their codes) a little later. 256 FP8 rows have
@@ -1137,15 +1137,33 @@ cudaError_t launch_wide(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
     return launch_attn_join(p, 128 * NT, kKeys, grid, kLeastWide, true, stream);
 }
 
+template <int D>
+cudaError_t launch_rows(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t stream)
+{
+    const bool narrow = p.rows <= 64, two = attn_wide_rows(p.c, p.rows) == 256;
+    switch (p.c.type) {
+    case kKvBf16:
+        return two ? launch_wide<kKvBf16, D, 2, false>(p, cfg, stream)
+               : narrow ? launch_wide<kKvBf16, D, 1, true>(p, cfg, stream) : launch_wide<kKvBf16, D, 1, false>(p, cfg, stream);
+    case kKvFp8:
+        return two ? launch_wide<kKvFp8, D, 2, false>(p, cfg, stream)
+               : narrow ? launch_wide<kKvFp8, D, 1, true>(p, cfg, stream) : launch_wide<kKvFp8, D, 1, false>(p, cfg, stream);
+    default: return two ? launch_wide<kKvInt4, D, 2, false>(p, cfg, stream) : launch_wide<kKvInt4, D, 1, false>(p, cfg, stream);
+    }
+}
+
 }  // namespace
 
-// Rows of a block of the wide kernel, or 0 where it does not serve: more than 32
-// rows; bf16 rows of 64 or 128 elements (two accumulators and two score tiles fill
-// TMEM), FP8 rows of 128 (a row is one 128-byte line of an operand; an INT4 key's exact
-// value does not fit a bf16); fewer rows in the pool than a tensor map's coordinates reach.
+// Rows of a block of the wide kernel, or 0 where it does not serve: rows of 64 or 128
+// elements (two accumulators and two score tiles fill TMEM); fewer rows in the pool than a
+// tensor map's coordinates reach; more than 32 rows, of INT4, whose keys are converted to
+// two tiles, more than 64. us in blocks of 32 rows and here, over long contexts: 64 rows of
+// FP8 x 64 95 and 70, of INT4 x 128 132 and 142, 96 of INT4 x 128 186 and 147, 100 of
+// INT4 x 64 174 and 108. Over some hundred keys this kernel's longer start costs 2 to 6 us
+// (40 rows over 800 keys: 18.4 and 20.4); the host does not know the lengths.
 int attn_wide_rows(const KvView &c, long rows)
 {
-    if (rows <= (c.type == kKvInt4 ? 64 : 32) || !(c.type == kKvBf16 ? c.D <= 128 : c.D == 128))
+    if (rows <= (c.type == kKvInt4 ? 64 : 32) || c.D > 128)
         return 0;
     if (((c.n_pages * c.heads) << c.page_shift) >= (1l << 31) - kKeys)
         return 0;
@@ -1154,18 +1172,7 @@ int attn_wide_rows(const KvView &c, long rows)
 
 cudaError_t launch_attn_wide(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t stream)
 {
-    const bool narrow = p.rows <= 64, two = attn_wide_rows(p.c, p.rows) == 256;
-    if (p.c.type == kKvBf16) {
-        if (p.c.D == 64)
-            return two ? launch_wide<kKvBf16, 64, 2, false>(p, cfg, stream)
-                       : narrow ? launch_wide<kKvBf16, 64, 1, true>(p, cfg, stream) : launch_wide<kKvBf16, 64, 1, false>(p, cfg, stream);
-        return two ? launch_wide<kKvBf16, 128, 2, false>(p, cfg, stream)
-                   : narrow ? launch_wide<kKvBf16, 128, 1, true>(p, cfg, stream) : launch_wide<kKvBf16, 128, 1, false>(p, cfg, stream);
-    }
-    if (p.c.type == kKvInt4)
-        return two ? launch_wide<kKvInt4, 128, 2, false>(p, cfg, stream) : launch_wide<kKvInt4, 128, 1, false>(p, cfg, stream);
-    return two ? launch_wide<kKvFp8, 128, 2, false>(p, cfg, stream)
-               : narrow ? launch_wide<kKvFp8, 128, 1, true>(p, cfg, stream) : launch_wide<kKvFp8, 128, 1, false>(p, cfg, stream);
+    return p.c.D == 64 ? launch_rows<64>(p, cfg, stream) : launch_rows<128>(p, cfg, stream);
 }
 
 }  // namespace tshc

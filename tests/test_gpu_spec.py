@@ -634,6 +634,13 @@ def test_attention_wide_blocks_int4(group, hq, hk, t):
     run_attention(26, "int4", group, 128, hq, hk, 16, [0, 1, 127, 128, 129, 300, 1025, 2600], t, [random_tree(np.random.default_rng(t), t)] * 8)
 
 
+@pytest.mark.parametrize("kind,group", [("bf16", 0), ("fp8", 0), ("int4", 32), ("int4", 64)])
+@pytest.mark.parametrize("hq,t", [(4, 9), (8, 9), (8, 17), (12, 30)])
+def test_attention_wide_blocks_of_64(kind, group, hq, t):
+    """36 to 360 rows of 64 elements."""
+    run_attention(28, kind, group, 64, hq, 1, 32, [0, 1, 127, 128, 129, 300, 1025, 2600], t, [random_tree(np.random.default_rng(t), t)] * 8)
+
+
 @pytest.mark.parametrize("hq", [4, 8, 16])
 def test_attention_wide_blocks_int4_unseen_and_many_times(hq):
     """Unseen bad nodes change nothing; rows past the end neither; 100 runs have the same bits and no wait runs out."""
