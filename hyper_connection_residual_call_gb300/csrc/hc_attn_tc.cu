@@ -1043,14 +1043,12 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         if (value == values && there) {
                             uint8_t *codes = tiles + P::kRing + rs * P::kRawBytes;
                             const uint8_t *from = values ? p.c.v : p.c.k, *scales = values ? p.c.vs : p.c.ks, *biases = values ? p.c.vb : p.c.kb;
-                            if (!(part & 1)) {
-                                bulk_copy_g2s(codes + c * per_page * P::kRawRow, from + row * P::kRawRow, per_page * P::kRawRow, &sh.raw_full[rs]);
-                            } else {
-                                uint8_t *to = codes + P::kRawCodes + c * per_page * of_row;
-                                bulk_copy_g2s(to, scales + row * of_row, per_page * of_row, &sh.raw_full[rs]);
-                                if (kType == kKvInt4)
-                                    bulk_copy_g2s(to + P::kRawScales, biases + row * of_row, per_page * of_row, &sh.raw_full[rs]);
-                            }
+                            const bool code = !(part & 1);
+                            uint8_t *to = code ? codes + c * per_page * P::kRawRow : codes + P::kRawCodes + c * per_page * of_row;
+                            bulk_copy_g2s(to, code ? from + row * P::kRawRow : scales + row * of_row, per_page * (code ? P::kRawRow : of_row),
+                                          &sh.raw_full[rs]);
+                            if (kType == kKvInt4 && !code)
+                                bulk_copy_g2s(to + P::kRawScales, biases + row * of_row, per_page * of_row, &sh.raw_full[rs]);
                         }
                         __syncwarp();
                         return true;
