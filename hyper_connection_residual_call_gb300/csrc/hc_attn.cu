@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kAttnThreads, (Format<kType, D>::template bloc
     pdl_wait();
     pdl_launch_dependents();  // after the wait: the join reads the lengths before its own
     const int tid = threadIdx.x;
-    const Line line(p, kTile, scratch);
+    const Line<> line(p, kTile, scratch);
     const int ctas = attn_ctas(line.total, gridDim.x, least);
     if ((int)blockIdx.x >= ctas || line.total == 0)
         return;
@@ -882,19 +882,19 @@ struct Segments {
 
     __device__ __forceinline__ Segments(const AttnParams &p, int rows, int tile, int grid, int least, LineScratch &scratch)
     {
-        const Line line(p, tile, scratch);
+        const Line<true> line(p, tile, scratch);
         const int ctas = attn_ctas(line.total, grid, least);
         const int blocks = p.c.heads * p.row_blocks;
         b = blockIdx.x / blocks;
         item = blockIdx.x % blocks;
         if (line.total == 0)
             return;
-        const SeqLen seq = attn_seq(p, b, tile);
+        const SeqLen seq = attn_seq<true>(p, b, tile);
         // the line's index of sequence b: the thread that has it in its run
         if (b >= line.b0 && b < line.b1) {
             long at = line.base;
             for (int i = line.b0; i < b; ++i)
-                at += attn_seq(p, i, tile).tiles * line.per;
+                at += attn_seq<true>(p, i, tile).tiles * line.per;
             scratch.base = at;
         }
         __syncthreads();

@@ -27,11 +27,13 @@ struct SeqLen {
     bool bad;
 };
 
+// kFromL2: not from L1, for the join, which reads the lengths before its wait.
+template <bool kFromL2 = false>
 __device__ __forceinline__ SeqLen attn_seq(const AttnParams &p, int b, int tile)
 {
     SeqLen s;
     const long cap = (long)p.c.max_pages << p.c.page_shift;
-    const int raw = __ldcg(p.ctx_len + b);  // from L2: the join reads it before its wait
+    const int raw = kFromL2 ? __ldcg(p.ctx_len + b) : p.ctx_len[b];
     s.ctx = (int)max(0l, min((long)raw, cap));
     const long keys = min((long)s.ctx + p.T, cap);
     s.bad = raw < 0 || (long)raw + p.T > cap;
@@ -50,6 +52,7 @@ struct LineScratch {
 
 // The line, scanned by all threads of a block (kAttnThreads at least, whose first
 // kAttnThreads each take a run of sequences [b0, b1)): `total` tiles.
+template <bool kFromL2 = false>
 struct Line {
     long total, base, sum, per;
     int b0, b1;
@@ -64,7 +67,7 @@ struct Line {
         sum = 0;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b)
-            sum += attn_seq(p, b, tile).tiles * per;
+            sum += attn_seq<kFromL2>(p, b, tile).tiles * per;
         long incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -77,8 +80,8 @@ struct Line {
         __syncthreads();
         long before = 0;
         total = 0;
-#pragma unroll 1
-        for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+#pragma unroll
+        for (int w = 0; w < kAttnThreads / 32; ++w) {  // further warps have no sequences
             if (w < warp)
                 before += sc.warp_sum[w];
             total += sc.warp_sum[w];
@@ -94,8 +97,8 @@ struct Line {
             long at = base;
             int b = b0;
 #pragma unroll 1
-            for (;; ++b) {
-                const long n = attn_seq(p, b, tile).tiles * per;
+            for (; b + 1 < b1; ++b) {
+                const long n = attn_seq<kFromL2>(p, b, tile).tiles * per;
                 if (x < at + n)
                     break;
                 at += n;
@@ -107,22 +110,25 @@ struct Line {
     }
 };
 
+// a / b for a >= 0, b > 0, in 32 bits where they fit: the call's start is a chain of such steps.
+__device__ __forceinline__ long attn_div(long a, long b) { return (a | b) <= 0x7FFFFFFF ? (long)((unsigned)a / (unsigned)b) : a / b; }
+
 // CTAs that take part: none has fewer than `least` tiles but the only one.
 __device__ __forceinline__ int attn_ctas(long n, int grid, int least)
 {
-    return (int)max(1l, min((long)grid, n / least));
+    return (int)max(1l, min((long)grid, attn_div(n, least)));
 }
 
 // How the line is cut: the first `more` CTAs have share + 1 tiles, the others share.
 struct Cut {
     long share, more;
-    __device__ __forceinline__ Cut(long n, int ctas) : share(n / ctas), more(n - share * ctas) {}
+    __device__ __forceinline__ Cut(long n, int ctas) : share(attn_div(n, ctas)), more(n - share * ctas) {}
     __device__ __forceinline__ long first(int c) const { return c * share + min((long)c, more); }
     // The CTA whose range holds tile x.
     __device__ __forceinline__ int cta_of(long x) const
     {
         const long big = more * (share + 1);
-        return x < big ? (int)(x / (share + 1)) : (int)(more + (x - big) / share);
+        return x < big ? (int)attn_div(x, share + 1) : (int)(more + attn_div(x - big, share));
     }
 };
 

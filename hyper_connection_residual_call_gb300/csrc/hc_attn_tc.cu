@@ -269,7 +269,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
 
-    const Line line(p, kKeys, sh.line);
+    const Line<> line(p, kKeys, sh.line);
     const int ctas = attn_ctas(line.total, gridDim.x, least);
     if ((int)blockIdx.x >= ctas || line.total == 0)
         return;
