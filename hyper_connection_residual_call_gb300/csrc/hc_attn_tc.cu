@@ -38,10 +38,10 @@
 // rounded, which costs some 2% (119.6 -> 123 us, 110 -> 112) and takes the results'
 // error against 64 bits from 1.3 times a plain fp32 form's to 1.15 (its mean).
 //
-// What bounds it: 4 x 512 rows over 16384 bf16 keys take 123 us, 55 of them tensor-core
+// What bounds it: 4 x 512 rows over 16384 bf16 keys take 122 us, 55 of them tensor-core
 // time: a stream's chain of product, softmax and product, of some 3500 cycles a tile
-// against 2048 of products. 4 x 64 rows over 32768 bf16 keys, 88 us for 60 of bytes: five
-// tiles in shared memory are what is in flight. 64 FP8 rows, 112 us for 60 of bytes: the
+// against 2048 of products. 4 x 64 rows over 32768 bf16 keys, 87 us for 60 of bytes: five
+// tiles in shared memory are what is in flight. 64 FP8 rows, 110 us for 60 of bytes: the
 // softmax's chain, the conversion of the values and the copy warp's instructions, each
 // some 2000 of the 2400 cycles a tile.
 //
