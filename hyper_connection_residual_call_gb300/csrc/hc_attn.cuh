@@ -139,9 +139,8 @@ struct Items {
     int b, head, block, t0, t1;
     SeqLen seq;
 
-    // (A call of its own in kernels whose roles each walk the items: their code has to
-    // fit the instruction caches.)
-    __device__ __noinline__ bool next(const AttnParams &p, int tile)
+    // (Inlined in each role: 4 x 64 rows over 32768 bf16 keys take 80 us, and 87 with a function that is called.)
+    __device__ __forceinline__ bool next(const AttnParams &p, int tile)
     {
         while (at < end) {
             seq = attn_seq(p, b, tile);
@@ -204,7 +203,7 @@ __device__ __forceinline__ float kv_value_at(const KvView &c, size_t row, int d)
 // The kernels put zeros in the place of such values of nodes -- in a product, a
 // zero weight would not keep them from the rows that do not see them -- and add
 // this where one was found.
-static __device__ __noinline__ float attn_wild_values(const AttnParams &p, int b, int head, int t, int d, int ctx, int from, int to)
+static __device__ __forceinline__ float attn_wild_values(const AttnParams &p, int b, int head, int t, int d, int ctx, int from, int to)
 {
     const uint32_t *mask = attn_mask_row(p, b, t);
     float sum = 0.f;
@@ -223,7 +222,7 @@ static __device__ __noinline__ float attn_wild_values(const AttnParams &p, int b
 
 // Which of the 32 positions ctx + n0 .. ctx + n0 + 31 node row t sees (n0 may be
 // negative: the context), bit i for ctx + n0 + i.
-static __device__ __noinline__ uint32_t attn_sees32(const AttnParams &p, const uint32_t *mask_row, int t, int n0, const SeqLen &seq)
+static __device__ __forceinline__ uint32_t attn_sees32(const AttnParams &p, const uint32_t *mask_row, int t, int n0, const SeqLen &seq)
 {
     const auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
     const uint32_t present = low(seq.keys - seq.ctx - n0);

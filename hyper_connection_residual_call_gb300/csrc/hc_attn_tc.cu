@@ -332,7 +332,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         // there, and every further wait returns at once.)
         for (int item = 0; it.next(p, kKeys); ++item) {
             const SeqLen seq = it.seq;
-            const int it_b = it.b, it_head = it.head, it_t0 = it.t0, it_t1 = it.t1, it_block = it.block;  // (the walk itself lives in memory)
+            const int it_b = it.b, it_head = it.head, it_t0 = it.t0, it_t1 = it.t1, it_block = it.block;
             if (seq.bad && tid == 0 && status)
                 atomicExch(status, kStatusBadArg);
             const int n = it_t1 - it_t0, row0 = it_block * kRows;
@@ -615,7 +615,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         uint32_t q_phase = 1;
         for (int item = 0; it.next(p, kKeys); ++item) {  // (as above: no wait ends it)
             const SeqLen seq = it.seq;
-            const int it_b = it.b, it_head = it.head, it_t0 = it.t0, it_t1 = it.t1, it_block = it.block;  // (the walk itself lives in memory)
+            const int it_b = it.b, it_head = it.head, it_t0 = it.t0, it_t1 = it.t1, it_block = it.block;
             const int n = it_t1 - it_t0, row0 = it_block * kRows;
             if (ct == 0)
                 *reinterpret_cast<volatile int *>(&sh.wild[item & 3]) = 0;
@@ -969,7 +969,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         uint8_t *const tiles = smem_raw + (base - smem_addr(smem_raw));
         while (ok && it.next(p, kKeys)) {
             const SeqLen seq = it.seq;
-            const int it_b = it.b, it_head = it.head, it_t0 = it.t0, it_t1 = it.t1;  // (the walk itself lives in memory)
+            const int it_b = it.b, it_head = it.head, it_t0 = it.t0, it_t1 = it.t1;
             const int n = it_t1 - it_t0;
             // pages: lane 8 i + c holds chunk c of tile 4 g + i, for the group g at hand and the next
             const auto pages_of = [&](int g) {
