@@ -24,8 +24,8 @@
 // An INT4 value becomes q * scale + bias in fp16.
 //
 // What it measures: 32 chains of 8 tokens x 4 heads over up to 6000 bf16 keys of 8 heads,
-// 113 us for 0.6 GB, 0.78 of the measured copy rate (103 of them this kernel at 74% of
-// DRAM's peak, the rest the join). 2 x 12 rows over 131072 keys of 8 heads: INT4 96 us for
+// 110 us for 0.6 GB, 0.80 of the measured copy rate (some 100 of them this kernel at 74% of
+// DRAM's peak, the rest the join). 2 x 12 rows over 131072 keys of 8 heads: INT4 94 us for
 // 0.23 GB, bound by its instructions, some 490 for a warp's 16 keys at 59% of the issue
 // slots (of them 110 that turn codes into operands, 32 products); FP8 97 us for 0.41 GB,
 // likewise. One token of 20 heads over 1000 keys: 12 us, two launches and some six

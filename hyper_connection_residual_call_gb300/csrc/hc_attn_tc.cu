@@ -35,13 +35,13 @@
 // the conversion is hidden as well: some 160 us for 96 rows either way.)
 //
 // As in hc_attn.cu, a row's sums are divided by the sum of the weights as they were
-// rounded, which costs some 2% (119.6 -> 123 us, 110 -> 112) and takes the results'
+// rounded, which costs some 2% (119.6 -> 123 us, 110 -> 112, when it was taken) and takes the results'
 // error against 64 bits from 1.3 times a plain fp32 form's to 1.15 (its mean).
 //
-// What bounds it: 4 x 512 rows over 16384 bf16 keys take 122 us, 55 of them tensor-core
+// What bounds it: 4 x 512 rows over 16384 bf16 keys take 119 us, 55 of them tensor-core
 // time: a stream's chain of product, softmax and product, of some 3500 cycles a tile
-// against 2048 of products. 4 x 64 rows over 32768 bf16 keys, 87 us for 60 of bytes: five
-// tiles in shared memory are what is in flight. 64 FP8 rows, 110 us for 60 of bytes: the
+// against 2048 of products. 4 x 64 rows over 32768 bf16 keys, 81 us for 60 of bytes: five
+// tiles in shared memory are what is in flight. 64 FP8 rows, 109 us for 60 of bytes: the
 // softmax's chain, the conversion of the values and the copy warp's instructions, each
 // some 2000 of the 2400 cycles a tile.
 //
@@ -1156,9 +1156,9 @@ cudaError_t launch_rows(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t 
 // elements (two accumulators and two score tiles fill TMEM); fewer rows in the pool than a
 // tensor map's coordinates reach; more than 32 rows, of INT4, whose keys are converted to
 // two tiles, more than 64. us in blocks of 32 rows and here, over long contexts: 64 rows of
-// FP8 x 64 95 and 70, of INT4 x 128 132 and 142, 96 of INT4 x 128 186 and 147, 100 of
-// INT4 x 64 174 and 108. Over some hundred keys this kernel's longer start costs 2 to 6 us
-// (40 rows over 800 keys: 18.4 and 20.4); the host does not know the lengths.
+// FP8 x 64 95 and 65, of INT4 x 128 132 and 142, 96 of INT4 x 128 186 and 145, 100 of
+// INT4 x 64 174 and 106. Over some hundred keys this kernel's longer start costs 2 us or so;
+// the host does not know the lengths.
 int attn_wide_rows(const KvView &c, long rows)
 {
     if (rows <= (c.type == kKvInt4 ? 64 : 32) || c.D > 128)
