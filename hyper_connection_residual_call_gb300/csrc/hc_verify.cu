@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(kVerifyThreads) hc_verify_kernel(const VerifyP
 cudaError_t launch_verify(const VerifyParams &p, const LaunchCfg &cfg, cudaStream_t stream)
 {
     // As many CTAs a sequence as the SMs hold (up to 8, a portable cluster), with
-    // no fewer than 2048 words of a row for each.
+    // no fewer than 2048 words of a row for each. A chain of 5 over 32768 words: 18.4 us with
+    // 8 or 4 CTAs, 23.8 with 2, 36 with 1; 8 trees of 8 over 16384: 20.2 with 4, 22.3 with 2.
     int ranks = 8;
     while (ranks > 1 && ((long)p.B * ranks > cfg.sm_count || p.V / ranks < 2048))
         ranks /= 2;
