@@ -158,8 +158,9 @@ __device__ __forceinline__ void write_row(const KvView &c, const RowAt<kLanes> &
     __half scale[2], bias[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        // Infinities and NaNs are the largest or the smallest.
-        const bool bad = (int16_t)(range[k] & 0xFFFFu) >= 0x7F80 || (int16_t)(range[k] >> 16) >= 0x7F7F;
+        // Infinities and NaNs are the largest or the smallest: from 0x7F80 on in both halves, where the
+        // lowest finite bf16's complement is 0x7F7F like the highest itself.
+        const bool bad = (int16_t)(range[k] & 0xFFFFu) >= 0x7F80 || (int16_t)(range[k] >> 16) >= 0x7F80;
         // Values saturate at +-57344, so that q * scale + bias stays inside fp16 for every q.
         const uint32_t most = ordered16x2(range[k] & 0xFFFFu) << 16, least = ordered16x2(~range[k] >> 16) << 16;
         const float top = fminf(fmaxf(__uint_as_float(most), -kInt4Most), kInt4Most);
