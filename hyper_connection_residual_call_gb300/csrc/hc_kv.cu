@@ -98,7 +98,7 @@ __device__ __forceinline__ void write_row(const KvView &c, const RowAt<kLanes> &
         }
         return;
     }
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (kType == kKvFp8) {
         // |x| as 16-bit integers keeps its order, and infinities and NaNs are the largest
         uint32_t top = 0;
@@ -112,6 +112,11 @@ __device__ __forceinline__ void write_row(const KvView &c, const RowAt<kLanes> &
         const bool bad = top >= 0x7F80u;
         const int byte = bad ? kFp8BadRow : fp8_scale_byte(__uint_as_float(top << 16));
         const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);  // 2^-e, exact
+        if (byte == kFp8TopRow) {  // (the same for a row's lanes, and rare)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[j] = (w[j] & 0x80008000u) | __vminu2(w[j] & 0x7FFF7FFFu, kFp8TopBits * 0x10001u);
+        }
         uint32_t out[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -34,6 +34,12 @@ __device__ __forceinline__ size_t kv_row(const KvView &c, long page, int h, long
 // A row that held an infinity or a NaN (FP8).
 constexpr int kFp8BadRow = 255;
 
+// The byte of the largest scale, 2^120, whose code 256 would be 2^128, more than a bf16 holds: elements
+// that would round to it are held back to 240 2^120, the bf16 with these bits (off by 2^-4 of themselves
+// at most, as e4m3 is elsewhere).
+constexpr int kFp8TopRow = 247;
+constexpr uint32_t kFp8TopBits = 0x7F70u;
+
 // The scale byte of a row with finite maximum amax: the smallest e >= -117 with
 // amax <= 448 * 2^e, plus 127. From the bits: 448 = 1.75 * 2^8. At e >= -117 the
 // smallest code, 2^-9 * 2^e, is a normal bf16, so that rows read back exactly.

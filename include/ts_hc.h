@@ -494,8 +494,10 @@ ts_status ts_hc_rope(const void *q, long q_stride, const void *k, long k_stride,
 typedef enum {
     TS_KV_BF16 = 0,           /* bf16 [D] */
     TS_KV_FP8 = 1,            /* e4m3 [D] and one scale 2^(byte - 127) a row: the smallest power of two
-                                 with max|x| <= 448 * scale, at least 2^-117. Byte 255 marks a row that
-                                 held an infinity or a NaN; it reads back as NaN. No code is a NaN */
+                                 with max|x| <= 448 * scale, at least 2^-117. Elements beyond +-240 * 2^120,
+                                 whose nearest code would be 2^128, are stored as that. Byte 255 marks a row
+                                 that held an infinity or a NaN; it reads back as NaN. No code is a NaN, and
+                                 code * scale is a finite bf16 */
     TS_KV_INT4 = 2            /* uint8 [D/2], element 2i in the low nibble of byte i, and fp16 scale and
                                  bias per group, as TS_W_INT4_AFFINE: x = q * scale + bias with
                                  scale = (max - min) / 15, bias = min (rounded to fp16; values beyond

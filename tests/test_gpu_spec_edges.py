@@ -7,7 +7,7 @@ import torch
 import spec_reference as R
 from gpu_common import require_gpu
 from hyper_connection_residual_call_gb300 import binding as B
-from test_gpu_spec import U16, gen, make_cache, randn
+from test_gpu_spec import TREE, U16, gen, make_cache, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -45,4 +45,46 @@ def test_int4_largest_finite_values_saturate(group):
         assert (np.abs(R.f64(got) - want) <= U16 * np.abs(want) + 1e-6).all()
     out, lse = B.hc_tree_attention(x[:, :1] * 0, cache, zeros() + 5)
     assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    assert B.device_status() == B.TS_OK
+
+
+FP8_LARGEST = (0x7F7F, 0xFF7F, 0x7F78, 0xFF78, 0x7F77, 0x7F61)  # +-(2 - 2^-7) 2^127, +-1.9375 2^127, and below it
+
+
+def test_fp8_largest_finite_values_read_back_finite():
+    """With a scale of 2^120 the code 256 would be 2^128: such an element is stored as 240 2^120."""
+    g = gen(41)
+    cache = make_cache(g, "fp8", 1, 16, 1, 16, 128)
+    x = randn(g, 1, 8, 1, 128, scale=1e37)
+    for i, v in enumerate(bf16_bits(*FP8_LARGEST)):
+        x[0, i, 0, 7 * i + 1] = v
+    x[0, 6] = bf16_bits(0xFF7F)[0]
+    B.hc_kv_write(x, x, cache, zeros())
+    x64 = R.f64(x)
+    want = np.stack([R.fp8_row(r)[2] for r in x64.reshape(-1, 128)]).reshape(x64.shape)
+    want = np.clip(want, -240 * 2.0 ** 120, 240 * 2.0 ** 120)
+    for got in B.hc_kv_read(cache, zeros(), 8):
+        assert np.array_equal(R.f64(got), want)
+    assert (np.abs(want - x64) <= 2.0 ** -4 * np.abs(x64) + 2.0 ** 110).all()  # half a spacing of e4m3, also where it is held back
+    assert B.device_status() == B.TS_OK
+
+
+@pytest.mark.parametrize("hq", [2, 4, 8, 16])
+def test_fp8_largest_values_of_unseen_nodes_do_not_reach_a_row(hq):
+    """24, 48, 96 and 192 rows: a node's largest finite values are no infinities to the rows that do not see it."""
+    g = gen(42)
+    t, ctx, d = 12, 150, 128
+    cache = make_cache(g, "fp8", 1, ctx + t, 1, 32, d)
+    k, v = randn(g, 1, ctx + t, 1, d), randn(g, 1, ctx + t, 1, d)
+    see = R.sees(TREE)
+    mask = R.words(see)[None].cuda()
+    q = randn(g, 1, t, hq, d)
+    B.hc_kv_write(k, v, cache, zeros())
+    out, lse = B.hc_tree_attention(q, cache, zeros() + ctx, mask=mask)
+    largest = bf16_bits(*FP8_LARGEST)
+    v[0, ctx + 5, 0, :6], v[0, ctx + 9, 0, 60:66] = largest, largest
+    B.hc_kv_write(k, v, cache, zeros())
+    out2, lse2 = B.hc_tree_attention(q, cache, zeros() + ctx, mask=mask)
+    clean = torch.from_numpy(~(see[:, 5] | see[:, 9])).cuda()
+    assert torch.equal(out2[:, clean], out[:, clean]) and torch.equal(lse2, lse)
     assert B.device_status() == B.TS_OK
