@@ -240,12 +240,20 @@ __global__ void __launch_bounds__(kVerifyThreads) hc_verify_kernel(const VerifyP
             const Pair none{-INFINITY, __int_as_float(0x7FFFFFFF)};
             const Best best;
             st = none;
+            bool nan = false;  // which better() passes over
 #pragma unroll
-            for (int i = 0; i < kHold; ++i)
+            for (int i = 0; i < kHold; ++i) {
                 if (v0 + tid + i * kVerifyThreads < v1)
                     st = best.better(st, Pair{l[i], __int_as_float(v0 + tid + i * kVerifyThreads)});
-            for (int v = v0 + tid + kHold * kVerifyThreads; v < v1; v += kVerifyThreads)
-                st = best.better(st, Pair{row[v], __int_as_float(v)});
+                nan |= l[i] != l[i];
+            }
+            for (int v = v0 + tid + kHold * kVerifyThreads; v < v1; v += kVerifyThreads) {
+                const float x = row[v];
+                st = best.better(st, Pair{x, __int_as_float(v)});
+                nan |= x != x;
+            }
+            if (nan)  // before every other
+                st = Pair{INFINITY, __int_as_float(-1)};
             st = reduce<kRanks>(st, best, none, sc, turn);
         } else {
             const Pair none{-INFINITY, 0.f};
@@ -264,13 +272,15 @@ __global__ void __launch_bounds__(kVerifyThreads) hc_verify_kernel(const VerifyP
                     st.b *= ex2f((st.a - x) * k);  // 0 at the first
                     st.a = x;
                 }
-                if (st.a > -INFINITY)
-                    st.b += ex2f((x - st.a) * k);
+                st.b += ex2f((x - (st.a > -INFINITY ? st.a : 0.f)) * k);
             }
             st = reduce<kRanks>(st, Softmax{k}, none, sc, turn);
         }
         const float m = st.a, inv = greedy || !(m > -INFINITY) ? 0.f : 1.f / st.b;
-        const int top = greedy ? __float_as_int(st.b) : 0;
+        const int top = greedy ? __float_as_int(st.b) : -1;
+        // A NaN, and for a softmax an infinity or nothing but -infinity, is no distribution: the walk ends here.
+        if (greedy ? top < 0 : !(st.b > 0.f))
+            kids = 0;
         const auto prob = [&](float x) { return m > -INFINITY ? ex2f((x - m) * k) * inv : 0.f; };
 
         // its children, in their order
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__(kVerifyThreads) hc_verify_kernel(const VerifyP
 
         // no child is left: the next token
         int token = top;
-        if (!greedy) {
+        if (!greedy && st.b > 0.f) {
             const Best best;
             const Pair none{-1.f, __int_as_float(0x7FFFFFFF)};
             Pair win = none;
@@ -358,8 +368,11 @@ __global__ void __launch_bounds__(kVerifyThreads) hc_verify_kernel(const VerifyP
             token = __float_as_int(win.b);
         }
         if (lead) {
+            const bool found = token >= 0 && token < p.V;
+            if (!found && p.status)
+                atomicExch(p.status, kStatusInvalidArg);
             p.n_accepted[b] = count;
-            p.next_token[b] = token >= 0 && token < p.V ? token : 0;
+            p.next_token[b] = found ? token : 0;
         }
         break;
     }

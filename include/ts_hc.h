@@ -608,7 +608,9 @@ ts_status ts_hc_tree_attention(const void *q, long q_stride, const ts_hc_kv_cach
  *   u            fp32 [B][T], in [0, 1): node i's at u[b][i] (the root's is not read)
  *   noise        fp32 [B][V], > 0
  *   n_accepted   int32 [B]; path int32 [B][T]: 0 and the accepted nodes, then -1; next_token int32 [B]
- * Only the rows that a walk reaches are read. T <= 4096, V < 2^30.
+ * Only the rows that a walk reaches are read. A walk ends at a row that is no distribution -- a NaN in it,
+ * or, not greedy, a +infinity or nothing but -infinity -- with 0 as the next token, and TS_ERR_INVALID_ARG
+ * is recorded. T <= 4096, V < 2^30.
  */
 ts_status ts_hc_verify(const float *logits, const float *draft_probs, const int32_t *tokens,
                        const int32_t *parents, long parents_stride, const float *temperature, const float *u,

@@ -88,3 +88,74 @@ def test_fp8_largest_values_of_unseen_nodes_do_not_reach_a_row(hq):
     clean = torch.from_numpy(~(see[:, 5] | see[:, 9])).cuda()
     assert torch.equal(out2[:, clean], out[:, clean]) and torch.equal(lse2, lse)
     assert B.device_status() == B.TS_OK
+
+
+# ------------------------------------------------------------------ logits without a distribution
+
+def accepting_chain(v, t=4, seed=43):
+    """Logits, tokens and the rest of a call whose chain of drafts holds at every node, greedy and sampled."""
+    g = gen(seed)
+    logits = torch.randn(1, t, v, generator=g, device="cuda")
+    tokens = torch.zeros(1, t, dtype=torch.int32, device="cuda")
+    tokens[0, 1:] = logits[0, :-1].argmax(-1).int()
+    draft = torch.softmax(logits.double(), -1).float()
+    rest = dict(draft_probs=draft, u=torch.zeros(1, t, device="cuda"), noise=torch.ones(1, v, device="cuda"))
+    return logits, tokens, rest
+
+
+def verify_both(logits, tokens, rest, sampled):
+    if sampled:
+        return B.hc_verify(logits, tokens, None, torch.ones(1, device="cuda"), **rest)
+    return B.hc_verify(logits, tokens)
+
+
+@pytest.mark.parametrize("v", [1, 50, 5000, 40001, 160000])
+@pytest.mark.parametrize("node", [0, 2, 3])
+@pytest.mark.parametrize("sampled", [False, True])
+def test_verify_records_a_nan(v, node, sampled):
+    """A NaN in a row that the walk reaches ends it there: recorded, and the next token is 0."""
+    logits, tokens, rest = accepting_chain(v)
+    for at in sorted({0, v // 2, v - 1}):
+        bad = logits.clone()
+        bad[0, node, at] = float("nan")
+        n, path, nxt = verify_both(bad, tokens, rest, sampled)
+        assert B.device_status() == B.TS_ERR_INVALID_ARG
+        assert n.tolist() == [node] and path[0].tolist() == list(range(node + 1)) + [-1] * (3 - node) and nxt.tolist() == [0]
+
+
+@pytest.mark.parametrize("sampled", [False, True])
+def test_verify_records_a_nan_among_ruled_out_words(sampled):
+    """160000 words over 8 CTAs: a thread that has nothing but -infinity before the NaN, which lies past what it keeps in registers."""
+    logits, tokens, rest = accepting_chain(160000)
+    logits[0, 0] = float("-inf")
+    logits[0, 0, 7], logits[0, 0, 16384 + 5] = 1.0, float("nan")
+    n, _, nxt = verify_both(logits, tokens, rest, sampled)
+    assert B.device_status() == B.TS_ERR_INVALID_ARG
+    assert n.tolist() == [0] and nxt.tolist() == [0]
+
+
+def test_verify_infinities():
+    """An infinite logit has no softmax (recorded) but an argmax; a row that is all -infinity has no softmax."""
+    logits, tokens, rest = accepting_chain(3000)
+    for value, all_of_it in ((float("inf"), False), (float("-inf"), True)):
+        bad = logits.clone()
+        bad[0, 1, slice(None) if all_of_it else 17] = value
+        n, path, nxt = verify_both(bad, tokens, rest, True)
+        assert B.device_status() == B.TS_ERR_INVALID_ARG
+        assert n.tolist() == [1] and path[0].tolist() == [0, 1, -1, -1] and nxt.tolist() == [0]
+        if not all_of_it:
+            n, _, nxt = verify_both(bad, tokens, rest, False)
+            assert n.tolist() == [1] and nxt.tolist() == [17]
+            assert B.device_status() == B.TS_OK
+
+
+@pytest.mark.parametrize("sampled", [False, True])
+def test_verify_does_not_look_at_rows_off_the_walk(sampled):
+    logits, tokens, rest = accepting_chain(3000)
+    parents = torch.tensor([-1, 0, 0, 1], dtype=torch.int32, device="cuda")
+    tokens[0, 3] = logits[0, 1].argmax().int()
+    logits[0, 2] = float("nan")
+    kw = dict(rest) if sampled else {}
+    n, path, _ = B.hc_verify(logits, tokens, parents, torch.ones(1, device="cuda") if sampled else None, **kw)
+    assert n.tolist() == [2] and path[0].tolist() == [0, 1, 3, -1]
+    assert B.device_status() == B.TS_OK
