@@ -310,9 +310,10 @@ __global__ void __launch_bounds__(kKvThreads) hc_kv_compact_kernel(const KvCompa
     pdl_wait();
     const int b = blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads;
     const int ctx = p.ctx_len[b];
+    const bool lead = threadIdx.x == 0 && h == 0 && blockIdx.y == 0;
     int n = p.n_accepted[b];
     if (ctx < 0 || n < 0 || n >= p.T) {
-        if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0) {
+        if (lead) {
             if (p.status)
                 atomicExch(p.status, kStatusBadArg);
             if (p.new_len)
@@ -320,8 +321,6 @@ __global__ void __launch_bounds__(kKvThreads) hc_kv_compact_kernel(const KvCompa
         }
         return;
     }
-    if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0 && p.new_len)
-        p.new_len[b] = ctx + n + 1;
     const int cols = row_bytes(p.c.type, p.c.D) / 16;
     const int scols = p.c.type == kKvBf16 ? 0 : p.c.type == kKvFp8 ? 1 : 2 * (p.c.D / p.c.group);
     const int per = cols + scols;
@@ -338,7 +337,8 @@ __global__ void __launch_bounds__(kKvThreads) hc_kv_compact_kernel(const KvCompa
         if (node <= last || node >= p.T || src < 0 || dst < 0) {  // not an ascending path, or no place
             if (i == 0 && p.status)
                 atomicExch(p.status, kStatusBadArg);
-            return;
+            n = step - 1;
+            break;
         }
         last = node;
         if (node == step)
@@ -356,6 +356,8 @@ __global__ void __launch_bounds__(kKvThreads) hc_kv_compact_kernel(const KvCompa
             x[d * groups + g] = x[s * groups + g];
         }
     }
+    if (lead && p.new_len)
+        p.new_len[b] = ctx + n + 1;  // the root and the steps that were moved
 }
 
 // One thread per (sequence, node): walks up to the root. An entry that is not a

@@ -547,6 +547,8 @@ ts_status ts_hc_kv_read(const ts_hc_kv_cache *cache, const int32_t *start, void 
  * After a verification: the rows of the accepted nodes, at ctx_len[b] + path[b][i], move to
  * ctx_len[b] + i for i = 1 .. n_accepted[b] (codes and scales as they are), and new_len[b] =
  * ctx_len[b] + n_accepted[b] + 1. A path ascends, so that no row is overwritten before it is read.
+ * A step that does not ascend or has no place ends its path there (recorded): the steps before it are
+ * moved, and new_len counts those. With a length or a count out of range nothing is, and new_len = ctx_len.
  *   path         int32 [B][T] and n_accepted int32 [B], as ts_hc_verify writes them
  *   new_len      int32 [B] or NULL; must not be ctx_len
  */

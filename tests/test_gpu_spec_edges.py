@@ -159,3 +159,38 @@ def test_verify_does_not_look_at_rows_off_the_walk(sampled):
     n, path, _ = B.hc_verify(logits, tokens, parents, torch.ones(1, device="cuda") if sampled else None, **kw)
     assert n.tolist() == [2] and path[0].tolist() == [0, 1, 3, -1]
     assert B.device_status() == B.TS_OK
+
+
+# ------------------------------------------------------------------ compaction of a refused path
+
+@pytest.mark.parametrize("kind,group", [("bf16", 0), ("fp8", 0), ("int4", 32)])
+def test_compact_counts_what_it_moved(kind, group):
+    """A path that is refused at a step: the rows before it are moved, and new_len counts those."""
+    g = gen(44)
+    b, t, heads, page, d = 6, 8, 2, 16, 64
+    cache = make_cache(g, kind, b, 64, heads, page, d, group or 64)
+    lens = torch.tensor([0, 9, 12, 3, 5, 10], dtype=torch.int32, device="cuda")
+    B.hc_kv_write(randn(g, b, t, heads, d), randn(g, b, t, heads, d), cache, lens)
+    k0, v0 = B.hc_kv_read(cache, lens, t)
+    table = cache.tensors[2]
+    was = table[2, 1].clone()
+    table[2, 1] = -1  # positions 16 .. 31 of sequence 2, its nodes 4 and on
+    paths = [[0, 3, 2], [0, 2, 9], [0, 2, 3, 5], [0, 2, 4, 7], [0, 1, 3], [0, 0]]
+    moved = [1, 1, 2, 3, 0, 0]  # steps that hold
+    path = torch.full((b, t), -1, dtype=torch.int32)
+    for i, p in enumerate(paths):
+        path[i, :len(p)] = torch.tensor(p)
+    n = torch.tensor([2, 2, 3, 3, 9, 1], dtype=torch.int32, device="cuda")  # sequence 4: more than there are nodes
+    new = B.hc_kv_compact(cache, lens, path.cuda(), n)
+    assert B.device_status() == B.TS_ERR_INVALID_ARG
+    want = [int(c) + m + 1 for c, m in zip(lens.tolist(), moved)]
+    want[4] = 5  # nothing is known of its path
+    assert new.tolist() == want
+    table[2, 1] = was
+    k1, v1 = B.hc_kv_read(cache, lens, t)
+    for i, (p, m) in enumerate(zip(paths, moved)):
+        source = list(range(t))
+        source[:m + 1] = p[:m + 1]
+        for a, z in ((k0, k1), (v0, v1)):
+            assert torch.equal(z[i], a[i, torch.tensor(source, device="cuda")])
+    assert B.device_status() == B.TS_OK
