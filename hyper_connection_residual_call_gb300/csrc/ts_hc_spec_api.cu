@@ -341,6 +341,10 @@ ts_status ts_hc_kv_compact(const ts_hc_kv_cache *cache, const int32_t *ctx_len, 
         TS_TRY(check_ptr_api(new_len, "new_len", 4));
         if (overlap(new_len, sizeof(int32_t) * (size_t)B, ctx_len, sizeof(int32_t) * (size_t)B))
             return api_error(TS_ERR_INVALID_ARG, "new_len overlaps ctx_len");
+        if (overlap(new_len, sizeof(int32_t) * (size_t)B, n_accepted, sizeof(int32_t) * (size_t)B))
+            return api_error(TS_ERR_INVALID_ARG, "new_len overlaps n_accepted");
+        if (overlap(new_len, sizeof(int32_t) * (size_t)B, path, sizeof(int32_t) * (size_t)B * T))
+            return api_error(TS_ERR_INVALID_ARG, "new_len overlaps path");
     }
     tshc::LaunchCfg cfg;
     tshc::KvCompactParams p{};

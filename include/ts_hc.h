@@ -550,7 +550,7 @@ ts_status ts_hc_kv_read(const ts_hc_kv_cache *cache, const int32_t *start, void 
  * A step that does not ascend or has no place ends its path there (recorded): the steps before it are
  * moved, and new_len counts those. With a length or a count out of range nothing is, and new_len = ctx_len.
  *   path         int32 [B][T] and n_accepted int32 [B], as ts_hc_verify writes them
- *   new_len      int32 [B] or NULL; must not be ctx_len
+ *   new_len      int32 [B] or NULL; must not overlap ctx_len, n_accepted or path (other blocks still read them)
  */
 ts_status ts_hc_kv_compact(const ts_hc_kv_cache *cache, const int32_t *ctx_len, const int32_t *path,
                            const int32_t *n_accepted, int32_t *new_len, int B, int T, cudaStream_t stream);
