@@ -31,7 +31,10 @@
 // likewise. One token of 20 heads over 1000 keys: 12 us, two launches and some six
 // dependent loads.
 #include <algorithm>
+#include <map>
+#include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "hc_attn.cuh"
 
@@ -1128,13 +1131,10 @@ cudaError_t launch_few(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
     constexpr int kSmem = Smem<kType, D, MT>::kTotal;
     p.row_blocks = (p.rows + kRows - 1) / kRows;
     auto *kernel = hc_attn_few_kernel<kType, D, MT, kGroup>;
-    static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (set != cudaSuccess)
-        return set;
-    static const int per_sm = [kernel] {  // of this build's kernel on this GPU type
-        int n = 0;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kAttnThreads, kSmem) == cudaSuccess ? std::max(n, 1) : 1;
-    }();
+    int per_sm = 1;
+    cudaError_t e = attn_ready(reinterpret_cast<const void *>(kernel), kAttnThreads, kSmem, &per_sm);
+    if (e != cudaSuccess)
+        return e;
     const int grid = std::min(per_sm * cfg.sm_count, kAttnMaxGrid);
     cudaLaunchConfig_t lc{};
     cudaLaunchAttribute at[1];
@@ -1146,7 +1146,7 @@ cudaError_t launch_few(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
     lc.blockDim = dim3(kAttnThreads);
     lc.gridDim = dim3(grid);
     lc.dynamicSmemBytes = kSmem;
-    cudaError_t e = cudaLaunchKernelEx(&lc, kernel, p, kLeastTiles);
+    e = cudaLaunchKernelEx(&lc, kernel, p, kLeastTiles);
     if (e != cudaSuccess)
         return e;
     return launch_attn_join(p, kRows, kTile, grid, kLeastTiles, false, stream);
@@ -1168,6 +1168,30 @@ cudaError_t launch_type(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t 
 }
 
 }  // namespace
+
+cudaError_t attn_ready(const void *kernel, int threads, int smem, int *per_sm)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    static std::mutex mu;
+    static std::map<std::pair<const void *, int>, int> done;
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_pair(kernel, dev);
+    const auto at = done.find(key);
+    if (at != done.end()) {
+        *per_sm = at->second;
+        return cudaSuccess;
+    }
+    int n = 0;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+    if (e == cudaSuccess)
+        done[key] = *per_sm = std::max(n, 1);
+    return e;
+}
 
 cudaError_t launch_attn_join(const AttnParams &p, int rows, int tile, int grid, int least, bool by_columns, cudaStream_t stream)
 {

@@ -274,6 +274,11 @@ __device__ __forceinline__ uint32_t int4_f16x2(uint32_t w, __half2 scale, __half
     return reinterpret_cast<const uint32_t &>(v);
 }
 
+// Once per kernel and device: raises the dynamic shared-memory limit to `smem` and finds how many CTAs of
+// `threads` an SM holds. A failure is not remembered. (The largest carveout, which the other kernels of the
+// library ask for, makes nothing faster here, and 4 x 512 rows over 16384 bf16 keys 0.7% slower: their shared
+// memory leaves no room for another kernel's CTAs either way.)
+cudaError_t attn_ready(const void *kernel, int threads, int smem, int *per_sm);
 // The wide kernel's rows of a block (0: the few-row kernel serves) and its launcher.
 int attn_wide_rows(const KvView &c, long rows);
 cudaError_t launch_attn_wide(const AttnParams &p, const LaunchCfg &cfg, cudaStream_t stream);

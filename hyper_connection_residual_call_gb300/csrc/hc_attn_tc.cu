@@ -1102,9 +1102,10 @@ cudaError_t launch_wide(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
     using Pl = Plan<kType, D, NT, kNarrow>;
     auto *kernel = hc_attn_wide_kernel<kType, D, NT, kNarrow>;
     static_assert(Pl::kTotal + sizeof(Shared<NT, Pl::kRawKeys, kNarrow>) <= 227 * 1024, "shared memory");
-    static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Pl::kTotal);
-    if (set != cudaSuccess)
-        return set;
+    int per_sm = 1;
+    cudaError_t e = attn_ready(reinterpret_cast<const void *>(kernel), kThreads, Pl::kTotal, &per_sm);
+    if (e != cudaSuccess)
+        return e;
     p.row_blocks = (p.rows + 128 * NT - 1) / (128 * NT);
     CUtensorMap map_k{}, map_v{};
     if (kType == kKvBf16) {
@@ -1126,10 +1127,10 @@ cudaError_t launch_wide(AttnParams p, const LaunchCfg &cfg, cudaStream_t stream)
     lc.numAttrs = 1;
     lc.stream = stream;
     lc.blockDim = dim3(kThreads);
-    const int grid = std::min(cfg.sm_count, kAttnWideGrid);
+    const int grid = std::min(per_sm * cfg.sm_count, kAttnWideGrid);
     lc.gridDim = dim3(grid);
     lc.dynamicSmemBytes = Pl::kTotal;
-    cudaError_t e = cudaLaunchKernelEx(&lc, kernel, p, map_k, map_v, kLeastWide);
+    e = cudaLaunchKernelEx(&lc, kernel, p, map_k, map_v, kLeastWide);
     if (e != cudaSuccess)
         return e;
     return launch_attn_join(p, 128 * NT, kKeys, grid, kLeastWide, true, stream);
