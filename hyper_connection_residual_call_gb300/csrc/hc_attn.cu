@@ -234,6 +234,7 @@ struct Walk {
     static constexpr int kSpans = kType == kKvInt4 ? kGroup / 32 : 1;   // 32-element spans of a group
     static_assert(kType != kKvBf16 || F::kStage % 512 == 0, "constants are XORed into a bf16 stage's addresses");
     static constexpr bool kHalf = kType == kKvInt4;  // P and the values in fp16
+    static constexpr float kLift = kHalf ? kFp16Lift : 0.f;
     static constexpr int kSteps = D / 16;
     static constexpr int kCols = D / 8;
 
@@ -518,14 +519,14 @@ struct Walk {
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
                 mx[i][h] = top * sc;
-                move |= mx[i][h] > m[i][h] + kRescale;  // also the first that is not -infinity
+                move |= mx[i][h] > m[i][h] + (kRescale + kLift);  // also the first that is not -infinity
             }
         if (__any_sync(0xFFFFFFFFu, move)) {
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float to = fmaxf(m[i][h], mx[i][h]);
+                    const float to = fmaxf(m[i][h], mx[i][h] - kLift);
                     const float by = to == -INFINITY ? 1.f : ex2(m[i][h] - to);
                     m[i][h] = to;
                     l[i][h] *= by;

@@ -167,6 +167,13 @@ struct Items {
     __device__ __forceinline__ int slot() const { return from > first ? 1 : 0; }
 };
 
+// How far below a row's maximum the reference of its weights is kept (log2), where they are held in fp16: at
+// 2^6 of themselves and more, weights of 2^-20 of the largest and up are normal numbers, and smaller ones are off by
+// 2^-31 of it at most. (With the maximum as the reference those below 2^-25 were nothing in the products.) The
+// reference moves when the maximum has grown by 2^8 more, so that a weight is at most 2^14, and an infinity in fp16
+// only where scores are so large (2^25) that fp32 holds them to no better than a factor of 2 or so.
+constexpr float kFp16Lift = 6.f;
+
 // A partial slot: unnormalised sums [rows][D] (the wide kernel's [D / 4][rows][4]), then
 // the rows' maxima (in units of log2) and sums.
 __host__ __device__ __forceinline__ size_t attn_slot_floats(int rows, int D) { return (size_t)rows * (D + 2); }

@@ -263,6 +263,7 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     extern __shared__ uint8_t smem_raw[];
     constexpr bool kRawKeys = P::kRawKeys, kCoded = P::kCoded;
     constexpr bool kHalf = kType == kKvInt4;  // weights and values in fp16, which holds an INT4 value's 11 bits
+    constexpr float kLift = kHalf ? kFp16Lift : 0.f;
     __shared__ Shared<NT, kRawKeys, kNarrow> sh;
     pdl_wait();
     pdl_launch_dependents();  // after the wait: the join reads the lengths before its own
@@ -394,8 +395,8 @@ hc_attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         top = fmaxf(top, sh.top[s][turn][half ^ 1][row_in]);
                     }
                     top *= by_row;
-                    if (__any_sync(0xFFFFFFFFu, top > m + kGrow)) {  // also the first that is not -infinity
-                        const float to_m = fmaxf(m, top), by = ex2(m - (to_m == -INFINITY ? 0.f : to_m));
+                    if (__any_sync(0xFFFFFFFFu, top > m + (kGrow + kLift))) {  // also the first that is not -infinity
+                        const float to_m = fmaxf(m, top - kLift), by = ex2(m - (to_m == -INFINITY ? 0.f : to_m));
                         m = to_m;
                         l *= by;
                         lr *= by;

@@ -580,8 +580,8 @@ ts_status ts_hc_tree_build(const int32_t *parents, long parents_stride, const in
  *   out        bf16 [B][T][q_heads][D], 16-byte aligned; lse fp32 [B][T][q_heads] or NULL
  *   workspace  >= ts_hc_tree_attention_workspace_bytes(...) bytes, 256-byte aligned; it need not be
  *              initialised and must not be shared by calls that can run at the same time
- * The products run on the tensor cores in bf16 (an INT4 row's values in fp16) with fp32 sums; the softmax's
- * maximum and sum are fp32. Over FP8 rows of 128 elements, 33 to 64 rows a key head
+ * The products run on the tensor cores in bf16 (an INT4 row's values, and their weights, in fp16: a weight is
+ * off by 2^-11 of itself or 2^-31 of the row's largest) with fp32 sums; the softmax's maximum and sum are fp32. Over FP8 rows of 128 elements, 33 to 64 rows a key head
  * (T * q_heads/n_kv_heads) meet the keys as two e4m3 parts each, which leaves an element of q off by at
  * most 2^-17.8 of its row's largest. T <= 4096, T * q_heads/n_kv_heads <= 32768.
  */

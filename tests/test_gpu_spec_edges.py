@@ -7,7 +7,7 @@ import torch
 import spec_reference as R
 from gpu_common import require_gpu
 from hyper_connection_residual_call_gb300 import binding as B
-from test_gpu_spec import TREE, U16, gen, make_cache, randn
+from test_gpu_spec import TREE, U16, U32, gen, make_cache, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -193,4 +193,35 @@ def test_compact_counts_what_it_moved(kind, group):
         source[:m + 1] = p[:m + 1]
         for a, z in ((k0, k1), (v0, v1)):
             assert torch.equal(z[i], a[i, torch.tensor(source, device="cuda")])
+    assert B.device_status() == B.TS_OK
+
+
+# ------------------------------------------------------------------ very small weights
+
+@pytest.mark.parametrize("heads,g,batch", [(608, 1, 4), (152, 72, 2)])
+def test_int4_weights_far_below_the_largest(heads, g, batch):
+    """Few-row and wide blocks with several items a CTA: keys of weight 1 with values of 0, and 8192 of weight
+    2^-25.4 with values of 1, which are all of the result. A weight is held in fp16 as 2^6 of itself or more
+    (relative to the largest), with a spacing of at most 2^-24 where it is subnormal, so that it is off by
+    2^-31 at most, beside the 2^-11 that the bound has: 2^-31 sum|v| / Z more."""
+    d, page, n = 64, 64, 8192
+    table = torch.ones(batch, n // page, dtype=torch.int32, device="cuda")
+    table[:, :4] = 0  # both streams of the wide kernel and every warp of the other have a large weight
+    cache = B.kv_cache("int4", 2, heads, page, d, table, group=64)
+    k = torch.full((1, 2 * page, heads, d), -17.625, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones_like(k)
+    k[:, :page:16], v[:, :page:16] = 0.0, 0.0
+    B.hc_kv_write(k, v, B.KVCache("int4", *cache.tensors[:2], torch.arange(2, dtype=torch.int32, device="cuda")[None],
+                                  k_scale=cache.tensors[3], v_scale=cache.tensors[4], k_bias=cache.tensors[5], v_bias=cache.tensors[6],
+                                  group=64), zeros())
+    q = torch.full((batch, 1, heads * g, d), 0.125, dtype=torch.bfloat16, device="cuda")
+    out, lse = B.hc_tree_attention(q, cache, zeros(batch) + (n - 1), scale=0.125)
+    small, large = n - 16, 16
+    mass = small * np.exp(-17.625)
+    z = large + mass
+    want, reach = mass / z, 0.125 * 0.125 * 17.625 * d
+    delta = (d + 8) * U32 * reach
+    tol = (1.5 * U16 + 4 * delta + 64 * U32) * want + U16 * want + U32 + 2.0 ** -31 * small / z
+    assert float(np.abs(R.f64(out) - want).max()) <= tol, (float(out.min()), float(out.max()), want, tol)
+    assert float(np.abs(R.f64(lse) - np.log(z)).max()) <= 2 * delta + 64 * U32 * (1 + np.log(z))
     assert B.device_status() == B.TS_OK
