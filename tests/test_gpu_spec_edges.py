@@ -1,5 +1,6 @@
-"""GPU tests of the speculative decoding step's operators at the ends of their ranges. Tolerances are
-test_gpu_spec's, with what a test adds to them derived beside it."""
+"""GPU tests of the speculative decoding step's operators at the ends of their ranges: the largest finite
+values, logits without a distribution, refused paths, very small weights, and the sizes at which a kernel
+takes another path. Tolerances are test_gpu_spec's, with what a test adds to them derived beside it."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +8,7 @@ import torch
 import spec_reference as R
 from gpu_common import require_gpu
 from hyper_connection_residual_call_gb300 import binding as B
-from test_gpu_spec import TREE, U16, U32, gen, make_cache, randn
+from test_gpu_spec import TREE, U16, U32, check_verify, gen, make_cache, randn, random_tree, run_attention, verify_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -224,4 +225,41 @@ def test_int4_weights_far_below_the_largest(heads, g, batch):
     tol = (1.5 * U16 + 4 * delta + 64 * U32) * want + U16 * want + U32 + 2.0 ** -31 * small / z
     assert float(np.abs(R.f64(out) - want).max()) <= tol, (float(out.min()), float(out.max()), want, tol)
     assert float(np.abs(R.f64(lse) - np.log(z)).max()) <= 2 * delta + 64 * U32 * (1 + np.log(z))
+    assert B.device_status() == B.TS_OK
+
+
+# ------------------------------------------------------------------ other paths of the kernels
+
+@pytest.mark.parametrize("kind,group", [("bf16", 0), ("fp8", 0), ("int4", 64)])
+@pytest.mark.parametrize("page", [128, 256, 1024])
+@pytest.mark.parametrize("d,hq,t", [(64, 4, 2), (128, 4, 12), (128, 8, 12), (128, 8, 24), (256, 2, 5)])
+def test_attention_large_pages(kind, group, page, d, hq, t):
+    """Pages of a tile's keys and more: lengths around a page's end, a page that ends inside a tile's rows."""
+    run_attention(45, kind, group, d, hq, 1, page, [0, page - 1, page, page + 3, 1500], t, [random_tree(np.random.default_rng(t), t)] * 5)
+
+
+@pytest.mark.parametrize("kind,group", [("bf16", 0), ("fp8", 0), ("int4", 32)])
+@pytest.mark.parametrize("d,hq,hk,t", [(128, 1, 1, 65), (128, 1, 1, 100), (64, 2, 1, 97), (128, 2, 1, 130), (256, 1, 1, 70)])
+def test_attention_masks_of_many_words(kind, group, d, hq, hk, t):
+    """Mask rows of three to five words, in blocks of 64, 128 and 256 rows; nodes that reach over several tiles."""
+    rng = np.random.default_rng(t)
+    run_attention(46, kind, group, d, hq, hk, 16, [0, 1, 127, 350], t, [random_tree(rng, t) for _ in range(4)])
+
+
+@pytest.mark.parametrize("kind,group", [("bf16", 0), ("fp8", 0), ("int4", 64)])
+@pytest.mark.parametrize("hq,t", [(1, 140), (2, 300)])
+def test_attention_of_a_prompt(kind, group, hq, t):
+    """A chain of several tiles of nodes."""
+    run_attention(47, kind, group, 128, hq, 1, 64, [0, 77], t)
+
+
+@pytest.mark.parametrize("t,v,tree", [(1024, 60, True), (1025, 60, False), (1500, 300, True), (4096, 20, True)])
+def test_verify_many_nodes(t, v, tree):
+    """More nodes than a block keeps in shared memory."""
+    args = verify_inputs(t, 2, t, v, tree, [0.9, 0.0], agree=0.3)
+    logits, tokens, parents, temp, draft, u, noise = (torch.from_numpy(x).cuda() for x in args)
+    check_verify(args, B.hc_verify(logits, tokens, parents, temp, draft_probs=draft, u=u, noise=noise))
+    if not tree:
+        check_verify(args, B.hc_verify(logits, tokens, None, temp, draft_probs=draft, u=u, noise=noise), chain=True)
+    check_verify(args, B.hc_verify(logits, tokens, parents), greedy=True)
     assert B.device_status() == B.TS_OK
