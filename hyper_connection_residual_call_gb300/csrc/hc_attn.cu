@@ -23,13 +23,15 @@
 //   q . k = sum_groups scale (sum Q (q + 16)) + (bias - 16 scale) sum Q
 // An INT4 value becomes q * scale + bias in fp16.
 //
-// What it measures: 32 chains of 8 tokens x 4 heads over up to 6000 bf16 keys of 8 heads,
-// 110 us for 0.6 GB, 0.80 of the measured copy rate (some 100 of them this kernel at 74% of
-// DRAM's peak, the rest the join). 2 x 12 rows over 131072 keys of 8 heads: INT4 94 us for
-// 0.23 GB, bound by its instructions, some 490 for a warp's 16 keys at 59% of the issue
-// slots (of them 110 that turn codes into operands, 32 products); FP8 97 us for 0.41 GB,
-// likewise. One token of 20 heads over 1000 keys: 12 us, two launches and some six
-// dependent loads.
+// What it measures (GPU times of a call, the join included, replayed back to back in a CUDA
+// graph): 32 chains of 8 tokens x 4 heads over up to 6000 bf16 keys of 8 heads,
+// 110 us for 0.6 GB, 0.80 of the measured copy rate (some 100 of them this kernel at 76% of
+// DRAM's peak, the rest the join); 4 x 16 rows of 256 elements over up to 32768 keys 133 us for
+// 0.8 GB. 2 x 12 rows over 131072 keys of 8 heads: INT4 94 us for
+// 0.23 GB, bound by its instructions, some 490 for a warp's 16 keys at 61% of the issue
+// slots (of them 110 that turn codes into operands, 32 products); FP8 98 us for 0.41 GB,
+// likewise (64% of the issue slots). One token of 20 heads over 1000 keys: 10 to 11 us, two
+// launches and some six dependent loads.
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -225,8 +227,8 @@ __device__ __forceinline__ int value_element(int j, int g)
 }
 
 // kGroup: an INT4 group's elements. It is known when compiled, so that a group's sum begins
-// without zeros and ends without a branch (2 x 12 rows over 131072 keys: 98 us, with a
-// variable 111).
+// without zeros and ends without a branch (2 x 12 rows over 131072 keys: 98 us when it was
+// taken, with a variable 111).
 template <int kType, int D, int MT, int kGroup>
 struct Walk {
     using F = Format<kType, D>;

@@ -2,11 +2,12 @@
 // over the CTAs, where partial results lie, and which nodes a row sees.
 //
 // An item is one (sequence, key head, block of rows): its keys in tiles, all
-// with the same softmax rows. The items' tiles form one line, in the order
-// sequence, head, row block, tile, and CTA c of G takes the tiles
-// its N/G tiles of it: every CTA has the same number of tiles (to
-// one) whatever the sequences' lengths are, and a long context is split over
-// as many CTAs as it takes. An item that lies within one CTA is written to the
+// with the same softmax rows. The items' tiles form one line of N, in the order
+// sequence, head, row block, tile, which is cut into one run for each of G CTAs: the
+// first N mod G of them take N / G + 1 tiles and the others N / G (Cut::first is where
+// CTA c's run begins, Cut::cta_of whose run holds a tile). So every CTA has the same
+// number of tiles, to one, whatever the sequences' lengths are, and a long context is
+// split over as many CTAs as it takes. An item that lies within one CTA is written to the
 // output by it; the segments of the others go to the workspace, at most two
 // for a CTA (its first and its last item), and a second kernel joins them in
 // CTA order, so the result does not depend on timing.

@@ -23,8 +23,9 @@
 //   - a reduction has one cluster barrier: each warp leaves its result, and every warp
 //     of the cluster reads all of them through distributed shared memory and joins them
 //     in the same order, so that every CTA takes the same decisions.
-// A chain of 5 nodes over 32768 words: 18 us, a node some 3 us. 16 trees of 26 nodes over
-// 128001 words: 49 us, where the walks' 25 MB would take 4: the longest walk's passes, one
+// GPU times of calls replayed back to back in a CUDA graph: a chain of 5 nodes over 32768
+// words 18 us, a node some 3 us (greedy 15). 16 trees of 26 nodes over 128001 words: 49 to 52 us,
+// where the walks' 25 MB would take 4 (greedy 30, and 1.2): the longest walk's passes, one
 // after the other, each a round of loads, the sums and an exchange between the CTAs.
 #include <algorithm>
 

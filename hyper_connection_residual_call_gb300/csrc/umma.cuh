@@ -52,11 +52,7 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N)
 // The same with fp16 A and B.
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) { return umma_idesc_bf16(M, N) & ~(1u << 7 | 1u << 10); }
 
-// Descriptors of an MN-major tile, 128-byte swizzle: rows of K hold 64 elements
-// (128 bytes) of M or N, 8 rows an atom (1024 bytes), atoms along K 1024 bytes
-// apart (the stride byte offset); the next 64 elements of M or N lie the leading
-// byte offset on. The same bytes as a K-major tile of the transposed matrix.
-// The high words of the two kinds of descriptor, and the low word of either for an
+// The high word of a descriptor, of a K-major or an MN-major tile, and the low word for an
 // address (leading byte offset `lead`): a descriptor for an address `n` bytes on has
 // n / 16 added to the low word.
 constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
@@ -112,7 +108,10 @@ __device__ __forceinline__ void umma_e4m3_lo(uint32_t d_tmem, uint32_t a_lo, uin
         : "memory");
 }
 
-// Instruction descriptor bit: B is MN-major.
+// Instruction descriptor bit: B is MN-major. Such a tile with the 128-byte swizzle has rows
+// of K that hold 64 elements (128 bytes) of N, 8 rows an atom (1024 bytes), atoms along K
+// 1024 bytes apart (the stride byte offset); the next 64 elements of N lie the leading byte
+// offset on. They are the same bytes as a K-major tile's of the transposed matrix.
 constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
 // ---- TMEM ------------------------------------------------------------------

@@ -448,7 +448,8 @@ typedef enum {
     TS_ROPE_NTK = 2,          /* theta replaced by theta * factor^(rot/(rot-2)) */
     TS_ROPE_BY_PARTS = 3      /* f_i / factor where f_i turns fewer than beta_slow times in
                                  original_positions, f_i where more than beta_fast times, a
-                                 linear blend of the two between */
+                                 blend of the two between, linear in the number of turns (not, as
+                                 some programs have it, in i between two rounded indices) */
 } ts_rope_scaling_type;
 
 typedef struct {
@@ -583,7 +584,11 @@ ts_status ts_hc_tree_build(const int32_t *parents, long parents_stride, const in
  * The products run on the tensor cores in bf16 (an INT4 row's values, and their weights, in fp16: a weight is
  * off by 2^-11 of itself or 2^-31 of the row's largest) with fp32 sums; the softmax's maximum and sum are fp32. Over FP8 rows of 128 elements, 33 to 64 rows a key head
  * (T * q_heads/n_kv_heads) meet the keys as two e4m3 parts each, which leaves an element of q off by at
- * most 2^-17.8 of its row's largest. T <= 4096, T * q_heads/n_kv_heads <= 32768.
+ * most 2^-17.8 of its row's largest. Weights times values are added up in fp32 before they are divided by the
+ * weights' sum, a weight being up to 2^8 times the one that a row's sum is kept relative to: values beyond
+ * 2^119 / (the keys that a row sees) can overflow to an infinity, and below 2^-100 they lose bits. A length
+ * out of the page table's range is taken as the nearest one in it (recorded).
+ * T <= 4096, T * q_heads/n_kv_heads <= 32768.
  */
 size_t ts_hc_tree_attention_workspace_bytes(int B, int T, int q_heads, const ts_hc_kv_cache *cache);
 ts_status ts_hc_tree_attention(const void *q, long q_stride, const ts_hc_kv_cache *cache, const int32_t *ctx_len,
