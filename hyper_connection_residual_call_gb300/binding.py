@@ -982,7 +982,8 @@ def hc_kv_read(cache: KVCache, start, n: int, *, k_out=None, v_out=None, stream=
 
 def hc_kv_compact(cache: KVCache, ctx_len, path, n_accepted, *, new_len=None, stream=None):
     """Moves the accepted nodes' rows (``path`` int32 [B, T] and ``n_accepted`` int32 [B] of ``hc_verify``)
-    to the positions after ``ctx_len``; returns new_len int32 [B] = ctx_len + n_accepted + 1."""
+    to the positions after ``ctx_len``; returns new_len int32 [B] = ctx_len + n_accepted + 1. A path that is
+    refused at a step (recorded, see ``device_status``) counts the steps before it."""
     torch = _torch()
     cp = _is(ctx_len, "ctx_len", torch.int32, cache.lengths)
     np_ = _is(n_accepted, "n_accepted", torch.int32, cache.lengths)
@@ -1076,7 +1077,8 @@ def hc_verify(logits, tokens, parents=None, temperature=None, *, draft_probs=Non
     """Which of the drafted ``tokens`` int32 [B, T] hold, given the target's ``logits`` fp32 [B, T, V] and the
     draft's ``draft_probs`` fp32 [B, T, V]; ``parents`` int32 [B, T], [T] or None (a chain); ``temperature``
     fp32 [B]; ``u`` fp32 [B, T] in [0, 1) and ``noise`` fp32 [B, V] exponential variates. Without draft_probs, u
-    and noise every sequence is greedy. Returns (n_accepted [B], path [B, T], next_token [B]), int32."""
+    and noise every sequence is greedy. Returns (n_accepted [B], path [B, T], next_token [B]), int32. A walk
+    ends, with next token 0, at logits that are no distribution (recorded, see ``device_status``)."""
     torch = _torch()
     i32, f32 = torch.int32, torch.float32
     lp = _is(logits, "logits", f32)
