@@ -179,12 +179,13 @@ constexpr float kFp16Lift = 6.f;
 // the rows' maxima (in units of log2) and sums.
 __host__ __device__ __forceinline__ size_t attn_slot_floats(int rows, int D) { return (size_t)rows * (D + 2); }
 
-// Whether node row t sees position ctx + i (i >= 0).
+// Whether node row t sees position ctx + i (i >= 0). (From L2: an ordinary load here, where it hardly ever
+// runs, changes what the compiler makes of the few-row kernel's loop, 94 us to 96 for 2 x 12 rows over 131072 INT4 keys.)
 __device__ __forceinline__ bool attn_sees(const AttnParams &p, const uint32_t *mask_row, int t, int i)
 {
     if (i >= p.T)
         return false;
-    return p.mask ? ((__ldg(mask_row + (i >> 5)) >> (i & 31)) & 1u) != 0 : i <= t;
+    return p.mask ? ((__ldcg(mask_row + (i >> 5)) >> (i & 31)) & 1u) != 0 : i <= t;
 }
 
 __device__ __forceinline__ const uint32_t *attn_mask_row(const AttnParams &p, int b, int t)
@@ -229,7 +230,9 @@ static __device__ __forceinline__ float attn_wild_values(const AttnParams &p, in
 }
 
 // Which of the 32 positions ctx + n0 .. ctx + n0 + 31 node row t sees (n0 may be
-// negative: the context), bit i for ctx + n0 + i.
+// negative: the context), bit i for ctx + n0 + i. The mask may have been written while this kernel was
+// already launched and waiting, so its words are not loaded as read-only data. (Past L1 the softmax
+// waits longer for them: 32 x 160 rows over 300 keys of 64, 45 us and 47.)
 static __device__ __forceinline__ uint32_t attn_sees32(const AttnParams &p, const uint32_t *mask_row, int t, int n0, const SeqLen &seq)
 {
     const auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
@@ -237,7 +240,7 @@ static __device__ __forceinline__ uint32_t attn_sees32(const AttnParams &p, cons
     if (!p.mask)
         return low(t + 1 - n0) & present;
     const int w = n0 >> 5;
-    const auto word = [&](int i) { return i < 0 ? 0xFFFFFFFFu : i < p.mask_words ? __ldg(mask_row + i) & low(p.T - 32 * i) : 0u; };
+    const auto word = [&](int i) { return i < 0 ? 0xFFFFFFFFu : i < p.mask_words ? mask_row[i] & low(p.T - 32 * i) : 0u; };
     return __funnelshift_r(word(w), word(w + 1), n0 & 31) & present;
 }
 

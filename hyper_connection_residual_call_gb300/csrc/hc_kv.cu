@@ -51,7 +51,7 @@ struct RowAt {
         row = 0;
         if (!valid)
             return;
-        const int start = __ldg(p.start + b);
+        const int start = p.start[b];
         const long pos = (long)start + t;
         const long page = start < 0 ? -1 : kv_page(p.c, (int)b, pos);
         placed = page >= 0;

@@ -14,7 +14,9 @@ namespace tshc {
 constexpr int kKvBf16 = 0, kKvFp8 = 1, kKvInt4 = 2;  // ts_kvtype
 constexpr unsigned kStatusBadArg = 1u;               // TS_ERR_INVALID_ARG of ts_hc.h
 
-// Page of position pos of sequence b, or -1 (out of the table, or not a page).
+// Page of position pos of sequence b, or -1 (out of the table, or not a page). Only the page table is loaded
+// as read-only data: no kernel of the library writes it, and one that does launches no dependent before it ends.
+// (Ordinary loads are not moved ahead of the waits: 4 x 64 rows over 65536 FP8 keys 108 us, 119 with them.)
 __device__ __forceinline__ long kv_page(const KvView &c, int b, long pos)
 {
     const long i = pos >> c.page_shift;

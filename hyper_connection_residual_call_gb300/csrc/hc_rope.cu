@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kRopeThreads) hc_rope_kernel(const RopeParams 
         const float4 *t = reinterpret_cast<const float4 *>(p.table + (size_t)(ok ? pos : 0) * p.rot);  // two pairs each
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float4 w = __ldg(t + (kInterleaved ? (j < 2 ? 2 * v0 + j : 2 * v1 + j - 2) : 4 * u + j));
+            float4 w = t[kInterleaved ? (j < 2 ? 2 * v0 + j : 2 * v1 + j - 2) : 4 * u + j];
             if (!ok)
                 w = make_float4(0.f, 0.f, 0.f, 0.f);
             if (p.inverse) {

@@ -263,3 +263,54 @@ def test_verify_many_nodes(t, v, tree):
         check_verify(args, B.hc_verify(logits, tokens, None, temp, draft_probs=draft, u=u, noise=noise), chain=True)
     check_verify(args, B.hc_verify(logits, tokens, parents), greedy=True)
     assert B.device_status() == B.TS_OK
+
+
+# ------------------------------------------------------------------ dependent launches
+
+@pytest.mark.parametrize("kind,hq", [("bf16", 2), ("fp8", 4), ("int4", 8), ("bf16", 16)])
+def test_steps_back_to_back_read_what_the_step_before_wrote(kind, hq):
+    """Steps whose masks, positions, lengths, rows and table lie in the same buffers and change each time, with
+    nothing between the launches, against the same steps with the GPU waited for after each call."""
+    g = gen(48)
+    b, t, hk, d, steps = 3, 12, 1, 128, 40
+    rng = np.random.default_rng(48)
+    parents = torch.tensor(np.array([[random_tree(rng, t) for _ in range(b)] for _ in range(steps)]), dtype=torch.int32, device="cuda")
+    q, k, v = randn(g, steps, b, t, hq, d), randn(g, steps, b, t, hk, d), randn(g, steps, b, t, hk, d)
+    path = torch.full((b, t), -1, dtype=torch.int32, device="cuda")
+    path[:, :3] = torch.tensor([0, 2, 5], dtype=torch.int32)
+    count = torch.tensor([2, 1, 0], dtype=torch.int32, device="cuda")
+
+    def run(wait):
+        after = torch.cuda.synchronize if wait else lambda: None
+        cache = make_cache(gen(49), kind, b, 4 * steps + t, hk, 16, d, 64)
+        lens = [zeros(b), zeros(b)]
+        mask, pos = torch.zeros(b, t, 1, dtype=torch.int32, device="cuda"), torch.zeros(b, t, dtype=torch.int32, device="cuda")
+        table = torch.zeros(4 * steps + 2 * t, d // 2, 2, device="cuda")
+        qo, ko = torch.empty_like(q[0]), torch.empty_like(k[0])
+        outs = torch.empty(steps, b, t, hq, d, dtype=torch.bfloat16, device="cuda")
+        ws = B.tree_attention_workspace(b, t, hq, cache)
+        lse = torch.empty(b, t, hq, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(steps):
+            now, then = lens[i % 2], lens[(i + 1) % 2]
+            assert B.ts_hc_rope_table(table.data_ptr(), table.shape[0], d, 1000.0 + i, None, torch.cuda.current_stream().cuda_stream) == B.TS_OK
+            after()
+            B.hc_tree_build(parents[i], now, mask=mask, positions=pos)
+            after()
+            B.hc_rope(q[i], k[i], pos.view(-1), table, q_out=qo, k_out=ko)
+            after()
+            B.hc_kv_write(ko, v[i], cache, now)
+            after()
+            B.hc_tree_attention(qo, cache, now, mask=mask, out=outs[i], lse=lse, ws=ws)
+            after()
+            B.hc_kv_compact(cache, now, path, count, new_len=then)
+            after()
+        torch.cuda.synchronize()
+        return outs, lens[steps % 2].clone()
+
+    want, want_len = run(True)
+    assert want_len.tolist() == [3 * steps, 2 * steps, steps]
+    for _ in range(5):
+        got, got_len = run(False)
+        assert torch.equal(got, want) and torch.equal(got_len, want_len)
+    assert B.device_status() == B.TS_OK
