@@ -25,12 +25,12 @@
 //
 // What it measures (GPU times of a call, the join included, replayed back to back in a CUDA
 // graph): 32 chains of 8 tokens x 4 heads over up to 6000 bf16 keys of 8 heads,
-// 110 us for 0.6 GB, 0.80 of the measured copy rate (some 100 of them this kernel at 76% of
+// 110 us for 0.6 GB, 0.80 of the measured copy rate (some 100 of them this kernel at 75% of
 // DRAM's peak, the rest the join); 4 x 16 rows of 256 elements over up to 32768 keys 133 us for
 // 0.8 GB. 2 x 12 rows over 131072 keys of 8 heads: INT4 94 us for
 // 0.23 GB, bound by its instructions, some 490 for a warp's 16 keys at 61% of the issue
 // slots (of them 110 that turn codes into operands, 32 products); FP8 98 us for 0.41 GB,
-// likewise (64% of the issue slots). One token of 20 heads over 1000 keys: 10 to 11 us, two
+// likewise (65% of the issue slots). One token of 20 heads over 1000 keys: 10 to 11 us, two
 // launches and some six dependent loads.
 #include <algorithm>
 #include <map>

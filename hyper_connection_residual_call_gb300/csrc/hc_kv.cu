@@ -210,7 +210,7 @@ __device__ __forceinline__ void write_row(const KvView &c, const RowAt<kLanes> &
 // write and 32 to read, 0.2 GB each, 0.96 of the measured copy rate, with the arithmetic
 // pipe busy 63% and 37% of the time; bf16 both ways 86 us for 0.54 GB, 0.92. INT4 in
 // groups of 64, both ways: 102 us for 0.34 GB (63 and 41 alone), of them 51 its bytes': 3.2 of
-// 4 instructions a cycle and the arithmetic pipe busy 69% to write, 2.7 and 70% to read. A step's
+// 4 instructions a cycle and the arithmetic pipe busy 68% to write, 2.7 and 70% to read. A step's
 // rows (8 x 13 tokens of 4 heads, both ways) take 8.3 us: two launches and their chains
 // of lengths, pages and rows.
 template <int kType, int kLanes>
