@@ -29,6 +29,7 @@ TS_OK, TS_ERR_INVALID_ARG, TS_ERR_UNSUPPORTED, TS_ERR_CUDA, TS_ERR_WORKSPACE, TS
 TS_W_BF16, TS_W_INT4_AFFINE = 0, 1
 TS_KV_BF16, TS_KV_FP8, TS_KV_INT4 = range(3)
 TS_ROPE_PLAIN, TS_ROPE_LINEAR, TS_ROPE_NTK, TS_ROPE_BY_PARTS = range(4)
+TS_LOGITS_FP32, TS_LOGITS_BF16 = range(2)
 RMS_EPS = 1e-6  # families/qwen4/mod.rs, RMS_EPS
 
 EXPORTS = ("ts_hc_workspace_bytes", "ts_hc_workspace_layout", "ts_hc_call", "ts_hc_inject_add",
@@ -38,7 +39,8 @@ EXPORTS = ("ts_hc_workspace_bytes", "ts_hc_workspace_layout", "ts_hc_call", "ts_
            "ts_hc_device_status", "ts_hc_call_noalloc", "ts_hc_stack_workspace_bytes", "ts_hc_stack",
            "ts_hc_stack_ple_workspace_bytes", "ts_hc_stack_ple", "ts_hc_selftest_timeout",
            "ts_hc_rope_table", "ts_hc_rope", "ts_hc_kv_write", "ts_hc_kv_read", "ts_hc_kv_compact", "ts_hc_tree_build",
-           "ts_hc_tree_attention_workspace_bytes", "ts_hc_tree_attention", "ts_hc_verify")
+           "ts_hc_tree_attention_workspace_bytes", "ts_hc_tree_attention", "ts_hc_verify",
+           "ts_hc_qk_norm_rope", "ts_hc_delta_step", "ts_hc_logprobs")
 TS_HC_STATIC_SCRATCH_BYTES = 64 * 1024 * 1024  # include/ts_hc.h
 
 
@@ -191,6 +193,12 @@ def library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.ts_hc_tree_attention.restype = i
         lib.ts_hc_verify.argtypes = [vp, vp, vp, vp, l, vp, vp, vp, vp, vp, vp, i, i, i, vp]
         lib.ts_hc_verify.restype = i
+        lib.ts_hc_qk_norm_rope.argtypes = [vp, l, vp, l, vp, vp, i, vp, vp, f, vp, l, vp, l, i, i, i, i, i, i, vp]
+        lib.ts_hc_qk_norm_rope.restype = i
+        lib.ts_hc_delta_step.argtypes = [vp, l, vp, l, vp, l, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, f, vp]
+        lib.ts_hc_delta_step.restype = i
+        lib.ts_hc_logprobs.argtypes = [vp, i, l, vp, vp, vp, vp, vp, i, i, i, i, vp]
+        lib.ts_hc_logprobs.restype = i
         lib.ts_hc_selftest_timeout.argtypes = [vp]
         lib.ts_hc_selftest_timeout.restype = i
         lib.ts_hc_last_error.argtypes = []
@@ -360,6 +368,23 @@ def ts_hc_verify(logits, draft_probs, tokens, parents, parents_stride, temperatu
                  next_token, B, T, V, stream) -> int:
     return library().ts_hc_verify(logits, draft_probs, tokens, parents, parents_stride, temperature, u, noise, n_accepted,
                                   path, next_token, B, T, V, stream)
+
+
+def ts_hc_qk_norm_rope(q, q_stride, k, k_stride, positions, table, max_pos, q_norm_w, k_norm_w, eps, q_out, q_out_stride, k_out,
+                       k_out_stride, N, q_heads, k_heads, D, rot, interleaved, stream) -> int:
+    return library().ts_hc_qk_norm_rope(q, q_stride, k, k_stride, positions, table, max_pos, q_norm_w, k_norm_w, eps, q_out,
+                                        q_out_stride, k_out, k_out_stride, N, q_heads, k_heads, D, rot, interleaved, stream)
+
+
+def ts_hc_delta_step(q, q_stride, k, k_stride, v, v_stride, decay, beta, counts, state_in, state_out, out, B, T, k_heads, v_heads,
+                     D, scale, norm_eps, stream) -> int:
+    return library().ts_hc_delta_step(q, q_stride, k, k_stride, v, v_stride, decay, beta, counts, state_in, state_out, out, B, T,
+                                      k_heads, v_heads, D, scale, norm_eps, stream)
+
+
+def ts_hc_logprobs(logits, logits_type, logits_stride, tokens, logp, entropy, top_ids, top_logp, N, V, J, top, stream) -> int:
+    return library().ts_hc_logprobs(logits, logits_type, logits_stride, tokens, logp, entropy, top_ids, top_logp, N, V, J, top,
+                                    stream)
 
 
 def ts_hc_selftest_timeout(stream) -> int:
@@ -1110,3 +1135,145 @@ def hc_verify(logits, tokens, parents=None, temperature=None, *, draft_probs=Non
     if st:
         _check(st)
     return n_accepted, path, next_token
+
+
+def _together(stream, first, **tensors):
+    """The handle of the stream to use, with every tensor on ``first``'s device and that device current: the
+    library launches on the current device."""
+    torch = _torch()
+    dev = first.device
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise HCError(TS_ERR_INVALID_ARG, f"{name} is on {t.device}, expected {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise HCError(TS_ERR_INVALID_ARG, f"the tensors are on {dev}, the current device is {torch.cuda.current_device()}")
+    return _stream_of(stream, first)
+
+
+def _out(t, name, dtype, shape, like, stream):
+    """``t``, or a new tensor where it is None."""
+    if t is None:
+        return _made(_torch().empty(shape, dtype=dtype, device=like.device), stream)
+    _is(t, name, dtype, shape)
+    return t
+
+
+def hc_qk_norm_rope(q, k, positions, table, q_weight, k_weight=None, *, eps: float = RMS_EPS, interleaved: bool = False, q_out=None,
+                    k_out=None, stream=None):
+    """The norms of the heads of ``q`` [N, q_heads, D] and ``k`` [N, k_heads, D] (or [B, T, heads, D]; k may be
+    None) bf16, with the heads' shared weights ``q_weight`` and ``k_weight`` bf16 [D], and their rotary positions
+    as ``hc_rope`` gives them, in one pass. Returns (q_out, k_out); passing q and k as them works in place."""
+    torch = _torch()
+    n, hq, d, sq = _rows(q, "q")
+    q_out = _made(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream) if q_out is None else q_out
+    no, ho, do, so = _rows(q_out, "q_out")
+    if (no, ho, do) != (n, hq, d):
+        raise HCError(TS_ERR_INVALID_ARG, f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+    hk, sk, sko, kp, kop, kwp = 0, 0, 0, None, None, None
+    if k is not None:
+        nk, hk, dk, sk = _rows(k, "k")
+        if nk != n or dk != d:
+            raise HCError(TS_ERR_INVALID_ARG, f"k has shape {tuple(k.shape)}, q has {tuple(q.shape)}")
+        k_out = _made(torch.empty(k.shape, dtype=torch.bfloat16, device=q.device), stream) if k_out is None else k_out
+        no, ho, do, sko = _rows(k_out, "k_out")
+        if (no, ho, do) != (n, hk, d):
+            raise HCError(TS_ERR_INVALID_ARG, f"k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
+        kp, kop, kwp = k.data_ptr(), k_out.data_ptr(), _is(k_weight, "k_weight", torch.bfloat16, (d,))
+    pp = _is(positions, "positions", torch.int32)
+    if positions.numel() != n:
+        raise HCError(TS_ERR_INVALID_ARG, f"positions has {positions.numel()} entries for {n} tokens")
+    tp = _is(table, "table", torch.float32)
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2:
+        raise HCError(TS_ERR_INVALID_ARG, f"table has shape {tuple(shape)}, expected [max_pos, rot/2, 2]")
+    handle = _together(stream, q, k=k, positions=positions, table=table, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
+    st = (_lib or library()).ts_hc_qk_norm_rope(q.data_ptr(), sq, kp, sk, pp, tp, shape[0], _is(q_weight, "q_weight", torch.bfloat16, (d,)),
+                                                kwp, eps, q_out.data_ptr(), so, kop, sko, n, hq, hk, d, 2 * shape[1], interleaved, handle)
+    if st:
+        _check(st)
+    return q_out, k_out
+
+
+def _delta_rows(q, k, v, decay, beta, dims):
+    """(tokens, key heads, value heads, D, strides) of a delta rule's inputs, ``dims`` dimensions each."""
+    f32 = _torch().float32
+    n, hk, d, sq = _rows(q, "q")
+    nk, hk2, dk, sk = _rows(k, "k")
+    nv, hv, dv, sv = _rows(v, "v")
+    if q.dim() != dims or k.shape != q.shape:
+        raise HCError(TS_ERR_INVALID_ARG, f"q and k have shapes {tuple(q.shape)} and {tuple(k.shape)}, expected {dims} dimensions of the same")
+    if v.dim() != dims or v.shape[:-2] != q.shape[:-2] or dv != d:
+        raise HCError(TS_ERR_INVALID_ARG, f"v has shape {tuple(v.shape)}, q has {tuple(q.shape)}")
+    _is(decay, "decay", f32, v.shape[:-1])
+    _is(beta, "beta", f32, v.shape[:-1])
+    return n, hk, hv, d, sq, sk, sv
+
+
+def hc_delta_step(q, k, v, decay, beta, state, *, counts=None, scale: Optional[float] = None, norm_eps: Optional[float] = RMS_EPS,
+                  out=None, state_out=None, stream=None):
+    """The gated delta rule for ``q``, ``k`` [B, T, k_heads, D] and ``v`` [B, T, v_heads, D] bf16, ``decay`` (its
+    logarithm) and ``beta`` fp32 [B, T, v_heads], from ``state`` fp32 [B, v_heads, D, D], token by token;
+    ``counts`` int32 [B]: how many of its tokens a sequence takes. ``norm_eps``: q and k are divided by the root
+    of their squares' sum and it, None: they are taken as they are. ``scale`` defaults to D ** -0.5. Returns (out
+    bf16 [B, T, v_heads, D], state_out); ``state_out`` defaults to ``state``, which is updated in place."""
+    torch = _torch()
+    _, hk, hv, d, sq, sk, sv = _delta_rows(q, k, v, decay, beta, 4)
+    b, t = q.shape[:2]
+    shape = (b, hv, d, d)
+    ip = _is(state, "state", torch.float32, shape)
+    state_out = state if state_out is None else state_out
+    op = _is(state_out, "state_out", torch.float32, shape)
+    cp = None if counts is None else _is(counts, "counts", torch.int32, (b,))
+    out = _out(out, "out", torch.bfloat16, v.shape, q, stream)
+    handle = _together(stream, q, k=k, v=v, decay=decay, beta=beta, state=state, state_out=state_out, counts=counts, out=out)
+    st = (_lib or library()).ts_hc_delta_step(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, decay.data_ptr(), beta.data_ptr(), cp,
+                                              ip, op, out.data_ptr(), b, t, hk, hv, d, d ** -0.5 if scale is None else scale,
+                                              -1.0 if norm_eps is None else norm_eps, handle)
+    if st:
+        _check(st)
+    return out, state_out
+
+
+def hc_logprobs(logits, tokens=None, *, top: int = 0, entropy=None, logp=None, top_ids=None, top_logp=None, stream=None):
+    """Log probabilities under ``logits`` [N, V] (or [B, T, V]) fp32 or bf16, whose rows lie side by side or at one
+    stride: of ``tokens`` int32 [N, J] ([B, T, J]; a negative one is none), the entropies, and the ``top`` most
+    probable tokens of each row with theirs, the lowest index first of equal ones. Returns (logp fp32 [.., J],
+    entropy fp32 [..], top_ids int32 [.., top], top_logp fp32 [.., top]), with None where tokens is None or top 0."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise HCError(TS_ERR_INVALID_ARG, "logits must be a CUDA tensor")
+    if logits.dtype not in (f32, torch.bfloat16):
+        raise HCError(TS_ERR_INVALID_ARG, f"logits must be {f32} or {torch.bfloat16}, got {logits.dtype}")
+    if logits.dim() not in (2, 3):
+        raise HCError(TS_ERR_INVALID_ARG, f"logits has shape {tuple(logits.shape)}, expected [N, V] or [B, T, V]")
+    lead, v, stride = tuple(logits.shape[:-1]), logits.shape[-1], logits.stride()
+    n = 1
+    for x in lead:
+        n *= x
+    step = stride[-2] if lead[-1] != 1 else stride[0]
+    if (stride[-1] != 1 and v > 1) or (len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and stride[0] != lead[1] * step):
+        raise HCError(TS_ERR_INVALID_ARG, f"logits: its rows are not at one stride: {tuple(stride)}")
+    j, tp = 0, None
+    if tokens is not None:
+        if tokens.dim() != len(lead) + 1 or tuple(tokens.shape[:-1]) != lead:
+            raise HCError(TS_ERR_INVALID_ARG, f"tokens has shape {tuple(tokens.shape)}, expected {lead + ('J',)}")
+        j = tokens.shape[-1]
+        tp = _is(tokens, "tokens", i32)
+        logp = _out(logp, "logp", f32, lead + (j,), logits, stream)
+    else:
+        logp = None
+    entropy = _out(entropy, "entropy", f32, lead, logits, stream)
+    if top > 0:
+        top_ids = _out(top_ids, "top_ids", i32, lead + (top,), logits, stream)
+        top_logp = _out(top_logp, "top_logp", f32, lead + (top,), logits, stream)
+    else:
+        top_ids = top_logp = None
+    handle = _together(stream, logits, tokens=tokens, logp=logp, entropy=entropy, top_ids=top_ids, top_logp=top_logp)
+    st = (_lib or library()).ts_hc_logprobs(logits.data_ptr(), TS_LOGITS_BF16 if logits.dtype is torch.bfloat16 else TS_LOGITS_FP32,
+                                            step if n > 1 else v, tp, None if logp is None else logp.data_ptr(), entropy.data_ptr(),
+                                            None if top_ids is None else top_ids.data_ptr(), None if top_logp is None else top_logp.data_ptr(),
+                                            n, v, j, top, handle)
+    if st:
+        _check(st)
+    return logp, entropy, top_ids, top_logp

@@ -1,0 +1,46 @@
+// hc_prompt.h -- launch parameters and launchers of the operators of a prompt's
+// pass and of the token after it: head norms with rotary positions, attention
+// over packed prompts, the gated delta rule, log probabilities (internal; the
+// public ABI is include/ts_hc.h).
+#pragma once
+
+#include "hc_spec.h"
+
+namespace tshc {
+
+struct NormRopeParams {
+    RopeParams r;
+    const uint16_t *qw, *kw;  // [D]
+    float eps;
+};
+
+struct DeltaStepParams {
+    const uint16_t *q, *k, *v;
+    long q_stride, k_stride, v_stride;
+    const float *decay, *beta;  // [B*T][Hv]
+    const int32_t *counts;      // or nullptr: T
+    const float *state_in;      // [B][Hv][D][D]
+    float *state_out;
+    uint16_t *out;              // [B*T][Hv][D]
+    int B, T, Hk, Hv, D;
+    float scale, norm_eps;      // norm_eps < 0: q and k as they are
+    unsigned *status;
+};
+
+struct LogprobParams {
+    const void *logits;
+    long stride;              // elements between rows
+    const int32_t *tokens;    // [N][J] or nullptr
+    float *logp;              // [N][J]
+    float *entropy;           // [N] or nullptr
+    int32_t *top_ids;         // [N][top]
+    float *top_logp;
+    int N, V, J, top;
+    unsigned *status;
+};
+
+cudaError_t launch_qk_norm_rope(const NormRopeParams &p, const LaunchCfg &cfg, cudaStream_t stream);
+cudaError_t launch_delta_step(const DeltaStepParams &p, const LaunchCfg &cfg, cudaStream_t stream);
+cudaError_t launch_logprobs(const LogprobParams &p, bool bf16, const LaunchCfg &cfg, cudaStream_t stream);
+
+}  // namespace tshc

@@ -6,42 +6,27 @@
 
 #include "hc_spec.h"
 #include "ts_hc.h"
-#include "ts_hc_internal.h"
+#include "ts_hc_checks.h"
 
 namespace {
 
 using tshc::api_error;
+using tshc::check_count;
 using tshc::check_ptr_api;
-
-#define TS_TRY(expr)                      \
-    do {                                  \
-        const ts_status st_ = (expr);     \
-        if (st_ != TS_OK)                 \
-            return st_;                   \
-    } while (0)
+using tshc::check_stride;
+using tshc::device;
+using tshc::kMaxBatch;
+using tshc::kMaxHeads;
+using tshc::launched;
+using tshc::overlap;
+using tshc::rows_overlap;
 
 constexpr int kMaxNodes = 4096;
-constexpr int kMaxHeads = 1024;
-constexpr int kMaxBatch = 65535;
-
-ts_status check_count(int v, const char *name, int lo, int hi)
-{
-    if (v < lo || v > hi)
-        return api_error(TS_ERR_INVALID_ARG, "%s = %d must be in [%d, %d]", name, v, lo, hi);
-    return TS_OK;
-}
 
 ts_status check_batch(int B, int T)
 {
     TS_TRY(check_count(B, "B", 0, kMaxBatch));
     return check_count(T, "T", 0, kMaxNodes);
-}
-
-ts_status check_stride(long stride, const char *name, long least, long multiple)
-{
-    if (stride < least || stride % multiple != 0)
-        return api_error(TS_ERR_INVALID_ARG, "%s = %ld must be a multiple of %ld and >= %ld", name, stride, multiple, least);
-    return TS_OK;
 }
 
 ts_status check_tree_stride(long stride, int T)
@@ -107,14 +92,6 @@ tshc::KvView view(const ts_hc_kv_cache *c)
     return v;
 }
 
-ts_status device(tshc::LaunchCfg *cfg, unsigned **status)
-{
-    cfg->pdl = true;
-    return tshc::device_api(&cfg->sm_count, status);
-}
-
-ts_status launched(cudaError_t e, const char *what) { return e == cudaSuccess ? TS_OK : tshc::cuda_error(e, what); }
-
 // Rows of the cache that one call moves, one thread for 16 elements: 32-bit indices.
 ts_status check_rows(long B, long T, const ts_hc_kv_cache *c)
 {
@@ -122,27 +99,6 @@ ts_status check_rows(long B, long T, const ts_hc_kv_cache *c)
         return api_error(TS_ERR_UNSUPPORTED, "%ld tokens of %d heads are too many for one call: split them", B * T,
                          (int)c->n_kv_heads);
     return TS_OK;
-}
-
-// Whether [a, a + na) and [b, b + nb) (bytes) share one.
-bool overlap(const void *a, size_t na, const void *b, size_t nb)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-// Whether n rows of wa 16-bit elements at a + i*sa and n rows of wb at b + i*sb
-// share one. Exact for equal strides (slices of one projection's output are
-// disjoint), by the address ranges otherwise.
-bool rows_overlap(const void *a, long sa, long wa, const void *b, long sb, long wb, int n)
-{
-    if (!overlap(a, 2 * ((size_t)(n - 1) * sa + wa), b, 2 * ((size_t)(n - 1) * sb + wb)))
-        return false;
-    const intptr_t bytes = reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a);
-    if (sa != sb || bytes % 2 != 0)
-        return true;
-    const long m = ((long)(bytes / 2) % sa + sa) % sa;
-    return !(m >= wa && m + wb <= sa);
 }
 
 }  // namespace

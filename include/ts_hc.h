@@ -624,6 +624,76 @@ ts_status ts_hc_verify(const float *logits, const float *draft_probs, const int3
                        const float *noise, int32_t *n_accepted, int32_t *path, int32_t *next_token, int B, int T,
                        int V, cudaStream_t stream);
 
+/* ---- a prompt's pass and the token after it: head norms, packed prompts, the delta rule, log probabilities ----
+ *
+ * What a decoder's sublayers need for prompts of different lengths packed one behind the other, and for the
+ * tokens that follow them. N packed tokens are S sequences: sequence s has the tokens starts[s] ..
+ * starts[s+1] - 1, with starts int32 [S+1] ascending from 0 on the device; tokens from starts[S] on belong to
+ * none, and their rows of an output are left as they were. What the host cannot check of starts the kernels do:
+ * a sequence that begins before token 0, ends before it begins or reaches past N is taken as empty and
+ * TS_ERR_INVALID_ARG is recorded in the device status word. Sequences of no tokens are fine.
+ */
+
+/*
+ * The norms of N tokens' query and key heads and their rotary positions, one launch: each head's row x of D
+ * elements becomes n_i = x_i w_i / sqrt(mean_j x_j^2 + eps) (w the heads' shared weights, applied as they are),
+ * which is turned as in ts_hc_rope; elements rot .. D-1 are normed only. fp32 arithmetic, rounded to bf16 once.
+ * A row whose sum of squares passes fp32's range comes out as zeros.
+ *   q_norm_w, k_norm_w   bf16 [D], 16-byte aligned (k_norm_w NULL with k_heads == 0)
+ *   eps                  > 0
+ * Other arguments as for ts_hc_rope (no inverse). A position out of range leaves zeros in the turned elements
+ * and is recorded.
+ */
+ts_status ts_hc_qk_norm_rope(const void *q, long q_stride, const void *k, long k_stride, const int32_t *positions,
+                             const float *table, int max_pos, const void *q_norm_w, const void *k_norm_w, float eps,
+                             void *q_out, long q_out_stride, void *k_out, long k_out_stride, int N, int q_heads,
+                             int k_heads, int D, int rot, int interleaved, cudaStream_t stream);
+
+/*
+ * The gated delta rule (families/qwen4/mod.rs, the GDN sublayer's recurrence) for T tokens of B sequences, one
+ * token after the other. A value head h has a state S, D x D, and key head h / (v_heads/k_heads); per token
+ *     S <- e^decay S;  u = beta (v - S^T k);  S <- S + k u^T;  out = scale S^T q
+ * with q and k divided by sqrt(sum of their squares + norm_eps) first where norm_eps >= 0 (norm_eps < 0: as they
+ * are). fp32 arithmetic; out is rounded to bf16 once.
+ *   q, k       bf16: head h of token t of sequence b at q + (b*T + t)*q_stride + h*D, k_heads of them; v likewise,
+ *              v_heads; strides in elements, multiples of 8; 16-byte aligned
+ *   decay      fp32 [B*T][v_heads], the logarithm of a token's decay (0 or less, -infinity for none kept);
+ *              beta fp32 [B*T][v_heads]
+ *   counts     int32 [B] or NULL (T each): a sequence takes its first counts[b] tokens; the rows of out after
+ *              them stay as they were. A count out of [0, T] is taken as the nearest one in it (recorded)
+ *   state_in   fp32 [B][v_heads][D][D], key element major, 16-byte aligned; state_out likewise, which may be
+ *              state_in. (A step whose tokens may yet be refused writes its states elsewhere, and is run again
+ *              from state_in with the counts that held.)
+ *   out        bf16 [B*T][v_heads][D]
+ * D is 64 or 128 (TS_ERR_UNSUPPORTED otherwise); v_heads is a multiple of k_heads; T <= 4096.
+ */
+ts_status ts_hc_delta_step(const void *q, long q_stride, const void *k, long k_stride, const void *v, long v_stride,
+                           const float *decay, const float *beta, const int32_t *counts, const float *state_in,
+                           float *state_out, void *out, int B, int T, int k_heads, int v_heads, int D, float scale,
+                           float norm_eps, cudaStream_t stream);
+
+typedef enum {
+    TS_LOGITS_FP32 = 0,       /* as ts_hc_exit_logits writes them */
+    TS_LOGITS_BF16 = 1
+} ts_logits_type;
+
+/*
+ * Log probabilities under N rows of logits: of J given tokens a row, the distribution's entropy, and its `top`
+ * most probable tokens with theirs, from one pass over the logits.
+ *   logits     [N][V] of logits_type, rows logits_stride >= V elements apart
+ *   tokens     int32 [N][J] (NULL with J == 0); logp fp32 [N][J]: log softmax(row)[token]. A negative token is
+ *              none, and its entry 0; one from V on gives a NaN and is recorded
+ *   entropy    fp32 [N] or NULL: -sum_v p_v log p_v (natural logarithms)
+ *   top_ids    int32 [N][top] and top_logp fp32 [N][top], best first; of equal logits the lowest index first.
+ *              Not used with top == 0; top <= 32 and top <= V
+ * Sums are fp32. A logit of -infinity is a probability of 0. A row that is no distribution (a NaN or a +infinity
+ * in it, or nothing but -infinity) gives NaNs, and -1 as ids, and is recorded.
+ * Outputs must not overlap the inputs or one another. V < 2^30.
+ */
+ts_status ts_hc_logprobs(const void *logits, int logits_type, long logits_stride, const int32_t *tokens, float *logp,
+                         float *entropy, int32_t *top_ids, float *top_logp, int N, int V, int J, int top,
+                         cudaStream_t stream);
+
 /*
  * Self-test of the failure path. Launches one thread that waits, with the same
  * bounded wait the kernels use for their asynchronous copies, on a
