@@ -1137,23 +1137,23 @@ def hc_verify(logits, tokens, parents=None, temperature=None, *, draft_probs=Non
     return n_accepted, path, next_token
 
 
-def _together(stream, first, **tensors):
-    """The handle of the stream to use, with every tensor on ``first``'s device and that device current: the
-    library launches on the current device."""
-    torch = _torch()
-    dev = first.device
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise HCError(TS_ERR_INVALID_ARG, f"{name} is on {t.device}, expected {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise HCError(TS_ERR_INVALID_ARG, f"the tensors are on {dev}, the current device is {torch.cuda.current_device()}")
-    return _stream_of(stream, first)
+def _together(stream, *tensors) -> int:
+    """The handle of the stream to use. All tensors (None left out) lie on one device, and it is the current one:
+    the library launches there."""
+    dev = _torch()._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise HCError(TS_ERR_INVALID_ARG, f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    return _stream_of(stream, tensors[0])
 
 
 def _out(t, name, dtype, shape, like, stream):
     """``t``, or a new tensor where it is None."""
     if t is None:
-        return _made(_torch().empty(shape, dtype=dtype, device=like.device), stream)
+        t = _torch().empty(shape, dtype=dtype, device=like.device)
+        if stream is not None:
+            t.record_stream(stream)
+        return t
     _is(t, name, dtype, shape)
     return t
 
@@ -1186,7 +1186,7 @@ def hc_qk_norm_rope(q, k, positions, table, q_weight, k_weight=None, *, eps: flo
     shape = table.shape
     if len(shape) != 3 or shape[2] != 2:
         raise HCError(TS_ERR_INVALID_ARG, f"table has shape {tuple(shape)}, expected [max_pos, rot/2, 2]")
-    handle = _together(stream, q, k=k, positions=positions, table=table, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
+    handle = _together(stream, q, k, positions, table, q_weight, k_weight, q_out, k_out)
     st = (_lib or library()).ts_hc_qk_norm_rope(q.data_ptr(), sq, kp, sk, pp, tp, shape[0], _is(q_weight, "q_weight", torch.bfloat16, (d,)),
                                                 kwp, eps, q_out.data_ptr(), so, kop, sko, n, hq, hk, d, 2 * shape[1], interleaved, handle)
     if st:
@@ -1225,7 +1225,7 @@ def hc_delta_step(q, k, v, decay, beta, state, *, counts=None, scale: Optional[f
     op = _is(state_out, "state_out", torch.float32, shape)
     cp = None if counts is None else _is(counts, "counts", torch.int32, (b,))
     out = _out(out, "out", torch.bfloat16, v.shape, q, stream)
-    handle = _together(stream, q, k=k, v=v, decay=decay, beta=beta, state=state, state_out=state_out, counts=counts, out=out)
+    handle = _together(stream, q, k, v, decay, beta, state, state_out, counts, out)
     st = (_lib or library()).ts_hc_delta_step(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, decay.data_ptr(), beta.data_ptr(), cp,
                                               ip, op, out.data_ptr(), b, t, hk, hv, d, d ** -0.5 if scale is None else scale,
                                               -1.0 if norm_eps is None else norm_eps, handle)
@@ -1269,7 +1269,7 @@ def hc_logprobs(logits, tokens=None, *, top: int = 0, entropy=None, logp=None, t
         top_logp = _out(top_logp, "top_logp", f32, lead + (top,), logits, stream)
     else:
         top_ids = top_logp = None
-    handle = _together(stream, logits, tokens=tokens, logp=logp, entropy=entropy, top_ids=top_ids, top_logp=top_logp)
+    handle = _together(stream, logits, tokens, logp, entropy, top_ids, top_logp)
     st = (_lib or library()).ts_hc_logprobs(logits.data_ptr(), TS_LOGITS_BF16 if logits.dtype is torch.bfloat16 else TS_LOGITS_FP32,
                                             step if n > 1 else v, tp, None if logp is None else logp.data_ptr(), entropy.data_ptr(),
                                             None if top_ids is None else top_ids.data_ptr(), None if top_logp is None else top_logp.data_ptr(),

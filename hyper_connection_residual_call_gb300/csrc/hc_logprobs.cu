@@ -10,46 +10,60 @@
 // The best alternatives come from the same pass. An element is a 64-bit key, its
 // value in an order that unsigned comparison keeps above its index's complement, so
 // that keys are distinct and the larger key is the larger value or, of equal ones,
-// the lower index. A chunk of 8192 elements lies in the block's registers, and a
-// threshold, which n elements are known to reach, says which of them are kept in
-// shared memory: the n-th largest of the maxima of 128 groups of a chunk's elements
-// is such a threshold, and at most n groups hold an element that reaches it. So what
-// is kept is bounded for any logits, and the few hundred keys that a vocabulary leaves
-// are ranked by counting, for each, the larger ones.
+// the lower index. The n-th largest of the maxima of 120 groups of a row's first
+// 7680 elements is a threshold that n elements reach; what passes it goes to shared
+// memory (some 20 elements of each further 7680), and is ranked at the row's end by
+// counting, for each key, the larger ones. Rows in whose order too many pass it, a
+// rising one say, are read a second time, with a threshold a chunk: at most n groups
+// hold an element that reaches one, which bounds what is kept for any logits.
 #include <algorithm>
+#include <type_traits>
 
 #include "hc_prompt.h"
-#include "ptx.cuh"
+#include "hc_attn.cuh"
+#include "umma.cuh"
 
 namespace tshc {
 
 namespace {
 
 constexpr unsigned kStatusInvalidArg = 1u;  // TS_ERR_INVALID_ARG of ts_hc.h
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 480, kWarps = kThreads / 32;  // that take the elements; one more warp asks for copies
+constexpr int kBlock = kThreads + 32;
 constexpr int kHold = 16;                    // elements of a chunk that a thread holds
 constexpr int kGroups = kThreads / 4;        // of four threads each
 constexpr int kMaxTop = 32;
-constexpr int kDirect = 128;                 // threads that may keep elements without a new threshold
-constexpr int kKeep = 4096;                  // keys kept; a chunk adds at most kMaxTop * 4 * kHold = kDirect * kHold
-constexpr int kFew = 1024;                   // keys that a compaction leaves, at most kMaxTop * 4 * (kKeep / kThreads)
-static_assert(kMaxTop * 4 * kHold <= kKeep / 2 && kDirect * kHold <= kKeep / 2, "a chunk's keys");
-static_assert(kMaxTop * 4 * (kKeep / kThreads) <= kFew, "what a compaction leaves");
+constexpr int kKeep = 4096;                  // keys kept; a chunk's threshold leaves at most kMaxTop * 4 * kHold of it
+constexpr int kRank = 64;                    // keys that are ranked without a threshold first
+constexpr int kEach = (kKeep + kThreads - 1) / kThreads;  // kept keys of a thread
+constexpr int kFew = 1184;                   // keys that a compaction leaves, at most kMaxTop * 4 * kEach
+static_assert(kMaxTop * 4 * kHold <= kKeep / 2, "a chunk's keys");
+static_assert(kMaxTop * 4 * kEach <= kFew, "what a compaction leaves");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLeast = -200.f;           // of d: 2^d is 0 from -127 on, and d 2^d no NaN
 constexpr float kNaN = __builtin_nanf("");
-
-__device__ __forceinline__ float ex2f(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ float max_nan(float a, float b)
 {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
+}
+
+// mbar_wait_bounded, for warps that have nothing else to do: each attempt may take a microsecond of the
+// hardware's own waiting, so that the others have the issue slots.
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(smem_addr(bar)), "r"(parity), "r"(1000u) : "memory");
+        if (done)
+            return true;
+        if (global_timer_ns() - t0 > kWaitLimitNs)
+            return false;
+    }
 }
 
 // A value's and index's key, and back.
@@ -67,17 +81,25 @@ __device__ __forceinline__ float key_value(uint64_t k)
 
 __device__ __forceinline__ uint32_t key_index(uint64_t k) { return 0xFFFFFFFFu - (uint32_t)k; }
 
-// A distribution's part: its largest logit, and Z and S (in log2 units) relative to it.
+// A distribution's part: its largest logit m, and Z = sum 2^d and S = sum d 2^d over d = (x - m) log2 e.
 struct Part {
     float m, z, s;
 };
 
-__device__ __forceinline__ Part join(Part a, Part b)
+// The parts of a warp's lanes.
+__device__ __forceinline__ Part join_warp(Part a)
 {
-    const float m = fmaxf(a.m, b.m), ref = m == -INFINITY ? 0.f : m;
-    const float da = max_nan((a.m - ref) * kLog2e, -200.f), db = max_nan((b.m - ref) * kLog2e, -200.f);
-    const float fa = ex2f(da), fb = ex2f(db);
-    return Part{m, a.z * fa + b.z * fb, fa * fmaf(da, a.z, a.s) + fb * fmaf(db, b.z, b.s)};
+    const uint32_t u = __float_as_uint(a.m);
+    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u));
+    const float m = __uint_as_float((most & 0x80000000u) ? most ^ 0x80000000u : ~most);
+    const float d = max_nan((a.m - (m == -INFINITY ? 0.f : m)) * kLog2e, kLeast), f = ex2(d);
+    float z = a.z * f, s = f * fmaf(d, a.z, a.s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    }
+    return Part{m, z, s};
 }
 
 struct Shared {
@@ -87,10 +109,14 @@ struct Shared {
     uint64_t top[kMaxTop];   // this block's, best first; a block of a cluster reads the others'
     uint64_t all[8 * kMaxTop];
     uint64_t threshold;
-    Part part[kWarps];
+    Part part[2][kWarps];    // by rows in turn
     Part whole;
-    int kept, left;
+    uint64_t full[4], empty[4];
+    int kept, left, dead;
 };
+
+// A barrier of the threads that take the elements.
+__device__ __forceinline__ void sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 // The n-th largest of the groups' largest keys (0 if fewer than n groups have one).
 __device__ __forceinline__ uint64_t threshold_of(uint64_t best, int n, Shared &sh)
@@ -102,7 +128,7 @@ __device__ __forceinline__ uint64_t threshold_of(uint64_t best, int n, Shared &s
         sh.group[tid >> 2] = best;
     if (tid == 0)
         sh.threshold = 0;
-    __syncthreads();
+    sync();
     if (tid < kGroups) {
         const uint64_t mine = sh.group[tid];
         int larger = 0;
@@ -112,7 +138,7 @@ __device__ __forceinline__ uint64_t threshold_of(uint64_t best, int n, Shared &s
         if (larger == n - 1 && mine != 0)  // keys are distinct
             sh.threshold = mine;
     }
-    __syncthreads();
+    sync();
     return sh.threshold;
 }
 
@@ -120,256 +146,408 @@ __device__ __forceinline__ uint64_t threshold_of(uint64_t best, int n, Shared &s
 __device__ __forceinline__ void compact(int n, Shared &sh)
 {
     const int tid = threadIdx.x, kept = sh.kept;
-    uint64_t best = 0, k[kKeep / kThreads];
-#pragma unroll
-    for (int i = 0; i < kKeep / kThreads; ++i) {
-        k[i] = i * kThreads + tid < kept ? sh.keep[i * kThreads + tid] : 0;
-        best = max(best, k[i]);
-    }
-    if (tid == 0)
-        sh.left = 0;
+    int left = kept;
+    const uint64_t *from = sh.keep;
     if (tid < kMaxTop)
         sh.top[tid] = 0;
-    const uint64_t least = threshold_of(best, n, sh);
+    if (kept > kRank) {  // what cannot be among the n best goes first
+        uint64_t best = 0, k[kEach];
 #pragma unroll
-    for (int i = 0; i < kKeep / kThreads; ++i)
-        if (k[i] != 0 && k[i] >= least)
-            sh.few[atomicAdd(&sh.left, 1)] = k[i];
-    __syncthreads();
-    const int left = sh.left;
+        for (int i = 0; i < kEach; ++i) {
+            k[i] = i * kThreads + tid < kept ? sh.keep[i * kThreads + tid] : 0;
+            best = max(best, k[i]);
+        }
+        if (tid == 0)
+            sh.left = 0;
+        const uint64_t least = threshold_of(best, n, sh);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (k[i] != 0 && k[i] >= least)
+                sh.few[atomicAdd(&sh.left, 1)] = k[i];
+        sync();
+        left = sh.left;
+        from = sh.few;
+    } else {
+        sync();
+    }
     for (int i = tid; i < left; i += kThreads) {
-        const uint64_t mine = sh.few[i];
+        const uint64_t mine = from[i];
         int larger = 0;
 #pragma unroll 4
         for (int j = 0; j < left; ++j)
-            larger += sh.few[j] > mine;
+            larger += from[j] > mine;
         if (larger < n)
             sh.top[larger] = mine;
     }
-    __syncthreads();
+    sync();
     if (tid < n)
         sh.keep[tid] = sh.top[tid];
     if (tid == 0)
         sh.kept = min(left, n);
-    __syncthreads();
+    sync();
 }
 
-// Elements of a row as vectors of 16 bytes, the first and the last perhaps in part.
+// Elements of a row as vectors of 16 bytes, the ends perhaps in part. Vectors are copied to shared memory by the
+// chunk, but where the logits begin or end inside one: its elements are loaded one by one.
 template <bool kBf16>
 struct Row {
-    static constexpr int kPer = kBf16 ? 8 : 4;  // elements of a vector
-    const char *at;                             // a multiple of 16
-    int lead, V;                                // elements before the row's first, in the first vector
-    __device__ __forceinline__ void load(int vec, float (&x)[kPer]) const
+    static constexpr int kPer = kBf16 ? 8 : 4;             // elements of a vector
+    static constexpr int kVecs = kHold / kPer;             // a thread's of a chunk
+    static constexpr int kStep = kThreads * kVecs;         // a chunk's
+    static constexpr int kStages = kBf16 ? 4 : 2;          // chunks in shared memory: 64 KB of them
+    static constexpr int kRing = kStages * kStep * 16;
+    const char *base, *at;                                 // the row, and the multiple of 128 at or before it, so that copies
+                                                           // begin on whole lines
+    int lead, V;                                           // elements between them
+    int w0, w1;                                            // vectors that lie in the logits whole
+    int in0, in1;                                          // the block's whose elements are all the row's
+    int v0, v1, chunks;                                    // the block's vectors
+
+    __device__ __forceinline__ Row(const LogprobParams &p, long row, int rank, int ranks)
     {
-        const int first = vec * kPer - lead;
-        const char *src = at + (long)vec * 16;
-        if (first >= 0 && first + kPer <= V) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(src));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        base = static_cast<const char *>(p.logits) + row * p.stride * (kBf16 ? 2 : 4);
+        lead = (int)(reinterpret_cast<uintptr_t>(base) & 127) / (kBf16 ? 2 : 4);
+        at = base - lead * (kBf16 ? 2 : 4);
+        V = p.V;
+        const int vecs = (lead + V + kPer - 1) / kPer, per = (vecs + ranks - 1) / ranks;
+        v0 = rank * per;
+        v1 = min(vecs, v0 + per);
+        const char *first = static_cast<const char *>(p.logits), *last = first + ((p.N - 1) * p.stride + V) * (kBf16 ? 2 : 4);
+        w0 = at >= first ? 0 : (int)((first - at + 15) >> 4);
+        w1 = (int)min((long)vecs, (long)(last - at) >> 4);
+        in0 = (lead + kPer - 1) / kPer;
+        in1 = min(v1, (lead + V) / kPer);
+        chunks = v0 < v1 ? (v1 - v0 + kStep - 1) / kStep : 0;
+    }
+    __device__ __forceinline__ float logit(int i) const
+    {
+        return kBf16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(base)[i] << 16) : reinterpret_cast<const float *>(base)[i];
+    }
+    // Whether a vector can be read whole: in the row, or at its end with bytes of the rows beside it.
+    __device__ __forceinline__ bool whole(int vec) const { return vec >= w0 && vec < w1; }
+    // ... and, of one that can, the row's elements, the others -infinity
+    __device__ __forceinline__ uint4 trim(uint4 x, int vec) const
+    {
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (kBf16) {
-                    x[2 * i] = bf16_lo(u[i]);
-                    x[2 * i + 1] = bf16_hi(u[i]);
-                } else {
-                    x[i] = __uint_as_float(u[i]);
-                }
+        for (int i = 0; i < kPer; ++i)
+            if (!exists(vec, i)) {
+                if (kBf16)
+                    w[i / 2] = i & 1 ? (w[i / 2] & 0xFFFFu) | 0xFF800000u : (w[i / 2] & 0xFFFF0000u) | 0xFF80u;
+                else
+                    w[i & 3] = 0xFF800000u;
             }
-        } else {
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ uint4 none()
+    {
+        const uint32_t w = kBf16 ? 0xFF80FF80u : 0xFF800000u;  // -infinity
+        return make_uint4(w, w, w, w);
+    }
+    __device__ __forceinline__ uint4 part(int vec) const
+    {
+        uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                x[i] = -INFINITY;
-                if (first + i >= 0 && first + i < V)
-                    x[i] = kBf16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(src)[i] << 16)
-                                 : reinterpret_cast<const float *>(src)[i];
-            }
+        for (int i = 0; i < kPer; ++i) {
+            const int e = vec * kPer - lead + i;
+            const float x = e >= 0 && e < V ? logit(e) : -INFINITY;
+            if (kBf16)
+                w[i / 2] = i & 1 ? w[i / 2] | (__float_as_uint(x) & 0xFFFF0000u) : __float_as_uint(x) >> 16;
+            else
+                w[i & 3] = __float_as_uint(x);
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ bool exists(int vec, int c) const { return vec < v1 && vec * kPer + c >= lead && vec * kPer + c < lead + V; }
+    // the vectors of chunk c that can be read whole to `to`
+    __device__ __forceinline__ void copy(int c, uint8_t *to, uint64_t *bar) const
+    {
+        const int first = v0 + c * kStep;
+        const int lo = max(first, max(w0, lead / kPer)), hi = min(min(v1, first + kStep), w1);
+        const uint32_t bytes = lo < hi ? (uint32_t)(hi - lo) * 16 : 0;
+        mbar_arrive_expect_tx(bar, bytes);
+        if (bytes)
+            bulk_copy_g2s(to + (lo - first) * 16, at + (long)lo * 16, bytes, bar);
     }
 };
 
-// kRanks: CTAs of the cluster that shares a row.
-template <bool kBf16, int kRanks>
-__global__ void __launch_bounds__(kThreads, 2) hc_logprobs_kernel(const LogprobParams p)
+template <bool kBf16>
+__device__ __forceinline__ void unpack(uint4 w, float (&x)[kBf16 ? 8 : 4])
 {
-    constexpr int kPer = Row<kBf16>::kPer, kVecs = kHold / kPer;
-    __shared__ Shared sh;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = kRanks == 1 ? 0 : (int)cluster_rank();
-    const long row = blockIdx.x / kRanks;
-    const int n = p.top;
-    Row<kBf16> r;
-    const char *base = static_cast<const char *>(p.logits) + row * p.stride * (kBf16 ? 2 : 4);
-    r.lead = (int)(reinterpret_cast<uintptr_t>(base) & 15) / (kBf16 ? 2 : 4);
-    r.at = base - r.lead * (kBf16 ? 2 : 4);
-    r.V = p.V;
-    const int vecs = (r.lead + p.V + kPer - 1) / kPer, per = (vecs + kRanks - 1) / kRanks;
-    const int v0 = rank * per, v1 = min(vecs, v0 + per);
-
-    // a given token's logit is asked for before the pass
-    const bool asks = rank == 0 && tid < p.J;
-    int token = -1;
-    float given = 0.f;
-    const auto logit = [&](int t) {
-        return kBf16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(base)[t] << 16) : reinterpret_cast<const float *>(base)[t];
-    };
-    if (asks) {
-        token = p.tokens[row * p.J + tid];
-        if (token >= 0 && token < p.V)
-            given = logit(token);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if (kBf16) {
+            x[2 * c] = bf16_lo(u[c]);
+            x[2 * c + 1] = bf16_hi(u[c]);
+        } else {
+            x[c] = __uint_as_float(u[c]);
+        }
     }
+}
+
+// The first chunk's threshold, or any chunk's after it: keeps what reaches it among the thread's elements that
+// `in` names. Returns it (0: fewer than n groups have an element).
+template <typename R, typename In>
+__device__ __forceinline__ uint64_t keep_best(const float (&x)[R::kVecs][R::kPer], int first, int n, const In &in, Shared &sh)
+{
+    const auto key = [&](int i, int c) { return key_of(x[i][c], (uint32_t)(first + i * kThreads * R::kPer + c)); };
+    uint64_t best = 0;
+#pragma unroll
+    for (int i = 0; i < R::kVecs; ++i)
+#pragma unroll
+        for (int c = 0; c < R::kPer; ++c)
+            if (in(i, c))
+                best = max(best, key(i, c));
+    const uint64_t least = threshold_of(best, n, sh);
+    if (best != 0 && best >= least) {
+#pragma unroll
+        for (int i = 0; i < R::kVecs; ++i)
+#pragma unroll
+            for (int c = 0; c < R::kPer; ++c)
+                if (in(i, c)) {
+                    const uint64_t k = key(i, c);
+                    if (k >= least)
+                        sh.keep[atomicAdd(&sh.kept, 1)] = k;
+                }
+    }
+    return least;
+}
+
+// The n best of the block's part of a row in bounded space, for rows whose order let too many elements pass the
+// first chunk's threshold: each chunk has a threshold of its own, and the kept keys are ranked in between.
+template <typename R>
+__device__ __noinline__ void keep_again(const LogprobParams &p, long row, int rank, int ranks, Shared &sh)
+{
+    const R r(p, row, rank, ranks);
+    const int tid = threadIdx.x, n = p.top;
+    float limit = -INFINITY;
+    bool has = false;
+    sync();             // everyone has seen that too many were kept
     if (tid == 0)
         sh.kept = 0;
+    for (int ch = 0; ch < r.chunks; ++ch) {
+        const int v = r.v0 + ch * R::kStep + tid;
+        float x[R::kVecs][R::kPer];
+#pragma unroll
+        for (int i = 0; i < R::kVecs; ++i) {
+            const int at = v + i * kThreads;
+            unpack<R::kPer == 8>(at >= r.v1 ? R::none() : r.whole(at) ? r.trim(*reinterpret_cast<const uint4 *>(r.at + (long)at * 16), at) : r.part(at), x[i]);
+        }
+        const uint64_t least = keep_best<R>(x, v * R::kPer - r.lead, n, [&](int i, int c) { return has ? x[i][c] > limit : r.exists(v + i * kThreads, c); }, sh);
+        if (least != 0) {
+            limit = key_value(least);
+            has = true;
+        }
+        sync();
+        if (sh.kept > kKeep / 2) {
+            compact(n, sh);
+            limit = key_value(sh.top[n - 1]);
+            has = true;
+        }
+    }
+    sync();
+}
 
-    float x[kVecs][kPer], m = -INFINITY;
-    float z[2] = {0.f, 0.f}, s[2] = {0.f, 0.f};
-    float limit = -INFINITY;     // values up to this one are not among the n best (once there is a threshold)
-    bool has = false;            // a threshold
-    const auto fetch = [&](int v, float(&y)[kVecs][kPer]) {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int at = v + i * kThreads + tid;
-            if (at < v1) {
-                r.load(at, y[i]);
-            } else {
-#pragma unroll
-                for (int c = 0; c < kPer; ++c)
-                    y[i][c] = -INFINITY;
-            }
+// kRanks: CTAs of the cluster that shares a row; kTop: alternatives are asked for. The grid takes rows in turn; the copies run ahead of the chunk at
+// hand, past the end of a row, so that a row's joins and lists do not stop them.
+template <bool kBf16, int kRanks, bool kTop>
+__global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobParams p)
+{
+    using R = Row<kBf16>;
+    constexpr int kPer = R::kPer, kVecs = R::kVecs, kStages = R::kStages;
+    extern __shared__ uint4 ring[];
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        sh.kept = 0;
+        sh.dead = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], kWarps);
         }
-    };
-    if (v0 < v1)
-        fetch(v0, x);
-#pragma unroll 1
-    for (int v = v0; v < v1; v += kVecs * kThreads) {
-        float next[kVecs][kPer];
-        const bool more = v + kVecs * kThreads < v1;
-        if (more)
-            fetch(v + kVecs * kThreads, next);
-        float top = x[0][0];
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-            for (int c = 0; c < kPer; ++c)
-                top = fmaxf(top, x[i][c]);
-        if (top > m) {
-            const float d = max_nan((m - top) * kLog2e, -200.f), f = ex2f(d);
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                s[a] = f * fmaf(d, z[a], s[a]);
-                z[a] *= f;
-            }
-            m = top;
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-            for (int c = 0; c < kPer; ++c) {
-                const float d = max_nan((x[i][c] - ref) * kLog2e, -200.f), e = ex2f(d);
-                z[c & 1] += e;
-                s[c & 1] = fmaf(d, e, s[c & 1]);
-            }
-        if (n > 0) {
-            const auto exists = [&](int i, int c) {
-                const int at = v + i * kThreads + tid, e = at * kPer + c - r.lead;
-                return at < v1 && e >= 0 && e < p.V;
-            };
-            const auto key = [&](int i, int c) { return key_of(x[i][c], (uint32_t)((v + i * kThreads + tid) * kPer + c - r.lead)); };
-            const bool some = !has || top > limit;
-            const int many = __syncthreads_count(some);
-            if (many > 0) {
-                uint64_t least = 0;
-                if (many > kDirect) {
-                    uint64_t best = 0;
-                    if (some) {
-#pragma unroll
-                        for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-                            for (int c = 0; c < kPer; ++c)
-                                if (exists(i, c) && (!has || x[i][c] > limit))
-                                    best = max(best, key(i, c));
-                    }
-                    least = threshold_of(best, n, sh);
+        mbar_fence_init();
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();
+    const int rank = kRanks == 1 ? 0 : (int)cluster_rank();
+    const int rows = gridDim.x / kRanks, n = kTop ? p.top : 0;  // rows of the grid at a time
+    const long row0 = blockIdx.x / kRanks;
+
+    if (warp == kWarps) {
+        if (lane == 0) {
+            unsigned asked = 0;
+            bool ok = true;
+            for (long row = row0; ok && row < p.N; row += rows) {
+                const R r(p, row, rank, kRanks);
+                for (int c = 0; ok && c < r.chunks; ++c, ++asked) {
+                    const unsigned stage = asked % kStages, use = asked / kStages;
+                    ok = use == 0 || mbar_wait_bounded(&sh.empty[stage], (use & 1) ^ 1);  // (else the waits for it run out and say so)
+                    if (ok)
+                        r.copy(c, reinterpret_cast<uint8_t *>(ring + stage * R::kStep), &sh.full[stage]);
                 }
-                if (some) {
+            }
+        }
+        if (kRanks > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
+    }
+
+    const int back = kThreads - 1 - tid;             // results are the last threads'
+    unsigned taken = 0;                              // chunks that came
+    int turn = 0;                                    // rows, in turn
+#pragma unroll 1
+    for (long row = row0; row < p.N; row += rows, turn ^= 1) {
+        const R r(p, row, rank, kRanks);
+        // a given token's logit is asked for before the pass
+        const bool asks = rank == 0 && back < p.J;
+        int token = -1;
+        float given = 0.f;
+        if (asks) {
+            token = p.tokens[row * p.J + back];
+            if (token >= 0 && token < p.V)
+                given = r.logit(token);
+        }
+        Part a{-INFINITY, 0.f, 0.f};                 // the thread's
+        float limit = -INFINITY;                     // values up to this one are not among the n best
+#pragma unroll 1
+        for (int ch = 0; ch < r.chunks; ++ch, ++taken) {
+            const int v = r.v0 + ch * R::kStep + tid, stage = (int)(taken % kStages);
+            const uint32_t phase = (taken / kStages) & 1;
+            if (kTop && (ch == 2 || ch == 5)) {
+                // The threads' maxima so far give a higher threshold (its elements come before this chunk's, so that
+                // of equal ones none is missed). 20 of 128001: some 100 are kept in all, 320 with the first alone.
+                const uint64_t least = threshold_of(key_of(a.m, tid), n, sh);
+                limit = fmaxf(limit, key_value(least));
+            }
+            if (!wait_bounded(&sh.full[stage], phase)) {
+                *reinterpret_cast<volatile int *>(&sh.dead) = 1;
+                if (p.status)
+                    atomicExch(p.status, kStatusTimeout);
+            }
+            float x[kVecs][kPer];
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int at = v + i * kThreads;
+                uint4 w = ring[stage * R::kStep + i * kThreads + tid];
+                if (at < r.in0 || at >= r.in1)  // an end of the row, or past it
+                    w = at >= r.v1 ? R::none() : r.whole(at) ? r.trim(w, at) : r.part(at);
+                unpack<kBf16>(w, x[i]);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.empty[stage]);
+            float top = x[0][0];
+            if (v - lane < r.v1) {  // the warp has some of the chunk
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c)
+                        top = fmaxf(top, x[i][c]);
+                if (top > a.m) {
+                    const float d = max_nan((a.m - top) * kLog2e, kLeast), f = ex2(d);
+                    a = Part{top, a.z * f, f * fmaf(d, a.z, a.s)};
+                }
+                // Two elements an instruction. A -infinity makes the chunk's S a NaN: it is taken again with d bounded.
+                const float ref = a.m == -INFINITY ? 0.f : a.m;
+                const auto add = [&](auto bounded) {
+                    const uint64_t by = f32x2(kLog2e, kLog2e), off = f32x2(-ref, -ref);
+                    uint64_t z = 0, s = 0;
+#pragma unroll
+                    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+                        for (int c = 0; c < kPer; c += 2) {
+                            uint64_t d = ffma2(fadd2(f32x2(x[i][c], x[i][c + 1]), off), by, 0x8000000080000000ull);  // (x - m) log2 e
+                            float y0, y1;
+                            f32x2_unpack(d, y0, y1);
+                            if (decltype(bounded)::value) {
+                                y0 = max_nan(y0, kLeast);
+                                y1 = max_nan(y1, kLeast);
+                                d = f32x2(y0, y1);
+                            }
+                            const uint64_t e = f32x2(ex2(y0), ex2(y1));
+                            z = fadd2(z, e);
+                            s = ffma2(d, e, s);
+                        }
+                    float z0, z1, s0, s1;
+                    f32x2_unpack(z, z0, z1);
+                    f32x2_unpack(s, s0, s1);
+                    s0 += s1;
+                    if (!decltype(bounded)::value && s0 != s0)
+                        return false;
+                    a.z += z0 + z1;
+                    a.s += s0;
+                    return true;
+                };
+                if (!add(std::false_type{}))
+                    add(std::true_type{});
+            }
+            if (!kTop)
+                continue;
+            const int first = v * kPer - r.lead;
+            if (ch == 0) {
+                const uint64_t least = keep_best<R>(x, first, n, [&](int i, int c) { return r.exists(v + i * kThreads, c); }, sh);
+                limit = least != 0 ? key_value(least) : INFINITY;  // (0: then there is no second chunk)
+            } else if (top > limit) {
+                // few have any: their elements' bits first, so that what follows runs once for each
+                uint32_t over = 0;
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c)
+                        over |= x[i][c] > limit ? 1u << (i * kPer + c) : 0u;
+                while (over) {
+                    const int bit = __ffs(over) - 1;
+                    over &= over - 1;
+                    float y = x[0][0];
 #pragma unroll
                     for (int i = 0; i < kVecs; ++i)
 #pragma unroll
                         for (int c = 0; c < kPer; ++c)
-                            if (exists(i, c) && (!has || x[i][c] > limit)) {
-                                const uint64_t k = key(i, c);
-                                if (k >= least)
-                                    sh.keep[atomicAdd(&sh.kept, 1)] = k;
-                            }
-                }
-                __syncthreads();
-                if (least != 0) {
-                    limit = key_value(least);
-                    has = true;
-                }
-                if (more && sh.kept > kKeep / 2) {
-                    compact(n, sh);
-                    if (sh.kept == n) {
-                        limit = key_value(sh.top[n - 1]);
-                        has = true;
-                    }
+                            y = bit == i * kPer + c ? x[i][c] : y;
+                    const int place = atomicAdd(&sh.kept, 1);
+                    if (place < kKeep)
+                        sh.keep[place] = key_of(y, (uint32_t)(first + bit / kPer * kThreads * kPer + bit % kPer));
                 }
             }
         }
-        if (more) {
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-                for (int c = 0; c < kPer; ++c)
-                    x[i][c] = next[i][c];
-        }
-    }
-    Part a{m, z[0] + z[1], s[0] + s[1]};
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        a = join(a, Part{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.z, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o)});
-    if (lane == 0)
-        sh.part[warp] = a;
-    __syncthreads();
-    if (n > 0)
-        compact(n, sh);
-    if (warp == 0) {
-        a = lane < kWarps ? sh.part[lane] : Part{-INFINITY, 0.f, 0.f};
-#pragma unroll
-        for (int o = kWarps / 2; o > 0; o >>= 1)
-            a = join(a, Part{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.z, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o)});
+        a = join_warp(a);
         if (lane == 0)
-            sh.whole = a;
-    }
-    if (kRanks > 1) {
-        cluster_sync();
-        if (rank == 0) {
-            if (warp == 0) {
+            sh.part[turn][warp] = a;
+        sync();
+        if (kTop) {
+            if (sh.kept > kKeep)
+                keep_again<R>(p, row, rank, kRanks, sh);
+            compact(n, sh);
+            if (tid == 0)
+                sh.kept = 0;
+        }
+        if (kRanks == 1 && back - 31 + lane >= max(p.J, max(n, 1)))
+            continue;                                // the warp has no results to write
+        a = lane < kWarps ? sh.part[turn][lane] : Part{-INFINITY, 0.f, 0.f};
+        a = join_warp(a);
+        if (kRanks > 1) {
+            if (tid == 0)
+                sh.whole = a;
+            cluster_sync();
+            if (rank == 0) {
                 a = Part{-INFINITY, 0.f, 0.f};
                 if (lane < kRanks) {
                     const uint32_t from = dsmem_addr(&sh.whole, lane);
                     a = Part{dsmem_ld_f32(from), dsmem_ld_f32(from + 4), dsmem_ld_f32(from + 8)};
                 }
-#pragma unroll
-                for (int o = kRanks / 2; o > 0; o >>= 1)
-                    a = join(a, Part{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.z, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o)});
-            } else if (warp <= n * kRanks / 32 + 1) {  // the ranks' lists, n keys each
-                const int i = tid - 32;
-                if (i < n * kRanks) {
-                    const uint32_t from = dsmem_addr(&sh.top[i % n], i / n);
-                    sh.all[i] = (uint64_t)__float_as_uint(dsmem_ld_f32(from + 4)) << 32 | __float_as_uint(dsmem_ld_f32(from));
+                a = join_warp(a);
+                if (kTop && tid < n * kRanks) {  // the ranks' lists, n keys each
+                    const uint32_t from = dsmem_addr(&sh.top[tid % max(n, 1)], tid / max(n, 1));
+                    sh.all[tid] = (uint64_t)__float_as_uint(dsmem_ld_f32(from + 4)) << 32 | __float_as_uint(dsmem_ld_f32(from));
                 }
             }
-        }
-        cluster_sync();  // the others' memory has been read
-        if (rank != 0)
-            return;
-        if (tid == 0)
-            sh.whole = a;
-        if (n > 0) {
+            cluster_sync();  // the others' memory has been read
+            if (rank != 0)
+                break;       // (a cluster has one row)
             if (tid < n * kRanks && sh.all[tid] != 0) {
                 const uint64_t mine = sh.all[tid];
                 int larger = 0;
@@ -378,40 +556,49 @@ __global__ void __launch_bounds__(kThreads, 2) hc_logprobs_kernel(const LogprobP
                 if (larger < n)
                     sh.top[larger] = mine;
             }
+            sync();
         }
-    }
-    __syncthreads();
-    a = sh.whole;
-    // a row with a NaN, with +infinity, or with nothing but -infinity is no distribution
-    const bool bad = !(a.m > -INFINITY && a.m < INFINITY) || !(a.z >= 0.f);
-    const float log_z = bad ? kNaN : logf(a.z);
-    bool wrong = bad;
-    if (asks) {
-        for (int j = tid; j < p.J; j += kThreads) {
-            if (j != tid) {
-                token = p.tokens[row * p.J + j];
-                if (token >= 0 && token < p.V)
-                    given = logit(token);
+        // a row with a NaN, with +infinity, or with nothing but -infinity is no distribution
+        const bool bad = !(a.m > -INFINITY && a.m < INFINITY) || !(a.z >= 0.f);
+        const float log_z = bad ? kNaN : logf(a.z);
+        bool wrong = bad;
+        if (asks) {
+            for (int j = back; j < p.J; j += kThreads) {
+                if (j != back) {
+                    token = p.tokens[row * p.J + j];
+                    if (token >= 0 && token < p.V)
+                        given = r.logit(token);
+                }
+                wrong |= token >= p.V;
+                p.logp[row * p.J + j] = token < 0 ? 0.f : token >= p.V ? kNaN : (given - a.m) - log_z;
             }
-            wrong |= token >= p.V;
-            p.logp[row * p.J + j] = token < 0 ? 0.f : token >= p.V ? kNaN : (given - a.m) - log_z;
         }
+        if (back == 0 && p.entropy)
+            p.entropy[row] = log_z - a.s * kLn2 / a.z;
+        if (back < n) {
+            const uint64_t k = sh.top[back];
+            p.top_ids[row * n + back] = bad ? -1 : (int)key_index(k);
+            p.top_logp[row * n + back] = (key_value(k) - a.m) - log_z;
+        }
+        if (wrong && p.status)
+            atomicExch(p.status, kStatusInvalidArg);
     }
-    if (tid == 0 && p.entropy)
-        p.entropy[row] = log_z - a.s * kLn2 / a.z;
-    if (tid < n) {
-        const uint64_t k = sh.top[tid];
-        p.top_ids[row * n + tid] = bad ? -1 : (int)key_index(k);
-        p.top_logp[row * n + tid] = (key_value(k) - a.m) - log_z;
+    if (*reinterpret_cast<volatile int *>(&sh.dead)) {  // a copy may still be in flight: give it time before the memory goes
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 50000000ull) {}
     }
-    if (wrong && p.status)
-        atomicExch(p.status, kStatusInvalidArg);
 }
 
 template <bool kBf16, int kRanks>
-cudaError_t launch(const LogprobParams &p, cudaStream_t stream)
+cudaError_t launch(const LogprobParams &p, const LaunchCfg &cfg, cudaStream_t stream)
 {
-    return launch_pdl(hc_logprobs_kernel<kBf16, kRanks>, dim3((unsigned)p.N * kRanks), dim3(kThreads), 0, true, stream, p, kRanks);
+    auto *kernel = p.top > 0 ? hc_logprobs_kernel<kBf16, kRanks, true> : hc_logprobs_kernel<kBf16, kRanks, false>;
+    int per_sm = 1;
+    const cudaError_t e = attn_ready(reinterpret_cast<const void *>(kernel), kBlock, Row<kBf16>::kRing, &per_sm);
+    if (e != cudaSuccess)
+        return e;
+    const int grid = kRanks > 1 ? p.N * kRanks : std::min(p.N, per_sm * cfg.sm_count);
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kBlock), Row<kBf16>::kRing, true, stream, p, kRanks);
 }
 
 template <bool kBf16>
@@ -422,10 +609,10 @@ cudaError_t launch_type(const LogprobParams &p, const LaunchCfg &cfg, cudaStream
     while (ranks < 8 && (long)p.N * ranks < cfg.sm_count && p.V / (ranks * 2) >= 2048)
         ranks *= 2;
     switch (ranks) {
-    case 1: return launch<kBf16, 1>(p, stream);
-    case 2: return launch<kBf16, 2>(p, stream);
-    case 4: return launch<kBf16, 4>(p, stream);
-    default: return launch<kBf16, 8>(p, stream);
+    case 1: return launch<kBf16, 1>(p, cfg, stream);
+    case 2: return launch<kBf16, 2>(p, cfg, stream);
+    case 4: return launch<kBf16, 4>(p, cfg, stream);
+    default: return launch<kBf16, 8>(p, cfg, stream);
     }
 }
 
