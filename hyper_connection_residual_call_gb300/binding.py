@@ -40,7 +40,7 @@ EXPORTS = ("ts_hc_workspace_bytes", "ts_hc_workspace_layout", "ts_hc_call", "ts_
            "ts_hc_stack_ple_workspace_bytes", "ts_hc_stack_ple", "ts_hc_selftest_timeout",
            "ts_hc_rope_table", "ts_hc_rope", "ts_hc_kv_write", "ts_hc_kv_read", "ts_hc_kv_compact", "ts_hc_tree_build",
            "ts_hc_tree_attention_workspace_bytes", "ts_hc_tree_attention", "ts_hc_verify",
-           "ts_hc_qk_norm_rope", "ts_hc_delta_step", "ts_hc_logprobs")
+           "ts_hc_qk_norm_rope", "ts_hc_prompt_attention", "ts_hc_delta_step", "ts_hc_logprobs")
 TS_HC_STATIC_SCRATCH_BYTES = 64 * 1024 * 1024  # include/ts_hc.h
 
 
@@ -195,6 +195,8 @@ def library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.ts_hc_verify.restype = i
         lib.ts_hc_qk_norm_rope.argtypes = [vp, l, vp, l, vp, vp, i, vp, vp, f, vp, l, vp, l, i, i, i, i, i, i, vp]
         lib.ts_hc_qk_norm_rope.restype = i
+        lib.ts_hc_prompt_attention.argtypes = [vp, l, vp, l, vp, l, vp, vp, vp, i, i, i, i, i, f, vp]
+        lib.ts_hc_prompt_attention.restype = i
         lib.ts_hc_delta_step.argtypes = [vp, l, vp, l, vp, l, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, f, vp]
         lib.ts_hc_delta_step.restype = i
         lib.ts_hc_logprobs.argtypes = [vp, i, l, vp, vp, vp, vp, vp, i, i, i, i, vp]
@@ -374,6 +376,11 @@ def ts_hc_qk_norm_rope(q, q_stride, k, k_stride, positions, table, max_pos, q_no
                        k_out_stride, N, q_heads, k_heads, D, rot, interleaved, stream) -> int:
     return library().ts_hc_qk_norm_rope(q, q_stride, k, k_stride, positions, table, max_pos, q_norm_w, k_norm_w, eps, q_out,
                                         q_out_stride, k_out, k_out_stride, N, q_heads, k_heads, D, rot, interleaved, stream)
+
+
+def ts_hc_prompt_attention(q, q_stride, k, k_stride, v, v_stride, starts, out, lse, N, S, q_heads, kv_heads, D, scale, stream) -> int:
+    return library().ts_hc_prompt_attention(q, q_stride, k, k_stride, v, v_stride, starts, out, lse, N, S, q_heads, kv_heads, D, scale,
+                                            stream)
 
 
 def ts_hc_delta_step(q, q_stride, k, k_stride, v, v_stride, decay, beta, counts, state_in, state_out, out, B, T, k_heads, v_heads,
@@ -1192,6 +1199,37 @@ def hc_qk_norm_rope(q, k, positions, table, q_weight, k_weight=None, *, eps: flo
     if st:
         _check(st)
     return q_out, k_out
+
+
+def _starts(starts):
+    """(address, sequences) of packed prompts' first rows, int32 [S + 1]."""
+    sp = _is(starts, "starts", _torch().int32)
+    if starts.dim() != 1 or starts.shape[0] < 1:
+        raise HCError(TS_ERR_INVALID_ARG, f"starts has shape {tuple(starts.shape)}, expected [S + 1]")
+    return sp, starts.shape[0] - 1
+
+
+def hc_prompt_attention(q, k, v, starts, *, scale: Optional[float] = None, out=None, lse=None, stream=None):
+    """Causal attention over packed prompts: ``q`` [N, q_heads, D], ``k`` and ``v`` [N, kv_heads, D] bf16, the
+    sequences' rows starts[s] .. starts[s+1] - 1 with ``starts`` int32 [S + 1]; rows from starts[S] on are left as
+    they were. ``scale`` defaults to D ** -0.5. Returns (out bf16 [N, q_heads, D], lse fp32 [N, q_heads])."""
+    torch = _torch()
+    n, hq, d, sq = _rows(q, "q")
+    nk, hk, dk, sk = _rows(k, "k")
+    nv, hv, dv, sv = _rows(v, "v")
+    if q.dim() != 3 or k.dim() != 3 or (nk, dk) != (n, d):
+        raise HCError(TS_ERR_INVALID_ARG, f"k has shape {tuple(k.shape)}, q has {tuple(q.shape)}, expected [N, heads, D]")
+    if v.dim() != 3 or (nv, hv, dv) != (n, hk, d):
+        raise HCError(TS_ERR_INVALID_ARG, f"v has shape {tuple(v.shape)}, k has {tuple(k.shape)}")
+    sp, s = _starts(starts)
+    out = _out(out, "out", torch.bfloat16, q.shape, q, stream)
+    lse = _out(lse, "lse", torch.float32, (n, hq), q, stream)
+    handle = _together(stream, q, k, v, starts, out, lse)
+    st = (_lib or library()).ts_hc_prompt_attention(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, sp, out.data_ptr(), lse.data_ptr(),
+                                                    n, s, hq, hk, d, d ** -0.5 if scale is None else scale, handle)
+    if st:
+        _check(st)
+    return out, lse
 
 
 def _delta_rows(q, k, v, decay, beta, dims):

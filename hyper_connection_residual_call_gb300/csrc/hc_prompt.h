@@ -14,6 +14,18 @@ struct NormRopeParams {
     float eps;
 };
 
+struct PromptAttnParams {
+    const uint16_t *v;        // for the values that a row's tile could not hold (infinities, NaNs)
+    long v_stride;
+    const int32_t *starts;    // [S + 1]
+    uint16_t *out;            // [N][q_heads][D]
+    float *lse;               // [N][q_heads] or nullptr
+    int N, S, q_heads, kv_heads;
+    int G, Gp, TB;            // query heads a key head; of a block; tokens of 128 rows (Gp * TB <= 128)
+    float scale_log2;         // scale * log2(e), > 0
+    unsigned *status;
+};
+
 struct DeltaStepParams {
     const uint16_t *q, *k, *v;
     long q_stride, k_stride, v_stride;
@@ -40,6 +52,12 @@ struct LogprobParams {
 };
 
 cudaError_t launch_qk_norm_rope(const NormRopeParams &p, const LaunchCfg &cfg, cudaStream_t stream);
+// q, k: the first heads; strides in elements.
+cudaError_t launch_prompt_attention(PromptAttnParams p, const uint16_t *q, long q_stride, const uint16_t *k, long k_stride, int D,
+                                    const LaunchCfg &cfg, cudaStream_t stream);
+// The query heads of a block and the blocks that a call can have at most.
+int prompt_attn_heads(int G);
+long prompt_attn_blocks(int N, int S, int q_heads, int kv_heads);
 cudaError_t launch_delta_step(const DeltaStepParams &p, const LaunchCfg &cfg, cudaStream_t stream);
 cudaError_t launch_logprobs(const LogprobParams &p, bool bf16, const LaunchCfg &cfg, cudaStream_t stream);
 

@@ -1,6 +1,6 @@
 // ts_hc_prompt_api.cu -- the C ABI of the operators of a prompt's pass and of the
-// token after it in include/ts_hc.h (head norms with rotary positions, the gated
-// delta rule, log probabilities): argument validation on the host, then the
+// token after it in include/ts_hc.h (head norms with rotary positions,
+// attention over packed prompts, the gated delta rule, log probabilities): argument validation on the host, then the
 // launches.
 #include <climits>
 #include <cmath>
@@ -170,6 +170,60 @@ ts_status ts_hc_qk_norm_rope(const void *q, long q_stride, const void *k, long k
     p.kw = static_cast<const uint16_t *>(k_norm_w);
     p.eps = eps;
     return launched(tshc::launch_qk_norm_rope(p, cfg, stream), "launching the head norm kernel");
+}
+
+ts_status ts_hc_prompt_attention(const void *q, long q_stride, const void *k, long k_stride, const void *v, long v_stride,
+                                 const int32_t *starts, void *out, float *lse, int N, int S, int q_heads, int kv_heads, int D, float scale,
+                                 cudaStream_t stream)
+{
+    tshc::clear_error();
+    TS_TRY(check_count(N, "N", 0, INT_MAX));
+    TS_TRY(check_count(S, "S", 0, kMaxBatch));
+    TS_TRY(check_count(q_heads, "q_heads", 1, kMaxHeads));
+    TS_TRY(check_count(kv_heads, "kv_heads", 1, kMaxHeads));
+    if (q_heads % kv_heads != 0)
+        return api_error(TS_ERR_INVALID_ARG, "q_heads = %d must be a multiple of kv_heads = %d", q_heads, kv_heads);
+    if (D != 64 && D != 128)
+        return api_error(TS_ERR_UNSUPPORTED, "D = %d: heads of 64 and 128 are supported", D);
+    if (!(scale > 0.f) || !std::isfinite(scale))
+        return api_error(TS_ERR_INVALID_ARG, "scale = %g must be > 0", (double)scale);
+    if (N == 0 || S == 0)
+        return TS_OK;
+    const long qw = (long)q_heads * D, kw = (long)kv_heads * D;
+    TS_TRY(check_ptr_api(q, "q", 16));
+    TS_TRY(check_ptr_api(k, "k", 16));
+    TS_TRY(check_ptr_api(v, "v", 16));
+    TS_TRY(check_stride(q_stride, "q_stride", qw, 8));
+    TS_TRY(check_stride(k_stride, "k_stride", kw, 8));
+    TS_TRY(check_stride(v_stride, "v_stride", kw, 8));
+    TS_TRY(check_ptr_api(starts, "starts", 4));
+    TS_TRY(check_ptr_api(out, "out", 16));
+    if (lse)
+        TS_TRY(check_ptr_api(lse, "lse", 4));
+    if (rows_overlap(out, qw, qw, q, q_stride, qw, N))
+        return api_error(TS_ERR_INVALID_ARG, "out overlaps q");
+    if (rows_overlap(out, qw, qw, k, k_stride, kw, N))
+        return api_error(TS_ERR_INVALID_ARG, "out overlaps k");
+    if (rows_overlap(out, qw, qw, v, v_stride, kw, N))
+        return api_error(TS_ERR_INVALID_ARG, "out overlaps v");
+    if (tshc::prompt_attn_blocks(N, S, q_heads, kv_heads) > INT_MAX)
+        return api_error(TS_ERR_UNSUPPORTED, "%d tokens of %d heads are too many for one call: split them", N, q_heads);
+    tshc::LaunchCfg cfg;
+    tshc::PromptAttnParams p{};
+    TS_TRY(device(&cfg, &p.status));
+    p.v = static_cast<const uint16_t *>(v);
+    p.v_stride = v_stride;
+    p.starts = starts;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.N = N;
+    p.S = S;
+    p.q_heads = q_heads;
+    p.kv_heads = kv_heads;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    return launched(tshc::launch_prompt_attention(p, static_cast<const uint16_t *>(q), q_stride, static_cast<const uint16_t *>(k), k_stride, D, cfg,
+                                                  stream),
+                    "launching the prompt attention kernel");
 }
 
 ts_status ts_hc_delta_step(const void *q, long q_stride, const void *k, long k_stride, const void *v, long v_stride, const float *decay,

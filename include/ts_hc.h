@@ -631,7 +631,8 @@ ts_status ts_hc_verify(const float *logits, const float *draft_probs, const int3
  * starts[s+1] - 1, with starts int32 [S+1] ascending from 0 on the device; tokens from starts[S] on belong to
  * none, and their rows of an output are left as they were. What the host cannot check of starts the kernels do:
  * a sequence that begins before token 0, ends before it begins or reaches past N is taken as empty and
- * TS_ERR_INVALID_ARG is recorded in the device status word. Sequences of no tokens are fine.
+ * TS_ERR_INVALID_ARG is recorded in the device status word. Sequences of no tokens are fine; rows that two sequences
+ * claim, where starts descends, get either's results.
  */
 
 /*
@@ -648,6 +649,26 @@ ts_status ts_hc_qk_norm_rope(const void *q, long q_stride, const void *k, long k
                              const float *table, int max_pos, const void *q_norm_w, const void *k_norm_w, float eps,
                              void *q_out, long q_out_stride, void *k_out, long k_out_stride, int N, int q_heads,
                              int k_heads, int D, int rot, int interleaved, cudaStream_t stream);
+
+/*
+ * Causal attention over packed prompts: token t of a sequence sees the sequence's tokens j <= t,
+ *     out_t = softmax_j(scale * q_t . k_j) v,   lse_t = log sum_j exp(scale * q_t . k_j)
+ * with head h's keys and values those of head h / (q_heads/kv_heads). What a token does not see does not reach it,
+ * whatever it holds: an infinity or a NaN in a later token's or another sequence's key or value changes nothing.
+ *   q, k, v    bf16: head h of token n at q + n*q_stride + h*D; k and v likewise, kv_heads of them; strides in
+ *              elements, multiples of 8 (slices of one projection's output will do); 16-byte aligned
+ *   starts     int32 [S+1], as above
+ *   out        bf16 [N][q_heads][D], 16-byte aligned; lse fp32 [N][q_heads] or NULL; rows of no sequence are not
+ *              written
+ *   scale      > 0
+ * The products run on the tensor cores in bf16 with fp32 sums (the weights are rounded to bf16 for the second); the
+ * softmax's maximum and sum are fp32. Weights times values are added up before they are divided by the weights' sum,
+ * a weight being up to 2^8 times the one that a row's sum is kept relative to: values beyond 2^119 / (the keys that a
+ * row sees) can overflow to an infinity. D is 64 or 128 (TS_ERR_UNSUPPORTED otherwise); S <= 65535.
+ */
+ts_status ts_hc_prompt_attention(const void *q, long q_stride, const void *k, long k_stride, const void *v, long v_stride,
+                                 const int32_t *starts, void *out, float *lse, int N, int S, int q_heads, int kv_heads,
+                                 int D, float scale, cudaStream_t stream);
 
 /*
  * The gated delta rule (families/qwen4/mod.rs, the GDN sublayer's recurrence) for T tokens of B sequences, one

@@ -5,6 +5,10 @@ Tolerances, from the number formats (unit roundoffs: u16 = 2^-8 of bf16, u32 = 2
   head norms  a row's sum of D squares is off by at most D u32 of itself, its root by half of that; with the
               products and the turn's two products and sum, and one rounding to bf16:
                 |err| <= u16 |y| + (D + 16) u32 (|n0| + |n1|), n the normed elements of the pair
+  attention   the scores are off by at most d = (D + 8) u32 max_j scale sum|q||k| (a sum of D products in fp32; the
+              8 for the scale, the maximum and the exponential), so that each weight is off by a factor of
+              1 + 2 d; weights are rounded to bf16 (u16 of p |v|), the result to bf16: with A = sum p |v|
+                |err| <= (1.5 u16 + 4 d + 64 u32) A + u16 |out| + 2^-24,  lse: 2 d + 64 u32 (1 + |lse|)
   delta rule  columns of the state do not meet. With keys of norm 1 at most and beta <= 1, I - beta k k^T makes no
               column's error longer, and a token adds at most (D + 16) u32 M to it: M the largest that a column's
               norm plus |v| was, D u32 of it from the sum over the keys, the rest from the decay (expf is within
@@ -129,6 +133,157 @@ def test_norm_rope_nan_stays_in_its_head():
         assert got[1, 2].isnan().all()
         got[1, 2] = want[1, 2]
         assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ attention over packed prompts
+
+def prompts(lens, hq, hk, d, seed, *, behind=0, q_scale=1.5):
+    """Slices of one projection's output, the sequences' starts, and rows of no sequence behind them."""
+    g = gen(seed)
+    at = [0]
+    for n in lens:
+        at.append(at[-1] + n)
+    x = randn(g, at[-1] + behind, hq + 2 * hk, d)
+    x[:, :hq] *= q_scale
+    return x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], torch.tensor(at, device="cuda", dtype=torch.int32), at
+
+
+def check_attention(q, k, v, at, got, scale=None, rows=None):
+    """``rows``: the heads that are looked at."""
+    d = q.shape[-1]
+    scale = d ** -0.5 if scale is None else scale
+    out, lse, size, mass = P.attention(P.f64(q), P.f64(k), P.f64(v), at, scale)
+    err = (d + 8) * U32 * size
+    in_use = slice(at[0], at[-1])
+    a, z = P.f64(got[0])[in_use], P.f64(got[1])[in_use]
+    out, lse, err, mass = out[in_use], lse[in_use], err[in_use], mass[in_use]
+    limit = (1.5 * U16 + 4 * err + 64 * U32)[..., None] * mass + U16 * np.abs(out) + 2.0 ** -24
+    within(a, out, limit, "out")
+    within(z, lse, 2 * err + 64 * U32 * (1 + np.abs(lse)), "lse")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (4, 1), (6, 2), (8, 1), (5, 1)])
+@pytest.mark.parametrize("lens", [[1], [2, 1], [127, 128, 129], [0, 17, 0, 0, 64, 0], [255, 1, 256, 257], [300]])
+def test_attention_lengths(d, hq, hk, lens):
+    q, k, v, starts, at = prompts(lens, hq, hk, d, sum(lens) + hq)
+    check_attention(q, k, v, at, B.hc_prompt_attention(q, k, v, starts))
+    fine()
+
+
+@pytest.mark.parametrize("hq,hk", [(40, 1), (33, 1), (37, 1), (128, 2), (3, 1), (7, 7), (48, 16)])
+def test_attention_heads(hq, hk):
+    q, k, v, starts, at = prompts([70, 3, 150], hq, hk, 64, hq)
+    check_attention(q, k, v, at, B.hc_prompt_attention(q, k, v, starts))
+    fine()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_long(d):
+    q, k, v, starts, at = prompts([1100, 1500], 2, 1, d, 5)
+    check_attention(q, k, v, at, B.hc_prompt_attention(q, k, v, starts))
+    fine()
+
+
+def test_attention_many_sequences():
+    """More than one round of the blocks' order, sequences of no tokens among them."""
+    r = np.random.default_rng(3)
+    lens = [int(x) for x in r.integers(0, 9, 700)]
+    lens[5], lens[400], lens[699] = 300, 0, 140
+    q, k, v, starts, at = prompts(lens, 2, 1, 64, 6)
+    check_attention(q, k, v, at, B.hc_prompt_attention(q, k, v, starts))
+    fine()
+
+
+def test_attention_leaves_rows_behind():
+    q, k, v, starts, at = prompts([50, 200], 4, 2, 128, 7, behind=60)
+    k[250:], v[250:] = float("nan"), float("inf")
+    out, lse = torch.full(q.shape, 7.0, device="cuda").bfloat16(), torch.full(q.shape[:2], 7.0, device="cuda")
+    got = B.hc_prompt_attention(q, k, v, starts, out=out, lse=lse)
+    assert got[0] is out and got[1] is lse and (out[250:] == 7).all() and (lse[250:] == 7).all()
+    check_attention(q[:250], k[:250], v[:250], at, (out[:250], lse[:250]))
+    fine()
+
+
+@pytest.mark.parametrize("scale", [1e-3, 0.3, 4.0])
+def test_attention_scale(scale):
+    q, k, v, starts, at = prompts([200, 90], 2, 1, 64, 8, q_scale=3.0)
+    check_attention(q, k, v, at, B.hc_prompt_attention(q, k, v, starts, scale=scale), scale)
+
+
+def test_attention_growing_scores():
+    """Keys whose scores grow with their place, so that a row's maximum does in every tile."""
+    q, k, v, starts, at = prompts([700], 2, 1, 128, 9)
+    q[:] = q.abs()
+    k[:] = (torch.arange(700, device="cuda")[:, None, None] * 0.02 * torch.ones_like(k)).bfloat16()
+    check_attention(q, k, v, at, B.hc_prompt_attention(q, k, v, starts))
+    k[:] = k.flip(0)
+    check_attention(q, k, v, at, B.hc_prompt_attention(q, k, v, starts))
+
+
+@pytest.mark.parametrize("what", ["k nan", "v nan", "v inf", "k inf", "q nan"])
+@pytest.mark.parametrize("token", [0, 40, 130, 299])
+def test_attention_what_is_not_seen_does_not_reach(what, token):
+    """An infinity or a NaN at a token of the second sequence: earlier tokens and other sequences are as without."""
+    q, k, v, starts, at = prompts([90, 300, 45], 4, 2, 64, 10)
+    want, want_lse = B.hc_prompt_attention(q, k, v, starts)
+    t = at[1] + token
+    bad = float(what.split()[1])
+    dict(q=q, k=k, v=v)[what[0]][t, 1, 5] = bad
+    got, lse = B.hc_prompt_attention(q, k, v, starts)
+    for now, then in ((got, want), (lse, want_lse)):
+        assert torch.equal(now[:t], then[:t]) and torch.equal(now[at[2]:], then[at[2]:])
+    heads = slice(1, 2) if what[0] == "q" else slice(2, 4)  # the query heads of key head 1
+    rows = slice(t, t + 1) if what[0] == "q" else slice(t, at[2])
+    if what == "v nan":
+        assert got[rows, heads, 5].isnan().all()
+        got[rows, heads, 5] = want[rows, heads, 5]
+    elif what == "v inf":
+        assert (got[rows, heads, 5] == float("inf")).all()
+        got[rows, heads, 5] = want[rows, heads, 5]
+    else:
+        if what != "k inf":
+            assert got[rows, heads].isnan().all()
+        got[rows, heads], lse[rows, heads] = want[rows, heads], want_lse[rows, heads]
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
+    fine()
+
+
+def test_attention_starts_out_of_range():
+    q, k, v, starts, at = prompts([50, 60, 70], 2, 1, 64, 11)
+    want, _ = B.hc_prompt_attention(q, k, v, starts)
+    for bad in ([0, 50, 110, 181], [-1, 50, 110, 180], [0, 120, 110, 180]):
+        out = torch.full_like(q, 7.0).contiguous()
+        got, _ = B.hc_prompt_attention(q, k, v, torch.tensor(bad, device="cuda", dtype=torch.int32), out=out)
+        assert B.device_status() == B.TS_ERR_INVALID_ARG
+        if bad[1] == 50:
+            assert torch.equal(got[50:110], want[50:110])
+        # (rows 110 .. 119 are two sequences' with the last of these)
+        assert (got[110:] == 7).all() if bad[3] == 181 else torch.equal(got[120:], want[120:])
+        if bad[0] == -1:
+            assert (got[:50] == 7).all()
+
+
+def test_attention_is_the_same_every_time_and_over_the_cache():
+    """The same bits each time, replayed too; and what the attention over a paged cache gives for the same rows."""
+    q, k, v, starts, at = prompts([512, 512], 8, 2, 128, 12)
+    out, lse = B.hc_prompt_attention(q, k, v, starts)
+    graph = torch.cuda.CUDAGraph()
+    o2, l2 = torch.zeros_like(out), torch.zeros_like(lse)
+    with torch.cuda.graph(graph):
+        B.hc_prompt_attention(q, k, v, starts, out=o2, lse=l2)
+    for _ in range(5):
+        o2.zero_(), l2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+    cache = B.kv_cache("bf16", 2 * 8, 2, 64, 128, torch.arange(16, device="cuda", dtype=torch.int32).view(2, 8))
+    ctx = torch.zeros(2, device="cuda", dtype=torch.int32)
+    B.hc_kv_write(k.unflatten(0, (2, 512)), v.unflatten(0, (2, 512)), cache, ctx)
+    tree, tree_lse = B.hc_tree_attention(q.unflatten(0, (2, 512)), cache, ctx)
+    assert (tree.flatten(0, 1).float() - out.float()).abs().max() < 0.05
+    assert (tree_lse.flatten(0, 1) - lse).abs().max() < 1e-4
+    fine()
 
 
 # ------------------------------------------------------------------ the gated delta rule

@@ -52,6 +52,28 @@ def test_norm_rope_refusals(kw, status, needle):
     refused(norm_rope(**kw), status, needle)
 
 
+def attention(**kw):
+    a = dict(q=FAKE, sq=512, k=FAKE + MB, sk=256, v=FAKE + 2 * MB, sv=256, starts=FAKE + 3 * MB, out=FAKE + 4 * MB, lse=FAKE + 5 * MB, N=10, S=2,
+             hq=4, hk=2, D=128, scale=1.0)
+    a.update(kw)
+    return B.ts_hc_prompt_attention(a["q"], a["sq"], a["k"], a["sk"], a["v"], a["sv"], a["starts"], a["out"], a["lse"], a["N"], a["S"], a["hq"],
+                                    a["hk"], a["D"], a["scale"], None)
+
+
+@pytest.mark.parametrize("kw,status,needle", [
+    (dict(N=-1), INVALID, "N = -1"), (dict(S=-1), INVALID, "S = -1"), (dict(S=65536), INVALID, "S = 65536"), (dict(hq=0), INVALID, "q_heads = 0"),
+    (dict(hk=0), INVALID, "kv_heads = 0"), (dict(hq=5), INVALID, "q_heads = 5 must be a multiple"), (dict(D=256), UNSUPPORTED, "D = 256"),
+    (dict(D=80), UNSUPPORTED, "D = 80"), (dict(scale=0.0), INVALID, "scale = 0"), (dict(scale=-1.0), INVALID, "scale"),
+    (dict(scale=float("inf")), INVALID, "scale"), (dict(scale=float("nan")), INVALID, "scale"), (dict(q=None), INVALID, "q is NULL"),
+    (dict(k=FAKE + 8), INVALID, "k is not"), (dict(v=None), INVALID, "v is NULL"), (dict(sq=511), INVALID, "q_stride"),
+    (dict(sk=128), INVALID, "k_stride = 128"), (dict(sv=260), INVALID, "v_stride = 260"), (dict(starts=None), INVALID, "starts"),
+    (dict(out=FAKE + 4 * MB + 2), INVALID, "out is not"), (dict(lse=FAKE + 1), INVALID, "lse"), (dict(out=FAKE), INVALID, "out overlaps q"),
+    (dict(out=FAKE + MB), INVALID, "out overlaps k"), (dict(out=FAKE + 2 * MB), INVALID, "out overlaps v"),
+])
+def test_attention_refusals(kw, status, needle):
+    refused(attention(**kw), status, needle)
+
+
 def step(**kw):
     a = dict(q=FAKE, sq=256, k=FAKE + MB, sk=256, v=FAKE + 2 * MB, sv=512, decay=FAKE + 3 * MB, beta=FAKE + 4 * MB, counts=FAKE + 5 * MB,
              si=FAKE + 6 * MB, so=FAKE + 8 * MB, out=FAKE + 10 * MB, B=2, T=3, hk=2, hv=4, D=128, scale=1.0, eps=1e-6)
@@ -101,6 +123,8 @@ def test_logprobs_refusals(kw, status, needle):
 
 def test_nothing_to_do():
     assert norm_rope(N=0, q=None, qo=None) == B.TS_OK
+    assert attention(N=0, q=None) == B.TS_OK
+    assert attention(S=0, q=None) == B.TS_OK
     assert step(B=0, q=None) == B.TS_OK
     assert step(T=0, q=None, out=None) == B.TS_OK
     assert logprobs(N=0, logits=None) == B.TS_OK
