@@ -40,7 +40,8 @@ EXPORTS = ("ts_hc_workspace_bytes", "ts_hc_workspace_layout", "ts_hc_call", "ts_
            "ts_hc_stack_ple_workspace_bytes", "ts_hc_stack_ple", "ts_hc_selftest_timeout",
            "ts_hc_rope_table", "ts_hc_rope", "ts_hc_kv_write", "ts_hc_kv_read", "ts_hc_kv_compact", "ts_hc_tree_build",
            "ts_hc_tree_attention_workspace_bytes", "ts_hc_tree_attention", "ts_hc_verify",
-           "ts_hc_qk_norm_rope", "ts_hc_prompt_attention", "ts_hc_delta_step", "ts_hc_logprobs")
+           "ts_hc_qk_norm_rope", "ts_hc_prompt_attention", "ts_hc_delta_step", "ts_hc_delta_prompt_workspace_bytes",
+           "ts_hc_delta_prompt", "ts_hc_logprobs")
 TS_HC_STATIC_SCRATCH_BYTES = 64 * 1024 * 1024  # include/ts_hc.h
 
 
@@ -199,6 +200,10 @@ def library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.ts_hc_prompt_attention.restype = i
         lib.ts_hc_delta_step.argtypes = [vp, l, vp, l, vp, l, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, f, vp]
         lib.ts_hc_delta_step.restype = i
+        lib.ts_hc_delta_prompt_workspace_bytes.argtypes = [i, i, i, i, i]
+        lib.ts_hc_delta_prompt_workspace_bytes.restype = sz
+        lib.ts_hc_delta_prompt.argtypes = [vp, l, vp, l, vp, l, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, f, vp, sz, vp]
+        lib.ts_hc_delta_prompt.restype = i
         lib.ts_hc_logprobs.argtypes = [vp, i, l, vp, vp, vp, vp, vp, i, i, i, i, vp]
         lib.ts_hc_logprobs.restype = i
         lib.ts_hc_selftest_timeout.argtypes = [vp]
@@ -387,6 +392,16 @@ def ts_hc_delta_step(q, q_stride, k, k_stride, v, v_stride, decay, beta, counts,
                      D, scale, norm_eps, stream) -> int:
     return library().ts_hc_delta_step(q, q_stride, k, k_stride, v, v_stride, decay, beta, counts, state_in, state_out, out, B, T,
                                       k_heads, v_heads, D, scale, norm_eps, stream)
+
+
+def ts_hc_delta_prompt_workspace_bytes(N: int, S: int, k_heads: int, v_heads: int, D: int) -> int:
+    return library().ts_hc_delta_prompt_workspace_bytes(N, S, k_heads, v_heads, D)
+
+
+def ts_hc_delta_prompt(q, q_stride, k, k_stride, v, v_stride, decay, beta, starts, state_in, state_out, out, N, S, k_heads, v_heads, D,
+                       scale, norm_eps, workspace, workspace_bytes, stream) -> int:
+    return library().ts_hc_delta_prompt(q, q_stride, k, k_stride, v, v_stride, decay, beta, starts, state_in, state_out, out, N, S,
+                                        k_heads, v_heads, D, scale, norm_eps, workspace, workspace_bytes, stream)
 
 
 def ts_hc_logprobs(logits, logits_type, logits_stride, tokens, logp, entropy, top_ids, top_logp, N, V, J, top, stream) -> int:
@@ -1267,6 +1282,37 @@ def hc_delta_step(q, k, v, decay, beta, state, *, counts=None, scale: Optional[f
     st = (_lib or library()).ts_hc_delta_step(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, decay.data_ptr(), beta.data_ptr(), cp,
                                               ip, op, out.data_ptr(), b, t, hk, hv, d, d ** -0.5 if scale is None else scale,
                                               -1.0 if norm_eps is None else norm_eps, handle)
+    if st:
+        _check(st)
+    return out, state_out
+
+
+def delta_prompt_workspace(N: int, S: int, k_heads: int, v_heads: int, D: int, device=None):
+    torch = _torch()
+    n = ts_hc_delta_prompt_workspace_bytes(N, S, k_heads, v_heads, D)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def hc_delta_prompt(q, k, v, decay, beta, state, starts, *, scale: Optional[float] = None, norm_eps: Optional[float] = RMS_EPS, out=None,
+                    state_out=None, ws=None, stream=None):
+    """The gated delta rule over packed prompts: ``q``, ``k`` [N, k_heads, D], ``v`` [N, v_heads, D] bf16, ``decay``
+    and ``beta`` fp32 [N, v_heads], ``state`` fp32 [S, v_heads, D, D], the sequences' rows starts[s] ..
+    starts[s+1] - 1 with ``starts`` int32 [S + 1]. Arguments and results as for ``hc_delta_step``: (out bf16
+    [N, v_heads, D], state_out, ``state`` itself unless given)."""
+    torch = _torch()
+    n, hk, hv, d, sq, sk, sv = _delta_rows(q, k, v, decay, beta, 3)
+    sp, s = _starts(starts)
+    shape = (s, hv, d, d)
+    ip = _is(state, "state", torch.float32, shape)
+    state_out = state if state_out is None else state_out
+    op = _is(state_out, "state_out", torch.float32, shape)
+    out = _out(out, "out", torch.bfloat16, v.shape, q, stream)
+    if ws is None:
+        ws = _made(delta_prompt_workspace(n, s, hk, hv, d, q.device), stream)
+    handle = _together(stream, q, k, v, decay, beta, state, state_out, starts, out, ws)
+    st = (_lib or library()).ts_hc_delta_prompt(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, decay.data_ptr(), beta.data_ptr(), sp,
+                                                ip, op, out.data_ptr(), n, s, hk, hv, d, d ** -0.5 if scale is None else scale,
+                                                -1.0 if norm_eps is None else norm_eps, ws.data_ptr(), ws.nbytes, handle)
     if st:
         _check(st)
     return out, state_out

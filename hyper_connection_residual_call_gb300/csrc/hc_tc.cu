@@ -1069,17 +1069,18 @@ bool tc_make_map_2d_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64
 }
 
 bool tc_make_map_heads(CUtensorMap *map, const void *base, uint64_t tokens, uint64_t heads, uint64_t D, uint64_t stride,
-                       uint32_t box_heads, uint32_t box_tokens)
+                       uint32_t box_heads, uint32_t box_tokens, bool plain)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc)
         return false;
     const cuuint64_t dims[3] = {D, heads, tokens};
     const cuuint64_t strides[2] = {D * 2, stride * 2};
-    const cuuint32_t box[3] = {64, box_heads, box_tokens};
+    const cuuint32_t box[3] = {plain ? (cuuint32_t)D : 64, box_heads, box_tokens};
     const cuuint32_t es[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               plain ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool tc_make_map_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows)

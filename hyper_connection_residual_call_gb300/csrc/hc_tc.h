@@ -129,8 +129,8 @@ bool tc_make_map_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t 
 bool tc_make_map_2d_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows);
 
 // Of heads of D bf16 elements, tokens `stride` elements apart: boxes of 64 elements, box_heads heads and box_tokens
-// tokens, coordinates (element, head, token).
+// tokens, coordinates (element, head, token); `plain`: boxes of whole rows, not swizzled.
 bool tc_make_map_heads(CUtensorMap *map, const void *base, uint64_t tokens, uint64_t heads, uint64_t D, uint64_t stride,
-                       uint32_t box_heads, uint32_t box_tokens);
+                       uint32_t box_heads, uint32_t box_tokens, bool plain = false);
 
 }  // namespace tshc

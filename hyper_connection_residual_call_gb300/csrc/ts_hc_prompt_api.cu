@@ -266,6 +266,60 @@ ts_status ts_hc_delta_step(const void *q, long q_stride, const void *k, long k_s
     return launched(tshc::launch_delta_step(p, cfg, stream), "launching the delta rule's step kernel");
 }
 
+size_t ts_hc_delta_prompt_workspace_bytes(int N, int S, int k_heads, int v_heads, int D)
+{
+    if (check_count(N, "N", 0, INT_MAX) != TS_OK || check_count(S, "S", 0, kMaxBatch) != TS_OK || check_delta_heads(k_heads, v_heads, D) != TS_OK)
+        return 0;
+    return tshc::delta_prompt_bytes(N, S, v_heads);
+}
+
+ts_status ts_hc_delta_prompt(const void *q, long q_stride, const void *k, long k_stride, const void *v, long v_stride, const float *decay,
+                             const float *beta, const int32_t *starts, const float *state_in, float *state_out, void *out, int N, int S,
+                             int k_heads, int v_heads, int D, float scale, float norm_eps, void *workspace, size_t workspace_bytes,
+                             cudaStream_t stream)
+{
+    tshc::clear_error();
+    TS_TRY(check_count(N, "N", 0, INT_MAX));
+    TS_TRY(check_count(S, "S", 0, kMaxBatch));
+    TS_TRY(check_delta_heads(k_heads, v_heads, D));
+    TS_TRY(check_scale(scale, norm_eps));
+    if (N == 0 || S == 0)
+        return TS_OK;
+    TS_TRY(check_delta_rows(q, q_stride, k, k_stride, v, v_stride, decay, beta, out, N, k_heads, v_heads, D));
+    TS_TRY(check_states(state_in, state_out, S, v_heads, D, out, span(N, (long)v_heads * D, (long)v_heads * D, 2)));
+    TS_TRY(check_ptr_api(starts, "starts", 4));
+    if (((long)N / 64 + S) * v_heads > INT_MAX)
+        return api_error(TS_ERR_UNSUPPORTED, "%d tokens of %d heads are too many for one call: split them", N, v_heads);
+    const size_t need = tshc::delta_prompt_bytes(N, S, v_heads);
+    if (!workspace || workspace_bytes < need)
+        return api_error(TS_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace ? workspace_bytes : (size_t)0, need);
+    TS_TRY(check_ptr_api(workspace, "workspace", 256));
+    tshc::LaunchCfg cfg;
+    tshc::DeltaPromptParams p{};
+    TS_TRY(device(&cfg, &p.status));
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.decay = decay;
+    p.beta = beta;
+    p.starts = starts;
+    p.state_in = state_in;
+    p.state_out = state_out;
+    p.out = static_cast<uint16_t *>(out);
+    p.work = static_cast<uint8_t *>(workspace);
+    p.N = N;
+    p.S = S;
+    p.Hk = k_heads;
+    p.Hv = v_heads;
+    p.D = D;
+    p.scale = scale;
+    p.norm_eps = norm_eps;
+    return launched(tshc::launch_delta_prompt(p, cfg, stream), "launching the delta rule's prompt kernels");
+}
+
 ts_status ts_hc_logprobs(const void *logits, int logits_type, long logits_stride, const int32_t *tokens, float *logp, float *entropy,
                          int32_t *top_ids, float *top_logp, int N, int V, int J, int top, cudaStream_t stream)
 {

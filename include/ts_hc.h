@@ -693,6 +693,32 @@ ts_status ts_hc_delta_step(const void *q, long q_stride, const void *k, long k_s
                            float *state_out, void *out, int B, int T, int k_heads, int v_heads, int D, float scale,
                            float norm_eps, cudaStream_t stream);
 
+/*
+ * The gated delta rule for packed prompts: ts_hc_delta_step's recurrence from each sequence's state over all of its
+ * tokens, in chunks of 64 on the tensor cores.
+ *   q, k, v    bf16: head h of token n at q + n*q_stride + h*D, k likewise, k_heads of them, v with v_heads; strides
+ *              in elements, multiples of 8; 16-byte aligned
+ *   decay, beta   fp32 [N][v_heads], as for ts_hc_delta_step
+ *   starts     int32 [S+1], as above; where it descends anywhere the results are undefined (recorded)
+ *   state_in   fp32 [S][v_heads][D][D]; state_out likewise, which may be state_in. A sequence of no tokens keeps its
+ *              state
+ *   out        bf16 [N][v_heads][D]; rows of no sequence are not written
+ *   workspace  >= ts_hc_delta_prompt_workspace_bytes(...) bytes, 256-byte aligned (some 33 KB for 64 tokens of a value
+ *              head); it need not be initialised and must not be shared by calls that can run at the same time
+ * The state is held in fp32. What goes into the tensor cores is the keys and queries as they are and every other
+ * operand (the state among them) as the sum of two bf16, 16 bits of significand; sums are fp32. An infinity or a NaN
+ * in a token's inputs leaves NaNs in the outputs from that token on that it reaches and in the state, and the
+ * outputs before it as they are without.
+ * Keys are of norm 1 or less in effect (norm_eps >= 0, or made so by the caller) and beta at most 2: with much longer
+ * ones the recurrence itself diverges. D is 64 or 128 (TS_ERR_UNSUPPORTED otherwise); v_heads is a multiple of
+ * k_heads; S <= 65535. N == 0 is a no-op: state_out is not written either (nor is it by a step with T == 0).
+ */
+size_t ts_hc_delta_prompt_workspace_bytes(int N, int S, int k_heads, int v_heads, int D);
+ts_status ts_hc_delta_prompt(const void *q, long q_stride, const void *k, long k_stride, const void *v, long v_stride,
+                             const float *decay, const float *beta, const int32_t *starts, const float *state_in,
+                             float *state_out, void *out, int N, int S, int k_heads, int v_heads, int D, float scale,
+                             float norm_eps, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 typedef enum {
     TS_LOGITS_FP32 = 0,       /* as ts_hc_exit_logits writes them */
     TS_LOGITS_BF16 = 1

@@ -15,6 +15,13 @@ Tolerances, from the number formats (unit roundoffs: u16 = 2^-8 of bf16, u32 = 2
               two units of the last place), the norms and the update. After T tokens and from an output's own sum:
                 |state err| <= T (D + 16) u32 M + u32 |S|
                 |out err| <= u16 |out| + scale |q| (T + 1) (D + 16) u32 M
+              In chunks, an operand is the sum of two bf16 and off by 2^-17 of itself at most (each part by u16 of
+              itself; what is left of the second counts 2^-16 / 2). With the state's columns and the values within M,
+              X and so R are off by 2^-17 M a token (keys of norm 1); U = T R: T's columns are the effect of one
+              token's value on the later tokens' updates, with sums of squares of at most 2 or so for keys of norm 1,
+              and three such errors (of R, of T, of the product that is left out) of up to sqrt(64) terms of size M:
+              some 3 * 8 * 2^-17 M; the state takes that on, and its own two errors. 40 * 2^-17 M a chunk bounds
+              them; they are not made longer after it. An output has the state's and U's errors: twice that
   log probabilities  e^d is off by 2 |d| u32 (the product with log2 e) and 2^-22 (the function) of itself, sums
               run over V/1024 elements a thread and then 40 joins: log Z is off by at most
               r = (V/1024 + 100) u32 (the |d| weighted with p add up to less than the entropy, at most 21), so
@@ -31,7 +38,7 @@ from gpu_common import require_gpu
 from hyper_connection_residual_call_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
-U16, U32 = 2.0 ** -8, 2.0 ** -24
+U16, U32, SPLIT = 2.0 ** -8, 2.0 ** -24, 2.0 ** -17
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -374,6 +381,162 @@ def test_delta_step_decays_that_keep_nothing():
         fresh, want = B.hc_delta_step(*(x[:, 1:].contiguous() for x in args[:3]), *(x[:, 1:].contiguous() for x in args[3:5]),
                                       torch.zeros_like(args[5]))
         assert torch.equal(state, want) and torch.equal(out[:, 1:], fresh)
+
+
+def prompt_case(lens, hk, hv, d, seed, *, behind=0, low=4.0):
+    g = gen(seed)
+    at = [0]
+    for n in lens:
+        at.append(at[-1] + n)
+    n = at[-1] + behind
+    x = randn(g, n, 2 * hk + hv, d)
+    decay = -torch.rand(n, hv, generator=g, device="cuda") ** 3 * low
+    return (x[:, :hk], x[:, hk:2 * hk], x[:, 2 * hk:], decay, torch.rand(n, hv, generator=g, device="cuda"),
+            torch.randn(len(lens), hv, d, d, generator=g, device="cuda") * 0.3, torch.tensor(at, device="cuda", dtype=torch.int32)), at
+
+
+def check_prompt(args, at, out, state, norm_eps=1e-6):
+    q, k, v, decay, beta, before = (P.f64(x) for x in args[:6])
+    d = v.shape[-1]
+    scale = d ** -0.5
+    for i, (lo, hi) in enumerate(zip(at[:-1], at[1:])):
+        want, after, size = P.delta(q[lo:hi], k[lo:hi], v[lo:hi], decay[lo:hi], beta[lo:hi], before[i], scale, norm_eps)
+        chunks = (hi - lo + 63) // 64
+        step = 40 * SPLIT * size * chunks
+        if hi > lo:
+            within(out[lo:hi], want, U16 * np.abs(want) + scale * 2 * step + 1e-38, "out")
+        within(state[i], after, step[:, None] + U32 * np.abs(after) + 1e-38, "state")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hk,hv", [(1, 1), (2, 4), (1, 3)])
+@pytest.mark.parametrize("lens", [[1], [64], [65, 63], [0, 5, 0, 130, 0], [200, 1, 64, 128]])
+def test_delta_prompt(d, hk, hv, lens):
+    args, at = prompt_case(lens, hk, hv, d, sum(lens) + hv)
+    before = args[5].clone()
+    apart = torch.empty_like(before)
+    out, same = B.hc_delta_prompt(*args, state_out=apart)
+    assert same is apart and torch.equal(args[5], before)
+    check_prompt(args, at, out, apart)
+    again, state = B.hc_delta_prompt(*args[:5], before, args[6])  # in place
+    assert state is before and torch.equal(state, apart) and torch.equal(again, out)
+    fine()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("low", [0.01, 1.0, 60.0])
+def test_delta_prompt_long(d, low):
+    args, at = prompt_case([700], 1, 2, d, 3, low=low)
+    out, state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    check_prompt(args, at, out, state)
+    fine()
+
+
+def test_delta_prompt_many_sequences():
+    r = np.random.default_rng(4)
+    lens = [int(x) for x in r.integers(0, 90, 70)]
+    args, at = prompt_case(lens, 1, 2, 64, 5)
+    out, state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    check_prompt(args, at, out, state)
+    fine()
+
+
+@pytest.mark.parametrize("norm_eps", [0.5, None])
+def test_delta_prompt_norms(norm_eps):
+    args, at = prompt_case([150, 20], 2, 2, 128, 6)
+    if norm_eps is None:  # norms of 1 at most
+        for y in args[:2]:
+            y /= y.float().norm(dim=-1, keepdim=True).bfloat16() * 1.02
+    out, state = B.hc_delta_prompt(*args, norm_eps=norm_eps, state_out=torch.empty_like(args[5]))
+    check_prompt(args, at, out, state, norm_eps)
+
+
+def test_delta_prompt_equal_keys():
+    """All keys the same, beta 1: each token's update takes back the one before."""
+    args, at = prompt_case([130], 1, 1, 64, 7, low=0.0)
+    args[1][:] = args[1][0].clone()
+    args[4].fill_(1.0)
+    out, state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    check_prompt(args, at, out, state)
+
+
+@pytest.mark.parametrize("decay", [-200.0, float("-inf"), torch.finfo(torch.float32).min, -90.0])
+def test_delta_prompt_strong_decays(decay):
+    """After a token that keeps nothing all is as from a state of zeros, weak decays after strong ones among it."""
+    args, at = prompt_case([190], 1, 2, 64, 8, low=0.05)
+    args[3][[3, 40, 41, 100]] = decay
+    out, state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    bounded = list(args)
+    bounded[3] = args[3].clamp(min=-1e4)
+    check_prompt(bounded, at, out, state)
+
+
+def test_delta_prompt_leaves_rows_behind():
+    args, at = prompt_case([50, 100], 1, 2, 128, 9, behind=40)
+    for x in args[:5]:
+        x[150:] = float("nan")
+    out = torch.full((190, 2, 128), 7.0, device="cuda").bfloat16()
+    _, state = B.hc_delta_prompt(*args, out=out, state_out=torch.empty_like(args[5]))
+    assert (out[150:] == 7).all()
+    check_prompt([x[:150] if i < 5 else x for i, x in enumerate(args)], at, out[:150], state)
+    fine()
+
+
+@pytest.mark.parametrize("what", ["q", "k", "v", "decay", "beta", "state"])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+@pytest.mark.parametrize("token", [0, 17, 64, 90, 149])
+def test_delta_prompt_what_came_before_is_not_reached(what, bad, token):
+    args, at = prompt_case([70, 150, 66], 2, 4, 64, 10)
+    want, want_state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    t, x = at[1] + token, float(bad)
+    if what == "state":
+        args[5][1, 2, 3, 5] = x
+        t = at[1]
+    else:
+        args[dict(q=0, k=1, v=2, decay=3, beta=4)[what]][(t, 1, 5) if what in "qkv" else (t, 1)] = x
+    got, state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    heads = dict(q=slice(2, 4), k=slice(2, 4), v=slice(1, 2), decay=slice(1, 2), beta=slice(1, 2), state=slice(2, 3))[what]
+    cols = slice(5, 6) if what in ("v", "state") else slice(None)
+    rows = slice(t, t + 1) if what == "q" else slice(t, at[2])
+    assert not torch.isfinite(got[rows, heads, cols]).any()
+    got[rows, heads, cols] = want[rows, heads, cols]
+    assert torch.equal(got, want)
+    if what != "q":
+        assert not torch.isfinite(state[1, heads, :, cols]).any()
+        state[1, heads, :, cols] = want_state[1, heads, :, cols]
+    assert torch.equal(state, want_state)
+    fine()
+
+
+def test_delta_prompt_is_the_same_every_time_and_as_token_by_token():
+    args, at = prompt_case([200, 200], 2, 4, 128, 11)
+    out, state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    ws = B.delta_prompt_workspace(400, 2, 2, 4, 128)
+    o2, s2 = torch.zeros_like(out), torch.zeros_like(state)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.hc_delta_prompt(*args, out=o2, state_out=s2, ws=ws)
+    for _ in range(3):
+        o2.zero_(), s2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, out) and torch.equal(s2, state)
+    step = [x.unflatten(0, (2, 200)) for x in args[:5]]
+    o3, s3 = B.hc_delta_step(*step, args[5], state_out=torch.empty_like(state))
+    assert (s3 - state).norm() <= 1e-4 * state.norm()
+    assert (o3.flatten(0, 1).float() - out.float()).norm() <= 2e-3 * out.float().norm()
+    fine()
+
+
+def test_delta_prompt_starts_out_of_range():
+    args, at = prompt_case([50, 60, 70], 1, 1, 64, 12)
+    want, want_state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    out = torch.full_like(want, 7.0)
+    state = torch.zeros_like(want_state)
+    B.hc_delta_prompt(*args[:6], torch.tensor([-1, 50, 110, 181], device="cuda", dtype=torch.int32), out=out, state_out=state)
+    assert B.device_status() == B.TS_ERR_INVALID_ARG
+    assert (out[:50] == 7).all() and (out[110:] == 7).all() and torch.equal(out[50:110], want[50:110])
+    assert torch.equal(state[0], args[5][0]) and torch.equal(state[2], args[5][2]) and torch.equal(state[1], want_state[1])
 
 
 # ------------------------------------------------------------------ log probabilities

@@ -99,6 +99,34 @@ def test_delta_step_refusals(kw, status, needle):
     refused(step(**kw), status, needle)
 
 
+def prompt(**kw):
+    a = dict(q=FAKE, sq=256, k=FAKE + MB, sk=256, v=FAKE + 2 * MB, sv=512, decay=FAKE + 3 * MB, beta=FAKE + 4 * MB, starts=FAKE + 5 * MB,
+             si=FAKE + 6 * MB, so=FAKE + 8 * MB, out=FAKE + 10 * MB, N=100, S=3, hk=2, hv=4, D=128, scale=1.0, eps=1e-6, ws=FAKE + 16 * MB,
+             n=1 << 30)
+    a.update(kw)
+    return B.ts_hc_delta_prompt(a["q"], a["sq"], a["k"], a["sk"], a["v"], a["sv"], a["decay"], a["beta"], a["starts"], a["si"], a["so"],
+                                a["out"], a["N"], a["S"], a["hk"], a["hv"], a["D"], a["scale"], a["eps"], a["ws"], a["n"], None)
+
+
+@pytest.mark.parametrize("kw,status,needle", [
+    (dict(N=-1), INVALID, "N = -1"), (dict(S=65536), INVALID, "S = 65536"), (dict(hk=3), INVALID, "v_heads = 4 must be a multiple"),
+    (dict(D=32), UNSUPPORTED, "D = 32"), (dict(scale=float("inf")), INVALID, "scale"), (dict(eps=float("nan")), INVALID, "norm_eps"),
+    (dict(q=None), INVALID, "q is NULL"), (dict(sk=8), INVALID, "k_stride = 8"), (dict(sv=511), INVALID, "v_stride"),
+    (dict(beta=None), INVALID, "beta"), (dict(starts=None), INVALID, "starts"), (dict(si=FAKE + 4), INVALID, "state_in"),
+    (dict(so=FAKE + 6 * MB + 16), INVALID, "state_out overlaps state_in"), (dict(out=FAKE + 2 * MB), INVALID, "out overlaps v"),
+    (dict(out=FAKE + 8 * MB), INVALID, "out overlaps the states"), (dict(ws=None), WORKSPACE, "needed"), (dict(n=1000), WORKSPACE, "1000 bytes given"),
+    (dict(ws=FAKE + 16 * MB + 64), INVALID, "workspace"),
+])
+def test_delta_prompt_refusals(kw, status, needle):
+    refused(prompt(**kw), status, needle)
+
+
+def test_delta_prompt_workspace():
+    assert B.ts_hc_delta_prompt_workspace_bytes(100, 3, 2, 4, 128) == (100 // 64 + 3) * 4 * 33792
+    assert B.ts_hc_delta_prompt_workspace_bytes(100, 3, 2, 5, 128) == 0
+    assert B.ts_hc_delta_prompt_workspace_bytes(1 << 30, 65535, 2, 64, 128) == ((1 << 24) + 65535) * 64 * 33792  # past 32 bits
+
+
 def logprobs(**kw):
     a = dict(logits=FAKE, type=B.TS_LOGITS_FP32, stride=1000, tokens=FAKE + MB, logp=FAKE + 2 * MB, entropy=FAKE + 3 * MB, ids=FAKE + 4 * MB,
              best=FAKE + 5 * MB, N=4, V=1000, J=2, top=3)
@@ -127,6 +155,8 @@ def test_nothing_to_do():
     assert attention(S=0, q=None) == B.TS_OK
     assert step(B=0, q=None) == B.TS_OK
     assert step(T=0, q=None, out=None) == B.TS_OK
+    assert prompt(N=0, q=None, ws=None) == B.TS_OK
+    assert prompt(S=0, q=None, ws=None) == B.TS_OK
     assert logprobs(N=0, logits=None) == B.TS_OK
 
 
