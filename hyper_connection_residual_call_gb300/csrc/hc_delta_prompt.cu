@@ -2,41 +2,44 @@
 // tokens on the tensor cores (ts_hc_delta_prompt in include/ts_hc.h).
 //
 // Within a chunk that begins with the state S0 (D x D), with G_i the sum of the decays'
-// logarithms up to token i, k_i and q_i of norm 1 (their norms' inverses are r_i and, with
-// the scale, s_i), the updates u_i of
+// logarithms up to token i, and r_i, s_i the inverses of the norms of k_i, q_i (s_i with the
+// scale), the updates u_i of
 //     S <- e^g S,  u = beta (v - S^T k),  S <- S + k u^T,  o = scale S^T q
 // are the rows of  U = T R,  with
-//     R_i = v_i - e^(G_i) r_i (S0^T k_i),       T = (I + A)^-1 diag(beta),
+//     R_i = v_i - e^(G_i) r_i X_i,   X_i = S0^T k_i,     T = (I + A)^-1 diag(beta),
 //     A_ij = beta_i r_i r_j (k_i . k_j) e^(G_i - G_j)  for j < i, else 0,
 // and then
 //     o_i = e^(G_i) s_i (S0^T q_i) + sum_{j <= i} P_ij u_j,   P_ij = s_i r_j (q_i . k_j) e^(G_i - G_j)
 //     S1  = e^(G_64) S0 + sum_j k_j w_j u_j^T,                 w_j = r_j e^(G_64 - G_j).
 //
-// What does not depend on the state is one kernel's, a block a chunk and key head: the
+// What does not depend on the state is one kernel's, a block a chunk and value head: the
 // products of keys and queries with keys, T by inverting blocks of 16 and joining them, P
-// and the factors, in fp32; T and P are written as sums of two bf16 and in the order in
-// which the second kernel's tensor cores want them, so that they come by one bulk copy.
+// and the factors, in fp32, written in the order in which the second kernel's tensor cores
+// want them, so that they come by bulk copies.
 //
-// The second kernel walks a sequence's chunks, a block a value head. A TMEM lane is a
-// column of the state. Two threads a lane keep that column in fp32 registers, half each;
-// every operand that is made on the way (the state, R, U, w U) goes back to TMEM as an A
-// operand's rows, so that nothing is exchanged between threads, and keys, queries, T and P
-// are B operands as they lie in shared memory:
-//     X = S0^T K^T   ->  R  ->   U = R T^T   ->   w U   ->   dS = (w U)^T K   ->   S1
-// and beside that chain Y = S0^T Q^T and Z = U P^T, the outputs' two parts.
+// The second kernel walks a sequence's chunks, a CTA a value head. A TMEM lane is a column of
+// the state. Operands that are made on the way (the state, R, U, w U) go back to TMEM as
+// rows of A operands, from the threads that own the lane, so that but for the largest element
+// nothing is exchanged between threads; keys, queries, T and P are B operands in shared memory. From chunk to
+// chunk, X would have to wait for the state; but with S1 put in,
+//     X' = e^(G_64) (S0^T K'^T) + (w U)^T M^T,   M = K' K^T  of this chunk's and the next one's keys,
+// whose first part needs the state before and whose second needs no state: so the chain from
+// chunk to chunk is  M's product -> R -> T's product -> w U,  and what is the state's (its
+// update, its split, the next chunk's S0^T K'^T) and the outputs fall into the waits for T's and
+// for M's product. A column has two threads; the state stays in their fp32 registers.
 //
-// Each of these operands is split into two bf16 (16 bits of significand), and each product
-// into two or three: a state is off by some 2^-17 of the terms that made it, a chunk. (With
-// one bf16 an operand it would be 2^-9.) Keys and queries are bf16 as they are; their norms
-// are in the factors.
-//
-// What bounds it: the chain. A chunk's products take 1400 cycles of it, the work in between
-// some 1000 instructions a scheduler, and there are three round trips.
+// Each operand is scaled by a power of two (a column of the state, of R and of U by its own, a
+// row of P, a key and a query by its own, T by one) and rounded to fp16: to the sum of two, 22
+// bits of significand, wherever it goes on into the state, and to one, 11 bits, where it goes to
+// the outputs alone, which are bf16. Keys and queries are exact (down to 2^-25 of their
+// row's largest). As sums of two bf16, 16 bits, states were off by some 1e-5; so it is that
+// of fp32's own sums.
 //
 // An infinity or a NaN reaches the outputs from its token on and the state, and nothing
 // before: factors of a chunk's tokens from a bad key, decay or beta on make R a NaN, and a
 // lane sets its R to 0 from the first that is not finite, and its outputs and state to NaN.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -51,24 +54,75 @@ namespace {
 
 constexpr unsigned kStatusInvalidArg = 1u;   // TS_ERR_INVALID_ARG of ts_hc.h
 constexpr int kChunk = 64;
-constexpr int kTile = kChunk * 128;           // bytes of a 64 x 64 bf16 tile
-// A record: T's and P's two parts (64 rows of 128 bytes, swizzled), then the factors.
-constexpr int kTh = 0, kTl = kTile, kPh = 2 * kTile, kPl = 3 * kTile, kFactors = 4 * kTile;
-constexpr int kRecord = kFactors + 1024;
+constexpr int kTile = kChunk * 128;           // bytes of a 64 x 64 fp16 tile: 64 rows of 128 bytes, swizzled
 struct Factors {
-    float c[kChunk];          // -e^(G_i) r_i
-    float w[kChunk];          // r_j e^(G_64 - G_j)
-    float y[kChunk];          // e^(G_i) s_i
+    float c[kChunk];          // -e^(G_i) r_i, r with the key's power of two
+    float w[kChunk];          // r_j e^(G_64 - G_j), by a power of two so that the largest is in [1, 2)
+    float y[kChunk];          // e^(G_i) s_i, s with the query's power of two
+    float p[kChunk];          // what undoes the powers of two of P's rows
     float keep;               // e^(G_64)
+    float t, w_undo;          // what undoes T's power of two, and w's
 };
-static_assert(sizeof(Factors) <= kRecord - kFactors, "a record's factors");
+constexpr int kFactorBytes = 1040;
+static_assert(sizeof(Factors) <= kFactorBytes && kFactorBytes % 16 == 0, "a record's factors");
+// What the first kernel leaves: of a chunk and key head, keys, the chunk's keys with the one's before (M, two parts),
+// queries; of a chunk and value head, T's two parts, P, the factors.
+template <int D>
+struct Record {
+    static constexpr int kRows = kChunk * D * 2;  // bytes of a chunk's keys, queries or values
+    static constexpr int kK = 0, kM = kRows, kQ = kRows + 2 * kTile, kKeyBytes = 2 * kRows + 2 * kTile;
+    static constexpr int kT = 0, kP = 2 * kTile, kFactors = 3 * kTile, kValueBytes = 3 * kTile + kFactorBytes;
+};
 constexpr float kNoDecay = -120.f;            // e^-120 is 0 in fp32; sums of -infinities would be no numbers
 constexpr float kNaN = __builtin_nanf("");
 
-// Records lie by value head, and within one by the sequence's first token / 64, plus the sequence, plus the chunk:
+// Records lie by head, and within one by the sequence's first token / 64, plus the sequence, plus the chunk:
 // no two sequences' overlap, and nobody needs a sum over the sequences before.
 __host__ __device__ inline long record_slots(int N, int S) { return (long)N / kChunk + S; }
 __device__ __forceinline__ long record_of(int start, int seq, int chunk) { return (long)(start / kChunk) + seq + chunk; }
+template <int D>
+__device__ __forceinline__ uint8_t *key_record(const DeltaPromptParams &p, int hk, long slot)
+{
+    return p.work + ((size_t)hk * record_slots(p.N, p.S) + slot) * Record<D>::kKeyBytes;
+}
+template <int D>
+__device__ __forceinline__ uint8_t *value_record(const DeltaPromptParams &p, int h, long slot)
+{
+    const size_t slots = record_slots(p.N, p.S);
+    return p.work + (size_t)p.Hk * slots * Record<D>::kKeyBytes + ((size_t)h * slots + slot) * Record<D>::kValueBytes;
+}
+
+// The power of two that brings values of up to `most` (bits of a float) to less than 2^14, and what undoes it: fp16
+// holds 2^-24 of them, and what is left of the first of two parts 2^-38.
+struct Scale {
+    float by, undo;
+    __device__ __forceinline__ explicit Scale(uint32_t most)
+    {
+        const uint32_t e = min(267u - (most >> 23), 253u);
+        by = __uint_as_float(e << 23);
+        undo = __uint_as_float((254u - e) << 23);
+    }
+};
+
+// Eight values times `by` (a pair of factors for each pair of them) as two fp16 each. In the order written: one pair
+// after the other, as a compiler short of registers has it, it is a chain of some 30 cycles a pair.
+__device__ __forceinline__ void split8(const uint64_t v0, const uint64_t v1, const uint64_t v2, const uint64_t v3, const uint64_t by, uint32_t *hi,
+                                       uint32_t *lo)
+{
+    asm volatile(
+        "{\n\t.reg .b64 t0, t1, t2, t3;\n\t.reg .f32 a0, a1, a2, a3, z0, z1, z2, z3;\n\t.reg .b32 m0, m1, m2, m3;\n\t"
+        ".reg .b16 l0, l1, l2, l3, h0, h1, h2, h3;\n\t"
+        "mul.rn.f32x2 t0, %8, %12;\n\tmul.rn.f32x2 t1, %9, %12;\n\tmul.rn.f32x2 t2, %10, %12;\n\tmul.rn.f32x2 t3, %11, %12;\n\t"
+        "mov.b64 {a0, z0}, t0;\n\tmov.b64 {a1, z1}, t1;\n\tmov.b64 {a2, z2}, t2;\n\tmov.b64 {a3, z3}, t3;\n\t"
+        "cvt.rn.f16x2.f32 %0, z0, a0;\n\tcvt.rn.f16x2.f32 %1, z1, a1;\n\tcvt.rn.f16x2.f32 %2, z2, a2;\n\tcvt.rn.f16x2.f32 %3, z3, a3;\n\t"
+        "xor.b32 m0, %0, 0x80008000;\n\txor.b32 m1, %1, 0x80008000;\n\txor.b32 m2, %2, 0x80008000;\n\txor.b32 m3, %3, 0x80008000;\n\t"
+        "mov.b32 {l0, h0}, m0;\n\tmov.b32 {l1, h1}, m1;\n\tmov.b32 {l2, h2}, m2;\n\tmov.b32 {l3, h3}, m3;\n\t"
+        "add.f32.f16 a0, l0, a0;\n\tadd.f32.f16 a1, l1, a1;\n\tadd.f32.f16 a2, l2, a2;\n\tadd.f32.f16 a3, l3, a3;\n\t"
+        "add.f32.f16 z0, h0, z0;\n\tadd.f32.f16 z1, h1, z1;\n\tadd.f32.f16 z2, h2, z2;\n\tadd.f32.f16 z3, h3, z3;\n\t"
+        "cvt.rn.f16x2.f32 %4, z0, a0;\n\tcvt.rn.f16x2.f32 %5, z1, a1;\n\tcvt.rn.f16x2.f32 %6, z2, a2;\n\tcvt.rn.f16x2.f32 %7, z3, a3;\n\t}"
+        : "=&r"(hi[0]), "=&r"(hi[1]), "=&r"(hi[2]), "=&r"(hi[3]), "=&r"(lo[0]), "=&r"(lo[1]), "=&r"(lo[2]), "=&r"(lo[3])
+        : "l"(v0), "l"(v1), "l"(v2), "l"(v3), "l"(by));
+}
 
 // A sequence's rows; false for one that is out of range (recorded).
 __device__ __forceinline__ bool rows_of(const DeltaPromptParams &p, int s, int &lo, int &n)
@@ -83,19 +137,19 @@ __device__ __forceinline__ bool rows_of(const DeltaPromptParams &p, int s, int &
     return false;
 }
 
-// ------------------------------------------------------------------ T, P and the factors
+// ------------------------------------------------------------------ keys and queries, T, P and the factors
 
 constexpr int kPrepThreads = 256;
 constexpr int kPitch = 68;    // floats of a row of a 64 x 64 matrix in shared memory
 
 template <int D>
 struct PrepShared {
-    uint16_t k[kChunk][D + 8], q[kChunk][D + 8];
-    float kk[kChunk][kPitch], qk[kChunk][kPitch];
-    float a[kChunk][kPitch], t[kChunk][kPitch], tmp[32][36];
-    float r[kChunk], s[kChunk];                    // the inverse norms
+    uint16_t k[kChunk][D + 8], q[kChunk][D + 8];   // fp16; q's place is the keys before's in the end
+    alignas(16) float a[kChunk][kPitch], t[kChunk][kPitch], tmp[32][36];  // keys with keys, then A; queries with keys, then T
+    float r[kChunk], s[kChunk];                    // the inverse norms, with the powers of two
     float gh[kChunk], gl[kChunk], beta[kChunk];    // G in two parts
-    int bad_key, bad;                              // the first token with an infinity or a NaN
+    int bad;                                       // the first token with an infinity or a NaN
+    uint32_t most_t;
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void *at)
@@ -106,35 +160,98 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void *at)
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Eight values as two bf16 each, to piece x of row i of two tiles.
+// 16 rows of x (from `row`) with 8 kCols rows of y (from `col`).
+template <int D, int kCols>
+__device__ __forceinline__ void rows_with_rows(const uint16_t (*x)[D + 8], int row, const uint16_t (*y)[D + 8], int col, float (&d)[kCols][4])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            d[i][c] = 0.f;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+        uint32_t a[4];
+        ldmatrix4(a, &x[row + (lane & 15)][s * 16 + (lane >> 4) * 8]);
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) {  // 16 columns: two tiles' two halves of the sum's 16 terms
+            uint32_t b[4];
+            ldmatrix4(b, &y[col + i * 16 + (lane >> 4) * 8 + (lane & 7)][s * 16 + ((lane >> 3) & 1) * 8]);
+            mma16816(d[2 * i], a, b[0], b[1]);
+            mma16816(d[2 * i + 1], a, b[2], b[3]);
+        }
+    }
+}
+
+__device__ __forceinline__ int piece_at(int row, int x) { return row * 128 + ((x ^ (row & 7)) << 4); }
+
+// Eight values as two fp16 each (or one), to piece x of row i of two tiles.
+template <bool kTwo>
 __device__ __forceinline__ void put8(uint8_t *hi, uint8_t *lo, int i, int x, const float (&v)[8])
 {
     uint32_t h[4], l[4];
+    if (kTwo) {
+        split8(f32x2(v[0], v[1]), f32x2(v[2], v[3]), f32x2(v[4], v[5]), f32x2(v[6], v[7]), f32x2(1.f, 1.f), h, l);
+    } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        h[c] = pack2_bf16(v[2 * c], v[2 * c + 1]);
-        l[c] = pack2_bf16(v[2 * c] - bf16_lo(h[c]), v[2 * c + 1] - bf16_hi(h[c]));
+        for (int c = 0; c < 4; ++c)
+            h[c] = pack2_f16(v[2 * c], v[2 * c + 1]);
     }
-    const int at = i * 128 + ((x ^ (i & 7)) << 4);
-    *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    *reinterpret_cast<uint4 *>(hi + piece_at(i, x)) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (kTwo)
+        *reinterpret_cast<uint4 *>(lo + piece_at(i, x)) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// A row's piece x of 8 elements, of the D / 8 lanes that share it: scaled by a power of two so that the row's largest
+// is in [1, 2), as fp16. Returns the row's sum of squares (before); `undo`: the power of two back.
+template <int D>
+__device__ __forceinline__ float row_to_half(const uint16_t *src, bool there, int x, uint16_t *to, float &undo, bool &odd)
+{
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (there)
+        w = *reinterpret_cast<const uint4 *>(src + x * 8);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    float sum = 0.f;
+    uint32_t most = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        sum = fmaf(bf16_lo(u[c]), bf16_lo(u[c]), sum);
+        sum = fmaf(bf16_hi(u[c]), bf16_hi(u[c]), sum);
+        most = max(most, max((u[c] << 16) & 0x7F800000u, u[c] & 0x7F800000u));
+    }
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    }
+    odd = most == 0x7F800000u;
+    const uint32_t e = min(most >> 23, 253u);
+    const float by = e == 0 || odd ? 1.f : __uint_as_float((254u - e) << 23);
+    undo = e == 0 || odd ? 1.f : __uint_as_float(e << 23);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        reinterpret_cast<uint32_t *>(to + x * 8)[c] = pack2_f16(bf16_lo(u[c]) * by, bf16_hi(u[c]) * by);
+    return sum;
+}
+
+// A block a chunk and value head. The first of a key head's value heads writes the keys' record.
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads) hc_delta_prep_kernel(const DeltaPromptParams p)
 {
+    using Rec = Record<D>;
     extern __shared__ uint4 smem4[];
     auto &sh = *reinterpret_cast<PrepShared<D> *>(smem4);
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long slots = record_slots(p.N, p.S);
-    const long slot = blockIdx.x / p.Hk;
-    const int hk = (int)(blockIdx.x - slot * p.Hk);
+    const long slot = blockIdx.x / p.Hv;
+    const int h = (int)(blockIdx.x - slot * p.Hv), group = p.Hv / p.Hk, hk = h / group;
+    const bool writes = h == hk * group;
     // the sequence whose records this one is among: the last that begins at or before it
     int seq = 0;
     for (int lo = 0, hi = p.S - 1; lo < hi;) {
@@ -153,252 +270,318 @@ __global__ void __launch_bounds__(kPrepThreads) hc_delta_prep_kernel(const Delta
         return;
     first += (int)chunk * kChunk;
     const int n = min(kChunk, len - (int)chunk * kChunk);
-    if (tid == 0)
-        sh.bad_key = n;
+    uint8_t *const key_rec = key_record<D>(p, hk, slot), *const rec = value_record<D>(p, h, slot);
+    // the gates are asked for first, by the warp that adds them up
+    float decay[2] = {0.f, 0.f}, beta[2] = {0.f, 0.f};
+    if (warp == 0)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (2 * lane + i < n) {
+                decay[i] = p.decay[(size_t)(first + 2 * lane + i) * p.Hv + h];
+                beta[i] = p.beta[(size_t)(first + 2 * lane + i) * p.Hv + h];
+            }
+    if (tid == 0) {
+        sh.bad = n;
+        sh.most_t = 0;
+    }
     __syncthreads();
 
-    // keys and queries, zeros after the last token, and their norms: D / 8 lanes a row
+    // keys and queries, zeros after the last token, and their norms
     constexpr int kPieces = D / 8;
+#pragma unroll
     for (int i = tid; i < kChunk * kPieces * 2; i += kPrepThreads) {
         const bool query = i >= kChunk * kPieces;
         const int r = i / kPieces % kChunk, x = i % kPieces;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (r < n)
-            w = *reinterpret_cast<const uint4 *>((query ? p.q + (size_t)(first + r) * p.q_stride : p.k + (size_t)(first + r) * p.k_stride) +
-                                                 (size_t)hk * D + x * 8);
-        *reinterpret_cast<uint4 *>(query ? &sh.q[r][x * 8] : &sh.k[r][x * 8]) = w;
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        float sum = 0.f;
-        bool odd = false;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            sum = fmaf(bf16_lo(u[c]), bf16_lo(u[c]), sum);
-            sum = fmaf(bf16_hi(u[c]), bf16_hi(u[c]), sum);
-            odd |= !(fabsf(bf16_lo(u[c])) < INFINITY) || !(fabsf(bf16_hi(u[c])) < INFINITY);
-        }
-#pragma unroll
-        for (int o = kPieces / 2; o > 0; o >>= 1)
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (odd && !query)
-            atomicMin(&sh.bad_key, r);
+        const uint16_t *src = query ? p.q + (size_t)(first + r) * p.q_stride : p.k + (size_t)(first + r) * p.k_stride;
+        float undo;
+        bool odd;
+        const float sum = row_to_half<D>(src + (size_t)hk * D, r < n, x, query ? sh.q[r] : sh.k[r], undo, odd);
         if (x == 0) {
-            const float inv = p.norm_eps >= 0.f ? 1.f / sqrtf(sum + p.norm_eps) : 1.f;
-            if (query)
+            const float inv = (p.norm_eps >= 0.f ? 1.f / sqrtf(sum + p.norm_eps) : 1.f) * undo;
+            if (query) {
                 sh.s[r] = inv * p.scale;
-            else
+            } else {
                 sh.r[r] = inv;
+                if (odd || !(inv < INFINITY))
+                    atomicMin(&sh.bad, r);
+            }
         }
     }
     __syncthreads();
 
+    if (warp == 0) {
+        // the decays' sums in 64 bits, kept as two floats: differences of near ones are right after strong decays too
+        int bad = sh.bad;
+        double x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!(decay[i] < INFINITY) || !(fabsf(beta[i]) < INFINITY))
+                bad = min(bad, 2 * lane + i);
+            x[i] = fmaxf(decay[i], kNoDecay);
+        }
+        bad = __reduce_min_sync(0xFFFFFFFFu, bad);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (2 * lane + i >= bad) {
+                x[i] = 0.0;
+                beta[i] = 0.f;
+            }
+        x[1] += x[0];
+        double pre = x[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xFFFFFFFFu, pre, o);
+            if (lane >= o)
+                pre += y;
+        }
+        const double all = __shfl_sync(0xFFFFFFFFu, pre, 31), before = pre - x[1];
+        auto &f = *reinterpret_cast<Factors *>(rec + Rec::kFactors);
+        float w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            const double G = before + x[i];
+            sh.gh[r] = (float)G;
+            sh.gl[r] = (float)(G - (float)G);
+            sh.beta[r] = beta[i];
+            const float e = expf((float)G);
+            f.c[r] = r < bad ? -e * sh.r[r] : r < n ? kNaN : 0.f;
+            w[i] = r < bad ? expf((float)(all - G)) * sh.r[r] : 0.f;
+            f.y[r] = e * sh.s[r];
+        }
+        const uint32_t top = min(max(__reduce_max_sync(0xFFFFFFFFu, max(__float_as_uint(w[0]), __float_as_uint(w[1]))) >> 23, 1u), 253u);
+        const float w_by = __uint_as_float((254u - top) << 23);
+        *reinterpret_cast<float2 *>(&f.w[2 * lane]) = make_float2(w[0] * w_by, w[1] * w_by);
+        if (lane == 0) {
+            f.keep = expf((float)all);
+            f.w_undo = __uint_as_float(top << 23);
+            sh.bad = bad;
+        }
+    }
     // keys with keys (warps 0-3) and queries with keys (4-7), 16 rows a warp
     {
         const int row = (warp & 3) * 16;
-        const bool query = warp >= 4;
         float d[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                d[i][c] = 0.f;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-            uint32_t a[4];
-            const int ar = row + (lane & 15), ac = s * 16 + (lane >> 4) * 8;
-            ldmatrix4(a, query ? &sh.q[ar][ac] : &sh.k[ar][ac]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // 16 columns: two tiles' two halves of the sum's 16 terms
-                uint32_t b[4];
-                ldmatrix4(b, &sh.k[i * 16 + (lane >> 4) * 8 + (lane & 7)][s * 16 + ((lane >> 3) & 1) * 8]);
-                mma16816(d[2 * i], a, b[0], b[1]);
-                mma16816(d[2 * i + 1], a, b[2], b[3]);
-            }
-        }
+        rows_with_rows<D, 8>(warp >= 4 ? sh.q : sh.k, row, sh.k, 0, d);
+        float (*const to)[kPitch] = warp >= 4 ? sh.t : sh.a;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float *to = query ? &sh.qk[row + (lane >> 2)][i * 8 + (lane & 3) * 2] : &sh.kk[row + (lane >> 2)][i * 8 + (lane & 3) * 2];
-            *reinterpret_cast<float2 *>(to) = make_float2(d[i][0], d[i][1]);
-            *reinterpret_cast<float2 *>(to + 8 * kPitch) = make_float2(d[i][2], d[i][3]);
+            float *at = &to[row + (lane >> 2)][i * 8 + (lane & 3) * 2];
+            *reinterpret_cast<float2 *>(at) = make_float2(d[i][0], d[i][1]);
+            *reinterpret_cast<float2 *>(at + 8 * kPitch) = make_float2(d[i][2], d[i][3]);
         }
     }
+    if (writes)
+        for (int i = tid; i < kChunk * kPieces * 2; i += kPrepThreads) {
+            const bool query = i >= kChunk * kPieces;
+            const int r = i / kPieces % kChunk, x = i % kPieces;
+            *reinterpret_cast<uint4 *>(key_rec + (query ? Rec::kQ : Rec::kK) + (x >> 3) * kTile + piece_at(r, x & 7)) =
+                *reinterpret_cast<const uint4 *>(query ? &sh.q[r][x * 8] : &sh.k[r][x * 8]);
+        }
+    __syncthreads();
 
-    const int group = p.Hv / p.Hk;
-    for (int g = 0; g < group; ++g) {
-        const int h = hk * group + g;
-        uint8_t *const rec = p.work + ((size_t)h * slots + slot) * kRecord;
-        auto &f = *reinterpret_cast<Factors *>(rec + kFactors);
-        __syncthreads();                           // the products, and the head before
-        if (warp == 0) {
-            // the decays' sums in 64 bits, kept as two floats: differences of near ones are right after strong decays too
-            double x[2];
-            float bt[2];
-            int bad = sh.bad_key;
+    // A, in place, and P, 16 columns of a row a thread, a row's by a power of two of its own
+    const int bad = sh.bad;
+    {
+        const int i = tid >> 2, j0 = (tid & 3) * 16;
+        const float gh = sh.gh[i], gl = sh.gl[i], bi = sh.beta[i] * sh.r[i], si = sh.s[i];
+        float pv[16];
+        uint32_t most = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 2 * lane + i;
-                float d = 0.f;
-                bt[i] = 0.f;
-                if (r < n) {
-                    d = p.decay[(size_t)(first + r) * p.Hv + h];
-                    bt[i] = p.beta[(size_t)(first + r) * p.Hv + h];
-                    if (!(d < INFINITY) || !(fabsf(bt[i]) < INFINITY) || !(sh.r[r] < INFINITY))
-                        bad = min(bad, r);
-                    d = fmaxf(d, kNoDecay);
-                }
-                x[i] = d;
-            }
-            bad = __reduce_min_sync(0xFFFFFFFFu, bad);
+        for (int c = 0; c < 16; c += 4) {
+            float4 *const at = reinterpret_cast<float4 *>(&sh.a[i][j0 + c]);
+            const float4 kk = *at, qk = *reinterpret_cast<const float4 *>(&sh.t[i][j0 + c]);
+            const float kv[4] = {kk.x, kk.y, kk.z, kk.w}, qv[4] = {qk.x, qk.y, qk.z, qk.w};
+            float av[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (2 * lane + i >= bad) {
-                    x[i] = 0.0;
-                    bt[i] = 0.f;
-                }
-            x[1] += x[0];
-            double pre = x[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xFFFFFFFFu, pre, o);
-                if (lane >= o)
-                    pre += y;
-            }
-            const double all = __shfl_sync(0xFFFFFFFFu, pre, 31), before = pre - x[1];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 2 * lane + i;
-                const double G = before + x[i];
-                sh.gh[r] = (float)G;
-                sh.gl[r] = (float)(G - (float)G);
-                sh.beta[r] = bt[i];
-                const float e = expf((float)G);
-                f.c[r] = r < bad ? -e * sh.r[r] : r < n ? kNaN : 0.f;
-                f.w[r] = r < bad ? expf((float)(all - G)) * sh.r[r] : 0.f;
-                f.y[r] = e * sh.s[r];
-            }
-            if (lane == 0) {
-                f.keep = expf((float)all);
-                sh.bad = bad;
-            }
-        }
-        __syncthreads();
-        const int bad = sh.bad;
-        // A and P, 8 columns of a row a time
-        for (int u = tid; u < kChunk * 8; u += kPrepThreads) {
-            const int i = u >> 3, x = u & 7;
-            const float gh = sh.gh[i], gl = sh.gl[i], bi = sh.beta[i] * sh.r[i], si = sh.s[i];
-            float pv[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const int j = x * 8 + c;
+            for (int d = 0; d < 4; ++d) {
+                const int j = j0 + c + d;
                 const bool in = j <= i && i < bad;
-                const float e = in ? expf((gh - sh.gh[j]) + (gl - sh.gl[j])) * sh.r[j] : 0.f;
-                sh.a[i][j] = in && j < i ? bi * sh.kk[i][j] * e : 0.f;
-                pv[c] = in ? si * sh.qk[i][j] * e : 0.f;
+                // (the exponential's error, |x| 2^-24 of it or so, is at most 2^-25 of 1)
+                const float e = in ? __expf((gh - sh.gh[j]) + (gl - sh.gl[j])) * sh.r[j] : 0.f;
+                av[d] = in && j < i ? bi * kv[d] * e : 0.f;
+                pv[c + d] = in ? si * qv[d] * e : 0.f;
+                most = max(most, __float_as_uint(pv[c + d]) & 0x7FFFFFFFu);
             }
-            put8(rec + kPh, rec + kPl, i, x, pv);
+            *at = make_float4(av[0], av[1], av[2], av[3]);
         }
+        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+        const Scale sp(most);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float v[8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                v[d] = pv[c * 8 + d] * sp.by;
+            put8<false>(rec + Rec::kP, nullptr, i, (tid & 3) * 2 + c, v);
+        }
+        if ((tid & 3) == 0)
+            reinterpret_cast<Factors *>(rec + Rec::kFactors)->p[i] = sp.undo;
+    }
+    __syncthreads();
+    // T = (I + A)^-1: the blocks of 16 on the diagonal, a thread a column; the blocks above them are 0
+    if (tid < kChunk) {
+        const int b = tid & 48, j = tid & 15;
+        float t[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < i; ++k)
+                sum[k & 3] = fmaf(sh.a[b + i][b + k], t[k], sum[k & 3]);
+            t[i] = i < j ? 0.f : i == j ? 1.f : -((sum[0] + sum[1]) + (sum[2] + sum[3]));
+            sh.t[b + i][b + j] = t[i];
+        }
+    } else {
+        for (int u = tid - kChunk; u < kChunk * kChunk; u += kPrepThreads - kChunk)
+            if ((u & 63) >> 4 > u >> 10)
+                sh.t[u >> 6][u & 63] = 0.f;
+    }
+    __syncthreads();
+    // (T11 0; T21 T22) has T21 = -T22 A21 T11: two pairs of blocks of 16, then one of 32
+    {
+        const int pair = tid >> 7, i = (tid >> 3) & 15, j = (tid & 7) * 2, b = pair * 32;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float a = sh.a[b + 16 + i][b + k];
+            const float2 t = *reinterpret_cast<const float2 *>(&sh.t[b + k][b + j]);
+            s0 = fmaf(a, t.x, s0);
+            s1 = fmaf(a, t.y, s1);
+        }
+        *reinterpret_cast<float2 *>(&sh.tmp[pair * 16 + i][j]) = make_float2(s0, s1);
         __syncthreads();
-        // T = (I + A)^-1: the blocks of 16 on the diagonal, a thread a column; the others' upper halves are 0
-        if (tid < kChunk) {
-            const int b = tid & 48, j = tid & 15;
-            float t[16];
+        s0 = s1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float sum = 0.f;
-#pragma unroll
-                for (int k = 0; k < i; ++k)
-                    sum = fmaf(sh.a[b + i][b + k], t[k], sum);
-                t[i] = i < j ? 0.f : i == j ? 1.f : -sum;
-                sh.t[b + i][b + j] = t[i];
-            }
-        } else {
-            for (int u = tid - kChunk; u < kChunk * kChunk; u += kPrepThreads - kChunk)
-                if ((u & 63) >> 4 > u >> 10)
-                    sh.t[u >> 6][u & 63] = 0.f;
+        for (int k = 0; k < 16; ++k) {
+            const float a = sh.t[b + 16 + i][b + 16 + k];
+            const float2 t = *reinterpret_cast<const float2 *>(&sh.tmp[pair * 16 + k][j]);
+            s0 = fmaf(a, t.x, s0);
+            s1 = fmaf(a, t.y, s1);
         }
+        *reinterpret_cast<float2 *>(&sh.t[b + 16 + i][b + j]) = make_float2(-s0, -s1);
         __syncthreads();
-        // (T11 0; T21 T22) has T21 = -T22 A21 T11: two pairs of blocks of 16, then one of 32
-        {
-            const int pair = tid >> 7, i = (tid >> 3) & 15, j = (tid & 7) * 2, b = pair * 32;
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float a = sh.a[b + 16 + i][b + k];
-                s0 = fmaf(a, sh.t[b + k][b + j], s0);
-                s1 = fmaf(a, sh.t[b + k][b + j + 1], s1);
-            }
-            sh.tmp[pair * 16 + i][j] = s0;
-            sh.tmp[pair * 16 + i][j + 1] = s1;
-            __syncthreads();
-            s0 = s1 = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float a = sh.t[b + 16 + i][b + 16 + k];
-                s0 = fmaf(a, sh.tmp[pair * 16 + k][j], s0);
-                s1 = fmaf(a, sh.tmp[pair * 16 + k][j + 1], s1);
-            }
-            sh.t[b + 16 + i][b + j] = -s0;
-            sh.t[b + 16 + i][b + j + 1] = -s1;
-            __syncthreads();
-        }
-        {
-            const int i = tid >> 3, j = (tid & 7) * 4;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    {
+        const int i = tid >> 3, j = (tid & 7) * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-                const float a = sh.a[32 + i][k];
-                const float4 t = *reinterpret_cast<const float4 *>(&sh.t[k][j]);
-                s = make_float4(fmaf(a, t.x, s.x), fmaf(a, t.y, s.y), fmaf(a, t.z, s.z), fmaf(a, t.w, s.w));
-            }
-            *reinterpret_cast<float4 *>(&sh.tmp[i][j]) = s;
-            __syncthreads();
-            s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-                const float a = sh.t[32 + i][32 + k];
-                const float4 t = *reinterpret_cast<const float4 *>(&sh.tmp[k][j]);
-                s = make_float4(fmaf(a, t.x, s.x), fmaf(a, t.y, s.y), fmaf(a, t.z, s.z), fmaf(a, t.w, s.w));
-            }
-            *reinterpret_cast<float4 *>(&sh.t[32 + i][j]) = make_float4(-s.x, -s.y, -s.z, -s.w);
-            __syncthreads();
+        for (int k = 0; k < 32; ++k) {
+            const float a = sh.a[32 + i][k];
+            const float4 t = *reinterpret_cast<const float4 *>(&sh.t[k][j]);
+            s = make_float4(fmaf(a, t.x, s.x), fmaf(a, t.y, s.y), fmaf(a, t.z, s.z), fmaf(a, t.w, s.w));
         }
-        for (int u = tid; u < kChunk * 8; u += kPrepThreads) {
-            const int i = u >> 3, x = u & 7;
-            float tv[8];
+        *reinterpret_cast<float4 *>(&sh.tmp[i][j]) = s;
+        __syncthreads();
+        s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+            const float a = sh.t[32 + i][32 + k];
+            const float4 t = *reinterpret_cast<const float4 *>(&sh.tmp[k][j]);
+            s = make_float4(fmaf(a, t.x, s.x), fmaf(a, t.y, s.y), fmaf(a, t.z, s.z), fmaf(a, t.w, s.w));
+        }
+        *reinterpret_cast<float4 *>(&sh.t[32 + i][j]) = make_float4(-s.x, -s.y, -s.z, -s.w);
+        __syncthreads();
+    }
+    float tv[2][8];
+    {
+        const int i = tid >> 2, x = (tid & 3) * 2;
+        uint32_t most = 0;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                tv[c] = sh.t[i][x * 8 + c] * sh.beta[x * 8 + c];
-            put8(rec + kTh, rec + kTl, i, x, tv);
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int d = 0; d < 8; d += 4) {
+                const int j = (x + c) * 8 + d;
+                const float4 t = *reinterpret_cast<const float4 *>(&sh.t[i][j]);
+                tv[c][d] = t.x * sh.beta[j];
+                tv[c][d + 1] = t.y * sh.beta[j + 1];
+                tv[c][d + 2] = t.z * sh.beta[j + 2];
+                tv[c][d + 3] = t.w * sh.beta[j + 3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    most = max(most, __float_as_uint(tv[c][d + e]) & 0x7FFFFFFFu);
+            }
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        if (lane == 0)
+            atomicMax(&sh.most_t, most);
+        __syncthreads();
+        const Scale st(sh.most_t);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                tv[c][d] *= st.by;
+            put8<true>(rec + Rec::kT, rec + Rec::kT + kTile, i, x + c, tv[c]);
+        }
+        if (tid == 0)
+            reinterpret_cast<Factors *>(rec + Rec::kFactors)->t = st.undo;
+    }
+    if (!writes || chunk == 0)
+        return;
+    // M: the keys with those of the chunk before, which is whole
+#pragma unroll
+    for (int i = tid; i < kChunk * kPieces; i += kPrepThreads) {
+        const int r = i / kPieces, x = i % kPieces;
+        float undo;
+        bool odd;
+        row_to_half<D>(p.k + (size_t)(first - kChunk + r) * p.k_stride + (size_t)hk * D, true, x, sh.q[r], undo, odd);
+    }
+    __syncthreads();
+    {
+        const int row = (warp & 3) * 16, col = (warp >> 2) * 32;
+        float d[4][4];
+        rows_with_rows<D, 4>(sh.k, row, sh.q, col, d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float *at = &sh.a[row + (lane >> 2)][col + i * 8 + (lane & 3) * 2];
+            *reinterpret_cast<float2 *>(at) = make_float2(d[i][0], d[i][1]);
+            *reinterpret_cast<float2 *>(at + 8 * kPitch) = make_float2(d[i][2], d[i][3]);
+        }
+    }
+    __syncthreads();
+    {
+        const int i = tid >> 2, x = (tid & 3) * 2;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float4 u = *reinterpret_cast<const float4 *>(&sh.a[i][(x + c) * 8]), w = *reinterpret_cast<const float4 *>(&sh.a[i][(x + c) * 8 + 4]);
+            const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+            put8<true>(key_rec + Rec::kM, key_rec + Rec::kM + kTile, i, x + c, v);
         }
     }
 }
 
 // ------------------------------------------------------------------ the walk over the chunks
 
-constexpr int kColThreads = 256, kThreads = kColThreads + 128;  // two threads a column; the products, the copies, and two idle warps
+// Two threads a column (in warps w and w + 4), which have 32 tokens of a chunk and half of the state each and do all of its
+// work; then the products, the copies, two idle warps. (The chain's, the state's and the outputs' work in threads of their
+// own ran side by side, but their code, some 50 KB, did not fit the instruction cache: 7000 cycles a chunk.)
+constexpr int kColumnThreads = 256, kThreads = kColumnThreads + 128;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kColRegs = 216, kOtherRegs = 72;  // 256 * 216 + 128 * 72 = 64512 = 384 * 168, what the launch has
+constexpr int kColumnRegs = 216, kOtherRegs = 72;  // 256 * 216 + 128 * 72 = 64512 = 384 * 168, what the launch has
 constexpr uint32_t kTmemCols = 512;
-// TMEM columns. Where an operand takes an accumulator's place, each half of the threads writes over the 32 columns
-// that it read itself: the high parts of its 32 tokens, then the low ones.
-constexpr uint32_t kS = 0, kX = 128, kU = 192, kY = 256, kZ = 320, kDS = 384;  // kX: X, R, U; kU: U, w U
+// TMEM columns: the state's two parts; S0^T K'^T, then the second half of the state's update; M's product, then R's two
+// parts; T's product, then w U's two parts; the outputs' two; the first half of the state's update, then U.
+constexpr uint32_t kS = 0, kXA = 128, kXB = 192, kU = 256, kY = 320, kZ = 384, kDS = 448;
 
+// Shared memory: what is used from one chunk into the next, three of them; the rest twice.
 template <int D>
-struct Stage {
-    static constexpr int kRows = kChunk * D * 2;   // bytes of a chunk's keys, queries or values
-    static constexpr int kK = 0, kQ = kRows, kV = 2 * kRows, kMat = 3 * kRows;
-    static constexpr int kBytes = 3 * kRows + kRecord;                 // a multiple of 1024
-    static constexpr int kTotal = 2 * kBytes + 1024;
-    static_assert(kBytes % 1024 == 0, "a tile's alignment");
+struct Plan {
+    using Rec = Record<D>;
+    static constexpr int kA = 3, kB = 2, kC = 2, kF = 4;                   // places of (K, M), (T, V), (Q, P), factors
+    static constexpr int kABytes = Rec::kRows + 2 * kTile, kBBytes = 2 * kTile + Rec::kRows, kCBytes = Rec::kRows + kTile;
+    static constexpr int kAt = 0, kBt = kA * kABytes, kCt = kBt + kB * kBBytes, kFt = kCt + kC * kCBytes;
+    static constexpr int kTotal = kFt + kF * kFactorBytes + 1024;                   // and alignment
 };
 
 struct Shared {
-    uint64_t full[2], empty[2];
-    uint64_t s_ready, r_ready, w_ready, y_free;  // of the columns' threads
-    uint64_t x_done, u_done, d_done, o_done;     // of the products
+    uint64_t a_full[3], a_empty[3], b_full[2], b_empty[2], c_full[2], c_empty[2], f_full[4];
+    uint64_t s_ready, r_ready, w_ready, y_free;             // of the columns' threads
+    uint64_t x_done, u_done, da_done, db_done, o_done;      // of the products
     uint32_t tmem;
     int dead;
-    int bad[2][128];                             // by chunks in turn: a lane's first token that is not finite
+    int bad[2][2][128];                          // by chunks in turn and halves: a lane's first token that is not finite
+    float top_r[2][128], top_u[2][128], top_s[2][128];  // what a column's two threads tell one another
 };
 
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Shared &sh, unsigned *status)
@@ -425,24 +608,29 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Shared &sh,
     return __all_sync(0xFFFFFFFFu, there);
 }
 
-// Two values as two bf16 each.
-__device__ __forceinline__ void split2(uint64_t v, uint32_t &hi, uint32_t &lo)
+template <int N>
+__device__ __forceinline__ uint64_t pair_of(const uint32_t (&x)[N], int c) { return f32x2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])); }
+constexpr uint64_t kMinusZeros = 0x8000000080000000ull;
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) { return ffma2(a, b, kMinusZeros); }
+// The larger of |a|, |b| and |c|: a NaN if one of them is.
+__device__ __forceinline__ float most3(float a, float b, float c)
+{
+    float y;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float most_of(float most, uint64_t v)
 {
     float a, z;
     f32x2_unpack(v, a, z);
-    hi = pack2_bf16(a, z);
-    f32x2_unpack(fadd2(v, f32x2(-bf16_lo(hi), -bf16_hi(hi))), a, z);
-    lo = pack2_bf16(a, z);
+    return most3(most, a, z);
 }
 
-__device__ __forceinline__ uint64_t pair_of(const uint32_t (&x)[32], int c) { return f32x2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])); }
-
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-hc_delta_scan_kernel(const __grid_constant__ DeltaPromptParams p, const __grid_constant__ CUtensorMap map_q,
-                     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
+__global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid_constant__ DeltaPromptParams p, const __grid_constant__ CUtensorMap map_v)
 {
-    using St = Stage<D>;
+    using P = Plan<D>;
+    using Rec = Record<D>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -450,24 +638,31 @@ hc_delta_scan_kernel(const __grid_constant__ DeltaPromptParams p, const __grid_c
     uint8_t *const smem = smem_raw + (base - smem_addr(smem_raw));
     unsigned *const status = p.status;
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 1 + kColThreads / 32);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&sh.a_full[i], 1);
+            mbar_init(&sh.a_empty[i], 1);
         }
-        mbar_init(&sh.s_ready, kColThreads);
-        mbar_init(&sh.r_ready, kColThreads);
-        mbar_init(&sh.w_ready, kColThreads);
-        mbar_init(&sh.y_free, kColThreads);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.b_full[i], 1);
+            mbar_init(&sh.b_empty[i], 1 + kColumnThreads / 32);
+            mbar_init(&sh.c_full[i], 1);
+            mbar_init(&sh.c_empty[i], 1);
+        }
+        for (int i = 0; i < 4; ++i)
+            mbar_init(&sh.f_full[i], 1);
+        mbar_init(&sh.s_ready, kColumnThreads);
+        mbar_init(&sh.y_free, kColumnThreads);
+        mbar_init(&sh.r_ready, kColumnThreads);
+        mbar_init(&sh.w_ready, kColumnThreads);
         mbar_init(&sh.x_done, 1);
         mbar_init(&sh.u_done, 1);
-        mbar_init(&sh.d_done, 1);
+        mbar_init(&sh.da_done, 1);
+        mbar_init(&sh.db_done, 1);
         mbar_init(&sh.o_done, 1);
         sh.dead = 0;
         mbar_fence_init();
         fence_async_shared();
     }
-    if (tid < 256)
-        sh.bad[tid >> 7][tid & 127] = kChunk;
     if (warp == kMmaWarp) {
         tmem_alloc(&sh.tmem, kTmemCols);
         tmem_relinquish();
@@ -483,257 +678,371 @@ hc_delta_scan_kernel(const __grid_constant__ DeltaPromptParams p, const __grid_c
     if (!rows_of(p, seq, first, len))
         len = 0;
     const int chunks = (len + kChunk - 1) / kChunk;
+    const int col = tid & 127;                      // of the threads that have one
+    const bool there = col < D;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const auto factors = [&](int ch) -> const Factors & { return *reinterpret_cast<const Factors *>(smem + P::kFt + (ch % P::kF) * kFactorBytes); };
 
+    // (In the columns' threads a wait that ran out ends nothing: they go on through the same barriers, on
+    // whatever lies there, and every further wait returns at once.)
     if (warp < kMmaWarp) {
-        // ---------------------------------------------------------- a column's two threads
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kColRegs));
-        const int half = warp >> 2, col = (warp & 3) * 32 + lane;
-        const bool there = col < D;
-        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        constexpr int kMine = D / 2;                // elements of the column that a thread has
-        const size_t state_at = (((size_t)seq * p.Hv + h) * D + half * kMine) * D + col;
+        // ---------------------------------------------------------- the columns
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kColumnRegs));
+        const int half = warp >> 2, t0 = half * 32;
+        const auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };  // the two warps of these columns
+        // of each 64 elements of the column a thread has 32
+        const size_t state_at = (((size_t)seq * p.Hv + h) * D + half * 32) * D + col, step = (size_t)p.Hv * D;
+        constexpr int kMine = D / 2;
         float s[kMine];
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
-            s[i] = there ? p.state_in[state_at + (size_t)i * D] : 0.f;
-        const auto state_out = [&] {                // the state as an A operand: D / 4 columns a half and part
-            uint32_t hi[16], lo[16];
+            s[i] = there ? p.state_in[state_at + (size_t)((i >> 5) * 64 + (i & 31)) * D] : 0.f;
+        float keep = 1.f, s_undo, y_by = 0.f, z_by = 0.f, w_undo = 0.f;  // of the chunk before, and what undoes the scales
+        int bad = kChunk;                           // of the chunk before
+        const auto to_operand = [&] {               // the state, D / 2 columns a part
+            float tops[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kMine; i += 2)
+                tops[(i >> 1) & 3] = most3(tops[(i >> 1) & 3], s[i], s[i + 1]);
+            const float most = most3(most3(tops[0], tops[1], tops[2]), tops[3], 0.f);
+            sh.top_s[half][col] = most;
+            meet();
+            const Scale sc(__float_as_uint(most3(most, sh.top_s[half ^ 1][col], 0.f)));
+            s_undo = sc.undo;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < kMine / 32; ++i) {
+                uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    split2(f32x2(s[32 * i + 2 * c], s[32 * i + 2 * c + 1]), hi[c], lo[c]);
-                tmem_st16_async(lane_base + kS + half * (D / 2) + 16 * i, hi);
-                tmem_st16_async(lane_base + kS + half * (D / 2) + D / 4 + 16 * i, lo);
+                for (int c = 0; c < 16; c += 4) {
+                    const float *const e = s + 32 * i + 2 * c;
+                    split8(f32x2(e[0], e[1]), f32x2(e[2], e[3]), f32x2(e[4], e[5]), f32x2(e[6], e[7]), f32x2(sc.by, sc.by), hi + c, lo + c);
+                }
+                tmem_st16_async(lane_base + kS + 32 * i + 16 * half, hi);
+                tmem_st16_async(lane_base + kS + D / 2 + 32 * i + 16 * half, lo);
             }
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&sh.s_ready);
         };
-        if (chunks > 0)
-            state_out();
-        // (A wait that ran out ends nothing here: the warps go on through the same barriers, on whatever lies
-        // there, and every further wait returns at once.)
-#pragma unroll 1
-        for (int ch = 0; ch < chunks; ++ch) {
-            const int stage = ch & 1, n = min(kChunk, len - ch * kChunk), t0 = half * 32;
-            const uint32_t phase = ch & 1;
-            const uint8_t *const at = smem + stage * St::kBytes;
-            const auto &f = *reinterpret_cast<const Factors *>(at + St::kMat + kFactors);
-            uint32_t x[32], hi[16], lo[16];
-            // R
-            wait(&sh.full[stage], (ch >> 1) & 1, sh, status);
-            uint32_t v[32];
+        // the state after chunk ch
+        const auto update = [&](int ch) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-                v[c] = there && t0 + c < n ? (uint32_t) reinterpret_cast<const uint16_t *>(at + St::kV)[(t0 + c) * D + col] << 16 : 0u;
-            wait(&sh.x_done, phase, sh, status);
-            tc_fence_after();
-            if (half == 0)                          // both threads of the column have read the last chunk's
-                *reinterpret_cast<volatile int *>(&sh.bad[stage ^ 1][col]) = kChunk;
-            tmem_ld32(lane_base + kX + t0, x);
-            uint64_t odd = 0;                       // 0 times every element: a NaN if one is not finite
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const float2 k = *reinterpret_cast<const float2 *>(&f.c[t0 + 2 * c]);
-                const uint64_t r = ffma2(pair_of(x, c), f32x2(k.x, k.y), pair_of(v, c));
-                odd = ffma2(r, 0, odd);
-                split2(r, hi[c], lo[c]);
-            }
-            float odd0, odd1;
-            f32x2_unpack(odd, odd0, odd1);
-            const bool fine = odd0 == 0.f && odd1 == 0.f;
-            if (!__all_sync(0xFFFFFFFFu, fine || !there)) {  // zeros from the first that is not finite
-                bool gone = false;
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float r = fmaf(__uint_as_float(x[c]), f.c[t0 + c], __uint_as_float(v[c]));
-                    if (!gone && !(fabsf(r) < INFINITY)) {
-                        gone = true;
-                        atomicMin(&sh.bad[stage][col], t0 + c);
-                    }
-                    if (gone) {
-                        hi[c / 2] &= c & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                        lo[c / 2] &= c & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                    }
-                }
-            }
-            __syncwarp();
-            tmem_st16_async(lane_base + kX + t0, hi);
-            tmem_st16_async(lane_base + kX + t0 + 16, lo);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&sh.r_ready);
-            // U and w U
-            wait(&sh.u_done, phase, sh, status);
-            tc_fence_after();
-            tmem_ld32(lane_base + kU + t0, x);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const float2 w = *reinterpret_cast<const float2 *>(&f.w[t0 + 2 * c]);
-                split2(ffma2(pair_of(x, c), f32x2(w.x, w.y), 0x8000000080000000ull), hi[c], lo[c]);
-            }
-            tmem_st16_async(lane_base + kU + t0, hi);
-            tmem_st16_async(lane_base + kU + t0 + 16, lo);
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-                split2(pair_of(x, c), hi[c], lo[c]);
-            tmem_st16_async(lane_base + kX + t0, hi);
-            tmem_st16_async(lane_base + kX + t0 + 16, lo);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&sh.w_ready);
-            // the state
-            const float keep = f.keep;
-            wait(&sh.d_done, phase, sh, status);
-            tc_fence_after();
-            const int bad = *reinterpret_cast<volatile int *>(&sh.bad[stage][col]);
-#pragma unroll
-            for (int i = 0; i < kMine / 32; ++i) {
-                tmem_ld32(lane_base + kDS + half * kMine + 32 * i, x);
+            for (int j = 0; j < D / 64; ++j) {
+                wait(j == 0 ? &sh.da_done : &sh.db_done, ch & 1, sh, status);
+                tc_fence_after();
+                uint32_t x[32];
+                tmem_ld32(lane_base + (j == 0 ? kDS : kXA) + t0, x);
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
-                    s[32 * i + c] = fmaf(s[32 * i + c], keep, __uint_as_float(x[c]));
+                    s[32 * j + c] = fmaf(s[32 * j + c], keep, __uint_as_float(x[c]) * w_undo);
             }
             if (bad < kChunk)
 #pragma unroll
                 for (int i = 0; i < kMine; ++i)
                     s[i] = kNaN;
-            if (ch + 1 < chunks)
-                state_out();
-            // the outputs
-            wait(&sh.o_done, phase, sh, status);
+        };
+        // chunk ch's outputs
+        const auto outputs = [&](int ch) {
+            const Factors &f = factors(ch);
+            const int n = min(kChunk, len - ch * kChunk) - t0;
+            wait(&sh.o_done, ch & 1, sh, status);
             tc_fence_after();
-            tmem_ld32(lane_base + kY + t0, x);
-            tmem_ld32(lane_base + kZ + t0, v);
+            uint32_t y[32], z[32];
+            __syncwarp();
+            tmem_ld32_async(lane_base + kY + t0, y);
+            tmem_ld32_async(lane_base + kZ + t0, z);
+            tmem_wait_ld32(y);
+            tmem_wait_ld32(z);
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                const float4 fy = *reinterpret_cast<const float4 *>(&f.y[t0 + c]), fp = *reinterpret_cast<const float4 *>(&f.p[t0 + c]);
+                const float a[4] = {fy.x, fy.y, fy.z, fy.w}, b[4] = {fp.x, fp.y, fp.z, fp.w};
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const float o = fmaf(a[d] * y_by, __uint_as_float(y[c + d]), b[d] * z_by * __uint_as_float(z[c + d]));
+                    y[c + d] = __float_as_uint(t0 + c + d >= bad ? kNaN : o);
+                }
+            }
             tc_fence_before();
             mbar_arrive(&sh.y_free);
-            uint16_t *const out = p.out + ((size_t)(first + ch * kChunk + t0) * p.Hv + h) * D + col;
+            uint16_t *const to = p.out + (size_t)(first + ch * kChunk + t0) * step + (size_t)h * D + col;
+            if (!there)
+                return;
+            if (n >= 32) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                float o = fmaf(f.y[t0 + c], __uint_as_float(x[c]), __uint_as_float(v[c]));
-                o = t0 + c >= bad ? kNaN : o;
-                if (there && t0 + c < n)
-                    out[(size_t)c * p.Hv * D] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+                for (int c = 0; c < 32; ++c)
+                    to[c * step] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(y[c])));
+            } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c < n)
+                        to[c * step] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(y[c])));
+            }
+        };
+        if (chunks > 0)
+            to_operand();
+#pragma unroll 1
+        for (int ch = 0; ch < chunks; ++ch) {
+            const int n = min(kChunk, len - ch * kChunk) - t0, turn = ch & 1;
+            const uint32_t phase = ch & 1;
+            // R
+            wait(&sh.f_full[ch % P::kF], (ch / P::kF) & 1, sh, status);
+            wait(&sh.b_full[ch % P::kB], (ch / P::kB) & 1, sh, status);
+            const Factors &f = factors(ch);
+            const uint16_t *const v = reinterpret_cast<const uint16_t *>(smem + P::kBt + (ch % P::kB) * P::kBBytes + 2 * kTile) + t0 * D + col;
+            uint32_t vw[16];                        // two tokens' values
+            if (n >= 32) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    vw[c] = there ? v[2 * c * D] | (uint32_t)v[(2 * c + 1) * D] << 16 : 0u;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    vw[c] = (there && 2 * c < n ? v[2 * c * D] : 0u) | (there && 2 * c + 1 < n ? (uint32_t)v[(2 * c + 1) * D] << 16 : 0u);
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&sh.empty[stage]);
+                mbar_arrive(&sh.b_empty[ch % P::kB]);
+            wait(&sh.x_done, phase, sh, status);
+            tc_fence_after();
+            uint64_t r[16];
+            float tops[4] = {0.f, 0.f, 0.f, 0.f};
+            {
+                uint32_t x[32], z[32];
+                tmem_ld32_async(lane_base + kXA + t0, x);
+                tmem_ld32_async(lane_base + kXB + t0, z);  // (before the second chunk: whatever lies there)
+                // the first part is of the state before the chunk before
+                const float xa = s_undo * keep;
+                const uint64_t xa2 = f32x2(xa, xa), xb2 = f32x2(w_undo, w_undo);
+                tmem_wait_ld32(x);
+                tmem_wait_ld32(z);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    r[c] = fmul2(pair_of(x, c), xa2);
+                if (ch > 0)
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        r[c] = ffma2(pair_of(z, c), xb2, r[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const float2 k = *reinterpret_cast<const float2 *>(&f.c[t0 + 2 * c]);
+                r[c] = ffma2(r[c], f32x2(k.x, k.y), f32x2(bf16_lo(vw[c]), bf16_hi(vw[c])));
+                tops[c & 3] = most_of(tops[c & 3], r[c]);
+            }
+            float most = most3(most3(tops[0], tops[1], tops[2]), tops[3], 0.f);
+            int gone = kChunk;
+            if (__builtin_expect(!__all_sync(0xFFFFFFFFu, most < INFINITY), 0)) {  // zeros from the first that is not finite
+                most = 0.f;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    float a, z;
+                    f32x2_unpack(r[c], a, z);
+                    if (gone == kChunk && !(fabsf(a) < INFINITY))
+                        gone = t0 + 2 * c;
+                    a = gone == kChunk ? a : 0.f;
+                    if (gone == kChunk && !(fabsf(z) < INFINITY))
+                        gone = t0 + 2 * c + 1;
+                    z = gone == kChunk ? z : 0.f;
+                    r[c] = f32x2(a, z);
+                    most = most_of(most, r[c]);
+                }
+            }
+            sh.bad[turn][half][col] = gone;
+            sh.top_r[half][col] = most;
+            meet();                                 // (both have read their products, too)
+            const Scale sr(__float_as_uint(fmaxf(most, sh.top_r[half ^ 1][col])));
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int c = 0; c < 16; c += 4)
+                split8(r[c], r[c + 1], r[c + 2], r[c + 3], f32x2(sr.by, sr.by), hi + c, lo + c);
+            __syncwarp();
+            tmem_st16_async(lane_base + kXB + t0 / 2, hi);
+            tmem_st16_async(lane_base + kXB + 32 + t0 / 2, lo);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&sh.r_ready);
+            // the state, while T's product runs
+            if (ch > 0) {
+                y_by = s_undo;                      // of the outputs of the chunk before
+                update(ch - 1);
+                to_operand();
+            }
+            // U and w U, with one scale: w is at most 2
+            const float u_by = sr.undo * f.t, w_by = f.w_undo;
+            wait(&sh.u_done, phase, sh, status);
+            tc_fence_after();
+            uint32_t x[32];
+            tmem_ld32(lane_base + kU + t0, x);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                tops[c & 3] = most3(c < 4 ? 0.f : tops[c & 3], __uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+            most = most3(most3(tops[0], tops[1], tops[2]), tops[3], 0.f);
+            sh.top_u[half][col] = most;
+            meet();                                 // (both have read the state's update, too)
+            const Scale su(__float_as_uint(fmaxf(most, sh.top_u[half ^ 1][col])));  // of the products as they came
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const float2 w = *reinterpret_cast<const float2 *>(&f.w[t0 + 2 * c]);
+                r[c] = fmul2(pair_of(x, c), f32x2(w.x, w.y));
+                x[c] = pack2_f16(__uint_as_float(x[2 * c]) * su.by, __uint_as_float(x[2 * c + 1]) * su.by);
+            }
+#pragma unroll
+            for (int c = 0; c < 16; c += 4)
+                split8(r[c], r[c + 1], r[c + 2], r[c + 3], f32x2(su.by, su.by), hi + c, lo + c);
+            __syncwarp();
+            tmem_st16_async(lane_base + kU + t0 / 2, hi);
+            tmem_st16_async(lane_base + kU + 32 + t0 / 2, lo);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                hi[c] = x[c];
+            tmem_st16_async(lane_base + kDS + t0 / 2, hi);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&sh.w_ready);
+            // the outputs of the chunk before, while M's product runs
+            if (ch > 0)
+                outputs(ch - 1);
+            keep = f.keep;
+            z_by = su.undo * u_by;
+            w_undo = z_by * w_by;
+            bad = min(sh.bad[turn][0][col], sh.bad[turn][1][col]);
+        }
+        if (chunks > 0) {
+            y_by = s_undo;
+            update(chunks - 1);
+            outputs(chunks - 1);
         }
         if (there && (chunks > 0 || p.state_out != p.state_in))
 #pragma unroll
             for (int i = 0; i < kMine; ++i)
-                p.state_out[state_at + (size_t)i * D] = s[i];
+                p.state_out[state_at + (size_t)((i >> 5) * 64 + (i & 31)) * D] = s[i];
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kMmaWarp) {
             // ---------------------------------------------------------- products
-            constexpr uint32_t kIdesc = umma_idesc_bf16(128, kChunk), kIdescS = umma_idesc_bf16(128, D) | kIdescBMnMajor;
-            bool ok = true;
-#pragma unroll 1
-            for (int ch = 0; ok && ch < chunks; ++ch) {
-                const int stage = ch & 1, n = min(kChunk, len - ch * kChunk);
-                const uint32_t phase = ch & 1, at = base + stage * St::kBytes;
-                ok = wait(&sh.full[stage], (ch >> 1) & 1, sh, status);
-                if (!ok)
-                    break;
-                if (n < kChunk) {  // keys after the last are another sequence's: their products with zeros have to be zeros
-                    for (int i = lane; i < (kChunk - n) * (D / 8); i += 32) {
-                        const int r = n + i / (D / 8), x = i % (D / 8);
-                        *reinterpret_cast<uint4 *>(smem + stage * St::kBytes + St::kK + (x >> 3) * kTile + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_shared();
-                    __syncwarp();
-                }
-                const uint32_t k = desc_lo(at + St::kK, 16), q = desc_lo(at + St::kQ, 16);
-                // one operand of D terms in TMEM (the state), the other's rows in shared memory
-                const auto by_state = [&](uint32_t to, uint32_t b) {
+            constexpr uint32_t kIdesc = umma_idesc_f16(128, kChunk);
+            const auto place_a = [&](int ch) { return base + P::kAt + (ch % P::kA) * P::kABytes; };
+            const auto place_b = [&](int ch) { return base + P::kBt + (ch % P::kB) * P::kBBytes; };
+            const auto place_c = [&](int ch) { return base + P::kCt + (ch % P::kC) * P::kCBytes; };
+            const auto full_a = [&](int ch) { return wait(&sh.a_full[ch % P::kA], (ch / P::kA) & 1, sh, status); };
+            // the state's parts with 64 rows of D elements
+            const auto by_state = [&](uint32_t to, uint32_t rows, int parts) {
+                const uint32_t b = desc_lo(rows, 16);
+                for (int part = 0; part < parts; ++part)
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int i = 0; i < D / 16; ++i)
+                        umma_bf16_ts_lo(tmem + to, tmem + kS + part * (D / 2) + i * 8, b + (((i >> 2) * kTile + (i & 3) * 32) >> 4), kIdesc, part + i > 0);
+            };
+            // 64 tokens' part at `from` with 64 rows of 64 elements
+            const auto by_tokens = [&](uint32_t to, uint32_t from, uint32_t rows, uint32_t more) {
+                const uint32_t b = desc_lo(rows, 16);
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            const int of = i / (D / 32), in = i % (D / 32);  // the half of the column
-                            umma_bf16_ts_lo(tmem + to, tmem + kS + of * (D / 2) + part * (D / 4) + in * 8, b + (((i >> 2) * kTile + (i & 3) * 32) >> 4), kIdesc,
-                                            part + i > 0);
-                        }
-                };
-                // ... of 64 tokens, and 64 rows of a record's tile
-                const auto by_tokens = [&](uint32_t to, uint32_t from, int part, int tile, uint32_t more) {
-                    const uint32_t b = desc_lo(at + St::kMat + tile, 16);
+                for (int i = 0; i < 4; ++i)
+                    umma_bf16_ts_lo(tmem + to, tmem + from + i * 8, b + i * 2, kIdesc, more + i > 0);
+            };
+            // ... both in two parts
+            const auto by_tokens2 = [&](uint32_t to, uint32_t from, uint32_t rows) {
+                by_tokens(to, from, rows, 0);
+                by_tokens(to, from + 32, rows, 1);
+                by_tokens(to, from, rows + kTile, 1);
+            };
+            // half j of the state's update
+            const auto update = [&](int ch, int j) {
+                const uint32_t k = desc_lo(place_a(ch) + j * kTile, kTile);
+                for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        umma_bf16_ts_lo(tmem + to, tmem + from + (i >> 1) * 32 + part * 16 + (i & 1) * 8, b + ((i * 32) >> 4), kIdesc, more + i > 0);
-                };
-                ok = wait(&sh.s_ready, phase, sh, status);
-                if (!ok)
-                    break;
+                        umma_bf16_ts_lo(tmem + (j == 0 ? kDS : kXA), tmem + kU + part * 32 + i * 8, k + i * (2048 >> 4), kIdesc | kIdescBMnMajor, part + i > 0);
+                umma_commit(j == 0 ? &sh.da_done : &sh.db_done);
+                if (j == D / 64 - 1)
+                    umma_commit(&sh.a_empty[ch % P::kA]);
+            };
+            bool ok = chunks > 0 && full_a(0) && wait(&sh.s_ready, 0, sh, status);
+            if (ok) {
                 tc_fence_after();
                 if (elect_one()) {
-                    by_state(kX, k);
+                    by_state(kXA, place_a(0), 2);
                     umma_commit(&sh.x_done);
                 }
                 __syncwarp();
-                if (ch > 0) {
-                    ok = wait(&sh.y_free, phase ^ 1, sh, status);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                }
-                if (elect_one())
-                    by_state(kY, q);
-                __syncwarp();
-                ok = wait(&sh.r_ready, phase, sh, status);
+            }
+#pragma unroll 1
+            for (int ch = 0; ok && ch < chunks; ++ch) {
+                const uint32_t phase = ch & 1;
+                const bool more = ch + 1 < chunks;
+                ok = wait(&sh.b_full[ch % P::kB], (ch / P::kB) & 1, sh, status) && wait(&sh.r_ready, phase, sh, status);
                 if (!ok)
                     break;
                 tc_fence_after();
                 if (elect_one()) {
-                    by_tokens(kU, kX, 0, kTh, 0);
-                    by_tokens(kU, kX, 1, kTh, 1);
-                    by_tokens(kU, kX, 0, kTl, 1);
+                    if (D > 64 && ch > 0)           // before T's product takes w U's place, and once S0^T K^T has been read
+                        update(ch - 1, 1);
+                    by_tokens2(kU, kXB, place_b(ch));
                     umma_commit(&sh.u_done);
+                    umma_commit(&sh.b_empty[ch % P::kB]);
                 }
+                __syncwarp();
+                ok = (ch == 0 || wait(&sh.s_ready, phase, sh, status)) && (!more || full_a(ch + 1));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (more && elect_one())
+                    by_state(kXA, place_a(ch + 1), 2);
                 __syncwarp();
                 ok = wait(&sh.w_ready, phase, sh, status);
                 if (!ok)
                     break;
                 tc_fence_after();
+                if (more && elect_one()) {
+                    by_tokens2(kXB, kU, place_a(ch + 1) + Rec::kRows);
+                    umma_commit(&sh.x_done);
+                }
+                __syncwarp();
+                ok = wait(&sh.c_full[ch % P::kC], (ch / P::kC) & 1, sh, status) && (ch == 0 || wait(&sh.y_free, phase ^ 1, sh, status));
+                if (!ok)
+                    break;
+                tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t km = desc_lo(at + St::kK, kTile);
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            umma_bf16_ts_lo(tmem + kDS, tmem + kU + (i >> 1) * 32 + part * 16 + (i & 1) * 8, km + i * (2048 >> 4), kIdescS, part + i > 0);
-                    umma_commit(&sh.d_done);
-                    by_tokens(kZ, kX, 0, kPh, 0);
-                    by_tokens(kZ, kX, 1, kPh, 1);
-                    by_tokens(kZ, kX, 0, kPl, 1);
+                    by_state(kY, place_c(ch), 1);
+                    by_tokens(kZ, kDS, place_c(ch) + Rec::kRows, 0);
                     umma_commit(&sh.o_done);
-                    umma_commit(&sh.empty[stage]);
+                    umma_commit(&sh.c_empty[ch % P::kC]);
+                    update(ch, 0);
+                    if (D > 64 && !more)
+                        update(ch, 1);
                 }
                 __syncwarp();
             }
         } else if (warp == kLoadWarp) {
             // ---------------------------------------------------------- copies
-            const long slots = record_slots(p.N, p.S);
-            const uint8_t *const rec = p.work + ((size_t)h * slots + record_of(first, seq, 0)) * kRecord;
+            const long slot = record_of(first, seq, 0);
+            const uint8_t *key = key_record<D>(p, hk, slot), *value = value_record<D>(p, h, slot);
             bool ok = true;
 #pragma unroll 1
-            for (int ch = 0; ok && ch < chunks; ++ch) {
-                const int stage = ch & 1;
-                ok = wait(&sh.empty[stage], ((ch >> 1) & 1) ^ 1, sh, status);
+            for (int ch = 0; ok && ch < chunks; ++ch, key += Rec::kKeyBytes, value += Rec::kValueBytes) {
+                const int a = ch % P::kA, b = ch % P::kB, c = ch % P::kC, f = ch % P::kF;
+                ok = wait(&sh.a_empty[a], ((ch / P::kA) & 1) ^ 1, sh, status);
                 if (ok && lane == 0) {
-                    uint8_t *const to = smem + stage * St::kBytes;
-                    uint64_t *bar = &sh.full[stage];
-                    const int row = first + ch * kChunk;
-                    mbar_arrive_expect_tx(bar, 3 * St::kRows + kRecord);
-                    for (int i = 0; i < D / 64; ++i)
-                        tma_load_3d(to + St::kK + i * kTile, &map_k, i * 64, hk, row, bar);
-                    bulk_copy_g2s(to + St::kMat, rec + (size_t)ch * kRecord, kRecord, bar);
-                    for (int i = 0; i < D / 64; ++i)
-                        tma_load_3d(to + St::kQ + i * kTile, &map_q, i * 64, hk, row, bar);
-                    tma_load_3d(to + St::kV, &map_v, 0, h, row, bar);
+                    mbar_arrive_expect_tx(&sh.a_full[a], P::kABytes);
+                    bulk_copy_g2s(smem + P::kAt + a * P::kABytes, key + Rec::kK, P::kABytes, &sh.a_full[a]);
+                }
+                __syncwarp();
+                ok = ok && wait(&sh.b_empty[b], ((ch / P::kB) & 1) ^ 1, sh, status);
+                if (ok && lane == 0) {
+                    mbar_arrive_expect_tx(&sh.b_full[b], P::kBBytes);
+                    tma_load_3d(smem + P::kBt + b * P::kBBytes + 2 * kTile, &map_v, 0, h, first + ch * kChunk, &sh.b_full[b]);
+                    bulk_copy_g2s(smem + P::kBt + b * P::kBBytes, value + Rec::kT, 2 * kTile, &sh.b_full[b]);
+                    mbar_arrive_expect_tx(&sh.f_full[f], kFactorBytes);
+                    bulk_copy_g2s(smem + P::kFt + f * kFactorBytes, value + Rec::kFactors, kFactorBytes, &sh.f_full[f]);
+                }
+                __syncwarp();
+                ok = ok && wait(&sh.c_empty[c], ((ch / P::kC) & 1) ^ 1, sh, status);
+                if (ok && lane == 0) {
+                    mbar_arrive_expect_tx(&sh.c_full[c], P::kCBytes);
+                    bulk_copy_g2s(smem + P::kCt + c * P::kCBytes, key + Rec::kQ, Rec::kRows, &sh.c_full[c]);
+                    bulk_copy_g2s(smem + P::kCt + c * P::kCBytes + Rec::kRows, value + Rec::kP, kTile, &sh.c_full[c]);
                 }
                 __syncwarp();
             }
@@ -757,19 +1066,17 @@ hc_delta_scan_kernel(const __grid_constant__ DeltaPromptParams p, const __grid_c
 template <int D>
 cudaError_t launch(const DeltaPromptParams &p, cudaStream_t stream)
 {
+    static_assert(Plan<D>::kTotal + sizeof(Shared) <= 227 * 1024 && sizeof(PrepShared<D>) <= 227 * 1024, "shared memory");
     int per_sm = 1;
     cudaError_t e = attn_ready(reinterpret_cast<const void *>(hc_delta_prep_kernel<D>), kPrepThreads, (int)sizeof(PrepShared<D>), &per_sm);
     if (e == cudaSuccess)
-        e = attn_ready(reinterpret_cast<const void *>(hc_delta_scan_kernel<D>), kThreads, Stage<D>::kTotal, &per_sm);
+        e = attn_ready(reinterpret_cast<const void *>(hc_delta_scan_kernel<D>), kThreads, Plan<D>::kTotal, &per_sm);
     if (e != cudaSuccess)
         return e;
-    static_assert(Stage<D>::kTotal + sizeof(Shared) <= 227 * 1024 && sizeof(PrepShared<D>) <= 227 * 1024, "shared memory");
-    CUtensorMap map_q{}, map_k{}, map_v{};
-    if (p.N > 0 && (!tc_make_map_heads(&map_q, p.q, p.N, p.Hk, D, p.q_stride, 1, kChunk) ||
-                    !tc_make_map_heads(&map_k, p.k, p.N, p.Hk, D, p.k_stride, 1, kChunk) ||
-                    !tc_make_map_heads(&map_v, p.v, p.N, p.Hv, D, p.v_stride, 1, kChunk, true)))
+    CUtensorMap map_v{};
+    if (!tc_make_map_heads(&map_v, p.v, p.N, p.Hv, D, p.v_stride, 1, kChunk, true))
         return cudaErrorInvalidValue;
-    e = launch_pdl(hc_delta_prep_kernel<D>, dim3((unsigned)(record_slots(p.N, p.S) * p.Hk)), dim3(kPrepThreads), sizeof(PrepShared<D>), true, stream, p);
+    e = launch_pdl(hc_delta_prep_kernel<D>, dim3((unsigned)(record_slots(p.N, p.S) * p.Hv)), dim3(kPrepThreads), sizeof(PrepShared<D>), true, stream, p);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t lc{};
@@ -781,13 +1088,18 @@ cudaError_t launch(const DeltaPromptParams &p, cudaStream_t stream)
     lc.stream = stream;
     lc.blockDim = dim3(kThreads);
     lc.gridDim = dim3((unsigned)(p.S * p.Hv));
-    lc.dynamicSmemBytes = Stage<D>::kTotal;
-    return cudaLaunchKernelEx(&lc, hc_delta_scan_kernel<D>, p, map_q, map_k, map_v);
+    lc.dynamicSmemBytes = Plan<D>::kTotal;
+    return cudaLaunchKernelEx(&lc, hc_delta_scan_kernel<D>, p, map_v);
 }
 
 }  // namespace
 
-size_t delta_prompt_bytes(int N, int S, int Hv) { return (size_t)record_slots(N, S) * Hv * kRecord; }
+size_t delta_prompt_bytes(int N, int S, int Hk, int Hv, int D)
+{
+    const size_t slots = record_slots(N, S);
+    return D == 64 ? slots * ((size_t)Hk * Record<64>::kKeyBytes + (size_t)Hv * Record<64>::kValueBytes)
+                   : slots * ((size_t)Hk * Record<128>::kKeyBytes + (size_t)Hv * Record<128>::kValueBytes);
+}
 
 cudaError_t launch_delta_prompt(const DeltaPromptParams &p, const LaunchCfg &, cudaStream_t stream)
 {

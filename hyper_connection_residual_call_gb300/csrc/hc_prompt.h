@@ -47,7 +47,7 @@ struct DeltaPromptParams {
     const float *state_in;      // [S][Hv][D][D]
     float *state_out;
     uint16_t *out;              // [N][Hv][D]
-    uint8_t *work;              // one record a chunk and value head
+    uint8_t *work;              // one record a chunk and head
     int N, S, Hk, Hv, D;
     float scale, norm_eps;
     unsigned *status;
@@ -73,7 +73,7 @@ cudaError_t launch_prompt_attention(PromptAttnParams p, const uint16_t *q, long 
 int prompt_attn_heads(int G);
 long prompt_attn_blocks(int N, int S, int q_heads, int kv_heads);
 cudaError_t launch_delta_step(const DeltaStepParams &p, const LaunchCfg &cfg, cudaStream_t stream);
-size_t delta_prompt_bytes(int N, int S, int Hv);
+size_t delta_prompt_bytes(int N, int S, int Hk, int Hv, int D);
 cudaError_t launch_delta_prompt(const DeltaPromptParams &p, const LaunchCfg &cfg, cudaStream_t stream);
 cudaError_t launch_logprobs(const LogprobParams &p, bool bf16, const LaunchCfg &cfg, cudaStream_t stream);
 

@@ -270,7 +270,7 @@ size_t ts_hc_delta_prompt_workspace_bytes(int N, int S, int k_heads, int v_heads
 {
     if (check_count(N, "N", 0, INT_MAX) != TS_OK || check_count(S, "S", 0, kMaxBatch) != TS_OK || check_delta_heads(k_heads, v_heads, D) != TS_OK)
         return 0;
-    return tshc::delta_prompt_bytes(N, S, v_heads);
+    return tshc::delta_prompt_bytes(N, S, k_heads, v_heads, D);
 }
 
 ts_status ts_hc_delta_prompt(const void *q, long q_stride, const void *k, long k_stride, const void *v, long v_stride, const float *decay,
@@ -290,7 +290,7 @@ ts_status ts_hc_delta_prompt(const void *q, long q_stride, const void *k, long k
     TS_TRY(check_ptr_api(starts, "starts", 4));
     if (((long)N / 64 + S) * v_heads > INT_MAX)
         return api_error(TS_ERR_UNSUPPORTED, "%d tokens of %d heads are too many for one call: split them", N, v_heads);
-    const size_t need = tshc::delta_prompt_bytes(N, S, v_heads);
+    const size_t need = tshc::delta_prompt_bytes(N, S, k_heads, v_heads, D);
     if (!workspace || workspace_bytes < need)
         return api_error(TS_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace ? workspace_bytes : (size_t)0, need);
     TS_TRY(check_ptr_api(workspace, "workspace", 256));

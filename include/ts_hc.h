@@ -703,12 +703,13 @@ ts_status ts_hc_delta_step(const void *q, long q_stride, const void *k, long k_s
  *   state_in   fp32 [S][v_heads][D][D]; state_out likewise, which may be state_in. A sequence of no tokens keeps its
  *              state
  *   out        bf16 [N][v_heads][D]; rows of no sequence are not written
- *   workspace  >= ts_hc_delta_prompt_workspace_bytes(...) bytes, 256-byte aligned (some 33 KB for 64 tokens of a value
- *              head); it need not be initialised and must not be shared by calls that can run at the same time
- * The state is held in fp32. What goes into the tensor cores is the keys and queries as they are and every other
- * operand (the state among them) as the sum of two bf16, 16 bits of significand; sums are fp32. An infinity or a NaN
- * in a token's inputs leaves NaNs in the outputs from that token on that it reaches and in the state, and the
- * outputs before it as they are without.
+ *   workspace  >= ts_hc_delta_prompt_workspace_bytes(...) bytes, 256-byte aligned (for 64 tokens of D = 128 some 48 KB a
+ *              key head and 25 KB a value head); it need not be initialised and must not be shared by calls that can
+ *              run at the same time
+ * The state is held in fp32, and what goes into it by the tensor cores has 22 bits of significand (the sum of two
+ * fp16, scaled by its column's largest), and fp32 sums; what goes to the outputs alone has 11. An infinity or a NaN in
+ * a token's inputs leaves NaNs in the outputs from that token on that it reaches and in the state, and does not reach
+ * the outputs before it (whose chunk may take other scales for it: a last bit, at most).
  * Keys are of norm 1 or less in effect (norm_eps >= 0, or made so by the caller) and beta at most 2: with much longer
  * ones the recurrence itself diverges. D is 64 or 128 (TS_ERR_UNSUPPORTED otherwise); v_heads is a multiple of
  * k_heads; S <= 65535. N == 0 is a no-op: state_out is not written either (nor is it by a step with T == 0).

@@ -15,13 +15,14 @@ Tolerances, from the number formats (unit roundoffs: u16 = 2^-8 of bf16, u32 = 2
               two units of the last place), the norms and the update. After T tokens and from an output's own sum:
                 |state err| <= T (D + 16) u32 M + u32 |S|
                 |out err| <= u16 |out| + scale |q| (T + 1) (D + 16) u32 M
-              In chunks, an operand is the sum of two bf16 and off by 2^-17 of itself at most (each part by u16 of
-              itself; what is left of the second counts 2^-16 / 2). With the state's columns and the values within M,
-              X and so R are off by 2^-17 M a token (keys of norm 1); U = T R: T's columns are the effect of one
-              token's value on the later tokens' updates, with sums of squares of at most 2 or so for keys of norm 1,
-              and three such errors (of R, of T, of the product that is left out) of up to sqrt(64) terms of size M:
-              some 3 * 8 * 2^-17 M; the state takes that on, and its own two errors. 40 * 2^-17 M a chunk bounds
-              them; they are not made longer after it. An output has the state's and U's errors: twice that
+              In chunks, an operand on the way to the state is the sum of two fp16, off by 2^-22 of itself or 2^-38 of
+              the largest of its column. With the state's columns and the values within M, X and so R are off by
+              (2^-22 + D u32) M a token (keys of norm 1), U = T R by that and two more 2^-22 of up to sqrt(64) terms
+              of size M times what T does to them (2 or so), U's 64 terms' sums by 64 u32; the state takes that
+              on, and its own errors: (D + 16) u32 M a token as above, over a chunk's 64, bound them. For the outputs
+              the state and U are rounded to 11 bits, P too: 3 2^-12 of terms of size M, of which up to 64 add up as
+              a root of a sum of squares at most (P's rows are within 1): 8 of them
+                |out err| <= u16 |out| + scale (24 2^-12 / 8 + (T + 64) (D + 16) u32) M
   log probabilities  e^d is off by 2 |d| u32 (the product with log2 e) and 2^-22 (the function) of itself, sums
               run over V/1024 elements a thread and then 40 joins: log Z is off by at most
               r = (V/1024 + 100) u32 (the |d| weighted with p add up to less than the entropy, at most 21), so
@@ -38,7 +39,7 @@ from gpu_common import require_gpu
 from hyper_connection_residual_call_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
-U16, U32, SPLIT = 2.0 ** -8, 2.0 ** -24, 2.0 ** -17
+U16, U32 = 2.0 ** -8, 2.0 ** -24
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -401,10 +402,9 @@ def check_prompt(args, at, out, state, norm_eps=1e-6):
     scale = d ** -0.5
     for i, (lo, hi) in enumerate(zip(at[:-1], at[1:])):
         want, after, size = P.delta(q[lo:hi], k[lo:hi], v[lo:hi], decay[lo:hi], beta[lo:hi], before[i], scale, norm_eps)
-        chunks = (hi - lo + 63) // 64
-        step = 40 * SPLIT * size * chunks
+        step = (d + 16) * U32 * size * (hi - lo + 64)
         if hi > lo:
-            within(out[lo:hi], want, U16 * np.abs(want) + scale * 2 * step + 1e-38, "out")
+            within(out[lo:hi], want, U16 * np.abs(want) + scale * (3 * 2.0 ** -12 * size + step) + 1e-38, "out")
         within(state[i], after, step[:, None] + U32 * np.abs(after) + 1e-38, "state")
 
 

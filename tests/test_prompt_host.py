@@ -122,9 +122,11 @@ def test_delta_prompt_refusals(kw, status, needle):
 
 
 def test_delta_prompt_workspace():
-    assert B.ts_hc_delta_prompt_workspace_bytes(100, 3, 2, 4, 128) == (100 // 64 + 3) * 4 * 33792
-    assert B.ts_hc_delta_prompt_workspace_bytes(100, 3, 2, 5, 128) == 0
-    assert B.ts_hc_delta_prompt_workspace_bytes(1 << 30, 65535, 2, 64, 128) == ((1 << 24) + 65535) * 64 * 33792  # past 32 bits
+    of = B.ts_hc_delta_prompt_workspace_bytes
+    one = of(64, 0, 1, 1, 128)
+    assert of(64, 0, 1, 1, 64) < one and of(100, 3, 1, 1, 128) == 4 * one and of(100, 3, 5, 5, 128) == 20 * one
+    assert of(100, 3, 2, 5, 128) == 0 and "v_heads = 5" in B.ts_hc_last_error()
+    assert of(1 << 30, 65535, 64, 64, 128) == ((1 << 24) + 65535) * 64 * one  # past 32 bits
 
 
 def logprobs(**kw):
