@@ -26,7 +26,7 @@
 // whose first part needs the state before and whose second needs no state: so the chain from
 // chunk to chunk is  M's product -> R -> T's product -> w U,  and what is the state's (its
 // update, its split, the next chunk's S0^T K'^T) and the outputs fall into the waits for T's and
-// for M's product. A column has two threads; the state stays in their fp32 registers.
+// for M's product. A column has four threads; the state stays in their fp32 registers.
 //
 // Each operand is scaled by a power of two (a column of the state, of R and of U by its own, a
 // row of P, a key and a query by its own, T by one) and rounded to fp16: to the sum of two, 22
@@ -553,12 +553,13 @@ __global__ void __launch_bounds__(kPrepThreads) hc_delta_prep_kernel(const Delta
 
 // ------------------------------------------------------------------ the walk over the chunks
 
-// Two threads a column (in warps w and w + 4), which have 32 tokens of a chunk and half of the state each and do all of its
-// work; then the products, the copies, two idle warps. (The chain's, the state's and the outputs' work in threads of their
-// own ran side by side, but their code, some 50 KB, did not fit the instruction cache: 7000 cycles a chunk.)
-constexpr int kColumnThreads = 256, kThreads = kColumnThreads + 128;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kColumnRegs = 216, kOtherRegs = 72;  // 256 * 216 + 128 * 72 = 64512 = 384 * 168, what the launch has
+// Four threads a column (in warps w, w + 4, ..), which have 16 tokens of a chunk and a quarter of the state each and do all of
+// its work; then the products, the copies, two idle warps. (Two threads a column took 6100 cycles a chunk. The chain's, the
+// state's and the outputs' work in threads of their own ran side by side, but their code, some 50 KB, did not fit the
+// instruction cache: 7000.)
+constexpr int kColumnThreads = 512, kThreads = kColumnThreads + 128;
+constexpr int kMmaWarp = 16, kLoadWarp = 17;
+constexpr int kColumnRegs = 104, kOtherRegs = 64;  // 512 * 104 + 128 * 64 = 61440 = 640 * 96, what the launch has
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns: the state's two parts; S0^T K'^T, then the second half of the state's update; M's product, then R's two
 // parts; T's product, then w U's two parts; the outputs' two; the first half of the state's update, then U.
@@ -580,30 +581,23 @@ struct Shared {
     uint64_t x_done, u_done, da_done, db_done, o_done;      // of the products
     uint32_t tmem;
     int dead;
-    int bad[2][2][128];                          // by chunks in turn and halves: a lane's first token that is not finite
-    float top_r[2][128], top_u[2][128], top_s[2][128];  // what a column's two threads tell one another
+    // What a column's threads tell one another: its first token that is not finite (by chunks in turn), largest elements.
+    int bad[2][4][128];
+    float top_r[4][128], top_u[4][128], top_s[4][128];
 };
 
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Shared &sh, unsigned *status)
+// Waits for the phase; false when it, or another wait of the block, ran out (recorded at the end). Short: what the loop over
+// the chunks has to stay within is the instruction cache.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Shared &sh)
 {
     bool there = mbar_try_wait(bar, parity);
     if (!there) {
         const uint64_t t0 = global_timer_ns();
-        for (;;) {
-            if (*reinterpret_cast<volatile int *>(&sh.dead))
-                break;
-#pragma unroll 1
-            for (int i = 0; i < 16 && !there; ++i)
-                there = mbar_try_wait(bar, parity);
-            if (there)
-                break;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-                *reinterpret_cast<volatile int *>(&sh.dead) = 1;
-                if (status)
-                    atomicExch(status, kStatusTimeout);
-                break;
-            }
-        }
+        do {
+            there = mbar_try_wait(bar, parity);
+        } while (!there && !*reinterpret_cast<volatile int *>(&sh.dead) && global_timer_ns() - t0 < kWaitLimitNs);
+        if (!there)
+            *reinterpret_cast<volatile int *>(&sh.dead) = 1;
     }
     return __all_sync(0xFFFFFFFFu, there);
 }
@@ -636,7 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t *const smem = smem_raw + (base - smem_addr(smem_raw));
-    unsigned *const status = p.status;
     if (tid == 0) {
         for (int i = 0; i < 3; ++i) {
             mbar_init(&sh.a_full[i], 1);
@@ -688,15 +681,18 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
     if (warp < kMmaWarp) {
         // ---------------------------------------------------------- the columns
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kColumnRegs));
-        const int half = warp >> 2, t0 = half * 32;
-        const auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };  // the two warps of these columns
-        // of each 64 elements of the column a thread has 32
-        const size_t state_at = (((size_t)seq * p.Hv + h) * D + half * 32) * D + col, step = (size_t)p.Hv * D;
-        constexpr int kMine = D / 2;
+        const int part = warp >> 2, t0 = part * 16;
+        const auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + (warp & 3)) : "memory"); };  // the four warps of these columns
+        const auto most_of_all = [&](const float (&top)[4][128]) {  // after they met
+            return most3(most3(top[0][col], top[1][col], top[2][col]), top[3][col], 0.f);
+        };
+        // of each 64 elements of the column a thread has 16
+        const size_t state_at = (((size_t)seq * p.Hv + h) * D + t0) * D + col, step = (size_t)p.Hv * D;
+        constexpr int kMine = D / 4;
         float s[kMine];
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
-            s[i] = there ? p.state_in[state_at + (size_t)((i >> 5) * 64 + (i & 31)) * D] : 0.f;
+            s[i] = there ? p.state_in[state_at + (size_t)((i >> 4) * 64 + (i & 15)) * D] : 0.f;
         float keep = 1.f, s_undo, y_by = 0.f, z_by = 0.f, w_undo = 0.f;  // of the chunk before, and what undoes the scales
         int bad = kChunk;                           // of the chunk before
         const auto to_operand = [&] {               // the state, D / 2 columns a part
@@ -704,22 +700,21 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < kMine; i += 2)
                 tops[(i >> 1) & 3] = most3(tops[(i >> 1) & 3], s[i], s[i + 1]);
-            const float most = most3(most3(tops[0], tops[1], tops[2]), tops[3], 0.f);
-            sh.top_s[half][col] = most;
+            sh.top_s[part][col] = most3(most3(tops[0], tops[1], tops[2]), tops[3], 0.f);
             meet();
-            const Scale sc(__float_as_uint(most3(most, sh.top_s[half ^ 1][col], 0.f)));
+            const Scale sc(__float_as_uint(most_of_all(sh.top_s)));
             s_undo = sc.undo;
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < kMine / 32; ++i) {
-                uint32_t hi[16], lo[16];
+            for (int i = 0; i < kMine / 16; ++i) {
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int c = 0; c < 16; c += 4) {
-                    const float *const e = s + 32 * i + 2 * c;
+                for (int c = 0; c < 8; c += 4) {
+                    const float *const e = s + 16 * i + 2 * c;
                     split8(f32x2(e[0], e[1]), f32x2(e[2], e[3]), f32x2(e[4], e[5]), f32x2(e[6], e[7]), f32x2(sc.by, sc.by), hi + c, lo + c);
                 }
-                tmem_st16_async(lane_base + kS + 32 * i + 16 * half, hi);
-                tmem_st16_async(lane_base + kS + D / 2 + 32 * i + 16 * half, lo);
+                tmem_st8_async(lane_base + kS + 32 * i + 8 * part, hi);
+                tmem_st8_async(lane_base + kS + D / 2 + 32 * i + 8 * part, lo);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -729,13 +724,14 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
         const auto update = [&](int ch) {
 #pragma unroll
             for (int j = 0; j < D / 64; ++j) {
-                wait(j == 0 ? &sh.da_done : &sh.db_done, ch & 1, sh, status);
+                wait(j == 0 ? &sh.da_done : &sh.db_done, ch & 1, sh);
                 tc_fence_after();
-                uint32_t x[32];
-                tmem_ld32(lane_base + (j == 0 ? kDS : kXA) + t0, x);
+                uint32_t x[16];
+                tmem_ld16_async(lane_base + (j == 0 ? kDS : kXA) + t0, x);
+                tmem_wait_ld(x);
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    s[32 * j + c] = fmaf(s[32 * j + c], keep, __uint_as_float(x[c]) * w_undo);
+                for (int c = 0; c < 16; ++c)
+                    s[16 * j + c] = fmaf(s[16 * j + c], keep, __uint_as_float(x[c]) * w_undo);
             }
             if (bad < kChunk)
 #pragma unroll
@@ -745,88 +741,73 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
         // chunk ch's outputs
         const auto outputs = [&](int ch) {
             const Factors &f = factors(ch);
-            const int n = min(kChunk, len - ch * kChunk) - t0;
-            wait(&sh.o_done, ch & 1, sh, status);
+            const int n = there ? min(kChunk, len - ch * kChunk) - t0 : 0;
+            wait(&sh.o_done, ch & 1, sh);
             tc_fence_after();
-            uint32_t y[32], z[32];
-            __syncwarp();
-            tmem_ld32_async(lane_base + kY + t0, y);
-            tmem_ld32_async(lane_base + kZ + t0, z);
-            tmem_wait_ld32(y);
-            tmem_wait_ld32(z);
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-                const float4 fy = *reinterpret_cast<const float4 *>(&f.y[t0 + c]), fp = *reinterpret_cast<const float4 *>(&f.p[t0 + c]);
+            uint16_t *to = p.out + (size_t)(first + ch * kChunk + t0) * step + (size_t)h * D + col;
+#pragma unroll 1
+            for (int i = 0; i < 16; i += 4) {       // (a loop for the instruction cache's sake)
+                uint32_t y[4], z[4];
+                __syncwarp();
+                tmem_ld4_async(lane_base + kY + t0 + i, y);
+                tmem_ld4_async(lane_base + kZ + t0 + i, z);
+                const float4 fy = *reinterpret_cast<const float4 *>(&f.y[t0 + i]), fp = *reinterpret_cast<const float4 *>(&f.p[t0 + i]);
+                tmem_wait_ld4(y);
+                tmem_wait_ld4(z);
                 const float a[4] = {fy.x, fy.y, fy.z, fy.w}, b[4] = {fp.x, fp.y, fp.z, fp.w};
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const float o = fmaf(a[d] * y_by, __uint_as_float(y[c + d]), b[d] * z_by * __uint_as_float(z[c + d]));
-                    y[c + d] = __float_as_uint(t0 + c + d >= bad ? kNaN : o);
+                for (int c = 0; c < 4; ++c) {
+                    float o = fmaf(a[c] * y_by, __uint_as_float(y[c]), b[c] * z_by * __uint_as_float(z[c]));
+                    o = t0 + i + c >= bad ? kNaN : o;
+                    if (i + c < n)
+                        *to = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+                    to += step;
                 }
             }
             tc_fence_before();
             mbar_arrive(&sh.y_free);
-            uint16_t *const to = p.out + (size_t)(first + ch * kChunk + t0) * step + (size_t)h * D + col;
-            if (!there)
-                return;
-            if (n >= 32) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    to[c * step] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(y[c])));
-            } else {
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (c < n)
-                        to[c * step] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(y[c])));
-            }
         };
         if (chunks > 0)
             to_operand();
 #pragma unroll 1
         for (int ch = 0; ch < chunks; ++ch) {
-            const int n = min(kChunk, len - ch * kChunk) - t0, turn = ch & 1;
+            const int n = there ? min(kChunk, len - ch * kChunk) - t0 : 0, turn = ch & 1;
             const uint32_t phase = ch & 1;
             // R
-            wait(&sh.f_full[ch % P::kF], (ch / P::kF) & 1, sh, status);
-            wait(&sh.b_full[ch % P::kB], (ch / P::kB) & 1, sh, status);
+            wait(&sh.f_full[ch % P::kF], (ch / P::kF) & 1, sh);
+            wait(&sh.b_full[ch % P::kB], (ch / P::kB) & 1, sh);
             const Factors &f = factors(ch);
             const uint16_t *const v = reinterpret_cast<const uint16_t *>(smem + P::kBt + (ch % P::kB) * P::kBBytes + 2 * kTile) + t0 * D + col;
-            uint32_t vw[16];                        // two tokens' values
-            if (n >= 32) {
+            uint32_t vw[8];                         // two tokens' values
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    vw[c] = there ? v[2 * c * D] | (uint32_t)v[(2 * c + 1) * D] << 16 : 0u;
-            } else {
-#pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    vw[c] = (there && 2 * c < n ? v[2 * c * D] : 0u) | (there && 2 * c + 1 < n ? (uint32_t)v[(2 * c + 1) * D] << 16 : 0u);
-            }
+            for (int c = 0; c < 8; ++c)
+                vw[c] = (2 * c < n ? v[2 * c * D] : 0u) | (2 * c + 1 < n ? (uint32_t)v[(2 * c + 1) * D] << 16 : 0u);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.b_empty[ch % P::kB]);
-            wait(&sh.x_done, phase, sh, status);
+            wait(&sh.x_done, phase, sh);
             tc_fence_after();
-            uint64_t r[16];
+            uint64_t r[8];
             float tops[4] = {0.f, 0.f, 0.f, 0.f};
             {
-                uint32_t x[32], z[32];
-                tmem_ld32_async(lane_base + kXA + t0, x);
-                tmem_ld32_async(lane_base + kXB + t0, z);  // (before the second chunk: whatever lies there)
+                uint32_t x[16], z[16];
+                tmem_ld16_async(lane_base + kXA + t0, x);
+                tmem_ld16_async(lane_base + kXB + t0, z);  // (before the second chunk: whatever lies there)
                 // the first part is of the state before the chunk before
                 const float xa = s_undo * keep;
                 const uint64_t xa2 = f32x2(xa, xa), xb2 = f32x2(w_undo, w_undo);
-                tmem_wait_ld32(x);
-                tmem_wait_ld32(z);
+                tmem_wait_ld(x);
+                tmem_wait_ld(z);
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
+                for (int c = 0; c < 8; ++c)
                     r[c] = fmul2(pair_of(x, c), xa2);
                 if (ch > 0)
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
+                    for (int c = 0; c < 8; ++c)
                         r[c] = ffma2(pair_of(z, c), xb2, r[c]);
             }
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
+            for (int c = 0; c < 8; ++c) {
                 const float2 k = *reinterpret_cast<const float2 *>(&f.c[t0 + 2 * c]);
                 r[c] = ffma2(r[c], f32x2(k.x, k.y), f32x2(bf16_lo(vw[c]), bf16_hi(vw[c])));
                 tops[c & 3] = most_of(tops[c & 3], r[c]);
@@ -836,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             if (__builtin_expect(!__all_sync(0xFFFFFFFFu, most < INFINITY), 0)) {  // zeros from the first that is not finite
                 most = 0.f;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < 8; ++c) {
                     float a, z;
                     f32x2_unpack(r[c], a, z);
                     if (gone == kChunk && !(fabsf(a) < INFINITY))
@@ -849,17 +830,16 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
                     most = most_of(most, r[c]);
                 }
             }
-            sh.bad[turn][half][col] = gone;
-            sh.top_r[half][col] = most;
-            meet();                                 // (both have read their products, too)
-            const Scale sr(__float_as_uint(fmaxf(most, sh.top_r[half ^ 1][col])));
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int c = 0; c < 16; c += 4)
-                split8(r[c], r[c + 1], r[c + 2], r[c + 3], f32x2(sr.by, sr.by), hi + c, lo + c);
+            sh.bad[turn][part][col] = gone;
+            sh.top_r[part][col] = most;
+            meet();                                 // (all have read their products, too)
+            const Scale sr(__float_as_uint(most_of_all(sh.top_r)));
+            uint32_t hi[8], lo[8];
+            split8(r[0], r[1], r[2], r[3], f32x2(sr.by, sr.by), hi, lo);
+            split8(r[4], r[5], r[6], r[7], f32x2(sr.by, sr.by), hi + 4, lo + 4);
             __syncwarp();
-            tmem_st16_async(lane_base + kXB + t0 / 2, hi);
-            tmem_st16_async(lane_base + kXB + 32 + t0 / 2, lo);
+            tmem_st8_async(lane_base + kXB + t0 / 2, hi);
+            tmem_st8_async(lane_base + kXB + 32 + t0 / 2, lo);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&sh.r_ready);
@@ -871,33 +851,29 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             }
             // U and w U, with one scale: w is at most 2
             const float u_by = sr.undo * f.t, w_by = f.w_undo;
-            wait(&sh.u_done, phase, sh, status);
+            wait(&sh.u_done, phase, sh);
             tc_fence_after();
-            uint32_t x[32];
-            tmem_ld32(lane_base + kU + t0, x);
+            uint32_t x[16], us[8];
+            tmem_ld16_async(lane_base + kU + t0, x);
+            tmem_wait_ld(x);
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
+            for (int c = 0; c < 8; ++c)
                 tops[c & 3] = most3(c < 4 ? 0.f : tops[c & 3], __uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
-            most = most3(most3(tops[0], tops[1], tops[2]), tops[3], 0.f);
-            sh.top_u[half][col] = most;
-            meet();                                 // (both have read the state's update, too)
-            const Scale su(__float_as_uint(fmaxf(most, sh.top_u[half ^ 1][col])));  // of the products as they came
+            sh.top_u[part][col] = most3(most3(tops[0], tops[1], tops[2]), tops[3], 0.f);
+            meet();                                 // (all have read the state's update, too)
+            const Scale su(__float_as_uint(most_of_all(sh.top_u)));  // of the products as they came
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
+            for (int c = 0; c < 8; ++c) {
                 const float2 w = *reinterpret_cast<const float2 *>(&f.w[t0 + 2 * c]);
                 r[c] = fmul2(pair_of(x, c), f32x2(w.x, w.y));
-                x[c] = pack2_f16(__uint_as_float(x[2 * c]) * su.by, __uint_as_float(x[2 * c + 1]) * su.by);
+                us[c] = pack2_f16(__uint_as_float(x[2 * c]) * su.by, __uint_as_float(x[2 * c + 1]) * su.by);
             }
-#pragma unroll
-            for (int c = 0; c < 16; c += 4)
-                split8(r[c], r[c + 1], r[c + 2], r[c + 3], f32x2(su.by, su.by), hi + c, lo + c);
+            split8(r[0], r[1], r[2], r[3], f32x2(su.by, su.by), hi, lo);
+            split8(r[4], r[5], r[6], r[7], f32x2(su.by, su.by), hi + 4, lo + 4);
             __syncwarp();
-            tmem_st16_async(lane_base + kU + t0 / 2, hi);
-            tmem_st16_async(lane_base + kU + 32 + t0 / 2, lo);
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-                hi[c] = x[c];
-            tmem_st16_async(lane_base + kDS + t0 / 2, hi);
+            tmem_st8_async(lane_base + kU + t0 / 2, hi);
+            tmem_st8_async(lane_base + kU + 32 + t0 / 2, lo);
+            tmem_st8_async(lane_base + kDS + t0 / 2, us);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&sh.w_ready);
@@ -907,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             keep = f.keep;
             z_by = su.undo * u_by;
             w_undo = z_by * w_by;
-            bad = min(sh.bad[turn][0][col], sh.bad[turn][1][col]);
+            bad = min(min(sh.bad[turn][0][col], sh.bad[turn][1][col]), min(sh.bad[turn][2][col], sh.bad[turn][3][col]));
         }
         if (chunks > 0) {
             y_by = s_undo;
@@ -917,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
         if (there && (chunks > 0 || p.state_out != p.state_in))
 #pragma unroll
             for (int i = 0; i < kMine; ++i)
-                p.state_out[state_at + (size_t)((i >> 5) * 64 + (i & 31)) * D] = s[i];
+                p.state_out[state_at + (size_t)((i >> 4) * 64 + (i & 15)) * D] = s[i];
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kMmaWarp) {
@@ -926,10 +902,11 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             const auto place_a = [&](int ch) { return base + P::kAt + (ch % P::kA) * P::kABytes; };
             const auto place_b = [&](int ch) { return base + P::kBt + (ch % P::kB) * P::kBBytes; };
             const auto place_c = [&](int ch) { return base + P::kCt + (ch % P::kC) * P::kCBytes; };
-            const auto full_a = [&](int ch) { return wait(&sh.a_full[ch % P::kA], (ch / P::kA) & 1, sh, status); };
+            const auto full_a = [&](int ch) { return wait(&sh.a_full[ch % P::kA], (ch / P::kA) & 1, sh); };
             // the state's parts with 64 rows of D elements
             const auto by_state = [&](uint32_t to, uint32_t rows, int parts) {
                 const uint32_t b = desc_lo(rows, 16);
+#pragma unroll 1
                 for (int part = 0; part < parts; ++part)
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i)
@@ -944,13 +921,14 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             };
             // ... both in two parts
             const auto by_tokens2 = [&](uint32_t to, uint32_t from, uint32_t rows) {
-                by_tokens(to, from, rows, 0);
-                by_tokens(to, from + 32, rows, 1);
-                by_tokens(to, from, rows + kTile, 1);
+#pragma unroll 1
+                for (int i = 0; i < 3; ++i)
+                    by_tokens(to, from + (i == 1 ? 32 : 0), rows + (i == 2 ? kTile : 0), i);
             };
             // half j of the state's update
             const auto update = [&](int ch, int j) {
                 const uint32_t k = desc_lo(place_a(ch) + j * kTile, kTile);
+#pragma unroll 1
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -959,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
                 if (j == D / 64 - 1)
                     umma_commit(&sh.a_empty[ch % P::kA]);
             };
-            bool ok = chunks > 0 && full_a(0) && wait(&sh.s_ready, 0, sh, status);
+            bool ok = chunks > 0 && full_a(0) && wait(&sh.s_ready, 0, sh);
             if (ok) {
                 tc_fence_after();
                 if (elect_one()) {
@@ -972,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             for (int ch = 0; ok && ch < chunks; ++ch) {
                 const uint32_t phase = ch & 1;
                 const bool more = ch + 1 < chunks;
-                ok = wait(&sh.b_full[ch % P::kB], (ch / P::kB) & 1, sh, status) && wait(&sh.r_ready, phase, sh, status);
+                ok = wait(&sh.b_full[ch % P::kB], (ch / P::kB) & 1, sh) && wait(&sh.r_ready, phase, sh);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -984,14 +962,14 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
                     umma_commit(&sh.b_empty[ch % P::kB]);
                 }
                 __syncwarp();
-                ok = (ch == 0 || wait(&sh.s_ready, phase, sh, status)) && (!more || full_a(ch + 1));
+                ok = (ch == 0 || wait(&sh.s_ready, phase, sh)) && (!more || full_a(ch + 1));
                 if (!ok)
                     break;
                 tc_fence_after();
                 if (more && elect_one())
                     by_state(kXA, place_a(ch + 1), 2);
                 __syncwarp();
-                ok = wait(&sh.w_ready, phase, sh, status);
+                ok = wait(&sh.w_ready, phase, sh);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -1000,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
                     umma_commit(&sh.x_done);
                 }
                 __syncwarp();
-                ok = wait(&sh.c_full[ch % P::kC], (ch / P::kC) & 1, sh, status) && (ch == 0 || wait(&sh.y_free, phase ^ 1, sh, status));
+                ok = wait(&sh.c_full[ch % P::kC], (ch / P::kC) & 1, sh) && (ch == 0 || wait(&sh.y_free, phase ^ 1, sh));
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -1023,13 +1001,13 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
 #pragma unroll 1
             for (int ch = 0; ok && ch < chunks; ++ch, key += Rec::kKeyBytes, value += Rec::kValueBytes) {
                 const int a = ch % P::kA, b = ch % P::kB, c = ch % P::kC, f = ch % P::kF;
-                ok = wait(&sh.a_empty[a], ((ch / P::kA) & 1) ^ 1, sh, status);
+                ok = wait(&sh.a_empty[a], ((ch / P::kA) & 1) ^ 1, sh);
                 if (ok && lane == 0) {
                     mbar_arrive_expect_tx(&sh.a_full[a], P::kABytes);
                     bulk_copy_g2s(smem + P::kAt + a * P::kABytes, key + Rec::kK, P::kABytes, &sh.a_full[a]);
                 }
                 __syncwarp();
-                ok = ok && wait(&sh.b_empty[b], ((ch / P::kB) & 1) ^ 1, sh, status);
+                ok = ok && wait(&sh.b_empty[b], ((ch / P::kB) & 1) ^ 1, sh);
                 if (ok && lane == 0) {
                     mbar_arrive_expect_tx(&sh.b_full[b], P::kBBytes);
                     tma_load_3d(smem + P::kBt + b * P::kBBytes + 2 * kTile, &map_v, 0, h, first + ch * kChunk, &sh.b_full[b]);
@@ -1038,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
                     bulk_copy_g2s(smem + P::kFt + f * kFactorBytes, value + Rec::kFactors, kFactorBytes, &sh.f_full[f]);
                 }
                 __syncwarp();
-                ok = ok && wait(&sh.c_empty[c], ((ch / P::kC) & 1) ^ 1, sh, status);
+                ok = ok && wait(&sh.c_empty[c], ((ch / P::kC) & 1) ^ 1, sh);
                 if (ok && lane == 0) {
                     mbar_arrive_expect_tx(&sh.c_full[c], P::kCBytes);
                     bulk_copy_g2s(smem + P::kCt + c * P::kCBytes, key + Rec::kQ, Rec::kRows, &sh.c_full[c]);
@@ -1055,6 +1033,8 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
     tc_fence_after();
     if (*reinterpret_cast<volatile int *>(&sh.dead)) {
         // a wait ran out: copies and products may still be in flight; give them time before the memory goes
+        if (tid == 0 && p.status)
+            atomicExch(p.status, kStatusTimeout);
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 50000000ull) {}
         __syncthreads();
