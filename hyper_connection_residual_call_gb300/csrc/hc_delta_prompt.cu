@@ -144,8 +144,13 @@ constexpr int kPitch = 68;    // floats of a row of a 64 x 64 matrix in shared m
 
 template <int D>
 struct PrepShared {
-    uint16_t k[kChunk][D + 8], q[kChunk][D + 8];   // fp16; q's place is the keys before's in the end
-    alignas(16) float a[kChunk][kPitch], t[kChunk][kPitch], tmp[32][36];  // keys with keys, then A; queries with keys, then T
+    uint16_t k[kChunk][D + 8];                     // fp16
+    union {                                        // one after the other
+        uint16_t q[kChunk][D + 8];
+        alignas(16) float t[kChunk][kPitch];       // T
+        uint16_t before[kChunk][D + 8];            // the keys of the chunk before
+    };
+    alignas(16) float a[kChunk][kPitch], tmp[32][36];  // A, in the end M
     float r[kChunk], s[kChunk];                    // the inverse norms, with the powers of two
     float gh[kChunk], gl[kChunk], beta[kChunk];    // G in two parts
     int bad;                                       // the first token with an infinity or a NaN
@@ -190,21 +195,13 @@ __device__ __forceinline__ void rows_with_rows(const uint16_t (*x)[D + 8], int r
 
 __device__ __forceinline__ int piece_at(int row, int x) { return row * 128 + ((x ^ (row & 7)) << 4); }
 
-// Eight values as two fp16 each (or one), to piece x of row i of two tiles.
-template <bool kTwo>
+// Eight values as two fp16 each, to piece x of row i of two tiles.
 __device__ __forceinline__ void put8(uint8_t *hi, uint8_t *lo, int i, int x, const float (&v)[8])
 {
     uint32_t h[4], l[4];
-    if (kTwo) {
-        split8(f32x2(v[0], v[1]), f32x2(v[2], v[3]), f32x2(v[4], v[5]), f32x2(v[6], v[7]), f32x2(1.f, 1.f), h, l);
-    } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            h[c] = pack2_f16(v[2 * c], v[2 * c + 1]);
-    }
+    split8(f32x2(v[0], v[1]), f32x2(v[2], v[3]), f32x2(v[4], v[5]), f32x2(v[6], v[7]), f32x2(1.f, 1.f), h, l);
     *reinterpret_cast<uint4 *>(hi + piece_at(i, x)) = make_uint4(h[0], h[1], h[2], h[3]);
-    if (kTwo)
-        *reinterpret_cast<uint4 *>(lo + piece_at(i, x)) = make_uint4(l[0], l[1], l[2], l[3]);
+    *reinterpret_cast<uint4 *>(lo + piece_at(i, x)) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 // A row's piece x of 8 elements, of the D / 8 lanes that share it: scaled by a power of two so that the row's largest
@@ -241,7 +238,7 @@ __device__ __forceinline__ float row_to_half(const uint16_t *src, bool there, in
 
 // A block a chunk and value head. The first of a key head's value heads writes the keys' record.
 template <int D>
-__global__ void __launch_bounds__(kPrepThreads) hc_delta_prep_kernel(const DeltaPromptParams p)
+__global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const DeltaPromptParams p)
 {
     using Rec = Record<D>;
     extern __shared__ uint4 smem4[];
@@ -358,19 +355,10 @@ __global__ void __launch_bounds__(kPrepThreads) hc_delta_prep_kernel(const Delta
             sh.bad = bad;
         }
     }
-    // keys with keys (warps 0-3) and queries with keys (4-7), 16 rows a warp
-    {
-        const int row = (warp & 3) * 16;
-        float d[8][4];
-        rows_with_rows<D, 8>(warp >= 4 ? sh.q : sh.k, row, sh.k, 0, d);
-        float (*const to)[kPitch] = warp >= 4 ? sh.t : sh.a;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float *at = &to[row + (lane >> 2)][i * 8 + (lane & 3) * 2];
-            *reinterpret_cast<float2 *>(at) = make_float2(d[i][0], d[i][1]);
-            *reinterpret_cast<float2 *>(at + 8 * kPitch) = make_float2(d[i][2], d[i][3]);
-        }
-    }
+    // keys with keys (warps 0-3) and queries with keys (4-7), 16 rows a warp, in registers
+    const int row = (warp & 3) * 16 + (lane >> 2);
+    float d[8][4];                                 // of rows row and row + 8: columns 8 i + 2 (lane % 4) and the next
+    rows_with_rows<D, 8>(warp >= 4 ? sh.q : sh.k, (warp & 3) * 16, sh.k, 0, d);
     if (writes)
         for (int i = tid; i < kChunk * kPieces * 2; i += kPrepThreads) {
             const bool query = i >= kChunk * kPieces;
@@ -380,44 +368,38 @@ __global__ void __launch_bounds__(kPrepThreads) hc_delta_prep_kernel(const Delta
         }
     __syncthreads();
 
-    // A, in place, and P, 16 columns of a row a thread, a row's by a power of two of its own
+    // A, to shared memory, and P, a row by a power of two of its own
     const int bad = sh.bad;
-    {
-        const int i = tid >> 2, j0 = (tid & 3) * 16;
-        const float gh = sh.gh[i], gl = sh.gl[i], bi = sh.beta[i] * sh.r[i], si = sh.s[i];
-        float pv[16];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int i = row + 8 * half;
+        const float gh = sh.gh[i], gl = sh.gl[i], by = warp < 4 ? sh.beta[i] * sh.r[i] : sh.s[i];
         uint32_t most = 0;
 #pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-            float4 *const at = reinterpret_cast<float4 *>(&sh.a[i][j0 + c]);
-            const float4 kk = *at, qk = *reinterpret_cast<const float4 *>(&sh.t[i][j0 + c]);
-            const float kv[4] = {kk.x, kk.y, kk.z, kk.w}, qv[4] = {qk.x, qk.y, qk.z, qk.w};
-            float av[4];
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const int j = j0 + c + d;
-                const bool in = j <= i && i < bad;
+            for (int c = 0; c < 2; ++c) {
+                const int j = 8 * t + 2 * (lane & 3) + c;
+                const bool in = i < bad && (warp < 4 ? j < i : j <= i);
                 // (the exponential's error, |x| 2^-24 of it or so, is at most 2^-25 of 1)
-                const float e = in ? __expf((gh - sh.gh[j]) + (gl - sh.gl[j])) * sh.r[j] : 0.f;
-                av[d] = in && j < i ? bi * kv[d] * e : 0.f;
-                pv[c + d] = in ? si * qv[d] * e : 0.f;
-                most = max(most, __float_as_uint(pv[c + d]) & 0x7FFFFFFFu);
+                float &x = d[t][2 * half + c];
+                x = in ? by * x * __expf((gh - sh.gh[j]) + (gl - sh.gl[j])) * sh.r[j] : 0.f;
+                most = max(most, __float_as_uint(x) & 0x7FFFFFFFu);
             }
-            *at = make_float4(av[0], av[1], av[2], av[3]);
-        }
-        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-        const Scale sp(most);
+        if (warp < 4) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float v[8];
+            for (int t = 0; t < 8; ++t)
+                *reinterpret_cast<float2 *>(&sh.a[i][8 * t + 2 * (lane & 3)]) = make_float2(d[t][2 * half], d[t][2 * half + 1]);
+        } else {
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+            const Scale sp(most);
 #pragma unroll
-            for (int d = 0; d < 8; ++d)
-                v[d] = pv[c * 8 + d] * sp.by;
-            put8<false>(rec + Rec::kP, nullptr, i, (tid & 3) * 2 + c, v);
+            for (int t = 0; t < 8; ++t)
+                *reinterpret_cast<uint32_t *>(rec + Rec::kP + piece_at(i, t) + (lane & 3) * 4) = pack2_f16(d[t][2 * half] * sp.by, d[t][2 * half + 1] * sp.by);
+            if ((lane & 3) == 0)
+                reinterpret_cast<Factors *>(rec + Rec::kFactors)->p[i] = sp.undo;
         }
-        if ((tid & 3) == 0)
-            reinterpret_cast<Factors *>(rec + Rec::kFactors)->p[i] = sp.undo;
     }
     __syncthreads();
     // T = (I + A)^-1: the blocks of 16 on the diagonal, a thread a column; the blocks above them are 0
@@ -512,29 +494,30 @@ __global__ void __launch_bounds__(kPrepThreads) hc_delta_prep_kernel(const Delta
 #pragma unroll
             for (int d = 0; d < 8; ++d)
                 tv[c][d] *= st.by;
-            put8<true>(rec + Rec::kT, rec + Rec::kT + kTile, i, x + c, tv[c]);
+            put8(rec + Rec::kT, rec + Rec::kT + kTile, i, x + c, tv[c]);
         }
         if (tid == 0)
             reinterpret_cast<Factors *>(rec + Rec::kFactors)->t = st.undo;
     }
     if (!writes || chunk == 0)
         return;
+    __syncthreads();                               // T has been read
     // M: the keys with those of the chunk before, which is whole
 #pragma unroll
     for (int i = tid; i < kChunk * kPieces; i += kPrepThreads) {
         const int r = i / kPieces, x = i % kPieces;
         float undo;
         bool odd;
-        row_to_half<D>(p.k + (size_t)(first - kChunk + r) * p.k_stride + (size_t)hk * D, true, x, sh.q[r], undo, odd);
+        row_to_half<D>(p.k + (size_t)(first - kChunk + r) * p.k_stride + (size_t)hk * D, true, x, sh.before[r], undo, odd);
     }
     __syncthreads();
     {
-        const int row = (warp & 3) * 16, col = (warp >> 2) * 32;
+        const int col = (warp >> 2) * 32;
         float d[4][4];
-        rows_with_rows<D, 4>(sh.k, row, sh.q, col, d);
+        rows_with_rows<D, 4>(sh.k, (warp & 3) * 16, sh.before, col, d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float *at = &sh.a[row + (lane >> 2)][col + i * 8 + (lane & 3) * 2];
+            float *at = &sh.a[row][col + i * 8 + (lane & 3) * 2];
             *reinterpret_cast<float2 *>(at) = make_float2(d[i][0], d[i][1]);
             *reinterpret_cast<float2 *>(at + 8 * kPitch) = make_float2(d[i][2], d[i][3]);
         }
@@ -546,7 +529,7 @@ __global__ void __launch_bounds__(kPrepThreads) hc_delta_prep_kernel(const Delta
         for (int c = 0; c < 2; ++c) {
             const float4 u = *reinterpret_cast<const float4 *>(&sh.a[i][(x + c) * 8]), w = *reinterpret_cast<const float4 *>(&sh.a[i][(x + c) * 8 + 4]);
             const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-            put8<true>(key_rec + Rec::kM, key_rec + Rec::kM + kTile, i, x + c, v);
+            put8(key_rec + Rec::kM, key_rec + Rec::kM + kTile, i, x + c, v);
         }
     }
 }
@@ -689,17 +672,19 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
         // of each 64 elements of the column a thread has 16
         const size_t state_at = (((size_t)seq * p.Hv + h) * D + t0) * D + col, step = (size_t)p.Hv * D;
         constexpr int kMine = D / 4;
-        float s[kMine];
+        uint64_t s[kMine / 2];                      // two elements each
 #pragma unroll
-        for (int i = 0; i < kMine; ++i)
-            s[i] = there ? p.state_in[state_at + (size_t)((i >> 4) * 64 + (i & 15)) * D] : 0.f;
+        for (int i = 0; i < kMine / 2; ++i) {
+            const float *const at = p.state_in + state_at + (size_t)((i >> 3) * 64 + (i & 7) * 2) * D;
+            s[i] = there ? f32x2(at[0], at[D]) : 0;
+        }
         float keep = 1.f, s_undo, y_by = 0.f, z_by = 0.f, w_undo = 0.f;  // of the chunk before, and what undoes the scales
         int bad = kChunk;                           // of the chunk before
         const auto to_operand = [&] {               // the state, D / 2 columns a part
             float tops[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < kMine; i += 2)
-                tops[(i >> 1) & 3] = most3(tops[(i >> 1) & 3], s[i], s[i + 1]);
+            for (int i = 0; i < kMine / 2; ++i)
+                tops[i & 3] = most_of(tops[i & 3], s[i]);
             sh.top_s[part][col] = most3(most3(tops[0], tops[1], tops[2]), tops[3], 0.f);
             meet();
             const Scale sc(__float_as_uint(most_of_all(sh.top_s)));
@@ -709,10 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             for (int i = 0; i < kMine / 16; ++i) {
                 uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int c = 0; c < 8; c += 4) {
-                    const float *const e = s + 16 * i + 2 * c;
-                    split8(f32x2(e[0], e[1]), f32x2(e[2], e[3]), f32x2(e[4], e[5]), f32x2(e[6], e[7]), f32x2(sc.by, sc.by), hi + c, lo + c);
-                }
+                for (int c = 0; c < 8; c += 4)
+                    split8(s[8 * i + c], s[8 * i + c + 1], s[8 * i + c + 2], s[8 * i + c + 3], f32x2(sc.by, sc.by), hi + c, lo + c);
                 tmem_st8_async(lane_base + kS + 32 * i + 8 * part, hi);
                 tmem_st8_async(lane_base + kS + D / 2 + 32 * i + 8 * part, lo);
             }
@@ -730,13 +713,13 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
                 tmem_ld16_async(lane_base + (j == 0 ? kDS : kXA) + t0, x);
                 tmem_wait_ld(x);
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    s[16 * j + c] = fmaf(s[16 * j + c], keep, __uint_as_float(x[c]) * w_undo);
+                for (int c = 0; c < 8; ++c)
+                    s[8 * j + c] = ffma2(s[8 * j + c], f32x2(keep, keep), fmul2(pair_of(x, c), f32x2(w_undo, w_undo)));
             }
             if (bad < kChunk)
 #pragma unroll
-                for (int i = 0; i < kMine; ++i)
-                    s[i] = kNaN;
+                for (int i = 0; i < kMine / 2; ++i)
+                    s[i] = f32x2(kNaN, kNaN);
         };
         // chunk ch's outputs
         const auto outputs = [&](int ch) {
@@ -745,8 +728,10 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             wait(&sh.o_done, ch & 1, sh);
             tc_fence_after();
             uint16_t *to = p.out + (size_t)(first + ch * kChunk + t0) * step + (size_t)h * D + col;
+            const bool plain = __all_sync(0xFFFFFFFFu, n >= 16 && bad == kChunk);
+            const uint64_t y2 = f32x2(y_by, y_by), z2 = f32x2(z_by, z_by);
 #pragma unroll 1
-            for (int i = 0; i < 16; i += 4) {       // (a loop for the instruction cache's sake)
+            for (int i = 0; i < 16; i += 4) {
                 uint32_t y[4], z[4];
                 __syncwarp();
                 tmem_ld4_async(lane_base + kY + t0 + i, y);
@@ -754,15 +739,26 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
                 const float4 fy = *reinterpret_cast<const float4 *>(&f.y[t0 + i]), fp = *reinterpret_cast<const float4 *>(&f.p[t0 + i]);
                 tmem_wait_ld4(y);
                 tmem_wait_ld4(z);
-                const float a[4] = {fy.x, fy.y, fy.z, fy.w}, b[4] = {fp.x, fp.y, fp.z, fp.w};
+                const uint64_t o0 = ffma2(fmul2(f32x2(fy.x, fy.y), y2), pair_of(y, 0), fmul2(fmul2(f32x2(fp.x, fp.y), z2), pair_of(z, 0)));
+                const uint64_t o1 = ffma2(fmul2(f32x2(fy.z, fy.w), y2), pair_of(y, 1), fmul2(fmul2(f32x2(fp.z, fp.w), z2), pair_of(z, 1)));
+                float o[4];
+                f32x2_unpack(o0, o[0], o[1]);
+                f32x2_unpack(o1, o[2], o[3]);
+                if (plain) {
+                    // two tokens a word, then two columns: lanes trade halves, even ones take the tokens 0 and 2, odd ones 1 and 3
+                    const uint32_t p0 = pack2_bf16(o[0], o[1]), p1 = pack2_bf16(o[2], o[3]);
+                    const uint32_t q0 = __shfl_xor_sync(0xFFFFFFFFu, p0, 1), q1 = __shfl_xor_sync(0xFFFFFFFFu, p1, 1);
+                    const uint32_t which = lane & 1 ? 0x3276u : 0x5410u;
+                    uint16_t *const at = to + ((lane & 1) ? (long)step - 1 : 0);
+                    *reinterpret_cast<uint32_t *>(at) = __byte_perm(p0, q0, which);
+                    *reinterpret_cast<uint32_t *>(at + 2 * step) = __byte_perm(p1, q1, which);
+                } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float o = fmaf(a[c] * y_by, __uint_as_float(y[c]), b[c] * z_by * __uint_as_float(z[c]));
-                    o = t0 + i + c >= bad ? kNaN : o;
-                    if (i + c < n)
-                        *to = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-                    to += step;
+                    for (int c = 0; c < 4; ++c)
+                        if (i + c < n)
+                            to[c * step] = __bfloat16_as_ushort(__float2bfloat16_rn(t0 + i + c >= bad ? kNaN : o[c]));
                 }
+                to += 4 * step;
             }
             tc_fence_before();
             mbar_arrive(&sh.y_free);
@@ -779,9 +775,15 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             const Factors &f = factors(ch);
             const uint16_t *const v = reinterpret_cast<const uint16_t *>(smem + P::kBt + (ch % P::kB) * P::kBBytes + 2 * kTile) + t0 * D + col;
             uint32_t vw[8];                         // two tokens' values
+            if (n >= 16) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                vw[c] = (2 * c < n ? v[2 * c * D] : 0u) | (2 * c + 1 < n ? (uint32_t)v[(2 * c + 1) * D] << 16 : 0u);
+                for (int c = 0; c < 8; ++c)
+                    vw[c] = v[2 * c * D] | (uint32_t)v[(2 * c + 1) * D] << 16;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    vw[c] = (2 * c < n ? v[2 * c * D] : 0u) | (2 * c + 1 < n ? (uint32_t)v[(2 * c + 1) * D] << 16 : 0u);
+            }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.b_empty[ch % P::kB]);
@@ -892,8 +894,10 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
         }
         if (there && (chunks > 0 || p.state_out != p.state_in))
 #pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                p.state_out[state_at + (size_t)((i >> 4) * 64 + (i & 15)) * D] = s[i];
+            for (int i = 0; i < kMine / 2; ++i) {
+                float *const at = p.state_out + state_at + (size_t)((i >> 3) * 64 + (i & 7) * 2) * D;
+                f32x2_unpack(s[i], at[0], at[D]);
+            }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kMmaWarp) {
