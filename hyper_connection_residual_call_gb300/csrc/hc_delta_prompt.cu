@@ -12,7 +12,7 @@
 //     o_i = e^(G_i) s_i (S0^T q_i) + sum_{j <= i} P_ij u_j,   P_ij = s_i r_j (q_i . k_j) e^(G_i - G_j)
 //     S1  = e^(G_64) S0 + sum_j k_j w_j u_j^T,                 w_j = r_j e^(G_64 - G_j).
 //
-// What does not depend on the state is one kernel's, a block a chunk and value head: the
+// What does not depend on the state is one kernel's, a block a chunk and key head: the
 // products of keys and queries with keys, T by inverting blocks of 16 and joining them, P
 // and the factors, in fp32, written in the order in which the second kernel's tensor cores
 // want them, so that they come by bulk copies.
@@ -152,9 +152,12 @@ struct PrepShared {
     };
     alignas(16) float a[kChunk][kPitch], tmp[32][36];  // A, in the end M
     float r[kChunk], s[kChunk];                    // the inverse norms, with the powers of two
-    float gh[kChunk], gl[kChunk], beta[kChunk];    // G in two parts
-    int bad;                                       // the first token with an infinity or a NaN
-    uint32_t most_t;
+    struct {
+        float gh[kChunk], gl[kChunk], beta[kChunk];  // G in two parts
+        int bad;                                   // the first token with an infinity or a NaN
+        uint32_t most_t;
+    } gate[kPrepThreads / 32];                     // of eight value heads
+    int bad_key;                                   // the first key with one
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void *at)
@@ -236,9 +239,10 @@ __device__ __forceinline__ float row_to_half(const uint16_t *src, bool there, in
     return sum;
 }
 
-// A block a chunk and value head. The first of a key head's value heads writes the keys' record.
+// A block a chunk and key head, with the key head's value heads one after the other. (A block a value head, which does
+// the keys' part again for each: 217 us for 8192 tokens of 32 heads, two a key head.)
 template <int D>
-__global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const DeltaPromptParams p)
+__global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_kernel(const DeltaPromptParams p)
 {
     using Rec = Record<D>;
     extern __shared__ uint4 smem4[];
@@ -246,9 +250,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const De
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long slot = blockIdx.x / p.Hv;
-    const int h = (int)(blockIdx.x - slot * p.Hv), group = p.Hv / p.Hk, hk = h / group;
-    const bool writes = h == hk * group;
+    const long slot = blockIdx.x / p.Hk;
+    const int hk = (int)(blockIdx.x - slot * p.Hk), group = p.Hv / p.Hk;
     // the sequence whose records this one is among: the last that begins at or before it
     int seq = 0;
     for (int lo = 0, hi = p.S - 1; lo < hi;) {
@@ -267,20 +270,21 @@ __global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const De
         return;
     first += (int)chunk * kChunk;
     const int n = min(kChunk, len - (int)chunk * kChunk);
-    uint8_t *const key_rec = key_record<D>(p, hk, slot), *const rec = value_record<D>(p, h, slot);
-    // the gates are asked for first, by the warp that adds them up
+    uint8_t *const key_rec = key_record<D>(p, hk, slot);
+    // the gates are asked for first, by the warps that add them up: a value head a warp, eight at a time
     float decay[2] = {0.f, 0.f}, beta[2] = {0.f, 0.f};
-    if (warp == 0)
+    const auto ask = [&](int g) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (2 * lane + i < n) {
-                decay[i] = p.decay[(size_t)(first + 2 * lane + i) * p.Hv + h];
-                beta[i] = p.beta[(size_t)(first + 2 * lane + i) * p.Hv + h];
-            }
-    if (tid == 0) {
-        sh.bad = n;
-        sh.most_t = 0;
-    }
+        for (int i = 0; i < 2; ++i) {
+            const bool in = g < group && 2 * lane + i < n;
+            const size_t at = (size_t)(first + 2 * lane + i) * p.Hv + hk * group + g;
+            decay[i] = in ? p.decay[at] : 0.f;
+            beta[i] = in ? p.beta[at] : 0.f;
+        }
+    };
+    ask(warp);
+    if (tid == 0)
+        sh.bad_key = n;
     __syncthreads();
 
     // keys and queries, zeros after the last token, and their norms
@@ -300,15 +304,18 @@ __global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const De
             } else {
                 sh.r[r] = inv;
                 if (odd || !(inv < INFINITY))
-                    atomicMin(&sh.bad, r);
+                    atomicMin(&sh.bad_key, r);
             }
         }
     }
     __syncthreads();
 
-    if (warp == 0) {
-        // the decays' sums in 64 bits, kept as two floats: differences of near ones are right after strong decays too
-        int bad = sh.bad;
+    // the decays' sums in 64 bits, kept as two floats: differences of near ones are right after strong decays too
+    const auto gates = [&](int g) {
+        if (g >= group)
+            return;
+        auto &gate = sh.gate[warp];
+        int bad = sh.bad_key;
         double x[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -332,15 +339,15 @@ __global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const De
                 pre += y;
         }
         const double all = __shfl_sync(0xFFFFFFFFu, pre, 31), before = pre - x[1];
-        auto &f = *reinterpret_cast<Factors *>(rec + Rec::kFactors);
+        auto &f = *reinterpret_cast<Factors *>(value_record<D>(p, hk * group + g, slot) + Rec::kFactors);
         float w[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = 2 * lane + i;
             const double G = before + x[i];
-            sh.gh[r] = (float)G;
-            sh.gl[r] = (float)(G - (float)G);
-            sh.beta[r] = beta[i];
+            gate.gh[r] = (float)G;
+            gate.gl[r] = (float)(G - (float)G);
+            gate.beta[r] = beta[i];
             const float e = expf((float)G);
             f.c[r] = r < bad ? -e * sh.r[r] : r < n ? kNaN : 0.f;
             w[i] = r < bad ? expf((float)(all - G)) * sh.r[r] : 0.f;
@@ -352,154 +359,169 @@ __global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const De
         if (lane == 0) {
             f.keep = expf((float)all);
             f.w_undo = __uint_as_float(top << 23);
-            sh.bad = bad;
+            gate.bad = bad;
+            gate.most_t = 0;
         }
-    }
+    };
+    gates(warp);
     // keys with keys (warps 0-3) and queries with keys (4-7), 16 rows a warp, in registers
     const int row = (warp & 3) * 16 + (lane >> 2);
     float d[8][4];                                 // of rows row and row + 8: columns 8 i + 2 (lane % 4) and the next
     rows_with_rows<D, 8>(warp >= 4 ? sh.q : sh.k, (warp & 3) * 16, sh.k, 0, d);
-    if (writes)
-        for (int i = tid; i < kChunk * kPieces * 2; i += kPrepThreads) {
-            const bool query = i >= kChunk * kPieces;
-            const int r = i / kPieces % kChunk, x = i % kPieces;
-            *reinterpret_cast<uint4 *>(key_rec + (query ? Rec::kQ : Rec::kK) + (x >> 3) * kTile + piece_at(r, x & 7)) =
-                *reinterpret_cast<const uint4 *>(query ? &sh.q[r][x * 8] : &sh.k[r][x * 8]);
-        }
+    for (int i = tid; i < kChunk * kPieces * 2; i += kPrepThreads) {
+        const bool query = i >= kChunk * kPieces;
+        const int r = i / kPieces % kChunk, x = i % kPieces;
+        *reinterpret_cast<uint4 *>(key_rec + (query ? Rec::kQ : Rec::kK) + (x >> 3) * kTile + piece_at(r, x & 7)) =
+            *reinterpret_cast<const uint4 *>(query ? &sh.q[r][x * 8] : &sh.k[r][x * 8]);
+    }
     __syncthreads();
 
-    // A, to shared memory, and P, a row by a power of two of its own
-    const int bad = sh.bad;
+#pragma unroll 1
+    for (int g = 0; g < group; ++g) {
+        if (g > 0) {
+            __syncthreads();                           // T has been read
+            if ((g & 7) == 0) {
+                ask(g + warp);
+                gates(g + warp);
+                __syncthreads();
+            }
+        }
+        // A, to shared memory, and P, a row by a power of two of its own
+        const auto &gate = sh.gate[g & 7];
+        const int bad = gate.bad;
+        uint8_t *const rec = value_record<D>(p, hk * group + g, slot);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int i = row + 8 * half;
-        const float gh = sh.gh[i], gl = sh.gl[i], by = warp < 4 ? sh.beta[i] * sh.r[i] : sh.s[i];
-        uint32_t most = 0;
+        for (int half = 0; half < 2; ++half) {
+            const int i = row + 8 * half;
+            const float gh = gate.gh[i], gl = gate.gl[i], by = warp < 4 ? gate.beta[i] * sh.r[i] : sh.s[i];
+            uint32_t most = 0;
+            float e[8][2];
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int j = 8 * t + 2 * (lane & 3) + c;
+                    const bool in = i < bad && (warp < 4 ? j < i : j <= i);
+                    // (the exponential's error, |x| 2^-24 of it or so, is at most 2^-25 of 1)
+                    float &x = e[t][c];
+                    x = in ? by * d[t][2 * half + c] * __expf((gh - gate.gh[j]) + (gl - gate.gl[j])) * sh.r[j] : 0.f;
+                    most = max(most, __float_as_uint(x) & 0x7FFFFFFFu);
+                }
+            if (warp < 4) {
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    *reinterpret_cast<float2 *>(&sh.a[i][8 * t + 2 * (lane & 3)]) = make_float2(e[t][0], e[t][1]);
+            } else {
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+                const Scale sp(most);
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    *reinterpret_cast<uint32_t *>(rec + Rec::kP + piece_at(i, t) + (lane & 3) * 4) = pack2_f16(e[t][0] * sp.by, e[t][1] * sp.by);
+                if ((lane & 3) == 0)
+                    reinterpret_cast<Factors *>(rec + Rec::kFactors)->p[i] = sp.undo;
+            }
+        }
+        __syncthreads();
+        // T = (I + A)^-1: the blocks of 16 on the diagonal, a thread a column; the blocks above them are 0
+        if (tid < kChunk) {
+            const int b = tid & 48, j = tid & 15;
+            float t[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < i; ++k)
+                    sum[k & 3] = fmaf(sh.a[b + i][b + k], t[k], sum[k & 3]);
+                t[i] = i < j ? 0.f : i == j ? 1.f : -((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                sh.t[b + i][b + j] = t[i];
+            }
+        } else {
+            for (int u = tid - kChunk; u < kChunk * kChunk; u += kPrepThreads - kChunk)
+                if ((u & 63) >> 4 > u >> 10)
+                    sh.t[u >> 6][u & 63] = 0.f;
+        }
+        __syncthreads();
+        // (T11 0; T21 T22) has T21 = -T22 A21 T11: two pairs of blocks of 16, then one of 32
+        {
+            const int pair = tid >> 7, i = (tid >> 3) & 15, j = (tid & 7) * 2, b = pair * 32;
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float a = sh.a[b + 16 + i][b + k];
+                const float2 t = *reinterpret_cast<const float2 *>(&sh.t[b + k][b + j]);
+                s0 = fmaf(a, t.x, s0);
+                s1 = fmaf(a, t.y, s1);
+            }
+            *reinterpret_cast<float2 *>(&sh.tmp[pair * 16 + i][j]) = make_float2(s0, s1);
+            __syncthreads();
+            s0 = s1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float a = sh.t[b + 16 + i][b + 16 + k];
+                const float2 t = *reinterpret_cast<const float2 *>(&sh.tmp[pair * 16 + k][j]);
+                s0 = fmaf(a, t.x, s0);
+                s1 = fmaf(a, t.y, s1);
+            }
+            *reinterpret_cast<float2 *>(&sh.t[b + 16 + i][b + j]) = make_float2(-s0, -s1);
+            __syncthreads();
+        }
+        {
+            const int i = tid >> 3, j = (tid & 7) * 4;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) {
+                const float a = sh.a[32 + i][k];
+                const float4 t = *reinterpret_cast<const float4 *>(&sh.t[k][j]);
+                s = make_float4(fmaf(a, t.x, s.x), fmaf(a, t.y, s.y), fmaf(a, t.z, s.z), fmaf(a, t.w, s.w));
+            }
+            *reinterpret_cast<float4 *>(&sh.tmp[i][j]) = s;
+            __syncthreads();
+            s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) {
+                const float a = sh.t[32 + i][32 + k];
+                const float4 t = *reinterpret_cast<const float4 *>(&sh.tmp[k][j]);
+                s = make_float4(fmaf(a, t.x, s.x), fmaf(a, t.y, s.y), fmaf(a, t.z, s.z), fmaf(a, t.w, s.w));
+            }
+            *reinterpret_cast<float4 *>(&sh.t[32 + i][j]) = make_float4(-s.x, -s.y, -s.z, -s.w);
+            __syncthreads();
+        }
+        float tv[2][8];
+        {
+            const int i = tid >> 2, x = (tid & 3) * 2;
+            uint32_t most = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int d = 0; d < 8; d += 4) {
+                    const int j = (x + c) * 8 + d;
+                    const float4 t = *reinterpret_cast<const float4 *>(&sh.t[i][j]);
+                    tv[c][d] = t.x * gate.beta[j];
+                    tv[c][d + 1] = t.y * gate.beta[j + 1];
+                    tv[c][d + 2] = t.z * gate.beta[j + 2];
+                    tv[c][d + 3] = t.w * gate.beta[j + 3];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        most = max(most, __float_as_uint(tv[c][d + e]) & 0x7FFFFFFFu);
+                }
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            if (lane == 0)
+                atomicMax(&sh.gate[g & 7].most_t, most);
+            __syncthreads();
+            const Scale st(sh.gate[g & 7].most_t);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int j = 8 * t + 2 * (lane & 3) + c;
-                const bool in = i < bad && (warp < 4 ? j < i : j <= i);
-                // (the exponential's error, |x| 2^-24 of it or so, is at most 2^-25 of 1)
-                float &x = d[t][2 * half + c];
-                x = in ? by * x * __expf((gh - sh.gh[j]) + (gl - sh.gl[j])) * sh.r[j] : 0.f;
-                most = max(most, __float_as_uint(x) & 0x7FFFFFFFu);
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                    tv[c][d] *= st.by;
+                put8(rec + Rec::kT, rec + Rec::kT + kTile, i, x + c, tv[c]);
             }
-        if (warp < 4) {
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-                *reinterpret_cast<float2 *>(&sh.a[i][8 * t + 2 * (lane & 3)]) = make_float2(d[t][2 * half], d[t][2 * half + 1]);
-        } else {
-            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-            const Scale sp(most);
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-                *reinterpret_cast<uint32_t *>(rec + Rec::kP + piece_at(i, t) + (lane & 3) * 4) = pack2_f16(d[t][2 * half] * sp.by, d[t][2 * half + 1] * sp.by);
-            if ((lane & 3) == 0)
-                reinterpret_cast<Factors *>(rec + Rec::kFactors)->p[i] = sp.undo;
+            if (tid == 0)
+                reinterpret_cast<Factors *>(rec + Rec::kFactors)->t = st.undo;
         }
     }
-    __syncthreads();
-    // T = (I + A)^-1: the blocks of 16 on the diagonal, a thread a column; the blocks above them are 0
-    if (tid < kChunk) {
-        const int b = tid & 48, j = tid & 15;
-        float t[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < i; ++k)
-                sum[k & 3] = fmaf(sh.a[b + i][b + k], t[k], sum[k & 3]);
-            t[i] = i < j ? 0.f : i == j ? 1.f : -((sum[0] + sum[1]) + (sum[2] + sum[3]));
-            sh.t[b + i][b + j] = t[i];
-        }
-    } else {
-        for (int u = tid - kChunk; u < kChunk * kChunk; u += kPrepThreads - kChunk)
-            if ((u & 63) >> 4 > u >> 10)
-                sh.t[u >> 6][u & 63] = 0.f;
-    }
-    __syncthreads();
-    // (T11 0; T21 T22) has T21 = -T22 A21 T11: two pairs of blocks of 16, then one of 32
-    {
-        const int pair = tid >> 7, i = (tid >> 3) & 15, j = (tid & 7) * 2, b = pair * 32;
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float a = sh.a[b + 16 + i][b + k];
-            const float2 t = *reinterpret_cast<const float2 *>(&sh.t[b + k][b + j]);
-            s0 = fmaf(a, t.x, s0);
-            s1 = fmaf(a, t.y, s1);
-        }
-        *reinterpret_cast<float2 *>(&sh.tmp[pair * 16 + i][j]) = make_float2(s0, s1);
-        __syncthreads();
-        s0 = s1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float a = sh.t[b + 16 + i][b + 16 + k];
-            const float2 t = *reinterpret_cast<const float2 *>(&sh.tmp[pair * 16 + k][j]);
-            s0 = fmaf(a, t.x, s0);
-            s1 = fmaf(a, t.y, s1);
-        }
-        *reinterpret_cast<float2 *>(&sh.t[b + 16 + i][b + j]) = make_float2(-s0, -s1);
-        __syncthreads();
-    }
-    {
-        const int i = tid >> 3, j = (tid & 7) * 4;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float a = sh.a[32 + i][k];
-            const float4 t = *reinterpret_cast<const float4 *>(&sh.t[k][j]);
-            s = make_float4(fmaf(a, t.x, s.x), fmaf(a, t.y, s.y), fmaf(a, t.z, s.z), fmaf(a, t.w, s.w));
-        }
-        *reinterpret_cast<float4 *>(&sh.tmp[i][j]) = s;
-        __syncthreads();
-        s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float a = sh.t[32 + i][32 + k];
-            const float4 t = *reinterpret_cast<const float4 *>(&sh.tmp[k][j]);
-            s = make_float4(fmaf(a, t.x, s.x), fmaf(a, t.y, s.y), fmaf(a, t.z, s.z), fmaf(a, t.w, s.w));
-        }
-        *reinterpret_cast<float4 *>(&sh.t[32 + i][j]) = make_float4(-s.x, -s.y, -s.z, -s.w);
-        __syncthreads();
-    }
-    float tv[2][8];
-    {
-        const int i = tid >> 2, x = (tid & 3) * 2;
-        uint32_t most = 0;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int d = 0; d < 8; d += 4) {
-                const int j = (x + c) * 8 + d;
-                const float4 t = *reinterpret_cast<const float4 *>(&sh.t[i][j]);
-                tv[c][d] = t.x * sh.beta[j];
-                tv[c][d + 1] = t.y * sh.beta[j + 1];
-                tv[c][d + 2] = t.z * sh.beta[j + 2];
-                tv[c][d + 3] = t.w * sh.beta[j + 3];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    most = max(most, __float_as_uint(tv[c][d + e]) & 0x7FFFFFFFu);
-            }
-        most = __reduce_max_sync(0xFFFFFFFFu, most);
-        if (lane == 0)
-            atomicMax(&sh.most_t, most);
-        __syncthreads();
-        const Scale st(sh.most_t);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-            for (int d = 0; d < 8; ++d)
-                tv[c][d] *= st.by;
-            put8(rec + Rec::kT, rec + Rec::kT + kTile, i, x + c, tv[c]);
-        }
-        if (tid == 0)
-            reinterpret_cast<Factors *>(rec + Rec::kFactors)->t = st.undo;
-    }
-    if (!writes || chunk == 0)
+    if (chunk == 0)
         return;
     __syncthreads();                               // T has been read
     // M: the keys with those of the chunk before, which is whole
@@ -1060,7 +1082,7 @@ cudaError_t launch(const DeltaPromptParams &p, cudaStream_t stream)
     CUtensorMap map_v{};
     if (!tc_make_map_heads(&map_v, p.v, p.N, p.Hv, D, p.v_stride, 1, kChunk, true))
         return cudaErrorInvalidValue;
-    e = launch_pdl(hc_delta_prep_kernel<D>, dim3((unsigned)(record_slots(p.N, p.S) * p.Hv)), dim3(kPrepThreads), sizeof(PrepShared<D>), true, stream, p);
+    e = launch_pdl(hc_delta_prep_kernel<D>, dim3((unsigned)(record_slots(p.N, p.S) * p.Hk)), dim3(kPrepThreads), sizeof(PrepShared<D>), true, stream, p);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t lc{};

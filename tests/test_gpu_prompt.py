@@ -432,6 +432,14 @@ def test_delta_prompt_long(d, low):
     fine()
 
 
+@pytest.mark.parametrize("hk,hv", [(1, 9), (3, 51), (2, 16)])
+def test_delta_prompt_heads(hk, hv):
+    args, at = prompt_case([70, 3], hk, hv, 64, hv)
+    out, state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    check_prompt(args, at, out, state)
+    fine()
+
+
 def test_delta_prompt_many_sequences():
     r = np.random.default_rng(4)
     lens = [int(x) for x in r.integers(0, 90, 70)]
