@@ -227,6 +227,13 @@ struct Items {
 // Bits 15 and 31: whether the halves are infinities or NaNs (exponents of ones carry into them).
 __device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
 
+// 32 bytes, a whole sector, by one instruction: a lane has a row of its own.
+__device__ __forceinline__ void store32(void *to, const uint32_t *w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 hc_prompt_attn_kernel(const __grid_constant__ PromptAttnParams p, const __grid_constant__ CUtensorMap map_q,
@@ -385,10 +392,9 @@ hc_prompt_attn_kernel(const __grid_constant__ PromptAttnParams p, const __grid_c
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
                     w[c] = pack2_bf16(__uint_as_float(x[2 * c]) * inv, __uint_as_float(x[2 * c + 1]) * inv);
-                uint4 *out = reinterpret_cast<uint4 *>(p.out + at * D + 32 * i);
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    out[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+                uint16_t *const out = p.out + at * D + 32 * i;
+                store32(out, w);
+                store32(out + 16, w + 8);
             }
             if (wild && valid) {  // infinities and NaNs among the values that were looked through and that the row sees
                 const int from = it.token / kKeys * kKeys;
