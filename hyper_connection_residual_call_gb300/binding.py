@@ -1187,19 +1187,23 @@ def hc_qk_norm_rope(q, k, positions, table, q_weight, k_weight=None, *, eps: flo
     as ``hc_rope`` gives them, in one pass. Returns (q_out, k_out); passing q and k as them works in place."""
     torch = _torch()
     n, hq, d, sq = _rows(q, "q")
-    q_out = _made(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream) if q_out is None else q_out
-    no, ho, do, so = _rows(q_out, "q_out")
-    if (no, ho, do) != (n, hq, d):
-        raise HCError(TS_ERR_INVALID_ARG, f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+    if q_out is None:
+        q_out, so = _made(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream), hq * d
+    else:
+        no, ho, do, so = _rows(q_out, "q_out")
+        if (no, ho, do) != (n, hq, d):
+            raise HCError(TS_ERR_INVALID_ARG, f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
     hk, sk, sko, kp, kop, kwp = 0, 0, 0, None, None, None
     if k is not None:
         nk, hk, dk, sk = _rows(k, "k")
         if nk != n or dk != d:
             raise HCError(TS_ERR_INVALID_ARG, f"k has shape {tuple(k.shape)}, q has {tuple(q.shape)}")
-        k_out = _made(torch.empty(k.shape, dtype=torch.bfloat16, device=q.device), stream) if k_out is None else k_out
-        no, ho, do, sko = _rows(k_out, "k_out")
-        if (no, ho, do) != (n, hk, d):
-            raise HCError(TS_ERR_INVALID_ARG, f"k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
+        if k_out is None:
+            k_out, sko = _made(torch.empty(k.shape, dtype=torch.bfloat16, device=q.device), stream), hk * d
+        else:
+            no, ho, do, sko = _rows(k_out, "k_out")
+            if (no, ho, do) != (n, hk, d):
+                raise HCError(TS_ERR_INVALID_ARG, f"k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
         kp, kop, kwp = k.data_ptr(), k_out.data_ptr(), _is(k_weight, "k_weight", torch.bfloat16, (d,))
     pp = _is(positions, "positions", torch.int32)
     if positions.numel() != n:

@@ -38,6 +38,8 @@
 // An infinity or a NaN reaches the outputs from its token on and the state, and nothing
 // before: factors of a chunk's tokens from a bad key, decay or beta on make R a NaN, and a
 // lane sets its R to 0 from the first that is not finite, and its outputs and state to NaN.
+//
+// Few long sequences leave SMs idle and are cut into segments (segment_chunks): three launches instead of the second.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -80,6 +82,52 @@ constexpr float kNaN = __builtin_nanf("");
 // no two sequences' overlap, and nobody needs a sum over the sequences before.
 __host__ __device__ inline long record_slots(int N, int S) { return (long)N / kChunk + S; }
 __device__ __forceinline__ long record_of(int start, int seq, int chunk) { return (long)(start / kChunk) + seq + chunk; }
+
+// Chunks of a segment, where sequences are cut into segments that are walked side by side; 0: they are not.
+// A segment after the first is walked for what it makes of a state, S -> F S + B (F from the identity and no
+// values, B from a state of zeros), then the segments' states are known one after the other, and it is walked again,
+// but for the first, for its outputs. So n segments take the time of two, with 2 n - 3 walks a head at once: n is what
+// the SMs hold, a walk a SM, and at least three, of eight chunks at least. One sequence, without and with segments: 8192
+// tokens of 32 heads of 128 (three segments) 571 and 471 us, of 8 heads 455 and 228; 65536 tokens of 4 heads 3290 and
+// 672; 2048 tokens of 8 heads 125 and 113; but 1100 tokens of 4 heads 81 and 96, hence the 24 chunks.
+constexpr int kSms = 152, kLeastSegment = 8, kLeastCut = 24;
+inline int segment_chunks(int N, int S, int Hv)
+{
+    const long walks = (long)S * Hv, chunks = ((long)N + kChunk - 1) / kChunk;
+    const long n = walks > 0 ? (kSms / walks + 3) / 2 : 0;
+    if (n < 3)
+        return 0;
+    const long each = std::max<long>((chunks + S * n - 1) / (S * n), kLeastSegment);
+    return chunks > S * std::max<long>(2 * each, kLeastCut) ? (int)each : 0;
+}
+// As records: by the sequence's first token, and the sequence, and the segment.
+__host__ __device__ inline long segment_slots(int N, int S, int seg) { return (long)N / kChunk / seg + S; }
+__device__ __forceinline__ long segment_of(const DeltaPromptParams &p, int seq)
+{
+    return (long)(min(max(p.starts[seq], 0), p.N) / kChunk / p.seg) + seq;  // (one that is out of range keeps its state)
+}
+
+size_t records_bytes(int N, int S, int Hk, int Hv, int D)
+{
+    const size_t slots = record_slots(N, S);
+    return D == 64 ? slots * ((size_t)Hk * Record<64>::kKeyBytes + (size_t)Hv * Record<64>::kValueBytes)
+                   : slots * ((size_t)Hk * Record<128>::kKeyBytes + (size_t)Hv * Record<128>::kValueBytes);
+}
+
+// The last sequence that `of` has at or before the slot.
+template <typename Of>
+__device__ __forceinline__ int sequence_at(int S, long slot, Of of)
+{
+    int lo = 0;
+    for (int hi = S - 1; lo < hi;) {
+        const int mid = (lo + hi + 1) / 2;
+        if (of(mid) <= slot)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
 template <int D>
 __device__ __forceinline__ uint8_t *key_record(const DeltaPromptParams &p, int hk, long slot)
 {
@@ -140,7 +188,7 @@ __device__ __forceinline__ bool rows_of(const DeltaPromptParams &p, int s, int &
 // ------------------------------------------------------------------ keys and queries, T, P and the factors
 
 constexpr int kPrepThreads = 256;
-constexpr int kPitch = 68;    // floats of a row of a 64 x 64 matrix in shared memory
+constexpr int kPitch = 68, kTmpPitch = 36;  // floats of a row of a 64 x 64 matrix in shared memory, of a 32 x 32 one
 
 template <int D>
 struct PrepShared {
@@ -150,9 +198,9 @@ struct PrepShared {
         alignas(16) float t[kChunk][kPitch];       // T
         uint16_t before[kChunk][D + 8];            // the keys of the chunk before
     };
-    alignas(16) float a[kChunk][kPitch], tmp[32][36];  // A, in the end M
-    float r[kChunk], s[kChunk];                    // the inverse norms, with the powers of two
-    struct {
+    alignas(16) float a[kChunk][kPitch], tmp[32][kTmpPitch];  // A, in the end M
+    alignas(16) float r[kChunk], s[kChunk];        // the inverse norms, with the powers of two
+    struct alignas(16) {
         float gh[kChunk], gl[kChunk], beta[kChunk];  // G in two parts
         int bad;                                   // the first token with an infinity or a NaN
         uint32_t most_t;
@@ -207,35 +255,32 @@ __device__ __forceinline__ void put8(uint8_t *hi, uint8_t *lo, int i, int x, con
     *reinterpret_cast<uint4 *>(lo + piece_at(i, x)) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// A row's piece x of 8 elements, of the D / 8 lanes that share it: scaled by a power of two so that the row's largest
-// is in [1, 2), as fp16. Returns the row's sum of squares (before); `undo`: the power of two back.
+// Eight elements of a row, a piece, of the D / 8 lanes that share it: scaled by a power of two so that the row's largest
+// is in [1, 2), as fp16, over them. Returns the row's sum of squares (before); `undo`: the power of two back.
 template <int D>
-__device__ __forceinline__ float row_to_half(const uint16_t *src, bool there, int x, uint16_t *to, float &undo, bool &odd)
+__device__ __forceinline__ float row_to_half(uint4 &w, float &undo, bool &odd)
 {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (there)
-        w = *reinterpret_cast<const uint4 *>(src + x * 8);
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
     float sum = 0.f;
-    uint32_t most = 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         sum = fmaf(bf16_lo(u[c]), bf16_lo(u[c]), sum);
         sum = fmaf(bf16_hi(u[c]), bf16_hi(u[c]), sum);
-        most = max(most, max((u[c] << 16) & 0x7F800000u, u[c] & 0x7F800000u));
     }
+    // exponents, whose order is that of 16-bit integers, two at a time
+    uint32_t tops = __vmaxu2(__vmaxu2(u[0] & 0x7F807F80u, u[1] & 0x7F807F80u), __vmaxu2(u[2] & 0x7F807F80u, u[3] & 0x7F807F80u));
 #pragma unroll
     for (int o = D / 16; o > 0; o >>= 1) {
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+        tops = __vmaxu2(tops, __shfl_xor_sync(0xFFFFFFFFu, tops, o));
     }
+    const uint32_t most = max(tops << 16, tops & 0xFFFF0000u);
     odd = most == 0x7F800000u;
     const uint32_t e = min(most >> 23, 253u);
     const float by = e == 0 || odd ? 1.f : __uint_as_float((254u - e) << 23);
     undo = e == 0 || odd ? 1.f : __uint_as_float(e << 23);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        reinterpret_cast<uint32_t *>(to + x * 8)[c] = pack2_f16(bf16_lo(u[c]) * by, bf16_hi(u[c]) * by);
+    w = make_uint4(pack2_f16(bf16_lo(u[0]) * by, bf16_hi(u[0]) * by), pack2_f16(bf16_lo(u[1]) * by, bf16_hi(u[1]) * by),
+                   pack2_f16(bf16_lo(u[2]) * by, bf16_hi(u[2]) * by), pack2_f16(bf16_lo(u[3]) * by, bf16_hi(u[3]) * by));
     return sum;
 }
 
@@ -253,15 +298,7 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
     const long slot = blockIdx.x / p.Hk;
     const int hk = (int)(blockIdx.x - slot * p.Hk), group = p.Hv / p.Hk;
     // the sequence whose records this one is among: the last that begins at or before it
-    int seq = 0;
-    for (int lo = 0, hi = p.S - 1; lo < hi;) {
-        const int mid = (lo + hi + 1) / 2;
-        if (record_of(p.starts[mid], mid, 0) <= slot)
-            lo = mid;
-        else
-            hi = mid - 1;
-        seq = lo;
-    }
+    const int seq = sequence_at(p.S, slot, [&](int i) { return record_of(p.starts[i], i, 0); });
     int first, len;
     if (!rows_of(p, seq, first, len))
         return;
@@ -288,16 +325,23 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
     __syncthreads();
 
     // keys and queries, zeros after the last token, and their norms
-    constexpr int kPieces = D / 8;
+    constexpr int kPieces = D / 8, kRowsAtOnce = kPrepThreads / kPieces;
+    const int piece = tid % kPieces, row0 = tid / kPieces;
+    const uint16_t *const k_row = p.k + (size_t)hk * D + piece * 8, *const q_row = p.q + (size_t)hk * D + piece * 8;
+    uint8_t *const key_to = key_rec + (piece >> 3) * kTile;
 #pragma unroll
-    for (int i = tid; i < kChunk * kPieces * 2; i += kPrepThreads) {
-        const bool query = i >= kChunk * kPieces;
-        const int r = i / kPieces % kChunk, x = i % kPieces;
-        const uint16_t *src = query ? p.q + (size_t)(first + r) * p.q_stride : p.k + (size_t)(first + r) * p.k_stride;
+    for (int i = 0; i < 2 * kChunk / kRowsAtOnce; ++i) {
+        const bool query = i >= kChunk / kRowsAtOnce;
+        const int r = row0 + (i - (query ? kChunk / kRowsAtOnce : 0)) * kRowsAtOnce;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < n)
+            w = *reinterpret_cast<const uint4 *>(query ? q_row + (first + r) * p.q_stride : k_row + (first + r) * p.k_stride);
         float undo;
         bool odd;
-        const float sum = row_to_half<D>(src + (size_t)hk * D, r < n, x, query ? sh.q[r] : sh.k[r], undo, odd);
-        if (x == 0) {
+        const float sum = row_to_half<D>(w, undo, odd);
+        *reinterpret_cast<uint4 *>(query ? &sh.q[r][piece * 8] : &sh.k[r][piece * 8]) = w;
+        *reinterpret_cast<uint4 *>(key_to + (query ? Rec::kQ : Rec::kK) + piece_at(r, piece & 7)) = w;
+        if (piece == 0) {
             const float inv = (p.norm_eps >= 0.f ? 1.f / sqrtf(sum + p.norm_eps) : 1.f) * undo;
             if (query) {
                 sh.s[r] = inv * p.scale;
@@ -368,13 +412,11 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
     const int row = (warp & 3) * 16 + (lane >> 2);
     float d[8][4];                                 // of rows row and row + 8: columns 8 i + 2 (lane % 4) and the next
     rows_with_rows<D, 8>(warp >= 4 ? sh.q : sh.k, (warp & 3) * 16, sh.k, 0, d);
-    for (int i = tid; i < kChunk * kPieces * 2; i += kPrepThreads) {
-        const bool query = i >= kChunk * kPieces;
-        const int r = i / kPieces % kChunk, x = i % kPieces;
-        *reinterpret_cast<uint4 *>(key_rec + (query ? Rec::kQ : Rec::kK) + (x >> 3) * kTile + piece_at(r, x & 7)) =
-            *reinterpret_cast<const uint4 *>(query ? &sh.q[r][x * 8] : &sh.k[r][x * 8]);
-    }
     __syncthreads();
+    // T's blocks above the diagonal stay 0
+    for (int u = tid; u < kChunk * kChunk / 4; u += kPrepThreads)
+        if ((u & 15) >> 2 > u >> 8)
+            *reinterpret_cast<float4 *>(&sh.t[u >> 4][(u & 15) * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
 
 #pragma unroll 1
     for (int g = 0; g < group; ++g) {
@@ -390,36 +432,60 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
         const auto &gate = sh.gate[g & 7];
         const int bad = gate.bad;
         uint8_t *const rec = value_record<D>(p, hk * group + g, slot);
+        {
+            const int cut = (warp & 3) * 2 + 1;            // the last eight columns that a row of the warp's can see
+            float gh[2], gl[2], by[2], e[8][4];            // of rows row and row + 8, as d
+            uint32_t most[2] = {0, 0};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int i = row + 8 * half;
-            const float gh = gate.gh[i], gl = gate.gl[i], by = warp < 4 ? gate.beta[i] * sh.r[i] : sh.s[i];
-            uint32_t most = 0;
-            float e[8][2];
+            for (int half = 0; half < 2; ++half) {
+                const int i = row + 8 * half;
+                gh[half] = gate.gh[i];
+                gl[half] = gate.gl[i];
+                by[half] = warp < 4 ? gate.beta[i] * sh.r[i] : sh.s[i];
+            }
+            const int above = row + (warp < 4 ? 0 : 1);    // row's first column that is 0, of a row before `bad`
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
+            for (int t = 0; t < 8; ++t) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int j = 8 * t + 2 * (lane & 3) + c;
-                    const bool in = i < bad && (warp < 4 ? j < i : j <= i);
+                for (int c = 0; c < 4; ++c)
+                    e[t][c] = 0.f;
+                if (t > cut)
+                    continue;
+                const int j = 8 * t + 2 * (lane & 3);
+                const float2 jh = *reinterpret_cast<const float2 *>(&gate.gh[j]), jl = *reinterpret_cast<const float2 *>(&gate.gl[j]);
+                const float2 jr = *reinterpret_cast<const float2 *>(&sh.r[j]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int half = c >> 1;
                     // (the exponential's error, |x| 2^-24 of it or so, is at most 2^-25 of 1)
-                    float &x = e[t][c];
-                    x = in ? by * d[t][2 * half + c] * __expf((gh - gate.gh[j]) + (gl - gate.gl[j])) * sh.r[j] : 0.f;
-                    most = max(most, __float_as_uint(x) & 0x7FFFFFFFu);
+                    const float g = (gh[half] - (c & 1 ? jh.y : jh.x)) + (gl[half] - (c & 1 ? jl.y : jl.x));
+                    const float x = by[half] * d[t][c] * __expf(g) * (c & 1 ? jr.y : jr.x);
+                    e[t][c] = j + (c & 1) < above + 8 * half && row + 8 * half < bad ? x : 0.f;
+                    most[half] = max(most[half], __float_as_uint(e[t][c]) & 0x7FFFFFFFu);
                 }
+            }
             if (warp < 4) {
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
-                    *reinterpret_cast<float2 *>(&sh.a[i][8 * t + 2 * (lane & 3)]) = make_float2(e[t][0], e[t][1]);
+                    if (t <= cut) {
+                        float *const at = &sh.a[row][8 * t + 2 * (lane & 3)];
+                        *reinterpret_cast<float2 *>(at) = make_float2(e[t][0], e[t][1]);
+                        *reinterpret_cast<float2 *>(at + 8 * kPitch) = make_float2(e[t][2], e[t][3]);
+                    }
             } else {
-                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-                const Scale sp(most);
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    *reinterpret_cast<uint32_t *>(rec + Rec::kP + piece_at(i, t) + (lane & 3) * 4) = pack2_f16(e[t][0] * sp.by, e[t][1] * sp.by);
-                if ((lane & 3) == 0)
-                    reinterpret_cast<Factors *>(rec + Rec::kFactors)->p[i] = sp.undo;
+                for (int half = 0; half < 2; ++half) {
+                    most[half] = max(most[half], __shfl_xor_sync(0xFFFFFFFFu, most[half], 1));
+                    most[half] = max(most[half], __shfl_xor_sync(0xFFFFFFFFu, most[half], 2));
+                    const Scale sp(most[half]);
+                    const int i = row + 8 * half;
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        *reinterpret_cast<uint32_t *>(rec + Rec::kP + piece_at(i, t) + (lane & 3) * 4) =
+                            pack2_f16(e[t][2 * half] * sp.by, e[t][2 * half + 1] * sp.by);
+                    if ((lane & 3) == 0)
+                        reinterpret_cast<Factors *>(rec + Rec::kFactors)->p[i] = sp.undo;
+                }
             }
         }
         __syncthreads();
@@ -431,59 +497,69 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
             for (int i = 0; i < 16; ++i) {
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < i; ++k)
-                    sum[k & 3] = fmaf(sh.a[b + i][b + k], t[k], sum[k & 3]);
+                for (int k = 0; k < i; k += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(&sh.a[b + i][b + k]);  // (beyond the diagonal: 0)
+                    sum[0] = fmaf(a.x, t[k], sum[0]);
+                    if (k + 1 < i)
+                        sum[1] = fmaf(a.y, t[k + 1], sum[1]);
+                    if (k + 2 < i)
+                        sum[2] = fmaf(a.z, t[k + 2], sum[2]);
+                    if (k + 3 < i)
+                        sum[3] = fmaf(a.w, t[k + 3], sum[3]);
+                }
                 t[i] = i < j ? 0.f : i == j ? 1.f : -((sum[0] + sum[1]) + (sum[2] + sum[3]));
                 sh.t[b + i][b + j] = t[i];
             }
-        } else {
-            for (int u = tid - kChunk; u < kChunk * kChunk; u += kPrepThreads - kChunk)
-                if ((u & 63) >> 4 > u >> 10)
-                    sh.t[u >> 6][u & 63] = 0.f;
         }
         __syncthreads();
         // (T11 0; T21 T22) has T21 = -T22 A21 T11: two pairs of blocks of 16, then one of 32
         {
             const int pair = tid >> 7, i = (tid >> 3) & 15, j = (tid & 7) * 2, b = pair * 32;
-            float s0 = 0.f, s1 = 0.f;
+            const auto sixteen = [&](const float *x, const float *y, int pitch) {  // a row's products with two columns
+                float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float a = sh.a[b + 16 + i][b + k];
-                const float2 t = *reinterpret_cast<const float2 *>(&sh.t[b + k][b + j]);
-                s0 = fmaf(a, t.x, s0);
-                s1 = fmaf(a, t.y, s1);
-            }
-            *reinterpret_cast<float2 *>(&sh.tmp[pair * 16 + i][j]) = make_float2(s0, s1);
+                for (int k = 0; k < 16; k += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(x + k);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 t = *reinterpret_cast<const float2 *>(y + (k + c) * pitch);
+                        const float f = c == 0 ? a.x : c == 1 ? a.y : c == 2 ? a.z : a.w;
+                        s0 = fmaf(f, t.x, s0);
+                        s1 = fmaf(f, t.y, s1);
+                    }
+                }
+                return make_float2(s0, s1);
+            };
+            *reinterpret_cast<float2 *>(&sh.tmp[pair * 16 + i][j]) = sixteen(&sh.a[b + 16 + i][b], &sh.t[b][b + j], kPitch);
             __syncthreads();
-            s0 = s1 = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float a = sh.t[b + 16 + i][b + 16 + k];
-                const float2 t = *reinterpret_cast<const float2 *>(&sh.tmp[pair * 16 + k][j]);
-                s0 = fmaf(a, t.x, s0);
-                s1 = fmaf(a, t.y, s1);
-            }
-            *reinterpret_cast<float2 *>(&sh.t[b + 16 + i][b + j]) = make_float2(-s0, -s1);
+            const float2 s = sixteen(&sh.t[b + 16 + i][b + 16], &sh.tmp[pair * 16][j], kTmpPitch);
+            *reinterpret_cast<float2 *>(&sh.t[b + 16 + i][b + j]) = make_float2(-s.x, -s.y);
             __syncthreads();
         }
         {
-            const int i = tid >> 3, j = (tid & 7) * 4;
+            // four terms of a row's sums for four columns
+            const auto four = [&](float4 &s, const float *x, const float *y, int pitch) {
+                const float4 a = *reinterpret_cast<const float4 *>(x);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float4 t = *reinterpret_cast<const float4 *>(y + c * pitch);
+                    const float f = c == 0 ? a.x : c == 1 ? a.y : c == 2 ? a.z : a.w;
+                    s = make_float4(fmaf(f, t.x, s.x), fmaf(f, t.y, s.y), fmaf(f, t.z, s.z), fmaf(f, t.w, s.w));
+                }
+            };
+            // A21 T11, a warp four columns: T11's rows before the columns' are 0
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-                const float a = sh.a[32 + i][k];
-                const float4 t = *reinterpret_cast<const float4 *>(&sh.t[k][j]);
-                s = make_float4(fmaf(a, t.x, s.x), fmaf(a, t.y, s.y), fmaf(a, t.z, s.z), fmaf(a, t.w, s.w));
-            }
-            *reinterpret_cast<float4 *>(&sh.tmp[i][j]) = s;
+#pragma unroll 2
+            for (int k = warp * 4; k < 32; k += 4)
+                four(s, &sh.a[32 + lane][k], &sh.t[k][warp * 4], kPitch);
+            *reinterpret_cast<float4 *>(&sh.tmp[lane][warp * 4]) = s;
             __syncthreads();
+            // T22 times that, a warp four rows: T22's columns after the rows' are 0
+            const int i = tid >> 3, j = (tid & 7) * 4;
             s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-                const float a = sh.t[32 + i][32 + k];
-                const float4 t = *reinterpret_cast<const float4 *>(&sh.tmp[k][j]);
-                s = make_float4(fmaf(a, t.x, s.x), fmaf(a, t.y, s.y), fmaf(a, t.z, s.z), fmaf(a, t.w, s.w));
-            }
+#pragma unroll 2
+            for (int k = 0; k <= warp * 4; k += 4)
+                four(s, &sh.t[32 + i][32 + k], &sh.tmp[k][j], kTmpPitch);
             *reinterpret_cast<float4 *>(&sh.t[32 + i][j]) = make_float4(-s.x, -s.y, -s.z, -s.w);
             __syncthreads();
         }
@@ -496,11 +572,11 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
 #pragma unroll
                 for (int d = 0; d < 8; d += 4) {
                     const int j = (x + c) * 8 + d;
-                    const float4 t = *reinterpret_cast<const float4 *>(&sh.t[i][j]);
-                    tv[c][d] = t.x * gate.beta[j];
-                    tv[c][d + 1] = t.y * gate.beta[j + 1];
-                    tv[c][d + 2] = t.z * gate.beta[j + 2];
-                    tv[c][d + 3] = t.w * gate.beta[j + 3];
+                    const float4 t = *reinterpret_cast<const float4 *>(&sh.t[i][j]), b = *reinterpret_cast<const float4 *>(&gate.beta[j]);
+                    tv[c][d] = t.x * b.x;
+                    tv[c][d + 1] = t.y * b.y;
+                    tv[c][d + 2] = t.z * b.z;
+                    tv[c][d + 3] = t.w * b.w;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         most = max(most, __float_as_uint(tv[c][d + e]) & 0x7FFFFFFFu);
@@ -526,11 +602,13 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
     __syncthreads();                               // T has been read
     // M: the keys with those of the chunk before, which is whole
 #pragma unroll
-    for (int i = tid; i < kChunk * kPieces; i += kPrepThreads) {
-        const int r = i / kPieces, x = i % kPieces;
+    for (int i = 0; i < kChunk / kRowsAtOnce; ++i) {
+        const int r = row0 + i * kRowsAtOnce;
+        uint4 w = *reinterpret_cast<const uint4 *>(k_row + (first - kChunk + r) * p.k_stride);
         float undo;
         bool odd;
-        row_to_half<D>(p.k + (size_t)(first - kChunk + r) * p.k_stride + (size_t)hk * D, true, x, sh.before[r], undo, odd);
+        row_to_half<D>(w, undo, odd);
+        *reinterpret_cast<uint4 *>(&sh.before[r][piece * 8]) = w;
     }
     __syncthreads();
     {
@@ -671,10 +749,41 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
     const uint32_t tmem = sh.tmem;
     pdl_launch_dependents();
     pdl_wait();
-    const int seq = blockIdx.x / p.Hv, h = blockIdx.x - seq * p.Hv, hk = h / (p.Hv / p.Hk);
-    int first, len;
-    if (!rows_of(p, seq, first, len))
-        len = 0;
+    const int h = blockIdx.x % p.Hv, hk = h / (p.Hv / p.Hk);
+    int seq = blockIdx.x / p.Hv, first, len;
+    // where the state comes from and goes to; of a walk without values from the identity: its column's 1
+    const float *from = nullptr;
+    float *to = nullptr;
+    bool with_values = true, with_outputs = true;
+    long record = 0;
+    if (p.seg == 0) {
+        if (!rows_of(p, seq, first, len))
+            len = 0;
+        record = record_of(first, seq, 0);
+        from = p.state_in + ((size_t)seq * p.Hv + h) * D * D;
+        to = len > 0 || p.state_out != p.state_in ? p.state_out + ((size_t)seq * p.Hv + h) * D * D : nullptr;
+    } else {
+        const long slots = segment_slots(p.N, p.S, p.seg);
+        long slot = seq;
+        with_values = slot < slots;
+        slot -= with_values ? 0 : slots;
+        seq = sequence_at(p.S, slot, [&](int i) { return segment_of(p, i); });
+        if (!rows_of(p, seq, first, len))
+            len = 0;
+        const long at = slot - segment_of(p, seq), last = max(((long)len + kChunk - 1) / kChunk - 1, 0l) / p.seg;
+        const auto end_of = [&](long slot, bool values) { return p.ends + (((values ? 0 : slots) + slot) * p.Hv + h) * D * D; };
+        const bool mine = at >= 0 && at <= last && (p.again ? at > 0 : at == 0 ? with_values : at < last);
+        if (mine) {
+            from = at == 0 ? p.state_in + ((size_t)seq * p.Hv + h) * D * D : p.again ? end_of(slot - 1, true) : nullptr;
+            to = at == last ? p.state_out + ((size_t)seq * p.Hv + h) * D * D : end_of(slot, with_values);
+            if (len == 0 && p.state_out == p.state_in)
+                to = nullptr;
+            with_outputs = p.again || at == 0;
+        }
+        record = record_of(first, seq, 0) + at * p.seg;
+        first += (int)(at * p.seg) * kChunk;
+        len = mine ? (int)min((long)len - at * p.seg * kChunk, (long)p.seg * kChunk) : 0;
+    }
     const int chunks = (len + kChunk - 1) / kChunk;
     const int col = tid & 127;                      // of the threads that have one
     const bool there = col < D;
@@ -692,13 +801,17 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             return most3(most3(top[0][col], top[1][col], top[2][col]), top[3][col], 0.f);
         };
         // of each 64 elements of the column a thread has 16
-        const size_t state_at = (((size_t)seq * p.Hv + h) * D + t0) * D + col, step = (size_t)p.Hv * D;
+        const size_t step = (size_t)p.Hv * D;
         constexpr int kMine = D / 4;
         uint64_t s[kMine / 2];                      // two elements each
 #pragma unroll
         for (int i = 0; i < kMine / 2; ++i) {
-            const float *const at = p.state_in + state_at + (size_t)((i >> 3) * 64 + (i & 7) * 2) * D;
-            s[i] = there ? f32x2(at[0], at[D]) : 0;
+            const int d = t0 + (i >> 3) * 64 + (i & 7) * 2;
+            s[i] = 0;
+            if (from && there)
+                s[i] = f32x2(from[d * D + col], from[(d + 1) * D + col]);
+            else if (!with_values)
+                s[i] = f32x2(d == col, d + 1 == col);
         }
         float keep = 1.f, s_undo, y_by = 0.f, z_by = 0.f, w_undo = 0.f;  // of the chunk before, and what undoes the scales
         int bad = kChunk;                           // of the chunk before
@@ -789,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             to_operand();
 #pragma unroll 1
         for (int ch = 0; ch < chunks; ++ch) {
-            const int n = there ? min(kChunk, len - ch * kChunk) - t0 : 0, turn = ch & 1;
+            const int n = there && with_values ? min(kChunk, len - ch * kChunk) - t0 : 0, turn = ch & 1;
             const uint32_t phase = ch & 1;
             // R
             wait(&sh.f_full[ch % P::kF], (ch / P::kF) & 1, sh);
@@ -902,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             tc_fence_before();
             mbar_arrive(&sh.w_ready);
             // the outputs of the chunk before, while M's product runs
-            if (ch > 0)
+            if (ch > 0 && with_outputs)
                 outputs(ch - 1);
             keep = f.keep;
             z_by = su.undo * u_by;
@@ -912,13 +1025,17 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
         if (chunks > 0) {
             y_by = s_undo;
             update(chunks - 1);
-            outputs(chunks - 1);
+            if (with_outputs)
+                outputs(chunks - 1);
         }
-        if (there && (chunks > 0 || p.state_out != p.state_in))
+        if (there && to)
 #pragma unroll
             for (int i = 0; i < kMine / 2; ++i) {
-                float *const at = p.state_out + state_at + (size_t)((i >> 3) * 64 + (i & 7) * 2) * D;
-                f32x2_unpack(s[i], at[0], at[D]);
+                const int d = t0 + (i >> 3) * 64 + (i & 7) * 2;
+                if (with_values)
+                    f32x2_unpack(s[i], to[d * D + col], to[(d + 1) * D + col]);
+                else                                // F by columns, as it is read
+                    *reinterpret_cast<uint64_t *>(&to[col * D + d]) = s[i];
             }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -1004,15 +1121,17 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
                     umma_commit(&sh.x_done);
                 }
                 __syncwarp();
-                ok = wait(&sh.c_full[ch % P::kC], (ch / P::kC) & 1, sh) && (ch == 0 || wait(&sh.y_free, phase ^ 1, sh));
+                ok = !with_outputs || (wait(&sh.c_full[ch % P::kC], (ch / P::kC) & 1, sh) && (ch == 0 || wait(&sh.y_free, phase ^ 1, sh)));
                 if (!ok)
                     break;
                 tc_fence_after();
                 if (elect_one()) {
-                    by_state(kY, place_c(ch), 1);
-                    by_tokens(kZ, kDS, place_c(ch) + Rec::kRows, 0);
-                    umma_commit(&sh.o_done);
-                    umma_commit(&sh.c_empty[ch % P::kC]);
+                    if (with_outputs) {
+                        by_state(kY, place_c(ch), 1);
+                        by_tokens(kZ, kDS, place_c(ch) + Rec::kRows, 0);
+                        umma_commit(&sh.o_done);
+                        umma_commit(&sh.c_empty[ch % P::kC]);
+                    }
                     update(ch, 0);
                     if (D > 64 && !more)
                         update(ch, 1);
@@ -1021,8 +1140,7 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             }
         } else if (warp == kLoadWarp) {
             // ---------------------------------------------------------- copies
-            const long slot = record_of(first, seq, 0);
-            const uint8_t *key = key_record<D>(p, hk, slot), *value = value_record<D>(p, h, slot);
+            const uint8_t *key = key_record<D>(p, hk, record), *value = value_record<D>(p, h, record);
             bool ok = true;
 #pragma unroll 1
             for (int ch = 0; ok && ch < chunks; ++ch, key += Rec::kKeyBytes, value += Rec::kValueBytes) {
@@ -1042,8 +1160,8 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
                     bulk_copy_g2s(smem + P::kFt + f * kFactorBytes, value + Rec::kFactors, kFactorBytes, &sh.f_full[f]);
                 }
                 __syncwarp();
-                ok = ok && wait(&sh.c_empty[c], ((ch / P::kC) & 1) ^ 1, sh);
-                if (ok && lane == 0) {
+                ok = ok && (!with_outputs || wait(&sh.c_empty[c], ((ch / P::kC) & 1) ^ 1, sh));
+                if (ok && with_outputs && lane == 0) {
                     mbar_arrive_expect_tx(&sh.c_full[c], P::kCBytes);
                     bulk_copy_g2s(smem + P::kCt + c * P::kCBytes, key + Rec::kQ, Rec::kRows, &sh.c_full[c]);
                     bulk_copy_g2s(smem + P::kCt + c * P::kCBytes + Rec::kRows, value + Rec::kP, kTile, &sh.c_full[c]);
@@ -1069,8 +1187,78 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
         tmem_dealloc(tmem, kTmemCols);
 }
 
+// The states after a sequence's segments but the last, from the first one's on: S <- F S + B, over B. A block has eight
+// columns of a head's; kSplit threads share a row's sum. F comes by columns, the next segment's a step ahead.
+constexpr int kJoinThreads = 256, kJoinColumns = 8;
 template <int D>
-cudaError_t launch(const DeltaPromptParams &p, cudaStream_t stream)
+__global__ void __launch_bounds__(kJoinThreads) hc_delta_join_kernel(const DeltaPromptParams p)
+{
+    constexpr int kSplit = kJoinThreads / D, kTerms = D / kSplit, kBlocks = D / kJoinColumns;
+    __shared__ __align__(16) float cur[D][kJoinColumns], sums[kSplit - 1][2][D][4];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, row = tid % D, part = tid / D, k0 = part * kTerms;
+    const int block = blockIdx.x % kBlocks, head = blockIdx.x / kBlocks, seq = head / p.Hv, h = head - seq * p.Hv;
+    int first, len;
+    if (!rows_of(p, seq, first, len))
+        return;
+    const long slots = segment_slots(p.N, p.S, p.seg), slot = segment_of(p, seq);
+    const long last = max(((long)len + kChunk - 1) / kChunk - 1, 0l) / p.seg;
+    if (last < 2)
+        return;
+    const auto end_of = [&](long at, bool values) { return p.ends + (((values ? 0 : slots) + slot + at) * p.Hv + h) * D * D; };
+    float f[kTerms];
+    const auto ask = [&](long at) {
+#pragma unroll
+        for (int i = 0; i < kTerms; ++i)
+            f[i] = end_of(at, false)[(k0 + i) * D + row];
+    };
+    ask(1);
+    if (part == 0) {
+        const float4 *const at = reinterpret_cast<const float4 *>(end_of(0, true) + row * D + block * kJoinColumns);
+        *reinterpret_cast<float4 *>(&cur[row][0]) = at[0];
+        *reinterpret_cast<float4 *>(&cur[row][4]) = at[1];
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (long at = 1; at < last; ++at) {
+        float4 *const end = reinterpret_cast<float4 *>(end_of(at, true) + row * D + block * kJoinColumns);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f), z = s;
+        if (part == 0) {
+            s = end[0];
+            z = end[1];
+        }
+#pragma unroll
+        for (int i = 0; i < kTerms; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(&cur[k0 + i][0]), y = *reinterpret_cast<const float4 *>(&cur[k0 + i][4]);
+            s = make_float4(fmaf(f[i], x.x, s.x), fmaf(f[i], x.y, s.y), fmaf(f[i], x.z, s.z), fmaf(f[i], x.w, s.w));
+            z = make_float4(fmaf(f[i], y.x, z.x), fmaf(f[i], y.y, z.y), fmaf(f[i], y.z, z.z), fmaf(f[i], y.w, z.w));
+        }
+        if (at + 1 < last)
+            ask(at + 1);
+        if (part > 0) {
+            *reinterpret_cast<float4 *>(&sums[part - 1][0][row][0]) = s;
+            *reinterpret_cast<float4 *>(&sums[part - 1][1][row][0]) = z;
+        }
+        __syncthreads();
+        if (part == 0) {
+#pragma unroll
+            for (int i = 0; i < kSplit - 1; ++i) {
+                const float4 x = *reinterpret_cast<const float4 *>(&sums[i][0][row][0]), y = *reinterpret_cast<const float4 *>(&sums[i][1][row][0]);
+                s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+                z = make_float4(z.x + y.x, z.y + y.y, z.z + y.z, z.w + y.w);
+            }
+            end[0] = s;
+            end[1] = z;
+            *reinterpret_cast<float4 *>(&cur[row][0]) = s;
+            *reinterpret_cast<float4 *>(&cur[row][4]) = z;
+        }
+        __syncthreads();
+    }
+}
+
+template <int D>
+cudaError_t launch(DeltaPromptParams p, cudaStream_t stream)
 {
     static_assert(Plan<D>::kTotal + sizeof(Shared) <= 227 * 1024 && sizeof(PrepShared<D>) <= 227 * 1024, "shared memory");
     int per_sm = 1;
@@ -1093,8 +1281,22 @@ cudaError_t launch(const DeltaPromptParams &p, cudaStream_t stream)
     lc.numAttrs = 1;
     lc.stream = stream;
     lc.blockDim = dim3(kThreads);
-    lc.gridDim = dim3((unsigned)(p.S * p.Hv));
     lc.dynamicSmemBytes = Plan<D>::kTotal;
+    p.seg = segment_chunks(p.N, p.S, p.Hv);
+    if (p.seg == 0) {
+        lc.gridDim = dim3((unsigned)(p.S * p.Hv));
+        return cudaLaunchKernelEx(&lc, hc_delta_scan_kernel<D>, p, map_v);
+    }
+    const long slots = segment_slots(p.N, p.S, p.seg);
+    p.ends = reinterpret_cast<float *>(p.work + records_bytes(p.N, p.S, p.Hk, p.Hv, D));
+    lc.gridDim = dim3((unsigned)(2 * slots * p.Hv));
+    e = cudaLaunchKernelEx(&lc, hc_delta_scan_kernel<D>, p, map_v);
+    if (e == cudaSuccess)
+        e = launch_pdl(hc_delta_join_kernel<D>, dim3((unsigned)(p.S * p.Hv * (D / kJoinColumns))), dim3(kJoinThreads), 0, true, stream, p);
+    if (e != cudaSuccess)
+        return e;
+    p.again = 1;
+    lc.gridDim = dim3((unsigned)(slots * p.Hv));
     return cudaLaunchKernelEx(&lc, hc_delta_scan_kernel<D>, p, map_v);
 }
 
@@ -1102,9 +1304,8 @@ cudaError_t launch(const DeltaPromptParams &p, cudaStream_t stream)
 
 size_t delta_prompt_bytes(int N, int S, int Hk, int Hv, int D)
 {
-    const size_t slots = record_slots(N, S);
-    return D == 64 ? slots * ((size_t)Hk * Record<64>::kKeyBytes + (size_t)Hv * Record<64>::kValueBytes)
-                   : slots * ((size_t)Hk * Record<128>::kKeyBytes + (size_t)Hv * Record<128>::kValueBytes);
+    const int seg = segment_chunks(N, S, Hv);
+    return records_bytes(N, S, Hk, Hv, D) + (seg ? sizeof(float) * 2 * (size_t)segment_slots(N, S, seg) * Hv * D * D : 0);
 }
 
 cudaError_t launch_delta_prompt(const DeltaPromptParams &p, const LaunchCfg &, cudaStream_t stream)
