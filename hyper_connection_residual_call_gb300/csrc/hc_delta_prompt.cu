@@ -195,10 +195,10 @@ struct PrepShared {
     uint16_t k[kChunk][D + 8];                     // fp16
     union {                                        // one after the other
         uint16_t q[kChunk][D + 8];
-        alignas(16) float t[kChunk][kPitch];       // T
         uint16_t before[kChunk][D + 8];            // the keys of the chunk before
+        alignas(16) float t[kChunk][kPitch];       // T
     };
-    alignas(16) float a[kChunk][kPitch], tmp[32][kTmpPitch];  // A, in the end M
+    alignas(16) float a[kChunk][kPitch], tmp[32][kTmpPitch];  // M, then A
     alignas(16) float r[kChunk], s[kChunk];        // the inverse norms, with the powers of two
     struct alignas(16) {
         float gh[kChunk], gl[kChunk], beta[kChunk];  // G in two parts
@@ -411,8 +411,43 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
     // keys with keys (warps 0-3) and queries with keys (4-7), 16 rows a warp, in registers
     const int row = (warp & 3) * 16 + (lane >> 2);
     float d[8][4];                                 // of rows row and row + 8: columns 8 i + 2 (lane % 4) and the next
+    // (the rows of the chunk before, which is whole, are asked for now)
+    uint4 before[kChunk / kRowsAtOnce];
+    if (chunk > 0)
+#pragma unroll
+        for (int i = 0; i < kChunk / kRowsAtOnce; ++i)
+            before[i] = *reinterpret_cast<const uint4 *>(k_row + (first - kChunk + row0 + i * kRowsAtOnce) * p.k_stride);
     rows_with_rows<D, 8>(warp >= 4 ? sh.q : sh.k, (warp & 3) * 16, sh.k, 0, d);
     __syncthreads();
+    if (chunk > 0) {
+        // M: the keys with those of the chunk before
+#pragma unroll
+        for (int i = 0; i < kChunk / kRowsAtOnce; ++i) {
+            float undo;
+            bool odd;
+            row_to_half<D>(before[i], undo, odd);
+            *reinterpret_cast<uint4 *>(&sh.before[row0 + i * kRowsAtOnce][piece * 8]) = before[i];
+        }
+        __syncthreads();
+        const int col = (warp >> 2) * 32;
+        float m[4][4];
+        rows_with_rows<D, 4>(sh.k, (warp & 3) * 16, sh.before, col, m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float *at = &sh.a[row][col + i * 8 + (lane & 3) * 2];
+            *reinterpret_cast<float2 *>(at) = make_float2(m[i][0], m[i][1]);
+            *reinterpret_cast<float2 *>(at + 8 * kPitch) = make_float2(m[i][2], m[i][3]);
+        }
+        __syncthreads();
+        const int i = tid >> 2, x = (tid & 3) * 2;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float4 u = *reinterpret_cast<const float4 *>(&sh.a[i][(x + c) * 8]), w = *reinterpret_cast<const float4 *>(&sh.a[i][(x + c) * 8 + 4]);
+            const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+            put8(key_rec + Rec::kM, key_rec + Rec::kM + kTile, i, x + c, v);
+        }
+        __syncthreads();
+    }
     // T's blocks above the diagonal stay 0
     for (int u = tid; u < kChunk * kChunk / 4; u += kPrepThreads)
         if ((u & 15) >> 2 > u >> 8)
@@ -595,41 +630,6 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
             }
             if (tid == 0)
                 reinterpret_cast<Factors *>(rec + Rec::kFactors)->t = st.undo;
-        }
-    }
-    if (chunk == 0)
-        return;
-    __syncthreads();                               // T has been read
-    // M: the keys with those of the chunk before, which is whole
-#pragma unroll
-    for (int i = 0; i < kChunk / kRowsAtOnce; ++i) {
-        const int r = row0 + i * kRowsAtOnce;
-        uint4 w = *reinterpret_cast<const uint4 *>(k_row + (first - kChunk + r) * p.k_stride);
-        float undo;
-        bool odd;
-        row_to_half<D>(w, undo, odd);
-        *reinterpret_cast<uint4 *>(&sh.before[r][piece * 8]) = w;
-    }
-    __syncthreads();
-    {
-        const int col = (warp >> 2) * 32;
-        float d[4][4];
-        rows_with_rows<D, 4>(sh.k, (warp & 3) * 16, sh.before, col, d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float *at = &sh.a[row][col + i * 8 + (lane & 3) * 2];
-            *reinterpret_cast<float2 *>(at) = make_float2(d[i][0], d[i][1]);
-            *reinterpret_cast<float2 *>(at + 8 * kPitch) = make_float2(d[i][2], d[i][3]);
-        }
-    }
-    __syncthreads();
-    {
-        const int i = tid >> 2, x = (tid & 3) * 2;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const float4 u = *reinterpret_cast<const float4 *>(&sh.a[i][(x + c) * 8]), w = *reinterpret_cast<const float4 *>(&sh.a[i][(x + c) * 8 + 4]);
-            const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-            put8(key_rec + Rec::kM, key_rec + Rec::kM + kTile, i, x + c, v);
         }
     }
 }
