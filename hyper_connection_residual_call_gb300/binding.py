@@ -9,8 +9,9 @@ runs in the library's CUDA kernels:
 * ``hc_call`` / ``hc_inject_call`` / ``hc_mixer`` / ``hc_inject_add`` /
   ``hc_replicate_entry`` / ``hc_stack``, and for a speculative decoding step
   ``hc_rope`` / ``hc_kv_write`` / ``hc_kv_read`` / ``hc_kv_compact`` /
-  ``hc_tree_build`` / ``hc_tree_attention`` / ``hc_verify``: the same calls
-  for torch CUDA tensors. They allocate outputs/workspace with torch when not given, pass
+  ``hc_tree_build`` / ``hc_tree_attention`` / ``hc_verify``, and for a prompt's
+  pass ``hc_qk_norm_rope`` / ``hc_prompt_attention`` / ``hc_delta_prompt`` /
+  ``hc_delta_step`` / ``hc_logprobs``: the same calls for torch CUDA tensors. They allocate outputs/workspace with torch when not given, pass
   the current torch stream, and raise ``HCError`` on any error status.
 
 There is no fallback: if the library is not built or cannot be loaded, every

