@@ -235,11 +235,17 @@ struct Items {
 // Bits 15 and 31: whether the halves are infinities or NaNs (exponents of ones carry into them).
 __device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
 
-// 32 bytes, a whole sector, by one instruction: a lane has a row of its own.
-__device__ __forceinline__ void store32(void *to, const uint32_t *w)
+// 32 bytes, a whole sector: a lane has a row of its own. By one instruction where the results lie so; they need only lie on
+// 16 bytes.
+__device__ __forceinline__ void store32(uint16_t *to, const uint32_t *w, bool whole)
 {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                 ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+    } else {
+        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(to + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 template <int D>
@@ -294,6 +300,7 @@ hc_prompt_attn_kernel(const __grid_constant__ PromptAttnParams p, const __grid_c
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_base + s * kKeys, to = tmem + lane_base + 256 + s * 128;
         const float sc = p.scale_log2;
+        const bool whole = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         const int row_t = row / p.Gp, row_g = row - row_t * p.Gp;
         uint32_t s_phase = 0, o_phase = 0;
         Items items;
@@ -401,8 +408,8 @@ hc_prompt_attn_kernel(const __grid_constant__ PromptAttnParams p, const __grid_c
                 for (int c = 0; c < 16; ++c)
                     w[c] = pack2_bf16(__uint_as_float(x[2 * c]) * inv, __uint_as_float(x[2 * c + 1]) * inv);
                 uint16_t *const out = p.out + at * D + 32 * i;
-                store32(out, w);
-                store32(out + 16, w + 8);
+                store32(out, w, whole);
+                store32(out + 16, w + 8, whole);
             }
             if (wild && valid) {  // infinities and NaNs among the values that were looked through and that the row sees
                 const int from = it.token / kKeys * kKeys;

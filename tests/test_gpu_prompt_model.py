@@ -319,3 +319,38 @@ def test_refusals():
             pytest.fail(f"{what} was taken")
     torch.cuda.synchronize()
     assert B.device_status() == B.TS_OK
+
+
+def shifted(t):
+    """``t``'s elements at an address that is a multiple of 16 bytes and not of 32."""
+    flat = torch.empty(t.numel() + 16 // t.element_size(), dtype=t.dtype, device=t.device)
+    got = flat[16 // t.element_size():].view(t.shape)
+    assert got.data_ptr() % 32 == 16
+    return got.copy_(t)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_addresses_on_16_bytes(d):
+    """Inputs, outputs and states need lie on 16 bytes only: the same bits as where they lie on more."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    n = 150
+    starts, positions = packed([90, 60])
+    q, k, v, w = r(n, 4, d).bfloat16(), r(n, 2, d).bfloat16(), r(n, 2, d).bfloat16(), r(d).bfloat16()
+    table, decay, beta, state = B.rope_table(256, d, 10000.0), -r(n, 2).abs(), torch.sigmoid(r(n, 2)), r(2, 2, d, d)
+    S = shifted
+    want = B.hc_prompt_attention(q, k, v, starts)
+    got = B.hc_prompt_attention(S(q), S(k), S(v), starts, out=S(torch.zeros_like(q)))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    want = B.hc_qk_norm_rope(q, k, positions, table, w, w)
+    got = B.hc_qk_norm_rope(S(q), S(k), positions, S(table), S(w), S(w), q_out=S(torch.zeros_like(q)), k_out=S(torch.zeros_like(k)))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    args = (k, q[:, :2], v, decay, beta, state, starts)
+    want = B.hc_delta_prompt(*args, state_out=torch.zeros_like(state))
+    got = B.hc_delta_prompt(*map(S, args[:6]), starts, out=S(torch.zeros_like(v)), state_out=S(torch.zeros_like(state)))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    args = [x[:8].reshape(2, 4, *x.shape[1:]) for x in args[:5]] + [state]
+    want = B.hc_delta_step(*args, state_out=torch.zeros_like(state))
+    got = B.hc_delta_step(*map(S, args), out=S(torch.zeros_like(args[2])), state_out=S(torch.zeros_like(state)))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert B.device_status() == B.TS_OK
