@@ -25,6 +25,28 @@ using tshc::rows_overlap;
 // Bytes from the first row's first element to the last row's last.
 size_t span(int n, long stride, long width, size_t size) { return ((size_t)(n - 1) * stride + width) * size; }
 
+// Memory that a call reads or writes (n = 0: not given).
+struct Part {
+    const void *p;
+    size_t n;
+    const char *name;
+};
+
+// What is written apart from all of what is read, and from one another.
+template <int W, int R>
+ts_status check_apart(const Part (&written)[W], const Part (&read)[R])
+{
+    for (int i = 0; i < W; ++i) {
+        for (const Part &r : read)
+            if (written[i].n > 0 && r.n > 0 && overlap(written[i].p, written[i].n, r.p, r.n))
+                return api_error(TS_ERR_INVALID_ARG, "%s overlaps %s", written[i].name, r.name);
+        for (int j = 0; j < i; ++j)
+            if (written[i].n > 0 && written[j].n > 0 && overlap(written[i].p, written[i].n, written[j].p, written[j].n))
+                return api_error(TS_ERR_INVALID_ARG, "%s overlaps %s", written[j].name, written[i].name);
+    }
+    return TS_OK;
+}
+
 // The heads of the gated delta rule: D, the key heads and the value heads that share them.
 ts_status check_delta_heads(int k_heads, int v_heads, int D)
 {
@@ -206,6 +228,11 @@ ts_status ts_hc_prompt_attention(const void *q, long q_stride, const void *k, lo
         return api_error(TS_ERR_INVALID_ARG, "out overlaps k");
     if (rows_overlap(out, qw, qw, v, v_stride, kw, N))
         return api_error(TS_ERR_INVALID_ARG, "out overlaps v");
+    const Part written[] = {{out, span(N, qw, qw, 2), "out"}, {lse, lse ? sizeof(float) * (size_t)N * q_heads : 0, "lse"}};
+    const Part rows[] = {{q, span(N, q_stride, qw, 2), "q"}, {k, span(N, k_stride, kw, 2), "k"}, {v, span(N, v_stride, kw, 2), "v"}};
+    const Part places[] = {{starts, sizeof(int32_t) * ((size_t)S + 1), "starts"}}, lse_alone[] = {written[1]};
+    TS_TRY(check_apart(written, places));
+    TS_TRY(check_apart(lse_alone, rows));
     if (tshc::prompt_attn_blocks(N, S, q_heads, kv_heads) > INT_MAX)
         return api_error(TS_ERR_UNSUPPORTED, "%d tokens of %d heads are too many for one call: split them", N, q_heads);
     tshc::LaunchCfg cfg;
@@ -241,6 +268,14 @@ ts_status ts_hc_delta_step(const void *q, long q_stride, const void *k, long k_s
     TS_TRY(check_states(state_in, state_out, B, v_heads, D, out, span(B * T, (long)v_heads * D, (long)v_heads * D, 2)));
     if (counts)
         TS_TRY(check_ptr_api(counts, "counts", 4));
+    const long kw = (long)k_heads * D, vw = (long)v_heads * D;
+    const size_t gates = sizeof(float) * (size_t)B * T * v_heads;
+    const Part written[] = {{state_out, sizeof(float) * (size_t)B * vw * D, "state_out"}}, outs[] = {{out, span(B * T, vw, vw, 2), "out"}};
+    const Part read[] = {{q, span(B * T, q_stride, kw, 2), "q"}, {k, span(B * T, k_stride, kw, 2), "k"}, {v, span(B * T, v_stride, vw, 2), "v"},
+                         {decay, gates, "decay"}, {beta, gates, "beta"}, {counts, counts ? sizeof(int32_t) * (size_t)B : 0, "counts"}};
+    const Part counted[] = {read[5]};
+    TS_TRY(check_apart(written, read));
+    TS_TRY(check_apart(outs, counted));
     tshc::LaunchCfg cfg;
     tshc::DeltaStepParams p{};
     TS_TRY(device(&cfg, &p.status));
@@ -294,6 +329,15 @@ ts_status ts_hc_delta_prompt(const void *q, long q_stride, const void *k, long k
     if (!workspace || workspace_bytes < need)
         return api_error(TS_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace ? workspace_bytes : (size_t)0, need);
     TS_TRY(check_ptr_api(workspace, "workspace", 256));
+    const long kw = (long)k_heads * D, vw = (long)v_heads * D;
+    const size_t gates = sizeof(float) * (size_t)N * v_heads, states = sizeof(float) * (size_t)S * vw * D;
+    const Part written[] = {{state_out, states, "state_out"}, {workspace, need, "workspace"}}, outs[] = {{out, span(N, vw, vw, 2), "out"}};
+    const Part read[] = {{q, span(N, q_stride, kw, 2), "q"}, {k, span(N, k_stride, kw, 2), "k"}, {v, span(N, v_stride, vw, 2), "v"},
+                         {decay, gates, "decay"}, {beta, gates, "beta"}, {starts, sizeof(int32_t) * ((size_t)S + 1), "starts"}};
+    const Part apart[] = {read[5], written[1]}, states_in[] = {{state_in, states, "state_in"}}, work[] = {written[1]};
+    TS_TRY(check_apart(written, read));
+    TS_TRY(check_apart(outs, apart));
+    TS_TRY(check_apart(work, states_in));
     tshc::LaunchCfg cfg;
     tshc::DeltaPromptParams p{};
     TS_TRY(device(&cfg, &p.status));

@@ -186,3 +186,32 @@ def test_reference_logprobs_match_torch():
     lp, h, _, _, order = P.logprobs(x.numpy())
     want = torch.log_softmax(x, 0)
     assert np.allclose(lp, want) and np.isclose(h, -(want.exp() * want).sum()) and order[0] == int(x.argmax())
+
+
+# ------------------------------------------------------------------ outputs over what else a call reads or writes
+
+@pytest.mark.parametrize("kw,needle", [
+    (dict(starts=FAKE + 4 * MB), "out overlaps starts"), (dict(lse=FAKE + 4 * MB), "out overlaps lse"), (dict(lse=FAKE + 64), "lse overlaps q"),
+    (dict(lse=FAKE + MB), "lse overlaps k"), (dict(lse=FAKE + 2 * MB), "lse overlaps v"), (dict(lse=FAKE + 3 * MB, starts=FAKE + 3 * MB), "lse overlaps starts"),
+])
+def test_attention_outputs_apart(kw, needle):
+    refused(attention(**kw), INVALID, needle)
+
+
+@pytest.mark.parametrize("kw,needle", [
+    (dict(so=FAKE), "state_out overlaps q"), (dict(so=FAKE + MB), "state_out overlaps k"), (dict(so=FAKE + 2 * MB), "state_out overlaps v"),
+    (dict(so=FAKE + 3 * MB), "state_out overlaps decay"), (dict(so=FAKE + 4 * MB), "state_out overlaps beta"),
+    (dict(so=FAKE + 5 * MB), "state_out overlaps counts"), (dict(counts=FAKE + 10 * MB), "out overlaps counts"),
+])
+def test_delta_step_outputs_apart(kw, needle):
+    refused(step(**kw), INVALID, needle)
+
+
+@pytest.mark.parametrize("kw,needle", [
+    (dict(so=FAKE), "state_out overlaps q"), (dict(so=FAKE + 5 * MB), "state_out overlaps starts"), (dict(starts=FAKE + 10 * MB), "out overlaps starts"),
+    (dict(ws=FAKE), "workspace overlaps q"), (dict(ws=FAKE + 2 * MB + 256), "workspace overlaps v"), (dict(ws=FAKE + 6 * MB), "workspace overlaps state_in"),
+    (dict(ws=FAKE + 8 * MB + 512), "state_out overlaps workspace"), (dict(ws=FAKE + 10 * MB), "out overlaps workspace"),
+    (dict(ws=FAKE + 4 * MB), "workspace overlaps beta"),
+])
+def test_delta_prompt_outputs_apart(kw, needle):
+    refused(prompt(**kw), INVALID, needle)
