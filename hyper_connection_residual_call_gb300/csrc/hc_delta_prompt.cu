@@ -194,23 +194,26 @@ __device__ __forceinline__ bool rows_of(const DeltaPromptParams &p, int s, int &
 // ------------------------------------------------------------------ keys and queries, T, P and the factors
 
 constexpr int kPrepThreads = 256;
-constexpr int kPitch = 68, kTmpPitch = 36;  // floats of a row of a 64 x 64 matrix in shared memory, of a 32 x 32 one
+constexpr int kPitch = 68;    // floats of a row of a 64 x 64 matrix in shared memory
+constexpr int kGates = 4;     // value heads whose gates are added up at once, a warp each
 
 template <int D>
 struct PrepShared {
     uint16_t k[kChunk][D + 8];                     // fp16
     union {                                        // one after the other
         uint16_t q[kChunk][D + 8];
-        uint16_t before[kChunk][D + 8];            // the keys of the chunk before
         alignas(16) float t[kChunk][kPitch];       // T
     };
-    alignas(16) float a[kChunk][kPitch], tmp[32][kTmpPitch];  // M, then A
+    union {
+        uint16_t before[kChunk][D + 8];            // the keys of the chunk before
+        alignas(16) float a[kChunk][kPitch];       // M, then A, and right of its first 32 columns an intermediate product
+    };
     alignas(16) float r[kChunk], s[kChunk];        // the inverse norms, with the powers of two
     struct alignas(16) {
         float gh[kChunk], gl[kChunk], beta[kChunk];  // G in two parts
         int bad;                                   // the first token with an infinity or a NaN
         uint32_t most_t;
-    } gate[kPrepThreads / 32];                     // of eight value heads
+    } gate[kGates];                                // of some value heads
     int bad_key;                                   // the first key with one
 };
 
@@ -293,7 +296,7 @@ __device__ __forceinline__ float row_to_half(uint4 &w, float &undo, bool &odd)
 // A block a chunk and key head, with the key head's value heads one after the other. (A block a value head, which does
 // the keys' part again for each: 217 us for 8192 tokens of 32 heads, two a key head.)
 template <int D>
-__global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_kernel(const DeltaPromptParams p)
+__global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const DeltaPromptParams p)
 {
     using Rec = Record<D>;
     extern __shared__ uint4 smem4[];
@@ -314,12 +317,12 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
     first += (int)chunk * kChunk;
     const int n = min(kChunk, len - (int)chunk * kChunk);
     uint8_t *const key_rec = key_record<D>(p, hk, slot);
-    // the gates are asked for first, by the warps that add them up: a value head a warp, eight at a time
+    // the gates are asked for first, by the warps that add them up: a value head a warp, some at a time
     float decay[2] = {0.f, 0.f}, beta[2] = {0.f, 0.f};
     const auto ask = [&](int g) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const bool in = g < group && 2 * lane + i < n;
+            const bool in = warp < kGates && g < group && 2 * lane + i < n;
             const size_t at = (size_t)(first + 2 * lane + i) * p.Hv + hk * group + g;
             decay[i] = in ? p.decay[at] : 0.f;
             beta[i] = in ? p.beta[at] : 0.f;
@@ -335,6 +338,16 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
     const int piece = tid % kPieces, row0 = tid / kPieces;
     const uint16_t *const k_row = p.k + (size_t)hk * D + piece * 8, *const q_row = p.q + (size_t)hk * D + piece * 8;
     uint8_t *const key_to = key_rec + (piece >> 3) * kTile;
+    if (chunk > 0)                                  // (which is whole)
+#pragma unroll
+        for (int i = 0; i < kChunk / kRowsAtOnce; ++i) {
+            const int r = row0 + i * kRowsAtOnce;
+            uint4 w = *reinterpret_cast<const uint4 *>(k_row + (first - kChunk + r) * p.k_stride);
+            float undo;
+            bool odd;
+            row_to_half<D>(w, undo, odd);
+            *reinterpret_cast<uint4 *>(&sh.before[r][piece * 8]) = w;
+        }
 #pragma unroll
     for (int i = 0; i < 2 * kChunk / kRowsAtOnce; ++i) {
         const bool query = i >= kChunk / kRowsAtOnce;
@@ -362,7 +375,7 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
 
     // the decays' sums in 64 bits, kept as two floats: differences of near ones are right after strong decays too
     const auto gates = [&](int g) {
-        if (g >= group)
+        if (warp >= kGates || g >= group)
             return;
         auto &gate = sh.gate[warp];
         int bad = sh.bad_key;
@@ -414,37 +427,24 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
         }
     };
     gates(warp);
-    // keys with keys (warps 0-3) and queries with keys (4-7), 16 rows a warp, in registers
     const int row = (warp & 3) * 16 + (lane >> 2);
-    float d[8][4];                                 // of rows row and row + 8: columns 8 i + 2 (lane % 4) and the next
-    // (the rows of the chunk before, which is whole, are asked for now)
-    uint4 before[kChunk / kRowsAtOnce];
-    if (chunk > 0)
-#pragma unroll
-        for (int i = 0; i < kChunk / kRowsAtOnce; ++i)
-            before[i] = *reinterpret_cast<const uint4 *>(k_row + (first - kChunk + row0 + i * kRowsAtOnce) * p.k_stride);
-    rows_with_rows<D, 8>(warp >= 4 ? sh.q : sh.k, (warp & 3) * 16, sh.k, 0, d);
-    __syncthreads();
-    if (chunk > 0) {
-        // M: the keys with those of the chunk before
-#pragma unroll
-        for (int i = 0; i < kChunk / kRowsAtOnce; ++i) {
-            float undo;
-            bool odd;
-            row_to_half<D>(before[i], undo, odd);
-            *reinterpret_cast<uint4 *>(&sh.before[row0 + i * kRowsAtOnce][piece * 8]) = before[i];
-        }
-        __syncthreads();
+    if (chunk > 0) {                                // M: the keys with those of the chunk before
         const int col = (warp >> 2) * 32;
         float m[4][4];
         rows_with_rows<D, 4>(sh.k, (warp & 3) * 16, sh.before, col, m);
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float *at = &sh.a[row][col + i * 8 + (lane & 3) * 2];
             *reinterpret_cast<float2 *>(at) = make_float2(m[i][0], m[i][1]);
             *reinterpret_cast<float2 *>(at + 8 * kPitch) = make_float2(m[i][2], m[i][3]);
         }
-        __syncthreads();
+    }
+    // keys with keys (warps 0-3) and queries with keys (4-7), 16 rows a warp, in registers
+    float d[8][4];                                 // of rows row and row + 8: columns 8 i + 2 (lane % 4) and the next
+    rows_with_rows<D, 8>(warp >= 4 ? sh.q : sh.k, (warp & 3) * 16, sh.k, 0, d);
+    __syncthreads();
+    if (chunk > 0) {
         const int i = tid >> 2, x = (tid & 3) * 2;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -459,24 +459,44 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
         if ((u & 15) >> 2 > u >> 8)
             *reinterpret_cast<float4 *>(&sh.t[u >> 4][(u & 15) * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
 
+    // A row of P is by the power of two that its products without decays, which are 1 at most, call for: all value heads'.
+    const int cut = (warp & 3) * 2 + 1;                // the last eight columns that a row of the warp's can see
+    float p_by[2] = {1.f, 1.f}, p_undo[2] = {1.f, 1.f};
+    if (warp >= 4) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t most = 0;
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                if (t <= cut) {
+                    const float2 jr = *reinterpret_cast<const float2 *>(&sh.r[8 * t + 2 * (lane & 3)]);
+                            const float a = fabsf(d[t][2 * half] * jr.x), z = fabsf(d[t][2 * half + 1] * jr.y);
+                    most = max(most, max(8 * t + 2 * (lane & 3) <= row + 8 * half ? __float_as_uint(a) : 0u,
+                                         8 * t + 2 * (lane & 3) + 1 <= row + 8 * half ? __float_as_uint(z) : 0u));
+                }
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+            const Scale sp(__float_as_uint(fabsf(__uint_as_float(most) * sh.s[row + 8 * half])));
+            p_by[half] = sp.by;
+            p_undo[half] = sp.undo;
+        }
+    }
 #pragma unroll 1
     for (int g = 0; g < group; ++g) {
         if (g > 0) {
             __syncthreads();                           // T has been read
-            if ((g & 7) == 0) {
+            if (g % kGates == 0) {
                 ask(g + warp);
                 gates(g + warp);
                 __syncthreads();
             }
         }
         // A, to shared memory, and P, a row by a power of two of its own
-        const auto &gate = sh.gate[g & 7];
+        const auto &gate = sh.gate[g % kGates];
         const int bad = gate.bad;
         uint8_t *const rec = value_record<D>(p, hk * group + g, slot);
         {
-            const int cut = (warp & 3) * 2 + 1;            // the last eight columns that a row of the warp's can see
-            float gh[2], gl[2], by[2], e[8][4];            // of rows row and row + 8, as d
-            uint32_t most[2] = {0, 0};
+            float gh[2], gl[2], by[2];                     // of rows row and row + 8, as d
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int i = row + 8 * half;
@@ -487,47 +507,34 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
             const int above = row + (warp < 4 ? 0 : 1);    // row's first column that is 0, of a row before `bad`
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    e[t][c] = 0.f;
-                if (t > cut)
-                    continue;
+                float e[4] = {0.f, 0.f, 0.f, 0.f};
                 const int j = 8 * t + 2 * (lane & 3);
-                const float2 jh = *reinterpret_cast<const float2 *>(&gate.gh[j]), jl = *reinterpret_cast<const float2 *>(&gate.gl[j]);
-                const float2 jr = *reinterpret_cast<const float2 *>(&sh.r[j]);
+                if (t <= cut) {
+                    const float2 jh = *reinterpret_cast<const float2 *>(&gate.gh[j]), jl = *reinterpret_cast<const float2 *>(&gate.gl[j]);
+                    const float2 jr = *reinterpret_cast<const float2 *>(&sh.r[j]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int half = c >> 1;
-                    // (the exponential's error, |x| 2^-24 of it or so, is at most 2^-25 of 1)
-                    const float g = (gh[half] - (c & 1 ? jh.y : jh.x)) + (gl[half] - (c & 1 ? jl.y : jl.x));
-                    const float x = by[half] * d[t][c] * __expf(g) * (c & 1 ? jr.y : jr.x);
-                    e[t][c] = j + (c & 1) < above + 8 * half && row + 8 * half < bad ? x : 0.f;
-                    most[half] = max(most[half], __float_as_uint(e[t][c]) & 0x7FFFFFFFu);
-                }
-            }
-            if (warp < 4) {
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    if (t <= cut) {
-                        float *const at = &sh.a[row][8 * t + 2 * (lane & 3)];
-                        *reinterpret_cast<float2 *>(at) = make_float2(e[t][0], e[t][1]);
-                        *reinterpret_cast<float2 *>(at + 8 * kPitch) = make_float2(e[t][2], e[t][3]);
+                    for (int c = 0; c < 4; ++c) {
+                        const int half = c >> 1;
+                        // (the exponential's error, |x| 2^-24 of it or so, is at most 2^-25 of 1)
+                        const float g = (gh[half] - (c & 1 ? jh.y : jh.x)) + (gl[half] - (c & 1 ? jl.y : jl.x));
+                        const float x = d[t][c] * (c & 1 ? jr.y : jr.x) * by[half] * __expf(g);
+                        e[c] = j + (c & 1) < above + 8 * half && row + 8 * half < bad ? x : 0.f;
                     }
-            } else {
+                }
+                if (warp >= 4) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    most[half] = max(most[half], __shfl_xor_sync(0xFFFFFFFFu, most[half], 1));
-                    most[half] = max(most[half], __shfl_xor_sync(0xFFFFFFFFu, most[half], 2));
-                    const Scale sp(most[half]);
-                    const int i = row + 8 * half;
-#pragma unroll
-                    for (int t = 0; t < 8; ++t)
-                        *reinterpret_cast<uint32_t *>(rec + Rec::kP + piece_at(i, t) + (lane & 3) * 4) =
-                            pack2_f16(e[t][2 * half] * sp.by, e[t][2 * half + 1] * sp.by);
-                    if ((lane & 3) == 0)
-                        reinterpret_cast<Factors *>(rec + Rec::kFactors)->p[i] = sp.undo;
+                    for (int half = 0; half < 2; ++half)
+                        *reinterpret_cast<uint32_t *>(rec + Rec::kP + piece_at(row + 8 * half, t) + (lane & 3) * 4) =
+                            pack2_f16(e[2 * half] * p_by[half], e[2 * half + 1] * p_by[half]);
+                } else if (t <= cut) {
+                    *reinterpret_cast<float2 *>(&sh.a[row][j]) = make_float2(e[0], e[1]);
+                    *reinterpret_cast<float2 *>(&sh.a[row + 8][j]) = make_float2(e[2], e[3]);
                 }
             }
+            if (warp >= 4 && (lane & 3) == 0)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    reinterpret_cast<Factors *>(rec + Rec::kFactors)->p[row + 8 * half] = p_undo[half];
         }
         __syncthreads();
         // T = (I + A)^-1: the blocks of 16 on the diagonal, a thread a column; the blocks above them are 0
@@ -571,9 +578,9 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
                 }
                 return make_float2(s0, s1);
             };
-            *reinterpret_cast<float2 *>(&sh.tmp[pair * 16 + i][j]) = sixteen(&sh.a[b + 16 + i][b], &sh.t[b][b + j], kPitch);
+            *reinterpret_cast<float2 *>(&sh.a[pair * 16 + i][32 + j]) = sixteen(&sh.a[b + 16 + i][b], &sh.t[b][b + j], kPitch);
             __syncthreads();
-            const float2 s = sixteen(&sh.t[b + 16 + i][b + 16], &sh.tmp[pair * 16][j], kTmpPitch);
+            const float2 s = sixteen(&sh.t[b + 16 + i][b + 16], &sh.a[pair * 16][32 + j], kPitch);
             *reinterpret_cast<float2 *>(&sh.t[b + 16 + i][b + j]) = make_float2(-s.x, -s.y);
             __syncthreads();
         }
@@ -593,14 +600,14 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
 #pragma unroll 2
             for (int k = warp * 4; k < 32; k += 4)
                 four(s, &sh.a[32 + lane][k], &sh.t[k][warp * 4], kPitch);
-            *reinterpret_cast<float4 *>(&sh.tmp[lane][warp * 4]) = s;
+            *reinterpret_cast<float4 *>(&sh.a[lane][32 + warp * 4]) = s;
             __syncthreads();
             // T22 times that, a warp four rows: T22's columns after the rows' are 0
             const int i = tid >> 3, j = (tid & 7) * 4;
             s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
             for (int k = 0; k <= warp * 4; k += 4)
-                four(s, &sh.t[32 + i][32 + k], &sh.tmp[k][j], kTmpPitch);
+                four(s, &sh.t[32 + i][32 + k], &sh.a[k][32 + j], kPitch);
             *reinterpret_cast<float4 *>(&sh.t[32 + i][j]) = make_float4(-s.x, -s.y, -s.z, -s.w);
             __syncthreads();
         }
@@ -624,9 +631,9 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) hc_delta_prep_k
                 }
             most = __reduce_max_sync(0xFFFFFFFFu, most);
             if (lane == 0)
-                atomicMax(&sh.gate[g & 7].most_t, most);
+                atomicMax(&sh.gate[g % kGates].most_t, most);
             __syncthreads();
-            const Scale st(sh.gate[g & 7].most_t);
+            const Scale st(sh.gate[g % kGates].most_t);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -709,6 +716,18 @@ __device__ __forceinline__ float most_of(float most, uint64_t v)
     return most3(most, a, z);
 }
 
+// The n-th longest of up to 32 sequences, so that long walks begin first: 192 walks of up to 24 chunks MEASURE2.
+__device__ __forceinline__ int longest(const DeltaPromptParams &p, int n)
+{
+    const int lane = threadIdx.x & 31, len = lane < p.S ? p.starts[lane + 1] - p.starts[lane] : -1;
+    int before = 0;
+    for (int i = 0; i < p.S; ++i) {
+        const int other = __shfl_sync(0xFFFFFFFFu, len, i);
+        before += other > len || (other == len && i < lane);
+    }
+    return __ffs(__ballot_sync(0xFFFFFFFFu, lane < p.S && before == n)) - 1;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid_constant__ DeltaPromptParams p, const __grid_constant__ CUtensorMap map_v)
 {
@@ -763,6 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
     bool with_values = true, with_outputs = true;
     long record = 0;
     if (p.seg == 0) {
+        if (p.S <= 32)
+            seq = longest(p, seq);
         if (!rows_of(p, seq, first, len))
             len = 0;
         record = record_of(first, seq, 0);
