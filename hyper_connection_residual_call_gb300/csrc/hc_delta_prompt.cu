@@ -41,11 +41,11 @@
 //
 // Few long sequences leave SMs idle and are cut into segments (segment_chunks): three launches instead of the second.
 //
-// 8192 tokens of 32 heads of 128 take 427 us: 143 the first kernel, which issues 1.7 of 4 instructions a cycle (barriers,
-// shared memory and the serial inversions of 16 rows), twice 140 the walks of a third of the chunks each, 14 the states
-// between; a chunk's turn is some 6300 cycles, two chains of a product, its way to registers, a column's largest element,
-// the split and its way back. 24 prompts of up to 1500 tokens, 8 heads of 64: 172 us, 95 and 80 of them; its 192 walks
-// are one a SM, so that 40 begin late. The bytes are 31 and 13 us' worth.
+// 8192 tokens of 32 heads of 128 take 419 us: 138 the first kernel, which issues 1.75 of 4 instructions a cycle (barriers,
+// shared memory and the serial inversions of 16 rows), twice 140 the walks of a third of the chunks each, 13 the states
+// between (less where one kernel's end and the next's begin overlap); a chunk's turn is some 6300 cycles, two chains of a
+// product, its way to registers, a column's largest element, the split and its way back. 24 prompts of up to 1500 tokens, 8
+// heads of 64: 165 us, 100 and 70 of them. The bytes are 31 and 13 us' worth.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -95,7 +95,8 @@ __device__ __forceinline__ long record_of(int start, int seq, int chunk) { retur
 // but for the first, for its outputs. So n segments take the time of two, with 2 n - 3 walks a head at once: n is what
 // the SMs hold, a walk a SM, and at least three, of eight chunks at least. One sequence, without and with segments: 8192
 // tokens of 32 heads of 128 (three segments) 571 and 471 us, of 8 heads 455 and 228; 65536 tokens of 4 heads 3290 and
-// 672; 2048 tokens of 8 heads 125 and 113; but 1100 tokens of 4 heads 81 and 96, hence the 24 chunks.
+// 672; 2048 tokens of 8 heads 125 and 113; but 1100 tokens of 4 heads 81 and 96, hence the 24 chunks. (Before the first
+// and the joining kernel had their present form; by now the second of each pair are 419, 161, 536 and 101.)
 constexpr int kSms = 152, kLeastSegment = 8, kLeastCut = 24;
 inline int segment_chunks(int N, int S, int Hv)
 {
@@ -294,7 +295,8 @@ __device__ __forceinline__ float row_to_half(uint4 &w, float &undo, bool &odd)
 }
 
 // A block a chunk and key head, with the key head's value heads one after the other. (A block a value head, which does
-// the keys' part again for each: 217 us for 8192 tokens of 32 heads, two a key head.)
+// the keys' part again for each, took a quarter longer. Four blocks a SM, in 64 registers, for D = 128, too: 8192 tokens of 32
+// heads in 419 us, with three, in 80, 426; but 2048 of 8 heads 101 and 94, where the blocks are few.)
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const DeltaPromptParams p)
 {
@@ -716,7 +718,8 @@ __device__ __forceinline__ float most_of(float most, uint64_t v)
     return most3(most, a, z);
 }
 
-// The n-th longest of up to 32 sequences, so that long walks begin first: 192 walks of up to 24 chunks MEASURE2.
+// The n-th longest of up to 32 sequences, so that long walks begin first: 24 prompts of up to 1500 tokens, 8 heads
+// of 64, 192 walks on 152 SMs, take 165 us; in their own order 177.
 __device__ __forceinline__ int longest(const DeltaPromptParams &p, int n)
 {
     const int lane = threadIdx.x & 31, len = lane < p.S ? p.starts[lane + 1] - p.starts[lane] : -1;

@@ -354,3 +354,71 @@ def test_addresses_on_16_bytes(d):
     got = B.hc_delta_step(*map(S, args), out=S(torch.zeros_like(args[2])), state_out=S(torch.zeros_like(state)))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert B.device_status() == B.TS_OK
+
+
+def far_apart(t, stride):
+    """``t``'s rows ``stride`` elements apart."""
+    flat = torch.empty((t.shape[0] - 1) * stride + t[0].numel(), dtype=t.dtype, device=t.device)
+    view = flat.as_strided(t.shape, (stride, *t.stride()[1:]))
+    return view.copy_(t)
+
+
+def test_offsets_past_32_bits():
+    """Rows so far apart that elements' offsets do not fit 32 bits: the same bits as side by side."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    n, far = 5, (1 << 30) + 8  # up to 8.6 GB
+    starts, positions = packed([3, 2])
+    q, k = r(n, 4, 64).bfloat16(), r(n, 2, 64).bfloat16()
+    w, table, decay, beta, state = r(64).bfloat16(), B.rope_table(64, 64, 10000.0), -r(n, 2).abs(), torch.sigmoid(r(n, 2)), r(2, 2, 64, 64)
+    q_far, k_far = far_apart(q, far), far_apart(k, far)
+    for got, want in ((B.hc_qk_norm_rope(q_far, k_far, positions, table, w, w), B.hc_qk_norm_rope(q, k, positions, table, w, w)),
+                      (B.hc_prompt_attention(q_far, k_far, k, starts), B.hc_prompt_attention(q, k, k, starts)),
+                      (B.hc_prompt_attention(q, k, k_far, starts), B.hc_prompt_attention(q, k, k, starts))):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    del q_far
+    out_far = far_apart(torch.zeros_like(q), far)
+    B.hc_qk_norm_rope(q, None, positions, table, w, q_out=out_far)
+    assert torch.equal(out_far, B.hc_qk_norm_rope(q, None, positions, table, w)[0])
+    del out_far
+    for args in ((k_far, k, k), (k, k_far, k), (k, k, k_far)):
+        apart = lambda: dict(state_out=torch.zeros_like(state))  # noqa: E731
+        for got, want in ((B.hc_delta_prompt(*args, decay, beta, state, starts, **apart()), B.hc_delta_prompt(k, k, k, decay, beta, state, starts, **apart())),
+                          (B.hc_delta_step(*(x.unsqueeze(0) for x in (*args, decay, beta)), state[:1].contiguous(), state_out=torch.zeros_like(state[:1])),
+                           B.hc_delta_step(*(x.unsqueeze(0) for x in (k, k, k, decay, beta)), state[:1].contiguous(), state_out=torch.zeros_like(state[:1])))):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    del k_far, args
+    x, chosen = r(n, 3000), torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    for got, want in zip(B.hc_logprobs(far_apart(x, (1 << 30) + 4), chosen, top=5), B.hc_logprobs(x, chosen, top=5)):
+        assert torch.equal(got, want)
+    assert B.device_status() == B.TS_OK
+
+
+def test_many_sequences_and_heads():
+    """The most sequences, most of them empty, and many heads."""
+    s = 65535
+    lens = torch.zeros(s, dtype=torch.int32)
+    lens[[0, 17, 300, 40000, s - 1]] = torch.tensor([3, 70, 1, 130, 2], dtype=torch.int32)
+    starts = torch.cat([torch.zeros(1, dtype=torch.int32), lens.cumsum(0).int()]).cuda()
+    few, _ = packed([3, 70, 1, 130, 2])
+    g = torch.Generator(device="cuda").manual_seed(8)
+    n = int(lens.sum())
+    q, k, v = (torch.randn(n, h, 64, generator=g, device="cuda").bfloat16() for h in (2, 1, 1))
+    for got, want in zip(B.hc_prompt_attention(q, k, v, starts), B.hc_prompt_attention(q, k, v, few)):
+        assert torch.equal(got, want)
+    decay, beta = -torch.rand(n, 1, generator=g, device="cuda"), torch.rand(n, 1, generator=g, device="cuda")
+    state = torch.zeros(s, 1, 64, 64, device="cuda")
+    some = torch.zeros(5, 1, 64, 64, device="cuda")
+    got, want = B.hc_delta_prompt(k, k, v, decay, beta, state, starts)[0], B.hc_delta_prompt(k, k, v, decay, beta, some, few)[0]
+    assert torch.equal(got, want)
+    assert torch.equal(state[[0, 17, 300, 40000, s - 1]], some)
+    state[[0, 17, 300, 40000, s - 1]] = 0
+    assert not state.any()
+    # 1024 heads
+    q, k = torch.randn(9, 1024, 64, generator=g, device="cuda").bfloat16(), torch.randn(9, 1024, 64, generator=g, device="cuda").bfloat16()
+    at, _ = packed([9])
+    wide = B.hc_prompt_attention(q, k, k, at)
+    for h in (0, 511, 1023):
+        one = B.hc_prompt_attention(*(x[:, h:h + 1].contiguous() for x in (q, k, k)), at)
+        assert torch.equal(wide[0][:, h], one[0][:, 0]) and torch.equal(wide[1][:, h], one[1][:, 0])
+    assert B.device_status() == B.TS_OK
