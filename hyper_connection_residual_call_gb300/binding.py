@@ -436,9 +436,16 @@ def _check(st: int) -> None:
 
 # ------------------------------------------------------------- torch layer
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported by the first call (an import statement a call is 0.2 us, and a call here comes to it some eight times)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(stream) -> int:
@@ -1173,7 +1180,7 @@ def _together(stream, *tensors) -> int:
 def _out(t, name, dtype, shape, like, stream):
     """``t``, or a new tensor where it is None."""
     if t is None:
-        t = _torch().empty(shape, dtype=dtype, device=like.device)
+        t = _torch().empty_like(like) if like.dtype is dtype and like.shape == shape else _torch().empty(shape, dtype=dtype, device=like.device)
         if stream is not None:
             t.record_stream(stream)
         return t
@@ -1189,7 +1196,7 @@ def hc_qk_norm_rope(q, k, positions, table, q_weight, k_weight=None, *, eps: flo
     torch = _torch()
     n, hq, d, sq = _rows(q, "q")
     if q_out is None:
-        q_out, so = _made(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream), hq * d
+        q_out, so = _made(torch.empty_like(q), stream), hq * d  # (dense, whatever q's strides)
     else:
         no, ho, do, so = _rows(q_out, "q_out")
         if (no, ho, do) != (n, hq, d):
@@ -1200,7 +1207,7 @@ def hc_qk_norm_rope(q, k, positions, table, q_weight, k_weight=None, *, eps: flo
         if nk != n or dk != d:
             raise HCError(TS_ERR_INVALID_ARG, f"k has shape {tuple(k.shape)}, q has {tuple(q.shape)}")
         if k_out is None:
-            k_out, sko = _made(torch.empty(k.shape, dtype=torch.bfloat16, device=q.device), stream), hk * d
+            k_out, sko = _made(torch.empty_like(k), stream), hk * d
         else:
             no, ho, do, sko = _rows(k_out, "k_out")
             if (no, ho, do) != (n, hk, d):
@@ -1282,7 +1289,7 @@ def hc_delta_step(q, k, v, decay, beta, state, *, counts=None, scale: Optional[f
     state_out = state if state_out is None else state_out
     op = _is(state_out, "state_out", torch.float32, shape)
     cp = None if counts is None else _is(counts, "counts", torch.int32, (b,))
-    out = _out(out, "out", torch.bfloat16, v.shape, q, stream)
+    out = _out(out, "out", torch.bfloat16, v.shape, v, stream)
     handle = _together(stream, q, k, v, decay, beta, state, state_out, counts, out)
     st = (_lib or library()).ts_hc_delta_step(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, decay.data_ptr(), beta.data_ptr(), cp,
                                               ip, op, out.data_ptr(), b, t, hk, hv, d, d ** -0.5 if scale is None else scale,
@@ -1311,7 +1318,7 @@ def hc_delta_prompt(q, k, v, decay, beta, state, starts, *, scale: Optional[floa
     ip = _is(state, "state", torch.float32, shape)
     state_out = state if state_out is None else state_out
     op = _is(state_out, "state_out", torch.float32, shape)
-    out = _out(out, "out", torch.bfloat16, v.shape, q, stream)
+    out = _out(out, "out", torch.bfloat16, v.shape, v, stream)
     if ws is None:
         ws = _made(delta_prompt_workspace(n, s, hk, hv, d, q.device), stream)
     handle = _together(stream, q, k, v, decay, beta, state, state_out, starts, out, ws)
