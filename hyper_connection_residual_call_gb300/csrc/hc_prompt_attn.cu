@@ -24,13 +24,14 @@
 // warp 10 looks through the last tiles' values, warp 11 finds the next block. Every wait is
 // bounded; the first that runs out records TS_ERR_TIMEOUT and ends the others.
 //
-// One prompt of 16384 tokens, 32 heads of 128 over 8, takes 1.54 ms, 1.43 PFLOP/s, 0.83 of what a library product holds
-// under the power cap: a block's pair of tiles takes some 3370 cycles, 2048 of them products, the rest what the
-// exponentials and the products of one stream wait for the other's. Eight prompts of 256 to 2048 tokens take 126 us,
-// of which 81 are tiles: the others are the blocks' first tiles, their last (700 cycles) and the results' way out (3700
-// cycles, 2000 of them the stores, a row a lane). 48 prompts of up to 200 tokens, 16 heads of 64 over 2: 18.7 us.
-// Two threads a row, 16 softmax warps: 1600, 131 and 21.8. Two places for the queries, one less for the
-// rest: 1566 and 125.
+// One prompt of 16384 tokens, 32 heads of 128 over 8, takes 1.50 ms, 1.47 PFLOP/s, 0.86 of what a library product holds
+// under the power cap: a block's pair of tiles takes some 3280 cycles, 2048 of them products, the rest what the
+// exponentials and the products of one stream wait for the other's. Eight prompts of 256 to 2048 tokens take 125 us,
+// of which 79 are tiles: the others are the blocks' first tiles, their last products (700 cycles) and the results' way
+// out (3700 cycles, 2000 of them the stores, a row a lane). 48 prompts of up to 200 tokens, 16 heads of 64 over 2: 18.7 us.
+// Before the last tiles' keys were masked by 32, and those that none of a warp's rows sees left out, it was 1.54 ms and 126
+// us, and to that compare: two threads a row, 16 softmax warps, 1.60 and 131; two places for the queries, one less for
+// the rest, 1.57 and 125.
 #include <algorithm>
 
 #include "hc_attn.cuh"
@@ -328,15 +329,16 @@ hc_prompt_attn_kernel(const __grid_constant__ PromptAttnParams p, const __grid_c
                 tmem_wait_ld32(x[1]);
                 tmem_wait_ld32(x[2]);
                 tmem_wait_ld32(x[3]);
-                if (j * kKeys + kKeys - 1 > first) {  // not every row sees all keys
-                    const int sees = t - j * kKeys;   // the last that this one sees
+                const bool cut = j * kKeys + kKeys - 1 > first;  // not every row sees all keys
+                const int sees = t - j * kKeys;                  // the last that this one sees
+                if (cut)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
+                        if (!__all_sync(0xFFFFFFFFu, sees >= i * 32 + 31))
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (i * 32 + c > sees)
-                                x[i][c] = 0xFF800000u;
-                }
+                            for (int c = 0; c < 32; ++c)
+                                if (i * 32 + c > sees)
+                                    x[i][c] = 0xFF800000u;
                 float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -368,6 +370,11 @@ hc_prompt_attn_kernel(const __grid_constant__ PromptAttnParams p, const __grid_c
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t w[16];
+                    if (cut && !__any_sync(0xFFFFFFFFu, sees >= i * 32)) {  // nobody sees these
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            w[c] = 0;
+                    } else
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         float a, z;
