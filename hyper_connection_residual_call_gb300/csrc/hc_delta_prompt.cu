@@ -41,11 +41,12 @@
 //
 // Few long sequences leave SMs idle and are cut into segments (segment_chunks): three launches instead of the second.
 //
-// 8192 tokens of 32 heads of 128 take 419 us: 138 the first kernel, which issues 1.75 of 4 instructions a cycle (barriers,
-// shared memory and the serial inversions of 16 rows), twice 140 the walks of a third of the chunks each, 13 the states
-// between (less where one kernel's end and the next's begin overlap); a chunk's turn is some 6300 cycles, two chains of a
-// product, its way to registers, a column's largest element, the split and its way back. 24 prompts of up to 1500 tokens, 8
-// heads of 64: 165 us, 100 and 70 of them. The bytes are 31 and 13 us' worth.
+// 8192 tokens of 32 heads of 128 take 394 us: the first kernel, 138 in one piece, which issues 1.75 of 4 instructions a cycle
+// (barriers, shared memory and the serial inversions of 16 rows), a third of it beside the first walks; twice 140 the walks of
+// a third of the chunks each; 13 the states between (less where one kernel's end and the next's begin overlap). A
+// chunk's turn is some 6300 cycles, two chains of a product, its way to registers, a column's largest element, the split
+// and its way back. 24 prompts of up to 1500 tokens, 8 heads of 64: 165 us, 100 and 70 of them. The bytes are 31 and
+// 13 us' worth.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -96,7 +97,7 @@ __device__ __forceinline__ long record_of(int start, int seq, int chunk) { retur
 // the SMs hold, a walk a SM, and at least three, of eight chunks at least. One sequence, without and with segments: 8192
 // tokens of 32 heads of 128 (three segments) 571 and 471 us, of 8 heads 455 and 228; 65536 tokens of 4 heads 3290 and
 // 672; 2048 tokens of 8 heads 125 and 113; but 1100 tokens of 4 heads 81 and 96, hence the 24 chunks. (Before the first
-// and the joining kernel had their present form; by now the second of each pair are 419, 161, 536 and 101.)
+// and the joining kernel had their present form; by now the second of each pair are 394, 161, 536 and 101.)
 constexpr int kSms = 152, kLeastSegment = 8, kLeastCut = 24;
 inline int segment_chunks(int N, int S, int Hv)
 {
@@ -107,6 +108,17 @@ inline int segment_chunks(int N, int S, int Hv)
     const long each = std::max<long>((chunks + S * n - 1) / (S * n), kLeastSegment);
     return chunks > S * std::max<long>(2 * each, kLeastCut) ? (int)each : 0;
 }
+// Whether the last segments' part of the first kernel runs beside the first walks, which do not need it, on the SMs that
+// these leave idle: where that is a quarter of them, and there is enough of it. 8192 tokens of 32 heads of 128, 96
+// walks, 419 us without and 394 with, but 2048 tokens 130 and 134.
+constexpr int kLeastApart = 40;               // chunks a sequence
+inline bool apart(int N, int S, int Hv, int seg)
+{
+    const long chunks = ((long)N + kChunk - 1) / kChunk, n = (chunks + (long)S * seg - 1) / ((long)S * seg);
+    return (long)S * Hv * (2 * n - 3) <= kSms * 3 / 4 && chunks >= (long)S * kLeastApart;
+}
+// Whose part of the first kernel a launch does.
+enum { kAllSegments, kFirstSegments, kLastSegments };
 // As records: by the sequence's first token, and the sequence, and the segment.
 __host__ __device__ inline long segment_slots(int N, int S, int seg) { return (long)N / kChunk / seg + S; }
 __device__ __forceinline__ long segment_of(const DeltaPromptParams &p, int seq)
@@ -304,7 +316,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const De
     extern __shared__ uint4 smem4[];
     auto &sh = *reinterpret_cast<PrepShared<D> *>(smem4);
     pdl_launch_dependents();
-    pdl_wait();
+    if (p.part != kLastSegments || blockIdx.x == 0)  // (those run beside the first walks, whose start they came after; the
+        pdl_wait();                                  // next kernel, which begins when all blocks have ended, is after the walks)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long slot = blockIdx.x / p.Hk;
     const int hk = (int)(blockIdx.x - slot * p.Hk), group = p.Hv / p.Hk;
@@ -316,6 +329,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const De
     const long chunk = slot - record_of(first, seq, 0);
     if (chunk < 0 || chunk * kChunk >= len)
         return;
+    if (p.part != kAllSegments) {
+        const long last = (((long)len + kChunk - 1) / kChunk - 1) / p.seg;
+        if ((last > 0 && chunk / p.seg == last) != (p.part == kLastSegments))
+            return;
+    }
     first += (int)chunk * kChunk;
     const int n = min(kChunk, len - (int)chunk * kChunk);
     uint8_t *const key_rec = key_record<D>(p, hk, slot);
@@ -775,8 +793,12 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    pdl_launch_dependents();
+    // What is launched to run beside the walks does not wait itself, and relies on what they have waited for.
+    if (p.part == kAllSegments)
+        pdl_launch_dependents();
     pdl_wait();
+    if (p.part != kAllSegments)
+        pdl_launch_dependents();
     const int h = blockIdx.x % p.Hv, hk = h / (p.Hv / p.Hk);
     int seq = blockIdx.x / p.Hv, first, len;
     // where the state comes from and goes to; of a walk without values from the identity: its column's 1
@@ -1300,7 +1322,13 @@ cudaError_t launch(DeltaPromptParams p, cudaStream_t stream)
     CUtensorMap map_v{};
     if (!tc_make_map_heads(&map_v, p.v, p.N, p.Hv, D, p.v_stride, 1, kChunk, true))
         return cudaErrorInvalidValue;
-    e = launch_pdl(hc_delta_prep_kernel<D>, dim3((unsigned)(record_slots(p.N, p.S) * p.Hk)), dim3(kPrepThreads), sizeof(PrepShared<D>), true, stream, p);
+    p.seg = segment_chunks(p.N, p.S, p.Hv);
+    const auto prep = [&](int part) {
+        p.part = part;
+        return launch_pdl(hc_delta_prep_kernel<D>, dim3((unsigned)(record_slots(p.N, p.S) * p.Hk)), dim3(kPrepThreads), sizeof(PrepShared<D>), true,
+                          stream, p);
+    };
+    e = prep(p.seg > 0 && apart(p.N, p.S, p.Hv, p.seg) ? kFirstSegments : kAllSegments);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t lc{};
@@ -1312,7 +1340,6 @@ cudaError_t launch(DeltaPromptParams p, cudaStream_t stream)
     lc.stream = stream;
     lc.blockDim = dim3(kThreads);
     lc.dynamicSmemBytes = Plan<D>::kTotal;
-    p.seg = segment_chunks(p.N, p.S, p.Hv);
     if (p.seg == 0) {
         lc.gridDim = dim3((unsigned)(p.S * p.Hv));
         return cudaLaunchKernelEx(&lc, hc_delta_scan_kernel<D>, p, map_v);
@@ -1321,6 +1348,10 @@ cudaError_t launch(DeltaPromptParams p, cudaStream_t stream)
     p.ends = reinterpret_cast<float *>(p.work + records_bytes(p.N, p.S, p.Hk, p.Hv, D));
     lc.gridDim = dim3((unsigned)(2 * slots * p.Hv));
     e = cudaLaunchKernelEx(&lc, hc_delta_scan_kernel<D>, p, map_v);
+    if (e == cudaSuccess && p.part != kAllSegments) {
+        e = prep(kLastSegments);
+        p.part = kAllSegments;
+    }
     if (e == cudaSuccess)
         e = launch_pdl(hc_delta_join_kernel<D>, dim3((unsigned)(p.S * p.Hv * (D / kJoinColumns))), dim3(kJoinThreads), 0, true, stream, p);
     if (e != cudaSuccess)

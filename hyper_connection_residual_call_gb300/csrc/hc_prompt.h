@@ -51,8 +51,9 @@ struct DeltaPromptParams {
     int N, S, Hk, Hv, D;
     float scale, norm_eps;
     unsigned *status;
-    // the launch's own: chunks of a segment (0: none), whether it is the walk for the outputs, the segments' ends
-    int seg, again;
+    // the launch's own: chunks of a segment (0: none), which segments' part, whether it is the walk for the outputs, the
+    // segments' ends
+    int seg, part, again;
     float *ends;
 };
 

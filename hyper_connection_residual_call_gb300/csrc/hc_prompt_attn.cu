@@ -385,7 +385,7 @@ hc_prompt_attn_kernel(const __grid_constant__ PromptAttnParams p, const __grid_c
                         w[c] = pack2_bf16(a, z);
                     }
                     tmem_st16_async(ts + 16 * i, w);
-                    if (i == 1) {  // the product can begin with the first 64 keys
+                    if (i == 1) {  // the product can begin with the first 64 keys (with 32: 1524 us for 1499, with 96: 1510)
                         tmem_wait_st();
                         tc_fence_before();
                         mbar_arrive(&sh.p_half[s]);

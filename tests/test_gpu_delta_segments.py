@@ -132,3 +132,48 @@ def test_segments_starts_out_of_range(first, last):
     assert B.device_status() == B.TS_ERR_INVALID_ARG
     assert (out[:50] == 7).all() and (out[5110:] == 7).all() and torch.equal(out[50:5110], want[50:5110])
     assert torch.equal(state[0], args[5][0]) and torch.equal(state[2], args[5][2]) and torch.equal(state[1], want_state[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hk,hv,lens", [(2, 4, [2600]), (1, 1, [5000, 2700, 300]), (4, 8, [2561])])
+def test_segments_whose_last_are_prepared_beside_the_walks(d, hk, hv, lens):
+    """From 40 chunks a sequence on and with SMs left idle; the same bits call after call, without a pause, on two streams."""
+    args, at = prompt_case(lens, hk, hv, d, sum(lens), low=0.1)
+    out, state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    check_prompt(args, at, out, state)
+    ws = [B.delta_prompt_workspace(sum(lens), len(lens), hk, hv, d) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    many = [B.hc_delta_prompt(*args, state_out=torch.zeros_like(args[5]), ws=ws[i % 2], stream=streams[i % 2]) for i in range(6)]
+    torch.cuda.synchronize()
+    for o, s in many:
+        assert torch.equal(o, out) and torch.equal(s, state)
+    # other inputs in between, in the same workspace: nothing of one call is left for the next
+    other, _ = prompt_case(lens, hk, hv, d, 77, low=0.1)
+    first = B.hc_delta_prompt(*other, state_out=torch.zeros_like(args[5]), ws=ws[0])
+    again = B.hc_delta_prompt(*args, state_out=torch.zeros_like(args[5]), ws=ws[0])
+    third = B.hc_delta_prompt(*other, state_out=torch.zeros_like(args[5]), ws=ws[0])
+    assert torch.equal(again[0], out) and torch.equal(again[1], state)
+    assert torch.equal(first[0], third[0]) and torch.equal(first[1], third[1])
+    fine()
+
+
+def test_segments_prepared_beside_the_walks_in_a_graph():
+    """Inputs that the kernels just before have written, replay after replay."""
+    args, at = prompt_case([3000], 2, 4, 128, 5, low=0.1)
+    k, v = args[1].clone(), args[2].clone()
+    out, state = torch.empty(3000, 4, 128, device="cuda").bfloat16(), torch.empty_like(args[5])
+    ws = B.delta_prompt_workspace(3000, 1, 2, 4, 128)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for scale in (1.0, 0.5):
+            torch.mul(v, scale, out=args[2].copy_(v))
+            args[1].copy_(k)
+            B.hc_delta_prompt(*args, out=out, state_out=state, ws=ws)
+    for _ in range(3):
+        out.zero_(), state.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want, want_state = B.hc_delta_prompt(args[0], k, v * 0.5, *args[3:], state_out=torch.empty_like(state))
+        assert torch.equal(out, want) and torch.equal(state, want_state)
+    fine()
