@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kThreads, 4) hc_qk_norm_kernel(const NormRopeP
             const bool is_q = h < p.q_heads;
             const uint4 *w = reinterpret_cast<const uint4 *>(is_q ? np.qw : np.kw);
             float wa[8], wb[8];
-            unpack8(__ldg(w + v0), wa);
-            unpack8(__ldg(w + v1), wb);
+            unpack8(w[v0], wa);  // (not as read-only data: that could be loaded before pdl_wait())
+            unpack8(w[v1], wb);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 a[j] *= inv * wa[j];
