@@ -20,9 +20,8 @@ Tolerances, from the number formats (unit roundoffs: u16 = 2^-8 of bf16, u32 = 2
               (2^-22 + D u32) M a token (keys of norm 1), U = T R by that and two more 2^-22 of up to sqrt(64) terms
               of size M times what T does to them (2 or so), U's 64 terms' sums by 64 u32; the state takes that
               on, and its own errors: (D + 16) u32 M a token as above, over a chunk's 64, bound them. For the outputs
-              the state and U are rounded to 11 bits, P too: 3 2^-12 of terms of size M, of which up to 64 add up as
-              a root of a sum of squares at most (P's rows are within 1): 8 of them
-                |out err| <= u16 |out| + scale (24 2^-12 / 8 + (T + 64) (D + 16) u32) M
+              the state and U are rounded to 11 bits, P too: three roundings of 2^-12, of sums within M
+                |out err| <= u16 |out| + scale (3 2^-12 + (T + 64) (D + 16) u32) M
   log probabilities  e^d is off by 2 |d| u32 (the product with log2 e) and 2^-22 (the function) of itself, sums
               run over V/1024 elements a thread and then 40 joins: log Z is off by at most
               r = (V/1024 + 100) u32 (the |d| weighted with p add up to less than the entropy, at most 21), so
