@@ -39,9 +39,10 @@ constexpr int kHold = 16;                    // elements of a chunk that a threa
 constexpr int kGroups = kThreads / 4;        // of four threads each
 constexpr int kMaxTop = 32;
 constexpr int kKeep = 4096;                  // keys kept; a chunk's threshold leaves at most kMaxTop * 4 * kHold of it
-constexpr int kRank = 64;                    // keys that are ranked without a threshold first
+constexpr int kRank = kThreads / 4;          // keys that are ranked without a threshold first
 constexpr int kEach = (kKeep + kThreads - 1) / kThreads;  // kept keys of a thread
 constexpr int kFew = 1184;                   // keys that a compaction leaves, at most kMaxTop * 4 * kEach
+static_assert(kGroups % 8 == 0, "quarters in pairs");
 static_assert(kMaxTop * 4 * kHold <= kKeep / 2, "a chunk's keys");
 static_assert(kMaxTop * 4 * kEach <= kFew, "what a compaction leaves");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -110,7 +111,7 @@ __device__ __forceinline__ Part join_warp(Part a)
 struct Shared {
     uint64_t keep[kKeep];
     uint64_t few[kFew];
-    uint64_t group[kGroups];
+    alignas(16) uint64_t group[kGroups];
     uint64_t top[kMaxTop];   // this block's, best first; a block of a cluster reads the others'
     uint64_t all[8 * kMaxTop];
     uint64_t threshold;
@@ -134,15 +135,18 @@ __device__ __forceinline__ uint64_t threshold_of(uint64_t best, int n, Shared &s
     if (tid == 0)
         sh.threshold = 0;
     sync();
-    if (tid < kGroups) {
-        const uint64_t mine = sh.group[tid];
-        int larger = 0;
-#pragma unroll 8
-        for (int i = 0; i < kGroups; ++i)
-            larger += sh.group[i] > mine;
-        if (larger == n - 1 && mine != 0)  // keys are distinct
-            sh.threshold = mine;
+    // a group's four threads have a quarter of the others each
+    constexpr int kQuarter = kGroups / 4;
+    int larger = 0;
+#pragma unroll 5
+    for (int i = 0; i < kQuarter; i += 2) {
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&sh.group[(tid & 3) * kQuarter + i]);
+        larger += (two.x > best) + (two.y > best);
     }
+    larger += __shfl_xor_sync(0xFFFFFFFFu, larger, 1);
+    larger += __shfl_xor_sync(0xFFFFFFFFu, larger, 2);
+    if ((tid & 3) == 0 && larger == n - 1 && best != 0)  // keys are distinct
+        sh.threshold = best;
     sync();
     return sh.threshold;
 }
@@ -175,13 +179,16 @@ __device__ __forceinline__ void compact(int n, Shared &sh)
     } else {
         sync();
     }
-    for (int i = tid; i < left; i += kThreads) {
-        const uint64_t mine = from[i];
+    for (int i0 = 0; i0 < left; i0 += kThreads / 4) {  // four threads a key, with a quarter of the others each
+        const int i = i0 + (tid >> 2);
+        const uint64_t mine = i < left ? from[i] : ~0ull;
         int larger = 0;
 #pragma unroll 4
-        for (int j = 0; j < left; ++j)
+        for (int j = tid & 3; j < left; j += 4)
             larger += from[j] > mine;
-        if (larger < n)
+        larger += __shfl_xor_sync(0xFFFFFFFFu, larger, 1);
+        larger += __shfl_xor_sync(0xFFFFFFFFu, larger, 2);
+        if ((tid & 3) == 0 && i < left && larger < n)
             sh.top[larger] = mine;
     }
     sync();
