@@ -298,7 +298,65 @@ __device__ __forceinline__ void unpack(uint4 w, float (&x)[kBf16 ? 8 : 4])
     }
 }
 
-// The first chunk's threshold, or any chunk's after it: keeps what reaches it among the thread's elements that
+// Keeps the thread's elements that `pass` names, by their keys (0: not after all). Few threads have any, and few of
+// their fours of elements.
+template <typename R, typename Pass, typename Key>
+__device__ __forceinline__ void keep_four(const float (&x)[R::kVecs][R::kPer], const Pass &pass, const Key &key, Shared &sh)
+{
+#pragma unroll
+    for (int f = 0; f < R::kVecs * R::kPer / 4; ++f) {
+        const int i = f * 4 / R::kPer, c0 = f * 4 % R::kPer;
+        const float *const e = &x[i][c0];
+        if (!pass(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]))))
+            continue;
+        uint32_t over = (pass(e[0]) ? 1u : 0u) | (pass(e[1]) ? 2u : 0u) | (pass(e[2]) ? 4u : 0u) | (pass(e[3]) ? 8u : 0u);
+#pragma unroll 1
+        for (; over; over &= over - 1) {
+            const int c = __ffs(over) - 1;
+            const uint64_t k = key(c < 2 ? (c == 0 ? e[0] : e[1]) : c == 2 ? e[2] : e[3], i, c0 + c);
+            if (k != 0) {
+                const int place = atomicAdd(&sh.kept, 1);
+                if (place < kKeep)
+                    sh.keep[place] = k;
+            }
+        }
+    }
+}
+
+// The first chunk's threshold: keeps what reaches it among the thread's elements that `in` names (all, where it is
+// `inside`), whose largest is `top`. Returns it (0: fewer than n groups have an element).
+template <typename R, typename In>
+__device__ __forceinline__ uint64_t keep_first(const float (&x)[R::kVecs][R::kPer], float top, int first, bool inside, int n, const In &in, Shared &sh)
+{
+    const auto key = [&](float y, int i, int c) { return key_of(y, (uint32_t)(first + i * kThreads * R::kPer + c)); };
+    uint64_t best = 0;
+    if (__all_sync(0xFFFFFFFFu, inside)) {  // the first of the largest
+        int at = 0;
+#pragma unroll
+        for (int i = R::kVecs - 1; i >= 0; --i)
+#pragma unroll
+            for (int c = R::kPer - 1; c >= 0; --c)
+                at = x[i][c] == top ? i * kThreads * R::kPer + c : at;
+        best = key_of(top, (uint32_t)(first + at));
+    } else {
+#pragma unroll
+        for (int i = 0; i < R::kVecs; ++i)
+#pragma unroll
+            for (int c = 0; c < R::kPer; ++c)
+                if (in(i, c))
+                    best = max(best, key(x[i][c], i, c));
+    }
+    const uint64_t least = threshold_of(best, n, sh);
+    const float limit = least != 0 ? key_value(least) : -INFINITY;
+    if (best != 0 && best >= least)
+        keep_four<R>(x, [&](float y) { return y >= limit; }, [&](float y, int i, int c) {
+            const uint64_t k = key(y, i, c);
+            return k >= least && in(i, c) ? k : 0;
+        }, sh);
+    return least;
+}
+
+// Any chunk's threshold, for rows that are read again: keeps what reaches it among the thread's elements that
 // `in` names. Returns it (0: fewer than n groups have an element).
 template <typename R, typename In>
 __device__ __forceinline__ uint64_t keep_best(const float (&x)[R::kVecs][R::kPer], int first, int n, const In &in, Shared &sh)
@@ -429,9 +487,10 @@ __global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobPar
         for (int ch = 0; ch < r.chunks; ++ch, ++taken) {
             const int v = r.v0 + ch * R::kStep + tid, stage = (int)(taken % kStages);
             const uint32_t phase = (taken / kStages) & 1;
-            if (kTop && (ch == 2 || ch == 5)) {
-                // The threads' maxima so far give a higher threshold (its elements come before this chunk's, so that
-                // of equal ones none is missed). 20 of 128001: some 100 are kept in all, 320 with the first alone.
+            if (kTop && ch == 3 && n > 2) {
+                // The threads' maxima so far give a higher threshold (its elements come before this chunk's, so that of
+                // equal ones none is missed). 20 of 128001: some 140 are kept in all, 320 with the first alone; 221 us for
+                // 2048 rows, with two such thresholds 222, without 229; for one alternative 188, 193, 182.
                 const uint64_t least = threshold_of(key_of(a.m, tid), n, sh);
                 limit = fmaxf(limit, key_value(least));
             }
@@ -501,29 +560,13 @@ __global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobPar
                 continue;
             const int first = v * kPer - r.lead;
             if (ch == 0) {
-                const uint64_t least = keep_best<R>(x, first, n, [&](int i, int c) { return r.exists(v + i * kThreads, c); }, sh);
+                const uint64_t least = keep_first<R>(x, top, first, v >= r.in0 && v + (kVecs - 1) * kThreads < r.in1, n,
+                                                     [&](int i, int c) { return r.exists(v + i * kThreads, c); }, sh);
                 limit = least != 0 ? key_value(least) : INFINITY;  // (0: then there is no second chunk)
             } else if (top > limit) {
-                // few have any: their elements' bits first, so that what follows runs once for each
-                uint32_t over = 0;
-#pragma unroll
-                for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c)
-                        over |= x[i][c] > limit ? 1u << (i * kPer + c) : 0u;
-                while (over) {
-                    const int bit = __ffs(over) - 1;
-                    over &= over - 1;
-                    float y = x[0][0];
-#pragma unroll
-                    for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-                        for (int c = 0; c < kPer; ++c)
-                            y = bit == i * kPer + c ? x[i][c] : y;
-                    const int place = atomicAdd(&sh.kept, 1);
-                    if (place < kKeep)
-                        sh.keep[place] = key_of(y, (uint32_t)(first + bit / kPer * kThreads * kPer + bit % kPer));
-                }
+                keep_four<R>(x, [&](float y) { return y > limit; }, [&](float y, int i, int c) {
+                    return key_of(y, (uint32_t)(first + i * kThreads * kPer + c));
+                }, sh);
             }
         }
         a = join_warp(a);
