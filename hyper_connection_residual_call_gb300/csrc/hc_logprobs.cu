@@ -18,8 +18,8 @@
 // hold an element that reaches one, which bounds what is kept for any logits.
 //
 // 4099 rows of 65537 bf16, eight tokens each, take 107 us for 0.54 GB, 0.74 of the measured copy rate; 2048 rows of
-// 128001 fp32 with the twenty best 229 us for 1.05 GB, 0.67. Both issue 2.3 to 2.7 of 4 instructions a cycle from two
-// blocks a SM; a block that ranks a row leaves the SM to the other. One row of 32768: 8.5 us, a launch, 16 KB a
+// 128001 fp32 with the twenty best 210 us for 1.05 GB, 0.74, without them 149. Both issue 2.3 to 2.7 of 4 instructions a cycle from two
+// blocks a SM; a block that ranks a row leaves the SM to the other. One row of 32768: 7.8 us, a launch, 16 KB a
 // CTA, a ranking and a join through the cluster. (Loads to registers, without copies ahead: 218 and 355 us.)
 #include <algorithm>
 #include <type_traits>
