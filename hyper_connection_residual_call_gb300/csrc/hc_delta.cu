@@ -13,8 +13,10 @@
 // in a lane and then two shuffles, and nothing is exchanged between warps. The output needs
 // no second pass over the state: S^T q = (e^g S)^T q + (k . q) u.
 //
-// 64 sequences x 4 tokens (2.5 on average) x 32 heads of 128: 54 us for 0.27 GB, 0.74 of the
-// measured copy rate; 16 columns a warp 57, 8 columns 76. One token of one sequence: 3.4 us.
+// 64 sequences x 4 tokens (2.5 on average) x 32 heads of 128: 48.8 us for 0.27 GB, 0.82 of the
+// measured copy rate. With states loaded and stored as what stays in the caches, 52 (the loads or the stores alone as
+// passing, 53 and 52); with a head's four warps in one block, 54, and one token of one sequence 3.7 for 2.8 us; 16 columns
+// a warp 57, 8 columns 76. Ten or twelve warps a SM, in 168 registers, spill: 52.5 for 52.
 #include <cuda_bf16.h>
 
 #include "hc_prompt.h"
@@ -37,30 +39,31 @@ __device__ __forceinline__ float warp_sum(float v)
 }
 
 template <int D>
-__global__ void __launch_bounds__(D / kCols * 32) hc_delta_step_kernel(const DeltaStepParams p)
+__global__ void __launch_bounds__(32) hc_delta_step_kernel(const DeltaStepParams p)
 {
     constexpr int kRows = D / kGroups;           // a lane's
     constexpr int kPer = D / 32;                 // elements of q and k that a lane loads
-    __shared__ alignas(16) float qk[D / kCols][2][D];  // by warp
+    __shared__ alignas(16) float qk[2][D];
     pdl_launch_dependents();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane / kLanes;
-    const int b = blockIdx.x / p.Hv, h = blockIdx.x - b * p.Hv, hk = h / (p.Hv / p.Hk);
-    const int col = warp * kCols + (lane % kLanes) * 4;
+    constexpr int kParts = D / kCols;
+    const int lane = threadIdx.x, group = lane / kLanes;
+    const int bh = blockIdx.x / kParts, b = bh / p.Hv, h = bh - b * p.Hv, hk = h / (p.Hv / p.Hk);
+    const int col = (blockIdx.x % kParts) * kCols + (lane % kLanes) * 4;
     // Lane group g has rows 16 i + 4 g .. + 3, so that its reads of q and k are 16 bytes wide and the groups' side by side.
-    const size_t at = ((size_t)blockIdx.x * D + 4 * group) * D + col;
+    const size_t at = ((size_t)bh * D + 4 * group) * D + col;
     const auto row = [](int i) { return (i >> 2) * (kGroups * 4) + (i & 3); };
     float4 s[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-        s[i] = *reinterpret_cast<const float4 *>(p.state_in + at + (size_t)row(i) * D);
+        s[i] = __ldcs(reinterpret_cast<const float4 *>(p.state_in + at + (size_t)row(i) * D));
     int n = p.counts ? p.counts[b] : p.T;
     if (n < 0 || n > p.T) {
         if (p.status && threadIdx.x == 0 && h == 0)
             atomicExch(p.status, kStatusInvalidArg);
         n = min(max(n, 0), p.T);
     }
-    float *const ks = qk[warp][0], *const qs = qk[warp][1];
+    float *const ks = qk[0], *const qs = qk[1];
     for (int t = 0; t < n; ++t) {
         const size_t tok = (size_t)b * p.T + t;
         const uint16_t *kp = p.k + tok * p.k_stride + (size_t)hk * D + lane * kPer, *qp = p.q + tok * p.q_stride + (size_t)hk * D + lane * kPer;
@@ -146,16 +149,16 @@ __global__ void __launch_bounds__(D / kCols * 32) hc_delta_step_kernel(const Del
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-        *reinterpret_cast<float4 *>(p.state_out + at + (size_t)row(i) * D) = s[i];
+        __stcs(reinterpret_cast<float4 *>(p.state_out + at + (size_t)row(i) * D), s[i]);
 }
 
 }  // namespace
 
 cudaError_t launch_delta_step(const DeltaStepParams &p, const LaunchCfg &, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)(p.B * p.Hv));
-    return p.D == 64 ? launch_pdl(hc_delta_step_kernel<64>, grid, dim3(64 / kCols * 32), 0, true, stream, p)
-                     : launch_pdl(hc_delta_step_kernel<128>, grid, dim3(128 / kCols * 32), 0, true, stream, p);
+    const dim3 grid((unsigned)p.B * p.Hv * (p.D / kCols));
+    return p.D == 64 ? launch_pdl(hc_delta_step_kernel<64>, grid, dim3(32), 0, true, stream, p)
+                     : launch_pdl(hc_delta_step_kernel<128>, grid, dim3(32), 0, true, stream, p);
 }
 
 }  // namespace tshc
