@@ -8,10 +8,11 @@
 // its own would read and write them again. Sums and products are fp32, and the result is
 // rounded to bf16 once.
 //
-// What bounds it is its bytes: 16381 tokens x 40 heads x 128, half of each turned, take 56 us for
-// 0.34 GB, 0.89 of the measured copy rate, with two heads' loads in flight a thread and four
-// blocks a SM; four heads', in 94 registers and two blocks, took 63 to 66. One token of 24 heads takes
-// 2.2 us: a launch, and a chain of two loads and a sum. (GPU times of calls replayed back to back in a
+// What bounds it is its bytes: 16381 tokens x 40 heads x 128, half of each turned, take 55 us for
+// 0.34 GB, 0.91 of the measured copy rate, with two heads' loads in flight a thread and eight
+// blocks a SM of 128 threads (four of 256: 56; loads as of passing data: 63); four heads' loads, in 94
+// registers and half of the threads, took 63 to 66. One token of 24 heads takes
+// 2.1 us: a launch, and a chain of two loads and a sum. (GPU times of calls replayed back to back in a
 // CUDA graph, here and below.)
 #include <cuda_bf16.h>
 
@@ -23,7 +24,7 @@ namespace tshc {
 namespace {
 
 constexpr unsigned kStatusInvalidArg = 1u;  // TS_ERR_INVALID_ARG of ts_hc.h
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
@@ -57,7 +58,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
 // every head that it walks. The sum of squares goes over the kUnits lanes. D = 16 kUnits,
 // rot a multiple of 16.
 template <int kUnits, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 4) hc_qk_norm_kernel(const NormRopeParams np, int lanes)
+__global__ void __launch_bounds__(kThreads, 8) hc_qk_norm_kernel(const NormRopeParams np, int lanes)
 {
     constexpr int D = kUnits * 16;
     pdl_launch_dependents();
@@ -206,7 +207,7 @@ cudaError_t launch_units(const NormRopeParams &p, const LaunchCfg &cfg, cudaLaun
     // head a thread, for latency.
     const int heads = p.r.q_heads + p.r.k_heads;
     const long one = (long)p.r.N * kUnits * heads;
-    const int walk = one > (long)cfg.sm_count * kThreads * 16 ? 8 : 1;
+    const int walk = one > (long)cfg.sm_count * 4096 ? 8 : 1;
     const int lanes = (heads + walk - 1) / walk;
     lc.gridDim = dim3((unsigned)(((unsigned long)p.r.N * kUnits * lanes + kThreads - 1) / kThreads));
     return cudaLaunchKernelEx(&lc, p.r.interleaved ? hc_qk_norm_kernel<kUnits, true> : hc_qk_norm_kernel<kUnits, false>, p, lanes);
