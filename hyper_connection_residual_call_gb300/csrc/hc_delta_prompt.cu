@@ -53,6 +53,7 @@
 #include <algorithm>
 
 #include "hc_attn.cuh"
+#include "hc_delta_plan.h"
 #include "hc_prompt.h"
 #include "hc_tc.h"
 #include "umma.cuh"
@@ -62,7 +63,6 @@ namespace tshc {
 namespace {
 
 constexpr unsigned kStatusInvalidArg = 1u;   // TS_ERR_INVALID_ARG of ts_hc.h
-constexpr int kChunk = 64;
 constexpr int kTile = kChunk * 128;           // bytes of a 64 x 64 fp16 tile: 64 rows of 128 bytes, swizzled
 struct Factors {
     float c[kChunk];          // -e^(G_i) r_i, r with the key's power of two
@@ -90,37 +90,8 @@ constexpr float kNaN = __builtin_nanf("");
 __host__ __device__ inline long record_slots(int N, int S) { return (long)N / kChunk + S; }
 __device__ __forceinline__ long record_of(int start, int seq, int chunk) { return (long)(start / kChunk) + seq + chunk; }
 
-// Chunks of a segment, where sequences are cut into segments that are walked side by side; 0: they are not.
-// A segment after the first is walked for what it makes of a state, S -> F S + B (F from the identity and no
-// values, B from a state of zeros), then the segments' states are known one after the other, and it is walked again,
-// but for the first, for its outputs. So n segments take the time of two, with 2 n - 3 walks a head at once: n is what
-// the SMs hold, a walk a SM, and at least three, of eight chunks at least. One sequence, without and with segments: 8192
-// tokens of 32 heads of 128 (three segments) 571 and 471 us, of 8 heads 455 and 228; 65536 tokens of 4 heads 3290 and
-// 672; 2048 tokens of 8 heads 125 and 113; but 1100 tokens of 4 heads 81 and 96, hence the 24 chunks. (Before the first
-// and the joining kernel had their present form; by now the second of each pair are 394, 161, 536 and 101.)
-constexpr int kSms = 152, kLeastSegment = 8, kLeastCut = 24;
-inline int segment_chunks(int N, int S, int Hv)
-{
-    const long walks = (long)S * Hv, chunks = ((long)N + kChunk - 1) / kChunk;
-    const long n = walks > 0 ? (kSms / walks + 3) / 2 : 0;
-    if (n < 3)
-        return 0;
-    const long each = std::max<long>((chunks + S * n - 1) / (S * n), kLeastSegment);
-    return chunks > S * std::max<long>(2 * each, kLeastCut) ? (int)each : 0;
-}
-// Whether the last segments' part of the first kernel runs beside the first walks, which do not need it, on the SMs that
-// these leave idle: where that is a quarter of them, and there is enough of it. 8192 tokens of 32 heads of 128, 96
-// walks, 419 us without and 394 with, but 2048 tokens 130 and 134.
-constexpr int kLeastApart = 40;               // chunks a sequence
-inline bool apart(int N, int S, int Hv, int seg)
-{
-    const long chunks = ((long)N + kChunk - 1) / kChunk, n = (chunks + (long)S * seg - 1) / ((long)S * seg);
-    return (long)S * Hv * (2 * n - 3) <= kSms * 3 / 4 && chunks >= (long)S * kLeastApart;
-}
 // Whose part of the first kernel a launch does.
 enum { kAllSegments, kFirstSegments, kLastSegments };
-// As records: by the sequence's first token, and the sequence, and the segment.
-__host__ __device__ inline long segment_slots(int N, int S, int seg) { return (long)N / kChunk / seg + S; }
 __device__ __forceinline__ long segment_of(const DeltaPromptParams &p, int seq)
 {
     return (long)(min(max(p.starts[seq], 0), p.N) / kChunk / p.seg) + seq;  // (one that is out of range keeps its state)
@@ -824,17 +795,17 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
             len = 0;
         const long at = slot - segment_of(p, seq), last = max(((long)len + kChunk - 1) / kChunk - 1, 0l) / p.seg;
         const auto end_of = [&](long slot, bool values) { return p.ends + (((values ? 0 : slots) + slot) * p.Hv + h) * D * D; };
-        const bool mine = at >= 0 && at <= last && (p.again ? at > 0 : at == 0 ? with_values : at < last);
-        if (mine) {
-            from = at == 0 ? p.state_in + ((size_t)seq * p.Hv + h) * D * D : p.again ? end_of(slot - 1, true) : nullptr;
-            to = at == last ? p.state_out + ((size_t)seq * p.Hv + h) * D * D : end_of(slot, with_values);
+        const Walk w = walk_of(at, last, with_values, p.again);
+        if (w.mine) {
+            from = w.from == kState ? p.state_in + ((size_t)seq * p.Hv + h) * D * D : w.from == kEndBefore ? end_of(slot - 1, true) : nullptr;
+            to = w.to == kState ? p.state_out + ((size_t)seq * p.Hv + h) * D * D : w.to == kEnd ? end_of(slot, with_values) : nullptr;
             if (len == 0 && p.state_out == p.state_in)
                 to = nullptr;
-            with_outputs = p.again || at == 0;
+            with_outputs = w.outputs;
         }
         record = record_of(first, seq, 0) + at * p.seg;
         first += (int)(at * p.seg) * kChunk;
-        len = mine ? (int)min((long)len - at * p.seg * kChunk, (long)p.seg * kChunk) : 0;
+        len = w.mine ? (int)min((long)len - at * p.seg * kChunk, (long)p.seg * kChunk) : 0;
     }
     const int chunks = (len + kChunk - 1) / kChunk;
     const int col = tid & 127;                      // of the threads that have one
