@@ -114,7 +114,7 @@ struct Shared {
     alignas(16) uint64_t group[kGroups];
     uint64_t top[kMaxTop];   // this block's, best first; a block of a cluster reads the others'
     uint64_t all[8 * kMaxTop];
-    uint64_t threshold;
+    uint64_t threshold[2];
     Part part[2][kWarps];    // by rows in turn
     Part whole;
     uint64_t full[4], empty[4];
@@ -124,8 +124,9 @@ struct Shared {
 // A barrier of the threads that take the elements.
 __device__ __forceinline__ void sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
-// The n-th largest of the groups' largest keys (0 if fewer than n groups have one).
-__device__ __forceinline__ uint64_t threshold_of(uint64_t best, int n, Shared &sh)
+// The n-th largest of the groups' largest keys (0 if fewer than n groups have one). Threads may still be reading it in
+// `word` when others go on, up to the next barrier: the next call before one takes the other word.
+__device__ __forceinline__ uint64_t threshold_of(uint64_t best, int n, Shared &sh, int word = 0)
 {
     best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, 1));
     best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, 2));
@@ -133,7 +134,7 @@ __device__ __forceinline__ uint64_t threshold_of(uint64_t best, int n, Shared &s
     if ((tid & 3) == 0)
         sh.group[tid >> 2] = best;
     if (tid == 0)
-        sh.threshold = 0;
+        sh.threshold[word] = 0;
     sync();
     // a group's four threads have a quarter of the others each
     constexpr int kQuarter = kGroups / 4;
@@ -146,9 +147,9 @@ __device__ __forceinline__ uint64_t threshold_of(uint64_t best, int n, Shared &s
     larger += __shfl_xor_sync(0xFFFFFFFFu, larger, 1);
     larger += __shfl_xor_sync(0xFFFFFFFFu, larger, 2);
     if ((tid & 3) == 0 && larger == n - 1 && best != 0)  // keys are distinct
-        sh.threshold = best;
+        sh.threshold[word] = best;
     sync();
-    return sh.threshold;
+    return sh.threshold[word];
 }
 
 // Replaces the kept keys by the n largest of them, best first (0 where there are fewer).
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobPar
                 // The threads' maxima so far give a higher threshold (its elements come before this chunk's, so that of
                 // equal ones none is missed). 20 of 128001: some 140 are kept in all, 320 with the first alone; 221 us for
                 // 2048 rows, with two such thresholds 222, without 229; for one alternative 188, 193, 182.
-                const uint64_t least = threshold_of(key_of(a.m, tid), n, sh);
+                const uint64_t least = threshold_of(key_of(a.m, tid), n, sh, 1);  // (no barrier since chunk 0's)
                 limit = fmaxf(limit, key_value(least));
             }
             if (!wait_bounded(&sh.full[stage], phase)) {

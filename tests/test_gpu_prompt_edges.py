@@ -5,7 +5,7 @@ import torch
 
 from gpu_common import require_gpu
 from hyper_connection_residual_call_gb300 import binding as B
-from test_gpu_prompt import check_prompt, fine, prompt_case
+from test_gpu_prompt import check_logprobs, check_prompt, fine, gen, logit_rows, prompt_case
 
 pytestmark = pytest.mark.gpu
 
@@ -38,4 +38,41 @@ def test_segments_on_a_busy_gpu(hk, hv, d, lens):
     torch.cuda.synchronize()
     for o, s in zip(outs, states):
         assert torch.equal(o, out) and torch.equal(s, state)
+    fine()
+
+
+# ------------------------------------------------------------------ log probabilities
+
+@pytest.mark.parametrize("kind", ["plain", "ruled out", "lowest", "equal", "rising", "falling", "few values", "one", "large"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("top", [3, 5, 32])
+def test_logprobs_second_threshold(kind, dtype, top):
+    """Rows of seven chunks a CTA, two blocks a SM: the alternatives' second threshold, from the fourth chunk on, in any
+    order of a row's elements; and the same bits call after call."""
+    n, v = 330, 50001
+    x = logit_rows(kind, n, v, 31, dtype)
+    tokens = torch.randint(0, v, (n, 1), generator=gen(v), device="cuda", dtype=torch.int32)
+    got = B.hc_logprobs(x, tokens, top=top)
+    for rows in (slice(0, 2), slice(303, 306), slice(n - 1, n)):
+        check_logprobs(x[rows], tokens[rows], top, [t[rows] for t in got])
+    for _ in range(4):
+        for a, z in zip(B.hc_logprobs(x, tokens, top=top), got):
+            assert torch.equal(a, z)
+    # the other rows against one sort (stable: of equal ones the lowest index)
+    order = (x.float() + 0.0).sort(dim=-1, descending=True, stable=True).indices[:, :top]
+    assert torch.equal(got[2].long(), order)
+    fine()
+
+
+@pytest.mark.parametrize("kind", ["plain", "ruled out", "lowest", "equal", "rising", "falling", "few values", "one"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,v", [(20, 20003), (60, 20003), (10, 131072), (38, 100003)])
+def test_logprobs_rows_of_two_and_four_ctas(kind, dtype, n, v):
+    """Clusters of two and of four CTAs, some with a second threshold in each CTA's part."""
+    x = logit_rows(kind, n, v, 32, dtype)
+    tokens = torch.randint(0, v, (n, 2), generator=gen(v), device="cuda", dtype=torch.int32)
+    got = B.hc_logprobs(x, tokens, top=20)
+    check_logprobs(x[-3:], tokens[-3:], 20, [t[-3:] for t in got])
+    order = (x.float() + 0.0).sort(dim=-1, descending=True, stable=True).indices[:, :20]
+    assert torch.equal(got[2].long(), order)
     fine()
