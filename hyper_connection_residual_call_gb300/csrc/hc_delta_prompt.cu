@@ -97,6 +97,8 @@ __device__ __forceinline__ long segment_of(const DeltaPromptParams &p, int seq)
     return (long)(min(max(p.starts[seq], 0), p.N) / kChunk / p.seg) + seq;  // (one that is out of range keeps its state)
 }
 
+constexpr size_t kBegunBytes = 16;            // a word behind the ends
+
 size_t records_bytes(int N, int S, int Hk, int Hv, int D)
 {
     const size_t slots = record_slots(N, S);
@@ -176,6 +178,17 @@ __device__ __forceinline__ bool rows_of(const DeltaPromptParams &p, int s, int &
 }
 
 // ------------------------------------------------------------------ keys and queries, T, P and the factors
+
+__device__ __forceinline__ uint32_t load_acquire(const unsigned *at)
+{
+    uint32_t x;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ void store_release(unsigned *at, uint32_t x)
+{
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(at), "r"(x) : "memory");
+}
 
 constexpr int kPrepThreads = 256;
 constexpr int kPitch = 68;    // floats of a row of a 64 x 64 matrix in shared memory
@@ -287,9 +300,15 @@ __global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const De
     extern __shared__ uint4 smem4[];
     auto &sh = *reinterpret_cast<PrepShared<D> *>(smem4);
     pdl_launch_dependents();
-    if (p.part != kLastSegments || blockIdx.x == 0)  // (those run beside the first walks, whose start they came after; the
-        pdl_wait();                                  // next kernel, which begins when all blocks have ended, is after the walks)
+    // The last segments' blocks run beside the first walks and do not wait for their end, but for one, after which the next
+    // kernel is after the walks. What was written before the call they may read because a walk's thread that had waited for it
+    // released `begun` before these blocks could be launched, and each of their threads acquires it; one that does not find
+    // it waits for the walks as any kernel does.
+    if (p.part != kLastSegments || blockIdx.x == 0 || load_acquire(p.begun) != 1u)
+        pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (p.part == kFirstSegments && blockIdx.x == 0 && tid == 0)
+        *p.begun = 0;
     const long slot = blockIdx.x / p.Hk;
     const int hk = (int)(blockIdx.x - slot * p.Hk), group = p.Hv / p.Hk;
     // the sequence whose records this one is among: the last that begins at or before it
@@ -764,12 +783,18 @@ __global__ void __launch_bounds__(kThreads, 1) hc_delta_scan_kernel(const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    // What is launched to run beside the walks does not wait itself, and relies on what they have waited for.
+    // What is launched to run beside the walks relies on what they have waited for (hc_delta_prep_kernel).
     if (p.part == kAllSegments)
         pdl_launch_dependents();
     pdl_wait();
-    if (p.part != kAllSegments)
+    if (p.part != kAllSegments) {
+        if (blockIdx.x == 0) {
+            if (tid == 0)
+                store_release(p.begun, 1u);
+            __syncthreads();
+        }
         pdl_launch_dependents();
+    }
     const int h = blockIdx.x % p.Hv, hk = h / (p.Hv / p.Hk);
     int seq = blockIdx.x / p.Hv, first, len;
     // where the state comes from and goes to; of a walk without values from the identity: its column's 1
@@ -1294,6 +1319,9 @@ cudaError_t launch(DeltaPromptParams p, cudaStream_t stream)
     if (!tc_make_map_heads(&map_v, p.v, p.N, p.Hv, D, p.v_stride, 1, kChunk, true))
         return cudaErrorInvalidValue;
     p.seg = segment_chunks(p.N, p.S, p.Hv);
+    const long slots = p.seg > 0 ? segment_slots(p.N, p.S, p.seg) : 0;
+    p.ends = reinterpret_cast<float *>(p.work + records_bytes(p.N, p.S, p.Hk, p.Hv, D));
+    p.begun = reinterpret_cast<unsigned *>(p.ends + 2 * slots * p.Hv * D * D);
     const auto prep = [&](int part) {
         p.part = part;
         return launch_pdl(hc_delta_prep_kernel<D>, dim3((unsigned)(record_slots(p.N, p.S) * p.Hk)), dim3(kPrepThreads), sizeof(PrepShared<D>), true,
@@ -1315,8 +1343,6 @@ cudaError_t launch(DeltaPromptParams p, cudaStream_t stream)
         lc.gridDim = dim3((unsigned)(p.S * p.Hv));
         return cudaLaunchKernelEx(&lc, hc_delta_scan_kernel<D>, p, map_v);
     }
-    const long slots = segment_slots(p.N, p.S, p.seg);
-    p.ends = reinterpret_cast<float *>(p.work + records_bytes(p.N, p.S, p.Hk, p.Hv, D));
     lc.gridDim = dim3((unsigned)(2 * slots * p.Hv));
     e = cudaLaunchKernelEx(&lc, hc_delta_scan_kernel<D>, p, map_v);
     if (e == cudaSuccess && p.part != kAllSegments) {
@@ -1337,7 +1363,7 @@ cudaError_t launch(DeltaPromptParams p, cudaStream_t stream)
 size_t delta_prompt_bytes(int N, int S, int Hk, int Hv, int D)
 {
     const int seg = segment_chunks(N, S, Hv);
-    return records_bytes(N, S, Hk, Hv, D) + (seg ? sizeof(float) * 2 * (size_t)segment_slots(N, S, seg) * Hv * D * D : 0);
+    return records_bytes(N, S, Hk, Hv, D) + (seg ? sizeof(float) * 2 * (size_t)segment_slots(N, S, seg) * Hv * D * D + kBegunBytes : 0);
 }
 
 cudaError_t launch_delta_prompt(const DeltaPromptParams &p, const LaunchCfg &, cudaStream_t stream)

@@ -55,6 +55,7 @@ struct DeltaPromptParams {
     // segments' ends
     int seg, part, again;
     float *ends;
+    unsigned *begun;            // 1 once the first walks have waited for what came before the call
 };
 
 struct LogprobParams {

@@ -41,6 +41,47 @@ def test_segments_on_a_busy_gpu(hk, hv, d, lens):
     fine()
 
 
+@pytest.mark.parametrize("hk,hv,d,n", [(1, 1, 64, 2700), (4, 8, 128, 5000)])
+def test_segments_read_what_was_just_written(hk, hv, d, n):
+    """All inputs are written by the kernels just before, other ones each time, in a graph and without; the workspace
+    holds all ones before, as it may."""
+    cases = [prompt_case([n], hk, hv, d, 41 + i, low=0.1)[0] for i in range(3)]
+    want = [B.hc_delta_prompt(*c, state_out=torch.empty_like(c[5])) for c in cases]
+    args = [torch.zeros_like(x) for x in cases[0]]
+    ws = B.delta_prompt_workspace(n, 1, hk, hv, d)
+    ws.view(torch.int32)[:] = 1
+    out, state = torch.zeros_like(want[0][0]), torch.zeros_like(args[5])
+    kept = [(torch.zeros_like(out), torch.zeros_like(state)) for _ in cases]
+
+    def all_cases():
+        for c, (o, s) in zip(cases, kept):
+            for mine, x in zip(args, c):
+                mine.copy_(x)
+            B.hc_delta_prompt(*args, out=out, state_out=state, ws=ws)
+            for mine in args:  # nobody reads them any more
+                mine.zero_()
+            o.copy_(out)
+            s.copy_(state)
+
+    def check():
+        torch.cuda.synchronize()
+        for (o, s), (wo, w) in zip(kept, want):
+            assert torch.equal(o, wo) and torch.equal(s, w)
+            o.zero_(), s.zero_()
+
+    for _ in range(5):
+        all_cases()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        all_cases()
+    for _ in range(5):
+        ws.view(torch.int32)[:] = 1
+        graph.replay()
+    check()
+    fine()
+
+
 # ------------------------------------------------------------------ log probabilities
 
 @pytest.mark.parametrize("kind", ["plain", "ruled out", "lowest", "equal", "rising", "falling", "few values", "one", "large"])
