@@ -44,6 +44,21 @@ inline bool apart(int N, int S, int Hv, int seg)
 // segment: no two sequences' overlap.
 __host__ __device__ inline long segment_slots(int N, int S, int seg) { return (long)N / kChunk / seg + S; }
 
+// The most of them that any call of up to N tokens and S sequences has, so that a workspace for the largest call serves
+// every smaller one: by s sequences, N / 64 / seg is at most N / 64 / kLeastSegment and at most their s n segments.
+inline long most_segment_slots(int N, int S, int Hv)
+{
+    const long chunks = ((long)N + kChunk - 1) / kChunk;
+    long most = 0;
+    for (long s = 1; s <= S && chunks > s * kLeastCut; ++s) {
+        const long n = (kSms / (s * Hv) + 3) / 2;
+        if (n < 3)
+            break;
+        most = std::max(most, std::min((long)N / kChunk / kLeastSegment, s * n) + s);
+    }
+    return most;
+}
+
 // Where a segment's walk takes its state from and leaves it.
 enum Place {
     kNowhere,

@@ -1362,8 +1362,8 @@ cudaError_t launch(DeltaPromptParams p, cudaStream_t stream)
 
 size_t delta_prompt_bytes(int N, int S, int Hk, int Hv, int D)
 {
-    const int seg = segment_chunks(N, S, Hv);
-    return records_bytes(N, S, Hk, Hv, D) + (seg ? sizeof(float) * 2 * (size_t)segment_slots(N, S, seg) * Hv * D * D + kBegunBytes : 0);
+    const long slots = most_segment_slots(N, S, Hv);
+    return records_bytes(N, S, Hk, Hv, D) + (slots > 0 ? sizeof(float) * 2 * (size_t)slots * Hv * D * D + kBegunBytes : 0);
 }
 
 cudaError_t launch_delta_prompt(const DeltaPromptParams &p, const LaunchCfg &, cudaStream_t stream)

@@ -705,8 +705,9 @@ ts_status ts_hc_delta_step(const void *q, long q_stride, const void *k, long k_s
  *   out        bf16 [N][v_heads][D]; rows of no sequence are not written
  *   workspace  >= ts_hc_delta_prompt_workspace_bytes(...) bytes, 256-byte aligned (for 64 tokens of D = 128 some 48 KB a
  *              key head and 25 KB a value head, and 128 KB a value head and segment where a few long sequences
- *              are walked in segments side by side); it need not be initialised and must not be shared by calls that can
- *              run at the same time
+ *              are walked in segments side by side); one for the largest N and S serves every call of no more tokens
+ *              and sequences (of the same heads and D); it need not be initialised and must not be shared by calls that
+ *              can run at the same time
  * The state is held in fp32, and what goes into it by the tensor cores has 22 bits of significand (the sum of two
  * fp16, scaled by its column's largest), and fp32 sums; what goes to the outputs alone has 11. An infinity or a NaN in
  * a token's inputs leaves NaNs in the outputs from that token on that it reaches and in the state, and does not reach

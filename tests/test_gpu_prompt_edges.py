@@ -82,6 +82,16 @@ def test_segments_read_what_was_just_written(hk, hv, d, n):
     fine()
 
 
+def test_one_workspace_serves_smaller_calls():
+    ws = B.delta_prompt_workspace(6000, 6, 1, 2, 64)
+    for lens in ([6000], [3000, 2900], [100, 5, 1, 0, 9, 300], [1], [2000, 1, 1, 1, 1, 1]):
+        args, at = prompt_case(lens, 1, 2, 64, 51, low=0.1)
+        want, want_state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+        out, state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]), ws=ws)
+        assert torch.equal(out, want) and torch.equal(state, want_state)
+    fine()
+
+
 # ------------------------------------------------------------------ log probabilities
 
 @pytest.mark.parametrize("kind", ["plain", "ruled out", "lowest", "equal", "rising", "falling", "few values", "one", "large"])
