@@ -36,6 +36,7 @@
 
 #include "hc_attn.cuh"
 #include "hc_prompt.h"
+#include "hc_prompt_plan.h"
 #include "hc_tc.h"
 #include "umma.cuh"
 
@@ -50,7 +51,6 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;  // and the planning
 constexpr int kSoftRegs = 208, kOtherRegs = 80;  // 256 * 208 + 128 * 80 = 63488 <= 384 * 168, what the launch has
 constexpr float kGrow = 8.f;                  // log2: how far a row's maximum may grow over its reference
 constexpr uint32_t kTmemCols = 512;           // S of two streams, O of two streams
-constexpr int kRound = 256;                   // sequences whose blocks are taken in turn
 
 template <int D>
 struct Plan {
@@ -109,13 +109,10 @@ __device__ __forceinline__ int blocks_of(const PromptAttnParams &p, int s)
 {
     if (s >= p.S)
         return 0;
-    const int lo = p.starts[s], hi = p.starts[s + 1];
-    if (lo < 0 || hi < lo || hi > p.N) {
-        if (p.status)
-            atomicExch(p.status, kStatusInvalidArg);
-        return 0;
-    }
-    return (hi - lo + 2 * p.TB - 1) / (2 * p.TB);
+    const int n = blocks_of_rows(p.starts[s], p.starts[s + 1], p.N, 2 * p.TB);
+    if (n < 0 && p.status)
+        atomicExch(p.status, kStatusInvalidArg);
+    return max(n, 0);
 }
 
 // The planning warp's work: which block is the n-th. Blocks of up to 256 sequences are taken in turn, each
@@ -134,7 +131,7 @@ struct Rounds {
 #pragma unroll
             for (int i = 0; i < kRound / 32; ++i)
                 mine += blocks_of(p, r * kRound + lane * (kRound / 32) + i);
-            sum += __reduce_add_sync(0xFFFFFFFFu, mine);
+            sum = add_blocks(sum, __reduce_add_sync(0xFFFFFFFFu, mine));
         }
         if (lane == 0)
             sh.before[(p.S + kRound - 1) / kRound] = sum;

@@ -631,8 +631,9 @@ ts_status ts_hc_verify(const float *logits, const float *draft_probs, const int3
  * starts[s+1] - 1, with starts int32 [S+1] ascending from 0 on the device; tokens from starts[S] on belong to
  * none, and their rows of an output are left as they were. What the host cannot check of starts the kernels do:
  * a sequence that begins before token 0, ends before it begins or reaches past N is taken as empty and
- * TS_ERR_INVALID_ARG is recorded in the device status word. Sequences of no tokens are fine; rows that two sequences
- * claim, where starts descends, get either's results.
+ * TS_ERR_INVALID_ARG is recorded in the device status word. Sequences of no tokens are fine. Where starts descends
+ * anywhere (recorded too), sequences can overlap, and their rows hold either's results or what was there before:
+ * a call does no more work than N tokens and S sequences that do not overlap call for.
  */
 
 /*

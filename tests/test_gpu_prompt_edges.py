@@ -5,7 +5,7 @@ import torch
 
 from gpu_common import require_gpu
 from hyper_connection_residual_call_gb300 import binding as B
-from test_gpu_prompt import check_logprobs, check_prompt, fine, gen, logit_rows, prompt_case
+from test_gpu_prompt import check_logprobs, check_prompt, fine, gen, logit_rows, prompt_case, prompts
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +14,25 @@ pytestmark = pytest.mark.gpu
 def _gpu():
     require_gpu()
     B.device_status()
+
+
+# ------------------------------------------------------------------ attention over packed prompts
+
+@pytest.mark.parametrize("n,s,hq", [(5000, 3, 1), (3000, 601, 1), (700, 65535, 32)])
+def test_attention_sequences_that_overlap(n, s, hq):
+    """Each other sequence claims all rows, those between end before they begin: recorded, rows hold the result or what was
+    there, and nothing beside them is written."""
+    q, k, v, starts, at = prompts([n], hq, 1, 64, 61)
+    want, want_lse = B.hc_prompt_attention(q, k, v, starts)
+    fine()
+    wide, lse = torch.full((n + 512, hq, 64), 7.0, device="cuda").bfloat16(), torch.full((n + 512, hq), 7.0, device="cuda")
+    over = torch.arange(s + 1, device="cuda", dtype=torch.int32) % 2 * n
+    B.hc_prompt_attention(q, k, v, over, out=wide[256:256 + n], lse=lse[256:256 + n])
+    assert B.device_status() == B.TS_ERR_INVALID_ARG
+    for got, right in ((wide, want), (lse, want_lse)):
+        assert (got[:256] == 7).all() and (got[256 + n:] == 7).all()
+        mine = got[256:256 + n]
+        assert ((mine == right) | (mine == 7)).all() and (mine == right).any()
 
 
 # ------------------------------------------------------------------ the delta rule's segments

@@ -1,4 +1,5 @@
-"""The plan of the gated delta rule over packed prompts, on the CPU."""
+"""The plans of the operators over packed prompts, on the CPU: how the delta rule is cut into segments, how the
+attention counts its blocks."""
 import os
 import subprocess
 
@@ -17,7 +18,7 @@ def lib():
 
 @pytest.fixture(scope="module")
 def plan(tmp_path_factory):
-    """Compiles one of tests/native against the plan's header and runs it."""
+    """Compiles one of tests/native against the plans' headers and runs it."""
     include = os.path.join(os.path.dirname(os.path.dirname(b.nvcc_path())), "include")
 
     def run(name):
@@ -47,4 +48,9 @@ def test_workspace_grows_with_tokens_and_sequences(hk, hv, d):
 
 def test_segments_fit_the_workspace(plan):
     run = plan("delta_workspace")
+    assert run.returncode == 0, run.stdout[:2000]
+
+
+def test_attention_blocks_are_counted(plan):
+    run = plan("attn_blocks")
     assert run.returncode == 0, run.stdout[:2000]
