@@ -1,11 +1,13 @@
 """GPU tests of the prompt operators on a busy GPU and in the branches that only some sizes take; limits are
 test_gpu_prompt's, or stand beside the test."""
+import numpy as np
 import pytest
 import torch
 
+import prompt_reference as P
 from gpu_common import require_gpu
 from hyper_connection_residual_call_gb300 import binding as B
-from test_gpu_prompt import check_logprobs, check_prompt, fine, gen, logit_rows, prompt_case, prompts
+from test_gpu_prompt import U16, U32, check_logprobs, check_prompt, fine, gen, logit_rows, prompt_case, prompts, randn, within
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +16,39 @@ pytestmark = pytest.mark.gpu
 def _gpu():
     require_gpu()
     B.device_status()
+
+
+# ------------------------------------------------------------------ head norms
+
+@pytest.mark.parametrize("n,hq,hk,d,rot", [(9001, 9, 0, 128, 64), (9001, 32, 8, 128, 128), (17401, 7, 2, 64, 32), (2500, 16, 1, 256, 256),
+                                           (5003, 16, 1, 128, 32)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_norm_rope_threads_that_walk_over_heads(n, hq, hk, d, rot, interleaved, in_place):
+    """Tokens and heads enough that a thread walks over up to eight heads, an odd number of them too: the same bits as of 100
+    tokens at a time, where it has one; and some rows against the formula (test_gpu_prompt's limit)."""
+    g = gen(n)
+    x = randn(g, n, hq + 2 * hk, d, scale=1.7)
+    q, k = x[:, :hq], x[:, hq:hq + hk] if hk else None
+    w = [(1 + 0.3 * torch.randn(d, generator=g, device="cuda")).bfloat16() for _ in range(2)]
+    table = B.rope_table(500, rot, 10000.0)
+    pos = torch.randint(0, 500, (n,), generator=g, device="cuda", dtype=torch.int32)
+    rows = [0, 1, n // 2, n - 2, n - 1]
+    before = [P.f64(t[rows]) if t is not None else None for t in (q, k)]
+    parts = [B.hc_qk_norm_rope(q[a:a + 100], k[a:a + 100] if hk else None, pos[a:a + 100], table, w[0], w[1] if hk else None,
+                               interleaved=interleaved) for a in range(0, n, 100)]
+    rest = x[:, hq + hk:].clone()
+    out = B.hc_qk_norm_rope(q, k, pos, table, w[0], w[1] if hk else None, interleaved=interleaved,
+                            **(dict(q_out=q, k_out=k) if in_place else {}))
+    for i in range(2 if hk else 1):
+        assert torch.equal(out[i], torch.cat([p[i] for p in parts]))
+        normed, want = P.norm_rope(before[i], P.f64(w[i]), 1e-6, pos[rows].cpu().numpy(), P.f64(table), interleaved)
+        pair, r = np.abs(normed), rot // 2
+        i0, i1 = (np.arange(0, rot, 2), np.arange(1, rot, 2)) if interleaved else (np.arange(r), np.arange(r) + r)
+        pair[..., i0] = pair[..., i1] = pair[..., i0] + pair[..., i1]
+        within(out[i][rows], want, U16 * np.abs(want) + (d + 16) * U32 * pair + 1e-38, "head norms")
+    assert torch.equal(rest, x[:, hq + hk:])
+    fine()
 
 
 # ------------------------------------------------------------------ attention over packed prompts
@@ -98,6 +133,28 @@ def test_segments_read_what_was_just_written(hk, hv, d, n):
         ws.view(torch.int32)[:] = 1
         graph.replay()
     check()
+    fine()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("low", [0.0, 0.02, 0.5])
+@pytest.mark.parametrize("hv,lens", [(60, [130]), (2, [700]), (2, [1800]), (1, [2000, 4]), (1, [2700])])
+def test_states_have_22_bits(d, low, hv, lens):
+    """The states' relative error in the Frobenius norm, of chunks in one walk, in segments, and in segments whose last are
+    prepared beside the walks. What goes into a state is off by 2^-23 of its column's largest at most, uniformly: an operand
+    by some 2^-24 rms, five of them on the way (the state, M, R, T, U); the tensor cores' fp32 sums of 64 to 128 terms by some
+    sqrt(128) 2^-25. Together 4e-7 of what a chunk adds, and the state holds the chunks' errors as it holds what they added: 1e-6
+    over the dozens here, with the segments' joins twice that. A part of 11 bits left out, 2^-12 rms of an operand, would be 1e-4; two
+    parts of bf16 (16 bits), 2^-18 rms of each operand, 9e-6. The limit is between: 2^-18."""
+    args, at = prompt_case(lens, 1, hv, d, d + hv + lens[0], low=low)
+    _, state = B.hc_delta_prompt(*args, state_out=torch.empty_like(args[5]))
+    q, k, v, decay, beta, before = (P.f64(x) for x in args[:6])
+    heads = [0, hv - 1] if hv > 2 else list(range(hv))
+    for i, (lo, hi) in enumerate(zip(at[:-1], at[1:])):
+        _, after, _ = P.delta(q[lo:hi], k[lo:hi], v[lo:hi][:, heads], decay[lo:hi][:, heads], beta[lo:hi][:, heads], before[i][heads], 1.0, 1e-6)
+        err = np.linalg.norm(P.f64(state[i, heads]) - after) / np.linalg.norm(after)
+        print(f"D {d} low {low} {hi - lo} tokens: {err:.3g}")
+        assert err <= 2.0 ** -18
     fine()
 
 
