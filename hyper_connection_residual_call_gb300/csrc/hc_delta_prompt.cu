@@ -262,7 +262,9 @@ __device__ __forceinline__ void put8(uint8_t *hi, uint8_t *lo, int i, int x, con
 }
 
 // Eight elements of a row, a piece, of the D / 8 lanes that share it: scaled by a power of two so that the row's largest
-// is in [1, 2), as fp16, over them. Returns the row's sum of squares (before); `undo`: the power of two back.
+// is in [1, 2), as fp16, over them. Returns the row's sum of squares (before); `undo`: the power of two back, 0 for a row of
+// zeros (and of what is below bf16's range): times the inverse of its norm, an epsilon's, it would be far above the others',
+// whose w it shares a scale with.
 template <int D>
 __device__ __forceinline__ float row_to_half(uint4 &w, float &undo, bool &odd)
 {
@@ -284,7 +286,7 @@ __device__ __forceinline__ float row_to_half(uint4 &w, float &undo, bool &odd)
     odd = most == 0x7F800000u;
     const uint32_t e = min(most >> 23, 253u);
     const float by = e == 0 || odd ? 1.f : __uint_as_float((254u - e) << 23);
-    undo = e == 0 || odd ? 1.f : __uint_as_float(e << 23);
+    undo = odd ? 1.f : __uint_as_float(e << 23);
     w = make_uint4(pack2_f16(bf16_lo(u[0]) * by, bf16_hi(u[0]) * by), pack2_f16(bf16_lo(u[1]) * by, bf16_hi(u[1]) * by),
                    pack2_f16(bf16_lo(u[2]) * by, bf16_hi(u[2]) * by), pack2_f16(bf16_lo(u[3]) * by, bf16_hi(u[3]) * by));
     return sum;

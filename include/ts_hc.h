@@ -676,7 +676,8 @@ ts_status ts_hc_prompt_attention(const void *q, long q_stride, const void *k, lo
  * token after the other. A value head h has a state S, D x D, and key head h / (v_heads/k_heads); per token
  *     S <- e^decay S;  u = beta (v - S^T k);  S <- S + k u^T;  out = scale S^T q
  * with q and k divided by sqrt(sum of their squares + norm_eps) first where norm_eps >= 0 (norm_eps < 0: as they
- * are). fp32 arithmetic; out is rounded to bf16 once.
+ * are). fp32 arithmetic; out is rounded to bf16 once. A key or query whose sum of squares passes fp32's range counts as
+ * zeros; a sum of 0 with norm_eps 0 gives NaNs.
  *   q, k       bf16: head h of token t of sequence b at q + (b*T + t)*q_stride + h*D, k_heads of them; v likewise,
  *              v_heads; strides in elements, multiples of 8; 16-byte aligned
  *   decay      fp32 [B*T][v_heads], the logarithm of a token's decay (0 or less, -infinity for none kept);

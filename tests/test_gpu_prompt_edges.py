@@ -158,6 +158,43 @@ def test_states_have_22_bits(d, low, hv, lens):
     fine()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("eps", [1e-6, 1e-12, 1e-30])
+def test_keys_of_zeros_leave_the_others_their_bits(d, eps):
+    """Keys and queries of zeros, as padding has them, beside others, whatever the epsilon that their norms are: the limits of
+    test_states_have_22_bits, and of test_gpu_prompt for the outputs."""
+    args, at = prompt_case([200], 1, 2, d, 81, low=0.1)
+    for x in args[:2]:
+        x[[0, 5, 70, 71, 150, 199]] = 0
+    out, state = B.hc_delta_prompt(*args, norm_eps=eps, state_out=torch.empty_like(args[5]))
+    q, k, v, decay, beta, before = (P.f64(x) for x in args[:6])
+    _, after, _ = P.delta(q, k, v, decay, beta, before[0], 1.0, eps)
+    assert np.linalg.norm(P.f64(state[0]) - after) <= 2.0 ** -18 * np.linalg.norm(after)
+    check_prompt(args, at, out, state, eps)
+    fine()
+
+
+@pytest.mark.parametrize("token", [0, 70, 129])
+def test_keys_and_queries_past_the_range_of_their_squares(token):
+    """They count as zeros, in chunks and token by token; without an epsilon zeros have no direction."""
+    args, at = prompt_case([130], 1, 2, 64, 71)
+    huge, zero = [x.clone() for x in args[:6]], [x.clone() for x in args[:6]]
+    for i in range(2):
+        huge[i][token] = args[i][token] * 2.0 ** 70
+        zero[i][token] = 0
+    a, sa = B.hc_delta_prompt(*huge, args[6], state_out=torch.empty_like(args[5]))
+    z, sz = B.hc_delta_prompt(*zero, args[6], state_out=torch.empty_like(args[5]))
+    assert torch.equal(a, z) and torch.equal(sa, sz) and not a[token].any()
+    a, sa = B.hc_delta_step(*(x[None] for x in huge[:5]), huge[5], state_out=torch.empty_like(args[5]))
+    z, sz = B.hc_delta_step(*(x[None] for x in zero[:5]), zero[5], state_out=torch.empty_like(args[5]))
+    assert torch.equal(a, z) and torch.equal(sa, sz) and not a[0, token].any()
+    a, sa = B.hc_delta_prompt(*zero, args[6], norm_eps=0.0, state_out=torch.empty_like(args[5]))
+    z, sz = B.hc_delta_step(*(x[None] for x in zero[:5]), zero[5], norm_eps=0.0, state_out=torch.empty_like(args[5]))
+    for out, state in ((a, sa), (z[0], sz)):
+        assert out[token:].isnan().all() and state.isnan().all() and torch.isfinite(out[:token]).all()
+    fine()
+
+
 def test_one_workspace_serves_smaller_calls():
     ws = B.delta_prompt_workspace(6000, 6, 1, 2, 64)
     for lens in ([6000], [3000, 2900], [100, 5, 1, 0, 9, 300], [1], [2000, 1, 1, 1, 1, 1]):
