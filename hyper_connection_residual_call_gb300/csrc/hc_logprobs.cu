@@ -5,7 +5,10 @@
 //   entropy = -sum_v p_v log p_v = log Z - S / Z,  S = sum_v (x_v - m) e^(x_v - m)
 //
 // One pass over the logits: each thread keeps a running maximum and Z and S
-// relative to it, in fp32, and they are joined in a fixed order.
+// relative to it, in fp32, and they are joined in a fixed order. Where one token has nearly all of the
+// probability, Z is 1 and little more, and log Z would have the rounding of 1 for its error (5e-7, of 4e-4 a
+// thousandth): the sum without the thread that holds the maximum is kept beside Z, that thread's few elements are
+// taken again without the maximum, and log Z is log1p of the two.
 //
 // The best alternatives come from the same pass. An element is a 64-bit key, its
 // value in an order that unsigned comparison keeps above its index's complement, so
@@ -17,10 +20,13 @@
 // rising one say, are read a second time, with a threshold a chunk: at most n groups
 // hold an element that reaches one, which bounds what is kept for any logits.
 //
-// 4099 rows of 65537 bf16, eight tokens each, take 107 us for 0.54 GB, 0.74 of the measured copy rate; 2048 rows of
-// 128001 fp32 with the twenty best 210 us for 1.05 GB, 0.74, without them 149. Both issue 2.3 to 2.7 of 4 instructions a cycle from two
-// blocks a SM; a block that ranks a row leaves the SM to the other. One row of 32768: 7.8 us, a launch, 16 KB a
-// CTA, a ranking and a join through the cluster. (Loads to registers, without copies ahead: 218 and 355 us.)
+// 4099 rows of 65537 bf16, eight tokens each, take 109 us for 0.54 GB, 0.73 of the measured copy rate; 2048 rows of
+// 128001 fp32 with the twenty best 211 us for 1.05 GB, 0.73, without them 152; 4096 rows of 65537 bf16 with the twenty best 235,
+// 0.34: what a row's alternatives cost does not depend on its length. All issue 2.3 to 2.7 of 4 instructions a cycle from two
+// blocks a SM; a block that ranks a row leaves the SM to the other. With alternatives the kernels spill 24 to 48 bytes in their 64
+// registers, a third block's would not fit. One row of 32768: 8.1 us, a launch, 16 KB a CTA, a ranking and a join
+// through the cluster. (Loads to registers, without copies ahead: 218 and 355 us. Without keeping the largest term apart: 106, 210,
+// 148, 234 and 7.5.)
 #include <algorithm>
 #include <type_traits>
 
@@ -47,6 +53,7 @@ static_assert(kMaxTop * 4 * kHold <= kKeep / 2, "a chunk's keys");
 static_assert(kMaxTop * 4 * kEach <= kFew, "what a compaction leaves");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLeast = -200.f;           // of d: 2^d is 0 from -127 on, and d 2^d no NaN
+constexpr float kNearlyOne = 1.25f;        // from here on log Z is right to 6 times what the sum is
 constexpr float kNaN = __builtin_nanf("");
 
 __device__ __forceinline__ float max_nan(float a, float b)
@@ -87,10 +94,13 @@ __device__ __forceinline__ float key_value(uint64_t k)
 
 __device__ __forceinline__ uint32_t key_index(uint64_t k) { return 0xFFFFFFFFu - (uint32_t)k; }
 
-// A distribution's part: its largest logit m, and Z = sum 2^d and S = sum d 2^d over d = (x - m) log2 e.
+// A distribution's part: its largest logit m, Z = sum 2^d and S = sum d 2^d over d = (x - m) log2 e, and Z without the
+// thread that has m (the first of several), `who`: these where Z is less than kNearlyOne.
 struct Part {
-    float m, z, s;
+    float m, z, s, rest;
+    int who;
 };
+__device__ __forceinline__ Part no_part() { return Part{-INFINITY, 0.f, 0.f, 0.f, 0}; }
 
 // The parts of a warp's lanes.
 __device__ __forceinline__ Part join_warp(Part a)
@@ -100,12 +110,20 @@ __device__ __forceinline__ Part join_warp(Part a)
     const float m = __uint_as_float((most & 0x80000000u) ? most ^ 0x80000000u : ~most);
     const float d = max_nan((a.m - (m == -INFINITY ? 0.f : m)) * kLog2e, kLeast), f = ex2(d);
     float z = a.z * f, s = f * fmaf(d, a.z, a.s);
+    const float mine = z;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
         s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     }
-    return Part{m, z, s};
+    if (!(z < kNearlyOne))   // nor is the row's then, if m is its maximum
+        return Part{m, z, s, 0.f, 0};
+    const int first = __ffs(__ballot_sync(0xFFFFFFFFu, a.m == m)) - 1;
+    float rest = (threadIdx.x & 31) == first ? a.rest : mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+    return Part{m, z, s, rest, __shfl_sync(0xFFFFFFFFu, a.who, first)};
 }
 
 struct Shared {
@@ -420,6 +438,35 @@ __device__ __noinline__ void keep_again(const LogprobParams &p, long row, int ra
     sync();
 }
 
+// Thread `who`'s sum of 2^d, of the row's part that it had, but for its elements that are the maximum: by a warp, its
+// chunks' 16 elements two chunks at a time, eight loads ahead. (The others go on with the next row meanwhile.)
+template <typename R>
+__device__ __noinline__ float rest_of(const LogprobParams &p, long row, int ranks, int who, float m)
+{
+    constexpr int kAhead = 8, kStride = 32 / kHold * R::kStep * R::kPer;
+    const R r(p, row, who / kThreads, ranks);
+    const int lane = threadIdx.x & 31, c = lane % kHold;
+    const int end = min(r.V, r.v1 * R::kPer - r.lead);
+    float sum = 0.f;
+    int at = (r.v0 + lane / kHold * R::kStep + c / R::kPer * kThreads + who % kThreads) * R::kPer + c % R::kPer - r.lead;
+    if (at < 0)
+        at += kStride;  // an element before the row
+#pragma unroll 1
+    for (; at < end; at += kAhead * kStride) {
+        float x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            x[j] = at + (long)j * kStride < end ? r.logit(at + j * kStride) : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            sum += x[j] < m ? ex2(fmaxf((x[j] - m) * kLog2e, kLeast)) : 0.f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    return sum;
+}
+
 // kRanks: CTAs of the cluster that shares a row; kTop: alternatives are asked for. The grid takes rows in turn; the copies run ahead of the chunk at
 // hand, past the end of a row, so that a row's joins and lists do not stop them.
 template <bool kBf16, int kRanks, bool kTop>
@@ -482,7 +529,7 @@ __global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobPar
             if (token >= 0 && token < p.V)
                 given = r.logit(token);
         }
-        Part a{-INFINITY, 0.f, 0.f};                 // the thread's
+        Part a = no_part();                          // the thread's
         float limit = -INFINITY;                     // values up to this one are not among the n best
 #pragma unroll 1
         for (int ch = 0; ch < r.chunks; ++ch, ++taken) {
@@ -521,7 +568,9 @@ __global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobPar
                         top = fmaxf(top, x[i][c]);
                 if (top > a.m) {
                     const float d = max_nan((a.m - top) * kLog2e, kLeast), f = ex2(d);
-                    a = Part{top, a.z * f, f * fmaf(d, a.z, a.s)};
+                    a.s = f * fmaf(d, a.z, a.s);
+                    a.z *= f;
+                    a.m = top;
                 }
                 // Two elements an instruction. A -infinity makes the chunk's S a NaN: it is taken again with d bounded.
                 const float ref = a.m == -INFINITY ? 0.f : a.m;
@@ -570,6 +619,7 @@ __global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobPar
                 }, sh);
             }
         }
+        a.who = tid;
         a = join_warp(a);
         if (lane == 0)
             sh.part[turn][warp] = a;
@@ -583,17 +633,18 @@ __global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobPar
         }
         if (kRanks == 1 && back - 31 + lane >= max(p.J, max(n, 1)))
             continue;                                // the warp has no results to write
-        a = lane < kWarps ? sh.part[turn][lane] : Part{-INFINITY, 0.f, 0.f};
+        a = lane < kWarps ? sh.part[turn][lane] : no_part();
         a = join_warp(a);
         if (kRanks > 1) {
             if (tid == 0)
                 sh.whole = a;
             cluster_sync();
             if (rank == 0) {
-                a = Part{-INFINITY, 0.f, 0.f};
+                a = no_part();
                 if (lane < kRanks) {
                     const uint32_t from = dsmem_addr(&sh.whole, lane);
-                    a = Part{dsmem_ld_f32(from), dsmem_ld_f32(from + 4), dsmem_ld_f32(from + 8)};
+                    a = Part{dsmem_ld_f32(from), dsmem_ld_f32(from + 4), dsmem_ld_f32(from + 8), dsmem_ld_f32(from + 12),
+                             __float_as_int(dsmem_ld_f32(from + 16)) + lane * kThreads};
                 }
                 a = join_warp(a);
                 if (kTop && tid < n * kRanks) {  // the ranks' lists, n keys each
@@ -616,7 +667,7 @@ __global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobPar
         }
         // a row with a NaN, with +infinity, or with nothing but -infinity is no distribution
         const bool bad = !(a.m > -INFINITY && a.m < INFINITY) || !(a.z >= 0.f);
-        const float log_z = bad ? kNaN : logf(a.z);
+        const float log_z = bad ? kNaN : a.z < kNearlyOne ? log1pf(a.rest + rest_of<R>(p, row, kRanks, a.who, a.m)) : logf(a.z);
         bool wrong = bad;
         if (asks) {
             for (int j = back; j < p.J; j += kThreads) {

@@ -738,8 +738,10 @@ typedef enum {
  *   entropy    fp32 [N] or NULL: -sum_v p_v log p_v (natural logarithms)
  *   top_ids    int32 [N][top] and top_logp fp32 [N][top], best first; of equal logits the lowest index first.
  *              Not used with top == 0; top <= 32 and top <= V
- * Sums are fp32. A logit of -infinity is a probability of 0. A row that is no distribution (a NaN or a +infinity
- * in it, or nothing but -infinity) gives NaNs, and -1 as ids, and is recorded.
+ * Sums are fp32, with the largest term's 1 apart from the others where these are little beside it: log probabilities
+ * and entropies near 0 are right to 1e-6 or so of themselves. A logit of -infinity is a probability of 0. A row that
+ * is no distribution (a NaN or a +infinity in it, or nothing but -infinity) gives NaNs, and -1 as ids, and is
+ * recorded.
  * Outputs must not overlap the inputs or one another. V < 2^30.
  */
 ts_status ts_hc_logprobs(const void *logits, int logits_type, long logits_stride, const int32_t *tokens, float *logp,

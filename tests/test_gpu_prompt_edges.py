@@ -240,3 +240,30 @@ def test_logprobs_rows_of_two_and_four_ctas(kind, dtype, n, v):
     order = (x.float() + 0.0).sort(dim=-1, descending=True, stable=True).indices[:, :20]
     assert torch.equal(got[2].long(), order)
     fine()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,v", [(1, 32768), (1, 40), (3, 7681), (20, 128001), (60, 20003), (330, 50001)])
+@pytest.mark.parametrize("top", [0, 3])
+def test_logprobs_of_a_token_that_is_nearly_certain(dtype, n, v, top):
+    """Log probabilities and entropies near 0 keep their relative precision. All terms but the largest one's 1 are added up
+    apart from it: with test_gpu_prompt's r for the sums, and e^d off by 2 |d| u32 + 2^-22 of itself (|d| of 64 at most), log Z is off
+    by (r + 132 u32) of itself; from Z = 1.25 on, where it is the logarithm of a sum with the 1 in it, by r (1 + 1 / log 1.25) < 6 r of
+    itself. S = sum d e^d likewise, with d's own error twice."""
+    g, r = gen(n + v), (v / 1024 + 100) * U32
+    x = torch.randn(n, v, generator=g, device="cuda")
+    at = torch.randint(0, v, (n,), generator=g, device="cuda")
+    at[0], at[-1] = 0, v - 1
+    x[torch.arange(n, device="cuda"), at] = torch.linspace(13.0, 40.0, n, device="cuda") if n > 1 else 20.0
+    x = x.to(dtype)
+    logp, entropy, ids, best = B.hc_logprobs(x, at.int()[:, None], top=top)
+    e = x.double() - x.double().amax(-1, keepdim=True)
+    assert (e[torch.arange(n, device="cuda"), at] == 0).all() and (e < 0).sum() == n * (v - 1)
+    z = torch.where(e < 0, e.exp(), 0.0).sum(-1)
+    want = torch.log1p(z)
+    h = want - (e * e.exp()).sum(-1) / (1 + z)
+    assert ((logp[:, 0].double() + want).abs() <= (6 * r + 132 * U32) * want).all()
+    assert ((entropy.double() - h).abs() <= (6 * r + 264 * U32) * h).all()
+    if top:
+        assert torch.equal(ids[:, 0].long(), at) and torch.equal(best[:, 0], logp[:, 0])
+    fine()
