@@ -20,11 +20,11 @@
 // rising one say, are read a second time, with a threshold a chunk: at most n groups
 // hold an element that reaches one, which bounds what is kept for any logits.
 //
-// 4099 rows of 65537 bf16, eight tokens each, take 109 us for 0.54 GB, 0.73 of the measured copy rate; 2048 rows of
-// 128001 fp32 with the twenty best 211 us for 1.05 GB, 0.73, without them 152; 4096 rows of 65537 bf16 with the twenty best 235,
-// 0.34: what a row's alternatives cost does not depend on its length. All issue 2.3 to 2.7 of 4 instructions a cycle from two
+// 4099 rows of 65537 bf16, eight tokens each, take 111 us for 0.54 GB, 0.72 of the measured copy rate; 2048 rows of
+// 128001 fp32 with the twenty best 212 us for 1.05 GB, 0.73, without them 152; 4096 rows of 65537 bf16 with the twenty best 237,
+// 0.33: what a row's alternatives cost does not depend on its length. All issue 2.3 to 2.7 of 4 instructions a cycle from two
 // blocks a SM; a block that ranks a row leaves the SM to the other. With alternatives the kernels spill 24 to 48 bytes in their 64
-// registers, a third block's would not fit. One row of 32768: 8.1 us, a launch, 16 KB a CTA, a ranking and a join
+// registers, a third block's would not fit. One row of 32768: 7.9 us, a launch, 16 KB a CTA, a ranking and a join
 // through the cluster. (Loads to registers, without copies ahead: 218 and 355 us. Without keeping the largest term apart: 106, 210,
 // 148, 234 and 7.5.)
 #include <algorithm>
@@ -64,8 +64,9 @@ __device__ __forceinline__ float max_nan(float a, float b)
 }
 
 // mbar_wait_bounded, for warps that have nothing else to do: each attempt may take a microsecond of the
-// hardware's own waiting, so that the others have the issue slots.
-__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity)
+// hardware's own waiting, so that the others have the issue slots. One wait that runs out is all of `limit`: the next ones
+// end after an attempt.
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, uint32_t &limit)
 {
     const uint64_t t0 = global_timer_ns();
     for (;;) {
@@ -74,8 +75,10 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity)
                      : "=r"(done) : "r"(smem_addr(bar)), "r"(parity), "r"(1000u) : "memory");
         if (done)
             return true;
-        if (global_timer_ns() - t0 > kWaitLimitNs)
+        if (global_timer_ns() - t0 > limit) {
+            limit = 0;
             return false;
+        }
     }
 }
 
@@ -517,6 +520,7 @@ __global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobPar
     const int back = kThreads - 1 - tid;             // results are the last threads'
     unsigned taken = 0;                              // chunks that came
     int turn = 0;                                    // rows, in turn
+    uint32_t wait_limit = kWaitLimitNs;
 #pragma unroll 1
     for (long row = row0; row < p.N; row += rows, turn ^= 1) {
         const R r(p, row, rank, kRanks);
@@ -542,7 +546,7 @@ __global__ void __launch_bounds__(kBlock, 2) hc_logprobs_kernel(const LogprobPar
                 const uint64_t least = threshold_of(key_of(a.m, tid), n, sh, 1);  // (no barrier since chunk 0's)
                 limit = fmaxf(limit, key_value(least));
             }
-            if (!wait_bounded(&sh.full[stage], phase)) {
+            if (!wait_bounded(&sh.full[stage], phase, wait_limit)) {
                 *reinterpret_cast<volatile int *>(&sh.dead) = 1;
                 if (p.status)
                     atomicExch(p.status, kStatusTimeout);
