@@ -1280,7 +1280,8 @@ def hc_delta_step(q, k, v, decay, beta, state, *, counts=None, scale: Optional[f
     logarithm) and ``beta`` fp32 [B, T, v_heads], from ``state`` fp32 [B, v_heads, D, D], token by token;
     ``counts`` int32 [B]: how many of its tokens a sequence takes. ``norm_eps``: q and k are divided by the root
     of their squares' sum and it, None: they are taken as they are. ``scale`` defaults to D ** -0.5. Returns (out
-    bf16 [B, T, v_heads, D], state_out); ``state_out`` defaults to ``state``, which is updated in place."""
+    bf16 [B, T, v_heads, D], state_out); ``state_out`` defaults to ``state``, which is updated in place. With B or T 0
+    nothing is written, another ``state_out`` neither."""
     torch = _torch()
     _, hk, hv, d, sq, sk, sv = _delta_rows(q, k, v, decay, beta, 4)
     b, t = q.shape[:2]
@@ -1310,7 +1311,8 @@ def hc_delta_prompt(q, k, v, decay, beta, state, starts, *, scale: Optional[floa
     """The gated delta rule over packed prompts: ``q``, ``k`` [N, k_heads, D], ``v`` [N, v_heads, D] bf16, ``decay``
     and ``beta`` fp32 [N, v_heads], ``state`` fp32 [S, v_heads, D, D], the sequences' rows starts[s] ..
     starts[s+1] - 1 with ``starts`` int32 [S + 1]. Arguments and results as for ``hc_delta_step``: (out bf16
-    [N, v_heads, D], state_out, ``state`` itself unless given)."""
+    [N, v_heads, D], state_out, ``state`` itself unless given). With N 0 nothing is written, another ``state_out``
+    neither."""
     torch = _torch()
     n, hk, hv, d, sq, sk, sv = _delta_rows(q, k, v, decay, beta, 3)
     sp, s = _starts(starts)

@@ -17,7 +17,7 @@ constexpr int kChunk = 64;
 // the SMs hold, a walk a SM, and at least three, of eight chunks at least. One sequence, without and with segments: 8192
 // tokens of 32 heads of 128 (three segments) 571 and 471 us, of 8 heads 455 and 228; 65536 tokens of 4 heads 3290 and
 // 672; 2048 tokens of 8 heads 125 and 113; but 1100 tokens of 4 heads 81 and 96, hence the 24 chunks. (Before the first
-// and the joining kernel had their present form; by now the second of each pair are 394, 161, 536 and 101.)
+// and the joining kernel had their present form; by now the second of each pair are 394, 175, 536 and 101.)
 // kSms is the GPU's, not asked of the device: the workspace's size follows from the plan and is known without one.
 constexpr int kSms = 152, kLeastSegment = 8, kLeastCut = 24;
 inline int segment_chunks(int N, int S, int Hv)

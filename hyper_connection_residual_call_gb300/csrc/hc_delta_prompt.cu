@@ -294,7 +294,7 @@ __device__ __forceinline__ float row_to_half(uint4 &w, float &undo, bool &odd)
 
 // A block a chunk and key head, with the key head's value heads one after the other. (A block a value head, which does
 // the keys' part again for each, took a quarter longer. Four blocks a SM, in 64 registers, for D = 128, too: 8192 tokens of 32
-// heads in 419 us, with three, in 80, 426; but 2048 of 8 heads 101 and 94, where the blocks are few.)
+// heads in 419 us, with three, in 80, 426; but 2048 of 8 heads 101 and 94, where the blocks are few. 52 bytes are spilled.)
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads, 4) hc_delta_prep_kernel(const DeltaPromptParams p)
 {

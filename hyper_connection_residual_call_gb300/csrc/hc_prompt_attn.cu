@@ -24,11 +24,15 @@
 // warp 10 looks through the last tiles' values, warp 11 finds the next block. Every wait is
 // bounded; the first that runs out records TS_ERR_TIMEOUT and ends the others.
 //
+// Results are divided by the sum of the weights as they were before they were rounded. By the rounded ones' sum, as in the
+// attention over the cache, they are off by 2.00e-3 and not by 2.02e-3 (1.61e-3 and not 1.81e-3 where a few keys have the
+// weight; the results' rounding is 1.6e-3 of it); the second sum costs the long prompt 46 us, the batch 2.6, the short ones 0.6.
+//
 // One prompt of 16384 tokens, 32 heads of 128 over 8, takes 1.50 ms, 1.47 PFLOP/s, 0.86 of what a library product holds
-// under the power cap: a block's pair of tiles takes some 3280 cycles, 2048 of them products, the rest what the
+// under the power cap (up to 1.59 in plain calls; heads of 64: 1.26): a block's pair of tiles takes some 3280 cycles, 2048 of them products, the rest what the
 // exponentials and the products of one stream wait for the other's. Eight prompts of 256 to 2048 tokens take 125 us,
 // of which 79 are tiles: the others are the blocks' first tiles, their last products (700 cycles) and the results' way
-// out (3700 cycles, 2000 of them the stores, a row a lane). 48 prompts of up to 200 tokens, 16 heads of 64 over 2: 18.7 us.
+// out (3700 cycles, 2000 of them the stores, a row a lane). 48 prompts of up to 200 tokens, 16 heads of 64 over 2: 18.9 us.
 // Before the last tiles' keys were masked by 32, and those that none of a warp's rows sees left out, it was 1.54 ms and 126
 // us, and to that compare: two threads a row, 16 softmax warps, 1.60 and 131; two places for the queries, one less for
 // the rest, 1.57 and 125.
